@@ -5,7 +5,10 @@
  * hand-written CUDA kernels:
  *   - a fused, multi-tensor, mixed-precision AdamW update;
  *   - the row-wise softmax backward;
- *   - the LayerNorm backward (dX, dgamma, dbeta).
+ *   - the LayerNorm backward (dX, dgamma, dbeta);
+ *   - rotary positions and the per-head RMS norm of queries and keys, with their
+ *     gradients;
+ *   - the softmax cross entropy of a linear output layer, with its gradients.
  *
  * Sources (web pages on the subject; cited by page title and section):
  *   [GPU-Opt-P2]  "GPU 优化实战 Part 2：用 CUDA/ROCm 实现 LLM 反向传播与训练循环"
@@ -14,7 +17,7 @@
  *
  * Conventions for every entry point
  *   - Buffers are device-accessible memory owned by the caller, row-major and
- *     contiguous.  The library keeps no pointer after a call returns, except the
+ *     contiguous (queries and keys are strided: see tb_heads).  The library keeps no pointer after a call returns, except the
  *     AdamW plan's copy of the tensor table (see tb_adamw_plan_create).
  *   - `stream` is a cudaStream_t passed as void*; NULL is the legacy default
  *     stream.  Work is enqueued on it and the call returns without waiting: a
@@ -435,6 +438,161 @@ tb_status tb_layernorm_bwd_noalloc(const void* dY, const void* x, const float* m
                                    const float* inv_std, const float* gamma,
                                    void* dX, float* dgamma, float* dbeta,
                                    int64_t rows, int64_t D, tb_dtype io_dtype, void* stream);
+
+/* ======================================================================== */
+/* Rotary positions; per-head RMS norm of queries and keys                   */
+/* ======================================================================== */
+/*
+ * The queries and keys of one attention layer on their way from the projection
+ * to the attention product, and their gradients on the way back.  (The pages
+ * have no counterpart: they take attention's softmax backward by itself.)
+ *
+ * A rotated pair (a, b) with frequency w_i, at position p and angle t = p * w_i:
+ *     a' = magnitude * (a cos t - b sin t),  b' = magnitude * (a sin t + b cos t)
+ * Pair i of a head, i < rotary_dim / 2, is elements (i, i + rotary_dim/2) in the
+ * half layout and (2i, 2i + 1) in the interleaved one.  Elements from rotary_dim
+ * on are not rotated.  The norm of one head of D elements, before the rotation:
+ *     inv_rms = 1/sqrt(mean_D(x^2) + eps),   n = gamma * x * inv_rms
+ * with one gamma [D] for all query heads and one for all key heads.
+ * All arithmetic is fp32, rounded once to the storage type.
+ */
+
+/* One tensor of heads, [batch, seq, heads, head_dim]: element (b, s, h, d) is at
+ * data + b*stride_batch + s*stride_seq + h*stride_head + d, in elements.  Strides
+ * are >= 0 and those of a size of 1 are ignored, so that any of [batch, seq,
+ * heads, dim], [batch, heads, seq, dim] and a slice of a joint projection's output
+ * can be passed as they are; a 0 stride repeats an input.  heads <= 1,048,576. */
+typedef struct tb_heads {
+    void* data;
+    int64_t stride_batch, stride_seq, stride_head;
+    int64_t heads;
+} tb_heads;
+
+typedef enum tb_rope_layout {
+    TB_ROPE_HALF = 0,         /* pairs (i, i + rotary_dim/2) */
+    TB_ROPE_INTERLEAVED = 1   /* pairs (2i, 2i + 1)          */
+} tb_rope_layout;
+
+/* How a call turns positions into angles. */
+typedef struct tb_rope_angles {
+    const uint64_t* freqs;     /* device [rotary_dim/2]: the part of a turn that one
+                                  position adds, in 2^-64 turn (tb_rope_freqs); 8-byte
+                                  aligned; may be NULL when rotary_dim is 0         */
+    const int64_t* positions;  /* device: position of (b, s) at b*positions_stride + s,
+                                  8-byte aligned; NULL: s                            */
+    int64_t positions_stride;  /* 0: one row for every batch entry, else >= seq      */
+    int64_t offset;            /* added to every position                            */
+    int rotary_dim;            /* even, 0 .. head_dim                                */
+    tb_rope_layout layout;
+    float magnitude;           /* factor on sines and cosines, finite; usually 1     */
+} tb_rope_angles;
+
+typedef enum tb_rope_scale_kind {
+    TB_ROPE_SCALE_NONE = 0,
+    TB_ROPE_SCALE_LINEAR = 1,      /* every frequency divided by factor              */
+    TB_ROPE_SCALE_NTK = 2,         /* base * factor^(rotary_dim / (rotary_dim - 2))  */
+    TB_ROPE_SCALE_YARN = 3,        /* pairs making more than `fast` turns over
+                                      original_context keep their frequency, pairs
+                                      making fewer than `slow` are divided by factor,
+                                      a linear blend over the pair's index between;
+                                      magnitude 0.1 ln(factor) + 1                   */
+    TB_ROPE_SCALE_WAVELENGTH = 4   /* the same with the blend linear in the turns and
+                                      magnitude 1                                    */
+} tb_rope_scale_kind;
+
+typedef struct tb_rope_scaling {
+    tb_rope_scale_kind kind;
+    double factor;             /* >= 1 */
+    double original_context;   /* YARN, WAVELENGTH: positions trained on, > 0        */
+    double fast, slow;         /* YARN, WAVELENGTH: turns, fast > slow > 0           */
+} tb_rope_scaling;
+
+/*
+ * tb_rope_freqs -- fill a host table with the frequencies base^(-2i/rotary_dim)
+ * radians per position, scaled for a longer context, as whole 2^-64 parts of a
+ * turn.  p * freq in wrapping 64-bit arithmetic is the angle of position p modulo
+ * one turn exactly, however far p is.  Needs no GPU; copy the table to the device.
+ *   rotary_dim  even, 0 .. 1024
+ *   base        > 0 (10000 is usual), > 1 with YARN
+ *   scaling     NULL: none
+ *   freqs       out: host [rotary_dim/2]
+ *   magnitude   out: the value for tb_rope_angles.magnitude
+ * Errors: TB_ERR_INVALID_VALUE.
+ */
+tb_status tb_rope_freqs(int rotary_dim, double base, const tb_rope_scaling* scaling,
+                        uint64_t* freqs, float* magnitude);
+
+/*
+ * tb_rope -- rotate queries and keys; tb_rope_bwd -- its gradient, the transposed
+ * rotation (also scaled by magnitude), which needs no forward values.
+ *   q, k            inputs; k may be NULL (then k_out is NULL too)
+ *   q_out, k_out    outputs with as many heads as their input.  An output may be the
+ *                   very same rows as its input (a call in place); otherwise it must
+ *                   share no element with any input or output.  Views that walk one
+ *                   buffer with the same strides are told apart exactly; views with
+ *                   different strides count as sharing when their address ranges meet.
+ *   batch, seq      >= 0; nothing is enqueued when either is 0.  Elements of a buffer
+ *                   outside the views are not touched.
+ *   head_dim        1 .. 1024
+ *   dtype           TB_F32, TB_BF16 or TB_F16, of all four
+ * Sizes, strides and pointers that are multiples of 16 bytes (8, or two elements) take
+ * vectorised kernels, others a general one.  The sines of 16-bit calls are good to
+ * 2^-21, those of fp32 calls to fp32 accuracy.
+ * Errors: TB_ERR_INVALID_VALUE, TB_ERR_UNSUPPORTED_DTYPE, TB_ERR_MISALIGNED,
+ * TB_ERR_ALIAS, TB_ERR_CUDA.
+ */
+tb_status tb_rope(const tb_heads* q, const tb_heads* k, const tb_heads* q_out,
+                  const tb_heads* k_out, int64_t batch, int64_t seq, int64_t head_dim,
+                  const tb_rope_angles* angles, tb_dtype dtype, void* stream);
+
+tb_status tb_rope_bwd(const tb_heads* dq_out, const tb_heads* dk_out, const tb_heads* dq,
+                      const tb_heads* dk, int64_t batch, int64_t seq, int64_t head_dim,
+                      const tb_rope_angles* angles, tb_dtype dtype, void* stream);
+
+/*
+ * tb_qk_norm_rope -- the per-head RMS norm of queries and keys and their rotation
+ * in one pass.  As tb_rope, with
+ *   gamma_q, gamma_k       fp32 [head_dim]; gamma_k may be NULL when k is
+ *   eps                    >= 0
+ *   inv_rms_q, inv_rms_k   out: fp32 [batch, seq, heads], contiguous, what the
+ *                          gradient needs; either may be NULL (serving)
+ * rotary_dim = 0 gives the norm alone.  A head of zeros gives inv_rms = 1/sqrt(eps)
+ * and zeros (NaN when eps is 0).
+ */
+tb_status tb_qk_norm_rope(const tb_heads* q, const tb_heads* k, const float* gamma_q,
+                          const float* gamma_k, float eps, const tb_heads* q_out,
+                          const tb_heads* k_out, float* inv_rms_q, float* inv_rms_k,
+                          int64_t batch, int64_t seq, int64_t head_dim,
+                          const tb_rope_angles* angles, tb_dtype dtype, void* stream);
+
+/*
+ * tb_qk_norm_rope_bwd -- its gradient.  With dn the transposed rotation of dq_out,
+ * xhat = x * inv_rms and dxhat = dn * gamma, for queries and keys alike:
+ *     dq       = inv_rms * (dxhat - xhat * mean_D(dxhat * xhat))
+ *     dgamma_q = sum over batch, seq and heads of dn * xhat   (overwritten)
+ * dgamma is reduced in a fixed order: results are bitwise reproducible.
+ *   dq_out, dk_out   gradients of the forward's outputs
+ *   q, k             the forward's inputs, inv_rms_q, inv_rms_k what it saved
+ *   dq, dk           outputs; each may be the same rows as its dq_out or its q
+ *   workspace        device scratch of tb_qk_norm_rope_bwd_workspace_size() bytes,
+ *                    16-byte aligned, contents ignored.  Calls that may run at the
+ *                    same time need workspaces of their own.
+ * No token or no head writes zeros to dgamma.
+ * Errors: as tb_rope, plus TB_ERR_WORKSPACE.
+ */
+tb_status tb_qk_norm_rope_bwd_workspace_size(int64_t batch, int64_t seq, int64_t heads_q,
+                                             int64_t heads_k, int64_t head_dim,
+                                             tb_dtype dtype, size_t* bytes);
+
+tb_status tb_qk_norm_rope_bwd(const tb_heads* dq_out, const tb_heads* dk_out,
+                              const tb_heads* q, const tb_heads* k,
+                              const float* inv_rms_q, const float* inv_rms_k,
+                              const float* gamma_q, const float* gamma_k,
+                              const tb_heads* dq, const tb_heads* dk,
+                              float* dgamma_q, float* dgamma_k,
+                              int64_t batch, int64_t seq, int64_t head_dim,
+                              const tb_rope_angles* angles, tb_dtype dtype,
+                              void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

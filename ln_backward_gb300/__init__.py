@@ -1,8 +1,9 @@
 """GB300-native memory-bound training-step kernels.
 
 ``libtb.so`` (built from ``csrc/`` for sm_103a) implements the fused
-mixed-precision multi-tensor AdamW step, the row-wise softmax backward and the
-LayerNorm backward behind the C ABI declared in ``include/tb.h``.  This package
+mixed-precision multi-tensor AdamW step, the row-wise softmax backward, the
+LayerNorm and RMSNorm backward, rotary positions with the per-head norm of
+queries and keys, and the output layer's cross entropy behind the C ABI declared in ``include/tb.h``.  This package
 is its thin Python binding (same names as the C entry points) plus the seeded
 synthetic-input module ``synth``.
 """
@@ -15,6 +16,8 @@ from ._binding import (  # noqa: F401
     tb_device_error,
     tb_layernorm_bwd, tb_layernorm_bwd_noalloc, tb_layernorm_bwd_selftest_timeout,
     tb_layernorm_bwd_workspace_size,
-    tb_rmsnorm_bwd, tb_rmsnorm_bwd_workspace_size, tb_softmax_bwd, tb_softmax_bwd_causal,
+    tb_qk_norm_rope, tb_qk_norm_rope_bwd, tb_qk_norm_rope_bwd_workspace_size,
+    tb_rmsnorm_bwd, tb_rmsnorm_bwd_workspace_size,
+    tb_rope, tb_rope_bwd, tb_rope_freqs, tb_softmax_bwd, tb_softmax_bwd_causal,
     tb_status_string, tb_version,
 )

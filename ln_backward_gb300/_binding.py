@@ -30,7 +30,9 @@ EXPORTS = ("tb_status_string", "tb_version", "tb_device_error", "tb_adamw_plan_c
            "tb_softmax_bwd_causal", "tb_rmsnorm_bwd_workspace_size", "tb_rmsnorm_bwd",
            "tb_adamw_grad_norm_workspace_size", "tb_adamw_grad_norm", "tb_adamw_step_clipped",
            "tb_cast_to_f32", "tb_cast_from_f32", "tb_layernorm_bwd_selftest_timeout",
-           "tb_adamw_step_device", "tb_adamw_selftest_stale_counter")
+           "tb_adamw_step_device", "tb_adamw_selftest_stale_counter", "tb_rope_freqs", "tb_rope",
+           "tb_rope_bwd", "tb_qk_norm_rope", "tb_qk_norm_rope_bwd_workspace_size",
+           "tb_qk_norm_rope_bwd")
 
 
 class TbError(RuntimeError):
@@ -47,6 +49,25 @@ class tb_tensor_desc(ctypes.Structure):
 class tb_adamw_hparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float)]
+
+
+class tb_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64),
+                ("stride_seq", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+                ("heads", ctypes.c_int64)]
+
+
+class tb_rope_angles(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("positions_stride", ctypes.c_int64), ("offset", ctypes.c_int64),
+                ("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int),
+                ("magnitude", ctypes.c_float)]
+
+
+class tb_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double),
+                ("original_context", ctypes.c_double), ("fast", ctypes.c_double),
+                ("slow", ctypes.c_double)]
 
 
 def _load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
@@ -99,6 +120,22 @@ def _load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.tb_layernorm_bwd_selftest_timeout.restype = i32
     lib.tb_adamw_selftest_stale_counter.argtypes = [vp, ctypes.c_uint64, vp]
     lib.tb_adamw_selftest_stale_counter.restype = i32
+    heads, angles = ctypes.POINTER(tb_heads), ctypes.POINTER(tb_rope_angles)
+    lib.tb_rope_freqs.argtypes = [i32, ctypes.c_double, ctypes.POINTER(tb_rope_scaling), vp,
+                                  ctypes.POINTER(f32)]
+    lib.tb_rope_freqs.restype = i32
+    for fn in (lib.tb_rope, lib.tb_rope_bwd):
+        fn.argtypes = [heads, heads, heads, heads, i64, i64, i64, angles, i32, vp]
+        fn.restype = i32
+    lib.tb_qk_norm_rope.argtypes = [heads, heads, vp, vp, f32, heads, heads, vp, vp, i64, i64, i64,
+                                    angles, i32, vp]
+    lib.tb_qk_norm_rope.restype = i32
+    lib.tb_qk_norm_rope_bwd_workspace_size.argtypes = [i64, i64, i64, i64, i64, i32,
+                                                       ctypes.POINTER(ctypes.c_size_t)]
+    lib.tb_qk_norm_rope_bwd_workspace_size.restype = i32
+    lib.tb_qk_norm_rope_bwd.argtypes = [heads, heads, heads, heads, vp, vp, vp, vp, heads, heads,
+                                        vp, vp, i64, i64, i64, angles, i32, vp, ctypes.c_size_t, vp]
+    lib.tb_qk_norm_rope_bwd.restype = i32
     return lib
 
 
@@ -402,3 +439,208 @@ def tb_layernorm_bwd_noalloc(dY: torch.Tensor, x: torch.Tensor, mean: torch.Tens
            lib.tb_layernorm_bwd_noalloc(_ptr(dY), _ptr(x), _ptr(mean), _ptr(inv_std), _ptr(gamma),
                                         _ptr(dX), _ptr(dgamma), _ptr(dbeta), rows, D, _dtype(x),
                                         _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- rotary positions
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
+
+
+def tb_rope_freqs(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                  original_context: float = 0.0, fast: float = 32.0, slow: float = 1.0,
+                  device=None):
+    """(freqs, magnitude): an int64 tensor of rotary_dim / 2 frequencies in 2^-64 turn a
+    position, on ``device`` (the current CUDA device by default), and the factor on sines and
+    cosines. ``scaling``: none, linear, ntk, yarn or wavelength (see include/tb.h)."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALING)}")
+    table = torch.empty(max(int(rotary_dim), 0) // 2, dtype=torch.int64)
+    magnitude = ctypes.c_float(0.0)
+    how = tb_rope_scaling(ROPE_SCALING[scaling], float(factor), float(original_context),
+                          float(fast), float(slow))
+    _check("tb_rope_freqs",
+           lib.tb_rope_freqs(int(rotary_dim), float(base), ctypes.byref(how),
+                             table.data_ptr() or None, ctypes.byref(magnitude)))
+    return table.to("cuda" if device is None else device), magnitude.value
+
+
+def _heads(t: Optional[torch.Tensor], like: torch.Tensor, name: str) -> Optional[tb_heads]:
+    """[batch, seq, heads, head_dim] with any strides but the last one's."""
+    if t is None:
+        return None
+    if t.dim() != 4 or t.shape[:2] != like.shape[:2] or t.shape[3] != like.shape[3]:
+        raise ValueError(f"{name} must be [batch, seq, heads, head_dim] with the batch, seq and "
+                         f"head_dim of the queries, got {tuple(t.shape)}")
+    if t.dtype != like.dtype:
+        raise ValueError(f"{name} must be {like.dtype} like the queries, got {t.dtype}")
+    sb, ss, sh, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return tb_heads(t.data_ptr() or None, sb, ss, sh, t.shape[2])
+
+
+def _on_current_device(*tensors: Optional[torch.Tensor]) -> None:
+    """As _ptr checks it, for tensors that need not be contiguous."""
+    current = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors passed to libtb must be CUDA tensors")
+        if current is None:
+            current = torch.cuda.current_device()
+        if t.device.index != current:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{current}")
+
+
+def _angles(q: torch.Tensor, freqs: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+            offset: int, interleaved: bool, magnitude: float) -> tb_rope_angles:
+    rotary_dim, table = 0, None
+    if freqs is not None:
+        if freqs.dtype != torch.int64 or freqs.dim() != 1:
+            raise ValueError("freqs must be the int64 table of tb_rope_freqs")
+        rotary_dim, table = 2 * freqs.numel(), _ptr(freqs)
+    where, stride = None, 0
+    if positions is not None:
+        if positions.dtype != torch.int64 or not positions.is_cuda or positions.device != q.device:
+            raise ValueError("positions must be an int64 tensor on the queries' device")
+        batch, seq = q.shape[:2]
+        if positions.shape != (batch, seq) and positions.shape != (seq,):
+            raise ValueError(f"positions must be [{batch}, {seq}] or [{seq}], got "
+                             f"{tuple(positions.shape)}")
+        if seq > 1 and positions.stride(-1) != 1:
+            raise ValueError("the last dimension of positions must be contiguous")
+        where = positions.data_ptr() or None
+        stride = positions.stride(0) if positions.dim() == 2 and batch > 1 else 0
+    return tb_rope_angles(table, where, stride, int(offset), rotary_dim, int(bool(interleaved)),
+                          float(magnitude))
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def _pairs(q, k, q_out, k_out, names):
+    if q.dim() != 4:
+        raise ValueError(f"{names[0]} must be [batch, seq, heads, head_dim], got {tuple(q.shape)}")
+    if (k is None) != (k_out is None):
+        raise ValueError(f"{names[1]} and {names[3]} must be given together")
+    views = [_heads(t, q, n) for t, n in zip((q, k, q_out, k_out), names)]
+    _on_current_device(q, k, q_out, k_out)
+    return views
+
+
+def _same_heads(a: Optional[tb_heads], b: Optional[tb_heads], name: str) -> None:
+    if a is not None and a.heads != b.heads:
+        raise ValueError(f"{name} must have {a.heads} heads, got {b.heads}")
+
+
+def _rope(fn, name, q, k, q_out, k_out, names, freqs, positions, offset, interleaved, magnitude,
+          stream) -> None:
+    a, b, c, d = _pairs(q, k, q_out, k_out, names)
+    _same_heads(a, c, names[2])
+    _same_heads(b, d, names[3])
+    ang = _angles(q, freqs, positions, offset, interleaved, magnitude)
+    batch, seq, _, dim = q.shape
+    _check(name, fn(_ref(a), _ref(b), _ref(c), _ref(d), batch, seq, dim, ctypes.byref(ang),
+                    _dtype(q), _stream(stream)))
+
+
+def tb_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_out: torch.Tensor,
+            k_out: Optional[torch.Tensor], freqs: torch.Tensor,
+            positions: Optional[torch.Tensor] = None, offset: int = 0, interleaved: bool = False,
+            magnitude: float = 1.0, stream=None) -> None:
+    """Rotary positions on [batch, seq, heads, head_dim] queries and keys (any strides but the
+    last). ``positions``: int64 [batch, seq] or [seq]; None counts from ``offset``. An output
+    may be its own input."""
+    _rope(lib.tb_rope, "tb_rope", q, k, q_out, k_out, ("q", "k", "q_out", "k_out"), freqs,
+          positions, offset, interleaved, magnitude, stream)
+
+
+def tb_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], dq: torch.Tensor,
+                dk: Optional[torch.Tensor], freqs: torch.Tensor,
+                positions: Optional[torch.Tensor] = None, offset: int = 0,
+                interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
+    """Gradient of tb_rope: the transposed rotation of dq_out and dk_out."""
+    _rope(lib.tb_rope_bwd, "tb_rope_bwd", dq_out, dk_out, dq, dk, ("dq_out", "dk_out", "dq", "dk"),
+          freqs, positions, offset, interleaved, magnitude, stream)
+
+
+def _gamma(g: Optional[torch.Tensor], dim: int, name: str) -> Optional[int]:
+    if g is None:
+        raise ValueError(f"{name} is missing")
+    _want(g, dim, torch.float32, name)
+    return _ptr(g)
+
+
+def tb_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], gamma_q: torch.Tensor,
+                    gamma_k: Optional[torch.Tensor], q_out: torch.Tensor,
+                    k_out: Optional[torch.Tensor], inv_rms_q: Optional[torch.Tensor] = None,
+                    inv_rms_k: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                    freqs: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                    offset: int = 0, interleaved: bool = False, magnitude: float = 1.0,
+                    stream=None) -> None:
+    """RMS norm of every head of q and k, then tb_rope, in one pass. inv_rms_q and inv_rms_k
+    (fp32, batch * seq * heads values) receive what tb_qk_norm_rope_bwd needs; leave them out
+    when serving. Without ``freqs`` the heads are normalised and not rotated."""
+    a, b, c, d = _pairs(q, k, q_out, k_out, ("q", "k", "q_out", "k_out"))
+    _same_heads(a, c, "q_out")
+    _same_heads(b, d, "k_out")
+    ang = _angles(q, freqs, positions, offset, interleaved, magnitude)
+    batch, seq, _, dim = q.shape
+    gq = _gamma(gamma_q, dim, "gamma_q")
+    gk = _gamma(gamma_k, dim, "gamma_k") if k is not None else None
+    if inv_rms_q is not None:
+        _want(inv_rms_q, batch * seq * a.heads, torch.float32, "inv_rms_q")
+    if inv_rms_k is not None:
+        _want(inv_rms_k, batch * seq * (b.heads if b is not None else 0), torch.float32, "inv_rms_k")
+    _check("tb_qk_norm_rope",
+           lib.tb_qk_norm_rope(_ref(a), _ref(b), gq, gk, float(eps), _ref(c), _ref(d),
+                               _ptr(inv_rms_q), _ptr(inv_rms_k), batch, seq, dim,
+                               ctypes.byref(ang), _dtype(q), _stream(stream)))
+
+
+def tb_qk_norm_rope_bwd_workspace_size(batch: int, seq: int, heads_q: int, heads_k: int,
+                                       head_dim: int, dtype: torch.dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check("tb_qk_norm_rope_bwd_workspace_size",
+           lib.tb_qk_norm_rope_bwd_workspace_size(int(batch), int(seq), int(heads_q), int(heads_k),
+                                                  int(head_dim), _DTYPE[dtype], ctypes.byref(out)))
+    return out.value
+
+
+def tb_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: torch.Tensor,
+                        k: Optional[torch.Tensor], inv_rms_q: torch.Tensor,
+                        inv_rms_k: Optional[torch.Tensor], gamma_q: torch.Tensor,
+                        gamma_k: Optional[torch.Tensor], dq: torch.Tensor,
+                        dk: Optional[torch.Tensor], dgamma_q: torch.Tensor,
+                        dgamma_k: Optional[torch.Tensor], freqs: Optional[torch.Tensor] = None,
+                        positions: Optional[torch.Tensor] = None, offset: int = 0,
+                        interleaved: bool = False, magnitude: float = 1.0,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradient of tb_qk_norm_rope: dq, dk and the (overwritten) dgamma_q, dgamma_k."""
+    a, b, c, d = _pairs(q, k, dq, dk, ("q", "k", "dq", "dk"))
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out must be given together")
+    ya, yb = _heads(dq_out, q, "dq_out"), _heads(dk_out, q, "dk_out")
+    _on_current_device(dq_out, dk_out)
+    for x, name in ((c, "dq"), (ya, "dq_out")):
+        _same_heads(a, x, name)
+    for x, name in ((d, "dk"), (yb, "dk_out")):
+        _same_heads(b, x, name)
+    ang = _angles(q, freqs, positions, offset, interleaved, magnitude)
+    batch, seq, _, dim = q.shape
+    gq, sq = _gamma(gamma_q, dim, "gamma_q"), _gamma(dgamma_q, dim, "dgamma_q")
+    gk, sk = (None, None) if k is None else (_gamma(gamma_k, dim, "gamma_k"),
+                                             _gamma(dgamma_k, dim, "dgamma_k"))
+    _want(inv_rms_q, batch * seq * a.heads, torch.float32, "inv_rms_q")
+    if k is not None:
+        if inv_rms_k is None:
+            raise ValueError("inv_rms_k is missing")
+        _want(inv_rms_k, batch * seq * b.heads, torch.float32, "inv_rms_k")
+    ws_ptr = _ptr(workspace) if workspace is not None else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("tb_qk_norm_rope_bwd",
+           lib.tb_qk_norm_rope_bwd(_ref(ya), _ref(yb), _ref(a), _ref(b), _ptr(inv_rms_q),
+                                   _ptr(inv_rms_k) if k is not None else None, gq, gk, _ref(c),
+                                   _ref(d), sq, sk, batch, seq, dim, ctypes.byref(ang), _dtype(q),
+                                   ws_ptr, ws_bytes, _stream(stream)))
