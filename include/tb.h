@@ -594,6 +594,70 @@ tb_status tb_qk_norm_rope_bwd(const tb_heads* dq_out, const tb_heads* dk_out,
                               const tb_rope_angles* angles, tb_dtype dtype,
                               void* workspace, size_t workspace_bytes, void* stream);
 
+/* ======================================================================== */
+/* Softmax cross entropy of a linear output layer                            */
+/* ======================================================================== */
+/*
+ * The loss at a decoder's output without its logits in memory.  With hidden states
+ * H [rows, D] and output weights W [vocab, D], logits l = H W^T:
+ *     lse  = log sum_v exp(l_v)
+ *     loss = lse - l[target]
+ * and, for the gradient dloss of each row's loss,
+ *     G  = dloss * (exp(l - lse) - onehot(target))
+ *     dH = G W,   dW = G^T H
+ * The loss keeps the logits in accumulators only; the gradient forms them again, one
+ * piece of the vocabulary at a time, and holds one piece of G (rounded to dtype) in the
+ * workspace, at most about 256 MiB unless rows exceeds 65,536.  (The pages take the
+ * softmax backward on stored probabilities: tb_softmax_bwd.)
+ *
+ * A row whose target is ignore_index takes no part: its loss is +0, its G is 0 (whatever
+ * its logits are), its dH is 0 where W is finite, and it adds 0 * H to dW, so its H has to
+ * be finite.  Its lse is written.  A target outside [0, vocab) that is not ignore_index
+ * gives a loss of NaN and the G of an ignored row, and the forward call sets the device
+ * error word to TB_ERR_INVALID_VALUE (tb_device_error).  A logit of +inf gives lse = +inf.
+ *
+ * tb_linear_xent
+ *   H, W             device [rows, D] and [vocab, D], TB_BF16 or TB_F16, 16-byte aligned
+ *   targets          device int64 [rows]
+ *   loss, lse        out: fp32 [rows]
+ *   ignore_index     any value; -100 is usual
+ *   workspace        device scratch of tb_linear_xent_workspace_size() bytes, 16-byte
+ *                    aligned, contents ignored.  Calls that may run at the same time need
+ *                    workspaces of their own, and so do graphs that may.
+ * tb_linear_xent_bwd
+ *   dloss            fp32 [rows]: gradient of each row's loss (for a mean over the rows
+ *                    that count, 1 / their number)
+ *   lse              what the forward call wrote
+ *   dH, dW           out: [rows, D] and [vocab, D] in dtype, overwritten; either may be
+ *                    NULL when it is not wanted
+ * Sums are fp32.  Results are bitwise reproducible on one device model.  TB_F16: G is
+ * held scaled by a power of two that puts the largest finite |dloss| into [2^14, 2^15), so
+ * small probabilities keep their digits; the scale is undone before dH and dW are rounded.
+ * D not a multiple of 8 costs a padded copy of H and W in the workspace per call.
+ * Results must not overlap inputs, each other or the workspace.  rows == 0 writes zeros to
+ * dW and nothing else.
+ * Errors: TB_ERR_INVALID_VALUE (null or negative; D or vocab below 1; rows, D or vocab of
+ * 2^31 - 511 or more, rows * D or vocab * D above 2^40; dH and dW both NULL),
+ * TB_ERR_UNSUPPORTED_DTYPE (TB_F32 has no such tensor-core product), TB_ERR_MISALIGNED,
+ * TB_ERR_ALIAS, TB_ERR_WORKSPACE, TB_ERR_CUDA.
+ */
+tb_status tb_linear_xent_workspace_size(int64_t rows, int64_t D, int64_t vocab,
+                                        tb_dtype dtype, size_t* bytes);
+
+tb_status tb_linear_xent(const void* H, const void* W, const int64_t* targets,
+                         float* loss, float* lse, int64_t rows, int64_t D, int64_t vocab,
+                         int64_t ignore_index, tb_dtype dtype,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+tb_status tb_linear_xent_bwd_workspace_size(int64_t rows, int64_t D, int64_t vocab,
+                                            tb_dtype dtype, size_t* bytes);
+
+tb_status tb_linear_xent_bwd(const float* dloss, const void* H, const void* W,
+                             const int64_t* targets, const float* lse, void* dH, void* dW,
+                             int64_t rows, int64_t D, int64_t vocab, int64_t ignore_index,
+                             tb_dtype dtype, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

@@ -32,7 +32,8 @@ EXPORTS = ("tb_status_string", "tb_version", "tb_device_error", "tb_adamw_plan_c
            "tb_cast_to_f32", "tb_cast_from_f32", "tb_layernorm_bwd_selftest_timeout",
            "tb_adamw_step_device", "tb_adamw_selftest_stale_counter", "tb_rope_freqs", "tb_rope",
            "tb_rope_bwd", "tb_qk_norm_rope", "tb_qk_norm_rope_bwd_workspace_size",
-           "tb_qk_norm_rope_bwd")
+           "tb_qk_norm_rope_bwd", "tb_linear_xent_workspace_size", "tb_linear_xent",
+           "tb_linear_xent_bwd_workspace_size", "tb_linear_xent_bwd")
 
 
 class TbError(RuntimeError):
@@ -136,6 +137,14 @@ def _load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.tb_qk_norm_rope_bwd.argtypes = [heads, heads, heads, heads, vp, vp, vp, vp, heads, heads,
                                         vp, vp, i64, i64, i64, angles, i32, vp, ctypes.c_size_t, vp]
     lib.tb_qk_norm_rope_bwd.restype = i32
+    for fn in (lib.tb_linear_xent_workspace_size, lib.tb_linear_xent_bwd_workspace_size):
+        fn.argtypes = [i64, i64, i64, i32, ctypes.POINTER(ctypes.c_size_t)]
+        fn.restype = i32
+    lib.tb_linear_xent.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, vp, ctypes.c_size_t, vp]
+    lib.tb_linear_xent.restype = i32
+    lib.tb_linear_xent_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, vp,
+                                       ctypes.c_size_t, vp]
+    lib.tb_linear_xent_bwd.restype = i32
     return lib
 
 
@@ -644,3 +653,65 @@ def tb_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q:
                                    _ptr(inv_rms_k) if k is not None else None, gq, gk, _ref(c),
                                    _ref(d), sq, sk, batch, seq, dim, ctypes.byref(ang), _dtype(q),
                                    ws_ptr, ws_bytes, _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- output layer's loss
+def _xent_sizes(H: torch.Tensor, W: torch.Tensor, targets: torch.Tensor):
+    if H.dim() != 2 or W.dim() != 2 or H.shape[1] != W.shape[1] or H.dtype != W.dtype:
+        raise ValueError("H [rows, D] and W [vocab, D] must share D and dtype, got "
+                         f"{tuple(H.shape)} {H.dtype} and {tuple(W.shape)} {W.dtype}")
+    rows, D = H.shape
+    _want(targets, rows, torch.int64, "targets")
+    return rows, D, W.shape[0]
+
+
+def _workspace_size(fn, name: str, *sizes) -> int:
+    out = ctypes.c_size_t(0)
+    _check(name, fn(*sizes, ctypes.byref(out)))
+    return out.value
+
+
+def tb_linear_xent_workspace_size(rows: int, D: int, vocab: int, dtype: torch.dtype) -> int:
+    return _workspace_size(lib.tb_linear_xent_workspace_size, "tb_linear_xent_workspace_size",
+                           int(rows), int(D), int(vocab), _DTYPE[dtype])
+
+
+def tb_linear_xent_bwd_workspace_size(rows: int, D: int, vocab: int, dtype: torch.dtype) -> int:
+    return _workspace_size(lib.tb_linear_xent_bwd_workspace_size,
+                           "tb_linear_xent_bwd_workspace_size", int(rows), int(D), int(vocab),
+                           _DTYPE[dtype])
+
+
+def tb_linear_xent(H: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, loss: torch.Tensor,
+                   lse: torch.Tensor, workspace: Optional[torch.Tensor], ignore_index: int = -100,
+                   stream=None) -> None:
+    """loss[r] = logsumexp(H[r] W^T) - (H[r] W^T)[targets[r]], without the logits in memory;
+    0 where targets[r] is ignore_index. lse receives the log sums for tb_linear_xent_bwd."""
+    rows, D, vocab = _xent_sizes(H, W, targets)
+    _want(loss, rows, torch.float32, "loss")
+    _want(lse, rows, torch.float32, "lse")
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("tb_linear_xent",
+           lib.tb_linear_xent(_ptr(H), _ptr(W), _ptr(targets), _ptr(loss), _ptr(lse), rows, D,
+                              vocab, int(ignore_index), _dtype(H), _ptr(workspace), ws_bytes,
+                              _stream(stream)))
+
+
+def tb_linear_xent_bwd(dloss: torch.Tensor, H: torch.Tensor, W: torch.Tensor, targets: torch.Tensor,
+                       lse: torch.Tensor, dH: Optional[torch.Tensor], dW: Optional[torch.Tensor],
+                       workspace: Optional[torch.Tensor], ignore_index: int = -100,
+                       stream=None) -> None:
+    """Gradients of tb_linear_xent: dH and dW (overwritten; None: not wanted) from dloss, the
+    gradient of each row's loss."""
+    rows, D, vocab = _xent_sizes(H, W, targets)
+    _want(dloss, rows, torch.float32, "dloss")
+    _want(lse, rows, torch.float32, "lse")
+    if dH is not None:
+        _want(dH, rows * D, H.dtype, "dH")
+    if dW is not None:
+        _want(dW, vocab * D, H.dtype, "dW")
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("tb_linear_xent_bwd",
+           lib.tb_linear_xent_bwd(_ptr(dloss), _ptr(H), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dH),
+                                  _ptr(dW), rows, D, vocab, int(ignore_index), _dtype(H),
+                                  _ptr(workspace), ws_bytes, _stream(stream)))
