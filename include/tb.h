@@ -603,18 +603,18 @@ tb_status tb_qk_norm_rope_bwd(const tb_heads* dq_out, const tb_heads* dk_out,
  *     lse  = log sum_v exp(l_v)
  *     loss = lse - l[target]
  * and, for the gradient dloss of each row's loss,
- *     G  = dloss * (exp(l - lse) - onehot(target))
- *     dH = G W,   dW = G^T H
+ *     G  = exp(l - lse) - onehot(target)
+ *     dH = dloss * (G W),   dW = G^T (dloss * H)
  * The loss keeps the logits in accumulators only; the gradient forms them again, one
  * piece of the vocabulary at a time, and holds one piece of G (rounded to dtype) in the
  * workspace, at most about 256 MiB unless rows exceeds 65,536.  (The pages take the
  * softmax backward on stored probabilities: tb_softmax_bwd.)
  *
- * A row whose target is ignore_index takes no part: its loss is +0, its G is 0 (whatever
- * its logits are), its dH is 0 where W is finite, and it adds 0 * H to dW, so its H has to
- * be finite.  Its lse is written.  A target outside [0, vocab) that is not ignore_index
- * gives a loss of NaN and the G of an ignored row, and the forward call sets the device
- * error word to TB_ERR_INVALID_VALUE (tb_device_error).  A logit of +inf gives lse = +inf.
+ * A row whose target is ignore_index takes no part, whatever its H is: its loss is +0, its
+ * dH is 0 and it adds nothing to dW.  Its lse is written.  A target outside [0, vocab) that
+ * is not ignore_index gives a loss of NaN and the gradient of an ignored row, and the forward
+ * call sets the device error word to TB_ERR_INVALID_VALUE (tb_device_error).  A row with a
+ * dloss of 0 takes no part in the gradient either.  A logit of +inf gives lse = +inf.
  *
  * tb_linear_xent
  *   H, W             device [rows, D] and [vocab, D], TB_BF16 or TB_F16, 16-byte aligned
@@ -630,9 +630,10 @@ tb_status tb_qk_norm_rope_bwd(const tb_heads* dq_out, const tb_heads* dk_out,
  *   lse              what the forward call wrote
  *   dH, dW           out: [rows, D] and [vocab, D] in dtype, overwritten; either may be
  *                    NULL when it is not wanted
- * Sums are fp32.  Results are bitwise reproducible on one device model.  TB_F16: G is
- * held scaled by a power of two that puts the largest finite |dloss| into [2^14, 2^15), so
- * small probabilities keep their digits; the scale is undone before dH and dW are rounded.
+ * Sums are fp32.  Results are bitwise reproducible on one device model.  Two values are
+ * rounded to dtype on the way: G, and for dW the rows of H times dloss / max |dloss| (exact
+ * where every dloss is the same, as for a mean).  TB_F16 holds G times 2^14, so that
+ * probabilities down to 2^-38 count.
  * D not a multiple of 8 costs a padded copy of H and W in the workspace per call.
  * Results must not overlap inputs, each other or the workspace.  rows == 0 writes zeros to
  * dW and nothing else.

@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
+from array import array
 from typing import Optional, Sequence
 
 import torch
@@ -121,7 +123,8 @@ def _load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.tb_layernorm_bwd_selftest_timeout.restype = i32
     lib.tb_adamw_selftest_stale_counter.argtypes = [vp, ctypes.c_uint64, vp]
     lib.tb_adamw_selftest_stale_counter.restype = i32
-    heads, angles = ctypes.POINTER(tb_heads), ctypes.POINTER(tb_rope_angles)
+    # tb_heads* and tb_rope_angles*: the binding passes addresses into one packed array
+    heads = angles = vp
     lib.tb_rope_freqs.argtypes = [i32, ctypes.c_double, ctypes.POINTER(tb_rope_scaling), vp,
                                   ctypes.POINTER(f32)]
     lib.tb_rope_freqs.restype = i32
@@ -160,8 +163,16 @@ def _check(fn: str, code: int) -> None:
         raise TbError(fn, code)
 
 
+# What torch.cuda.current_device() and current_stream() call, without the lazy initialisation
+# (a CUDA tensor exists by then) and the Stream object: a microsecond or two less per call.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -175,9 +186,9 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
         return None
     if not t.is_cuda:
         raise ValueError("tensors passed to libtb must be CUDA tensors")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != _current_device():
         raise ValueError(f"tensor on {t.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+                         f"cuda:{_current_device()}")
     if not t.is_contiguous():
         raise ValueError("tensors passed to libtb must be contiguous")
     return t.data_ptr() if t.numel() > 0 else (t.data_ptr() or None)
@@ -472,86 +483,112 @@ def tb_rope_freqs(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
     return table.to("cuda" if device is None else device), magnitude.value
 
 
-def _heads(t: Optional[torch.Tensor], like: torch.Tensor, name: str) -> Optional[tb_heads]:
-    """[batch, seq, heads, head_dim] with any strides but the last one's."""
-    if t is None:
-        return None
-    if t.dim() != 4 or t.shape[:2] != like.shape[:2] or t.shape[3] != like.shape[3]:
-        raise ValueError(f"{name} must be [batch, seq, heads, head_dim] with the batch, seq and "
-                         f"head_dim of the queries, got {tuple(t.shape)}")
-    if t.dtype != like.dtype:
-        raise ValueError(f"{name} must be {like.dtype} like the queries, got {t.dtype}")
-    sb, ss, sh, sd = t.stride()
-    if sd != 1 and t.shape[3] > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    return tb_heads(t.data_ptr() or None, sb, ss, sh, t.shape[2])
+_HEADS_BYTES = ctypes.sizeof(tb_heads)        # five 8-byte fields
+assert _HEADS_BYTES == 40 and ctypes.sizeof(tb_rope_angles) == 48
 
 
-def _on_current_device(*tensors: Optional[torch.Tensor]) -> None:
-    """As _ptr checks it, for tensors that need not be contiguous."""
-    current = None
-    for t in tensors:
+class _HeadsCall:
+    """The tb_heads of a call's tensors and its tb_rope_angles, packed into one array of 64-bit
+    words. Small calls take a few microseconds on the GPU, so this path makes no ctypes objects:
+    a struct each would cost more than the kernel."""
+
+    __slots__ = ("words", "at", "batch", "seq", "dim", "dtype", "device", "heads")
+
+    def __init__(self, q: torch.Tensor, name: str):
+        shape = q.shape
+        if len(shape) != 4:
+            raise ValueError(f"{name} must be [batch, seq, heads, head_dim], got {tuple(shape)}")
+        self.batch, self.seq, _, self.dim = shape
+        self.dtype, self.device, self.words, self.heads = q.dtype, q.get_device(), [], []
+
+    def add(self, t: Optional[torch.Tensor], name: str, like: Optional[int] = None) -> None:
+        """Checks a tensor against the queries (and `like`, an earlier one, for its heads)."""
         if t is None:
-            continue
-        if not t.is_cuda:
+            self.words += (0, 0, 0, 0, 0)
+            self.heads.append(None)
+            return
+        shape = t.shape
+        if len(shape) != 4 or shape[0] != self.batch or shape[1] != self.seq or shape[3] != self.dim:
+            raise ValueError(f"{name} must be [batch, seq, heads, head_dim] with the batch, seq and "
+                             f"head_dim of the queries, got {tuple(shape)}")
+        if t.dtype != self.dtype:
+            raise ValueError(f"{name} must be {self.dtype} like the queries, got {t.dtype}")
+        sb, ss, sh, sd = t.stride()
+        if sd != 1 and self.dim > 1:
+            raise ValueError(f"the last dimension of {name} must be contiguous")
+        heads = shape[2]
+        if like is not None and self.heads[like] != heads:
+            raise ValueError(f"{name} must have {self.heads[like]} heads, got {heads}")
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} is on {t.device}, the queries on another device")
+        self.words += (t.data_ptr(), sb, ss, sh, heads)
+        self.heads.append(heads)
+
+    def angles(self, freqs: Optional[torch.Tensor], positions: Optional[torch.Tensor], offset: int,
+               interleaved: bool, magnitude: float) -> None:
+        if self.device < 0:
             raise ValueError("tensors passed to libtb must be CUDA tensors")
-        if current is None:
-            current = torch.cuda.current_device()
-        if t.device.index != current:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{current}")
+        if self.device != _current_device():
+            raise ValueError(f"tensor on cuda:{self.device}, but the current device is "
+                             f"cuda:{_current_device()}")
+        rot, table, where, stride = 0, 0, 0, 0
+        if freqs is not None:
+            if freqs.dtype != torch.int64 or freqs.dim() != 1 or not freqs.is_contiguous():
+                raise ValueError("freqs must be the int64 table of tb_rope_freqs")
+            if freqs.get_device() != self.device:
+                raise ValueError(f"freqs is on {freqs.device}, the queries on cuda:{self.device}")
+            rot, table = 2 * freqs.numel(), freqs.data_ptr()
+        if positions is not None:
+            if positions.dtype != torch.int64 or positions.get_device() != self.device:
+                raise ValueError("positions must be an int64 tensor on the queries' device")
+            shape, strides = tuple(positions.shape), positions.stride()
+            if shape != (self.batch, self.seq) and shape != (self.seq,):
+                raise ValueError(f"positions must be [{self.batch}, {self.seq}] or [{self.seq}], got "
+                                 f"{shape}")
+            if self.seq > 1 and strides[-1] != 1:
+                raise ValueError("the last dimension of positions must be contiguous")
+            where = positions.data_ptr()
+            if len(shape) == 2 and self.batch > 1:
+                stride = strides[0]
+        size = _float_bits(magnitude) if magnitude != 1.0 else 0x3F800000
+        self.words += (table, where, stride, int(offset), rot | (bool(interleaved) << 32), size)
+        self.words = array("q", self.words)
+        self.at = self.words.buffer_info()[0]
+
+    def __call__(self, i: int) -> Optional[int]:
+        """Address of the i-th tensor's tb_heads; None for a tensor that was not given."""
+        return None if self.heads[i] is None else self.at + i * _HEADS_BYTES
+
+    def angles_at(self) -> int:
+        return self.at + len(self.heads) * _HEADS_BYTES
+
+    def code(self) -> int:
+        try:
+            return _DTYPE[self.dtype]
+        except KeyError:
+            raise TbError("dtype", 2) from None
 
 
-def _angles(q: torch.Tensor, freqs: Optional[torch.Tensor], positions: Optional[torch.Tensor],
-            offset: int, interleaved: bool, magnitude: float) -> tb_rope_angles:
-    rotary_dim, table = 0, None
-    if freqs is not None:
-        if freqs.dtype != torch.int64 or freqs.dim() != 1:
-            raise ValueError("freqs must be the int64 table of tb_rope_freqs")
-        rotary_dim, table = 2 * freqs.numel(), _ptr(freqs)
-    where, stride = None, 0
-    if positions is not None:
-        if positions.dtype != torch.int64 or not positions.is_cuda or positions.device != q.device:
-            raise ValueError("positions must be an int64 tensor on the queries' device")
-        batch, seq = q.shape[:2]
-        if positions.shape != (batch, seq) and positions.shape != (seq,):
-            raise ValueError(f"positions must be [{batch}, {seq}] or [{seq}], got "
-                             f"{tuple(positions.shape)}")
-        if seq > 1 and positions.stride(-1) != 1:
-            raise ValueError("the last dimension of positions must be contiguous")
-        where = positions.data_ptr() or None
-        stride = positions.stride(0) if positions.dim() == 2 and batch > 1 else 0
-    return tb_rope_angles(table, where, stride, int(offset), rotary_dim, int(bool(interleaved)),
-                          float(magnitude))
+def _float_bits(x: float) -> int:
+    return struct.unpack("<i", struct.pack("<f", float(x)))[0] & 0xFFFFFFFF
 
 
-def _ref(s):
-    return None if s is None else ctypes.byref(s)
-
-
-def _pairs(q, k, q_out, k_out, names):
-    if q.dim() != 4:
-        raise ValueError(f"{names[0]} must be [batch, seq, heads, head_dim], got {tuple(q.shape)}")
-    if (k is None) != (k_out is None):
-        raise ValueError(f"{names[1]} and {names[3]} must be given together")
-    views = [_heads(t, q, n) for t, n in zip((q, k, q_out, k_out), names)]
-    _on_current_device(q, k, q_out, k_out)
-    return views
-
-
-def _same_heads(a: Optional[tb_heads], b: Optional[tb_heads], name: str) -> None:
-    if a is not None and a.heads != b.heads:
-        raise ValueError(f"{name} must have {a.heads} heads, got {b.heads}")
+def _together(a, b, names) -> None:
+    if (a is None) != (b is None):
+        raise ValueError(f"{names[0]} and {names[1]} must be given together")
 
 
 def _rope(fn, name, q, k, q_out, k_out, names, freqs, positions, offset, interleaved, magnitude,
           stream) -> None:
-    a, b, c, d = _pairs(q, k, q_out, k_out, names)
-    _same_heads(a, c, names[2])
-    _same_heads(b, d, names[3])
-    ang = _angles(q, freqs, positions, offset, interleaved, magnitude)
-    batch, seq, _, dim = q.shape
-    _check(name, fn(_ref(a), _ref(b), _ref(c), _ref(d), batch, seq, dim, ctypes.byref(ang),
-                    _dtype(q), _stream(stream)))
+    c = _HeadsCall(q, names[0])
+    _together(k, k_out, (names[1], names[3]))
+    c.add(q, names[0])
+    c.add(k, names[1])
+    c.add(q_out, names[2], 0)
+    c.add(k_out, names[3], 1)
+    c.angles(freqs, positions, offset, interleaved, magnitude)
+    _check(name, fn(c(0), c(1), c(2), c(3), c.batch, c.seq, c.dim, c.angles_at(), c.code(),
+                    _stream(stream)))
 
 
 def tb_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_out: torch.Tensor,
@@ -591,21 +628,24 @@ def tb_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], gamma_q: torch.T
     """RMS norm of every head of q and k, then tb_rope, in one pass. inv_rms_q and inv_rms_k
     (fp32, batch * seq * heads values) receive what tb_qk_norm_rope_bwd needs; leave them out
     when serving. Without ``freqs`` the heads are normalised and not rotated."""
-    a, b, c, d = _pairs(q, k, q_out, k_out, ("q", "k", "q_out", "k_out"))
-    _same_heads(a, c, "q_out")
-    _same_heads(b, d, "k_out")
-    ang = _angles(q, freqs, positions, offset, interleaved, magnitude)
-    batch, seq, _, dim = q.shape
-    gq = _gamma(gamma_q, dim, "gamma_q")
-    gk = _gamma(gamma_k, dim, "gamma_k") if k is not None else None
+    c = _HeadsCall(q, "q")
+    _together(k, k_out, ("k", "k_out"))
+    c.add(q, "q")
+    c.add(k, "k")
+    c.add(q_out, "q_out", 0)
+    c.add(k_out, "k_out", 1)
+    c.angles(freqs, positions, offset, interleaved, magnitude)
+    gq = _gamma(gamma_q, c.dim, "gamma_q")
+    gk = _gamma(gamma_k, c.dim, "gamma_k") if k is not None else None
+    tokens = c.batch * c.seq
     if inv_rms_q is not None:
-        _want(inv_rms_q, batch * seq * a.heads, torch.float32, "inv_rms_q")
+        _want(inv_rms_q, tokens * c.heads[0], torch.float32, "inv_rms_q")
     if inv_rms_k is not None:
-        _want(inv_rms_k, batch * seq * (b.heads if b is not None else 0), torch.float32, "inv_rms_k")
+        _want(inv_rms_k, tokens * (c.heads[1] or 0), torch.float32, "inv_rms_k")
     _check("tb_qk_norm_rope",
-           lib.tb_qk_norm_rope(_ref(a), _ref(b), gq, gk, float(eps), _ref(c), _ref(d),
-                               _ptr(inv_rms_q), _ptr(inv_rms_k), batch, seq, dim,
-                               ctypes.byref(ang), _dtype(q), _stream(stream)))
+           lib.tb_qk_norm_rope(c(0), c(1), gq, gk, float(eps), c(2), c(3), _ptr(inv_rms_q),
+                               _ptr(inv_rms_k), c.batch, c.seq, c.dim, c.angles_at(), c.code(),
+                               _stream(stream)))
 
 
 def tb_qk_norm_rope_bwd_workspace_size(batch: int, seq: int, heads_q: int, heads_k: int,
@@ -627,32 +667,31 @@ def tb_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q:
                         interleaved: bool = False, magnitude: float = 1.0,
                         workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """Gradient of tb_qk_norm_rope: dq, dk and the (overwritten) dgamma_q, dgamma_k."""
-    a, b, c, d = _pairs(q, k, dq, dk, ("q", "k", "dq", "dk"))
-    if (k is None) != (dk_out is None):
-        raise ValueError("k and dk_out must be given together")
-    ya, yb = _heads(dq_out, q, "dq_out"), _heads(dk_out, q, "dk_out")
-    _on_current_device(dq_out, dk_out)
-    for x, name in ((c, "dq"), (ya, "dq_out")):
-        _same_heads(a, x, name)
-    for x, name in ((d, "dk"), (yb, "dk_out")):
-        _same_heads(b, x, name)
-    ang = _angles(q, freqs, positions, offset, interleaved, magnitude)
-    batch, seq, _, dim = q.shape
-    gq, sq = _gamma(gamma_q, dim, "gamma_q"), _gamma(dgamma_q, dim, "dgamma_q")
-    gk, sk = (None, None) if k is None else (_gamma(gamma_k, dim, "gamma_k"),
-                                             _gamma(dgamma_k, dim, "dgamma_k"))
-    _want(inv_rms_q, batch * seq * a.heads, torch.float32, "inv_rms_q")
+    c = _HeadsCall(q, "q")
+    _together(k, dk, ("k", "dk"))
+    _together(k, dk_out, ("k", "dk_out"))
+    c.add(q, "q")
+    c.add(k, "k")
+    c.add(dq, "dq", 0)
+    c.add(dk, "dk", 1)
+    c.add(dq_out, "dq_out", 0)
+    c.add(dk_out, "dk_out", 1)
+    c.angles(freqs, positions, offset, interleaved, magnitude)
+    tokens = c.batch * c.seq
+    gq, sq = _gamma(gamma_q, c.dim, "gamma_q"), _gamma(dgamma_q, c.dim, "dgamma_q")
+    _want(inv_rms_q, tokens * c.heads[0], torch.float32, "inv_rms_q")
+    gk = sk = rk = None
     if k is not None:
+        gk, sk = _gamma(gamma_k, c.dim, "gamma_k"), _gamma(dgamma_k, c.dim, "dgamma_k")
         if inv_rms_k is None:
             raise ValueError("inv_rms_k is missing")
-        _want(inv_rms_k, batch * seq * b.heads, torch.float32, "inv_rms_k")
-    ws_ptr = _ptr(workspace) if workspace is not None else None
+        _want(inv_rms_k, tokens * c.heads[1], torch.float32, "inv_rms_k")
+        rk = _ptr(inv_rms_k)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check("tb_qk_norm_rope_bwd",
-           lib.tb_qk_norm_rope_bwd(_ref(ya), _ref(yb), _ref(a), _ref(b), _ptr(inv_rms_q),
-                                   _ptr(inv_rms_k) if k is not None else None, gq, gk, _ref(c),
-                                   _ref(d), sq, sk, batch, seq, dim, ctypes.byref(ang), _dtype(q),
-                                   ws_ptr, ws_bytes, _stream(stream)))
+           lib.tb_qk_norm_rope_bwd(c(4), c(5), c(0), c(1), _ptr(inv_rms_q), rk, gq, gk, c(2), c(3),
+                                   sq, sk, c.batch, c.seq, c.dim, c.angles_at(), c.code(),
+                                   _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 # ----------------------------------------------------------------------------- output layer's loss

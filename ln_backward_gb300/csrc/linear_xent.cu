@@ -1,7 +1,7 @@
 // linear_xent.cu -- softmax cross entropy of a linear output layer, and its gradients.
 //
 //     l = H W^T,  lse = log sum_v exp(l_v),  loss = lse - l[target]
-//     G = dloss * (exp(l - lse) - onehot(target)),  dH = G W,  dW = G^T H
+//     G = exp(l - lse) - onehot(target),  dH = dloss * (G W),  dW = G^T (dloss * H)
 //
 // H [N, D] hidden states, W [V, D] output weights, 16-bit.  The N x V logits exist only as
 // accumulator tiles in tensor memory: the loss folds each tile into a running maximum and
@@ -21,6 +21,12 @@
 // The operands need no transposed copies: dH contracts over the vocabulary, along which W
 // is not contiguous, and dW over the tokens, along which neither G nor H is; those operands
 // are staged as 64-column boxes and described to the MMA as MN-major.
+//
+// dloss stays out of the 16-bit G: 1 / rows, the usual dloss, has a rounding of its own that
+// every entry of G would share (bf16 1/7168 is 0.19% off, and dH and dW were).  dH takes it in
+// fp32 in the epilogue; dW contracts over the rows, so there H is scaled beforehand, by
+// dloss / max |dloss|, which is exactly 1 for a mean.  That copy also holds zeros for the rows
+// that take no part, whatever their H is.
 //
 // Every mbarrier wait is bounded (about one second of %globaltimer); on expiry the device
 // error word is set and the CTAs drain what they issued and return.
@@ -190,8 +196,8 @@ struct Product {
     float2* part;             // kLse: [n_tiles][rows] maximum and sum
     float* target_logit;      // kLse: [rows]
     const float* lse;         // kGrad
-    const float* dloss;
-    const float* scale;       // kGrad, kDH, kDW: {scale of G, its inverse} or NULL
+    const float* weight;      // kDH: dloss by row, 0 where a row takes no part
+    const float* top;         // kDW: the largest |dloss|
     void* g;                  // kGrad: [rows][ldg]
     int ldg;
     // kDH, kDW
@@ -199,6 +205,19 @@ struct Product {
     int first, last;          // piece: starts the sums; writes the result
     void* out;                // [rows][cols] 16-bit
 };
+
+// fp16's G is held times 2^14, so that probabilities down to 2^-38 stay above its last step;
+// the products undo it in fp32.  bf16 has fp32's range.
+template <class Fmt>
+constexpr float kGBits = std::is_same<Fmt, F16>::value ? 14.f : 0.f;
+template <class Fmt>
+constexpr float kGScale = std::is_same<Fmt, F16>::value ? 16384.f : 1.f;
+
+// An element of dH; a row of weight 0 takes no part, whatever its sums are.
+template <class Fmt>
+__device__ __forceinline__ float weigh(float sum, float weight) {
+    return weight == 0.f ? 0.f : sum * (1.f / kGScale<Fmt>) * weight;
+}
 
 // Row tiles in groups of kGroup, the group's tiles column by column: the pairs that run
 // together share few column tiles and reuse the group's rows.
@@ -370,13 +389,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     } else if (warp >= kEpiWarp) {
         const int quad = warp - kEpiWarp;             // TMEM lanes 32 quad .. 32 quad + 31
         const uint32_t leader_empty = map_to(acc_empty, 0);
-        float out_scale = 1.f, g_scale = 1.f;
-        if constexpr (K != kLse) {
-            if (p.scale) {
-                g_scale = p.scale[0];
-                out_scale = p.scale[1];
-            }
-        }
+        const float top_weight = K == kDW ? *p.top : 1.f;
         int n = 0;
         for (int t = pair; t < tiles; t += pairs, ++n) {
             int split, mt, nt;
@@ -390,6 +403,9 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             // what the row needs, on its way before the accumulator is done
             int hit = -1;                             // the target's column in this tile
             float lse2 = 0.f, weight = 0.f;
+            if constexpr (K == kDH) {
+                if (live) weight = p.weight[row];
+            }
             if constexpr (K == kLse || K == kGrad) {
                 if (live) {
                     const int64_t tg = p.target[row];
@@ -397,9 +413,8 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     const int64_t c = tg - (K == kGrad ? p.b_base : 0) - n0;
                     if (counts && c >= 0 && c < width) hit = (int)c;
                     if constexpr (K == kGrad) {
-                        lse2 = p.lse[row] * kLog2e;
-                        weight = counts ? p.dloss[row] * g_scale : 0.f;
-                        if (!counts) lse2 = __int_as_float(0x7f800000);   // exp(l - inf) = 0
+                        lse2 = p.lse[row] * kLog2e - kGBits<Fmt>;
+                        weight = counts ? 1.f : 0.f;
                     }
                 }
             }
@@ -435,9 +450,9 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const float e = exp2_fast(fmaf(v[i], kLog2e, -lse2));
-                        v[i] = (c + i == hit ? e - 1.f : e) * weight;
+                        v[i] = c + i == hit ? e - kGScale<Fmt> : e;
                     }
-                    if (weight == 0.f) {              // no NaN from a row that takes no part
+                    if (weight == 0.f) {              // a row that takes no part
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.f;
                     }
@@ -469,7 +484,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     if (live && p.last && p.splits == 1) {
                         T* out = static_cast<T*>(p.out);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] *= out_scale;
+                        for (int i = 0; i < 32; ++i) v[i] = weigh<Fmt>(v[i], weight);
                         store16<Fmt>(out + (int64_t)row * p.cols, col, p.cols,
                                      (p.cols & 7) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0, v);
                     }
@@ -477,7 +492,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     T* out = static_cast<T*>(p.out);
                     if (live) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] *= out_scale;
+                        for (int i = 0; i < 32; ++i) v[i] = v[i] * (1.f / kGScale<Fmt>) * top_weight;
                         store16<Fmt>(out + (int64_t)row * p.cols, n0 + c, p.cols,
                                      (p.cols & 7) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0, v);
                     }
@@ -535,44 +550,68 @@ join_kernel(const float2* part, const float* target_logit, const int64_t* target
     }
 }
 
-// fp16 only: G is scaled by a power of two that brings the largest |dloss| to [2^14, 2^15),
-// so that small probabilities stay above fp16's 2^-24; the products undo it in fp32.
-__global__ void __launch_bounds__(1024)
-scale_kernel(const float* dloss, int64_t rows, float* scale) {
-    __shared__ float sh[32];
+// What the gradient needs of dloss: each row's weight (0 where it takes no part), the largest
+// magnitude among them, and H with every row times its weight over that.  Each CTA finds the
+// maximum by itself (rows * 12 bytes from L2), which saves a launch.
+template <class Fmt>
+__global__ void __launch_bounds__(256)
+weigh_kernel(const float* dloss, const int64_t* target, int64_t ignore, int vocab, int64_t rows,
+             const typename Fmt::T* H, int cols, int ld, typename Fmt::T* scaled, float* weight, float* top) {
+    __shared__ float sh[8];
     pdl_wait();
     pdl_trigger();
+    auto weight_of = [&](int64_t r) {
+        const int64_t t = target[r];
+        return t != ignore && t >= 0 && t < vocab ? dloss[r] : 0.f;
+    };
     float m = 0.f;
-    for (int64_t i = threadIdx.x; i < rows; i += 1024) {
-        const float v = fabsf(dloss[i]);
-        if (v <= 3.4028235e38f) m = fmaxf(m, v);      // neither infinite nor NaN
+#pragma unroll 4
+    for (int64_t r = threadIdx.x; r < rows; r += 256) {
+        const float w = weight_of(r);
+        if (blockIdx.x == 0) weight[r] = w;
+        if (fabsf(w) <= 3.4028235e38f) m = fmaxf(m, fabsf(w));   // neither infinite nor NaN
     }
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < 32; ++i) m = fmaxf(m, sh[i]);
-        int e = 0;
-        if (m > 0.f) {
-            frexpf(m, &e);                            // m in [2^(e-1), 2^e)
-            e = min(max(15 - e, -126), 126);
+    m = sh[0];
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, sh[i]);
+    if (m == 0.f) m = 1.f;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *top = m;
+    if (!scaled) return;
+    if (cols == ld) {                 // whole 16-byte vectors
+        const int per_row = ld / 8;
+        const int64_t n = rows * per_row;
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+            const float w = weight_of(i / per_row);
+            float f[8];
+            unpack8<Fmt>(reinterpret_cast<const uint4*>(H)[i], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = w == 0.f ? 0.f : f[e] * (w / m);
+            reinterpret_cast<uint4*>(scaled)[i] = pack8<Fmt>(f);
         }
-        scale[0] = ldexpf(1.f, e);
-        scale[1] = ldexpf(1.f, -e);
+    } else {
+        const int64_t n = rows * ld;
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+            const int64_t r = i / ld;
+            const int c = (int)(i - r * ld);
+            const float w = weight_of(r);
+            scaled[i] = Fmt::from_f32(c < cols && w != 0.f ? Fmt::to_f32(H[r * cols + c]) * (w / m) : 0.f);
+        }
     }
 }
 
 // Sums the splits of dH and rounds once.
 template <class Fmt>
 __global__ void __launch_bounds__(256)
-join_dh_kernel(const float* sums, int splits, int64_t n, const float* scale, typename Fmt::T* out) {
+join_dh_kernel(const float* sums, int splits, int64_t n, int cols, const float* weight,
+               typename Fmt::T* out) {
     pdl_wait();
     pdl_trigger();
-    const float f = scale ? scale[1] : 1.f;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         float v = 0.f;
         for (int s = 0; s < splits; ++s) v += sums[s * n + i];
-        out[i] = Fmt::from_f32(v * f);
+        out[i] = Fmt::from_f32(weigh<Fmt>(v, weight[i / cols]));
     }
 }
 
@@ -650,7 +689,7 @@ struct Cut {
     int64_t ldg;
     int splits;               // of dH's contraction
     // byte offsets into the workspace
-    size_t off_h, off_w, off_g, off_sums, off_scale, off_part, off_logit, total;
+    size_t off_h, off_w, off_scaled, off_weight, off_g, off_sums, off_top, off_part, off_logit, total;
 };
 
 // Parts of the vocabulary that dH's products are split into: as many as fill the machine
@@ -696,7 +735,9 @@ Cut cut_call(int64_t n, int64_t d, int64_t v, bool bwd, int sms) {
         c.splits = pick_splits(ceil_div(n, kTile), ceil_div(d, kTile), c.piece / kStageK, sms / 2);
         c.off_g = take((size_t)n * c.ldg * 2);
         if (c.pieces > 1 || c.splits > 1) c.off_sums = take((size_t)c.splits * n * d * sizeof(float));
-        c.off_scale = take(2 * sizeof(float));
+        c.off_scaled = take((size_t)n * c.ld * 2);
+        c.off_weight = take((size_t)n * sizeof(float));
+        c.off_top = take(sizeof(float));
     }
     c.total = at;
     return c;
@@ -797,16 +838,19 @@ tb_status run_grad(const Problem& q, const Cut& c) {
         H = q.ws + c.off_h;
         W = q.ws + c.off_w;
     }
-    float* scale = nullptr;
-    if (!bf) {
-        scale = reinterpret_cast<float*>(q.ws + c.off_scale);
-        if (launch_pdl(scale_kernel, dim3(1), dim3(1024), 0, q.st, q.dloss, q.n, scale) != cudaSuccess)
-            return TB_ERR_CUDA;
-    }
+    float* weight = reinterpret_cast<float*>(q.ws + c.off_weight);
+    float* top = reinterpret_cast<float*>(q.ws + c.off_top);
+    using T = typename Fmt::T;
+    T* scaled = reinterpret_cast<T*>(q.ws + c.off_scaled);
+    const int64_t copy_ctas = q.dW ? ceil_div(q.n * c.ld, 256 * 8 * 4) : 1;
+    if (launch_pdl(weigh_kernel<Fmt>, dim3((unsigned)std::min<int64_t>(copy_ctas, (int64_t)q.sms * 4)), dim3(256),
+                   0, q.st, q.dloss, q.target, q.ignore, (int)q.v, q.n, static_cast<const T*>(q.H), (int)q.d,
+                   (int)c.ld, q.dW ? scaled : (T*)nullptr, weight, top) != cudaSuccess)
+        return TB_ERR_CUDA;
     void* g = q.ws + c.off_g;
     CUtensorMap h_rows, w_rows, h_cols, w_cols, g_rows, g_cols;
     if (!make_map(&h_rows, H, q.n, q.d, c.ld, kHalf, bf) || !make_map(&w_rows, W, q.v, q.d, c.ld, kHalf, bf) ||
-        !make_map(&h_cols, H, q.n, q.d, c.ld, kStageK, bf) || !make_map(&w_cols, W, q.v, q.d, c.ld, kStageK, bf))
+        !make_map(&h_cols, scaled, q.n, q.d, c.ld, kStageK, bf) || !make_map(&w_cols, W, q.v, q.d, c.ld, kStageK, bf))
         return TB_ERR_CUDA;
     for (int64_t i = 0; i < c.pieces; ++i) {
         const int64_t v0 = i * c.piece, cols = std::min(c.piece, q.v - v0);
@@ -823,8 +867,8 @@ tb_status run_grad(const Problem& q, const Cut& c) {
         p.ignore = q.ignore;
         p.vocab = (int)q.v;
         p.lse = q.lse_in;
-        p.dloss = q.dloss;
-        p.scale = scale;
+        p.weight = weight;
+        p.top = top;
         p.g = g;
         p.ldg = (int)c.ldg;
         tb_status s = launch_product<Fmt, kGrad>(h_rows, w_rows, p, q.st);
@@ -863,8 +907,8 @@ tb_status run_grad(const Problem& q, const Cut& c) {
         const int64_t n = q.n * q.d, grid = std::min<int64_t>(ceil_div(n, 256), (int64_t)q.sms * 8);
         const int used = (int)std::min<int64_t>(c.splits, ceil_div(std::min(c.piece, q.v), kStageK));
         if (launch_pdl(join_dh_kernel<Fmt>, dim3((unsigned)grid), dim3(256), 0, q.st,
-                       (const float*)(q.ws + c.off_sums), used, n, (const float*)scale,
-                       static_cast<typename Fmt::T*>(q.dH)) != cudaSuccess)
+                       (const float*)(q.ws + c.off_sums), used, n, (int)q.d, (const float*)weight,
+                       static_cast<T*>(q.dH)) != cudaSuccess)
             return TB_ERR_CUDA;
     }
     return launch_status();

@@ -6,8 +6,9 @@ Bounds, with u = 2^-24 and the products of 16-bit values exact in fp32:
   2u (D + 8) sum |h w|;
 * log sum exp: the largest logit error, exp2 (2 ulp), its argument (|l - top| log2(e) u) and
   the additions of a row (at most V / 8 + 512 in a chain), and the final sum;
-* G: p off by its argument's error, rounded once to the type (half its eps), or by half of
-  fp16's last step where it is that small;
+* G = p - onehot: p off by its argument's error, rounded once to the type (half its eps), or
+  by half of fp16's last step (2^-24, under a scale of 2^14) where it is that small;
+* for dW, H times dloss / max |dloss|: another rounding to the type;
 * dH, dW: those errors through the product, and its own V (or rows) additions;
 
 and one rounding of every 16-bit result.
@@ -84,15 +85,17 @@ def check_backward(dH, dW, dloss, H, W, t, lse, ignore=-100):
     p = (l - lse.double()[:, None]).exp()
     p_err = p * (err_l + U * (4 + 2 * (l - lse.double()[:, None]).abs() + 2 * lse.double().abs()[:, None]))
     p[torch.arange(n, device="cuda"), torch.where(keep, t, 0)] -= 1.0
-    G = p * weight[:, None]
+    G, p_err = p * weight[:, None], p_err * weight.abs()[:, None]
     half = torch.finfo(H.dtype).eps / 2
-    tiny = 2.0 ** -25 * 2.0 ** -14 * float(dloss.abs().max()) if H.dtype == HF else 0.0
-    # (scaled so that the largest |dloss| is at least 2^14, a step of 2^-24 is at most this)
-    G_err = p_err * weight[:, None] + G.abs() * (half + 2 * U) + tiny * keep[:, None]
+    tiny = 2.0 ** -25 if H.dtype == HF else 0.0
+    G_err = p_err + G.abs() * (half + 4 * U) + tiny * 2.0 ** -14 * weight.abs()[:, None]
+    # a scaled H below fp16's normal numbers is off by half a step of the largest |dloss|
+    W_err = G_err + G.abs() * (half + 2 * U)
+    H_tiny = tiny * weight.abs().max()
 
-    def check(got, A, A_err, B, terms, what):
+    def check(got, A, A_err, B, terms, what, more=0.0):
         want = A @ B
-        err = A_err @ B.abs() + (A.abs() @ B.abs()) * (2 * U * (terms + 16))
+        err = more + A_err @ B.abs() + (A.abs() @ B.abs()) * (2 * U * (terms + 16))
         room = err + (want.abs() + err) * half + (2.0 ** -25 if H.dtype == HF else 0.0)
         off = (got.double() - want).abs()
         assert (off <= room).all(), f"{what}: {(off / room).max().item():.3g} of the bound"
@@ -100,7 +103,8 @@ def check_backward(dH, dW, dloss, H, W, t, lse, ignore=-100):
     if dH is not None:
         check(dH, G, G_err, W.double(), v, "dH")
     if dW is not None:
-        check(dW, G.T, G_err.T, H.double(), n, "dW")
+        check(dW, G.T, W_err.T, torch.where(keep[:, None], H.double(), 0.0), n, "dW",
+              (p.abs().T @ keep.double()[:, None]) * H_tiny)
 
 
 # one row, one column, one element; ragged in every direction; one element over a tile; row
