@@ -531,7 +531,7 @@ tb_status tb_rope_freqs(int rotary_dim, double base, const tb_rope_scaling* scal
  *                   share no element with any input or output.  Views that walk one
  *                   buffer with the same strides are told apart exactly; views with
  *                   different strides count as sharing when their address ranges meet.
- *   batch, seq      >= 0; nothing is enqueued when either is 0.  Elements of a buffer
+ *   batch, seq      >= 0, batch * seq < 2^31; nothing is enqueued when either is 0.  Elements of a buffer
  *                   outside the views are not touched.
  *   head_dim        1 .. 1024
  *   dtype           TB_F32, TB_BF16 or TB_F16, of all four

@@ -17,13 +17,16 @@
 // so a warp forms the sines of its token once and keeps them in registers over the
 // token's heads.
 //
-// Layout.  A head is dealt to L lanes (a power of two), each holding NU "units" of two
-// vectors of E elements: the two halves' corresponding vectors in the half layout, two
-// neighbouring vectors in the interleaved one and behind rotary_dim.  Both members of
-// every pair are then in one lane: no shuffles but the norm's row sums.  32 / L heads
-// go through a warp at a time.  Queries and keys get CTAs of their own, so gamma and
-// the dgamma sums of one tensor stay in registers.  Heads whose sizes, strides or
-// pointers no vector width fits take the general kernels (one element at a time).
+// Layout.  A head is dealt to L lanes, each holding NU "units" of two vectors of E
+// elements: the two halves' corresponding vectors in the half layout, two neighbouring
+// vectors in the interleaved one and behind rotary_dim.  Both members of every pair are
+// then in one lane: no shuffles but the norm's row sums.  32 / L heads go through a warp
+// at a time; L is the number of units, not a power of two above it, so that heads of 80
+// or 96 elements leave few lanes idle.  Queries and keys get CTAs of their own, so gamma
+// and the dgamma sums of one tensor stay in registers.  A warp of the persistent grid
+// loads its next heads, of the next token too, before it works on the present ones.
+// Heads whose sizes, strides or pointers no vector width fits take the general kernels
+// (one element at a time).
 #include <math.h>
 
 #include <algorithm>
@@ -65,8 +68,9 @@ struct Args {
     const int64_t* positions;
     int64_t pos_stride;
     int64_t offset;
-    int64_t tokens, seq;
-    int head_dim, rot, log2_lanes;
+    unsigned tokens, seq;      // batch * seq < 2^31
+    int head_dim, rot;
+    int lanes;           // of a head (vector kernels)
     int interleaved;
     float magnitude;     // sines and cosines are multiplied by it
     float turn;          // +1, or -1 for the transposed rotation
@@ -144,16 +148,12 @@ __device__ __forceinline__ void rotate(float (&u)[E], float (&v)[E], const float
     }
 }
 
-__device__ __forceinline__ void split_token(const Args& a, int64_t token, int64_t* b, int64_t* s) {
-    if ((uint64_t)token < (1ull << 32) && (uint64_t)a.seq < (1ull << 32)) {
-        *b = (unsigned)token / (unsigned)a.seq;
-    } else {
-        *b = token / a.seq;
-    }
+__device__ __forceinline__ void split_token(const Args& a, unsigned token, unsigned* b, unsigned* s) {
+    *b = token / a.seq;
     *s = token - *b * a.seq;
 }
 
-__device__ __forceinline__ long long position(const Args& a, int64_t b, int64_t s) {
+__device__ __forceinline__ long long position(const Args& a, unsigned b, unsigned s) {
     return (a.positions ? (long long)__ldg(a.positions + b * a.pos_stride + s) : (long long)s) +
            a.offset;
 }
@@ -165,13 +165,12 @@ struct Units {
     int freq[NU];                // its first frequency
     bool live[NU], turns[NU];
     __device__ __forceinline__ void init(const Args& a, int sub) {
-        const int lanes = 1 << a.log2_lanes;
         const int units = a.head_dim / (2 * E), rot_units = a.rot / (2 * E);
 #pragma unroll
         for (int j = 0; j < NU; ++j) {
-            const int c = sub + j * lanes;
-            live[j] = c < units;
-            turns[j] = c < rot_units;
+            const int c = sub + j * a.lanes;
+            live[j] = sub < a.lanes && c < units;
+            turns[j] = live[j] && c < rot_units;
             const bool half = turns[j] && !a.interleaved;
             first[j] = half ? c * E : 2 * c * E;
             second[j] = half ? a.rot / 2 + c * E : 2 * c * E + E;
@@ -196,9 +195,17 @@ __device__ __forceinline__ void angles(const Args& a, const Units<E, NU>& u, lon
     }
 }
 
-__device__ __forceinline__ float sum_lanes(float v, int log2_lanes) {
-    for (int i = 0; i < log2_lanes; ++i) v += __shfl_xor_sync(0xffffffffu, v, 1 << i);
-    return v;
+// Sum over a head's `lanes` lanes, in all of them.
+__device__ __forceinline__ float sum_lanes(float v, int lanes, int sub) {
+    if ((lanes & (lanes - 1)) == 0) {
+        for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+    for (int o = 16; o; o >>= 1) {
+        const float w = __shfl_down_sync(0xffffffffu, v, o);
+        if (sub + o < min(lanes, 2 * o)) v += w;
+    }
+    return __shfl_sync(0xffffffffu, v, (int)(threadIdx.x & 31) - sub);
 }
 
 template <int E, int NU>
@@ -213,91 +220,124 @@ __device__ __forceinline__ void load_gamma(const float* gamma, const Units<E, NU
         }
 }
 
+// Where a warp is: a head group of one token.
+template <class T>
+struct Cursor {
+    unsigned item, token;
+    int h0, h_end;
+    const T *x, *dy;
+    T* y;
+    __device__ __forceinline__ void open(const Args& a, const HeadsArg& t, int per_step, long long* pos) {
+        int chunk = 0;
+        token = item;
+        if (t.chunks > 1) {
+            token = item / (unsigned)t.chunks;
+            chunk = (int)(item - token * t.chunks);
+        }
+        unsigned b, s;
+        split_token(a, token, &b, &s);
+        x = static_cast<const T*>(t.x) + b * t.sx.b + s * t.sx.s;
+        dy = static_cast<const T*>(t.dy) + b * t.sdy.b + s * t.sdy.s;
+        y = static_cast<T*>(t.y) + b * t.sy.b + s * t.sy.s;
+        h0 = chunk * t.steps * per_step;
+        h_end = min(t.heads, h0 + t.steps * per_step);
+        *pos = position(a, b, s);
+    }
+};
+
+template <class Fmt, int E, int NU>
+struct Head {                      // one lane's vectors of a head
+    Chunk<Fmt, E> p[NU], q[NU];
+    __device__ __forceinline__ void load(const typename Fmt::T* head, const Units<E, NU>& u, bool mine) {
+#pragma unroll
+        for (int j = 0; j < NU; ++j) {
+            p[j].raw = {};
+            q[j].raw = {};
+            if (mine && u.live[j]) {
+                p[j].load(head + u.first[j]);
+                q[j].load(head + u.second[j]);
+            }
+        }
+    }
+};
+
 // ---------------------------------------------------------------- forward
 template <class Fmt, int E, int NU, int Mode>
-__global__ void __launch_bounds__(kThreads) heads_fwd_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, NU == 1 ? 3 : 2) heads_fwd_kernel(const __grid_constant__ Args a) {
     using T = typename Fmt::T;
     const int which = (int)blockIdx.x >= a.t[0].ctas;
     const HeadsArg& t = a.t[which];
     const int cta = (int)blockIdx.x - (which ? a.t[0].ctas : 0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane & ((1 << a.log2_lanes) - 1), grp = lane >> a.log2_lanes;
-    const int per_step = 32 >> a.log2_lanes;
+    const int per_step = 32 / a.lanes, grp = lane / a.lanes, sub = lane - grp * a.lanes;
     Units<E, NU> u;
-    u.init(a, sub);
+    u.init(a, grp < per_step ? sub : a.lanes);
     pdl_wait();
     pdl_trigger();
-    float g[NU][2 * E];
+    const unsigned items = a.tokens * t.chunks;
+    Cursor<T> cur;
+    cur.item = cta * kWarps + warp;
+    if (cur.item >= items) return;
+    long long pos;
+    cur.open(a, t, per_step, &pos);
+    Head<Fmt, E, NU> in;
+    in.load(cur.x + (cur.h0 + grp) * t.sx.h, u, cur.h0 + grp < cur.h_end);
+    float g[NU][2 * E], c[NU][E], sn[NU][E];
     if constexpr (Mode == kNorm) load_gamma<E, NU>(t.gamma, u, g);
-
-    const int64_t items = a.tokens * t.chunks;
-    for (int64_t item = (int64_t)cta * kWarps + warp; item < items; item += (int64_t)t.ctas * kWarps) {
-        int64_t token = item, b, s;
-        int chunk = 0;
-        if (t.chunks > 1) {
-            token = item / t.chunks;
-            chunk = (int)(item - token * t.chunks);
+    bool fresh = true, more = true;
+    while (more) {
+        Cursor<T> nxt = cur;
+        long long pos_nxt = pos;
+        bool fresh_nxt = false;
+        nxt.h0 += per_step;
+        if (nxt.h0 >= nxt.h_end) {
+            nxt.item += t.ctas * kWarps;
+            more = nxt.item < items;
+            fresh_nxt = true;
+            if (more) nxt.open(a, t, per_step, &pos_nxt);
         }
-        split_token(a, token, &b, &s);
-        const T* x = static_cast<const T*>(t.x) + b * t.sx.b + s * t.sx.s;
-        T* y = static_cast<T*>(t.y) + b * t.sy.b + s * t.sy.s;
-        float c[NU][E], sn[NU][E];
-        angles<Fmt, E, NU>(a, u, position(a, b, s), c, sn);
+        Head<Fmt, E, NU> ahead;
+        ahead.load(nxt.x + (nxt.h0 + grp) * t.sx.h, u, more && nxt.h0 + grp < nxt.h_end);
+        if (fresh) angles<Fmt, E, NU>(a, u, pos, c, sn);
 
-        constexpr int kAhead = 2;   // head groups loaded together
-        const int h_end = min(t.heads, (chunk + 1) * t.steps * per_step);
-        for (int h0 = chunk * t.steps * per_step; h0 < h_end; h0 += kAhead * per_step) {
-            Chunk<Fmt, E> p[kAhead][NU], q[kAhead][NU];
+        const int h = cur.h0 + grp;
+        const bool mine = h < cur.h_end && grp < per_step;
+        float r = 1.f;
+        if constexpr (Mode == kNorm) {
+            float ss = 0.f;
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int h = h0 + k * per_step + grp;
+            for (int j = 0; j < NU; ++j) {
+                float v[E], w[E];
+                in.p[j].get(v);
+                in.q[j].get(w);
 #pragma unroll
-                for (int j = 0; j < NU; ++j) {
-                    p[k][j].raw = {};
-                    q[k][j].raw = {};
-                    if (h < h_end && u.live[j]) {
-                        p[k][j].load(x + h * t.sx.h + u.first[j]);
-                        q[k][j].load(x + h * t.sx.h + u.second[j]);
-                    }
-                }
+                for (int e = 0; e < E; ++e) ss += v[e] * v[e] + w[e] * w[e];
             }
+            r = rsqrtf(sum_lanes(ss, a.lanes, sub) * a.inv_dim + a.eps);
+            if (t.inv_rms && sub == 0 && mine) t.inv_rms[(int64_t)cur.token * t.heads + h] = r;
+        }
+        if (mine) {
+            T* y = cur.y + h * t.sy.h;
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int h = h0 + k * per_step + grp;
-                float r = 1.f;
+            for (int j = 0; j < NU; ++j) {
+                float v[E], w[E];
+                in.p[j].get(v);
+                in.q[j].get(w);
                 if constexpr (Mode == kNorm) {
-                    float ss = 0.f;
 #pragma unroll
-                    for (int j = 0; j < NU; ++j) {
-                        float v[E], w[E];
-                        p[k][j].get(v);
-                        q[k][j].get(w);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) ss += v[e] * v[e] + w[e] * w[e];
-                    }
-                    r = rsqrtf(sum_lanes(ss, a.log2_lanes) * a.inv_dim + a.eps);
-                    if (t.inv_rms && sub == 0 && h < h_end)
-                        t.inv_rms[token * t.heads + h] = r;
+                    for (int e = 0; e < E; ++e) v[e] *= r * g[j][e], w[e] *= r * g[j][E + e];
                 }
-                if (h < h_end) {
-#pragma unroll
-                    for (int j = 0; j < NU; ++j) {
-                        float v[E], w[E];
-                        p[k][j].get(v);
-                        q[k][j].get(w);
-                        if constexpr (Mode == kNorm) {
-#pragma unroll
-                            for (int e = 0; e < E; ++e) v[e] *= r * g[j][e], w[e] *= r * g[j][E + e];
-                        }
-                        if (u.turns[j]) rotate<E>(v, w, c[j], sn[j], a.interleaved);
-                        if (u.live[j]) {
-                            Chunk<Fmt, E>::store(y + h * t.sy.h + u.first[j], v);
-                            Chunk<Fmt, E>::store(y + h * t.sy.h + u.second[j], w);
-                        }
-                    }
+                if (u.turns[j]) rotate<E>(v, w, c[j], sn[j], a.interleaved);
+                if (u.live[j]) {
+                    Chunk<Fmt, E>::store(y + u.first[j], v);
+                    Chunk<Fmt, E>::store(y + u.second[j], w);
                 }
             }
         }
+        in = ahead;
+        cur = nxt;
+        pos = pos_nxt;
+        fresh = fresh_nxt;
     }
 }
 
@@ -305,71 +345,69 @@ __global__ void __launch_bounds__(kThreads) heads_fwd_kernel(const __grid_consta
 // dn = the transposed rotation of dy; xhat = x * r; dxhat = dn * gamma;
 // dx = r * (dxhat - xhat * mean(dxhat * xhat)); dgamma = sum of dn * xhat.
 template <class Fmt, int E, int NU>
-__global__ void __launch_bounds__(kThreads) heads_bwd_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 2) heads_bwd_kernel(const __grid_constant__ Args a) {
     using T = typename Fmt::T;
     extern __shared__ float sums[];   // [kWarps][head_dim]
     const int which = (int)blockIdx.x >= a.t[0].ctas;
     const HeadsArg& t = a.t[which];
     const int cta = (int)blockIdx.x - (which ? a.t[0].ctas : 0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane & ((1 << a.log2_lanes) - 1), grp = lane >> a.log2_lanes;
-    const int per_step = 32 >> a.log2_lanes;
+    const int per_step = 32 / a.lanes, grp = lane / a.lanes, sub = lane - grp * a.lanes;
     Units<E, NU> u;
-    u.init(a, sub);
+    u.init(a, grp < per_step ? sub : a.lanes);
     pdl_wait();
     pdl_trigger();
-    float g[NU][2 * E], acc[NU][2 * E];
-    load_gamma<E, NU>(t.gamma, u, g);
+    float g[NU][2 * E], acc[NU][2 * E], c[NU][E], sn[NU][E];
 #pragma unroll
     for (int j = 0; j < NU; ++j)
 #pragma unroll
         for (int e = 0; e < 2 * E; ++e) acc[j][e] = 0.f;
 
-    const int64_t items = a.tokens * t.chunks;
-    for (int64_t item = (int64_t)cta * kWarps + warp; item < items; item += (int64_t)t.ctas * kWarps) {
-        int64_t token = item, b, s;
-        int chunk = 0;
-        if (t.chunks > 1) {
-            token = item / t.chunks;
-            chunk = (int)(item - token * t.chunks);
-        }
-        split_token(a, token, &b, &s);
-        const T* x = static_cast<const T*>(t.x) + b * t.sx.b + s * t.sx.s;
-        const T* dy = static_cast<const T*>(t.dy) + b * t.sdy.b + s * t.sdy.s;
-        T* dx = static_cast<T*>(t.y) + b * t.sy.b + s * t.sy.s;
-        float c[NU][E], sn[NU][E];
-        angles<Fmt, E, NU>(a, u, position(a, b, s), c, sn);
-
-        const int h_end = min(t.heads, (chunk + 1) * t.steps * per_step);
-        for (int h0 = chunk * t.steps * per_step; h0 < h_end; h0 += per_step) {
-            const int h = h0 + grp;
-            const bool mine = h < h_end;
-            Chunk<Fmt, E> px[NU], qx[NU], py[NU], qy[NU];
-            float r = 0.f;
-#pragma unroll
-            for (int j = 0; j < NU; ++j) {
-                px[j].raw = {};
-                qx[j].raw = {};
-                py[j].raw = {};
-                qy[j].raw = {};
-                if (mine && u.live[j]) {
-                    px[j].load(x + h * t.sx.h + u.first[j]);
-                    qx[j].load(x + h * t.sx.h + u.second[j]);
-                    py[j].load(dy + h * t.sdy.h + u.first[j]);
-                    qy[j].load(dy + h * t.sdy.h + u.second[j]);
-                }
+    const unsigned items = a.tokens * t.chunks;
+    Cursor<T> cur;
+    cur.item = cta * kWarps + warp;
+    bool more = cur.item < items;
+    if (more) {
+        long long pos;
+        cur.open(a, t, per_step, &pos);
+        Head<Fmt, E, NU> x, dy;
+        float r = 0.f;
+        auto load = [&](const Cursor<T>& at, bool any, Head<Fmt, E, NU>& hx, Head<Fmt, E, NU>& hdy, float& hr) {
+            const int h = at.h0 + grp;
+            const bool mine = any && h < at.h_end && grp < per_step;
+            hx.load(at.x + h * t.sx.h, u, mine);
+            hdy.load(at.dy + h * t.sdy.h, u, mine);
+            hr = mine ? __ldg(t.inv_rms + (int64_t)at.token * t.heads + h) : 0.f;
+        };
+        load(cur, true, x, dy, r);
+        load_gamma<E, NU>(t.gamma, u, g);
+        bool fresh = true;
+        while (more) {
+            Cursor<T> nxt = cur;
+            long long pos_nxt = pos;
+            bool fresh_nxt = false;
+            nxt.h0 += per_step;
+            if (nxt.h0 >= nxt.h_end) {
+                nxt.item += t.ctas * kWarps;
+                more = nxt.item < items;
+                fresh_nxt = true;
+                if (more) nxt.open(a, t, per_step, &pos_nxt);
             }
-            if (mine) r = __ldg(t.inv_rms + token * t.heads + h);
+            Head<Fmt, E, NU> x_ahead, dy_ahead;
+            float r_ahead;
+            load(nxt, more, x_ahead, dy_ahead, r_ahead);
+            if (fresh) angles<Fmt, E, NU>(a, u, pos, c, sn);
+
             float dot = 0.f;
             float d0[NU][E], d1[NU][E];
 #pragma unroll
             for (int j = 0; j < NU; ++j) {
-                py[j].get(d0[j]);
-                qy[j].get(d1[j]);
+                dy.p[j].get(d0[j]);
+                dy.q[j].get(d1[j]);
                 if (u.turns[j]) rotate<E>(d0[j], d1[j], c[j], sn[j], a.interleaved);
                 float v[E], w[E];
-                px[j].get(v);
-                qx[j].get(w);
+                x.p[j].get(v);
+                x.q[j].get(w);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     const float m0 = d0[j][e] * (v[e] * r), m1 = d1[j][e] * (w[e] * r);
@@ -378,24 +416,32 @@ __global__ void __launch_bounds__(kThreads) heads_bwd_kernel(const __grid_consta
                     dot += m0 * g[j][e] + m1 * g[j][E + e];
                 }
             }
-            const float m = sum_lanes(dot, a.log2_lanes) * a.inv_dim * r;   // mean * r
-            if (mine) {
+            const float m = sum_lanes(dot, a.lanes, sub) * a.inv_dim * r;   // mean * r
+            const int h = cur.h0 + grp;
+            if (h < cur.h_end && grp < per_step) {
+                T* dx = cur.y + h * t.sy.h;
 #pragma unroll
                 for (int j = 0; j < NU; ++j) {
                     float v[E], w[E];
-                    px[j].get(v);
-                    qx[j].get(w);
+                    x.p[j].get(v);
+                    x.q[j].get(w);
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
                         v[e] = r * (d0[j][e] * g[j][e] - v[e] * m);
                         w[e] = r * (d1[j][e] * g[j][E + e] - w[e] * m);
                     }
                     if (u.live[j]) {
-                        Chunk<Fmt, E>::store(dx + h * t.sy.h + u.first[j], v);
-                        Chunk<Fmt, E>::store(dx + h * t.sy.h + u.second[j], w);
+                        Chunk<Fmt, E>::store(dx + u.first[j], v);
+                        Chunk<Fmt, E>::store(dx + u.second[j], w);
                     }
                 }
             }
+            x = x_ahead;
+            dy = dy_ahead;
+            r = r_ahead;
+            cur = nxt;
+            pos = pos_nxt;
+            fresh = fresh_nxt;
         }
     }
 
@@ -405,7 +451,7 @@ __global__ void __launch_bounds__(kThreads) heads_bwd_kernel(const __grid_consta
 #pragma unroll
         for (int e = 0; e < 2 * E; ++e) {
             float v = acc[j][e];
-            for (int m = 16; m >= (1 << a.log2_lanes); m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+            for (int k = 1; k < per_step; ++k) v += __shfl_sync(0xffffffffu, acc[j][e], (sub + k * a.lanes) & 31);
             if (grp == 0 && u.live[j])
                 sums[warp * a.head_dim + (e < E ? u.first[j] + e : u.second[j] + e - E)] = v;
         }
@@ -449,11 +495,11 @@ __global__ void __launch_bounds__(kThreads) heads_general_kernel(const __grid_co
         __syncwarp();
     }
     const int pairs = pair_count(a);
-    const int64_t items = a.tokens * t.chunks;
-    for (int64_t item = cta; item < items; item += t.ctas) {
-        const int64_t token = item / t.chunks;
+    const unsigned items = a.tokens * t.chunks;
+    for (unsigned item = cta; item < items; item += t.ctas) {
+        const unsigned token = item / (unsigned)t.chunks;
         const int chunk = (int)(item - token * t.chunks);
-        int64_t b, s;
+        unsigned b, s;
         split_token(a, token, &b, &s);
         const long long pos = position(a, b, s);
         __syncthreads();   // the previous token's sines have been read
@@ -475,8 +521,8 @@ __global__ void __launch_bounds__(kThreads) heads_general_kernel(const __grid_co
                         const float v = Fmt::to_f32(x[d]);
                         ss += v * v;
                     }
-                    r = rsqrtf(sum_lanes(ss, 5) * a.inv_dim + a.eps);
-                    if (t.inv_rms && lane == 0) t.inv_rms[token * t.heads + h] = r;
+                    r = rsqrtf(sum_lanes(ss, 32, lane) * a.inv_dim + a.eps);
+                    if (t.inv_rms && lane == 0) t.inv_rms[(int64_t)token * t.heads + h] = r;
                 }
                 for (int p = lane; p < pairs; p += 32) {
                     const Pair e = pair_at(a, p);
@@ -493,7 +539,7 @@ __global__ void __launch_bounds__(kThreads) heads_general_kernel(const __grid_co
                 }
             } else {
                 const T* dy = dt + h * t.sdy.h;
-                const float r = __ldg(t.inv_rms + token * t.heads + h);
+                const float r = __ldg(t.inv_rms + (int64_t)token * t.heads + h);
                 float dot = 0.f;
                 for (int p = lane; p < pairs; p += 32) {
                     const Pair e = pair_at(a, p);
@@ -510,7 +556,7 @@ __global__ void __launch_bounds__(kThreads) heads_general_kernel(const __grid_co
                     sums[e.i] += m;
                     dot += m * __ldg(t.gamma + e.i);
                 }
-                const float m = sum_lanes(dot, 5) * a.inv_dim * r;
+                const float m = sum_lanes(dot, 32, lane) * a.inv_dim * r;
                 for (int p = lane; p < pairs; p += 32) {
                     const Pair e = pair_at(a, p);
                     float u = Fmt::to_f32(dy[e.i]), v = 0.f, xk = 0.f;
@@ -683,38 +729,32 @@ bool fits(const View& v, int E, size_t es) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Warps that a forward launch wants before one warp takes all heads of a token: about
-// two waves of 16 warps an SM.  Below it a token's heads are shared by several warps,
-// which each form the token's sines again.
-constexpr int64_t kFwdWarpsPerSm = 32;
-
+// Head groups of one token that a warp takes: all, so that it forms the token's sines once,
+// unless that would leave warps of the resident grid without work.
 template <class Fmt, int E, int NU>
 tb_status launch_vec(Args a, const Call& c, int sms, cudaStream_t st) {
     const int units = a.head_dim / (2 * E);
-    int l2 = 0;
-    while ((NU << l2) < units) ++l2;
-    a.log2_lanes = l2;
-    const int per_step = 32 >> l2;
+    a.lanes = (int)ceil_div(units, NU);
+    const int per_step = 32 / a.lanes;
     const void* kernel =
         c.bwd_norm ? reinterpret_cast<const void*>(&heads_bwd_kernel<Fmt, E, NU>)
         : c.norm   ? reinterpret_cast<const void*>(&heads_fwd_kernel<Fmt, E, NU, kNorm>)
                    : reinterpret_cast<const void*>(&heads_fwd_kernel<Fmt, E, NU, kRope>);
     const size_t smem = c.bwd_norm ? sizeof(float) * kWarps * a.head_dim : 0;
-    const int per_sm = std::min(resident_ctas_per_sm(kernel, kThreads, smem), kBwdCtasPerSm);
-    if (per_sm == 0) return TB_ERR_CUDA;
+    const int resident = resident_ctas_per_sm(kernel, kThreads, smem);
+    if (resident == 0) return TB_ERR_CUDA;
+    const int64_t grid_ctas = (int64_t)sms * (c.bwd_norm ? std::min(resident, kBwdCtasPerSm) : resident);
     int64_t all_steps = 0;
     for (int i = 0; i < c.n; ++i) all_steps += ceil_div(a.t[i].heads, per_step);
     for (int i = 0; i < c.n; ++i) {
         HeadsArg& t = a.t[i];
         const int64_t steps = ceil_div(t.heads, per_step);
-        const int64_t want = ceil_div(sms * kFwdWarpsPerSm, a.tokens);
-        t.chunks = (int)std::min(steps, std::max<int64_t>(1, want));
+        // the tensor's share of the grid, by its head groups
+        const int64_t share = std::max<int64_t>(1, grid_ctas * steps / all_steps);
+        t.chunks = (int)std::min(steps, ceil_div(share * kWarps, a.tokens));
         t.steps = (int)ceil_div(steps, t.chunks);
         t.chunks = (int)ceil_div(steps, t.steps);
-        int64_t ctas = ceil_div(a.tokens * t.chunks, kWarps);
-        if (c.bwd_norm)   // a persistent grid: its CTAs are dealt by the tensors' heads
-            ctas = std::min(ctas, std::max<int64_t>(1, (int64_t)sms * per_sm * steps / all_steps));
-        t.ctas = (int)std::min<int64_t>(ctas, INT32_MAX / 4);
+        t.ctas = (int)std::min(share, ceil_div(a.tokens * t.chunks, kWarps));
     }
     if (c.n == 1) a.t[1].ctas = 0;
     if (c.bwd_norm) a.t[1].partial = a.t[0].partial + (int64_t)a.t[0].ctas * a.head_dim;
@@ -842,7 +882,7 @@ tb_status run(const Entry& e, int64_t batch, int64_t seq, int64_t dim, const tb_
     tb_status why = check_angles(r, dim, batch, seq);
     if (why != TB_OK) return why;
     const size_t es = dtype_size(dtype);
-    if (batch > 0 && seq > (INT64_MAX >> 24) / batch) return TB_ERR_INVALID_VALUE;
+    if (batch > 0 && seq > INT32_MAX / batch) return TB_ERR_INVALID_VALUE;
     const int64_t tokens = batch * seq;
 
     Call c{};
@@ -967,8 +1007,8 @@ tb_status run(const Entry& e, int64_t batch, int64_t seq, int64_t dim, const tb_
     a.positions = r->positions;
     a.pos_stride = batch > 1 ? r->positions_stride : 0;
     a.offset = r->offset;
-    a.tokens = tokens;
-    a.seq = seq;
+    a.tokens = (unsigned)tokens;
+    a.seq = (unsigned)seq;
     a.head_dim = (int)dim;
     a.rot = r->rotary_dim;
     a.interleaved = r->layout == TB_ROPE_INTERLEAVED;
