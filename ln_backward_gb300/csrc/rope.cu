@@ -23,13 +23,18 @@
 // then in one lane: no shuffles but the norm's row sums.  32 / L heads go through a warp
 // at a time; L is the number of units, not a power of two above it, so that heads of 80
 // or 96 elements leave few lanes idle.  Queries and keys get CTAs of their own, so gamma
-// and the dgamma sums of one tensor stay in registers.  A warp of the persistent grid
-// loads its next heads, of the next token too, before it works on the present ones.
-// Heads whose sizes, strides or pointers no vector width fits take the general kernels
-// (one element at a time).
+// and the dgamma sums of one tensor stay in registers.  Heads whose sizes, strides or
+// pointers no vector width fits take the general kernels (one element at a time).
+//
+// Measured at bf16 2 x 8,192 tokens of 32 + 8 heads of 128, norm and rotation (50 us at the
+// copy bandwidth): 57.6 us.  What did not pay there: loads a group ahead in a persistent
+// grid (71 us), a ring of cp.async copies (69 us) or of bulk copies (76 us) per warp; all
+// spend on addresses and bookkeeping what they save in waiting, and the kernel is bound by
+// issue slots first.
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "tb_common.cuh"
 
@@ -77,28 +82,68 @@ struct Args {
     float eps, inv_dim;
 };
 
-// ---------------------------------------------------------------- vectors
+// ---------------------------------------------------------------- packed fp32
+// Two fp32 values in one 64-bit register pair: the packed multiply and FMA do both in one issue
+// slot, each rounded as the scalar one is.  Issue slots bound these kernels before HBM does.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void split(F2 a, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 swap(F2 a) {
+    float lo, hi;
+    split(a, lo, hi);
+    return f2(hi, lo);
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// ---------------------------------------------------------------- one lane's part of a head
 template <int Bytes> struct Raw;
 template <> struct Raw<16> { using V = uint4; };
 template <> struct Raw<8> { using V = uint2; };
 template <> struct Raw<4> { using V = unsigned; };
 
 template <class Fmt, int E>
-struct Chunk {
+struct Chunk {                    // a vector of E elements as loaded
     using T = typename Fmt::T;
     using V = typename Raw<E * (int)sizeof(T)>::V;
     V raw;
     __device__ __forceinline__ void load(const T* p) { raw = __ldcs(reinterpret_cast<const V*>(p)); }
-    __device__ __forceinline__ void get(float (&f)[E]) const {
+    __device__ __forceinline__ void get(F2 (&f)[E / 2]) const {
         const T* h = reinterpret_cast<const T*>(&raw);
 #pragma unroll
-        for (int e = 0; e < E; ++e) f[e] = Fmt::to_f32(h[e]);
+        for (int e = 0; e < E / 2; ++e) f[e] = f2(Fmt::to_f32(h[2 * e]), Fmt::to_f32(h[2 * e + 1]));
     }
-    __device__ __forceinline__ static void store(T* p, const float (&f)[E]) {
+    __device__ __forceinline__ static void store(T* p, const F2 (&f)[E / 2]) {
         V v;
         T* h = reinterpret_cast<T*>(&v);
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] = Fmt::from_f32(f[e]);
+        for (int e = 0; e < E / 2; ++e) {
+            float lo, hi;
+            split(f[e], lo, hi);
+            if constexpr (std::is_same<Fmt, BF16>::value)
+                reinterpret_cast<__nv_bfloat162*>(h)[e] = __floats2bfloat162_rn(lo, hi);
+            else if constexpr (std::is_same<Fmt, F16>::value)
+                reinterpret_cast<__half2*>(h)[e] = __floats2half2_rn(lo, hi);
+            else
+                h[2 * e] = lo, h[2 * e + 1] = hi;
+        }
         __stcs(reinterpret_cast<V*>(p), v);
     }
 };
@@ -113,39 +158,16 @@ __device__ __forceinline__ void cos_sin(const Args& a, long long pos, unsigned l
                                         float* c, float* s) {
     const unsigned long long phase = (unsigned long long)pos * freq;
     const float half_turns = (float)(int)(phase >> 32) * 0x1p-31f * a.turn;
+    float cv, sv;
     if constexpr (sizeof(typename Fmt::T) == 2) {
         const float x = half_turns * 3.14159265358979f;
-        *c = __cosf(x);
-        *s = __sinf(x);
+        cv = __cosf(x);
+        sv = __sinf(x);
     } else {
-        sincospif(half_turns, s, c);
+        sincospif(half_turns, &sv, &cv);
     }
-    *c *= a.magnitude;
-    *s *= a.magnitude;
-}
-
-// Rotates one unit: E pairs, whose frequencies are consecutive.
-template <int E>
-__device__ __forceinline__ void rotate(float (&u)[E], float (&v)[E], const float (&c)[E],
-                                       const float (&s)[E], int interleaved) {
-    if (interleaved) {
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-            const float a0 = u[2 * e], b0 = u[2 * e + 1];
-            u[2 * e] = a0 * c[e] - b0 * s[e];
-            u[2 * e + 1] = a0 * s[e] + b0 * c[e];
-            const float a1 = v[2 * e], b1 = v[2 * e + 1];
-            v[2 * e] = a1 * c[E / 2 + e] - b1 * s[E / 2 + e];
-            v[2 * e + 1] = a1 * s[E / 2 + e] + b1 * c[E / 2 + e];
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float p = u[e], q = v[e];
-            u[e] = p * c[e] - q * s[e];
-            v[e] = p * s[e] + q * c[e];
-        }
-    }
+    *c = cv * a.magnitude;
+    *s = sv * a.magnitude;
 }
 
 __device__ __forceinline__ void split_token(const Args& a, unsigned token, unsigned* b, unsigned* s) {
@@ -164,96 +186,31 @@ struct Units {
     int first[NU], second[NU];   // element offsets of a unit's two vectors
     int freq[NU];                // its first frequency
     bool live[NU], turns[NU];
-    __device__ __forceinline__ void init(const Args& a, int sub) {
+    __device__ __forceinline__ void init(const Args& a, int sub, int lanes) {
         const int units = a.head_dim / (2 * E), rot_units = a.rot / (2 * E);
 #pragma unroll
         for (int j = 0; j < NU; ++j) {
-            const int c = sub + j * a.lanes;
-            live[j] = sub < a.lanes && c < units;
-            turns[j] = live[j] && c < rot_units;
+            const int c = sub + j * lanes;
+            live[j] = c < units;
+            turns[j] = c < rot_units;
             const bool half = turns[j] && !a.interleaved;
             first[j] = half ? c * E : 2 * c * E;
             second[j] = half ? a.rot / 2 + c * E : 2 * c * E + E;
-            freq[j] = c * E;
+            freq[j] = turns[j] ? c * E : 0;
+            if (!live[j]) first[j] = second[j] = 0;
         }
     }
 };
 
 template <class Fmt, int E, int NU>
-__device__ __forceinline__ void angles(const Args& a, const Units<E, NU>& u, long long pos,
-                                       float (&c)[NU][E], float (&s)[NU][E]) {
-#pragma unroll
-    for (int j = 0; j < NU; ++j) {
-        if (u.turns[j]) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                cos_sin<Fmt>(a, pos, __ldg(a.freqs + u.freq[j] + e), &c[j][e], &s[j][e]);
-        } else {   // behind rotary_dim: unchanged
-#pragma unroll
-            for (int e = 0; e < E; ++e) c[j][e] = 1.f, s[j][e] = 0.f;
-        }
-    }
-}
-
-// Sum over a head's `lanes` lanes, in all of them.
-__device__ __forceinline__ float sum_lanes(float v, int lanes, int sub) {
-    if ((lanes & (lanes - 1)) == 0) {
-        for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        return v;
-    }
-    for (int o = 16; o; o >>= 1) {
-        const float w = __shfl_down_sync(0xffffffffu, v, o);
-        if (sub + o < min(lanes, 2 * o)) v += w;
-    }
-    return __shfl_sync(0xffffffffu, v, (int)(threadIdx.x & 31) - sub);
-}
-
-template <int E, int NU>
-__device__ __forceinline__ void load_gamma(const float* gamma, const Units<E, NU>& u,
-                                           float (&g)[NU][2 * E]) {
-#pragma unroll
-    for (int j = 0; j < NU; ++j)
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            g[j][e] = u.live[j] ? __ldg(gamma + u.first[j] + e) : 0.f;
-            g[j][E + e] = u.live[j] ? __ldg(gamma + u.second[j] + e) : 0.f;
-        }
-}
-
-// Where a warp is: a head group of one token.
-template <class T>
-struct Cursor {
-    unsigned item, token;
-    int h0, h_end;
-    const T *x, *dy;
-    T* y;
-    __device__ __forceinline__ void open(const Args& a, const HeadsArg& t, int per_step, long long* pos) {
-        int chunk = 0;
-        token = item;
-        if (t.chunks > 1) {
-            token = item / (unsigned)t.chunks;
-            chunk = (int)(item - token * t.chunks);
-        }
-        unsigned b, s;
-        split_token(a, token, &b, &s);
-        x = static_cast<const T*>(t.x) + b * t.sx.b + s * t.sx.s;
-        dy = static_cast<const T*>(t.dy) + b * t.sdy.b + s * t.sdy.s;
-        y = static_cast<T*>(t.y) + b * t.sy.b + s * t.sy.s;
-        h0 = chunk * t.steps * per_step;
-        h_end = min(t.heads, h0 + t.steps * per_step);
-        *pos = position(a, b, s);
-    }
-};
-
-template <class Fmt, int E, int NU>
-struct Head {                      // one lane's vectors of a head
+struct Head {                     // one lane's vectors of a head; dead units read as zeros
     Chunk<Fmt, E> p[NU], q[NU];
-    __device__ __forceinline__ void load(const typename Fmt::T* head, const Units<E, NU>& u, bool mine) {
+    __device__ __forceinline__ void load(const typename Fmt::T* head, const Units<E, NU>& u) {
 #pragma unroll
         for (int j = 0; j < NU; ++j) {
             p[j].raw = {};
             q[j].raw = {};
-            if (mine && u.live[j]) {
+            if (NU == 1 || u.live[j]) {
                 p[j].load(head + u.first[j]);
                 q[j].load(head + u.second[j]);
             }
@@ -261,187 +218,360 @@ struct Head {                      // one lane's vectors of a head
     }
 };
 
+// The rotation of one unit (vectors p and q) as p' = p A + partner(p) B, where the partner of p is
+// q in the half layout and p with its neighbours swapped in the interleaved one; likewise for q.
+// The forward's gamma is in A and B (element x of a pair counts gamma(x) x), so the norm costs a
+// head no more multiplications than the rotation and its 1/rms.
+template <int E>
+struct Turn {
+    F2 a[E], b[E];                // p's E / 2 pairs of elements, then q's
+    __device__ __forceinline__ void set(const float* c, const float* s, const float (&g)[2 * E], bool turns,
+                                        bool interleaved) {
+        constexpr int H = E / 2;
+#pragma unroll
+        for (int e = 0; e < E; ++e) a[e] = f2(g[2 * e], g[2 * e + 1]), b[e] = f2(0.f);
+        if (!turns) return;
+        if (interleaved) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                a[e] = f2(c[e]) * f2(g[2 * e], g[2 * e + 1]);
+                b[e] = f2(-s[e], s[e]) * f2(g[2 * e + 1], g[2 * e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+                const F2 gp = f2(g[2 * e], g[2 * e + 1]), gq = f2(g[E + 2 * e], g[E + 2 * e + 1]);
+                const F2 cc = f2(c[2 * e], c[2 * e + 1]);
+                a[e] = gp * cc;
+                b[e] = gq * f2(-s[2 * e], -s[2 * e + 1]);
+                a[H + e] = gq * cc;
+                b[H + e] = gp * f2(s[2 * e], s[2 * e + 1]);
+            }
+        }
+    }
+    __device__ __forceinline__ void apply(F2 (&p)[E / 2], F2 (&q)[E / 2], bool turns, bool interleaved) const {
+        constexpr int H = E / 2;
+        if (!turns) {             // behind rotary_dim nothing is added, not even 0 * inf
+#pragma unroll
+            for (int e = 0; e < H; ++e) p[e] = p[e] * a[e], q[e] = q[e] * a[H + e];
+        } else if (interleaved) {
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+                p[e] = fma2(swap(p[e]), b[e], p[e] * a[e]);
+                q[e] = fma2(swap(q[e]), b[H + e], q[e] * a[H + e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+                const F2 x = p[e], y = q[e];
+                p[e] = fma2(y, b[e], x * a[e]);
+                q[e] = fma2(x, b[H + e], y * a[H + e]);
+            }
+        }
+    }
+};
+
+// Sum over a head's lanes, in all of them.  Lanes: their number where it is known when compiling
+// (a power of two), else 0.
+template <int Lanes>
+__device__ __forceinline__ float sum_lanes(float v, int lanes, int sub) {
+    if constexpr (Lanes > 0) {
+#pragma unroll
+        for (int o = 1; o < Lanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float w = __shfl_down_sync(0xffffffffu, v, o);
+        v = sub + o < min(lanes, 2 * o) ? v + w : v;
+    }
+    return __shfl_sync(0xffffffffu, v, (int)(threadIdx.x & 31) - sub);
+}
+
+// A token's cosines and sines: each lane forms those of every 32nd pair, and the lanes share them
+// through the warp's table (rotary_dim floats).
+template <class Fmt>
+__device__ __forceinline__ void fill_table(const Args& a, long long pos, float* table, int lane) {
+    const int half = a.rot / 2;
+    __syncwarp();                 // the previous token's values have been read
+    for (int i = lane; i < half; i += 32) cos_sin<Fmt>(a, pos, __ldg(a.freqs + i), &table[i], &table[half + i]);
+    __syncwarp();
+}
+
+// An item: a token, or a share of its heads.
+struct Item {
+    unsigned token, b, s;
+    int head, end;
+    __device__ __forceinline__ void open(const Args& a, const HeadsArg& t, unsigned item, int per_step) {
+        int chunk = 0;
+        token = item;
+        if (t.chunks > 1) {
+            token = item / (unsigned)t.chunks;
+            chunk = (int)(item - token * t.chunks);
+        }
+        split_token(a, token, &b, &s);
+        head = chunk * t.steps * per_step;
+        end = min(t.heads, head + t.steps * per_step);
+    }
+    template <class P>
+    __device__ __forceinline__ P row(P base, const Strides& st) const {
+        return base + b * st.b + s * st.s;
+    }
+};
+
 // ---------------------------------------------------------------- forward
-template <class Fmt, int E, int NU, int Mode>
-__global__ void __launch_bounds__(kThreads, NU == 1 ? 3 : 2) heads_fwd_kernel(const __grid_constant__ Args a) {
+template <class Fmt, int E, int NU, int Mode, int Lanes>
+__device__ __forceinline__ void heads_fwd(const Args& a, const HeadsArg& t, int cta, float* table) {
     using T = typename Fmt::T;
-    const int which = (int)blockIdx.x >= a.t[0].ctas;
-    const HeadsArg& t = a.t[which];
-    const int cta = (int)blockIdx.x - (which ? a.t[0].ctas : 0);
+    constexpr int H = E / 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per_step = 32 / a.lanes, grp = lane / a.lanes, sub = lane - grp * a.lanes;
+    const int lanes = Lanes ? Lanes : a.lanes, per_step = 32 / lanes;
+    // lanes behind the last whole head double the last one's and write nothing
+    const int grp = min(lane / lanes, per_step - 1), sub = lane % lanes;
+    const bool whole = Lanes || lane < per_step * lanes;
+    table += warp * a.rot;
     Units<E, NU> u;
-    u.init(a, grp < per_step ? sub : a.lanes);
+    u.init(a, sub, lanes);
     pdl_wait();
     pdl_trigger();
     const unsigned items = a.tokens * t.chunks;
-    Cursor<T> cur;
-    cur.item = cta * kWarps + warp;
-    if (cur.item >= items) return;
-    long long pos;
-    cur.open(a, t, per_step, &pos);
-    Head<Fmt, E, NU> in;
-    in.load(cur.x + (cur.h0 + grp) * t.sx.h, u, cur.h0 + grp < cur.h_end);
-    float g[NU][2 * E], c[NU][E], sn[NU][E];
-    if constexpr (Mode == kNorm) load_gamma<E, NU>(t.gamma, u, g);
-    bool fresh = true, more = true;
-    while (more) {
-        Cursor<T> nxt = cur;
-        long long pos_nxt = pos;
-        bool fresh_nxt = false;
-        nxt.h0 += per_step;
-        if (nxt.h0 >= nxt.h_end) {
-            nxt.item += t.ctas * kWarps;
-            more = nxt.item < items;
-            fresh_nxt = true;
-            if (more) nxt.open(a, t, per_step, &pos_nxt);
-        }
-        Head<Fmt, E, NU> ahead;
-        ahead.load(nxt.x + (nxt.h0 + grp) * t.sx.h, u, more && nxt.h0 + grp < nxt.h_end);
-        if (fresh) angles<Fmt, E, NU>(a, u, pos, c, sn);
-
-        const int h = cur.h0 + grp;
-        const bool mine = h < cur.h_end && grp < per_step;
-        float r = 1.f;
-        if constexpr (Mode == kNorm) {
-            float ss = 0.f;
+    for (unsigned i = cta * kWarps + warp; i < items; i += t.ctas * kWarps) {
+        Item at;
+        at.open(a, t, i, per_step);
+        const long long pos = position(a, at.b, at.s);
+        const T* x = at.row(static_cast<const T*>(t.x), t.sx);
+        T* y = at.row(static_cast<T*>(t.y), t.sy);
+        Turn<E> turn[NU];
+        bool fresh = true;
+        constexpr int kAhead = 2;         // head groups loaded together
+        for (int h0 = at.head; h0 < at.end; h0 += kAhead * per_step) {
+            Head<Fmt, E, NU> in[kAhead];
 #pragma unroll
-            for (int j = 0; j < NU; ++j) {
-                float v[E], w[E];
-                in.p[j].get(v);
-                in.q[j].get(w);
+            for (int k = 0; k < kAhead; ++k)
+                in[k].load(x + min(h0 + k * per_step + grp, at.end - 1) * t.sx.h, u);
+            if (fresh) {                  // (while the first heads are on their way)
+                fill_table<Fmt>(a, pos, table, lane);
 #pragma unroll
-                for (int e = 0; e < E; ++e) ss += v[e] * v[e] + w[e] * w[e];
+                for (int j = 0; j < NU; ++j) {
+                    float g[2 * E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        g[e] = Mode == kNorm ? __ldg(t.gamma + u.first[j] + e) : 1.f;
+                        g[E + e] = Mode == kNorm ? __ldg(t.gamma + u.second[j] + e) : 1.f;
+                    }
+                    turn[j].set(table + u.freq[j], table + a.rot / 2 + u.freq[j], g, u.turns[j], a.interleaved);
+                }
+                fresh = false;
             }
-            r = rsqrtf(sum_lanes(ss, a.lanes, sub) * a.inv_dim + a.eps);
-            if (t.inv_rms && sub == 0 && mine) t.inv_rms[(int64_t)cur.token * t.heads + h] = r;
-        }
-        if (mine) {
-            T* y = cur.y + h * t.sy.h;
 #pragma unroll
-            for (int j = 0; j < NU; ++j) {
-                float v[E], w[E];
-                in.p[j].get(v);
-                in.q[j].get(w);
+            for (int k = 0; k < kAhead; ++k) {
+                const int h = h0 + k * per_step + grp;
+                if (k > 0 && h - grp >= at.end) break;
+                const bool mine = whole && h < at.end;
+                F2 p[NU][H], q[NU][H];
+#pragma unroll
+                for (int j = 0; j < NU; ++j) {
+                    in[k].p[j].get(p[j]);
+                    in[k].q[j].get(q[j]);
+                }
+                float r = 1.f;
                 if constexpr (Mode == kNorm) {
+                    F2 ss = f2(0.f);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) v[e] *= r * g[j][e], w[e] *= r * g[j][E + e];
+                    for (int j = 0; j < NU; ++j)
+#pragma unroll
+                        for (int e = 0; e < H; ++e) ss = fma2(q[j][e], q[j][e], fma2(p[j][e], p[j][e], ss));
+                    float lo, hi;
+                    split(ss, lo, hi);
+                    r = rsqrtf(sum_lanes<Lanes>(lo + hi, lanes, sub) * a.inv_dim + a.eps);
+                    if (t.inv_rms && sub == 0 && mine) t.inv_rms[(int64_t)at.token * t.heads + h] = r;
                 }
-                if (u.turns[j]) rotate<E>(v, w, c[j], sn[j], a.interleaved);
-                if (u.live[j]) {
-                    Chunk<Fmt, E>::store(y + u.first[j], v);
-                    Chunk<Fmt, E>::store(y + u.second[j], w);
+#pragma unroll
+                for (int j = 0; j < NU; ++j) {
+                    turn[j].apply(p[j], q[j], u.turns[j], a.interleaved);
+                    if constexpr (Mode == kNorm) {
+#pragma unroll
+                        for (int e = 0; e < H; ++e) p[j][e] = p[j][e] * f2(r), q[j][e] = q[j][e] * f2(r);
+                    }
+                }
+                if (mine) {
+                    T* row = y + h * t.sy.h;
+#pragma unroll
+                    for (int j = 0; j < NU; ++j) {
+                        if (NU > 1 && !u.live[j]) continue;
+                        Chunk<Fmt, E>::store(row + u.first[j], p[j]);
+                        Chunk<Fmt, E>::store(row + u.second[j], q[j]);
+                    }
                 }
             }
         }
-        in = ahead;
-        cur = nxt;
-        pos = pos_nxt;
-        fresh = fresh_nxt;
     }
+}
+
+// The body is there once for the queries and once for the keys, so that a tensor's strides and
+// pointers are operands in the constant bank and not loads by a computed index.
+template <class Fmt, int E, int NU, int Mode, int Lanes>
+__global__ void __launch_bounds__(kThreads, NU == 1 ? 3 : 2) heads_fwd_kernel(const __grid_constant__ Args a) {
+    extern __shared__ __align__(16) float shared[];   // tables [kWarps][rotary_dim]
+    const int cta = (int)blockIdx.x - a.t[0].ctas;
+    if (cta < 0) heads_fwd<Fmt, E, NU, Mode, Lanes>(a, a.t[0], (int)blockIdx.x, shared);
+    else heads_fwd<Fmt, E, NU, Mode, Lanes>(a, a.t[1], cta, shared);
 }
 
 // ---------------------------------------------------------------- gradient of the norm
 // dn = the transposed rotation of dy; xhat = x * r; dxhat = dn * gamma;
 // dx = r * (dxhat - xhat * mean(dxhat * xhat)); dgamma = sum of dn * xhat.
-template <class Fmt, int E, int NU>
-__global__ void __launch_bounds__(kThreads, 2) heads_bwd_kernel(const __grid_constant__ Args a) {
+//
+// 16-bit heads: the next group's vectors are loaded before the present group is worked on, at two
+// CTAs an SM.  fp32 heads hold half as many elements a lane, so three CTAs fit, and three without
+// the early loads are faster: 32,768 x 18 heads x 256 took 295 us against 356 us, bf16 4 x 4,096 x
+// 40 x 128 took 103 us with them and 118 us without (sum of the vectors over 6,766 GB/s: 268, 75).
+template <class Fmt>
+constexpr bool kBwdAhead = sizeof(typename Fmt::T) == 2;
+
+template <class Fmt, int E, int NU, int Lanes>
+__device__ __forceinline__ void heads_bwd(const Args& a, const HeadsArg& t, int cta, float* sums) {
     using T = typename Fmt::T;
-    extern __shared__ float sums[];   // [kWarps][head_dim]
-    const int which = (int)blockIdx.x >= a.t[0].ctas;
-    const HeadsArg& t = a.t[which];
-    const int cta = (int)blockIdx.x - (which ? a.t[0].ctas : 0);
+    constexpr int H = E / 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per_step = 32 / a.lanes, grp = lane / a.lanes, sub = lane - grp * a.lanes;
+    const int lanes = Lanes ? Lanes : a.lanes, per_step = 32 / lanes;
+    const int grp = min(lane / lanes, per_step - 1), sub = lane % lanes;
+    const bool whole = Lanes || lane < per_step * lanes;
+    float* table = sums + kWarps * a.head_dim + warp * a.rot;
     Units<E, NU> u;
-    u.init(a, grp < per_step ? sub : a.lanes);
+    u.init(a, sub, lanes);
     pdl_wait();
     pdl_trigger();
-    float g[NU][2 * E], acc[NU][2 * E], c[NU][E], sn[NU][E];
+    F2 g[NU][E], acc[NU][E];
+    float c[NU][E], sn[NU][E];
 #pragma unroll
     for (int j = 0; j < NU; ++j)
 #pragma unroll
-        for (int e = 0; e < 2 * E; ++e) acc[j][e] = 0.f;
-
-    const unsigned items = a.tokens * t.chunks;
-    Cursor<T> cur;
-    cur.item = cta * kWarps + warp;
-    bool more = cur.item < items;
-    if (more) {
-        long long pos;
-        cur.open(a, t, per_step, &pos);
-        Head<Fmt, E, NU> x, dy;
-        float r = 0.f;
-        auto load = [&](const Cursor<T>& at, bool any, Head<Fmt, E, NU>& hx, Head<Fmt, E, NU>& hdy, float& hr) {
-            const int h = at.h0 + grp;
-            const bool mine = any && h < at.h_end && grp < per_step;
-            hx.load(at.x + h * t.sx.h, u, mine);
-            hdy.load(at.dy + h * t.sdy.h, u, mine);
-            hr = mine ? __ldg(t.inv_rms + (int64_t)at.token * t.heads + h) : 0.f;
+        for (int e = 0; e < H; ++e) {
+            g[j][e] = f2(__ldg(t.gamma + u.first[j] + 2 * e), __ldg(t.gamma + u.first[j] + 2 * e + 1));
+            g[j][H + e] = f2(__ldg(t.gamma + u.second[j] + 2 * e), __ldg(t.gamma + u.second[j] + 2 * e + 1));
+            acc[j][e] = acc[j][H + e] = f2(0.f);
+        }
+    const unsigned items = a.tokens * t.chunks, stride = t.ctas * kWarps;
+    unsigned i = cta * kWarps + warp;
+    if (i < items) {
+        Item at, nxt;
+        at.open(a, t, i, per_step);
+        long long pos = position(a, at.b, at.s);
+        const T *x = at.row(static_cast<const T*>(t.x), t.sx), *dy = at.row(static_cast<const T*>(t.dy), t.sdy);
+        T* dx = at.row(static_cast<T*>(t.y), t.sy);
+        const float* inv = t.inv_rms + (int64_t)at.token * t.heads;
+        Head<Fmt, E, NU> hx, hdy, hx_n, hdy_n;
+        float r, r_n;
+        auto load = [&](const T* px, const T* pdy, const float* pinv, int h, Head<Fmt, E, NU>& ox,
+                        Head<Fmt, E, NU>& ody, float& or_) {
+            ox.load(px + h * t.sx.h, u);
+            ody.load(pdy + h * t.sdy.h, u);
+            or_ = __ldg(pinv + h);
         };
-        load(cur, true, x, dy, r);
-        load_gamma<E, NU>(t.gamma, u, g);
-        bool fresh = true;
-        while (more) {
-            Cursor<T> nxt = cur;
-            long long pos_nxt = pos;
-            bool fresh_nxt = false;
-            nxt.h0 += per_step;
-            if (nxt.h0 >= nxt.h_end) {
-                nxt.item += t.ctas * kWarps;
-                more = nxt.item < items;
-                fresh_nxt = true;
-                if (more) nxt.open(a, t, per_step, &pos_nxt);
-            }
-            Head<Fmt, E, NU> x_ahead, dy_ahead;
-            float r_ahead;
-            load(nxt, more, x_ahead, dy_ahead, r_ahead);
-            if (fresh) angles<Fmt, E, NU>(a, u, pos, c, sn);
-
-            float dot = 0.f;
-            float d0[NU][E], d1[NU][E];
+        if (kBwdAhead<Fmt>) load(x, dy, inv, min(at.head + grp, at.end - 1), hx, hdy, r);
+        for (;;) {                        // items
+            fill_table<Fmt>(a, pos, table, lane);
 #pragma unroll
-            for (int j = 0; j < NU; ++j) {
-                dy.p[j].get(d0[j]);
-                dy.q[j].get(d1[j]);
-                if (u.turns[j]) rotate<E>(d0[j], d1[j], c[j], sn[j], a.interleaved);
-                float v[E], w[E];
-                x.p[j].get(v);
-                x.q[j].get(w);
+            for (int j = 0; j < NU; ++j)
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    const float m0 = d0[j][e] * (v[e] * r), m1 = d1[j][e] * (w[e] * r);
-                    acc[j][e] += m0;
-                    acc[j][E + e] += m1;
-                    dot += m0 * g[j][e] + m1 * g[j][E + e];
+                    c[j][e] = u.turns[j] ? table[u.freq[j] + e] : 1.f;
+                    sn[j][e] = u.turns[j] ? table[a.rot / 2 + u.freq[j] + e] : 0.f;
                 }
+            i += stride;
+            const bool more = i < items;
+            nxt = at;
+            const T *x_n = x, *dy_n = dy;
+            if (more) {
+                nxt.open(a, t, i, per_step);
+                pos = position(a, nxt.b, nxt.s);
+                x_n = nxt.row(static_cast<const T*>(t.x), t.sx);
+                dy_n = nxt.row(static_cast<const T*>(t.dy), t.sdy);
             }
-            const float m = sum_lanes(dot, a.lanes, sub) * a.inv_dim * r;   // mean * r
-            const int h = cur.h0 + grp;
-            if (h < cur.h_end && grp < per_step) {
-                T* dx = cur.y + h * t.sy.h;
+            const float* inv_n = t.inv_rms + (int64_t)nxt.token * t.heads;
+            for (int h0 = at.head; h0 < at.end; h0 += per_step) {
+                // the next group's vectors, of the next item behind the last
+                const bool same = h0 + per_step < at.end;
+                if (kBwdAhead<Fmt> && (same || more))
+                    load(same ? x : x_n, same ? dy : dy_n, same ? inv : inv_n,
+                         same ? min(h0 + per_step + grp, at.end - 1) : min(nxt.head + grp, nxt.end - 1), hx_n, hdy_n,
+                         r_n);
+                const int h = h0 + grp;
+                const bool mine = whole && h < at.end;
+                if (!kBwdAhead<Fmt>) load(x, dy, inv, min(h, at.end - 1), hx, hdy, r);
+                F2 d[NU][E], xr[NU][E];
+                F2 dot2 = f2(0.f);
 #pragma unroll
                 for (int j = 0; j < NU; ++j) {
-                    float v[E], w[E];
-                    x.p[j].get(v);
-                    x.q[j].get(w);
+                    F2 p[H], q[H];
+                    hdy.p[j].get(p);
+                    hdy.q[j].get(q);
+                    if (u.turns[j]) {
+                        if (a.interleaved) {
+#pragma unroll
+                            for (int e = 0; e < E; ++e) {
+                                F2& v = e < H ? p[e % H] : q[e % H];
+                                float lo, hi;
+                                split(v, lo, hi);
+                                v = f2(lo * c[j][e] - hi * sn[j][e], lo * sn[j][e] + hi * c[j][e]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < H; ++e) {
+                                const F2 v = p[e], w = q[e];
+                                const F2 cc = f2(c[j][2 * e], c[j][2 * e + 1]), ss = f2(sn[j][2 * e], sn[j][2 * e + 1]);
+                                p[e] = fma2(w, ss * f2(-1.f), v * cc);
+                                q[e] = fma2(v, ss, w * cc);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < H; ++e) d[j][e] = p[e], d[j][H + e] = q[e];
+                    hx.p[j].get(p);
+                    hx.q[j].get(q);
+#pragma unroll
+                    for (int e = 0; e < H; ++e) xr[j][e] = p[e] * f2(r), xr[j][H + e] = q[e] * f2(r);
+                    if (mine) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) acc[j][e] = fma2(d[j][e], xr[j][e], acc[j][e]);
+                    }
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
-                        v[e] = r * (d0[j][e] * g[j][e] - v[e] * m);
-                        w[e] = r * (d1[j][e] * g[j][E + e] - w[e] * m);
-                    }
-                    if (u.live[j]) {
-                        Chunk<Fmt, E>::store(dx + u.first[j], v);
-                        Chunk<Fmt, E>::store(dx + u.second[j], w);
+                        d[j][e] = d[j][e] * g[j][e];
+                        dot2 = fma2(d[j][e], xr[j][e], dot2);
                     }
                 }
+                float lo, hi;
+                split(dot2, lo, hi);
+                const float m = sum_lanes<Lanes>(lo + hi, lanes, sub) * a.inv_dim;
+                if (mine) {
+                    T* row = dx + h * t.sy.h;
+#pragma unroll
+                    for (int j = 0; j < NU; ++j) {
+                        F2 p[H], q[H];
+#pragma unroll
+                        for (int e = 0; e < H; ++e) {
+                            p[e] = fma2(xr[j][e], f2(-m), d[j][e]) * f2(r);
+                            q[e] = fma2(xr[j][H + e], f2(-m), d[j][H + e]) * f2(r);
+                        }
+                        if (NU > 1 && !u.live[j]) continue;
+                        Chunk<Fmt, E>::store(row + u.first[j], p);
+                        Chunk<Fmt, E>::store(row + u.second[j], q);
+                    }
+                }
+                if (kBwdAhead<Fmt>) {
+                    hx = hx_n;
+                    hdy = hdy_n;
+                    r = r_n;
+                }
             }
-            x = x_ahead;
-            dy = dy_ahead;
-            r = r_ahead;
-            cur = nxt;
-            pos = pos_nxt;
-            fresh = fresh_nxt;
+            if (!more) break;
+            at = nxt;
+            x = x_n;
+            dy = dy_n;
+            inv = inv_n;
+            dx = at.row(static_cast<T*>(t.y), t.sy);
         }
     }
 
@@ -450,9 +580,12 @@ __global__ void __launch_bounds__(kThreads, 2) heads_bwd_kernel(const __grid_con
     for (int j = 0; j < NU; ++j)
 #pragma unroll
         for (int e = 0; e < 2 * E; ++e) {
-            float v = acc[j][e];
-            for (int k = 1; k < per_step; ++k) v += __shfl_sync(0xffffffffu, acc[j][e], (sub + k * a.lanes) & 31);
-            if (grp == 0 && u.live[j])
+            float lo, hi;
+            split(acc[j][e / 2], lo, hi);
+            const float own = e & 1 ? hi : lo;
+            float v = own;
+            for (int k = 1; k < per_step; ++k) v += __shfl_sync(0xffffffffu, own, (sub + k * lanes) & 31);
+            if (lane < lanes && u.live[j])
                 sums[warp * a.head_dim + (e < E ? u.first[j] + e : u.second[j] + e - E)] = v;
         }
     __syncthreads();
@@ -461,6 +594,14 @@ __global__ void __launch_bounds__(kThreads, 2) heads_bwd_kernel(const __grid_con
         for (int w = 0; w < kWarps; ++w) v += sums[w * a.head_dim + d];
         t.partial[(int64_t)cta * a.head_dim + d] = v;
     }
+}
+
+template <class Fmt, int E, int NU, int Lanes>
+__global__ void __launch_bounds__(kThreads, kBwdAhead<Fmt> ? 2 : 3) heads_bwd_kernel(const __grid_constant__ Args a) {
+    extern __shared__ __align__(16) float shared[];   // sums [kWarps][head_dim], tables
+    const int cta = (int)blockIdx.x - a.t[0].ctas;
+    if (cta < 0) heads_bwd<Fmt, E, NU, Lanes>(a, a.t[0], (int)blockIdx.x, shared);
+    else heads_bwd<Fmt, E, NU, Lanes>(a, a.t[1], cta, shared);
 }
 
 // ---------------------------------------------------------------- any sizes, strides and alignment
@@ -521,7 +662,7 @@ __global__ void __launch_bounds__(kThreads) heads_general_kernel(const __grid_co
                         const float v = Fmt::to_f32(x[d]);
                         ss += v * v;
                     }
-                    r = rsqrtf(sum_lanes(ss, 32, lane) * a.inv_dim + a.eps);
+                    r = rsqrtf(sum_lanes<32>(ss, 32, lane) * a.inv_dim + a.eps);
                     if (t.inv_rms && lane == 0) t.inv_rms[(int64_t)token * t.heads + h] = r;
                 }
                 for (int p = lane; p < pairs; p += 32) {
@@ -556,7 +697,7 @@ __global__ void __launch_bounds__(kThreads) heads_general_kernel(const __grid_co
                     sums[e.i] += m;
                     dot += m * __ldg(t.gamma + e.i);
                 }
-                const float m = sum_lanes(dot, 32, lane) * a.inv_dim * r;
+                const float m = sum_lanes<32>(dot, 32, lane) * a.inv_dim * r;
                 for (int p = lane; p < pairs; p += 32) {
                     const Pair e = pair_at(a, p);
                     float u = Fmt::to_f32(dy[e.i]), v = 0.f, xk = 0.f;
@@ -731,19 +872,23 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Head groups of one token that a warp takes: all, so that it forms the token's sines once,
 // unless that would leave warps of the resident grid without work.
-template <class Fmt, int E, int NU>
-tb_status launch_vec(Args a, const Call& c, int sms, cudaStream_t st) {
-    const int units = a.head_dim / (2 * E);
-    a.lanes = (int)ceil_div(units, NU);
+//
+// Forward: one launch of CTAs whose warps take kFwdItems tokens each; the hardware deals them out
+// as SMs come free, which a grid of resident CTAs cannot (the SMs of the two dies are not equally
+// fast).  The gradient keeps its dgamma sums in registers, so its grid is the resident one.
+constexpr int kFwdItems = 2;
+
+template <class Fmt, int E, int NU, int Lanes>
+tb_status launch_lanes(Args a, const Call& c, int sms, cudaStream_t st) {
     const int per_step = 32 / a.lanes;
     const void* kernel =
-        c.bwd_norm ? reinterpret_cast<const void*>(&heads_bwd_kernel<Fmt, E, NU>)
-        : c.norm   ? reinterpret_cast<const void*>(&heads_fwd_kernel<Fmt, E, NU, kNorm>)
-                   : reinterpret_cast<const void*>(&heads_fwd_kernel<Fmt, E, NU, kRope>);
-    const size_t smem = c.bwd_norm ? sizeof(float) * kWarps * a.head_dim : 0;
+        c.bwd_norm ? reinterpret_cast<const void*>(&heads_bwd_kernel<Fmt, E, NU, Lanes>)
+        : c.norm   ? reinterpret_cast<const void*>(&heads_fwd_kernel<Fmt, E, NU, kNorm, Lanes>)
+                   : reinterpret_cast<const void*>(&heads_fwd_kernel<Fmt, E, NU, kRope, Lanes>);
+    const size_t smem = sizeof(float) * kWarps * (a.rot + (c.bwd_norm ? a.head_dim : 0));
     const int resident = resident_ctas_per_sm(kernel, kThreads, smem);
     if (resident == 0) return TB_ERR_CUDA;
-    const int64_t grid_ctas = (int64_t)sms * (c.bwd_norm ? std::min(resident, kBwdCtasPerSm) : resident);
+    const int64_t grid_ctas = (int64_t)sms * std::min(resident, kBwdCtasPerSm);
     int64_t all_steps = 0;
     for (int i = 0; i < c.n; ++i) all_steps += ceil_div(a.t[i].heads, per_step);
     for (int i = 0; i < c.n; ++i) {
@@ -754,21 +899,35 @@ tb_status launch_vec(Args a, const Call& c, int sms, cudaStream_t st) {
         t.chunks = (int)std::min(steps, ceil_div(share * kWarps, a.tokens));
         t.steps = (int)ceil_div(steps, t.chunks);
         t.chunks = (int)ceil_div(steps, t.steps);
-        t.ctas = (int)std::min(share, ceil_div(a.tokens * t.chunks, kWarps));
+        const int64_t ctas = ceil_div((int64_t)a.tokens * t.chunks, kWarps);
+        t.ctas = (int)(c.bwd_norm ? std::min(share, ctas) : std::max(std::min(share, ctas), ceil_div(ctas, kFwdItems)));
     }
     if (c.n == 1) a.t[1].ctas = 0;
     if (c.bwd_norm) a.t[1].partial = a.t[0].partial + (int64_t)a.t[0].ctas * a.head_dim;
     const dim3 grid((unsigned)(a.t[0].ctas + a.t[1].ctas));
     cudaError_t e;
-    if (c.bwd_norm) e = launch_pdl(heads_bwd_kernel<Fmt, E, NU>, grid, dim3(kThreads), smem, st, a);
-    else if (c.norm) e = launch_pdl(heads_fwd_kernel<Fmt, E, NU, kNorm>, grid, dim3(kThreads), smem, st, a);
-    else e = launch_pdl(heads_fwd_kernel<Fmt, E, NU, kRope>, grid, dim3(kThreads), smem, st, a);
+    if (c.bwd_norm) e = launch_pdl(heads_bwd_kernel<Fmt, E, NU, Lanes>, grid, dim3(kThreads), smem, st, a);
+    else if (c.norm) e = launch_pdl(heads_fwd_kernel<Fmt, E, NU, kNorm, Lanes>, grid, dim3(kThreads), smem, st, a);
+    else e = launch_pdl(heads_fwd_kernel<Fmt, E, NU, kRope, Lanes>, grid, dim3(kThreads), smem, st, a);
     if (e != cudaSuccess) return TB_ERR_CUDA;
     if (c.bwd_norm &&
         launch_pdl(dgamma_kernel, dim3((unsigned)ceil_div(a.head_dim, 32), (unsigned)c.n),
                    dim3(kThreads), 0, st, a) != cudaSuccess)
         return TB_ERR_CUDA;
     return launch_status();
+}
+
+// Heads of 64, 128 and 256 elements in 16-byte vectors know their number of lanes when compiled.
+template <class Fmt, int E, int NU>
+tb_status launch_vec(Args a, const Call& c, int sms, cudaStream_t st) {
+    a.lanes = (int)ceil_div(a.head_dim / (2 * E), NU);
+    if constexpr (E * sizeof(typename Fmt::T) == 16) {
+        if (a.lanes == 4) return launch_lanes<Fmt, E, NU, 4>(a, c, sms, st);
+        if (a.lanes == 8) return launch_lanes<Fmt, E, NU, 8>(a, c, sms, st);
+        if (a.lanes == 16) return launch_lanes<Fmt, E, NU, 16>(a, c, sms, st);
+        if (a.lanes == 32) return launch_lanes<Fmt, E, NU, 32>(a, c, sms, st);
+    }
+    return launch_lanes<Fmt, E, NU, 0>(a, c, sms, st);
 }
 
 template <class Fmt>
