@@ -489,106 +489,103 @@ assert _HEADS_BYTES == 40 and ctypes.sizeof(tb_rope_angles) == 48
 
 class _HeadsCall:
     """The tb_heads of a call's tensors and its tb_rope_angles, packed into one array of 64-bit
-    words. Small calls take a few microseconds on the GPU, so this path makes no ctypes objects:
-    a struct each would cost more than the kernel."""
+    words. Small calls take a few microseconds on the GPU, so this path makes no ctypes objects
+    and few calls: a struct for each tensor would cost more than the kernel.
 
-    __slots__ = ("words", "at", "batch", "seq", "dim", "dtype", "device", "heads")
+    ``tensors`` are the queries, the keys (or None), and pairs behind them with as many heads as
+    the queries and the keys."""
 
-    def __init__(self, q: torch.Tensor, name: str):
+    __slots__ = ("words", "at", "batch", "seq", "dim", "code", "device", "heads")
+
+    def __init__(self, names, tensors, freqs: Optional[torch.Tensor],
+                 positions: Optional[torch.Tensor], offset: int, interleaved: bool,
+                 magnitude: float):
+        q = tensors[0]
         shape = q.shape
         if len(shape) != 4:
-            raise ValueError(f"{name} must be [batch, seq, heads, head_dim], got {tuple(shape)}")
-        self.batch, self.seq, _, self.dim = shape
-        self.dtype, self.device, self.words, self.heads = q.dtype, q.get_device(), [], []
-
-    def add(self, t: Optional[torch.Tensor], name: str, like: Optional[int] = None) -> None:
-        """Checks a tensor against the queries (and `like`, an earlier one, for its heads)."""
-        if t is None:
-            self.words += (0, 0, 0, 0, 0)
-            self.heads.append(None)
-            return
-        shape = t.shape
-        if len(shape) != 4 or shape[0] != self.batch or shape[1] != self.seq or shape[3] != self.dim:
-            raise ValueError(f"{name} must be [batch, seq, heads, head_dim] with the batch, seq and "
-                             f"head_dim of the queries, got {tuple(shape)}")
-        if t.dtype != self.dtype:
-            raise ValueError(f"{name} must be {self.dtype} like the queries, got {t.dtype}")
-        sb, ss, sh, sd = t.stride()
-        if sd != 1 and self.dim > 1:
-            raise ValueError(f"the last dimension of {name} must be contiguous")
-        heads = shape[2]
-        if like is not None and self.heads[like] != heads:
-            raise ValueError(f"{name} must have {self.heads[like]} heads, got {heads}")
-        if t.get_device() != self.device:
-            raise ValueError(f"{name} is on {t.device}, the queries on another device")
-        self.words += (t.data_ptr(), sb, ss, sh, heads)
-        self.heads.append(heads)
-
-    def angles(self, freqs: Optional[torch.Tensor], positions: Optional[torch.Tensor], offset: int,
-               interleaved: bool, magnitude: float) -> None:
-        if self.device < 0:
+            raise ValueError(f"{names[0]} must be [batch, seq, heads, head_dim], got {tuple(shape)}")
+        batch, seq, _, dim = shape
+        dtype, device = q.dtype, q.get_device()
+        words, heads = [], []
+        for i, t in enumerate(tensors):
+            if t is None:
+                if i > 1 and heads[i & 1] is not None:
+                    raise ValueError(f"{names[i & 1]} and {names[i]} must be given together")
+                words += (0, 0, 0, 0, 0)
+                heads.append(None)
+                continue
+            b, s, h, d = shape = t.shape if t.dim() == 4 else (-1, -1, -1, -1)
+            if b != batch or s != seq or d != dim:
+                raise ValueError(f"{names[i]} must be [batch, seq, heads, head_dim] with the batch, "
+                                 f"seq and head_dim of {names[0]}, got {tuple(t.shape)}")
+            if t.dtype != dtype:
+                raise ValueError(f"{names[i]} must be {dtype} like {names[0]}, got {t.dtype}")
+            sb, ss, sh, sd = t.stride()
+            if sd != 1 and dim > 1:
+                raise ValueError(f"the last dimension of {names[i]} must be contiguous")
+            if i > 1 and heads[i & 1] != h:
+                if heads[i & 1] is None:
+                    raise ValueError(f"{names[i & 1]} and {names[i]} must be given together")
+                raise ValueError(f"{names[i]} must have {heads[i & 1]} heads, got {h}")
+            if t.get_device() != device:
+                raise ValueError(f"{names[i]} is on {t.device}, {names[0]} on {q.device}")
+            words += (t.data_ptr(), sb, ss, sh, h)
+            heads.append(h)
+        if device < 0:
             raise ValueError("tensors passed to libtb must be CUDA tensors")
-        if self.device != _current_device():
-            raise ValueError(f"tensor on cuda:{self.device}, but the current device is "
+        if device != _current_device():
+            raise ValueError(f"tensor on cuda:{device}, but the current device is "
                              f"cuda:{_current_device()}")
-        rot, table, where, stride = 0, 0, 0, 0
+        rot = table = where = stride = 0
         if freqs is not None:
             if freqs.dtype != torch.int64 or freqs.dim() != 1 or not freqs.is_contiguous():
                 raise ValueError("freqs must be the int64 table of tb_rope_freqs")
-            if freqs.get_device() != self.device:
-                raise ValueError(f"freqs is on {freqs.device}, the queries on cuda:{self.device}")
+            if freqs.get_device() != device:
+                raise ValueError(f"freqs is on {freqs.device}, {names[0]} on cuda:{device}")
             rot, table = 2 * freqs.numel(), freqs.data_ptr()
         if positions is not None:
-            if positions.dtype != torch.int64 or positions.get_device() != self.device:
-                raise ValueError("positions must be an int64 tensor on the queries' device")
-            shape, strides = tuple(positions.shape), positions.stride()
-            if shape != (self.batch, self.seq) and shape != (self.seq,):
-                raise ValueError(f"positions must be [{self.batch}, {self.seq}] or [{self.seq}], got "
-                                 f"{shape}")
-            if self.seq > 1 and strides[-1] != 1:
+            if positions.dtype != torch.int64 or positions.get_device() != device:
+                raise ValueError(f"positions must be an int64 tensor on the device of {names[0]}")
+            shape, strides = positions.shape, positions.stride()
+            if len(shape) not in (1, 2) or shape[-1] != seq or (len(shape) == 2 and shape[0] != batch):
+                raise ValueError(f"positions must be [{batch}, {seq}] or [{seq}], got {tuple(shape)}")
+            if seq > 1 and strides[-1] != 1:
                 raise ValueError("the last dimension of positions must be contiguous")
             where = positions.data_ptr()
-            if len(shape) == 2 and self.batch > 1:
+            if len(shape) == 2 and batch > 1:
                 stride = strides[0]
         size = _float_bits(magnitude) if magnitude != 1.0 else 0x3F800000
-        self.words += (table, where, stride, int(offset), rot | (bool(interleaved) << 32), size)
-        self.words = array("q", self.words)
+        words += (table, where, stride, int(offset), rot | (bool(interleaved) << 32), size)
+        self.words = array("q", words)
         self.at = self.words.buffer_info()[0]
+        self.batch, self.seq, self.dim, self.device, self.heads = batch, seq, dim, device, heads
+        self.code = _DTYPE.get(dtype)
+        if self.code is None:
+            raise TbError("dtype", 2)
 
     def __call__(self, i: int) -> Optional[int]:
-        """Address of the i-th tensor's tb_heads; None for a tensor that was not given."""
-        return None if self.heads[i] is None else self.at + i * _HEADS_BYTES
+        """Address of the i-th tensor's tb_heads; None for a tensor that was not given. The one
+        behind the last is the tb_rope_angles."""
+        if i < len(self.heads) and self.heads[i] is None:
+            return None
+        return self.at + i * _HEADS_BYTES
 
-    def angles_at(self) -> int:
-        return self.at + len(self.heads) * _HEADS_BYTES
+    def fp32(self, t: Optional[torch.Tensor], n: int, name: str) -> Optional[int]:
+        """Address of a contiguous fp32 tensor of n values on the call's device."""
+        if t is None:
+            raise ValueError(f"{name} is missing")
+        if t.numel() != n or t.dtype != torch.float32:
+            _want(t, n, torch.float32, name)
+        if t.get_device() != self.device or not t.is_contiguous():
+            return _ptr(t)
+        return t.data_ptr() or None
 
-    def code(self) -> int:
-        try:
-            return _DTYPE[self.dtype]
-        except KeyError:
-            raise TbError("dtype", 2) from None
+    def stream(self, stream) -> Optional[int]:
+        return _raw_stream(self.device) if stream is None and _raw_stream else _stream(stream)
 
 
 def _float_bits(x: float) -> int:
     return struct.unpack("<i", struct.pack("<f", float(x)))[0] & 0xFFFFFFFF
-
-
-def _together(a, b, names) -> None:
-    if (a is None) != (b is None):
-        raise ValueError(f"{names[0]} and {names[1]} must be given together")
-
-
-def _rope(fn, name, q, k, q_out, k_out, names, freqs, positions, offset, interleaved, magnitude,
-          stream) -> None:
-    c = _HeadsCall(q, names[0])
-    _together(k, k_out, (names[1], names[3]))
-    c.add(q, names[0])
-    c.add(k, names[1])
-    c.add(q_out, names[2], 0)
-    c.add(k_out, names[3], 1)
-    c.angles(freqs, positions, offset, interleaved, magnitude)
-    _check(name, fn(c(0), c(1), c(2), c(3), c.batch, c.seq, c.dim, c.angles_at(), c.code(),
-                    _stream(stream)))
 
 
 def tb_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_out: torch.Tensor,
@@ -598,8 +595,10 @@ def tb_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_out: torch.Tensor,
     """Rotary positions on [batch, seq, heads, head_dim] queries and keys (any strides but the
     last). ``positions``: int64 [batch, seq] or [seq]; None counts from ``offset``. An output
     may be its own input."""
-    _rope(lib.tb_rope, "tb_rope", q, k, q_out, k_out, ("q", "k", "q_out", "k_out"), freqs,
-          positions, offset, interleaved, magnitude, stream)
+    c = _HeadsCall(("q", "k", "q_out", "k_out"), (q, k, q_out, k_out), freqs, positions, offset,
+                   interleaved, magnitude)
+    _check("tb_rope", lib.tb_rope(c(0), c(1), c(2), c(3), c.batch, c.seq, c.dim, c(4), c.code,
+                                  c.stream(stream)))
 
 
 def tb_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], dq: torch.Tensor,
@@ -607,15 +606,10 @@ def tb_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], dq: torch.
                 positions: Optional[torch.Tensor] = None, offset: int = 0,
                 interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
     """Gradient of tb_rope: the transposed rotation of dq_out and dk_out."""
-    _rope(lib.tb_rope_bwd, "tb_rope_bwd", dq_out, dk_out, dq, dk, ("dq_out", "dk_out", "dq", "dk"),
-          freqs, positions, offset, interleaved, magnitude, stream)
-
-
-def _gamma(g: Optional[torch.Tensor], dim: int, name: str) -> Optional[int]:
-    if g is None:
-        raise ValueError(f"{name} is missing")
-    _want(g, dim, torch.float32, name)
-    return _ptr(g)
+    c = _HeadsCall(("dq_out", "dk_out", "dq", "dk"), (dq_out, dk_out, dq, dk), freqs, positions,
+                   offset, interleaved, magnitude)
+    _check("tb_rope_bwd", lib.tb_rope_bwd(c(0), c(1), c(2), c(3), c.batch, c.seq, c.dim, c(4),
+                                          c.code, c.stream(stream)))
 
 
 def tb_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], gamma_q: torch.Tensor,
@@ -628,24 +622,16 @@ def tb_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], gamma_q: torch.T
     """RMS norm of every head of q and k, then tb_rope, in one pass. inv_rms_q and inv_rms_k
     (fp32, batch * seq * heads values) receive what tb_qk_norm_rope_bwd needs; leave them out
     when serving. Without ``freqs`` the heads are normalised and not rotated."""
-    c = _HeadsCall(q, "q")
-    _together(k, k_out, ("k", "k_out"))
-    c.add(q, "q")
-    c.add(k, "k")
-    c.add(q_out, "q_out", 0)
-    c.add(k_out, "k_out", 1)
-    c.angles(freqs, positions, offset, interleaved, magnitude)
-    gq = _gamma(gamma_q, c.dim, "gamma_q")
-    gk = _gamma(gamma_k, c.dim, "gamma_k") if k is not None else None
+    c = _HeadsCall(("q", "k", "q_out", "k_out"), (q, k, q_out, k_out), freqs, positions, offset,
+                   interleaved, magnitude)
     tokens = c.batch * c.seq
-    if inv_rms_q is not None:
-        _want(inv_rms_q, tokens * c.heads[0], torch.float32, "inv_rms_q")
-    if inv_rms_k is not None:
-        _want(inv_rms_k, tokens * (c.heads[1] or 0), torch.float32, "inv_rms_k")
+    gq = c.fp32(gamma_q, c.dim, "gamma_q")
+    gk = None if k is None else c.fp32(gamma_k, c.dim, "gamma_k")
+    rq = None if inv_rms_q is None else c.fp32(inv_rms_q, tokens * c.heads[0], "inv_rms_q")
+    rk = None if inv_rms_k is None else c.fp32(inv_rms_k, tokens * (c.heads[1] or 0), "inv_rms_k")
     _check("tb_qk_norm_rope",
-           lib.tb_qk_norm_rope(c(0), c(1), gq, gk, float(eps), c(2), c(3), _ptr(inv_rms_q),
-                               _ptr(inv_rms_k), c.batch, c.seq, c.dim, c.angles_at(), c.code(),
-                               _stream(stream)))
+           lib.tb_qk_norm_rope(c(0), c(1), gq, gk, float(eps), c(2), c(3), rq, rk, c.batch, c.seq,
+                               c.dim, c(4), c.code, c.stream(stream)))
 
 
 def tb_qk_norm_rope_bwd_workspace_size(batch: int, seq: int, heads_q: int, heads_k: int,
@@ -667,31 +653,20 @@ def tb_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q:
                         interleaved: bool = False, magnitude: float = 1.0,
                         workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """Gradient of tb_qk_norm_rope: dq, dk and the (overwritten) dgamma_q, dgamma_k."""
-    c = _HeadsCall(q, "q")
-    _together(k, dk, ("k", "dk"))
-    _together(k, dk_out, ("k", "dk_out"))
-    c.add(q, "q")
-    c.add(k, "k")
-    c.add(dq, "dq", 0)
-    c.add(dk, "dk", 1)
-    c.add(dq_out, "dq_out", 0)
-    c.add(dk_out, "dk_out", 1)
-    c.angles(freqs, positions, offset, interleaved, magnitude)
+    c = _HeadsCall(("q", "k", "dq", "dk", "dq_out", "dk_out"), (q, k, dq, dk, dq_out, dk_out), freqs,
+                   positions, offset, interleaved, magnitude)
     tokens = c.batch * c.seq
-    gq, sq = _gamma(gamma_q, c.dim, "gamma_q"), _gamma(dgamma_q, c.dim, "dgamma_q")
-    _want(inv_rms_q, tokens * c.heads[0], torch.float32, "inv_rms_q")
+    gq, sq = c.fp32(gamma_q, c.dim, "gamma_q"), c.fp32(dgamma_q, c.dim, "dgamma_q")
+    rq = c.fp32(inv_rms_q, tokens * c.heads[0], "inv_rms_q")
     gk = sk = rk = None
     if k is not None:
-        gk, sk = _gamma(gamma_k, c.dim, "gamma_k"), _gamma(dgamma_k, c.dim, "dgamma_k")
-        if inv_rms_k is None:
-            raise ValueError("inv_rms_k is missing")
-        _want(inv_rms_k, tokens * c.heads[1], torch.float32, "inv_rms_k")
-        rk = _ptr(inv_rms_k)
+        gk, sk = c.fp32(gamma_k, c.dim, "gamma_k"), c.fp32(dgamma_k, c.dim, "dgamma_k")
+        rk = c.fp32(inv_rms_k, tokens * c.heads[1], "inv_rms_k")
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check("tb_qk_norm_rope_bwd",
-           lib.tb_qk_norm_rope_bwd(c(4), c(5), c(0), c(1), _ptr(inv_rms_q), rk, gq, gk, c(2), c(3),
-                                   sq, sk, c.batch, c.seq, c.dim, c.angles_at(), c.code(),
-                                   _ptr(workspace), ws_bytes, _stream(stream)))
+           lib.tb_qk_norm_rope_bwd(c(4), c(5), c(0), c(1), rq, rk, gq, gk, c(2), c(3), sq, sk,
+                                   c.batch, c.seq, c.dim, c(6), c.code, _ptr(workspace), ws_bytes,
+                                   c.stream(stream)))
 
 
 # ----------------------------------------------------------------------------- output layer's loss
