@@ -12,7 +12,7 @@
 // 256 x 256 tile: tcgen05.mma.cta_group::2 with both operands in shared memory, 64 of the
 // contracted dimension a stage, 128-byte swizzled; each CTA stages its half of A and of B
 // (32 KB a stage, six stages), so a tile's operands cross from L2 once per pair.  Warp 0
-// feeds the stages by TMA, warp 1 of the pair's first CTA issues the MMAs, warps 4..7 drain
+// feeds the stages by TMA, warp 1 of the pair's first CTA issues the MMAs, warps 4..11 drain
 // the accumulator -- of which there are two, 256 TMEM columns each, so that the epilogue of
 // one tile runs under the MMAs of the next.  A thread of the epilogue owns one row of the
 // tile: row sums need no shuffles.  Tiles are dealt statically to a persistent grid of one
@@ -48,9 +48,12 @@ constexpr int kStageK = 64;                  // contracted elements a stage: 128
 constexpr int kStages = 6;
 constexpr int kOperandBytes = kHalf * kStageK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kThreads = 256;
-constexpr int kEpiWarp = 4;                  // first of the four epilogue warps
-constexpr int kSmem = kStages * kStageBytes + 1024 + 256;   // alignment, barriers
+constexpr int kThreads = 384;
+constexpr int kEpiWarp = 4;                  // first of the epilogue warps
+constexpr int kEpiWarps = 8;                 // two for each quarter of the accumulator's rows
+constexpr int kOutCols = 32;
+constexpr int kOutBytes = 32 * kOutCols * 2; // what an epilogue warp stores at once: 32 rows
+constexpr int kSmem = kStages * kStageBytes + 2 * kEpiWarps * kOutBytes + 1024 + 256;   // alignment, barriers
 constexpr int kTmemCols = 512;               // two accumulators
 constexpr int kGroup = 16;                   // row tiles walked together (see tile_at)
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;
@@ -131,19 +134,30 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
 }
 // Shared-memory operand descriptor: 128-byte swizzle.  K-major: 8-row groups every 1,024
 // bytes.  MN-major: 64-column blocks every 8,192 bytes (one box), 8-row groups along the
-// contracted dimension every 1,024.
+// contracted dimension every 1,024.  The upper word is a constant; the lower one is the address
+// in units of 16 bytes under it, so that the next operand is one addition.
 template <bool MnMajor>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
-    constexpr uint64_t lbo = MnMajor ? 8192 >> 4 : 1, sbo = 1024 >> 4;
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | (lbo << 16) | (sbo << 32) | (1ull << 46) | (2ull << 61);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr) {
+    return ((addr & 0x3FFFF) >> 4) | ((MnMajor ? 8192u >> 4 : 1u) << 16);
 }
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
-        : "memory");
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+template <bool Accumulate>
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (Accumulate)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.eq.u32 p, 0, 0;\n\t"
+            "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+            "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh), "r"(accumulate)
+            : "memory");
 }
 // Arrives on the mbarrier at this offset in both CTAs when the MMAs issued so far are done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -153,21 +167,35 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         "h"((uint16_t)3)
         : "memory");
 }
-__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
-    uint32_t r[32];
+// 32 columns of this warp's 32 accumulator rows, one row a lane; the values are there after
+// tmem_wait, which names the registers so that no use of them moves above it.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
         "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
         "%30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+          "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+          "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+        :
+        : "memory");
+}
+// A box of 32 rows by 32 columns from shared memory to `map` at column x, row y; what lies outside
+// the matrix is dropped.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -184,16 +212,26 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp, 0 below -126
 constexpr float kLog2e = 1.44269504088896341f;
 
 // ---------------------------------------------------------------- arguments
+struct Weigh {
+    const float* dloss;
+    const void* H;            // [rows][cols]
+    void* scaled;             // [rows][ld]; NULL: dW is not wanted
+    float *weight, *top;      // weight NULL: not in this launch
+    int64_t rows;
+    int cols, ld;
+};
 struct Product {
     int m_tiles, n_tiles, splits, k_stages;
     int rows, cols;           // of the result
+    int width;                // columns of a tile: at most kTile, fewer where that fills the last wave
+    int out_map;              // results go out by TMA (16-byte aligned rows), else element by element
     int b_base;               // kGrad, kDH: first vocabulary row of the piece
     int* err;
     // kLse, kGrad
     const int64_t* target;    // of this launch's rows
     int64_t ignore;
     int vocab;
-    float2* part;             // kLse: [n_tiles][rows] maximum and sum
+    float2* part;             // kLse: [2 n_tiles][rows] maximum and sum of half a tile
     float* target_logit;      // kLse: [rows]
     const float* lse;         // kGrad
     const float* weight;      // kDH: dloss by row, 0 where a row takes no part
@@ -204,6 +242,7 @@ struct Product {
     float* sums;              // kDH: [splits][rows][cols] fp32, NULL: one split, one piece
     int first, last;          // piece: starts the sums; writes the result
     void* out;                // [rows][cols] 16-bit
+    Weigh weigh;              // kGrad
 };
 
 // fp16's G is held times 2^14, so that probabilities down to 2^-38 stay above its last step;
@@ -221,33 +260,158 @@ __device__ __forceinline__ float weigh(float sum, float weight) {
 
 // Row tiles in groups of kGroup, the group's tiles column by column: the pairs that run
 // together share few column tiles and reuse the group's rows.
-__device__ __forceinline__ void tile_at(const Product& p, int t, int* split, int* mt, int* nt) {
-    const int per_split = p.m_tiles * p.n_tiles;
-    *split = t / per_split;
-    t -= *split * per_split;
-    const int group = t / (kGroup * p.n_tiles), first = group * kGroup;
-    const int height = min(kGroup, p.m_tiles - first);
-    t -= group * kGroup * p.n_tiles;
-    *nt = t / height;
-    *mt = first + t - *nt * height;
+__device__ __forceinline__ void tile_at(const Product& p, unsigned t, int* split, int* mt, int* nt) {
+    const unsigned per_split = (unsigned)(p.m_tiles * p.n_tiles);
+    *split = 0;
+    if (p.splits > 1) {
+        *split = (int)(t / per_split);
+        t -= *split * per_split;
+    }
+    unsigned first = 0;
+    if (p.m_tiles > kGroup) {
+        first = t / (unsigned)(kGroup * p.n_tiles);
+        t -= first * kGroup * p.n_tiles;
+        first *= kGroup;
+    }
+    const unsigned height = min(kGroup, p.m_tiles - (int)first);
+    *nt = (int)(t / height);
+    *mt = (int)(first + t - *nt * height);
+}
+// The contracted stages of a split.
+__device__ __forceinline__ void stages_of(const Product& p, int split, int* lo, int* hi) {
+    *lo = 0;
+    *hi = p.k_stages;
+    if (p.splits > 1) {           // (16 splits of at most 2^31 / 64 stages: no overflow)
+        *lo = (int)((unsigned)split * p.k_stages / (unsigned)p.splits);
+        *hi = (int)((unsigned)(split + 1) * p.k_stages / (unsigned)p.splits);
+    }
 }
 
+// An epilogue warp's way out for 16-bit results: 32 columns of its 32 rows into a 64-byte swizzled
+// box in shared memory (a lane's 16-byte pieces at piece ^ (row / 2 & 3): no two lanes of a quarter
+// warp share banks), and a TMA store of the box, of which each warp has two.  Stored from registers,
+// a warp's 16-byte pieces lie a row apart, 32 half sectors an instruction: the epilogue then took
+// longer than the MMAs of a tile with 768 contracted elements (78 us against 62 us, 1,021 x 50,257).
+// What the later products need of dloss: each row's weight (0 where it takes no part), the largest
+// magnitude among them, and H with every row times its weight over that.  One otherwise idle warp
+// of each CTA does its share of it while the logits' product runs (a kernel of its own in front of
+// them took 8 us at 1,021 x 768); each finds the maximum by itself, rows * 12 bytes from L2.
 template <class Fmt>
-__device__ __forceinline__ void store16(typename Fmt::T* row, int col, int cols, bool vec,
-                                        const float (&v)[32]) {
-    if (vec && col + 32 <= cols) {
+__device__ __forceinline__ void weigh_rows(const Weigh& w, const int64_t* target, int64_t ignore, int vocab,
+                                           int lane, int cta, int ctas) {
+    using T = typename Fmt::T;
+    auto weight_of = [&](int64_t r) {
+        const int64_t t = target[r];
+        return t != ignore && t >= 0 && t < vocab ? w.dloss[r] : 0.f;
+    };
+    float m = 0.f;
+#pragma unroll 8
+    for (int64_t r = lane; r < w.rows; r += 32) {
+        const float v = weight_of(r);
+        if (r / 32 % ctas == cta) w.weight[r] = v;
+        if (fabsf(v) <= 3.4028235e38f) m = fmaxf(m, fabsf(v));   // neither infinite nor NaN
+    }
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == 0.f) m = 1.f;
+    if (cta == 0 && lane == 0) *w.top = m;
+    if (!w.scaled) return;
+    const T* H = static_cast<const T*>(w.H);
+    T* scaled = static_cast<T*>(w.scaled);
+    for (int64_t r = cta; r < w.rows; r += ctas) {
+        const float v = weight_of(r), f = v / m;
+        if (w.cols == w.ld) {         // whole 16-byte vectors
+#pragma unroll 4
+            for (int c = lane * 8; c < w.cols; c += 256) {
+                float x[8];
+                unpack8<Fmt>(*reinterpret_cast<const uint4*>(H + r * w.cols + c), x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = v == 0.f ? 0.f : x[e] * f;
+                *reinterpret_cast<uint4*>(scaled + r * w.ld + c) = pack8<Fmt>(x);
+            }
+        } else {
+            for (int c = lane; c < w.ld; c += 32)
+                scaled[r * w.ld + c] =
+                    Fmt::from_f32(c < w.cols && v != 0.f ? Fmt::to_f32(H[r * w.cols + c]) * f : 0.f);
+        }
+    }
+}
+
+// What one CTA stages of a pair's tiles, stage after stage.
+template <int K>
+struct Feed {
+    static constexpr bool kAMn = K == kDW, kBMn = K == kDH || K == kDW;
+    const Product& p;
+    const CUtensorMap *a, *b;
+    int rank, pairs, tiles, t, k, k_hi, m0, n0;
+    int nk, nk_hi, nm0, nn0;      // of the next tile: worked out while the ring is full
+    __device__ __forceinline__ Feed(const Product& p_, const CUtensorMap* a_, const CUtensorMap* b_, int rank_,
+                                    int pair, int pairs_, int tiles_)
+        : p(p_), a(a_), b(b_), rank(rank_), pairs(pairs_), tiles(tiles_), t(pair) {
+        look(t);
+        take();
+    }
+    __device__ __forceinline__ bool more() const { return t < tiles; }
+    __device__ __forceinline__ void look(int tile) {
+        if (tile >= tiles) return;
+        int split, mt, nt;
+        tile_at(p, (unsigned)tile, &split, &mt, &nt);
+        stages_of(p, split, &nk, &nk_hi);
+        nm0 = mt * kTile + rank * kHalf;
+        nn0 = nt * p.width + rank * (p.width / 2);
+    }
+    __device__ __forceinline__ void take() { k = nk, k_hi = nk_hi, m0 = nm0, n0 = nn0; }
+    __device__ __forceinline__ void next() {
+        if (++k < k_hi) return;
+        t += pairs;
+        take();
+    }
+    // Calls f(operand 0 or 1, byte offset in it, map, x, y) for the boxes of this stage.
+    template <class F>
+    __device__ __forceinline__ void boxes(F f) const {
+        const int base = K == kGrad || K == kDH ? p.b_base : 0;
+        if constexpr (kAMn) {
+            f(0, 0, a, m0, k * kStageK);
+            f(0, 8192, a, m0 + 64, k * kStageK);
+        } else {
+            f(0, 0, a, k * kStageK, m0);
+        }
+        if constexpr (kBMn) {
+            f(1, 0, b, n0, base + k * kStageK);
+            f(1, 8192, b, n0 + 64, base + k * kStageK);
+        } else {
+            f(1, 0, b, k * kStageK, base + n0);
+        }
+    }
+};
+
+template <class Fmt>
+struct Outbox {
+    unsigned char* mem;       // this warp's two boxes
+    const CUtensorMap* map;
+    int lane, n;              // boxes filled so far
+    __device__ __forceinline__ void put(const float (&v)[32], int x, int y) {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();         // the box of two stores ago has been read
+        unsigned char* box = mem + (n & 1) * kOutBytes;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = v[8 * i + e];
-            *reinterpret_cast<uint4*>(row + col + 8 * i) = pack8<Fmt>(f);
+            *reinterpret_cast<uint4*>(box + lane * 64 + ((i ^ (lane / 2 & 3)) * 16)) = pack8<Fmt>(f);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (col + i < cols) row[col + i] = Fmt::from_f32(v[i]);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) tma_store(map, x, y, smem_addr(box));
+        ++n;
     }
+};
+
+template <class Fmt>
+__device__ __forceinline__ void store_each(typename Fmt::T* row, int col, int cols, const float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (col + i < cols) row[col + i] = Fmt::from_f32(v[i]);
 }
 
 // Folds 32 logits into a row's maximum m and sum s of exp(l - base(m)); base is 0 where the
@@ -266,13 +430,14 @@ __device__ __forceinline__ void fold(float& m, float& s, float m2, float s2) {
 template <class Fmt, int K>
 __global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-               const __grid_constant__ Product p) {
+               const __grid_constant__ CUtensorMap map_out, const __grid_constant__ Product p) {
     using T = typename Fmt::T;
     constexpr bool kAMn = K == kDW, kBMn = K == kDH || K == kDW;
     extern __shared__ unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+    unsigned char* outbox = smem + kStages * kStageBytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(outbox + 2 * kEpiWarps * kOutBytes);
     const uint32_t stage0 = smem_addr(smem), bar0 = smem_addr(bars);
     const uint32_t full = bar0, empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
                    acc_empty = acc_full + 16, drain = acc_empty + 16, slot = drain + 8;
@@ -286,7 +451,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
-            mbar_init(acc_empty + 8 * i, 8);      // four warps of each CTA
+            mbar_init(acc_empty + 8 * i, 2 * kEpiWarps);   // of both CTAs
         }
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -303,6 +468,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     tmem_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + (slot - stage0));
     pdl_wait();
+    asm volatile("fence.proxy.async;" ::: "memory");   // what earlier kernels stored, TMA reads
     pdl_trigger();
 
     const int tiles = p.m_tiles * p.n_tiles * p.splits;
@@ -312,35 +478,19 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         if (lane == 0) {
             const uint32_t leader_full = map_to(full, 0);
             int it = 0, failed = 0;
-            for (int t = pair; t < tiles && !failed; t += pairs) {
-                int split, mt, nt;
-                tile_at(p, t, &split, &mt, &nt);
-                const int k_lo = (int)((int64_t)split * p.k_stages / p.splits);
-                const int k_hi = (int)((int64_t)(split + 1) * p.k_stages / p.splits);
-                const int m0 = mt * kTile + (int)rank * kHalf, n0 = nt * kTile + (int)rank * kHalf;
-                for (int k = k_lo; k < k_hi; ++k, ++it) {
-                    const int s = it % kStages;
-                    if (it >= kStages && !mbar_wait(empty + 8 * s, (it / kStages - 1) & 1, p.err)) {
-                        failed = 1;
-                        break;
-                    }
-                    if (rank == 0) mbar_expect(full + 8 * s, 2 * kStageBytes);
-                    const uint32_t a = stage0 + s * kStageBytes, b = a + kOperandBytes;
-                    const uint32_t bar = leader_full + 8 * s;
-                    if constexpr (kAMn) {
-                        tma_box(a, &map_a, m0, k * kStageK, bar);
-                        tma_box(a + 8192, &map_a, m0 + 64, k * kStageK, bar);
-                    } else {
-                        tma_box(a, &map_a, k * kStageK, m0, bar);
-                    }
-                    const int base = K == kGrad || K == kDH ? p.b_base : 0;
-                    if constexpr (kBMn) {
-                        tma_box(b, &map_b, n0, base + k * kStageK, bar);
-                        tma_box(b + 8192, &map_b, n0 + 64, base + k * kStageK, bar);
-                    } else {
-                        tma_box(b, &map_b, k * kStageK, base + n0, bar);
-                    }
+            Feed<K> feed(p, &map_a, &map_b, (int)rank, pair, pairs, tiles);
+            for (; feed.more(); feed.next(), ++it) {
+                const int s = it % kStages;
+                if (it >= kStages && !mbar_wait(empty + 8 * s, (it / kStages - 1) & 1, p.err)) {
+                    failed = 1;
+                    break;
                 }
+                if (rank == 0) mbar_expect(full + 8 * s, 2 * kOperandBytes + p.width * kStageK * 2);
+                const uint32_t at = stage0 + s * kStageBytes, bar = leader_full + 8 * s;
+                feed.boxes([&](int operand, int offset, const CUtensorMap* m, int x, int y) {
+                    tma_box(at + operand * kOperandBytes + offset, m, x, y, bar);
+                });
+                if (feed.k + 1 == feed.k_hi) feed.look(feed.t + pairs);
             }
             if (failed && rank == 0)      // what both CTAs issued ends on these barriers
                 for (int q = max(0, it - kStages); q < it; ++q)
@@ -349,35 +499,41 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             constexpr uint32_t fmt = std::is_same<Fmt, BF16>::value ? 1 : 0;
-            constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)kAMn << 15) |
-                                       ((uint32_t)kBMn << 16) | ((kTile / 8) << 17) | ((kTile / 16) << 24);
+            const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)kAMn << 15) |
+                                   ((uint32_t)kBMn << 16) | ((uint32_t)(p.width / 8) << 17) | ((kTile / 16) << 24);
             // 16 contracted elements: 32 bytes of a K-major row, 16 rows of an MN-major box
-            constexpr uint32_t step_a = kAMn ? 2048 : 32, step_b = kBMn ? 2048 : 32;
-            int it = 0, n = 0;
+            constexpr uint32_t step_a = (kAMn ? 2048 : 32) >> 4, step_b = (kBMn ? 2048 : 32) >> 4;
+            const uint32_t a0 = desc_low<kAMn>(stage0), b0 = desc_low<kBMn>(stage0 + kOperandBytes);
+            // One thread issues everything: what stands between two MMAs is kept to a few
+            // additions, or the tensor core waits for it (660 clocks a stage instead of the 512
+            // of its MMAs, with descriptors and stage numbers worked out each time).
+            uint32_t s = 0, parity = 0;
+            int n = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs, ++n) {
-                const int split = t / (p.m_tiles * p.n_tiles);
-                const int k_lo = (int)((int64_t)split * p.k_stages / p.splits);
-                const int k_hi = (int)((int64_t)(split + 1) * p.k_stages / p.splits);
+                int k_lo, k_hi;
+                stages_of(p, p.splits > 1 ? t / (p.m_tiles * p.n_tiles) : 0, &k_lo, &k_hi);
                 const int buf = n & 1;
                 if (n >= 2 && !mbar_wait(acc_empty + 8 * buf, (n / 2 - 1) & 1, p.err)) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after();
-                for (int k = k_lo; k < k_hi; ++k, ++it) {
-                    const int s = it % kStages;
-                    if (!mbar_wait(full + 8 * s, (it / kStages) & 1, p.err)) {
+                const uint32_t d = tmem + buf * kTile;
+                uint32_t accumulate = 0;
+                for (int k = k_lo; k < k_hi; ++k) {
+                    if (!mbar_wait(full + 8 * s, parity, p.err)) {
                         ok = false;
                         break;
                     }
-                    tmem_fence_after();
-                    const uint32_t a = stage0 + s * kStageBytes, b = a + kOperandBytes;
+                    const uint32_t a = a0 + s * (kStageBytes >> 4), b = b0 + s * (kStageBytes >> 4);
+                    mma_pair<false>(d, a, b, idesc, accumulate);
 #pragma unroll
-                    for (int j = 0; j < kStageK / 16; ++j)
-                        mma_pair(tmem + buf * kTile, operand_desc<kAMn>(a + j * step_a),
-                                 operand_desc<kBMn>(b + j * step_b), idesc, k > k_lo || j > 0);
+                    for (int j = 1; j < kStageK / 16; ++j)
+                        mma_pair<true>(d, a + j * step_a, b + j * step_b, idesc, 1);
                     mma_commit(empty + 8 * s);
+                    accumulate = 1;
+                    if (++s == kStages) s = 0, parity ^= 1;
                 }
                 if (ok) mma_commit(acc_full + 8 * buf);
             }
@@ -386,18 +542,26 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 mbar_wait(drain, 0, p.err);
             }
         }
+    } else if (K == kGrad && warp == 3) {
+        if (p.weigh.weight)
+            weigh_rows<Fmt>(p.weigh, p.target, p.ignore, p.vocab, lane, blockIdx.x, gridDim.x);
     } else if (warp >= kEpiWarp) {
-        const int quad = warp - kEpiWarp;             // TMEM lanes 32 quad .. 32 quad + 31
+        // TMEM lanes 32 quad .. 32 quad + 31 (a warp reaches those of its number modulo 4), and
+        // the first or second half of the tile's columns
+        const int quad = warp & 3, half = (warp - kEpiWarp) >> 2;
         const uint32_t leader_empty = map_to(acc_empty, 0);
         const float top_weight = K == kDW ? *p.top : 1.f;
+        Outbox<Fmt> box{outbox + (warp - kEpiWarp) * 2 * kOutBytes, &map_out, lane, 0};
         int n = 0;
         for (int t = pair; t < tiles; t += pairs, ++n) {
             int split, mt, nt;
-            tile_at(p, t, &split, &mt, &nt);
+            tile_at(p, (unsigned)t, &split, &mt, &nt);
             const int buf = n & 1;
-            const int row = mt * kTile + (int)rank * kHalf + quad * 32 + lane;
+            const int row0 = mt * kTile + (int)rank * kHalf + quad * 32, row = row0 + lane;
             const bool live = row < p.rows;
-            const int n0 = nt * kTile, width = min(kTile, p.cols - n0);
+            const int n0 = nt * p.width, all = min(p.width, p.cols - n0);
+            const int middle = (all + 63) / 64 * 32;
+            const int c0 = half ? middle : 0, width = half ? all : min(all, middle);
             const uint32_t acc = tmem + buf * kTile + ((uint32_t)(quad * 32) << 16);
 
             // what the row needs, on its way before the accumulator is done
@@ -411,7 +575,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     const int64_t tg = p.target[row];
                     const bool counts = tg != p.ignore && tg >= 0 && tg < p.vocab;
                     const int64_t c = tg - (K == kGrad ? p.b_base : 0) - n0;
-                    if (counts && c >= 0 && c < width) hit = (int)c;
+                    if (counts && c >= c0 && c < width) hit = (int)c;
                     if constexpr (K == kGrad) {
                         lse2 = p.lse[row] * kLog2e - kGBits<Fmt>;
                         weight = counts ? 1.f : 0.f;
@@ -422,89 +586,110 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             tmem_fence_after();
 
             float m = __int_as_float(0xff800000), s = 0.f;
-            for (int c = 0; c < width; c += 32) {
+            auto work = [&](const uint32_t (&r)[32], int c) {
                 float v[32];
-                __syncwarp();
-                tmem_load32(acc + c, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
                 if constexpr (K == kLse) {
-                    if (c + 32 > width) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i >= width) v[i] = __int_as_float(0xff800000);
-                    }
-                    float top = v[0];
-#pragma unroll
-                    for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
-                    const float b = base_of(top) * kLog2e;
-                    float part = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) part += exp2_fast(fmaf(v[i], kLog2e, -b));
-                    fold(m, s, top, part);
                     if ((hit & ~31) == c) {           // (hit = -1: no chunk)
                         float x = v[0];
 #pragma unroll
                         for (int i = 1; i < 32; ++i) x = c + i == hit ? v[i] : x;
                         p.target_logit[row] = x;
                     }
+                    if (c + 32 > width) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i >= width) v[i] = __int_as_float(0xff800000);
+                    }
+                    float top = v[0], part = 0.f, part2 = 0.f;
+#pragma unroll
+                    for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
+                    const float b = base_of(top) * kLog2e;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        part += exp2_fast(fmaf(v[i], kLog2e, -b));
+                        part2 += exp2_fast(fmaf(v[i + 1], kLog2e, -b));
+                    }
+                    fold(m, s, top, part + part2);
                 } else if constexpr (K == kGrad) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float e = exp2_fast(fmaf(v[i], kLog2e, -lse2));
-                        v[i] = c + i == hit ? e - kGScale<Fmt> : e;
+                    for (int i = 0; i < 32; ++i) v[i] = exp2_fast(fmaf(v[i], kLog2e, -lse2));
+                    if ((hit & ~31) == c) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = c + i == hit ? v[i] - kGScale<Fmt> : v[i];
                     }
                     if (weight == 0.f) {              // a row that takes no part
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.f;
                     }
-                    if (live)                         // ldg is a multiple of 64: whole vectors
-                        store16<Fmt>(static_cast<T*>(p.g) + (int64_t)row * p.ldg, n0 + c, p.ldg, true, v);
-                } else if constexpr (K == kDH) {
-                    const int col = n0 + c;
-                    if (p.sums) {
-                        float* sum = p.sums + ((int64_t)split * p.rows + row) * p.cols + col;
-                        const bool vec = c + 32 <= width && (p.cols & 3) == 0;
-                        if (live && vec) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                                if (!p.first) o = *reinterpret_cast<float4*>(sum + 4 * i);
-                                o.x += v[4 * i], o.y += v[4 * i + 1], o.z += v[4 * i + 2], o.w += v[4 * i + 3];
-                                v[4 * i] = o.x, v[4 * i + 1] = o.y, v[4 * i + 2] = o.z, v[4 * i + 3] = o.w;
-                                if (!p.last || p.splits > 1) *reinterpret_cast<float4*>(sum + 4 * i) = o;
-                            }
-                        } else if (live) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c + i < width) {
-                                    if (!p.first) v[i] += sum[i];
-                                    if (!p.last || p.splits > 1) sum[i] = v[i];
-                                }
-                        }
-                    }
-                    if (live && p.last && p.splits == 1) {
-                        T* out = static_cast<T*>(p.out);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = weigh<Fmt>(v[i], weight);
-                        store16<Fmt>(out + (int64_t)row * p.cols, col, p.cols,
-                                     (p.cols & 7) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0, v);
-                    }
+                    if (row0 < p.rows) box.put(v, n0 + c, row0);
                 } else {
                     T* out = static_cast<T*>(p.out);
-                    if (live) {
+                    const int col = n0 + c;
+                    bool finish = true;
+                    if constexpr (K == kDH) {
+                        if (p.sums) {
+                            float* sum = p.sums + ((int64_t)split * p.rows + row) * p.cols + col;
+                            const bool keep = !p.last || p.splits > 1;
+                            if (live && c + 32 <= width && (p.cols & 3) == 0) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = v[i] * (1.f / kGScale<Fmt>) * top_weight;
-                        store16<Fmt>(out + (int64_t)row * p.cols, n0 + c, p.cols,
-                                     (p.cols & 7) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0, v);
+                                for (int i = 0; i < 8; ++i) {
+                                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                                    if (!p.first) o = *reinterpret_cast<float4*>(sum + 4 * i);
+                                    v[4 * i] += o.x, v[4 * i + 1] += o.y, v[4 * i + 2] += o.z, v[4 * i + 3] += o.w;
+                                    if (keep)
+                                        *reinterpret_cast<float4*>(sum + 4 * i) =
+                                            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                                }
+                            } else if (live) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (c + i < width) {
+                                        if (!p.first) v[i] += sum[i];
+                                        if (keep) sum[i] = v[i];
+                                    }
+                            }
+                            __syncwarp();
+                        }
+                        finish = p.last && p.splits == 1;
                     }
+                    if (finish) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = K == kDH ? weigh<Fmt>(v[i], weight) : v[i] * (1.f / kGScale<Fmt>) * top_weight;
+                        if (p.out_map) {
+                            if (row0 < p.rows) box.put(v, n0 + c, row0);
+                        } else if (live) {
+                            store_each<Fmt>(out + (int64_t)row * p.cols, col, p.cols, v);
+                        }
+                    }
+                }
+            };
+            // the next columns come while the present ones are worked on
+            uint32_t one[32], two[32];
+            __syncwarp();
+            if (c0 < width) tmem_load32(acc + c0, one);
+            for (int c = c0; c < width; c += 64) {
+                tmem_wait(one);
+                if (c + 32 < width) tmem_load32(acc + c + 32, two);
+                work(one, c);
+                __syncwarp();
+                if (c + 32 < width) {
+                    tmem_wait(two);
+                    if (c + 64 < width) tmem_load32(acc + c + 64, one);
+                    work(two, c + 32);
+                    __syncwarp();
                 }
             }
             if constexpr (K == kLse) {
-                if (live) p.part[(int64_t)nt * p.rows + row] = make_float2(m, s);
+                if (live) p.part[((int64_t)nt * 2 + half) * p.rows + row] = make_float2(m, s);
             }
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(leader_empty + 8 * buf);
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncwarp();
     tmem_fence_before();
@@ -516,26 +701,39 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 }
 
 // ---------------------------------------------------------------- around the products
-// A row's parts, one per column tile, in a fixed order: 32 rows a CTA, eight lanes a row.
+// A row's parts, two for each column tile, in a fixed order.  R rows a CTA, 256 / R lanes a row:
+// 32 rows side by side read whole sectors, eight put more loads in flight for calls of few rows.
+template <int R>
 __global__ void __launch_bounds__(256)
 join_kernel(const float2* part, const float* target_logit, const int64_t* target, int64_t ignore,
-            int vocab, int rows, int n_tiles, float* loss, float* lse, int* err) {
-    __shared__ float2 sh[8][32];
-    const int row = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+            int vocab, int rows, int n_parts, float* loss, float* lse, int* err) {
+    constexpr int kLanes = 256 / R;
+    __shared__ float2 sh[kLanes][R];
+    const int r = threadIdx.x % R, w = threadIdx.x / R, row = blockIdx.x * R + r;
     pdl_wait();
     pdl_trigger();
     float m = __int_as_float(0xff800000), s = 0.f;
     if (row < rows) {
-#pragma unroll 4
-        for (int t = w; t < n_tiles; t += 8) {
-            const float2 q = part[(int64_t)t * rows + row];
-            fold(m, s, q.x, q.y);
+        for (int t = w; t < n_parts; t += 8 * kLanes) {
+            float2 q[8];              // loaded together, folded one after another
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                q[k] = t + k * kLanes < n_parts ? part[(int64_t)(t + k * kLanes) * rows + row]
+                                                : make_float2(__int_as_float(0xff800000), 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) fold(m, s, q[k].x, q[k].y);
         }
     }
-    sh[w][threadIdx.x & 31] = make_float2(m, s);
+    sh[w][r] = make_float2(m, s);
     __syncthreads();
+    for (int k = kLanes / 2; k; k /= 2) {
+        if (w < k) {
+            fold(m, s, sh[w + k][r].x, sh[w + k][r].y);
+            sh[w][r] = make_float2(m, s);
+        }
+        __syncthreads();
+    }
     if (w == 0 && row < rows) {
-        for (int i = 1; i < 8; ++i) fold(m, s, sh[i][threadIdx.x].x, sh[i][threadIdx.x].y);
         const float total = base_of(m) + logf(s);
         lse[row] = total;
         const int64_t tg = target[row];
@@ -550,69 +748,33 @@ join_kernel(const float2* part, const float* target_logit, const int64_t* target
     }
 }
 
-// What the gradient needs of dloss: each row's weight (0 where it takes no part), the largest
-// magnitude among them, and H with every row times its weight over that.  Each CTA finds the
-// maximum by itself (rows * 12 bytes from L2), which saves a launch.
-template <class Fmt>
-__global__ void __launch_bounds__(256)
-weigh_kernel(const float* dloss, const int64_t* target, int64_t ignore, int vocab, int64_t rows,
-             const typename Fmt::T* H, int cols, int ld, typename Fmt::T* scaled, float* weight, float* top) {
-    __shared__ float sh[8];
-    pdl_wait();
-    pdl_trigger();
-    auto weight_of = [&](int64_t r) {
-        const int64_t t = target[r];
-        return t != ignore && t >= 0 && t < vocab ? dloss[r] : 0.f;
-    };
-    float m = 0.f;
-#pragma unroll 4
-    for (int64_t r = threadIdx.x; r < rows; r += 256) {
-        const float w = weight_of(r);
-        if (blockIdx.x == 0) weight[r] = w;
-        if (fabsf(w) <= 3.4028235e38f) m = fmaxf(m, fabsf(w));   // neither infinite nor NaN
-    }
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = sh[0];
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, sh[i]);
-    if (m == 0.f) m = 1.f;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *top = m;
-    if (!scaled) return;
-    if (cols == ld) {                 // whole 16-byte vectors
-        const int per_row = ld / 8;
-        const int64_t n = rows * per_row;
-        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-            const float w = weight_of(i / per_row);
-            float f[8];
-            unpack8<Fmt>(reinterpret_cast<const uint4*>(H)[i], f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = w == 0.f ? 0.f : f[e] * (w / m);
-            reinterpret_cast<uint4*>(scaled)[i] = pack8<Fmt>(f);
-        }
-    } else {
-        const int64_t n = rows * ld;
-        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-            const int64_t r = i / ld;
-            const int c = (int)(i - r * ld);
-            const float w = weight_of(r);
-            scaled[i] = Fmt::from_f32(c < cols && w != 0.f ? Fmt::to_f32(H[r * cols + c]) * (w / m) : 0.f);
-        }
-    }
-}
-
-// Sums the splits of dH and rounds once.
-template <class Fmt>
+// Sums the splits of dH and rounds once: V elements a thread, of one row.
+template <class Fmt, int V>
 __global__ void __launch_bounds__(256)
 join_dh_kernel(const float* sums, int splits, int64_t n, int cols, const float* weight,
                typename Fmt::T* out) {
     pdl_wait();
     pdl_trigger();
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        float v = 0.f;
-        for (int s = 0; s < splits; ++s) v += sums[s * n + i];
-        out[i] = Fmt::from_f32(weigh<Fmt>(v, weight[i / cols]));
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
+    if (i >= n) return;
+    const float w = weight[i / cols];
+    float v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+        if constexpr (V == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(sums + s * n + i);
+            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+        } else {
+            v[0] += sums[s * n + i];
+        }
     }
+    typename Fmt::T r[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) r[e] = Fmt::from_f32(weigh<Fmt>(v[e], w));
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(out + i) = *reinterpret_cast<const uint2*>(r);
+    else out[i] = r[0];
 }
 
 // Rows padded with zeros to a multiple of eight elements: TMA wants strides of 16 bytes.
@@ -653,29 +815,31 @@ EncodeFn encode_fn() {
 }
 
 // A row-major 16-bit matrix, read in boxes of 64 columns by `box_rows` rows, swizzled over
-// 128 bytes; what lies outside reads as zeros.
+// 128 bytes; what lies outside reads as zeros.  `out`: written in boxes of 32 columns, swizzled
+// over 64 bytes.
 bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows,
-              bool bf16) {
+              bool bf16, bool out = false) {
     const EncodeFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)kStageK, (cuuint32_t)box_rows};
+    const cuuint32_t box[2] = {(cuuint32_t)(out ? kOutCols : kStageK), (cuuint32_t)box_rows};
     const cuuint32_t ones[2] = {1, 1};
     return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
               const_cast<void*>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <class Fmt, int K>
-tb_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const Product& p, cudaStream_t st) {
+tb_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, const Product& p,
+                         cudaStream_t st) {
     const void* kernel = reinterpret_cast<const void*>(&product_kernel<Fmt, K>);
     const int pairs = resident_clusters(kernel, kThreads, kSmem, 2);
     if (pairs < 1) return TB_ERR_CUDA;
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles * p.splits;
     const int64_t grid = 2 * std::min<int64_t>(tiles, pairs);
-    if (launch_cluster(product_kernel<Fmt, K>, dim3((unsigned)grid), dim3(kThreads), kSmem, st, 2, a, b, p) !=
+    if (launch_clusters<true>(product_kernel<Fmt, K>, dim3((unsigned)grid), dim3(kThreads), kSmem, st, 2, a, b, out, p) !=
         cudaSuccess)
         return TB_ERR_CUDA;
     return launch_status();
@@ -683,6 +847,8 @@ tb_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const Produ
 
 // How a call of these sizes is cut up.
 struct Cut {
+    int lse_width, grad_width;   // columns of a tile of logits
+    int64_t lse_tiles;
     int64_t ld;               // padded row length of H and W (D where no copy is needed)
     bool pad;
     int64_t piece, pieces;    // gradient: columns of a piece of the vocabulary
@@ -707,6 +873,20 @@ int pick_splits(int64_t m_tiles, int64_t n_tiles, int64_t k_stages, int64_t pair
     return best;
 }
 
+// Columns of a tile of logits: the width among 256, 224, .. 128 that takes the fewest columns' time
+// when its tiles are dealt to the pairs in whole waves.  A narrower tile has the same cost per
+// column but reads its rows of A more often, so it has to save 3%.  (37 x 50,257: 225 tiles of 224
+// columns are three waves of 76 pairs, as are 197 of 256.)
+int pick_width(int64_t m_tiles, int64_t cols, int64_t pairs) {
+    int best = kTile;
+    double least = 1e30;
+    for (int w = kTile; w >= 128; w -= 32) {
+        const double cost = (double)ceil_div(m_tiles * ceil_div(cols, w), pairs) * w;
+        if (cost < least * 0.97) least = cost, best = w;
+    }
+    return best;
+}
+
 Cut cut_call(int64_t n, int64_t d, int64_t v, bool bwd, int sms) {
     Cut c{};
     c.ld = round_up(d, 8);
@@ -723,7 +903,9 @@ Cut cut_call(int64_t n, int64_t d, int64_t v, bool bwd, int sms) {
     }
     if (!bwd) {
         const int64_t rows = std::min(n, kLseRows);
-        c.off_part = take((size_t)rows * ceil_div(v, kTile) * sizeof(float2));
+        c.lse_width = pick_width(ceil_div(rows, kTile), v, sms / 2);
+        c.lse_tiles = ceil_div(v, c.lse_width);
+        c.off_part = take((size_t)rows * 2 * c.lse_tiles * sizeof(float2));
         c.off_logit = take((size_t)rows * sizeof(float));
     } else {
         int64_t most = std::max(kMinPiece, kPieceBytes / (2 * std::max<int64_t>(n, 1)));
@@ -732,6 +914,7 @@ Cut cut_call(int64_t n, int64_t d, int64_t v, bool bwd, int sms) {
         c.piece = std::min(round_up(ceil_div(v, c.pieces), kTile), round_up(v, kTile));
         c.pieces = ceil_div(v, c.piece);
         c.ldg = c.piece;
+        c.grad_width = pick_width(ceil_div(n, kTile), std::min(c.piece, v), sms / 2);
         c.splits = pick_splits(ceil_div(n, kTile), ceil_div(d, kTile), c.piece / kStageK, sms / 2);
         c.off_g = take((size_t)n * c.ldg * 2);
         if (c.pieces > 1 || c.splits > 1) c.off_sums = take((size_t)c.splits * n * d * sizeof(float));
@@ -799,14 +982,15 @@ tb_status run_loss(const Problem& q, const Cut& c) {
         W = q.ws + c.off_w;
     }
     CUtensorMap a, b;
-    if (!make_map(&b, W, q.v, q.d, c.ld, kHalf, bf)) return TB_ERR_CUDA;
+    if (!make_map(&b, W, q.v, q.d, c.ld, c.lse_width / 2, bf)) return TB_ERR_CUDA;
     for (int64_t r0 = 0; r0 < q.n; r0 += kLseRows) {
         const int64_t rows = std::min(kLseRows, q.n - r0);
         if (!make_map(&a, static_cast<const char*>(H) + r0 * c.ld * 2, rows, q.d, c.ld, kHalf, bf))
             return TB_ERR_CUDA;
         Product p{};
         p.m_tiles = (int)ceil_div(rows, kTile);
-        p.n_tiles = (int)ceil_div(q.v, kTile);
+        p.width = c.lse_width;
+        p.n_tiles = (int)c.lse_tiles;
         p.splits = 1;
         p.k_stages = (int)ceil_div(q.d, kStageK);
         p.rows = (int)rows;
@@ -817,12 +1001,14 @@ tb_status run_loss(const Problem& q, const Cut& c) {
         p.vocab = (int)q.v;
         p.part = reinterpret_cast<float2*>(q.ws + c.off_part);
         p.target_logit = reinterpret_cast<float*>(q.ws + c.off_logit);
-        const tb_status s = launch_product<Fmt, kLse>(a, b, p, q.st);
+        const tb_status s = launch_product<Fmt, kLse>(a, b, a, p, q.st);
         if (s != TB_OK) return s;
-        if (launch_pdl(join_kernel, dim3((unsigned)ceil_div(rows, 32)), dim3(256), 0, q.st,
-                       (const float2*)p.part, (const float*)p.target_logit, p.target, p.ignore, p.vocab,
-                       p.rows, p.n_tiles, q.loss + r0, q.lse + r0, q.err) != cudaSuccess)
-            return TB_ERR_CUDA;
+        const bool few = rows <= 32 * q.sms;
+        const dim3 grid((unsigned)ceil_div(rows, few ? 8 : 32));
+        const cudaError_t e = launch_pdl(few ? join_kernel<8> : join_kernel<32>, grid, dim3(256), 0, q.st,
+                                         (const float2*)p.part, (const float*)p.target_logit, p.target, p.ignore,
+                                         p.vocab, p.rows, 2 * p.n_tiles, q.loss + r0, q.lse + r0, q.err);
+        if (e != cudaSuccess) return TB_ERR_CUDA;
     }
     return launch_status();
 }
@@ -842,22 +1028,19 @@ tb_status run_grad(const Problem& q, const Cut& c) {
     float* top = reinterpret_cast<float*>(q.ws + c.off_top);
     using T = typename Fmt::T;
     T* scaled = reinterpret_cast<T*>(q.ws + c.off_scaled);
-    const int64_t copy_ctas = q.dW ? ceil_div(q.n * c.ld, 256 * 8 * 4) : 1;
-    if (launch_pdl(weigh_kernel<Fmt>, dim3((unsigned)std::min<int64_t>(copy_ctas, (int64_t)q.sms * 4)), dim3(256),
-                   0, q.st, q.dloss, q.target, q.ignore, (int)q.v, q.n, static_cast<const T*>(q.H), (int)q.d,
-                   (int)c.ld, q.dW ? scaled : (T*)nullptr, weight, top) != cudaSuccess)
-        return TB_ERR_CUDA;
     void* g = q.ws + c.off_g;
-    CUtensorMap h_rows, w_rows, h_cols, w_cols, g_rows, g_cols;
-    if (!make_map(&h_rows, H, q.n, q.d, c.ld, kHalf, bf) || !make_map(&w_rows, W, q.v, q.d, c.ld, kHalf, bf) ||
+    CUtensorMap h_rows, w_rows, h_cols, w_cols, g_rows, g_cols, out;
+    if (!make_map(&h_rows, H, q.n, q.d, c.ld, kHalf, bf) || !make_map(&w_rows, W, q.v, q.d, c.ld, c.grad_width / 2, bf) ||
         !make_map(&h_cols, scaled, q.n, q.d, c.ld, kStageK, bf) || !make_map(&w_cols, W, q.v, q.d, c.ld, kStageK, bf))
         return TB_ERR_CUDA;
     for (int64_t i = 0; i < c.pieces; ++i) {
         const int64_t v0 = i * c.piece, cols = std::min(c.piece, q.v - v0);
         Product p{};
         p.m_tiles = (int)ceil_div(q.n, kTile);
-        p.n_tiles = (int)ceil_div(cols, kTile);
+        p.width = c.grad_width;
+        p.n_tiles = (int)ceil_div(cols, p.width);
         p.splits = 1;
+        p.out_map = 1;
         p.k_stages = (int)ceil_div(q.d, kStageK);
         p.rows = (int)q.n;
         p.cols = (int)cols;
@@ -869,13 +1052,18 @@ tb_status run_grad(const Problem& q, const Cut& c) {
         p.lse = q.lse_in;
         p.weight = weight;
         p.top = top;
+        if (i == 0)
+            p.weigh = Weigh{q.dloss, q.H, q.dW ? scaled : nullptr, weight, top, q.n, (int)q.d, (int)c.ld};
         p.g = g;
         p.ldg = (int)c.ldg;
-        tb_status s = launch_product<Fmt, kGrad>(h_rows, w_rows, p, q.st);
+        if (!make_map(&out, g, q.n, cols, c.ldg, 32, bf, true)) return TB_ERR_CUDA;
+        tb_status s = launch_product<Fmt, kGrad>(h_rows, w_rows, out, p, q.st);
         if (s != TB_OK) return s;
         if (q.dH) {
             if (!make_map(&g_rows, g, q.n, cols, c.ldg, kHalf, bf)) return TB_ERR_CUDA;
             Product r = p;
+            r.width = kTile;
+            r.out_map = q.d % 8 == 0 && aligned_to(q.dH, 16);
             r.n_tiles = (int)ceil_div(q.d, kTile);
             r.k_stages = (int)ceil_div(cols, kStageK);
             r.splits = std::min(c.splits, r.k_stages);
@@ -887,7 +1075,8 @@ tb_status run_grad(const Problem& q, const Cut& c) {
             r.sums = c.pieces > 1 || c.splits > 1 ? reinterpret_cast<float*>(q.ws + c.off_sums) : nullptr;
             r.out = q.dH;
             if (c.splits > 1 && r.splits == 1) r.last = 0;
-            s = launch_product<Fmt, kDH>(g_rows, w_cols, r, q.st);
+            if (r.out_map && !make_map(&out, q.dH, q.n, q.d, q.d, 32, bf, true)) return TB_ERR_CUDA;
+            s = launch_product<Fmt, kDH>(g_rows, w_cols, out, r, q.st);
             if (s != TB_OK) return s;
         }
         if (q.dW) {
@@ -898,18 +1087,26 @@ tb_status run_grad(const Problem& q, const Cut& c) {
             r.k_stages = (int)ceil_div(q.n, kStageK);
             r.rows = (int)cols;
             r.cols = (int)q.d;
+            r.width = kTile;
             r.out = static_cast<char*>(q.dW) + v0 * q.d * 2;
-            s = launch_product<Fmt, kDW>(g_cols, h_cols, r, q.st);
+            r.out_map = q.d % 8 == 0 && aligned_to(q.dW, 16);
+            if (r.out_map && !make_map(&out, r.out, cols, q.d, q.d, 32, bf, true)) return TB_ERR_CUDA;
+            s = launch_product<Fmt, kDW>(g_cols, h_cols, out, r, q.st);
             if (s != TB_OK) return s;
         }
     }
     if (q.dH && c.splits > 1) {
-        const int64_t n = q.n * q.d, grid = std::min<int64_t>(ceil_div(n, 256), (int64_t)q.sms * 8);
+        const int64_t n = q.n * q.d;
         const int used = (int)std::min<int64_t>(c.splits, ceil_div(std::min(c.piece, q.v), kStageK));
-        if (launch_pdl(join_dh_kernel<Fmt>, dim3((unsigned)grid), dim3(256), 0, q.st,
-                       (const float*)(q.ws + c.off_sums), used, n, (int)q.d, (const float*)weight,
-                       static_cast<T*>(q.dH)) != cudaSuccess)
-            return TB_ERR_CUDA;
+        const float* sums = reinterpret_cast<const float*>(q.ws + c.off_sums);
+        const bool vec = q.d % 4 == 0 && aligned_to(q.dH, 8);
+        const dim3 grid((unsigned)ceil_div(n, vec ? 1024 : 256));
+        const cudaError_t e =
+            vec ? launch_pdl(join_dh_kernel<Fmt, 4>, grid, dim3(256), 0, q.st, sums, used, n, (int)q.d,
+                             (const float*)weight, static_cast<T*>(q.dH))
+                : launch_pdl(join_dh_kernel<Fmt, 1>, grid, dim3(256), 0, q.st, sums, used, n, (int)q.d,
+                             (const float*)weight, static_cast<T*>(q.dH));
+        if (e != cudaSuccess) return TB_ERR_CUDA;
     }
     return launch_status();
 }

@@ -112,25 +112,32 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
 }
 
 // Launches `kernel` on `st` in thread-block clusters of `cluster` CTAs along x
-// (grid.x a multiple of `cluster`), in plain stream order: it starts once the
-// previous work in the stream has completed, so every cluster finds its SMs free
-// (its pdl_wait() returns at once).
-template <class... KArgs, class... Args>
-inline cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                                  cudaStream_t st, int cluster, Args&&... args) {
+// (grid.x a multiple of `cluster`): with `pdl` as a programmatic dependent of the work
+// before it, without in plain stream order (it starts once that work has completed, so
+// every cluster finds its SMs free, and its pdl_wait() returns at once).
+template <bool pdl, class... KArgs, class... Args>
+inline cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                   cudaStream_t st, int cluster, Args&&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)cluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = pdl ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+template <class... KArgs, class... Args>
+inline cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                  cudaStream_t st, int cluster, Args&&... args) {
+    return launch_clusters<false>(kernel, grid, block, smem, st, cluster, static_cast<KArgs>(args)...);
 }
 
 // ---------------------------------------------------------------- device helpers
