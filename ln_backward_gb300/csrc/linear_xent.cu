@@ -105,6 +105,14 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return done != 0;
 }
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(yes));
+    return yes != 0;
+}
 __device__ __forceinline__ unsigned long long now_ns() {
     unsigned long long t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -441,7 +449,8 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     const uint32_t stage0 = smem_addr(smem), bar0 = smem_addr(bars);
     const uint32_t full = bar0, empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
                    acc_empty = acc_full + 16, drain = acc_empty + 16, slot = drain + 8;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (the shuffle tells the compiler that a warp agrees on its number)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
 
     if (threadIdx.x == 0) {
@@ -475,21 +484,23 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (warp == 0) {
-        if (lane == 0) {
+        {
             const uint32_t leader_full = map_to(full, 0);
             int it = 0, failed = 0;
             Feed<K> feed(p, &map_a, &map_b, (int)rank, pair, pairs, tiles);
             for (; feed.more(); feed.next(), ++it) {
                 const int s = it % kStages;
-                if (it >= kStages && !mbar_wait(empty + 8 * s, (it / kStages - 1) & 1, p.err)) {
+                if (it >= kStages && !__all_sync(0xffffffffu, mbar_wait(empty + 8 * s, (it / kStages - 1) & 1, p.err))) {
                     failed = 1;
                     break;
                 }
-                if (rank == 0) mbar_expect(full + 8 * s, 2 * kOperandBytes + p.width * kStageK * 2);
                 const uint32_t at = stage0 + s * kStageBytes, bar = leader_full + 8 * s;
-                feed.boxes([&](int operand, int offset, const CUtensorMap* m, int x, int y) {
-                    tma_box(at + operand * kOperandBytes + offset, m, x, y, bar);
-                });
+                if (elect_one()) {
+                    if (rank == 0) mbar_expect(full + 8 * s, 2 * kOperandBytes + p.width * kStageK * 2);
+                    feed.boxes([&](int operand, int offset, const CUtensorMap* m, int x, int y) {
+                        tma_box(at + operand * kOperandBytes + offset, m, x, y, bar);
+                    });
+                }
                 if (feed.k + 1 == feed.k_hi) feed.look(feed.t + pairs);
             }
             if (failed && rank == 0)      // what both CTAs issued ends on these barriers
@@ -497,7 +508,9 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     mbar_wait(full + 8 * (q % kStages), (q / kStages) & 1, p.err);
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            // The whole warp walks the stages and one lane issues: the operands of an MMA are uniform
+            // registers, which a loop of one lane would have to fill by copies.
             constexpr uint32_t fmt = std::is_same<Fmt, BF16>::value ? 1 : 0;
             const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)kAMn << 15) |
                                    ((uint32_t)kBMn << 16) | ((uint32_t)(p.width / 8) << 17) | ((kTile / 16) << 24);
@@ -514,7 +527,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 int k_lo, k_hi;
                 stages_of(p, p.splits > 1 ? t / (p.m_tiles * p.n_tiles) : 0, &k_lo, &k_hi);
                 const int buf = n & 1;
-                if (n >= 2 && !mbar_wait(acc_empty + 8 * buf, (n / 2 - 1) & 1, p.err)) {
+                if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(acc_empty + 8 * buf, (n / 2 - 1) & 1, p.err))) {
                     ok = false;
                     break;
                 }
@@ -522,23 +535,25 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 const uint32_t d = tmem + buf * kTile;
                 uint32_t accumulate = 0;
                 for (int k = k_lo; k < k_hi; ++k) {
-                    if (!mbar_wait(full + 8 * s, parity, p.err)) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * s, parity, p.err))) {
                         ok = false;
                         break;
                     }
                     const uint32_t a = a0 + s * (kStageBytes >> 4), b = b0 + s * (kStageBytes >> 4);
-                    mma_pair<false>(d, a, b, idesc, accumulate);
+                    if (elect_one()) {
+                        mma_pair<false>(d, a, b, idesc, accumulate);
 #pragma unroll
-                    for (int j = 1; j < kStageK / 16; ++j)
-                        mma_pair<true>(d, a + j * step_a, b + j * step_b, idesc, 1);
-                    mma_commit(empty + 8 * s);
+                        for (int j = 1; j < kStageK / 16; ++j)
+                            mma_pair<true>(d, a + j * step_a, b + j * step_b, idesc, 1);
+                        mma_commit(empty + 8 * s);
+                    }
                     accumulate = 1;
                     if (++s == kStages) s = 0, parity ^= 1;
                 }
-                if (ok) mma_commit(acc_full + 8 * buf);
+                if (ok && elect_one()) mma_commit(acc_full + 8 * buf);
             }
             if (!ok) {
-                mma_commit(drain);
+                if (elect_one()) mma_commit(drain);
                 mbar_wait(drain, 0, p.err);
             }
         }
