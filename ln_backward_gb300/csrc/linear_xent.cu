@@ -232,6 +232,7 @@ struct Product {
     int m_tiles, n_tiles, splits, k_stages;
     int rows, cols;           // of the result
     int width;                // columns of a tile: at most kTile, fewer where that fills the last wave
+    int a_rows;               // K-major A: rows of a box, fewer than kHalf where the result has no more
     int out_map;              // results go out by TMA (16-byte aligned rows), else element by element
     int b_base;               // kGrad, kDH: first vocabulary row of the piece
     int* err;
@@ -380,7 +381,7 @@ struct Feed {
         if constexpr (kAMn) {
             f(0, 0, a, m0, k * kStageK);
             f(0, 8192, a, m0 + 64, k * kStageK);
-        } else {
+        } else if (p.a_rows == kHalf || rank == 0) {
             f(0, 0, a, k * kStageK, m0);
         }
         if constexpr (kBMn) {
@@ -486,6 +487,8 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     if (warp == 0) {
         {
             const uint32_t leader_full = map_to(full, 0);
+            const uint32_t a_bytes = (kAMn || p.a_rows == kHalf ? 2 * kHalf : p.a_rows) * kStageK * 2;
+            const uint32_t stage_bytes = a_bytes + p.width * kStageK * 2;      // of both CTAs
             int it = 0, failed = 0;
             Feed<K> feed(p, &map_a, &map_b, (int)rank, pair, pairs, tiles);
             for (; feed.more(); feed.next(), ++it) {
@@ -496,7 +499,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 }
                 const uint32_t at = stage0 + s * kStageBytes, bar = leader_full + 8 * s;
                 if (elect_one()) {
-                    if (rank == 0) mbar_expect(full + 8 * s, 2 * kOperandBytes + p.width * kStageK * 2);
+                    if (rank == 0) mbar_expect(full + 8 * s, stage_bytes);
                     feed.boxes([&](int operand, int offset, const CUtensorMap* m, int x, int y) {
                         tma_box(at + operand * kOperandBytes + offset, m, x, y, bar);
                     });
@@ -941,6 +944,11 @@ Cut cut_call(int64_t n, int64_t d, int64_t v, bool bwd, int sms) {
     return c;
 }
 
+// Rows of a box of K-major A.  A result of at most kHalf rows lies in the pair's first CTA alone: its
+// boxes hold those rows and the second CTA loads none.  What the MMAs read in their place is what the
+// memory held; it reaches only rows that nothing stores.
+int box_rows(int64_t rows) { return rows < kHalf ? (int)round_up(rows, 8) : kHalf; }
+
 constexpr int64_t kMaxSize = (1ll << 31) - 512;
 
 tb_status check_sizes(int64_t n, int64_t d, int64_t v, tb_dtype dtype) {
@@ -1000,11 +1008,12 @@ tb_status run_loss(const Problem& q, const Cut& c) {
     if (!make_map(&b, W, q.v, q.d, c.ld, c.lse_width / 2, bf)) return TB_ERR_CUDA;
     for (int64_t r0 = 0; r0 < q.n; r0 += kLseRows) {
         const int64_t rows = std::min(kLseRows, q.n - r0);
-        if (!make_map(&a, static_cast<const char*>(H) + r0 * c.ld * 2, rows, q.d, c.ld, kHalf, bf))
+        if (!make_map(&a, static_cast<const char*>(H) + r0 * c.ld * 2, rows, q.d, c.ld, box_rows(rows), bf))
             return TB_ERR_CUDA;
         Product p{};
         p.m_tiles = (int)ceil_div(rows, kTile);
         p.width = c.lse_width;
+        p.a_rows = box_rows(rows);
         p.n_tiles = (int)c.lse_tiles;
         p.splits = 1;
         p.k_stages = (int)ceil_div(q.d, kStageK);
@@ -1045,7 +1054,7 @@ tb_status run_grad(const Problem& q, const Cut& c) {
     T* scaled = reinterpret_cast<T*>(q.ws + c.off_scaled);
     void* g = q.ws + c.off_g;
     CUtensorMap h_rows, w_rows, h_cols, w_cols, g_rows, g_cols, out;
-    if (!make_map(&h_rows, H, q.n, q.d, c.ld, kHalf, bf) || !make_map(&w_rows, W, q.v, q.d, c.ld, c.grad_width / 2, bf) ||
+    if (!make_map(&h_rows, H, q.n, q.d, c.ld, box_rows(q.n), bf) || !make_map(&w_rows, W, q.v, q.d, c.ld, c.grad_width / 2, bf) ||
         !make_map(&h_cols, scaled, q.n, q.d, c.ld, kStageK, bf) || !make_map(&w_cols, W, q.v, q.d, c.ld, kStageK, bf))
         return TB_ERR_CUDA;
     for (int64_t i = 0; i < c.pieces; ++i) {
@@ -1053,6 +1062,7 @@ tb_status run_grad(const Problem& q, const Cut& c) {
         Product p{};
         p.m_tiles = (int)ceil_div(q.n, kTile);
         p.width = c.grad_width;
+        p.a_rows = box_rows(q.n);
         p.n_tiles = (int)ceil_div(cols, p.width);
         p.splits = 1;
         p.out_map = 1;
@@ -1075,7 +1085,7 @@ tb_status run_grad(const Problem& q, const Cut& c) {
         tb_status s = launch_product<Fmt, kGrad>(h_rows, w_rows, out, p, q.st);
         if (s != TB_OK) return s;
         if (q.dH) {
-            if (!make_map(&g_rows, g, q.n, cols, c.ldg, kHalf, bf)) return TB_ERR_CUDA;
+            if (!make_map(&g_rows, g, q.n, cols, c.ldg, box_rows(q.n), bf)) return TB_ERR_CUDA;
             Product r = p;
             r.width = kTile;
             r.out_map = q.d % 8 == 0 && aligned_to(q.dH, 16);
