@@ -250,6 +250,7 @@ struct Product {
     // kDH, kDW
     float* sums;              // kDH: [splits][rows][cols] fp32, NULL: one split, one piece
     int first, last;          // piece: starts the sums; writes the result
+    int sums_map;             // rows of the sums are whole 16 bytes: they go out by TMA
     void* out;                // [rows][cols] 16-bit
     Weigh weigh;              // kGrad
 };
@@ -415,6 +416,31 @@ struct Outbox {
         ++n;
     }
 };
+
+// The same for 32 fp32 columns: one box of both halves' size, swizzled over 128 bytes, of split z.
+// `add`: onto what is there.  (Every element of dH's sums gets one addition a launch: the order of
+// the pieces decides the result, nothing else.)
+__device__ __forceinline__ void put_sums(unsigned char* box, const CUtensorMap* map, int lane, const float (&v)[32],
+                                         int x, int y, int z, bool add) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float4*>(box + lane * 128 + ((i ^ (lane & 7)) * 16)) =
+            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+        const uint32_t src = smem_addr(box);
+        if (add)
+            asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                         ::"l"(map), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
+        else
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                             map), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+}
 
 template <class Fmt>
 __device__ __forceinline__ void store_each(typename Fmt::T* row, int col, int cols, const float (&v)[32]) {
@@ -647,20 +673,19 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     const int col = n0 + c;
                     bool finish = true;
                     if constexpr (K == kDH) {
-                        if (p.sums) {
+                        const bool keep = !p.last || p.splits > 1;
+                        if (p.sums && keep && p.sums_map) {
+                            if (row0 < p.rows)
+                                put_sums(box.mem, &map_out, lane, v, col, row0, split, !p.first);
+                        } else if (p.sums && live) {
                             float* sum = p.sums + ((int64_t)split * p.rows + row) * p.cols + col;
-                            const bool keep = !p.last || p.splits > 1;
-                            if (live && c + 32 <= width && (p.cols & 3) == 0) {
+                            if (p.sums_map && c + 32 <= width) {
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
-                                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                                    if (!p.first) o = *reinterpret_cast<float4*>(sum + 4 * i);
+                                    const float4 o = *reinterpret_cast<const float4*>(sum + 4 * i);
                                     v[4 * i] += o.x, v[4 * i + 1] += o.y, v[4 * i + 2] += o.z, v[4 * i + 3] += o.w;
-                                    if (keep)
-                                        *reinterpret_cast<float4*>(sum + 4 * i) =
-                                            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                                 }
-                            } else if (live) {
+                            } else {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
                                     if (c + i < width) {
@@ -668,8 +693,8 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                                         if (keep) sum[i] = v[i];
                                     }
                             }
-                            __syncwarp();
                         }
+                        __syncwarp();
                         finish = p.last && p.splits == 1;
                     }
                     if (finish) {
@@ -846,6 +871,19 @@ bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64
     return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
               const_cast<void*>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
               out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// dH's fp32 sums [splits][rows][cols], written in boxes of 32 x 32.
+bool make_sums_map(CUtensorMap* map, float* p, int64_t splits, int64_t rows, int64_t cols) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)splits};
+    const cuuint64_t strides[2] = {(cuuint64_t)cols * 4, (cuuint64_t)(rows * cols) * 4};
+    const cuuint32_t box[3] = {32, 32, 1};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1100,7 +1138,12 @@ tb_status run_grad(const Problem& q, const Cut& c) {
             r.sums = c.pieces > 1 || c.splits > 1 ? reinterpret_cast<float*>(q.ws + c.off_sums) : nullptr;
             r.out = q.dH;
             if (c.splits > 1 && r.splits == 1) r.last = 0;
-            if (r.out_map && !make_map(&out, q.dH, q.n, q.d, q.d, 32, bf, true)) return TB_ERR_CUDA;
+            r.sums_map = r.sums && q.d % 4 == 0;
+            if (r.sums_map && (!r.last || r.splits > 1)) {
+                if (!make_sums_map(&out, r.sums, c.splits, q.n, q.d)) return TB_ERR_CUDA;
+            } else if (r.out_map && !make_map(&out, q.dH, q.n, q.d, q.d, 32, bf, true)) {
+                return TB_ERR_CUDA;
+            }
             s = launch_product<Fmt, kDH>(g_rows, w_cols, out, r, q.st);
             if (s != TB_OK) return s;
         }
