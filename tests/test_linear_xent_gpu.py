@@ -134,3 +134,184 @@ def test_gradients(tb, n, d, v, dtype):
     only_h, _ = backward(tb, dloss, H, W, t, lse, "H")
     _, only_w = backward(tb, dloss, H, W, t, lse, "W")
     assert torch.equal(only_h, dH) and torch.equal(only_w, dW)      # and every run is the same
+
+
+# several pieces of the vocabulary (of 256 MiB of G), launches of the loss, and with 7,000 columns
+# pieces whose dH is split as well; row lengths whose fp32 sums TMA can and cannot write
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("n, d, v", [(40000, 24, 5000), (20000, 32, 7000), (20000, 33, 7000)])
+def test_pieces_of_the_vocabulary(tb, n, d, v, dtype):
+    H, W, t, dloss = problem(n, d, v, dtype, 2)
+    loss, lse = forward(tb, H, W, t)
+    check_forward(loss, lse, H, W, t)
+    if dtype == HF:
+        dloss = dloss * 4096
+    dH, dW = backward(tb, dloss, H, W, t, lse)
+    check_backward(dH, dW, dloss, H, W, t, lse)
+    again = backward(tb, dloss, H, W, t, lse)
+    assert torch.equal(again[0], dH) and torch.equal(again[1], dW)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_masks(tb, dtype):
+    """No row counts; one row counts; ignore_index is a class; a dloss of zero."""
+    n, d, v = 70, 72, 300
+    H, W, t, dloss = problem(n, d, v, dtype, 3, ignored=0.0)
+    none = torch.full_like(t, -100)
+    loss, lse = forward(tb, H, W, none)
+    check_forward(loss, lse, H, W, none)
+    assert not loss.any()
+    dH, dW = backward(tb, dloss, H, W, none, lse)
+    assert not dH.any() and not dW.any()
+    one = none.clone()
+    one[17] = t[17]
+    dH, dW = backward(tb, dloss, H, W, one, lse)
+    check_backward(dH, dW, dloss, H, W, one, lse)
+    t[5:9] = 7
+    loss, lse = forward(tb, H, W, t, ignore_index=7)
+    check_forward(loss, lse, H, W, t, ignore=7)
+    dH, dW = backward(tb, dloss, H, W, t, lse, ignore_index=7)
+    check_backward(dH, dW, dloss, H, W, t, lse, ignore=7)
+    dloss[20:40] = 0
+    dH, dW = backward(tb, dloss, H, W, t, lse, ignore_index=7)
+    check_backward(dH, dW, dloss, H, W, t, lse, ignore=7)
+    dloss.zero_()
+    dH, dW = backward(tb, dloss, H, W, t, lse, ignore_index=7)
+    assert not dH.any() and not dW.any()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_what_an_ignored_row_holds_does_not_matter(tb, dtype):
+    n, d, v = 300, 136, 900
+    H, W, t, dloss = problem(n, d, v, dtype, 4)
+    loss, lse = forward(tb, H, W, t)
+    dH, dW = backward(tb, dloss, H, W, t, lse)
+    skip = t == -100
+    assert skip.any()
+    H2, dloss2, lse2 = H.clone(), dloss.clone(), lse.clone()
+    H2[skip] = float("nan")
+    dloss2[skip] = float("inf")
+    lse2[skip] = float("nan")
+    loss2, l2 = forward(tb, H2, W, t)
+    assert torch.equal(loss2, loss) and torch.equal(l2[~skip], lse[~skip])
+    dH2, dW2 = backward(tb, dloss2, H2, W, t, lse2)
+    assert torch.equal(dH2, dH) and torch.equal(dW2, dW)
+
+
+def test_a_target_outside_the_vocabulary(tb):
+    n, d, v = 40, 64, 200
+    H, W, t, dloss = problem(n, d, v, BF, 5, ignored=0.0)
+    loss, lse = forward(tb, H, W, t)
+    assert tb.tb_device_error() == 0
+    bad = t.clone()
+    bad[3], bad[4], bad[5] = v, -1, 2 ** 40
+    loss2, lse2 = forward(tb, H, W, bad)
+    assert tb.tb_device_error() == 1 and tb.tb_device_error() == 0       # read and reset
+    assert loss2[3:6].isnan().all() and torch.equal(lse2, lse)
+    keep = torch.ones(n, dtype=torch.bool, device="cuda")
+    keep[3:6] = False
+    assert torch.equal(loss2[keep], loss[keep])
+    dH, dW = backward(tb, dloss, H, W, bad, lse)
+    skipped = torch.where(keep, t, -100)
+    check_backward(dH, dW, dloss, H, W, skipped, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_infinities_and_large_logits(tb, dtype):
+    n, d, v = 33, 64, 700
+    H, W, t, dloss = problem(n, d, v, dtype, 6, ignored=0.0)
+    H = H * 20                                            # logits of hundreds: differences decide
+    loss, lse = forward(tb, H, W, t)
+    check_forward(loss, lse, H, W, t)
+    dH, dW = backward(tb, dloss, H, W, t, lse)
+    check_backward(dH, dW, dloss, H, W, t, lse)
+    H = H / 20
+    H[1, 0], W[:, 0] = float("inf"), W[:, 0].abs() + 0.01   # a row of +inf logits
+    H[2, 0] = -float("inf")                                 # a row of -inf
+    H[3, 0] = float("nan")
+    loss, lse = forward(tb, H, W, t)
+    assert lse[1] == float("inf") and lse[2] == -float("inf") and lse[3].isnan()
+    assert loss[1:4].isnan().all() and loss[4:].isfinite().all() and loss[0].isfinite()
+
+
+@pytest.mark.parametrize("off", [1, 2, 4])
+@pytest.mark.parametrize("d", [64, 24])
+def test_results_off_their_alignment(tb, d, off):
+    """dH and dW where TMA cannot write them; what lies around them stays."""
+    n, v = 150, 600
+    H, W, t, dloss = problem(n, d, v, BF, 7)
+    _, lse = forward(tb, H, W, t)
+    want = backward(tb, dloss, H, W, t, lse)
+    bufs = [torch.full((k * d + 2 * off + 8,), 5.0, dtype=BF, device="cuda") for k in (n, v)]
+    got = [b[off:off + k * d].view(k, d) for b, k in zip(bufs, (n, v))]
+    ws = workspace(tb.tb_linear_xent_bwd_workspace_size(n, d, v, BF))
+    tb.tb_linear_xent_bwd(dloss, H, W, t, lse, *got, ws)
+    for b, g, w, k in zip(bufs, got, want, (n, v)):
+        assert torch.equal(g, w)
+        assert (b[:off] == 5).all() and (b[off + k * d:] == 5).all()
+
+
+def test_no_rows(tb):
+    W = torch.randn(50, 64, device="cuda").to(BF)
+    H = torch.empty(0, 64, dtype=BF, device="cuda")
+    t, e = torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
+    tb.tb_linear_xent(H, W, t, e, e.clone(), None)
+    dW = torch.ones_like(W)
+    tb.tb_linear_xent_bwd(e, H, W, t, e, H.clone(), dW, None)
+    assert not dW.any()
+
+
+def test_gradient_against_differences(tb):
+    """<dH, a> and <dW, b> against central differences of the 64-bit loss."""
+    n, d, v = 60, 96, 500
+    H, W, t, dloss = problem(n, d, v, BF, 8)
+    _, lse = forward(tb, H, W, t)
+    dH, dW = backward(tb, dloss, H, W, t, lse)
+    keep = t != -100
+    col = torch.where(keep, t, 0)[:, None]
+
+    def f(h, w):
+        l = h @ w.T
+        return ((torch.logsumexp(l, -1) - l.gather(1, col)[:, 0]) * keep * dloss.double()).sum()
+
+    a, b = torch.randn(n, d, device="cuda").double(), torch.randn(v, d, device="cuda").double()
+    H64, W64, h = H.double(), W.double(), 1e-5
+    for grad, x, num in ((dH, a, f(H64 + h * a, W64) - f(H64 - h * a, W64)),
+                         (dW, b, f(H64, W64 + h * b) - f(H64, W64 - h * b))):
+        got, scale = (grad.double() * x).sum(), (grad.double() * x).abs().sum()
+        # three roundings to bf16 (G, H's copy, the result) of every term, and h^2
+        assert (got - num / (2 * h)).abs() <= scale * (3 * 2.0 ** -8 + 1e-6)
+
+
+def test_graph_replay_streams_and_two_calls_at_once(tb):
+    n, d, v = 300, 256, 3000
+    H, W, t, dloss = problem(n, d, v, BF, 9)
+    size = max(tb.tb_linear_xent_workspace_size(n, d, v, BF), tb.tb_linear_xent_bwd_workspace_size(n, d, v, BF))
+
+    def outputs():
+        return [torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty_like(H), torch.empty_like(W)]
+
+    def calls(o, ws):
+        tb.tb_linear_xent(H, W, t, o[0], o[1], ws)
+        tb.tb_linear_xent_bwd(dloss, H, W, t, o[1], o[2], o[3], ws)
+
+    eager, cap, side, side2 = outputs(), outputs(), outputs(), outputs()
+    ws = [workspace(size) for _ in range(4)]
+    calls(eager, ws[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls(cap, ws[1])
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for st, o, w in zip(streams, (side, side2), ws[2:]):
+            with torch.cuda.stream(st):
+                calls(o, w)
+    torch.cuda.synchronize()
+    for o in (cap, side, side2):
+        for x, y in zip(o, eager):
+            assert torch.equal(x, y)
+    assert tb.tb_device_error() == 0
