@@ -422,12 +422,29 @@ __global__ void __launch_bounds__(kThreads, NU == 1 ? 3 : 2) heads_fwd_kernel(co
 // dn = the transposed rotation of dy; xhat = x * r; dxhat = dn * gamma;
 // dx = r * (dxhat - xhat * mean(dxhat * xhat)); dgamma = sum of dn * xhat.
 //
-// 16-bit heads: the next group's vectors are loaded before the present group is worked on, at two
-// CTAs an SM.  fp32 heads hold half as many elements a lane, so three CTAs fit, and three without
-// the early loads are faster: 32,768 x 18 heads x 256 took 295 us against 356 us, bf16 4 x 4,096 x
-// 40 x 128 took 103 us with them and 118 us without (sum of the vectors over 6,766 GB/s: 268, 75).
+// 16-bit heads: the next group's vectors come by cp.async into the lane's own slots of shared memory
+// while the present group is worked on, at two CTAs an SM (a lane holds 16 elements of x, dy, gamma,
+// dgamma and the sines: 128 registers, none left for vectors on their way; loaded into registers and
+// copied, the copies wait for the loads).  bf16 4 x 4,096 tokens of 32 + 8 heads of 128 (75 us at the
+// copy bandwidth): 93 us, with the early loads in registers 103, without early loads 118 at three
+// CTAs.  fp32 heads hold half as many elements a lane, so three CTAs fit, and load when they need it:
+// 32,768 tokens of 16 + 2 heads of 256 (268 us): 295 us, with early loads at two CTAs 356.
 template <class Fmt>
 constexpr bool kBwdAhead = sizeof(typename Fmt::T) == 2;
+
+template <int Bytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    const unsigned to = (unsigned)__cvta_generic_to_shared(dst);
+    if constexpr (Bytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(src), "n"(Bytes) : "memory");
+}
+// A warp's two slots for vectors on their way: x's p and q, dy's p and q for each unit, 32 lanes side
+// by side, and inv_rms.  A lane reads back what it asked for itself: its own copies' completion is all
+// that it waits for.
+template <class Fmt, int E, int NU>
+constexpr int kSlotBytes = kBwdAhead<Fmt> ? 32 * (4 * NU * E * (int)sizeof(typename Fmt::T) + 4) : 0;
 
 template <class Fmt, int E, int NU, int Lanes>
 __device__ __forceinline__ void heads_bwd(const Args& a, const HeadsArg& t, int cta, float* sums) {
@@ -438,6 +455,12 @@ __device__ __forceinline__ void heads_bwd(const Args& a, const HeadsArg& t, int 
     const int grp = min(lane / lanes, per_step - 1), sub = lane % lanes;
     const bool whole = Lanes || lane < per_step * lanes;
     float* table = sums + kWarps * a.head_dim + warp * a.rot;
+    using V = typename Raw<E * (int)sizeof(T)>::V;
+    constexpr int kSlot = kSlotBytes<Fmt, E, NU>;
+    unsigned char* slots = reinterpret_cast<unsigned char*>(sums + (kWarps * (a.head_dim + a.rot) + 3) / 4 * 4) +
+                           warp * 2 * kSlot;
+    auto vec = [&](int slot, int v) { return reinterpret_cast<V*>(slots + slot * kSlot) + v * 32 + lane; };
+    auto inv_at = [&](int slot) { return reinterpret_cast<float*>(slots + (slot + 1) * kSlot - 128) + lane; };
     Units<E, NU> u;
     u.init(a, sub, lanes);
     pdl_wait();
@@ -461,15 +484,34 @@ __device__ __forceinline__ void heads_bwd(const Args& a, const HeadsArg& t, int 
         const T *x = at.row(static_cast<const T*>(t.x), t.sx), *dy = at.row(static_cast<const T*>(t.dy), t.sdy);
         T* dx = at.row(static_cast<T*>(t.y), t.sy);
         const float* inv = t.inv_rms + (int64_t)at.token * t.heads;
-        Head<Fmt, E, NU> hx, hdy, hx_n, hdy_n;
-        float r, r_n;
+        Head<Fmt, E, NU> hx, hdy;
+        float r = 0.f;
+        int slot = 0;
+        auto fetch = [&](const T* px, const T* pdy, const float* pinv, int h, int to) {
+#pragma unroll
+            for (int j = 0; j < NU; ++j) {
+                if (NU > 1 && !u.live[j]) continue;
+                constexpr int kVec = E * (int)sizeof(T);
+                copy_async<kVec>(vec(to, 4 * j), px + h * t.sx.h + u.first[j]);
+                copy_async<kVec>(vec(to, 4 * j + 1), px + h * t.sx.h + u.second[j]);
+                copy_async<kVec>(vec(to, 4 * j + 2), pdy + h * t.sdy.h + u.first[j]);
+                copy_async<kVec>(vec(to, 4 * j + 3), pdy + h * t.sdy.h + u.second[j]);
+            }
+            copy_async<4>(inv_at(to), pinv + h);
+        };
+        if constexpr (kBwdAhead<Fmt>) {
+            for (int k = 0; k < 8 * NU; ++k) *vec(k / (4 * NU), k % (4 * NU)) = {};    // (dead units)
+        }
         auto load = [&](const T* px, const T* pdy, const float* pinv, int h, Head<Fmt, E, NU>& ox,
                         Head<Fmt, E, NU>& ody, float& or_) {
             ox.load(px + h * t.sx.h, u);
             ody.load(pdy + h * t.sdy.h, u);
             or_ = __ldg(pinv + h);
         };
-        if (kBwdAhead<Fmt>) load(x, dy, inv, min(at.head + grp, at.end - 1), hx, hdy, r);
+        if constexpr (kBwdAhead<Fmt>) {
+            fetch(x, dy, inv, min(at.head + grp, at.end - 1), 0);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
         for (;;) {                        // items
             fill_table<Fmt>(a, pos, table, lane);
 #pragma unroll
@@ -493,13 +535,25 @@ __device__ __forceinline__ void heads_bwd(const Args& a, const HeadsArg& t, int 
             for (int h0 = at.head; h0 < at.end; h0 += per_step) {
                 // the next group's vectors, of the next item behind the last
                 const bool same = h0 + per_step < at.end;
-                if (kBwdAhead<Fmt> && (same || more))
-                    load(same ? x : x_n, same ? dy : dy_n, same ? inv : inv_n,
-                         same ? min(h0 + per_step + grp, at.end - 1) : min(nxt.head + grp, nxt.end - 1), hx_n, hdy_n,
-                         r_n);
                 const int h = h0 + grp;
                 const bool mine = whole && h < at.end;
-                if (!kBwdAhead<Fmt>) load(x, dy, inv, min(h, at.end - 1), hx, hdy, r);
+                if constexpr (kBwdAhead<Fmt>) {
+                    if (same || more)
+                        fetch(same ? x : x_n, same ? dy : dy_n, same ? inv : inv_n,
+                              same ? min(h + per_step, at.end - 1) : min(nxt.head + grp, nxt.end - 1), slot ^ 1);
+                    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory");
+#pragma unroll
+                    for (int j = 0; j < NU; ++j) {
+                        hx.p[j].raw = *vec(slot, 4 * j);
+                        hx.q[j].raw = *vec(slot, 4 * j + 1);
+                        hdy.p[j].raw = *vec(slot, 4 * j + 2);
+                        hdy.q[j].raw = *vec(slot, 4 * j + 3);
+                    }
+                    r = *inv_at(slot);
+                    slot ^= 1;
+                } else {
+                    load(x, dy, inv, min(h, at.end - 1), hx, hdy, r);
+                }
                 F2 d[NU][E], xr[NU][E];
                 F2 dot2 = f2(0.f);
 #pragma unroll
@@ -559,11 +613,6 @@ __device__ __forceinline__ void heads_bwd(const Args& a, const HeadsArg& t, int 
                         Chunk<Fmt, E>::store(row + u.first[j], p);
                         Chunk<Fmt, E>::store(row + u.second[j], q);
                     }
-                }
-                if (kBwdAhead<Fmt>) {
-                    hx = hx_n;
-                    hdy = hdy_n;
-                    r = r_n;
                 }
             }
             if (!more) break;
@@ -885,7 +934,8 @@ tb_status launch_lanes(Args a, const Call& c, int sms, cudaStream_t st) {
         c.bwd_norm ? reinterpret_cast<const void*>(&heads_bwd_kernel<Fmt, E, NU, Lanes>)
         : c.norm   ? reinterpret_cast<const void*>(&heads_fwd_kernel<Fmt, E, NU, kNorm, Lanes>)
                    : reinterpret_cast<const void*>(&heads_fwd_kernel<Fmt, E, NU, kRope, Lanes>);
-    const size_t smem = sizeof(float) * kWarps * (a.rot + (c.bwd_norm ? a.head_dim : 0));
+    size_t smem = sizeof(float) * kWarps * a.rot;
+    if (c.bwd_norm) smem = (smem + sizeof(float) * kWarps * a.head_dim + 15) / 16 * 16 + kWarps * 2 * kSlotBytes<Fmt, E, NU>;
     const int resident = resident_ctas_per_sm(kernel, kThreads, smem);
     if (resident == 0) return TB_ERR_CUDA;
     const int64_t grid_ctas = (int64_t)sms * std::min(resident, kBwdCtasPerSm);
