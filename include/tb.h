@@ -637,8 +637,8 @@ tb_status tb_qk_norm_rope_bwd(const tb_heads* dq_out, const tb_heads* dk_out,
  * D not a multiple of 8 costs a padded copy of H and W in the workspace per call.
  * Results must not overlap inputs, each other or the workspace.  rows == 0 writes zeros to
  * dW and nothing else.
- * Errors: TB_ERR_INVALID_VALUE (null or negative; D or vocab below 1; rows, D or vocab of
- * 2^31 - 511 or more, rows * D or vocab * D above 2^40; dH and dW both NULL),
+ * Errors: TB_ERR_INVALID_VALUE (null or negative; D or vocab below 1; rows, D or vocab above
+ * 2^24, rows * D or vocab * D above 2^40; dH and dW both NULL),
  * TB_ERR_UNSUPPORTED_DTYPE (TB_F32 has no such tensor-core product), TB_ERR_MISALIGNED,
  * TB_ERR_ALIAS, TB_ERR_WORKSPACE, TB_ERR_CUDA.
  */

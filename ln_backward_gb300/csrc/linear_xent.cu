@@ -245,8 +245,6 @@ struct Product {
     const float* lse;         // kGrad
     const float* weight;      // kDH: dloss by row, 0 where a row takes no part
     const float* top;         // kDW: the largest |dloss|
-    void* g;                  // kGrad: [rows][ldg]
-    int ldg;
     // kDH, kDW
     float* sums;              // kDH: [splits][rows][cols] fp32, NULL: one split, one piece
     int first, last;          // piece: starts the sums; writes the result
@@ -894,7 +892,8 @@ tb_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUten
     const int pairs = resident_clusters(kernel, kThreads, kSmem, 2);
     if (pairs < 1) return TB_ERR_CUDA;
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles * p.splits;
-    const int64_t grid = 2 * std::min<int64_t>(tiles, pairs);
+    // (pairs without a tile still take their share of weigh_rows)
+    const int64_t grid = 2 * (p.weigh.weight ? pairs : std::min<int64_t>(tiles, pairs));
     if (launch_clusters<true>(product_kernel<Fmt, K>, dim3((unsigned)grid), dim3(kThreads), kSmem, st, 2, a, b, out, p) !=
         cudaSuccess)
         return TB_ERR_CUDA;
@@ -987,7 +986,9 @@ Cut cut_call(int64_t n, int64_t d, int64_t v, bool bwd, int sms) {
 // memory held; it reaches only rows that nothing stores.
 int box_rows(int64_t rows) { return rows < kHalf ? (int)round_up(rows, 8) : kHalf; }
 
-constexpr int64_t kMaxSize = (1ll << 31) - 512;
+// A tile's MMAs take 0.3 to 0.7 us for 64 contracted elements, and the epilogue waits for a whole
+// tile: 2^24 of them stay well inside the wait limit.
+constexpr int64_t kMaxSize = 1ll << 24;
 
 tb_status check_sizes(int64_t n, int64_t d, int64_t v, tb_dtype dtype) {
     if (n < 0 || d < 1 || v < 1 || n > kMaxSize || d > kMaxSize || v > kMaxSize) return TB_ERR_INVALID_VALUE;
@@ -1117,8 +1118,6 @@ tb_status run_grad(const Problem& q, const Cut& c) {
         p.top = top;
         if (i == 0)
             p.weigh = Weigh{q.dloss, q.H, q.dW ? scaled : nullptr, weight, top, q.n, (int)q.d, (int)c.ld};
-        p.g = g;
-        p.ldg = (int)c.ldg;
         if (!make_map(&out, g, q.n, cols, c.ldg, 32, bf, true)) return TB_ERR_CUDA;
         tb_status s = launch_product<Fmt, kGrad>(h_rows, w_rows, out, p, q.st);
         if (s != TB_OK) return s;

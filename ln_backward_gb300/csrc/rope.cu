@@ -334,74 +334,73 @@ __device__ __forceinline__ void heads_fwd(const Args& a, const HeadsArg& t, int 
     u.init(a, sub, lanes);
     pdl_wait();
     pdl_trigger();
-    const unsigned items = a.tokens * t.chunks;
-    for (unsigned i = cta * kWarps + warp; i < items; i += t.ctas * kWarps) {
-        Item at;
-        at.open(a, t, i, per_step);
-        const long long pos = position(a, at.b, at.s);
-        const T* x = at.row(static_cast<const T*>(t.x), t.sx);
-        T* y = at.row(static_cast<T*>(t.y), t.sy);
-        Turn<E> turn[NU];
-        bool fresh = true;
-        constexpr int kAhead = 2;         // head groups loaded together
-        for (int h0 = at.head; h0 < at.end; h0 += kAhead * per_step) {
-            Head<Fmt, E, NU> in[kAhead];
+    const unsigned item = cta * kWarps + warp;    // one for each warp
+    if (item >= a.tokens * t.chunks) return;
+    Item at;
+    at.open(a, t, item, per_step);
+    const long long pos = position(a, at.b, at.s);
+    const T* x = at.row(static_cast<const T*>(t.x), t.sx);
+    T* y = at.row(static_cast<T*>(t.y), t.sy);
+    Turn<E> turn[NU];
+    bool fresh = true;
+    constexpr int kAhead = 2;         // head groups loaded together
+    for (int h0 = at.head; h0 < at.end; h0 += kAhead * per_step) {
+        Head<Fmt, E, NU> in[kAhead];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                in[k].load(x + min(h0 + k * per_step + grp, at.end - 1) * t.sx.h, u);
-            if (fresh) {                  // (while the first heads are on their way)
-                fill_table<Fmt>(a, pos, table, lane);
+        for (int k = 0; k < kAhead; ++k)
+            in[k].load(x + min(h0 + k * per_step + grp, at.end - 1) * t.sx.h, u);
+        if (fresh) {                  // (while the first heads are on their way)
+            fill_table<Fmt>(a, pos, table, lane);
 #pragma unroll
-                for (int j = 0; j < NU; ++j) {
-                    float g[2 * E];
+            for (int j = 0; j < NU; ++j) {
+                float g[2 * E];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        g[e] = Mode == kNorm ? __ldg(t.gamma + u.first[j] + e) : 1.f;
-                        g[E + e] = Mode == kNorm ? __ldg(t.gamma + u.second[j] + e) : 1.f;
-                    }
-                    turn[j].set(table + u.freq[j], table + a.rot / 2 + u.freq[j], g, u.turns[j], a.interleaved);
+                for (int e = 0; e < E; ++e) {
+                    g[e] = Mode == kNorm ? __ldg(t.gamma + u.first[j] + e) : 1.f;
+                    g[E + e] = Mode == kNorm ? __ldg(t.gamma + u.second[j] + e) : 1.f;
                 }
-                fresh = false;
+                turn[j].set(table + u.freq[j], table + a.rot / 2 + u.freq[j], g, u.turns[j], a.interleaved);
+            }
+            fresh = false;
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int h = h0 + k * per_step + grp;
+            if (k > 0 && h - grp >= at.end) break;
+            const bool mine = whole && h < at.end;
+            F2 p[NU][H], q[NU][H];
+#pragma unroll
+            for (int j = 0; j < NU; ++j) {
+                in[k].p[j].get(p[j]);
+                in[k].q[j].get(q[j]);
+            }
+            float r = 1.f;
+            if constexpr (Mode == kNorm) {
+                F2 ss = f2(0.f);
+#pragma unroll
+                for (int j = 0; j < NU; ++j)
+#pragma unroll
+                    for (int e = 0; e < H; ++e) ss = fma2(q[j][e], q[j][e], fma2(p[j][e], p[j][e], ss));
+                float lo, hi;
+                split(ss, lo, hi);
+                r = rsqrtf(sum_lanes<Lanes>(lo + hi, lanes, sub) * a.inv_dim + a.eps);
+                if (t.inv_rms && sub == 0 && mine) t.inv_rms[(int64_t)at.token * t.heads + h] = r;
             }
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int h = h0 + k * per_step + grp;
-                if (k > 0 && h - grp >= at.end) break;
-                const bool mine = whole && h < at.end;
-                F2 p[NU][H], q[NU][H];
-#pragma unroll
-                for (int j = 0; j < NU; ++j) {
-                    in[k].p[j].get(p[j]);
-                    in[k].q[j].get(q[j]);
-                }
-                float r = 1.f;
+            for (int j = 0; j < NU; ++j) {
+                turn[j].apply(p[j], q[j], u.turns[j], a.interleaved);
                 if constexpr (Mode == kNorm) {
-                    F2 ss = f2(0.f);
 #pragma unroll
-                    for (int j = 0; j < NU; ++j)
-#pragma unroll
-                        for (int e = 0; e < H; ++e) ss = fma2(q[j][e], q[j][e], fma2(p[j][e], p[j][e], ss));
-                    float lo, hi;
-                    split(ss, lo, hi);
-                    r = rsqrtf(sum_lanes<Lanes>(lo + hi, lanes, sub) * a.inv_dim + a.eps);
-                    if (t.inv_rms && sub == 0 && mine) t.inv_rms[(int64_t)at.token * t.heads + h] = r;
+                    for (int e = 0; e < H; ++e) p[j][e] = p[j][e] * f2(r), q[j][e] = q[j][e] * f2(r);
                 }
+            }
+            if (mine) {
+                T* row = y + h * t.sy.h;
 #pragma unroll
                 for (int j = 0; j < NU; ++j) {
-                    turn[j].apply(p[j], q[j], u.turns[j], a.interleaved);
-                    if constexpr (Mode == kNorm) {
-#pragma unroll
-                        for (int e = 0; e < H; ++e) p[j][e] = p[j][e] * f2(r), q[j][e] = q[j][e] * f2(r);
-                    }
-                }
-                if (mine) {
-                    T* row = y + h * t.sy.h;
-#pragma unroll
-                    for (int j = 0; j < NU; ++j) {
-                        if (NU > 1 && !u.live[j]) continue;
-                        Chunk<Fmt, E>::store(row + u.first[j], p[j]);
-                        Chunk<Fmt, E>::store(row + u.second[j], q[j]);
-                    }
+                    if (NU > 1 && !u.live[j]) continue;
+                    Chunk<Fmt, E>::store(row + u.first[j], p[j]);
+                    Chunk<Fmt, E>::store(row + u.second[j], q[j]);
                 }
             }
         }
@@ -500,7 +499,10 @@ __device__ __forceinline__ void heads_bwd(const Args& a, const HeadsArg& t, int 
             copy_async<4>(inv_at(to), pinv + h);
         };
         if constexpr (kBwdAhead<Fmt>) {
-            for (int k = 0; k < 8 * NU; ++k) *vec(k / (4 * NU), k % (4 * NU)) = {};    // (dead units)
+#pragma unroll
+            for (int j = 0; j < NU; ++j)      // units that no copy fills count as zeros
+                if (NU > 1 && !u.live[j])
+                    for (int k = 0; k < 8; ++k) *vec(k / 4, 4 * j + k % 4) = {};
         }
         auto load = [&](const T* px, const T* pdy, const float* pinv, int h, Head<Fmt, E, NU>& ox,
                         Head<Fmt, E, NU>& ody, float& or_) {
@@ -922,11 +924,10 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Head groups of one token that a warp takes: all, so that it forms the token's sines once,
 // unless that would leave warps of the resident grid without work.
 //
-// Forward: one launch of CTAs whose warps take kFwdItems tokens each; the hardware deals them out
-// as SMs come free, which a grid of resident CTAs cannot (the SMs of the two dies are not equally
-// fast).  The gradient keeps its dgamma sums in registers, so its grid is the resident one.
-constexpr int kFwdItems = 2;
-
+// Forward: one item a warp, and the hardware deals the CTAs out as SMs come free, which a grid of
+// resident CTAs cannot (the SMs of the two dies are not equally fast): bf16 4 x 4,096 tokens of 64
+// heads of 128 rotated in 83.2 us, 84.6 with two items a warp, 91.9 with four.  The gradient keeps
+// its dgamma sums in registers, so its grid is the resident one.
 template <class Fmt, int E, int NU, int Lanes>
 tb_status launch_lanes(Args a, const Call& c, int sms, cudaStream_t st) {
     const int per_step = 32 / a.lanes;
@@ -950,7 +951,7 @@ tb_status launch_lanes(Args a, const Call& c, int sms, cudaStream_t st) {
         t.steps = (int)ceil_div(steps, t.chunks);
         t.chunks = (int)ceil_div(steps, t.steps);
         const int64_t ctas = ceil_div((int64_t)a.tokens * t.chunks, kWarps);
-        t.ctas = (int)(c.bwd_norm ? std::min(share, ctas) : std::max(std::min(share, ctas), ceil_div(ctas, kFwdItems)));
+        t.ctas = (int)(c.bwd_norm ? std::min(share, ctas) : ctas);
     }
     if (c.n == 1) a.t[1].ctas = 0;
     if (c.bwd_norm) a.t[1].partial = a.t[0].partial + (int64_t)a.t[0].ctas * a.head_dim;
