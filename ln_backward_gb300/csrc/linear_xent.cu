@@ -62,7 +62,6 @@ constexpr unsigned long long kWaitLimitNs = 1000000000ull;
 constexpr int64_t kPieceBytes = 256ll << 20;
 constexpr int64_t kMinPiece = 2048;
 constexpr int64_t kLseRows = 16384;          // rows of one launch of the loss (workspace)
-constexpr int kMaxSplits = 16;
 
 // ---------------------------------------------------------------- PTX
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -217,6 +216,26 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp, 0 below -126
     return y;
 }
 
+// Two fp32 values in a register pair: both are added or multiplied in one issue slot.
+__device__ __forceinline__ unsigned long long pair_of(float lo, float hi) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split_pair(unsigned long long a, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a));
+}
+__device__ __forceinline__ unsigned long long fma_pair(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add_pair(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 constexpr float kLog2e = 1.44269504088896341f;
 
 // ---------------------------------------------------------------- arguments
@@ -289,7 +308,7 @@ __device__ __forceinline__ void tile_at(const Product& p, unsigned t, int* split
 __device__ __forceinline__ void stages_of(const Product& p, int split, int* lo, int* hi) {
     *lo = 0;
     *hi = p.k_stages;
-    if (p.splits > 1) {           // (16 splits of at most 2^31 / 64 stages: no overflow)
+    if (p.splits > 1) {           // (a split a pair of at most 2^24 / 64 stages: no overflow)
         *lo = (int)((unsigned)split * p.k_stages / (unsigned)p.splits);
         *hi = (int)((unsigned)(split + 1) * p.k_stages / (unsigned)p.splits);
     }
@@ -301,12 +320,12 @@ __device__ __forceinline__ void stages_of(const Product& p, int split, int* lo, 
 // a warp's 16-byte pieces lie a row apart, 32 half sectors an instruction: the epilogue then took
 // longer than the MMAs of a tile with 768 contracted elements (78 us against 62 us, 1,021 x 50,257).
 // What the later products need of dloss: each row's weight (0 where it takes no part), the largest
-// magnitude among them, and H with every row times its weight over that.  One otherwise idle warp
-// of each CTA does its share of it while the logits' product runs (a kernel of its own in front of
+// magnitude among them, and H with every row times its weight over that.  Two otherwise idle warps
+// of each CTA do their share of it while the logits' product runs (a kernel of its own in front of
 // them took 8 us at 1,021 x 768); each finds the maximum by itself, rows * 12 bytes from L2.
 template <class Fmt>
 __device__ __forceinline__ void weigh_rows(const Weigh& w, const int64_t* target, int64_t ignore, int vocab,
-                                           int lane, int cta, int ctas) {
+                                           int lane, int part, int parts) {
     using T = typename Fmt::T;
     auto weight_of = [&](int64_t r) {
         const int64_t t = target[r];
@@ -316,19 +335,21 @@ __device__ __forceinline__ void weigh_rows(const Weigh& w, const int64_t* target
 #pragma unroll 8
     for (int64_t r = lane; r < w.rows; r += 32) {
         const float v = weight_of(r);
-        if (r / 32 % ctas == cta) w.weight[r] = v;
+        if (r / 32 % parts == part) w.weight[r] = v;
         if (fabsf(v) <= 3.4028235e38f) m = fmaxf(m, fabsf(v));   // neither infinite nor NaN
     }
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (m == 0.f) m = 1.f;
-    if (cta == 0 && lane == 0) *w.top = m;
+    if (part == 0 && lane == 0) *w.top = m;
     if (!w.scaled) return;
     const T* H = static_cast<const T*>(w.H);
     T* scaled = static_cast<T*>(w.scaled);
-    for (int64_t r = cta; r < w.rows; r += ctas) {
-        const float v = weight_of(r), f = v / m;
+    float ahead = part < w.rows ? weight_of(part) : 0.f;
+    for (int64_t r = part; r < w.rows; r += parts) {
+        const float v = ahead, f = v / m;
+        if (r + parts < w.rows) ahead = weight_of(r + parts);
         if (w.cols == w.ld) {         // whole 16-byte vectors
-#pragma unroll 4
+#pragma unroll 8
             for (int c = lane * 8; c < w.cols; c += 256) {
                 float x[8];
                 unpack8<Fmt>(*reinterpret_cast<const uint4*>(H + r * w.cols + c), x);
@@ -397,10 +418,7 @@ struct Outbox {
     unsigned char* mem;       // this warp's two boxes
     const CUtensorMap* map;
     int lane, n;              // boxes filled so far
-    __device__ __forceinline__ void put(const float (&v)[32], int x, int y) {
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        __syncwarp();         // the box of two stores ago has been read
-        unsigned char* box = mem + (n & 1) * kOutBytes;
+    __device__ __forceinline__ void fill(unsigned char* box, const float (&v)[32]) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float f[8];
@@ -408,10 +426,31 @@ struct Outbox {
             for (int e = 0; e < 8; ++e) f[e] = v[8 * i + e];
             *reinterpret_cast<uint4*>(box + lane * 64 + ((i ^ (lane / 2 & 3)) * 16)) = pack8<Fmt>(f);
         }
+    }
+    __device__ __forceinline__ void put(const float (&v)[32], int x, int y) {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();         // the box of two stores ago has been read
+        unsigned char* box = mem + (n & 1) * kOutBytes;
+        fill(box, v);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) tma_store(map, x, y, smem_addr(box));
         ++n;
+    }
+    // Where rows do not start on 16 bytes: the box's rows one after another, a column a lane.
+    __device__ __forceinline__ void put_plain(const float (&v)[32], typename Fmt::T* out, int x, int y, int rows,
+                                              int cols) {
+        using T = typename Fmt::T;
+        __syncwarp();
+        fill(mem, v);
+        __syncwarp();
+        if (x + lane < cols) {
+            const int last = min(32, rows - y);
+            T* to = out + (int64_t)y * cols + x + lane;
+#pragma unroll 8
+            for (int r = 0; r < last; ++r, to += cols)
+                *to = *reinterpret_cast<const T*>(mem + r * 64 + (((lane / 8) ^ (r / 2 & 3)) * 16) + lane % 8 * 2);
+        }
     }
 };
 
@@ -438,13 +477,6 @@ __device__ __forceinline__ void put_sums(unsigned char* box, const CUtensorMap* 
                              map), "r"(x), "r"(y), "r"(z), "r"(src) : "memory");
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
-}
-
-template <class Fmt>
-__device__ __forceinline__ void store_each(typename Fmt::T* row, int col, int cols, const float (&v)[32]) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        if (col + i < cols) row[col + i] = Fmt::from_f32(v[i]);
 }
 
 // Folds 32 logits into a row's maximum m and sum s of exp(l - base(m)); base is 0 where the
@@ -584,9 +616,9 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 mbar_wait(drain, 0, p.err);
             }
         }
-    } else if (K == kGrad && warp == 3) {
+    } else if (K == kGrad && (warp == 2 || warp == 3)) {
         if (p.weigh.weight)
-            weigh_rows<Fmt>(p.weigh, p.target, p.ignore, p.vocab, lane, blockIdx.x, gridDim.x);
+            weigh_rows<Fmt>(p.weigh, p.target, p.ignore, p.vocab, lane, blockIdx.x * 2 + (warp & 1), gridDim.x * 2);
     } else if (warp >= kEpiWarp) {
         // TMEM lanes 32 quad .. 32 quad + 31 (a warp reaches those of its number modulo 4), and
         // the first or second half of the tile's columns
@@ -644,19 +676,32 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                         for (int i = 0; i < 32; ++i)
                             if (c + i >= width) v[i] = __int_as_float(0xff800000);
                     }
-                    float top = v[0], part = 0.f, part2 = 0.f;
+                    // four chains each: one of 31 maxima and one of 32 sums take longer than the
+                    // exponentials
+                    float top4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                    for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
-                    const float b = base_of(top) * kLog2e;
+                    for (int i = 4; i < 32; ++i) top4[i & 3] = fmaxf(top4[i & 3], v[i]);
+                    const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+                    const unsigned long long b2 = pair_of(-base_of(top) * kLog2e, -base_of(top) * kLog2e),
+                                             scale = pair_of(kLog2e, kLog2e);
+                    unsigned long long sum[4] = {0, 0, 0, 0};
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        part += exp2_fast(fmaf(v[i], kLog2e, -b));
-                        part2 += exp2_fast(fmaf(v[i + 1], kLog2e, -b));
+                    for (int i = 0; i < 16; ++i) {
+                        float lo, hi;
+                        split_pair(fma_pair(pair_of(v[2 * i], v[2 * i + 1]), scale, b2), lo, hi);
+                        sum[i & 3] = add_pair(sum[i & 3], pair_of(exp2_fast(lo), exp2_fast(hi)));
                     }
+                    float part, part2;
+                    split_pair(add_pair(add_pair(sum[0], sum[1]), add_pair(sum[2], sum[3])), part, part2);
                     fold(m, s, top, part + part2);
                 } else if constexpr (K == kGrad) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = exp2_fast(fmaf(v[i], kLog2e, -lse2));
+                    for (int i = 0; i < 32; i += 2) {
+                        split_pair(fma_pair(pair_of(v[i], v[i + 1]), pair_of(kLog2e, kLog2e), pair_of(-lse2, -lse2)),
+                                   v[i], v[i + 1]);
+                        v[i] = exp2_fast(v[i]);
+                        v[i + 1] = exp2_fast(v[i + 1]);
+                    }
                     if ((hit & ~31) == c) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = c + i == hit ? v[i] - kGScale<Fmt> : v[i];
@@ -699,10 +744,9 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             v[i] = K == kDH ? weigh<Fmt>(v[i], weight) : v[i] * (1.f / kGScale<Fmt>) * top_weight;
-                        if (p.out_map) {
-                            if (row0 < p.rows) box.put(v, n0 + c, row0);
-                        } else if (live) {
-                            store_each<Fmt>(out + (int64_t)row * p.cols, col, p.cols, v);
+                        if (row0 < p.rows) {
+                            if (p.out_map) box.put(v, col, row0);
+                            else box.put_plain(v, out, col, row0, p.rows, p.cols);
                         }
                     }
                 }
@@ -818,16 +862,50 @@ join_dh_kernel(const float* sums, int splits, int64_t n, int cols, const float* 
     else out[i] = r[0];
 }
 
-// Rows padded with zeros to a multiple of eight elements: TMA wants strides of 16 bytes.
-__global__ void __launch_bounds__(256)
-pad_kernel(const uint16_t* in, uint16_t* out, int64_t rows, int cols, int ld) {
+// Rows padded with zeros to a multiple of eight elements: TMA wants strides of 16 bytes.  A thread
+// writes one 16-byte vector; what it reads starts on any element, so it loads the words around it
+// (inside the matrix) and shifts.
+struct Pad {
+    const void* in[2];        // H, W
+    void* out[2];
+    int64_t rows[2];
+    unsigned ctas;            // of H
+    int cols, ld;
+};
+// Rows of a CTA: a thread finds its row by a 32-bit division, and has a few vectors.
+__host__ __device__ constexpr int64_t pad_rows_a_cta(int ld) { return 1024 / (ld / 8) + 1; }
+__global__ void __launch_bounds__(256) pad_kernel(const __grid_constant__ Pad p) {
     pdl_wait();
     pdl_trigger();
-    const int64_t n = rows * ld;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / ld;
-        const int c = (int)(i - r * ld);
-        out[i] = c < cols ? in[r * cols + c] : (uint16_t)0;
+    const int which = blockIdx.x >= p.ctas;
+    const void* in = p.in[which];
+    uint4* out = static_cast<uint4*>(p.out[which]);
+    const int64_t rows = p.rows[which];
+    const int cols = p.cols;
+    const unsigned per_row = (unsigned)p.ld / 8;
+    const int64_t total = rows * cols;
+    const int64_t row0 = (int64_t)(blockIdx.x - (which ? p.ctas : 0)) * pad_rows_a_cta(p.ld);
+    const int64_t rows_here = min(rows - row0, pad_rows_a_cta(p.ld));
+    for (unsigned i = threadIdx.x; i < (unsigned)rows_here * per_row; i += 256) {
+        const unsigned r = i / per_row, c = (i - r * per_row) * 8;
+        const int64_t at = (row0 + r) * cols + c, word = at >> 1;
+        const int64_t words = total >> 1;        // whole words of the matrix
+        const unsigned* w = reinterpret_cast<const unsigned*>(in);
+        unsigned x[5];
+#pragma unroll
+        for (int k = 0; k < 5; ++k)
+            x[k] = word + k < words ? w[word + k] : word + k == words && (total & 1) ? static_cast<const uint16_t*>(in)[total - 1] : 0u;
+        if (at & 1) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = __funnelshift_r(x[k], x[k + 1], 16);
+        }
+        const int keep = cols - (int)c;          // elements of this row in the vector
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (2 * k >= keep) x[k] = 0;
+            else if (2 * k + 1 >= keep) x[k] &= 0xffffu;
+        }
+        out[(row0 + r) * per_row + c / 8] = make_uint4(x[0], x[1], x[2], x[3]);
     }
 }
 
@@ -913,17 +991,18 @@ struct Cut {
     size_t off_h, off_w, off_scaled, off_weight, off_g, off_sums, off_top, off_part, off_logit, total;
 };
 
-// Parts of the vocabulary that dH's products are split into: as many as fill the machine
-// when its tiles do not.  One more split saves a share of the contraction and costs one
-// more pass over dH in fp32; the cost below counts both in stages (64 contracted elements
-// of a tile, about 0.3 us).
-int pick_splits(int64_t m_tiles, int64_t n_tiles, int64_t k_stages, int64_t pairs) {
+// Parts of the vocabulary that dH's products are split into: as many as fill the machine when its
+// tiles do not.  The cost counts in stages (64 contracted elements of a tile, about 0.3 us): waves of
+// tiles, about eight more for each one's epilogue, and for the sums that the splits leave a launch and
+// their bytes.  (fp16 1,021 x 768 against 50,257: six splits, 160 us; none, 314 us.)
+int pick_splits(int64_t n, int64_t d, int64_t k_stages, int64_t pairs) {
+    const int64_t tiles = ceil_div(n, kTile) * ceil_div(d, kTile);
     int best = 1;
     double least = 1e30;
-    for (int s = 1; s <= kMaxSplits && s <= k_stages; ++s) {
-        const double waves = (double)ceil_div(m_tiles * n_tiles * s, pairs);
-        const double cost = waves * ((double)ceil_div(k_stages, s) + 8.0) + (s > 1 ? 12.0 + 2.0 * s : 0.0);
-        if (cost < least * 0.97) least = cost, best = s;
+    for (int64_t s = 1; s <= std::min<int64_t>(pairs, k_stages); ++s) {
+        const double cost = (double)ceil_div(tiles * s, pairs) * ((double)ceil_div(k_stages, s) + 8.0) +
+                            (s > 1 ? 12.0 + (double)s * (0.05 + (double)(n * d) / 450000.0) : 0.0);
+        if (cost < least * 0.97) least = cost, best = (int)s;
     }
     return best;
 }
@@ -970,7 +1049,7 @@ Cut cut_call(int64_t n, int64_t d, int64_t v, bool bwd, int sms) {
         c.pieces = ceil_div(v, c.piece);
         c.ldg = c.piece;
         c.grad_width = pick_width(ceil_div(n, kTile), std::min(c.piece, v), sms / 2);
-        c.splits = pick_splits(ceil_div(n, kTile), ceil_div(d, kTile), c.piece / kStageK, sms / 2);
+        c.splits = pick_splits(n, d, c.piece / kStageK, sms / 2);
         c.off_g = take((size_t)n * c.ldg * 2);
         if (c.pieces > 1 || c.splits > 1) c.off_sums = take((size_t)c.splits * n * d * sizeof(float));
         c.off_scaled = take((size_t)n * c.ld * 2);
@@ -1010,13 +1089,16 @@ tb_status workspace(int64_t n, int64_t d, int64_t v, tb_dtype dtype, bool bwd, s
     return TB_OK;
 }
 
-tb_status pad_rows(const void* in, void* out, int64_t rows, int64_t cols, int64_t ld, int sms,
+tb_status pad_both(const void* H, const void* W, unsigned char* ws, const Cut& c, int64_t n, int64_t v, int64_t d,
                    cudaStream_t st) {
-    const int64_t grid = std::min<int64_t>(ceil_div(rows * ld, 256), (int64_t)sms * 8);
-    return launch_pdl(pad_kernel, dim3((unsigned)grid), dim3(256), 0, st, static_cast<const uint16_t*>(in),
-                      static_cast<uint16_t*>(out), rows, (int)cols, (int)ld) == cudaSuccess
-               ? TB_OK
-               : TB_ERR_CUDA;
+    Pad p{};
+    p.in[0] = H, p.in[1] = W;
+    p.out[0] = ws + c.off_h, p.out[1] = ws + c.off_w;
+    p.rows[0] = n, p.rows[1] = v;
+    p.cols = (int)d, p.ld = (int)c.ld;
+    p.ctas = (unsigned)ceil_div(n, pad_rows_a_cta(p.ld));
+    const int64_t grid = p.ctas + ceil_div(v, pad_rows_a_cta(p.ld));
+    return launch_pdl(pad_kernel, dim3((unsigned)grid), dim3(256), 0, st, p) == cudaSuccess ? TB_OK : TB_ERR_CUDA;
 }
 
 struct Problem {
@@ -1037,9 +1119,7 @@ tb_status run_loss(const Problem& q, const Cut& c) {
     constexpr bool bf = std::is_same<Fmt, BF16>::value;
     const void *H = q.H, *W = q.W;
     if (c.pad) {
-        if (pad_rows(q.H, q.ws + c.off_h, q.n, q.d, c.ld, q.sms, q.st) != TB_OK ||
-            pad_rows(q.W, q.ws + c.off_w, q.v, q.d, c.ld, q.sms, q.st) != TB_OK)
-            return TB_ERR_CUDA;
+        if (pad_both(q.H, q.W, q.ws, c, q.n, q.v, q.d, q.st) != TB_OK) return TB_ERR_CUDA;
         H = q.ws + c.off_h;
         W = q.ws + c.off_w;
     }
@@ -1081,9 +1161,7 @@ tb_status run_grad(const Problem& q, const Cut& c) {
     constexpr bool bf = std::is_same<Fmt, BF16>::value;
     const void *H = q.H, *W = q.W;
     if (c.pad) {
-        if (pad_rows(q.H, q.ws + c.off_h, q.n, q.d, c.ld, q.sms, q.st) != TB_OK ||
-            pad_rows(q.W, q.ws + c.off_w, q.v, q.d, c.ld, q.sms, q.st) != TB_OK)
-            return TB_ERR_CUDA;
+        if (pad_both(q.H, q.W, q.ws, c, q.n, q.v, q.d, q.st) != TB_OK) return TB_ERR_CUDA;
         H = q.ws + c.off_h;
         W = q.ws + c.off_w;
     }

@@ -62,6 +62,7 @@ struct HeadsArg {
     int heads;
     int chunks;          // warps (or CTAs, general kernels) that share one token's heads
     int steps;           // head groups of one token per chunk
+    int tokens;          // tokens that share a head group (above 1 where a token's heads leave room)
     int ctas;            // CTAs of this tensor
     float* partial;      // gradient: [ctas][head_dim] sums of dgamma
     float* dgamma;
@@ -288,26 +289,56 @@ __device__ __forceinline__ float sum_lanes(float v, int lanes, int sub) {
     return __shfl_sync(0xffffffffu, v, (int)(threadIdx.x & 31) - sub);
 }
 
-// A token's cosines and sines: each lane forms those of every 32nd pair, and the lanes share them
-// through the warp's table (rotary_dim floats).
+// An item's cosines and sines, one row of the warp's table (rotary_dim floats) for each of its
+// tokens: each lane forms those of every 32nd pair, and the lanes share them.  `pos` is the position
+// of the lane's own token; lane k * stride is one of token k.
 template <class Fmt>
-__device__ __forceinline__ void fill_table(const Args& a, long long pos, float* table, int lane) {
+__device__ __forceinline__ void fill_table(const Args& a, long long pos, float* table, int lane, int tokens = 1,
+                                           int stride = 0) {
     const int half = a.rot / 2;
-    __syncwarp();                 // the previous token's values have been read
-    for (int i = lane; i < half; i += 32) cos_sin<Fmt>(a, pos, __ldg(a.freqs + i), &table[i], &table[half + i]);
+    __syncwarp();                 // the previous item's values have been read
+    for (int k = 0; k < tokens; ++k, table += a.rot) {
+        const long long at = tokens > 1 ? __shfl_sync(0xffffffffu, pos, k * stride) : pos;
+        for (int i = lane; i < half; i += 32)
+            cos_sin<Fmt>(a, at, __ldg(a.freqs + i), &table[i], &table[half + i]);
+    }
     __syncwarp();
 }
 
-// An item: a token, or a share of its heads.
+// What a lane does in every item: which of a group's heads is its own.  Where a token has fewer heads
+// than a group (keys shared by many queries), a group takes several tokens' heads.
+struct Place {
+    int token, head;      // offsets in the item and in the group
+    bool own;             // false: the lane doubles another one and writes nothing
+    __device__ __forceinline__ void init(const HeadsArg& t, int grp, bool whole) {
+        token = 0;
+        head = grp;
+        own = whole;
+        if (t.tokens > 1) {
+            token = grp / t.heads;
+            head = grp - token * t.heads;
+            if (token >= t.tokens) token = head = 0, own = false;
+        }
+    }
+};
+
+// An item: a token, a share of its heads, or a few tokens; the lane's token of it.
 struct Item {
     unsigned token, b, s;
     int head, end;
-    __device__ __forceinline__ void open(const Args& a, const HeadsArg& t, unsigned item, int per_step) {
+    bool in;              // the token exists (the last item may have fewer than its tokens)
+    __device__ __forceinline__ void open(const Args& a, const HeadsArg& t, unsigned item, int per_step,
+                                         int token_offset = 0) {
         int chunk = 0;
         token = item;
+        in = true;
         if (t.chunks > 1) {
             token = item / (unsigned)t.chunks;
             chunk = (int)(item - token * t.chunks);
+        } else if (t.tokens > 1) {
+            token = item * t.tokens + token_offset;
+            in = token < a.tokens;
+            if (!in) token = a.tokens - 1;
         }
         split_token(a, token, &b, &s);
         head = chunk * t.steps * per_step;
@@ -318,6 +349,9 @@ struct Item {
         return base + b * st.b + s * st.s;
     }
 };
+__device__ __forceinline__ unsigned items_of(const Args& a, const HeadsArg& t) {
+    return t.tokens > 1 ? (a.tokens + t.tokens - 1) / t.tokens : a.tokens * t.chunks;
+}
 
 // ---------------------------------------------------------------- forward
 template <class Fmt, int E, int NU, int Mode, int Lanes>
@@ -329,15 +363,17 @@ __device__ __forceinline__ void heads_fwd(const Args& a, const HeadsArg& t, int 
     // lanes behind the last whole head double the last one's and write nothing
     const int grp = min(lane / lanes, per_step - 1), sub = lane % lanes;
     const bool whole = Lanes || lane < per_step * lanes;
-    table += warp * a.rot;
+    table += warp * t.tokens * a.rot;
+    Place place;
+    place.init(t, grp, whole);
     Units<E, NU> u;
     u.init(a, sub, lanes);
     pdl_wait();
     pdl_trigger();
     const unsigned item = cta * kWarps + warp;    // one for each warp
-    if (item >= a.tokens * t.chunks) return;
+    if (item >= items_of(a, t)) return;
     Item at;
-    at.open(a, t, item, per_step);
+    at.open(a, t, item, per_step, place.token);
     const long long pos = position(a, at.b, at.s);
     const T* x = at.row(static_cast<const T*>(t.x), t.sx);
     T* y = at.row(static_cast<T*>(t.y), t.sy);
@@ -348,9 +384,11 @@ __device__ __forceinline__ void heads_fwd(const Args& a, const HeadsArg& t, int 
         Head<Fmt, E, NU> in[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            in[k].load(x + min(h0 + k * per_step + grp, at.end - 1) * t.sx.h, u);
+            if (k == 0 || h0 + k * per_step < at.end)
+                in[k].load(x + min(h0 + k * per_step + place.head, at.end - 1) * t.sx.h, u);
         if (fresh) {                  // (while the first heads are on their way)
-            fill_table<Fmt>(a, pos, table, lane);
+            fill_table<Fmt>(a, pos, table, lane, t.tokens, t.heads * lanes);
+            const float* row = table + place.token * a.rot;
 #pragma unroll
             for (int j = 0; j < NU; ++j) {
                 float g[2 * E];
@@ -359,15 +397,15 @@ __device__ __forceinline__ void heads_fwd(const Args& a, const HeadsArg& t, int 
                     g[e] = Mode == kNorm ? __ldg(t.gamma + u.first[j] + e) : 1.f;
                     g[E + e] = Mode == kNorm ? __ldg(t.gamma + u.second[j] + e) : 1.f;
                 }
-                turn[j].set(table + u.freq[j], table + a.rot / 2 + u.freq[j], g, u.turns[j], a.interleaved);
+                turn[j].set(row + u.freq[j], row + a.rot / 2 + u.freq[j], g, u.turns[j], a.interleaved);
             }
             fresh = false;
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int h = h0 + k * per_step + grp;
-            if (k > 0 && h - grp >= at.end) break;
-            const bool mine = whole && h < at.end;
+            if (k > 0 && h0 + k * per_step >= at.end) break;
+            const int h = h0 + k * per_step + place.head;
+            const bool mine = place.own && at.in && h < at.end;
             F2 p[NU][H], q[NU][H];
 #pragma unroll
             for (int j = 0; j < NU; ++j) {
@@ -453,10 +491,13 @@ __device__ __forceinline__ void heads_bwd(const Args& a, const HeadsArg& t, int 
     const int lanes = Lanes ? Lanes : a.lanes, per_step = 32 / lanes;
     const int grp = min(lane / lanes, per_step - 1), sub = lane % lanes;
     const bool whole = Lanes || lane < per_step * lanes;
-    float* table = sums + kWarps * a.head_dim + warp * a.rot;
+    float* table = sums + kWarps * a.head_dim + warp * t.tokens * a.rot;
+    Place place;
+    place.init(t, grp, whole);
+    const float* turn_row = table + place.token * a.rot;
     using V = typename Raw<E * (int)sizeof(T)>::V;
     constexpr int kSlot = kSlotBytes<Fmt, E, NU>;
-    unsigned char* slots = reinterpret_cast<unsigned char*>(sums + (kWarps * (a.head_dim + a.rot) + 3) / 4 * 4) +
+    unsigned char* slots = reinterpret_cast<unsigned char*>(sums + (kWarps * (a.head_dim + t.tokens * a.rot) + 3) / 4 * 4) +
                            warp * 2 * kSlot;
     auto vec = [&](int slot, int v) { return reinterpret_cast<V*>(slots + slot * kSlot) + v * 32 + lane; };
     auto inv_at = [&](int slot) { return reinterpret_cast<float*>(slots + (slot + 1) * kSlot - 128) + lane; };
@@ -474,11 +515,11 @@ __device__ __forceinline__ void heads_bwd(const Args& a, const HeadsArg& t, int 
             g[j][H + e] = f2(__ldg(t.gamma + u.second[j] + 2 * e), __ldg(t.gamma + u.second[j] + 2 * e + 1));
             acc[j][e] = acc[j][H + e] = f2(0.f);
         }
-    const unsigned items = a.tokens * t.chunks, stride = t.ctas * kWarps;
+    const unsigned items = items_of(a, t), stride = t.ctas * kWarps;
     unsigned i = cta * kWarps + warp;
     if (i < items) {
         Item at, nxt;
-        at.open(a, t, i, per_step);
+        at.open(a, t, i, per_step, place.token);
         long long pos = position(a, at.b, at.s);
         const T *x = at.row(static_cast<const T*>(t.x), t.sx), *dy = at.row(static_cast<const T*>(t.dy), t.sdy);
         T* dx = at.row(static_cast<T*>(t.y), t.sy);
@@ -511,24 +552,24 @@ __device__ __forceinline__ void heads_bwd(const Args& a, const HeadsArg& t, int 
             or_ = __ldg(pinv + h);
         };
         if constexpr (kBwdAhead<Fmt>) {
-            fetch(x, dy, inv, min(at.head + grp, at.end - 1), 0);
+            fetch(x, dy, inv, min(at.head + place.head, at.end - 1), 0);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
         for (;;) {                        // items
-            fill_table<Fmt>(a, pos, table, lane);
+            fill_table<Fmt>(a, pos, table, lane, t.tokens, t.heads * lanes);
 #pragma unroll
             for (int j = 0; j < NU; ++j)
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    c[j][e] = u.turns[j] ? table[u.freq[j] + e] : 1.f;
-                    sn[j][e] = u.turns[j] ? table[a.rot / 2 + u.freq[j] + e] : 0.f;
+                    c[j][e] = u.turns[j] ? turn_row[u.freq[j] + e] : 1.f;
+                    sn[j][e] = u.turns[j] ? turn_row[a.rot / 2 + u.freq[j] + e] : 0.f;
                 }
             i += stride;
             const bool more = i < items;
             nxt = at;
             const T *x_n = x, *dy_n = dy;
             if (more) {
-                nxt.open(a, t, i, per_step);
+                nxt.open(a, t, i, per_step, place.token);
                 pos = position(a, nxt.b, nxt.s);
                 x_n = nxt.row(static_cast<const T*>(t.x), t.sx);
                 dy_n = nxt.row(static_cast<const T*>(t.dy), t.sdy);
@@ -537,12 +578,12 @@ __device__ __forceinline__ void heads_bwd(const Args& a, const HeadsArg& t, int 
             for (int h0 = at.head; h0 < at.end; h0 += per_step) {
                 // the next group's vectors, of the next item behind the last
                 const bool same = h0 + per_step < at.end;
-                const int h = h0 + grp;
-                const bool mine = whole && h < at.end;
+                const int h = h0 + place.head;
+                const bool mine = place.own && at.in && h < at.end;
                 if constexpr (kBwdAhead<Fmt>) {
                     if (same || more)
                         fetch(same ? x : x_n, same ? dy : dy_n, same ? inv : inv_n,
-                              same ? min(h + per_step, at.end - 1) : min(nxt.head + grp, nxt.end - 1), slot ^ 1);
+                              same ? min(h + per_step, at.end - 1) : min(nxt.head + place.head, nxt.end - 1), slot ^ 1);
                     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory");
 #pragma unroll
                     for (int j = 0; j < NU; ++j) {
@@ -656,9 +697,8 @@ __global__ void __launch_bounds__(kThreads, kBwdAhead<Fmt> ? 2 : 3) heads_bwd_ke
 }
 
 // ---------------------------------------------------------------- any sizes, strides and alignment
-// One CTA per token (or per chunk of a token's heads), one warp per head; the token's
-// sines are formed once, in shared memory.  A lane owns whole pairs, so that a call in
-// place reads both members before it writes them.
+// One element at a time, a head a warp after another of an item's.  A lane owns whole pairs, so that
+// a call in place reads both members before it writes them.
 struct Pair {
     int i, k;        // element offsets; k < 0: a single element behind rotary_dim
 };
@@ -672,14 +712,14 @@ __device__ __forceinline__ Pair pair_at(const Args& a, int p) {
 template <class Fmt, int Mode, bool Bwd>
 __global__ void __launch_bounds__(kThreads) heads_general_kernel(const __grid_constant__ Args a) {
     using T = typename Fmt::T;
-    extern __shared__ float sh[];     // cos [rot/2], sin [rot/2], gradient: sums [kWarps][head_dim]
-    float* cs = sh;
-    float* sn = sh + a.rot / 2;
+    extern __shared__ float sh[];     // tables [kWarps][rot], gradient: sums [kWarps][head_dim]
     const int which = (int)blockIdx.x >= a.t[0].ctas;
     const HeadsArg& t = a.t[which];
     const int cta = (int)blockIdx.x - (which ? a.t[0].ctas : 0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float* sums = sh + a.rot + warp * a.head_dim;
+    float* cs = sh + warp * a.rot;
+    float* sn = cs + a.rot / 2;
+    float* sums = sh + kWarps * a.rot + warp * a.head_dim;
     pdl_wait();
     pdl_trigger();
     if constexpr (Bwd) {
@@ -687,22 +727,16 @@ __global__ void __launch_bounds__(kThreads) heads_general_kernel(const __grid_co
         __syncwarp();
     }
     const int pairs = pair_count(a);
-    const unsigned items = a.tokens * t.chunks;
-    for (unsigned item = cta; item < items; item += t.ctas) {
-        const unsigned token = item / (unsigned)t.chunks;
-        const int chunk = (int)(item - token * t.chunks);
-        unsigned b, s;
-        split_token(a, token, &b, &s);
-        const long long pos = position(a, b, s);
-        __syncthreads();   // the previous token's sines have been read
-        for (int i = threadIdx.x; i < a.rot / 2; i += kThreads)
-            cos_sin<Fmt>(a, pos, __ldg(a.freqs + i), &cs[i], &sn[i]);
-        __syncthreads();
-        const T* xt = static_cast<const T*>(t.x) + b * t.sx.b + s * t.sx.s;
-        const T* dt = Bwd ? static_cast<const T*>(t.dy) + b * t.sdy.b + s * t.sdy.s : nullptr;
-        T* yt = static_cast<T*>(t.y) + b * t.sy.b + s * t.sy.s;
-        const int h_end = min(t.heads, (chunk + 1) * t.steps);
-        for (int h = chunk * t.steps + warp; h < h_end; h += kWarps) {
+    const unsigned items = items_of(a, t);
+    for (unsigned item = cta * kWarps + warp; item < items; item += t.ctas * kWarps) {
+        Item at;
+        at.open(a, t, item, 1);
+        const unsigned token = at.token;
+        fill_table<Fmt>(a, position(a, at.b, at.s), cs, lane);
+        const T* xt = at.row(static_cast<const T*>(t.x), t.sx);
+        const T* dt = at.row(static_cast<const T*>(t.dy), t.sdy);
+        T* yt = at.row(static_cast<T*>(t.y), t.sy);
+        for (int h = at.head; h < at.end; ++h) {
             const T* x = xt + h * t.sx.h;
             T* y = yt + h * t.sy.h;
             if constexpr (!Bwd) {
@@ -769,7 +803,7 @@ __global__ void __launch_bounds__(kThreads) heads_general_kernel(const __grid_co
         __syncthreads();
         for (int d = threadIdx.x; d < a.head_dim; d += kThreads) {
             float v = 0.f;
-            for (int w = 0; w < kWarps; ++w) v += sh[a.rot + w * a.head_dim + d];
+            for (int w = 0; w < kWarps; ++w) v += sh[kWarps * a.rot + w * a.head_dim + d];
             t.partial[(int64_t)cta * a.head_dim + d] = v;
         }
     }
@@ -935,22 +969,33 @@ tb_status launch_lanes(Args a, const Call& c, int sms, cudaStream_t st) {
         c.bwd_norm ? reinterpret_cast<const void*>(&heads_bwd_kernel<Fmt, E, NU, Lanes>)
         : c.norm   ? reinterpret_cast<const void*>(&heads_fwd_kernel<Fmt, E, NU, kNorm, Lanes>)
                    : reinterpret_cast<const void*>(&heads_fwd_kernel<Fmt, E, NU, kRope, Lanes>);
-    size_t smem = sizeof(float) * kWarps * a.rot;
+    int rows = 1;                     // of a warp's table of sines
+    for (int i = 0; i < c.n; ++i) rows = std::max(rows, per_step / a.t[i].heads);
+    size_t smem = sizeof(float) * kWarps * a.rot * rows;
     if (c.bwd_norm) smem = (smem + sizeof(float) * kWarps * a.head_dim + 15) / 16 * 16 + kWarps * 2 * kSlotBytes<Fmt, E, NU>;
     const int resident = resident_ctas_per_sm(kernel, kThreads, smem);
     if (resident == 0) return TB_ERR_CUDA;
     const int64_t grid_ctas = (int64_t)sms * std::min(resident, kBwdCtasPerSm);
-    int64_t all_steps = 0;
-    for (int i = 0; i < c.n; ++i) all_steps += ceil_div(a.t[i].heads, per_step);
+    // What a token of each tensor costs, in head groups: its groups, half of one for an item's
+    // addresses and 0.3 for every 32 pairs whose sines are formed.  The gradient's CTAs are dealt by
+    // it.  By the groups alone, the keys' CTAs were the last to end: 4 x 4,096 tokens, 32 query heads
+    // of 128, bf16, with 8 / 4 / 1 key heads took 98 / 113 / 149 us, so they take 84 / 77 / 73.
+    double cost[2] = {0, 0};
+    const double sines = 0.3 * (double)ceil_div(a.rot / 2, 32);
+    for (int i = 0; i < c.n; ++i) {
+        const int shared = std::max(1, per_step / a.t[i].heads);
+        cost[i] = ((double)ceil_div(a.t[i].heads, per_step) + 0.5) / shared + sines;
+    }
     for (int i = 0; i < c.n; ++i) {
         HeadsArg& t = a.t[i];
         const int64_t steps = ceil_div(t.heads, per_step);
+        t.tokens = std::max(1, per_step / t.heads);
         // the tensor's share of the grid, by its head groups
-        const int64_t share = std::max<int64_t>(1, grid_ctas * steps / all_steps);
+        const int64_t share = std::max<int64_t>(1, (int64_t)((double)grid_ctas * cost[i] / (cost[0] + cost[1])));
         t.chunks = (int)std::min(steps, ceil_div(share * kWarps, a.tokens));
         t.steps = (int)ceil_div(steps, t.chunks);
         t.chunks = (int)ceil_div(steps, t.steps);
-        const int64_t ctas = ceil_div((int64_t)a.tokens * t.chunks, kWarps);
+        const int64_t ctas = ceil_div(t.tokens > 1 ? ceil_div(a.tokens, t.tokens) : (int64_t)a.tokens * t.chunks, kWarps);
         t.ctas = (int)(c.bwd_norm ? std::min(share, ctas) : ctas);
     }
     if (c.n == 1) a.t[1].ctas = 0;
@@ -987,22 +1032,20 @@ tb_status launch_general(Args a, const Call& c, int sms, cudaStream_t st) {
         c.bwd_norm ? reinterpret_cast<const void*>(&heads_general_kernel<Fmt, kNorm, true>)
         : c.norm   ? reinterpret_cast<const void*>(&heads_general_kernel<Fmt, kNorm, false>)
                    : reinterpret_cast<const void*>(&heads_general_kernel<Fmt, kRope, false>);
-    const size_t smem = sizeof(float) * (a.rot + (c.bwd_norm ? (size_t)kWarps * a.head_dim : 0));
+    const size_t smem = sizeof(float) * kWarps * (a.rot + (c.bwd_norm ? a.head_dim : 0));
     const int per_sm = std::min(resident_ctas_per_sm(kernel, kThreads, smem), kBwdCtasPerSm);
     if (per_sm == 0) return TB_ERR_CUDA;
     int64_t all = 0;
     for (int i = 0; i < c.n; ++i) all += a.t[i].heads;
     for (int i = 0; i < c.n; ++i) {
         HeadsArg& t = a.t[i];
-        // chunks of whole rounds of the CTA's warps
-        const int64_t rounds = ceil_div(t.heads, kWarps);
-        t.chunks = (int)std::min(rounds, std::max<int64_t>(1, ceil_div(2 * sms, a.tokens)));
-        t.steps = (int)(ceil_div(rounds, t.chunks) * kWarps);
+        t.tokens = 1;
+        const int64_t share = std::max<int64_t>(1, (int64_t)sms * per_sm * t.heads / all);
+        t.chunks = (int)std::min<int64_t>(t.heads, ceil_div(share * kWarps, a.tokens));
+        t.steps = (int)ceil_div(t.heads, t.chunks);
         t.chunks = (int)ceil_div(t.heads, t.steps);
-        int64_t ctas = a.tokens * t.chunks;
-        if (c.bwd_norm)
-            ctas = std::min(ctas, std::max<int64_t>(1, (int64_t)sms * per_sm * t.heads / all));
-        t.ctas = (int)std::min<int64_t>(ctas, INT32_MAX / 4);
+        const int64_t ctas = ceil_div((int64_t)a.tokens * t.chunks, kWarps);
+        t.ctas = (int)(c.bwd_norm ? std::min(share, ctas) : ctas);
     }
     if (c.n == 1) a.t[1].ctas = 0;
     if (c.bwd_norm) a.t[1].partial = a.t[0].partial + (int64_t)a.t[0].ctas * a.head_dim;

@@ -37,12 +37,14 @@ def make(shape, dtype, layout, seed, shift=0):
 
 
 # (batch, seq, heads_q, heads_k, head_dim), rotary_dim: vector widths of 16, 8 and 4 bytes, two
-# units a lane, idle lanes, one head, heads that do not fill a warp, the general kernel
+# units a lane, idle lanes, one head, heads that do not fill a warp or share it with other tokens'
+# (up to 32 of them), the general kernel
 SIZES = [((2, 7, 4, 2, 128), 128), ((1, 1, 32, 8, 128), 128), ((3, 5, 5, 1, 64), 64),
          ((2, 9, 3, 3, 80), 40), ((2, 4, 6, 2, 96), 24), ((1, 33, 2, 1, 256), 64),
          ((2, 3, 2, 2, 192), 96), ((1, 6, 2, 1, 212), 106), ((1, 5, 3, 1, 33), 32),
          ((2, 3, 1, 1, 1024), 512), ((1, 4, 2, 1, 2), 2), ((1, 3, 2, 2, 1), 0), ((1, 2, 9, 9, 16), 8),
-         ((1, 300, 12, 4, 64), 32), ((5, 1, 7, 7, 128), 0), ((1, 3, 40, 3, 520), 130)]
+         ((1, 300, 12, 4, 64), 32), ((5, 1, 7, 7, 128), 0), ((1, 3, 40, 3, 520), 130),
+         ((3, 37, 2, 1, 64), 64), ((2, 41, 3, 2, 48), 32), ((2, 19, 4, 1, 16), 16), ((1, 53, 2, 1, 66), 16)]
 
 
 def _case(shape, rot, seed):
