@@ -241,11 +241,11 @@ constexpr float kLog2e = 1.44269504088896341f;
 // ---------------------------------------------------------------- arguments
 struct Weigh {
     const float* dloss;
-    const void* H;            // [rows][cols]
+    const void* H;            // [rows][ld], padded where it has to be
     void* scaled;             // [rows][ld]; NULL: dW is not wanted
     float *weight, *top;      // weight NULL: not in this launch
     int64_t rows;
-    int cols, ld;
+    int ld;
 };
 struct Product {
     int m_tiles, n_tiles, splits, k_stages;
@@ -348,19 +348,13 @@ __device__ __forceinline__ void weigh_rows(const Weigh& w, const int64_t* target
     for (int64_t r = part; r < w.rows; r += parts) {
         const float v = ahead, f = v / m;
         if (r + parts < w.rows) ahead = weight_of(r + parts);
-        if (w.cols == w.ld) {         // whole 16-byte vectors
 #pragma unroll 8
-            for (int c = lane * 8; c < w.cols; c += 256) {
-                float x[8];
-                unpack8<Fmt>(*reinterpret_cast<const uint4*>(H + r * w.cols + c), x);
+        for (int c = lane * 8; c < w.ld; c += 256) {
+            float x[8];
+            unpack8<Fmt>(*reinterpret_cast<const uint4*>(H + r * w.ld + c), x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = v == 0.f ? 0.f : x[e] * f;
-                *reinterpret_cast<uint4*>(scaled + r * w.ld + c) = pack8<Fmt>(x);
-            }
-        } else {
-            for (int c = lane; c < w.ld; c += 32)
-                scaled[r * w.ld + c] =
-                    Fmt::from_f32(c < w.cols && v != 0.f ? Fmt::to_f32(H[r * w.cols + c]) * f : 0.f);
+            for (int e = 0; e < 8; ++e) x[e] = v == 0.f ? 0.f : x[e] * f;
+            *reinterpret_cast<uint4*>(scaled + r * w.ld + c) = pack8<Fmt>(x);
         }
     }
 }
@@ -626,38 +620,49 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const uint32_t leader_empty = map_to(acc_empty, 0);
         const float top_weight = K == kDW ? *p.top : 1.f;
         Outbox<Fmt> box{outbox + (warp - kEpiWarp) * 2 * kOutBytes, &map_out, lane, 0};
+        // What a tile's row needs from memory is asked for while the tile before it is worked on: a
+        // load's latency at the start of every tile is as long as the work on one of few stages.
+        struct Tile {
+            int split, mt, nt, row0;
+            int64_t target;
+            float lse, weight;
+        };
+        auto look = [&](int t) {
+            Tile x{};
+            if (t >= tiles) return x;
+            tile_at(p, (unsigned)t, &x.split, &x.mt, &x.nt);
+            x.row0 = x.mt * kTile + (int)rank * kHalf + quad * 32;
+            if (x.row0 + lane < p.rows) {
+                if constexpr (K == kLse || K == kGrad) x.target = p.target[x.row0 + lane];
+                if constexpr (K == kGrad) x.lse = p.lse[x.row0 + lane];
+                if constexpr (K == kDH) x.weight = p.weight[x.row0 + lane];
+            }
+            return x;
+        };
         int n = 0;
+        Tile ahead = look(pair);
         for (int t = pair; t < tiles; t += pairs, ++n) {
-            int split, mt, nt;
-            tile_at(p, (unsigned)t, &split, &mt, &nt);
-            const int buf = n & 1;
-            const int row0 = mt * kTile + (int)rank * kHalf + quad * 32, row = row0 + lane;
+            const Tile tile = ahead;
+            const int buf = n & 1, split = tile.split, nt = tile.nt;
+            const int row0 = tile.row0, row = row0 + lane;
             const bool live = row < p.rows;
             const int n0 = nt * p.width, all = min(p.width, p.cols - n0);
             const int middle = (all + 63) / 64 * 32;
             const int c0 = half ? middle : 0, width = half ? all : min(all, middle);
             const uint32_t acc = tmem + buf * kTile + ((uint32_t)(quad * 32) << 16);
-
-            // what the row needs, on its way before the accumulator is done
-            int hit = -1;                             // the target's column in this tile
-            float lse2 = 0.f, weight = 0.f;
-            if constexpr (K == kDH) {
-                if (live) weight = p.weight[row];
-            }
-            if constexpr (K == kLse || K == kGrad) {
-                if (live) {
-                    const int64_t tg = p.target[row];
-                    const bool counts = tg != p.ignore && tg >= 0 && tg < p.vocab;
-                    const int64_t c = tg - (K == kGrad ? p.b_base : 0) - n0;
-                    if (counts && c >= c0 && c < width) hit = (int)c;
-                    if constexpr (K == kGrad) {
-                        lse2 = p.lse[row] * kLog2e - kGBits<Fmt>;
-                        weight = counts ? 1.f : 0.f;
-                    }
-                }
-            }
             if (!__all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, (n / 2) & 1, p.err))) break;
             tmem_fence_after();
+            ahead = look(t + pairs);
+            int hit = -1;                             // the target's column in this tile
+            const float weight = tile.weight;
+            float lse2 = 0.f;
+            bool counts = false;
+            if constexpr (K == kLse || K == kGrad) {
+                counts = live && tile.target != p.ignore && tile.target >= 0 && tile.target < p.vocab;
+                const int64_t c = tile.target - (K == kGrad ? p.b_base : 0) - n0;
+                if (counts && c >= c0 && c < width) hit = (int)c;
+                if constexpr (K == kGrad) lse2 = tile.lse * kLog2e - kGBits<Fmt>;
+            }
 
             float m = __int_as_float(0xff800000), s = 0.f;
             auto work = [&](const uint32_t (&r)[32], int c) {
@@ -706,7 +711,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = c + i == hit ? v[i] - kGScale<Fmt> : v[i];
                     }
-                    if (weight == 0.f) {              // a row that takes no part
+                    if (!counts) {                    // a row that takes no part
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.f;
                     }
@@ -751,18 +756,27 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     }
                 }
             };
-            // the next columns come while the present ones are worked on
+            // The next columns come while the present ones are worked on; behind the last ones the
+            // accumulator is free for the MMAs of the tile after the next.
             uint32_t one[32], two[32];
+            auto release = [&] {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(leader_empty + 8 * buf);
+            };
             __syncwarp();
             if (c0 < width) tmem_load32(acc + c0, one);
+            else release();
             for (int c = c0; c < width; c += 64) {
                 tmem_wait(one);
                 if (c + 32 < width) tmem_load32(acc + c + 32, two);
+                else release();
                 work(one, c);
                 __syncwarp();
                 if (c + 32 < width) {
                     tmem_wait(two);
                     if (c + 64 < width) tmem_load32(acc + c + 64, one);
+                    else release();
                     work(two, c + 32);
                     __syncwarp();
                 }
@@ -770,9 +784,6 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             if constexpr (K == kLse) {
                 if (live) p.part[((int64_t)nt * 2 + half) * p.rows + row] = make_float2(m, s);
             }
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(leader_empty + 8 * buf);
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
@@ -862,9 +873,8 @@ join_dh_kernel(const float* sums, int splits, int64_t n, int cols, const float* 
     else out[i] = r[0];
 }
 
-// Rows padded with zeros to a multiple of eight elements: TMA wants strides of 16 bytes.  A thread
-// writes one 16-byte vector; what it reads starts on any element, so it loads the words around it
-// (inside the matrix) and shifts.
+// Rows padded with zeros.  A thread writes one 16-byte vector; what it reads starts on any element,
+// so it loads the words around it (inside the matrix) and shifts.
 struct Pad {
     const void* in[2];        // H, W
     void* out[2];
@@ -899,7 +909,7 @@ __global__ void __launch_bounds__(256) pad_kernel(const __grid_constant__ Pad p)
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[k] = __funnelshift_r(x[k], x[k + 1], 16);
         }
-        const int keep = cols - (int)c;          // elements of this row in the vector
+        const int keep = cols - (int)c;          // elements of this row in the vector, if any
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (2 * k >= keep) x[k] = 0;
@@ -1023,8 +1033,10 @@ int pick_width(int64_t m_tiles, int64_t cols, int64_t pairs) {
 
 Cut cut_call(int64_t n, int64_t d, int64_t v, bool bwd, int sms) {
     Cut c{};
-    c.ld = round_up(d, 8);
-    c.pad = c.ld != d;
+    // TMA wants strides of 16 bytes; a copy that has to be made gets strides of 128, so that no
+    // box row lies across two lines
+    c.pad = d % 8 != 0;
+    c.ld = c.pad ? round_up(d, kStageK) : d;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t o = at;
@@ -1195,7 +1207,7 @@ tb_status run_grad(const Problem& q, const Cut& c) {
         p.weight = weight;
         p.top = top;
         if (i == 0)
-            p.weigh = Weigh{q.dloss, q.H, q.dW ? scaled : nullptr, weight, top, q.n, (int)q.d, (int)c.ld};
+            p.weigh = Weigh{q.dloss, H, q.dW ? scaled : nullptr, weight, top, q.n, (int)c.ld};
         if (!make_map(&out, g, q.n, cols, c.ldg, 32, bf, true)) return TB_ERR_CUDA;
         tb_status s = launch_product<Fmt, kGrad>(h_rows, w_rows, out, p, q.st);
         if (s != TB_OK) return s;
