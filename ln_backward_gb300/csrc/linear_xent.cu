@@ -320,41 +320,78 @@ __device__ __forceinline__ void stages_of(const Product& p, int split, int* lo, 
 // a warp's 16-byte pieces lie a row apart, 32 half sectors an instruction: the epilogue then took
 // longer than the MMAs of a tile with 768 contracted elements (78 us against 62 us, 1,021 x 50,257).
 // What the later products need of dloss: each row's weight (0 where it takes no part), the largest
-// magnitude among them, and H with every row times its weight over that.  Two otherwise idle warps
-// of each CTA do their share of it while the logits' product runs (a kernel of its own in front of
-// them took 8 us at 1,021 x 768); each finds the maximum by itself, rows * 12 bytes from L2.
+// magnitude among them, and H with every row times its weight over that.  It runs beside the logits'
+// product: the epilogue warps of every CTA find the maximum before their first tile (rows * 12 bytes
+// from L2), and two otherwise idle warps copy the CTA's share of the rows.  (A kernel of its own in
+// front of the products took 8 us at 1,021 x 768.)
 template <class Fmt>
-__device__ __forceinline__ void weigh_rows(const Weigh& w, const int64_t* target, int64_t ignore, int vocab,
-                                           int lane, int part, int parts) {
-    using T = typename Fmt::T;
-    auto weight_of = [&](int64_t r) {
-        const int64_t t = target[r];
-        return t != ignore && t >= 0 && t < vocab ? w.dloss[r] : 0.f;
-    };
+__device__ __forceinline__ float weight_of(const Product& p, int64_t r) {
+    const int64_t t = p.target[r];
+    const float v = p.weigh.dloss[r];
+    return t != p.ignore && t >= 0 && t < p.vocab ? v : 0.f;
+}
+constexpr int kWeighThreads = (kEpiWarps + 2) * 32;       // of named barrier 1
+
+// By the epilogue warps; thread 0 .. 255 of them.
+template <class Fmt>
+__device__ __forceinline__ void weigh_top(const Product& p, int thread, float* tops) {
     float m = 0.f;
+    unsigned owner = 0;               // of the next 256 rows' weights
+    const int64_t rows = p.weigh.rows;
 #pragma unroll 8
-    for (int64_t r = lane; r < w.rows; r += 32) {
-        const float v = weight_of(r);
-        if (r / 32 % parts == part) w.weight[r] = v;
+    for (int64_t r = thread; r < rows; r += 256) {
+        const float v = weight_of<Fmt>(p, r);
+        if (owner == blockIdx.x) p.weigh.weight[r] = v;
+        if (++owner == gridDim.x) owner = 0;
         if (fabsf(v) <= 3.4028235e38f) m = fmaxf(m, fabsf(v));   // neither infinite nor NaN
     }
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (thread % 32 == 0) tops[thread / 32] = m;
+    asm volatile("bar.arrive 1, %0;" ::"n"(kWeighThreads) : "memory");
+}
+
+// By the other two; part 0 .. parts - 1 of all CTAs' warps.
+template <class Fmt>
+__device__ __forceinline__ void weigh_rows(const Product& p, int lane, unsigned part, unsigned parts,
+                                           const float* tops) {
+    using T = typename Fmt::T;
+    asm volatile("bar.sync 1, %0;" ::"n"(kWeighThreads) : "memory");
+    float m = tops[0];
+    for (int i = 1; i < kEpiWarps; ++i) m = fmaxf(m, tops[i]);
     if (m == 0.f) m = 1.f;
-    if (part == 0 && lane == 0) *w.top = m;
-    if (!w.scaled) return;
-    const T* H = static_cast<const T*>(w.H);
-    T* scaled = static_cast<T*>(w.scaled);
-    float ahead = part < w.rows ? weight_of(part) : 0.f;
-    for (int64_t r = part; r < w.rows; r += parts) {
-        const float v = ahead, f = v / m;
-        if (r + parts < w.rows) ahead = weight_of(r + parts);
-#pragma unroll 8
-        for (int c = lane * 8; c < w.ld; c += 256) {
-            float x[8];
-            unpack8<Fmt>(*reinterpret_cast<const uint4*>(H + r * w.ld + c), x);
+    if (part == 0 && lane == 0) *p.weigh.top = m;
+    if (!p.weigh.scaled) return;
+    const uint4* H = static_cast<const uint4*>(p.weigh.H);
+    uint4* scaled = static_cast<uint4*>(p.weigh.scaled);
+    const int64_t rows = p.weigh.rows;
+    const unsigned per_row = (unsigned)p.weigh.ld / 8, first = part * 32 + lane, step = parts * 32;
+    int64_t row = first / per_row;
+    unsigned col = first % per_row;
+    while (row < rows) {              // four vectors at a time, a step apart
+        int64_t at[4];
+        uint4 x[4];
+        float w[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = v == 0.f ? 0.f : x[e] * f;
-            *reinterpret_cast<uint4*>(scaled + r * w.ld + c) = pack8<Fmt>(x);
+        for (int k = 0; k < 4; ++k) {
+            at[k] = -1;
+            if (row < rows) {
+                at[k] = row * per_row + col;
+                x[k] = H[at[k]];
+                w[k] = weight_of<Fmt>(p, row);
+            }
+            row += step / per_row;
+            col += step % per_row;
+            if (col >= per_row) col -= per_row, ++row;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (at[k] < 0) break;
+            const float f = w[k] / m;
+            float y[8];
+            unpack8<Fmt>(x[k], y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = w[k] == 0.f ? 0.f : y[e] * f;
+            scaled[at[k]] = pack8<Fmt>(y);
         }
     }
 }
@@ -531,6 +568,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     asm volatile("fence.proxy.async;" ::: "memory");   // what earlier kernels stored, TMA reads
     pdl_trigger();
 
+    __shared__ float tops[kEpiWarps];       // (kGrad: weigh_top)
     const int tiles = p.m_tiles * p.n_tiles * p.splits;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
@@ -611,13 +649,13 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             }
         }
     } else if (K == kGrad && (warp == 2 || warp == 3)) {
-        if (p.weigh.weight)
-            weigh_rows<Fmt>(p.weigh, p.target, p.ignore, p.vocab, lane, blockIdx.x * 2 + (warp & 1), gridDim.x * 2);
+        if (p.weigh.weight) weigh_rows<Fmt>(p, lane, blockIdx.x * 2 + (warp & 1), gridDim.x * 2, tops);
     } else if (warp >= kEpiWarp) {
         // TMEM lanes 32 quad .. 32 quad + 31 (a warp reaches those of its number modulo 4), and
         // the first or second half of the tile's columns
         const int quad = warp & 3, half = (warp - kEpiWarp) >> 2;
         const uint32_t leader_empty = map_to(acc_empty, 0);
+        if (K == kGrad && p.weigh.weight) weigh_top<Fmt>(p, threadIdx.x - kEpiWarp * 32, tops);
         const float top_weight = K == kDW ? *p.top : 1.f;
         Outbox<Fmt> box{outbox + (warp - kEpiWarp) * 2 * kOutBytes, &map_out, lane, 0};
         // What a tile's row needs from memory is asked for while the tile before it is worked on: a
