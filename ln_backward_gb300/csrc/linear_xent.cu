@@ -11,12 +11,24 @@
 // One kernel does the four products.  A pair of CTAs (one cluster of two SMs) owns a
 // 256 x 256 tile: tcgen05.mma.cta_group::2 with both operands in shared memory, 64 of the
 // contracted dimension a stage, 128-byte swizzled; each CTA stages its half of A and of B
-// (32 KB a stage, six stages), so a tile's operands cross from L2 once per pair.  Warp 0
-// feeds the stages by TMA, warp 1 of the pair's first CTA issues the MMAs, warps 4..11 drain
+// (32 KB a stage, a ring of six), so a tile's operands cross from L2 once per pair.  Warp 0
+// feeds the ring by TMA, warp 1 of the pair's first CTA issues the MMAs, warps 4..11 drain
 // the accumulator -- of which there are two, 256 TMEM columns each, so that the epilogue of
 // one tile runs under the MMAs of the next.  A thread of the epilogue owns one row of the
 // tile: row sums need no shuffles.  Tiles are dealt statically to a persistent grid of one
 // CTA per SM, in groups of kGroup row tiles that keep their rows of A in L2.
+//
+// What bounds it: the tensor cores.  A stage's MMAs take 237 ns with operands at hand, 277 ns
+// with them coming from L2 (2.1 GHz, one launch); under continuous load the power limit sets
+// the clock.  bf16 8,192 x 32,000 x 4,096: loss 1,130 us (1,900 TFLOP/s), gradient 3,590 to
+// 3,690 us (1,750 to 1,790 TFLOP/s; a cuBLAS product reaches 1,871 in a burst and 1,707 for
+// seconds).  Short contractions are bound by the epilogue and by the loads' latency: fp16
+// 1,021 x 50,257 x 768, gradient, 163 us (126 us at 1,871 TFLOP/s); bf16 37 rows against the
+// same weights, loss, 22 us, of which about 13 read W at 6 TB/s.
+//
+// The accumulators are fp32, but tensor cores cut off what an addition shifts below the sum's
+// last place, where fp32 arithmetic rounds: at D = 4,096 a logit comes out smaller by 4e-6 of
+// itself (fp32: 7e-7 either way), and the losses, of 7.7 in the mean square, are off by 1.4e-5.
 //
 // The operands need no transposed copies: dH contracts over the vocabulary, along which W
 // is not contiguous, and dW over the tokens, along which neither G nor H is; those operands
@@ -55,13 +67,16 @@ constexpr int kOutCols = 32;
 constexpr int kOutBytes = 32 * kOutCols * 2; // what an epilogue warp stores at once: 32 rows
 constexpr int kSmem = kStages * kStageBytes + 2 * kEpiWarps * kOutBytes + 1024 + 256;   // alignment, barriers
 constexpr int kTmemCols = 512;               // two accumulators
-constexpr int kGroup = 16;                   // row tiles walked together (see tile_at)
+// Row tiles walked together (see tile_at): bf16 8,192 x 32,000 x 4,096, loss and gradient, took 1,133
+// and 3,673 us with 16, 1,170 and 3,704 with 8, 1,180 and 3,943 with 32.
+constexpr int kGroup = 16;
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;
 
-// Bytes of G that one piece of the vocabulary may take, and the fewest columns of a piece.
+// Bytes of G that one piece of the vocabulary may take, and the fewest columns of a piece.  The same
+// gradient took 3,673 us with 256 MiB (two pieces), 3,996 with 128, 4,023 with 64, 3,631 with 1,024.
 constexpr int64_t kPieceBytes = 256ll << 20;
 constexpr int64_t kMinPiece = 2048;
-constexpr int64_t kLseRows = 16384;          // rows of one launch of the loss (workspace)
+constexpr int64_t kLseRows = 16384;          // rows of one launch of the loss: bounds its workspace
 
 // ---------------------------------------------------------------- PTX
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -529,6 +544,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                const __grid_constant__ CUtensorMap map_out, const __grid_constant__ Product p) {
     using T = typename Fmt::T;
     constexpr bool kAMn = K == kDW, kBMn = K == kDH || K == kDW;
+    __shared__ float tops[kEpiWarps];       // kGrad: see weigh_top
     extern __shared__ unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -568,36 +584,33 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     asm volatile("fence.proxy.async;" ::: "memory");   // what earlier kernels stored, TMA reads
     pdl_trigger();
 
-    __shared__ float tops[kEpiWarps];       // (kGrad: weigh_top)
     const int tiles = p.m_tiles * p.n_tiles * p.splits;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (warp == 0) {
-        {
-            const uint32_t leader_full = map_to(full, 0);
-            const uint32_t a_bytes = (kAMn || p.a_rows == kHalf ? 2 * kHalf : p.a_rows) * kStageK * 2;
-            const uint32_t stage_bytes = a_bytes + p.width * kStageK * 2;      // of both CTAs
-            int it = 0, failed = 0;
-            Feed<K> feed(p, &map_a, &map_b, (int)rank, pair, pairs, tiles);
-            for (; feed.more(); feed.next(), ++it) {
-                const int s = it % kStages;
-                if (it >= kStages && !__all_sync(0xffffffffu, mbar_wait(empty + 8 * s, (it / kStages - 1) & 1, p.err))) {
-                    failed = 1;
-                    break;
-                }
-                const uint32_t at = stage0 + s * kStageBytes, bar = leader_full + 8 * s;
-                if (elect_one()) {
-                    if (rank == 0) mbar_expect(full + 8 * s, stage_bytes);
-                    feed.boxes([&](int operand, int offset, const CUtensorMap* m, int x, int y) {
-                        tma_box(at + operand * kOperandBytes + offset, m, x, y, bar);
-                    });
-                }
-                if (feed.k + 1 == feed.k_hi) feed.look(feed.t + pairs);
+        const uint32_t leader_full = map_to(full, 0);
+        const uint32_t a_bytes = (kAMn || p.a_rows == kHalf ? 2 * kHalf : p.a_rows) * kStageK * 2;
+        const uint32_t stage_bytes = a_bytes + p.width * kStageK * 2;      // of both CTAs
+        int it = 0, failed = 0;
+        Feed<K> feed(p, &map_a, &map_b, (int)rank, pair, pairs, tiles);
+        for (; feed.more(); feed.next(), ++it) {
+            const int s = it % kStages;
+            if (it >= kStages && !__all_sync(0xffffffffu, mbar_wait(empty + 8 * s, (it / kStages - 1) & 1, p.err))) {
+                failed = 1;
+                break;
             }
-            if (failed && rank == 0)      // what both CTAs issued ends on these barriers
-                for (int q = max(0, it - kStages); q < it; ++q)
-                    mbar_wait(full + 8 * (q % kStages), (q / kStages) & 1, p.err);
+            const uint32_t at = stage0 + s * kStageBytes, bar = leader_full + 8 * s;
+            if (elect_one()) {
+                if (rank == 0) mbar_expect(full + 8 * s, stage_bytes);
+                feed.boxes([&](int operand, int offset, const CUtensorMap* m, int x, int y) {
+                    tma_box(at + operand * kOperandBytes + offset, m, x, y, bar);
+                });
+            }
+            if (feed.k + 1 == feed.k_hi) feed.look(feed.t + pairs);
         }
+        if (failed && rank == 0)      // what both CTAs issued ends on these barriers
+            for (int q = max(0, it - kStages); q < it; ++q)
+                mbar_wait(full + 8 * (q % kStages), (q / kStages) & 1, p.err);
     } else if (warp == 1) {
         if (rank == 0) {
             // The whole warp walks the stages and one lane issues: the operands of an MMA are uniform
