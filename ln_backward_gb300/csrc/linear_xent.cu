@@ -276,7 +276,7 @@ struct Product {
     int vocab;
     float2* part;             // kLse: [2 n_tiles][rows] maximum and sum of half a tile
     float* target_logit;      // kLse: [rows]
-    const float* lse;         // kGrad
+    const float *lse, *dloss; // kGrad
     const float* weight;      // kDH: dloss by row, 0 where a row takes no part
     const float* top;         // kDW: the largest |dloss|
     // kDH, kDW
@@ -685,7 +685,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             x.row0 = x.mt * kTile + (int)rank * kHalf + quad * 32;
             if (x.row0 + lane < p.rows) {
                 if constexpr (K == kLse || K == kGrad) x.target = p.target[x.row0 + lane];
-                if constexpr (K == kGrad) x.lse = p.lse[x.row0 + lane];
+                if constexpr (K == kGrad) x.lse = p.lse[x.row0 + lane], x.weight = p.dloss[x.row0 + lane];
                 if constexpr (K == kDH) x.weight = p.weight[x.row0 + lane];
             }
             return x;
@@ -712,7 +712,11 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 counts = live && tile.target != p.ignore && tile.target >= 0 && tile.target < p.vocab;
                 const int64_t c = tile.target - (K == kGrad ? p.b_base : 0) - n0;
                 if (counts && c >= c0 && c < width) hit = (int)c;
-                if constexpr (K == kGrad) lse2 = tile.lse * kLog2e - kGBits<Fmt>;
+                if constexpr (K == kGrad) {
+                    lse2 = tile.lse * kLog2e - kGBits<Fmt>;
+                    // a row that is weighted with 0 counts for nothing, not for 0 * NaN (dW)
+                    counts = counts && weight != 0.f;
+                }
             }
 
             float m = __int_as_float(0xff800000), s = 0.f;
@@ -1255,6 +1259,7 @@ tb_status run_grad(const Problem& q, const Cut& c) {
         p.ignore = q.ignore;
         p.vocab = (int)q.v;
         p.lse = q.lse_in;
+        p.dloss = q.dloss;
         p.weight = weight;
         p.top = top;
         if (i == 0)

@@ -198,6 +198,25 @@ def test_what_an_ignored_row_holds_does_not_matter(tb, dtype):
     assert torch.equal(dH2, dH) and torch.equal(dW2, dW)
 
 
+@pytest.mark.parametrize("n, d, v", [(300, 136, 900), (40000, 24, 5000)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_what_a_row_of_weight_zero_holds_does_not_matter(tb, n, d, v, dtype):
+    """Padding that has targets and a dloss of 0, in one piece of the vocabulary and in several."""
+    H, W, t, dloss = problem(n, d, v, dtype, 12, ignored=0.0)
+    pad = torch.arange(n, device="cuda") % 7 == 3
+    dloss[pad] = 0.0
+    dloss[3] = -0.0
+    _, lse = forward(tb, H, W, t)
+    dH, dW = backward(tb, dloss, H, W, t, lse)
+    assert not dH[pad].any() and dW.isfinite().all()
+    for value in (float("nan"), float("inf")):
+        H2 = H.clone()
+        H2[pad] = value
+        _, lse2 = forward(tb, H2, W, t)
+        dH2, dW2 = backward(tb, dloss, H2, W, t, lse2)
+        assert torch.equal(dH2, dH) and torch.equal(dW2, dW)
+
+
 def test_a_target_outside_the_vocabulary(tb):
     n, d, v = 40, 64, 200
     H, W, t, dloss = problem(n, d, v, BF, 5, ignored=0.0)
