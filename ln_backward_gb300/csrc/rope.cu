@@ -1305,6 +1305,10 @@ extern "C" tb_status tb_rope_freqs(int rotary_dim, double base, const tb_rope_sc
         low = fmax(floor(pair_of(s.fast)), 0.0);
         high = fmin(ceil(pair_of(s.slow)), (double)(rotary_dim - 1));
         if (low == high) high += 0.001;
+        // all pairs on one side of the blend: none makes as many turns as `slow` (all are
+        // divided), or none as few as `fast` (all keep their frequency)
+        if (low > high && high < 0) low = high - 1;
+        else if (low > high) high = low + 1;
     }
     for (int i = 0; i < half; ++i) {
         double w = pow(base, -2.0 * i / rotary_dim);

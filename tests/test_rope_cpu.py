@@ -67,6 +67,17 @@ def test_frequencies(tb, kind, kw, rot, base):
     assert mag == pytest.approx(0.1 * math.log(16) + 1 if kind == "yarn" else 1.0, rel=1e-6)
 
 
+@pytest.mark.parametrize("kind", ["yarn", "wavelength"])
+@pytest.mark.parametrize("ctx, divided", [(2.0, True), (3e8, False)])
+def test_blends_that_no_pair_lies_in(tb, kind, ctx, divided):
+    """Every pair makes fewer than `slow` turns over a context of 2, more than `fast` over 3e8."""
+    rot, base, factor = 16, 100.0, 4.0
+    table, _ = tb.tb_rope_freqs(rot, base, kind, factor=factor, original_context=ctx, device="cpu")
+    for i, got in enumerate(radians(table)):
+        w = base ** (-2.0 * i / rot) / (factor if divided else 1.0)
+        assert abs(got - w) <= 1e-13 * w + 2.0 ** -62
+
+
 def test_far_positions_keep_their_angle(tb):
     """pos * freq modulo 2^64 against whole-number arithmetic on the exact product."""
     table, _ = tb.tb_rope_freqs(64, device="cpu")
