@@ -940,6 +940,7 @@ tb_status check_angles(const tb_rope_angles* r, int64_t dim, int64_t batch, int6
     if (r->positions_stride < 0) return TB_ERR_INVALID_VALUE;
     if (batch > 0 && seq > 0 && r->positions_stride > 0 && r->positions_stride < seq && batch > 1)
         return TB_ERR_INVALID_VALUE;
+    if (batch > 1 && r->positions_stride > (1ll << 60) / batch) return TB_ERR_INVALID_VALUE;
     if (r->rotary_dim > 0 && !r->freqs) return TB_ERR_INVALID_VALUE;
     if (!aligned_to(r->freqs, 8) || !aligned_to(r->positions, 8)) return TB_ERR_MISALIGNED;
     return TB_OK;

@@ -196,6 +196,15 @@ def test_rope_refusals(tb, how, want):
         assert spoilt(tb, **how).norm() == want
 
 
+def test_positions_too_far_apart_are_refused(tb):
+    """Strides whose product with the batch leaves 64 bits, which a sum of them would wrap around."""
+    for stride in (1 << 60, (1 << 63) - 1):
+        assert spoilt(tb, ang__positions_stride=stride).rope() == INVALID
+        assert spoilt(tb, ang__positions_stride=stride, batch=3).norm() == INVALID
+    # without entries the stride is never used
+    assert spoilt(tb, ang__positions_stride=1 << 60, batch=1, seq=0).rope() == OK
+
+
 def test_slices_of_one_buffer_are_told_apart(tb):
     """Outputs among the heads of the buffer that holds the inputs: refused where an element is
     shared, although no row is the same.  (That disjoint slices pass is tested on the GPU,
