@@ -104,19 +104,33 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
+// Accumulators change hands between tcgen05 fences, which order the tcgen05 instructions: the
+// barrier itself need not order anything else.  (A release waited for the lane's stores before every
+// hand-over: fp16 gradient of 1,021 x 50,257 x 768 in 168 us, 158 without; loss of 4,096 x 50,257 x
+// 512, 137 and 108.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
                  : "memory");
 }
+template <bool Acquire>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if constexpr (Acquire)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
     return done != 0;
 }
 // One lane of a converged warp, the same one every time.
@@ -132,17 +146,19 @@ __device__ __forceinline__ unsigned long long now_ns() {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
+template <bool Acquire>
 __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, int* err) {
     const unsigned long long t0 = now_ns();
     for (uint32_t it = 1; it < (1u << 30); ++it) {
-        if (mbar_try(bar, parity)) return true;
+        if (mbar_try<Acquire>(bar, parity)) return true;
         if ((it & 63u) == 0 && now_ns() - t0 > kWaitLimitNs) break;
     }
     atomicExch(err, (int)TB_ERR_TIMEOUT);
     return false;
 }
+template <bool Acquire = true>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* err) {
-    return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, err);
+    return mbar_try<Acquire>(bar, parity) || mbar_wait_slow<Acquire>(bar, parity, err);
 }
 // A box of `map` at column x (a multiple of 64), row y into this CTA's shared memory,
 // counted on the mbarrier of the pair's first CTA.
@@ -280,8 +296,8 @@ struct Product {
     const float* weight;      // kDH: dloss by row, 0 where a row takes no part
     const float* top;         // kDW: the largest |dloss|
     // kDH, kDW
-    float* sums;              // kDH: [splits][rows][cols] fp32, NULL: one split, one piece
-    int first, last;          // piece: starts the sums; writes the result
+    float* sums;              // [splits][rows][cols] fp32, NULL: the tile is the result
+    int first, last;          // piece: starts the sums; writes the result (dW's is always both)
     int sums_map;             // rows of the sums are whole 16 bytes: they go out by TMA
     void* out;                // [rows][cols] 16-bit
     Weigh weigh;              // kGrad
@@ -329,11 +345,6 @@ __device__ __forceinline__ void stages_of(const Product& p, int split, int* lo, 
     }
 }
 
-// An epilogue warp's way out for 16-bit results: 32 columns of its 32 rows into a 64-byte swizzled
-// box in shared memory (a lane's 16-byte pieces at piece ^ (row / 2 & 3): no two lanes of a quarter
-// warp share banks), and a TMA store of the box, of which each warp has two.  Stored from registers,
-// a warp's 16-byte pieces lie a row apart, 32 half sectors an instruction: the epilogue then took
-// longer than the MMAs of a tile with 768 contracted elements (78 us against 62 us, 1,021 x 50,257).
 // What the later products need of dloss: each row's weight (0 where it takes no part), the largest
 // magnitude among them, and H with every row times its weight over that.  It runs beside the logits'
 // product: the epilogue warps of every CTA find the maximum before their first tile (rows * 12 bytes
@@ -459,6 +470,11 @@ struct Feed {
     }
 };
 
+// An epilogue warp's way out for 16-bit results: 32 columns of its 32 rows into a 64-byte swizzled
+// box in shared memory (a lane's 16-byte pieces at piece ^ (row / 2 & 3): no two lanes of a quarter
+// warp share banks), and a TMA store of the box, of which each warp has two.  Stored from registers,
+// a warp's 16-byte pieces lie a row apart, 32 half sectors an instruction: the epilogue then took
+// longer than the MMAs of a tile with 768 contracted elements (78 us against 62 us, 1,021 x 50,257).
 template <class Fmt>
 struct Outbox {
     unsigned char* mem;       // this warp's two boxes
@@ -631,7 +647,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 int k_lo, k_hi;
                 stages_of(p, p.splits > 1 ? t / (p.m_tiles * p.n_tiles) : 0, &k_lo, &k_hi);
                 const int buf = n & 1;
-                if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(acc_empty + 8 * buf, (n / 2 - 1) & 1, p.err))) {
+                if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait<false>(acc_empty + 8 * buf, (n / 2 - 1) & 1, p.err))) {
                     ok = false;
                     break;
                 }
@@ -701,7 +717,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             const int middle = (all + 63) / 64 * 32;
             const int c0 = half ? middle : 0, width = half ? all : min(all, middle);
             const uint32_t acc = tmem + buf * kTile + ((uint32_t)(quad * 32) << 16);
-            if (!__all_sync(0xffffffffu, mbar_wait(acc_full + 8 * buf, (n / 2) & 1, p.err))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait<false>(acc_full + 8 * buf, (n / 2) & 1, p.err))) break;
             tmem_fence_after();
             ahead = look(t + pairs);
             int hit = -1;                             // the target's column in this tile
@@ -774,33 +790,28 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 } else {
                     T* out = static_cast<T*>(p.out);
                     const int col = n0 + c;
-                    bool finish = true;
-                    if constexpr (K == kDH) {
-                        const bool keep = !p.last || p.splits > 1;
-                        if (p.sums && keep && p.sums_map) {
-                            if (row0 < p.rows)
-                                put_sums(box.mem, &map_out, lane, v, col, row0, split, !p.first);
-                        } else if (p.sums && live) {
-                            float* sum = p.sums + ((int64_t)split * p.rows + row) * p.cols + col;
-                            if (p.sums_map && c + 32 <= width) {
+                    const bool keep = !p.last || p.splits > 1;
+                    if (p.sums && keep && p.sums_map) {
+                        if (row0 < p.rows) put_sums(box.mem, &map_out, lane, v, col, row0, split, !p.first);
+                    } else if (p.sums && live) {
+                        float* sum = p.sums + ((int64_t)split * p.rows + row) * p.cols + col;
+                        if (p.sums_map && c + 32 <= width) {
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const float4 o = *reinterpret_cast<const float4*>(sum + 4 * i);
-                                    v[4 * i] += o.x, v[4 * i + 1] += o.y, v[4 * i + 2] += o.z, v[4 * i + 3] += o.w;
-                                }
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (c + i < width) {
-                                        if (!p.first) v[i] += sum[i];
-                                        if (keep) sum[i] = v[i];
-                                    }
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 o = *reinterpret_cast<const float4*>(sum + 4 * i);
+                                v[4 * i] += o.x, v[4 * i + 1] += o.y, v[4 * i + 2] += o.z, v[4 * i + 3] += o.w;
                             }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c + i < width) {
+                                    if (!p.first) v[i] += sum[i];
+                                    if (keep) sum[i] = v[i];
+                                }
                         }
-                        __syncwarp();
-                        finish = p.last && p.splits == 1;
                     }
-                    if (finish) {
+                    __syncwarp();
+                    if (!keep) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             v[i] = K == kDH ? weigh<Fmt>(v[i], weight) : v[i] * (1.f / kGScale<Fmt>) * top_weight;
@@ -899,16 +910,17 @@ join_kernel(const float2* part, const float* target_logit, const int64_t* target
     }
 }
 
-// Sums the splits of dH and rounds once: V elements a thread, of one row.
+// Sums the splits of dH or dW and rounds once: V elements a thread, of one row.  `weight`: by row
+// (dH), or one for all (dW: the largest |dloss|, never 0).
 template <class Fmt, int V>
 __global__ void __launch_bounds__(256)
-join_dh_kernel(const float* sums, int splits, int64_t n, int cols, const float* weight,
-               typename Fmt::T* out) {
+join_splits_kernel(const float* sums, int splits, int64_t n, int cols, const float* weight, bool by_row,
+                   typename Fmt::T* out) {
     pdl_wait();
     pdl_trigger();
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
     if (i >= n) return;
-    const float w = weight[i / cols];
+    const float w = by_row ? weight[i / cols] : *weight;
     float v[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] = 0.f;
@@ -1015,7 +1027,7 @@ bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// dH's fp32 sums [splits][rows][cols], written in boxes of 32 x 32.
+// The fp32 sums [splits][rows][cols] of dH or dW, written in boxes of 32 x 32.
 bool make_sums_map(CUtensorMap* map, float* p, int64_t splits, int64_t rows, int64_t cols) {
     const EncodeFn fn = encode_fn();
     if (!fn) return false;
@@ -1051,13 +1063,13 @@ struct Cut {
     bool pad;
     int64_t piece, pieces;    // gradient: columns of a piece of the vocabulary
     int64_t ldg;
-    int splits;               // of dH's contraction
+    int splits, splits_w;     // of dH's contraction, of dW's
     // byte offsets into the workspace
-    size_t off_h, off_w, off_scaled, off_weight, off_g, off_sums, off_top, off_part, off_logit, total;
+    size_t off_h, off_w, off_scaled, off_weight, off_g, off_sums, off_sums_w, off_top, off_part, off_logit, total;
 };
 
-// Parts of the vocabulary that dH's products are split into: as many as fill the machine when its
-// tiles do not.  The cost counts in stages (64 contracted elements of a tile, about 0.3 us): waves of
+// Parts of the vocabulary (of the rows) that dH's (dW's) products are split into: as many as fill the
+// machine when its tiles do not.  The result has n x d elements.  The cost counts in stages (64 contracted elements of a tile, about 0.3 us): waves of
 // tiles, about eight more for each one's epilogue, and for the sums that the splits leave a launch and
 // their bytes.  (fp16 1,021 x 768 against 50,257: six splits, 160 us; none, 314 us.)
 int pick_splits(int64_t n, int64_t d, int64_t k_stages, int64_t pairs) {
@@ -1117,8 +1129,10 @@ Cut cut_call(int64_t n, int64_t d, int64_t v, bool bwd, int sms) {
         c.ldg = c.piece;
         c.grad_width = pick_width(ceil_div(n, kTile), std::min(c.piece, v), sms / 2);
         c.splits = pick_splits(n, d, c.piece / kStageK, sms / 2);
+        c.splits_w = pick_splits(std::min(c.piece, v), d, ceil_div(n, kStageK), sms / 2);
         c.off_g = take((size_t)n * c.ldg * 2);
         if (c.pieces > 1 || c.splits > 1) c.off_sums = take((size_t)c.splits * n * d * sizeof(float));
+        if (c.splits_w > 1) c.off_sums_w = take((size_t)c.splits_w * std::min(c.piece, v) * d * sizeof(float));
         c.off_scaled = take((size_t)n * c.ld * 2);
         c.off_weight = take((size_t)n * sizeof(float));
         c.off_top = take(sizeof(float));
@@ -1224,6 +1238,16 @@ tb_status run_loss(const Problem& q, const Cut& c) {
 }
 
 template <class Fmt>
+bool join_splits(const float* sums, int splits, int64_t n, int64_t cols, const float* weight, bool by_row, void* out,
+                 cudaStream_t st) {
+    using T = typename Fmt::T;
+    const bool vec = cols % 4 == 0 && aligned_to(out, 8);
+    const dim3 grid((unsigned)ceil_div(n, vec ? 1024 : 256));
+    return launch_pdl(vec ? join_splits_kernel<Fmt, 4> : join_splits_kernel<Fmt, 1>, grid, dim3(256), 0, st, sums, splits,
+                      n, (int)cols, weight, by_row, static_cast<T*>(out)) == cudaSuccess;
+}
+
+template <class Fmt>
 tb_status run_grad(const Problem& q, const Cut& c) {
     constexpr bool bf = std::is_same<Fmt, BF16>::value;
     const void *H = q.H, *W = q.W;
@@ -1302,24 +1326,27 @@ tb_status run_grad(const Problem& q, const Cut& c) {
             r.cols = (int)q.d;
             r.width = kTile;
             r.out = static_cast<char*>(q.dW) + v0 * q.d * 2;
+            r.splits = c.splits_w;
+            r.first = r.last = 1;
+            r.sums = c.splits_w > 1 ? reinterpret_cast<float*>(q.ws + c.off_sums_w) : nullptr;
+            r.sums_map = r.sums && q.d % 4 == 0;
             r.out_map = q.d % 8 == 0 && aligned_to(q.dW, 16);
-            if (r.out_map && !make_map(&out, r.out, cols, q.d, q.d, 32, bf, true)) return TB_ERR_CUDA;
+            if (r.sums_map) {
+                if (!make_sums_map(&out, r.sums, r.splits, cols, q.d)) return TB_ERR_CUDA;
+            } else if (r.out_map && !make_map(&out, r.out, cols, q.d, q.d, 32, bf, true)) {
+                return TB_ERR_CUDA;
+            }
             s = launch_product<Fmt, kDW>(g_cols, h_cols, out, r, q.st);
             if (s != TB_OK) return s;
+            if (r.sums && !join_splits<Fmt>(r.sums, r.splits, cols * q.d, q.d, top, false, r.out, q.st))
+                return TB_ERR_CUDA;
         }
     }
     if (q.dH && c.splits > 1) {
-        const int64_t n = q.n * q.d;
         const int used = (int)std::min<int64_t>(c.splits, ceil_div(std::min(c.piece, q.v), kStageK));
-        const float* sums = reinterpret_cast<const float*>(q.ws + c.off_sums);
-        const bool vec = q.d % 4 == 0 && aligned_to(q.dH, 8);
-        const dim3 grid((unsigned)ceil_div(n, vec ? 1024 : 256));
-        const cudaError_t e =
-            vec ? launch_pdl(join_dh_kernel<Fmt, 4>, grid, dim3(256), 0, q.st, sums, used, n, (int)q.d,
-                             (const float*)weight, static_cast<T*>(q.dH))
-                : launch_pdl(join_dh_kernel<Fmt, 1>, grid, dim3(256), 0, q.st, sums, used, n, (int)q.d,
-                             (const float*)weight, static_cast<T*>(q.dH));
-        if (e != cudaSuccess) return TB_ERR_CUDA;
+        if (!join_splits<Fmt>(reinterpret_cast<const float*>(q.ws + c.off_sums), used, q.n * q.d, q.d, weight, true,
+                              q.dH, q.st))
+            return TB_ERR_CUDA;
     }
     return launch_status();
 }
