@@ -18,9 +18,8 @@
 // token's heads.
 //
 // Layout.  A head is dealt to L lanes, each holding NU "units" of two vectors of E
-// elements: the two halves' corresponding vectors in the half layout, two neighbouring
-// vectors in the interleaved one and behind rotary_dim.  Both members of every pair are
-// then in one lane: no shuffles but the norm's row sums.  32 / L heads go through a warp
+// elements, corresponding ones of the two halves of the rotated part or of the rest.  Both
+// members of every pair are then in one lane in either layout: no shuffles but the norm's row sums.  32 / L heads go through a warp
 // at a time; L is the number of units, not a power of two above it, so that heads of 80
 // or 96 elements leave few lanes idle.  Queries and keys get CTAs of their own, so gamma
 // and the dgamma sums of one tensor stay in registers.  Heads whose sizes, strides or
@@ -185,7 +184,7 @@ __device__ __forceinline__ long long position(const Args& a, unsigned b, unsigne
 template <int E, int NU>
 struct Units {
     int first[NU], second[NU];   // element offsets of a unit's two vectors
-    int freq[NU];                // its first frequency
+    int freq[NU], freq2[NU];     // the frequencies of its first and second E / 2 pairs
     bool live[NU], turns[NU];
     __device__ __forceinline__ void init(const Args& a, int sub, int lanes) {
         const int units = a.head_dim / (2 * E), rot_units = a.rot / (2 * E);
@@ -194,10 +193,12 @@ struct Units {
             const int c = sub + j * lanes;
             live[j] = c < units;
             turns[j] = c < rot_units;
-            const bool half = turns[j] && !a.interleaved;
-            first[j] = half ? c * E : 2 * c * E;
-            second[j] = half ? a.rot / 2 + c * E : 2 * c * E + E;
-            freq[j] = turns[j] ? c * E : 0;
+            // the second vector lies half of the rotated part (of the rest) behind the first in
+            // either layout: neighbouring lanes read neighbouring vectors
+            first[j] = turns[j] ? c * E : a.rot + (c - rot_units) * E;
+            second[j] = first[j] + (turns[j] ? a.rot / 2 : (a.head_dim - a.rot) / 2);
+            freq[j] = turns[j] ? (a.interleaved ? first[j] / 2 : first[j]) : 0;
+            freq2[j] = turns[j] ? (a.interleaved ? second[j] / 2 : first[j] + E / 2) : 0;
             if (!live[j]) first[j] = second[j] = 0;
         }
     }
@@ -226,27 +227,30 @@ struct Head {                     // one lane's vectors of a head; dead units re
 template <int E>
 struct Turn {
     F2 a[E], b[E];                // p's E / 2 pairs of elements, then q's
-    __device__ __forceinline__ void set(const float* c, const float* s, const float (&g)[2 * E], bool turns,
-                                        bool interleaved) {
+    // cos_p, cos_q: the cosines of the first and second E / 2 pairs; sines lie `sines` behind them
+    __device__ __forceinline__ void set(const float* cos_p, const float* cos_q, int sines, const float (&g)[2 * E],
+                                        bool turns, bool interleaved) {
         constexpr int H = E / 2;
+        auto c = [&](int e) { return e < H ? cos_p[e] : cos_q[e - H]; };
+        auto s = [&](int e) { return e < H ? cos_p[sines + e] : cos_q[sines + e - H]; };
 #pragma unroll
         for (int e = 0; e < E; ++e) a[e] = f2(g[2 * e], g[2 * e + 1]), b[e] = f2(0.f);
         if (!turns) return;
         if (interleaved) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                a[e] = f2(c[e]) * f2(g[2 * e], g[2 * e + 1]);
-                b[e] = f2(-s[e], s[e]) * f2(g[2 * e + 1], g[2 * e]);
+                a[e] = f2(c(e)) * f2(g[2 * e], g[2 * e + 1]);
+                b[e] = f2(-s(e), s(e)) * f2(g[2 * e + 1], g[2 * e]);
             }
         } else {
 #pragma unroll
             for (int e = 0; e < H; ++e) {
                 const F2 gp = f2(g[2 * e], g[2 * e + 1]), gq = f2(g[E + 2 * e], g[E + 2 * e + 1]);
-                const F2 cc = f2(c[2 * e], c[2 * e + 1]);
+                const F2 cc = f2(c(2 * e), c(2 * e + 1));
                 a[e] = gp * cc;
-                b[e] = gq * f2(-s[2 * e], -s[2 * e + 1]);
+                b[e] = gq * f2(-s(2 * e), -s(2 * e + 1));
                 a[H + e] = gq * cc;
-                b[H + e] = gp * f2(s[2 * e], s[2 * e + 1]);
+                b[H + e] = gp * f2(s(2 * e), s(2 * e + 1));
             }
         }
     }
@@ -397,7 +401,7 @@ __device__ __forceinline__ void heads_fwd(const Args& a, const HeadsArg& t, int 
                     g[e] = Mode == kNorm ? __ldg(t.gamma + u.first[j] + e) : 1.f;
                     g[E + e] = Mode == kNorm ? __ldg(t.gamma + u.second[j] + e) : 1.f;
                 }
-                turn[j].set(row + u.freq[j], row + a.rot / 2 + u.freq[j], g, u.turns[j], a.interleaved);
+                turn[j].set(row + u.freq[j], row + u.freq2[j], a.rot / 2, g, u.turns[j], a.interleaved);
             }
             fresh = false;
         }
@@ -561,8 +565,9 @@ __device__ __forceinline__ void heads_bwd(const Args& a, const HeadsArg& t, int 
             for (int j = 0; j < NU; ++j)
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    c[j][e] = u.turns[j] ? turn_row[u.freq[j] + e] : 1.f;
-                    sn[j][e] = u.turns[j] ? turn_row[a.rot / 2 + u.freq[j] + e] : 0.f;
+                    const float* at = turn_row + (e < H ? u.freq[j] + e : u.freq2[j] + e - H);
+                    c[j][e] = u.turns[j] ? at[0] : 1.f;
+                    sn[j][e] = u.turns[j] ? at[a.rot / 2] : 0.f;
                 }
             i += stride;
             const bool more = i < items;
