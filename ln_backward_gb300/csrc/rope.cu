@@ -276,21 +276,27 @@ struct Turn {
     }
 };
 
-// Sum over a head's lanes, in all of them.  Lanes: their number where it is known when compiling
-// (a power of two), else 0.
+// Whether heads of this many lanes fill a warp (a power of two, known when compiling).
+template <int Lanes>
+constexpr bool kWhole = Lanes > 0 && (Lanes & (Lanes - 1)) == 0;
+
+// Sum over a head's lanes, in all of them.  Lanes: their number where it is known when compiling,
+// else 0.
 template <int Lanes>
 __device__ __forceinline__ float sum_lanes(float v, int lanes, int sub) {
-    if constexpr (Lanes > 0) {
+    if constexpr (kWhole<Lanes>) {
 #pragma unroll
         for (int o = 1; o < Lanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
-    }
+    } else {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const float w = __shfl_down_sync(0xffffffffu, v, o);
-        v = sub + o < min(lanes, 2 * o) ? v + w : v;
+        for (int o = 16; o; o >>= 1) {
+            if (Lanes && o >= Lanes) continue;
+            const float w = __shfl_down_sync(0xffffffffu, v, o);
+            v = sub + o < min(lanes, 2 * o) ? v + w : v;
+        }
+        return __shfl_sync(0xffffffffu, v, (int)(threadIdx.x & 31) - sub);
     }
-    return __shfl_sync(0xffffffffu, v, (int)(threadIdx.x & 31) - sub);
 }
 
 // An item's cosines and sines, one row of the warp's table (rotary_dim floats) for each of its
@@ -366,7 +372,7 @@ __device__ __forceinline__ void heads_fwd(const Args& a, const HeadsArg& t, int 
     const int lanes = Lanes ? Lanes : a.lanes, per_step = 32 / lanes;
     // lanes behind the last whole head double the last one's and write nothing
     const int grp = min(lane / lanes, per_step - 1), sub = lane % lanes;
-    const bool whole = Lanes || lane < per_step * lanes;
+    const bool whole = kWhole<Lanes> || lane < per_step * lanes;
     table += warp * t.tokens * a.rot;
     Place place;
     place.init(t, grp, whole);
@@ -494,7 +500,7 @@ __device__ __forceinline__ void heads_bwd(const Args& a, const HeadsArg& t, int 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int lanes = Lanes ? Lanes : a.lanes, per_step = 32 / lanes;
     const int grp = min(lane / lanes, per_step - 1), sub = lane % lanes;
-    const bool whole = Lanes || lane < per_step * lanes;
+    const bool whole = kWhole<Lanes> || lane < per_step * lanes;
     float* table = sums + kWarps * a.head_dim + warp * t.tokens * a.rot;
     Place place;
     place.init(t, grp, whole);
@@ -1019,11 +1025,16 @@ tb_status launch_lanes(Args a, const Call& c, int sms, cudaStream_t st) {
     return launch_status();
 }
 
-// Heads of 64, 128 and 256 elements in 16-byte vectors know their number of lanes when compiled.
+// Heads of 64, 128 and 256 elements in 16-byte vectors know their number of lanes when compiled, and
+// so do those of 80, 96 and 192.
 template <class Fmt, int E, int NU>
 tb_status launch_vec(Args a, const Call& c, int sms, cudaStream_t st) {
     a.lanes = (int)ceil_div(a.head_dim / (2 * E), NU);
     if constexpr (E * sizeof(typename Fmt::T) == 16) {
+        constexpr int k80 = sizeof(typename Fmt::T) == 2 ? 5 : 10, k96 = sizeof(typename Fmt::T) == 2 ? 6 : 24;
+        if (a.lanes == k80) return launch_lanes<Fmt, E, NU, k80>(a, c, sms, st);
+        if (a.lanes == k96) return launch_lanes<Fmt, E, NU, k96>(a, c, sms, st);
+        if (a.lanes == 12) return launch_lanes<Fmt, E, NU, 12>(a, c, sms, st);
         if (a.lanes == 4) return launch_lanes<Fmt, E, NU, 4>(a, c, sms, st);
         if (a.lanes == 8) return launch_lanes<Fmt, E, NU, 8>(a, c, sms, st);
         if (a.lanes == 16) return launch_lanes<Fmt, E, NU, 16>(a, c, sms, st);
