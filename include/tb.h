@@ -17,14 +17,16 @@
  *
  * Conventions for every entry point
  *   - Buffers are device-accessible memory owned by the caller, row-major and
- *     contiguous (queries and keys are strided: see tb_heads).  The library keeps no pointer after a call returns, except the
- *     AdamW plan's copy of the tensor table (see tb_adamw_plan_create).
+ *     contiguous (queries and keys are strided: see tb_heads).  The library
+ *     keeps no pointer after a call returns, except the AdamW plan's copy of
+ *     the tensor table (see tb_adamw_plan_create).
  *   - `stream` is a cudaStream_t passed as void*; NULL is the legacy default
  *     stream.  Work is enqueued on it and the call returns without waiting: a
  *     fault inside a kernel surfaces at the caller's next synchronisation.
  *   - Argument errors are reported synchronously, before anything is enqueued,
  *     as a tb_status.  A failed launch reports TB_ERR_CUDA.
- *   - The softmax, LayerNorm and RMSNorm kernels are launched as programmatic
+ *   - The softmax, LayerNorm, RMSNorm, rotary and output-layer kernels are
+ *     launched as programmatic
  *     dependents of the work before them on `stream`: their blocks may start
  *     while the previous kernel drains, set up shared memory and (LayerNorm,
  *     RMSNorm) prefetch their first rows into L2, but they load and store no
@@ -531,8 +533,8 @@ tb_status tb_rope_freqs(int rotary_dim, double base, const tb_rope_scaling* scal
  *                   share no element with any input or output.  Views that walk one
  *                   buffer with the same strides are told apart exactly; views with
  *                   different strides count as sharing when their address ranges meet.
- *   batch, seq      >= 0, batch * seq < 2^31; nothing is enqueued when either is 0.  Elements of a buffer
- *                   outside the views are not touched.
+ *   batch, seq      >= 0, batch * seq < 2^31; nothing is enqueued when either is 0.
+ *                   Elements of a buffer outside the views are not touched.
  *   head_dim        1 .. 1024
  *   dtype           TB_F32, TB_BF16 or TB_F16, of all four
  * Sizes, strides and pointers that are multiples of 16 bytes (8, or two elements) take

@@ -19,14 +19,15 @@
 //
 // Layout.  A head is dealt to L lanes, each holding NU "units" of two vectors of E
 // elements, corresponding ones of the two halves of the rotated part or of the rest.  Both
-// members of every pair are then in one lane in either layout: no shuffles but the norm's row sums.  32 / L heads go through a warp
-// at a time; L is the number of units, not a power of two above it, so that heads of 80
-// or 96 elements leave few lanes idle.  Queries and keys get CTAs of their own, so gamma
-// and the dgamma sums of one tensor stay in registers.  Heads whose sizes, strides or
-// pointers no vector width fits take the general kernels (one element at a time).
+// members of every pair are then in one lane in either layout: no shuffles but the norm's
+// row sums.  32 / L heads go through a warp at a time; L is the number of units, not a power
+// of two above it, so that heads of 80 or 96 elements leave few lanes idle.  Queries and keys
+// get CTAs of their own, so gamma and the dgamma sums of one tensor stay in registers.  Heads
+// whose sizes, strides or pointers no vector width fits take the general kernels (one element
+// at a time).
 //
 // Measured at bf16 2 x 8,192 tokens of 32 + 8 heads of 128, norm and rotation (50 us at the
-// copy bandwidth): 57.6 us.  What did not pay there: loads a group ahead in a persistent
+// copy bandwidth): 58.8 us.  What did not pay there: loads a group ahead in a persistent
 // grid (71 us), a ring of cp.async copies (69 us) or of bulk copies (76 us) per warp; all
 // spend on addresses and bookkeeping what they save in waiting, and the kernel is bound by
 // issue slots first.
@@ -473,9 +474,10 @@ __global__ void __launch_bounds__(kThreads, NU == 1 ? 3 : 2) heads_fwd_kernel(co
 // while the present group is worked on, at two CTAs an SM (a lane holds 16 elements of x, dy, gamma,
 // dgamma and the sines: 128 registers, none left for vectors on their way; loaded into registers and
 // copied, the copies wait for the loads).  bf16 4 x 4,096 tokens of 32 + 8 heads of 128 (75 us at the
-// copy bandwidth): 93 us, with the early loads in registers 103, without early loads 118 at three
-// CTAs.  fp32 heads hold half as many elements a lane, so three CTAs fit, and load when they need it:
-// 32,768 tokens of 16 + 2 heads of 256 (268 us): 295 us, with early loads at two CTAs 356.
+// copy bandwidth): 93 us before the CTAs were dealt by cost (84 since), with the early loads in registers
+// 103, without early loads 118 at three CTAs.  fp32 heads hold half as many elements a lane, so three
+// CTAs fit, and load when they need it: 32,768 tokens of 16 + 2 heads of 256 (268 us): 295 us then (282
+// since), with early loads at two CTAs 356.
 template <class Fmt>
 constexpr bool kBwdAhead = sizeof(typename Fmt::T) == 2;
 
