@@ -483,6 +483,7 @@ def tb_rope_freqs(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
     return table.to("cuda" if device is None else device), magnitude.value
 
 
+_F32 = torch.float32
 _HEADS_BYTES = ctypes.sizeof(tb_heads)        # five 8-byte fields
 assert _HEADS_BYTES == 40 and ctypes.sizeof(tb_rope_angles) == 48
 
@@ -495,7 +496,7 @@ class _HeadsCall:
     ``tensors`` are the queries, the keys (or None), and pairs behind them with as many heads as
     the queries and the keys."""
 
-    __slots__ = ("words", "at", "batch", "seq", "dim", "code", "device", "heads")
+    __slots__ = ("words", "p", "batch", "seq", "dim", "code", "device", "heads")
 
     def __init__(self, names, tensors, freqs: Optional[torch.Tensor],
                  positions: Optional[torch.Tensor], offset: int, interleaved: bool,
@@ -514,10 +515,11 @@ class _HeadsCall:
                 words += (0, 0, 0, 0, 0)
                 heads.append(None)
                 continue
-            b, s, h, d = shape = t.shape if t.dim() == 4 else (-1, -1, -1, -1)
+            shape = t.shape
+            b, s, h, d = shape if len(shape) == 4 else (-1, -1, -1, -1)
             if b != batch or s != seq or d != dim:
                 raise ValueError(f"{names[i]} must be [batch, seq, heads, head_dim] with the batch, "
-                                 f"seq and head_dim of {names[0]}, got {tuple(t.shape)}")
+                                 f"seq and head_dim of {names[0]}, got {tuple(shape)}")
             if t.dtype != dtype:
                 raise ValueError(f"{names[i]} must be {dtype} like {names[0]}, got {t.dtype}")
             sb, ss, sh, sd = t.stride()
@@ -557,25 +559,24 @@ class _HeadsCall:
         size = _float_bits(magnitude) if magnitude != 1.0 else 0x3F800000
         words += (table, where, stride, int(offset), rot | (bool(interleaved) << 32), size)
         self.words = array("q", words)
-        self.at = self.words.buffer_info()[0]
+        at = self.words.buffer_info()[0]
+        # addresses of the tensors' tb_heads (None for one that was not given), the tb_rope_angles last
+        self.p = p = [at + i * _HEADS_BYTES for i in range(len(heads) + 1)]
+        if None in heads:
+            for i, h in enumerate(heads):
+                if h is None:
+                    p[i] = None
         self.batch, self.seq, self.dim, self.device, self.heads = batch, seq, dim, device, heads
         self.code = _DTYPE.get(dtype)
         if self.code is None:
             raise TbError("dtype", 2)
 
-    def __call__(self, i: int) -> Optional[int]:
-        """Address of the i-th tensor's tb_heads; None for a tensor that was not given. The one
-        behind the last is the tb_rope_angles."""
-        if i < len(self.heads) and self.heads[i] is None:
-            return None
-        return self.at + i * _HEADS_BYTES
-
     def fp32(self, t: Optional[torch.Tensor], n: int, name: str) -> Optional[int]:
         """Address of a contiguous fp32 tensor of n values on the call's device."""
         if t is None:
             raise ValueError(f"{name} is missing")
-        if t.numel() != n or t.dtype != torch.float32:
-            _want(t, n, torch.float32, name)
+        if t.numel() != n or t.dtype != _F32:
+            _want(t, n, _F32, name)
         if t.get_device() != self.device or not t.is_contiguous():
             return _ptr(t)
         return t.data_ptr() or None
@@ -597,8 +598,7 @@ def tb_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_out: torch.Tensor,
     may be its own input."""
     c = _HeadsCall(("q", "k", "q_out", "k_out"), (q, k, q_out, k_out), freqs, positions, offset,
                    interleaved, magnitude)
-    _check("tb_rope", lib.tb_rope(c(0), c(1), c(2), c(3), c.batch, c.seq, c.dim, c(4), c.code,
-                                  c.stream(stream)))
+    _check("tb_rope", lib.tb_rope(*c.p[:4], c.batch, c.seq, c.dim, c.p[4], c.code, c.stream(stream)))
 
 
 def tb_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], dq: torch.Tensor,
@@ -608,8 +608,8 @@ def tb_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], dq: torch.
     """Gradient of tb_rope: the transposed rotation of dq_out and dk_out."""
     c = _HeadsCall(("dq_out", "dk_out", "dq", "dk"), (dq_out, dk_out, dq, dk), freqs, positions,
                    offset, interleaved, magnitude)
-    _check("tb_rope_bwd", lib.tb_rope_bwd(c(0), c(1), c(2), c(3), c.batch, c.seq, c.dim, c(4),
-                                          c.code, c.stream(stream)))
+    _check("tb_rope_bwd", lib.tb_rope_bwd(*c.p[:4], c.batch, c.seq, c.dim, c.p[4], c.code,
+                                          c.stream(stream)))
 
 
 def tb_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], gamma_q: torch.Tensor,
@@ -630,8 +630,8 @@ def tb_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], gamma_q: torch.T
     rq = None if inv_rms_q is None else c.fp32(inv_rms_q, tokens * c.heads[0], "inv_rms_q")
     rk = None if inv_rms_k is None else c.fp32(inv_rms_k, tokens * (c.heads[1] or 0), "inv_rms_k")
     _check("tb_qk_norm_rope",
-           lib.tb_qk_norm_rope(c(0), c(1), gq, gk, float(eps), c(2), c(3), rq, rk, c.batch, c.seq,
-                               c.dim, c(4), c.code, c.stream(stream)))
+           lib.tb_qk_norm_rope(c.p[0], c.p[1], gq, gk, float(eps), c.p[2], c.p[3], rq, rk, c.batch,
+                               c.seq, c.dim, c.p[4], c.code, c.stream(stream)))
 
 
 def tb_qk_norm_rope_bwd_workspace_size(batch: int, seq: int, heads_q: int, heads_k: int,
@@ -662,11 +662,11 @@ def tb_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q:
     if k is not None:
         gk, sk = c.fp32(gamma_k, c.dim, "gamma_k"), c.fp32(dgamma_k, c.dim, "dgamma_k")
         rk = c.fp32(inv_rms_k, tokens * c.heads[1], "inv_rms_k")
+    px, pkx, pdx, pdk, py, pky, angles = c.p
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check("tb_qk_norm_rope_bwd",
-           lib.tb_qk_norm_rope_bwd(c(4), c(5), c(0), c(1), rq, rk, gq, gk, c(2), c(3), sq, sk,
-                                   c.batch, c.seq, c.dim, c(6), c.code, _ptr(workspace), ws_bytes,
-                                   c.stream(stream)))
+           lib.tb_qk_norm_rope_bwd(py, pky, px, pkx, rq, rk, gq, gk, pdx, pdk, sq, sk, c.batch, c.seq,
+                                   c.dim, angles, c.code, _ptr(workspace), ws_bytes, c.stream(stream)))
 
 
 # ----------------------------------------------------------------------------- output layer's loss

@@ -180,6 +180,33 @@ def test_in_place_equals_out_of_place(tb, dtype, dim, rot):
         assert torch.equal(dg[0], dg[2]) and torch.equal(dg[1], dg[3])
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("shape, rot, interleaved", [((2, 4001, 8, 2, 128), 128, False), ((3, 2003, 7, 3, 80), 32, True),
+                                                     ((1, 9001, 1, 1, 64), 64, True)])
+def test_gradient_in_place_over_many_tokens(tb, shape, rot, interleaved, dtype):
+    """Warps that take several tokens ask for the next one's heads before they write the last one's."""
+    b, s, hq, hk, d = shape
+    turns, freqs, pos, angle, gam = _case(shape, rot, 21)
+    ws = torch.empty(tb.tb_qk_norm_rope_bwd_workspace_size(*shape, dtype), dtype=torch.uint8, device="cuda")
+    kw = dict(freqs=freqs, positions=pos, interleaved=interleaved, workspace=ws)
+    xq, xk, _ = make(shape, dtype, "qkv", 22)
+    gq, gk, _ = make(shape, dtype, "bshd", 23)
+    inv = [ref.normed(x.double(), 1.0, 1e-6)[1].float() for x in (xq, xk)]
+    dq, dk, _ = make(shape, dtype, "bhsd", 24)
+    dg = [torch.empty(d, device="cuda") for _ in range(6)]
+    tb.tb_qk_norm_rope_bwd(gq, gk, xq, xk, *inv, *gam, dq, dk, *dg[:2], **kw)
+    want, want_g, err, err_g = ref.norm_grad(gq.double(), xq.double(), inv[0].double(), gam[0].double(), angle, rot, interleaved)
+    ref.check(dq, want, err)
+    ref.check(dg[0], want_g, err_g)
+    g2, x2, = [t.clone() for t in (gq, gk)], [t.clone() for t in (xq, xk)]
+    tb.tb_qk_norm_rope_bwd(*g2, xq, xk, *inv, *gam, *g2, *dg[2:4], **kw)
+    tb.tb_qk_norm_rope_bwd(gq, gk, *x2, *inv, *gam, *x2, *dg[4:], **kw)
+    for got in (g2, x2):
+        assert torch.equal(got[0], dq) and torch.equal(got[1], dk)
+    for i in (2, 4):
+        assert torch.equal(dg[i], dg[0]) and torch.equal(dg[i + 1], dg[1])
+
+
 def test_queries_alone_positions_and_offsets(tb):
     shape, rot = (3, 8, 4, 2, 64), 64
     turns, freqs = ref.frequencies(rot)
