@@ -12,7 +12,7 @@
 // 256 x 256 tile: tcgen05.mma.cta_group::2 with both operands in shared memory, 64 of the
 // contracted dimension a stage, 128-byte swizzled; each CTA stages its half of A and of B
 // (32 KB a stage, a ring of six), so a tile's operands cross from L2 once per pair.  Warp 0
-// feeds the ring by TMA, warp 1 of the pair's first CTA issues the MMAs, warps 4..11 drain
+// feeds the ring by TMA, warp 1 of the pair's first CTA issues the MMAs, warps 4..11 (or 4..19) drain
 // the accumulator -- of which there are two, 256 TMEM columns each, so that the epilogue of
 // one tile runs under the MMAs of the next.  A thread of the epilogue owns one row of the
 // tile: row sums need no shuffles.  Tiles are dealt statically to a persistent grid of one
@@ -60,12 +60,20 @@ constexpr int kStageK = 64;                  // contracted elements a stage: 128
 constexpr int kStages = 6;
 constexpr int kOperandBytes = kHalf * kStageK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kThreads = 384;
 constexpr int kEpiWarp = 4;                  // first of the epilogue warps
-constexpr int kEpiWarps = 8;                 // two for each quarter of the accumulator's rows
+// Epilogue warps: two for each quarter of the accumulator's rows, or four where logits have so few
+// contracted elements that the epilogue takes longer than a tile's MMAs.  Loss and G of 4,096 x 50,257:
+// at 256 contracted elements 97 and 119 us with 8 warps, 77 and 99 with 16; at 384, 100 and 129 against
+// 88 and 131; at 512, 117 and 170 against 124 and 170 (a warp of 16 has no second buffer for columns on
+// their way).  The loss of few tiles is bound by latency: 100 x 32,000 x 256 took 12.8 us with 8, 14.5
+// with 16.
+constexpr int kFewWarps = 8, kManyWarps = 16;
+constexpr int kShortStages = 384 / kStageK;
+constexpr int kThreadsOf(int epi) { return (kEpiWarp + epi) * 32; }
 constexpr int kOutCols = 32;
 constexpr int kOutBytes = 32 * kOutCols * 2; // what an epilogue warp stores at once: 32 rows
-constexpr int kSmem = kStages * kStageBytes + 2 * kEpiWarps * kOutBytes + 1024 + 256;   // alignment, barriers
+constexpr int kOutboxes = 16;                // one or two for each epilogue warp
+constexpr int kSmem = kStages * kStageBytes + kOutboxes * kOutBytes + 1024 + 256;   // alignment, barriers
 constexpr int kTmemCols = 512;               // two accumulators
 // Row tiles walked together (see tile_at): bf16 8,192 x 32,000 x 4,096, loss and gradient, took 1,133
 // and 3,673 us with 16, 1,170 and 3,704 with 8, 1,180 and 3,943 with 32.
@@ -290,7 +298,7 @@ struct Product {
     const int64_t* target;    // of this launch's rows
     int64_t ignore;
     int vocab;
-    float2* part;             // kLse: [2 n_tiles][rows] maximum and sum of half a tile
+    float2* part;             // kLse: [parts of a tile * n_tiles][rows] maximum and sum
     float* target_logit;      // kLse: [rows]
     const float *lse, *dloss; // kGrad
     const float* weight;      // kDH: dloss by row, 0 where a row takes no part
@@ -356,16 +364,19 @@ __device__ __forceinline__ float weight_of(const Product& p, int64_t r) {
     const float v = p.weigh.dloss[r];
     return t != p.ignore && t >= 0 && t < p.vocab ? v : 0.f;
 }
-constexpr int kWeighThreads = (kEpiWarps + 2) * 32;       // of named barrier 1
 
-// By the epilogue warps; thread 0 .. 255 of them.
-template <class Fmt>
+// Both meet at named barrier 1.
+template <int Epi>
+constexpr int kWeighThreads = (Epi + 2) * 32;
+
+// By the epilogue warps, `thread` counts theirs.
+template <class Fmt, int Epi>
 __device__ __forceinline__ void weigh_top(const Product& p, int thread, float* tops) {
     float m = 0.f;
-    unsigned owner = 0;               // of the next 256 rows' weights
+    unsigned owner = 0;               // of the next rows' weights
     const int64_t rows = p.weigh.rows;
 #pragma unroll 8
-    for (int64_t r = thread; r < rows; r += 256) {
+    for (int64_t r = thread; r < rows; r += Epi * 32) {
         const float v = weight_of<Fmt>(p, r);
         if (owner == blockIdx.x) p.weigh.weight[r] = v;
         if (++owner == gridDim.x) owner = 0;
@@ -373,17 +384,17 @@ __device__ __forceinline__ void weigh_top(const Product& p, int thread, float* t
     }
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (thread % 32 == 0) tops[thread / 32] = m;
-    asm volatile("bar.arrive 1, %0;" ::"n"(kWeighThreads) : "memory");
+    asm volatile("bar.arrive 1, %0;" ::"n"(kWeighThreads<Epi>) : "memory");
 }
 
 // By the other two; part 0 .. parts - 1 of all CTAs' warps.
-template <class Fmt>
+template <class Fmt, int Epi>
 __device__ __forceinline__ void weigh_rows(const Product& p, int lane, unsigned part, unsigned parts,
                                            const float* tops) {
     using T = typename Fmt::T;
-    asm volatile("bar.sync 1, %0;" ::"n"(kWeighThreads) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(kWeighThreads<Epi>) : "memory");
     float m = tops[0];
-    for (int i = 1; i < kEpiWarps; ++i) m = fmaxf(m, tops[i]);
+    for (int i = 1; i < Epi; ++i) m = fmaxf(m, tops[i]);
     if (m == 0.f) m = 1.f;
     if (part == 0 && lane == 0) *p.weigh.top = m;
     if (!p.weigh.scaled) return;
@@ -475,9 +486,9 @@ struct Feed {
 // warp share banks), and a TMA store of the box, of which each warp has two.  Stored from registers,
 // a warp's 16-byte pieces lie a row apart, 32 half sectors an instruction: the epilogue then took
 // longer than the MMAs of a tile with 768 contracted elements (78 us against 62 us, 1,021 x 50,257).
-template <class Fmt>
+template <class Fmt, int Boxes>
 struct Outbox {
-    unsigned char* mem;       // this warp's two boxes
+    unsigned char* mem;       // this warp's boxes
     const CUtensorMap* map;
     int lane, n;              // boxes filled so far
     __device__ __forceinline__ void fill(unsigned char* box, const float (&v)[32]) const {
@@ -490,9 +501,9 @@ struct Outbox {
         }
     }
     __device__ __forceinline__ void put(const float (&v)[32], int x, int y) {
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        __syncwarp();         // the box of two stores ago has been read
-        unsigned char* box = mem + (n & 1) * kOutBytes;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(Boxes - 1) : "memory");
+        __syncwarp();         // the box of `Boxes` stores ago has been read
+        unsigned char* box = mem + n % Boxes * kOutBytes;
         fill(box, v);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -554,18 +565,19 @@ __device__ __forceinline__ void fold(float& m, float& s, float m2, float s2) {
 }
 
 // ---------------------------------------------------------------- the product
-template <class Fmt, int K>
-__global__ void __launch_bounds__(kThreads, 1)
+template <class Fmt, int K, int Epi>
+__global__ void __launch_bounds__(kThreadsOf(Epi), 1)
 product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                const __grid_constant__ CUtensorMap map_out, const __grid_constant__ Product p) {
     using T = typename Fmt::T;
     constexpr bool kAMn = K == kDW, kBMn = K == kDH || K == kDW;
-    __shared__ float tops[kEpiWarps];       // kGrad: see weigh_top
+    constexpr int kParts = Epi / 4;         // of a tile's columns
+    __shared__ float tops[Epi];       // kGrad: see weigh_top
     extern __shared__ unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     unsigned char* outbox = smem + kStages * kStageBytes;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(outbox + 2 * kEpiWarps * kOutBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(outbox + kOutboxes * kOutBytes);
     const uint32_t stage0 = smem_addr(smem), bar0 = smem_addr(bars);
     const uint32_t full = bar0, empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
                    acc_empty = acc_full + 16, drain = acc_empty + 16, slot = drain + 8;
@@ -580,7 +592,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
-            mbar_init(acc_empty + 8 * i, 2 * kEpiWarps);   // of both CTAs
+            mbar_init(acc_empty + 8 * i, 2 * Epi);    // of both CTAs
         }
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -678,15 +690,15 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             }
         }
     } else if (K == kGrad && (warp == 2 || warp == 3)) {
-        if (p.weigh.weight) weigh_rows<Fmt>(p, lane, blockIdx.x * 2 + (warp & 1), gridDim.x * 2, tops);
+        if (p.weigh.weight) weigh_rows<Fmt, Epi>(p, lane, blockIdx.x * 2 + (warp & 1), gridDim.x * 2, tops);
     } else if (warp >= kEpiWarp) {
         // TMEM lanes 32 quad .. 32 quad + 31 (a warp reaches those of its number modulo 4), and
-        // the first or second half of the tile's columns
-        const int quad = warp & 3, half = (warp - kEpiWarp) >> 2;
+        // one of the parts of the tile's columns
+        const int quad = warp & 3, part_no = (warp - kEpiWarp) >> 2;
         const uint32_t leader_empty = map_to(acc_empty, 0);
-        if (K == kGrad && p.weigh.weight) weigh_top<Fmt>(p, threadIdx.x - kEpiWarp * 32, tops);
+        if (K == kGrad && p.weigh.weight) weigh_top<Fmt, Epi>(p, threadIdx.x - kEpiWarp * 32, tops);
         const float top_weight = K == kDW ? *p.top : 1.f;
-        Outbox<Fmt> box{outbox + (warp - kEpiWarp) * 2 * kOutBytes, &map_out, lane, 0};
+        Outbox<Fmt, kOutboxes / Epi> box{outbox + (warp - kEpiWarp) * (kOutboxes / Epi) * kOutBytes, &map_out, lane, 0};
         // What a tile's row needs from memory is asked for while the tile before it is worked on: a
         // load's latency at the start of every tile is as long as the work on one of few stages.
         struct Tile {
@@ -714,8 +726,8 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             const int row0 = tile.row0, row = row0 + lane;
             const bool live = row < p.rows;
             const int n0 = nt * p.width, all = min(p.width, p.cols - n0);
-            const int middle = (all + 63) / 64 * 32;
-            const int c0 = half ? middle : 0, width = half ? all : min(all, middle);
+            const int share = (all + 32 * kParts - 1) / (32 * kParts) * 32;
+            const int c0 = part_no * share, width = min(all, c0 + share);
             const uint32_t acc = tmem + buf * kTile + ((uint32_t)(quad * 32) << 16);
             if (!__all_sync(0xffffffffu, mbar_wait<false>(acc_full + 8 * buf, (n / 2) & 1, p.err))) break;
             tmem_fence_after();
@@ -824,31 +836,43 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             };
             // The next columns come while the present ones are worked on; behind the last ones the
             // accumulator is free for the MMAs of the tile after the next.
-            uint32_t one[32], two[32];
+            uint32_t one[32];
             auto release = [&] {
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(leader_empty + 8 * buf);
             };
             __syncwarp();
-            if (c0 < width) tmem_load32(acc + c0, one);
-            else release();
-            for (int c = c0; c < width; c += 64) {
-                tmem_wait(one);
-                if (c + 32 < width) tmem_load32(acc + c + 32, two);
-                else release();
-                work(one, c);
-                __syncwarp();
-                if (c + 32 < width) {
-                    tmem_wait(two);
-                    if (c + 64 < width) tmem_load32(acc + c + 64, one);
-                    else release();
-                    work(two, c + 32);
+            if constexpr (kParts > 2) {   // four warps a scheduler: the others work while one waits
+                if (c0 >= width) release();
+                for (int c = c0; c < width; c += 32) {
+                    tmem_load32(acc + c, one);
+                    tmem_wait(one);
+                    if (c + 32 >= width) release();
+                    work(one, c);
                     __syncwarp();
+                }
+            } else {
+                uint32_t two[32];
+                if (c0 < width) tmem_load32(acc + c0, one);
+                else release();
+                for (int c = c0; c < width; c += 64) {
+                    tmem_wait(one);
+                    if (c + 32 < width) tmem_load32(acc + c + 32, two);
+                    else release();
+                    work(one, c);
+                    __syncwarp();
+                    if (c + 32 < width) {
+                        tmem_wait(two);
+                        if (c + 64 < width) tmem_load32(acc + c + 64, one);
+                        else release();
+                        work(two, c + 32);
+                        __syncwarp();
+                    }
                 }
             }
             if constexpr (K == kLse) {
-                if (live) p.part[((int64_t)nt * 2 + half) * p.rows + row] = make_float2(m, s);
+                if (live) p.part[((int64_t)nt * kParts + part_no) * p.rows + row] = make_float2(m, s);
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -863,7 +887,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 }
 
 // ---------------------------------------------------------------- around the products
-// A row's parts, two for each column tile, in a fixed order.  R rows a CTA, 256 / R lanes a row:
+// A row's parts, two or four for each column tile, in a fixed order.  R rows a CTA, 256 / R lanes a row:
 // 32 rows side by side read whole sectors, eight put more loads in flight for calls of few rows.
 template <int R>
 __global__ void __launch_bounds__(256)
@@ -1040,17 +1064,17 @@ bool make_sums_map(CUtensorMap* map, float* p, int64_t splits, int64_t rows, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class Fmt, int K>
+template <class Fmt, int K, int Epi = kFewWarps>
 tb_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, const Product& p,
                          cudaStream_t st) {
-    const void* kernel = reinterpret_cast<const void*>(&product_kernel<Fmt, K>);
-    const int pairs = resident_clusters(kernel, kThreads, kSmem, 2);
+    const void* kernel = reinterpret_cast<const void*>(&product_kernel<Fmt, K, Epi>);
+    const int pairs = resident_clusters(kernel, kThreadsOf(Epi), kSmem, 2);
     if (pairs < 1) return TB_ERR_CUDA;
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles * p.splits;
     // (pairs without a tile still take their share of weigh_rows)
     const int64_t grid = 2 * (p.weigh.weight ? pairs : std::min<int64_t>(tiles, pairs));
-    if (launch_clusters<true>(product_kernel<Fmt, K>, dim3((unsigned)grid), dim3(kThreads), kSmem, st, 2, a, b, out, p) !=
-        cudaSuccess)
+    if (launch_clusters<true>(product_kernel<Fmt, K, Epi>, dim3((unsigned)grid), dim3(kThreadsOf(Epi)), kSmem, st, 2, a, b,
+                              out, p) != cudaSuccess)
         return TB_ERR_CUDA;
     return launch_status();
 }
@@ -1059,6 +1083,7 @@ tb_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUten
 struct Cut {
     int lse_width, grad_width;   // columns of a tile of logits
     int64_t lse_tiles;
+    int lse_warps, grad_warps;   // of the epilogue of logits
     int64_t ld;               // padded row length of H and W (D where no copy is needed)
     bool pad;
     int64_t piece, pieces;    // gradient: columns of a piece of the vocabulary
@@ -1118,7 +1143,9 @@ Cut cut_call(int64_t n, int64_t d, int64_t v, bool bwd, int sms) {
         const int64_t rows = std::min(n, kLseRows);
         c.lse_width = pick_width(ceil_div(rows, kTile), v, sms / 2);
         c.lse_tiles = ceil_div(v, c.lse_width);
-        c.off_part = take((size_t)rows * 2 * c.lse_tiles * sizeof(float2));
+        const bool many = ceil_div(d, kStageK) <= kShortStages && ceil_div(rows, kTile) * c.lse_tiles > 8 * (sms / 2);
+        c.lse_warps = many ? kManyWarps : kFewWarps;
+        c.off_part = take((size_t)rows * (c.lse_warps / 4) * c.lse_tiles * sizeof(float2));
         c.off_logit = take((size_t)rows * sizeof(float));
     } else {
         int64_t most = std::max(kMinPiece, kPieceBytes / (2 * std::max<int64_t>(n, 1)));
@@ -1127,6 +1154,7 @@ Cut cut_call(int64_t n, int64_t d, int64_t v, bool bwd, int sms) {
         c.piece = std::min(round_up(ceil_div(v, c.pieces), kTile), round_up(v, kTile));
         c.pieces = ceil_div(v, c.piece);
         c.ldg = c.piece;
+        c.grad_warps = ceil_div(d, kStageK) <= kShortStages ? kManyWarps : kFewWarps;
         c.grad_width = pick_width(ceil_div(n, kTile), std::min(c.piece, v), sms / 2);
         c.splits = pick_splits(n, d, c.piece / kStageK, sms / 2);
         c.splits_w = pick_splits(std::min(c.piece, v), d, ceil_div(n, kStageK), sms / 2);
@@ -1225,13 +1253,14 @@ tb_status run_loss(const Problem& q, const Cut& c) {
         p.vocab = (int)q.v;
         p.part = reinterpret_cast<float2*>(q.ws + c.off_part);
         p.target_logit = reinterpret_cast<float*>(q.ws + c.off_logit);
-        const tb_status s = launch_product<Fmt, kLse>(a, b, a, p, q.st);
+        const tb_status s = c.lse_warps == kManyWarps ? launch_product<Fmt, kLse, kManyWarps>(a, b, a, p, q.st)
+                                                      : launch_product<Fmt, kLse>(a, b, a, p, q.st);
         if (s != TB_OK) return s;
         const bool few = rows <= 32 * q.sms;
         const dim3 grid((unsigned)ceil_div(rows, few ? 8 : 32));
         const cudaError_t e = launch_pdl(few ? join_kernel<8> : join_kernel<32>, grid, dim3(256), 0, q.st,
                                          (const float2*)p.part, (const float*)p.target_logit, p.target, p.ignore,
-                                         p.vocab, p.rows, 2 * p.n_tiles, q.loss + r0, q.lse + r0, q.err);
+                                         p.vocab, p.rows, c.lse_warps / 4 * p.n_tiles, q.loss + r0, q.lse + r0, q.err);
         if (e != cudaSuccess) return TB_ERR_CUDA;
     }
     return launch_status();
@@ -1289,7 +1318,8 @@ tb_status run_grad(const Problem& q, const Cut& c) {
         if (i == 0)
             p.weigh = Weigh{q.dloss, H, q.dW ? scaled : nullptr, weight, top, q.n, (int)c.ld};
         if (!make_map(&out, g, q.n, cols, c.ldg, 32, bf, true)) return TB_ERR_CUDA;
-        tb_status s = launch_product<Fmt, kGrad>(h_rows, w_rows, out, p, q.st);
+        tb_status s = c.grad_warps == kManyWarps ? launch_product<Fmt, kGrad, kManyWarps>(h_rows, w_rows, out, p, q.st)
+                                                 : launch_product<Fmt, kGrad>(h_rows, w_rows, out, p, q.st);
         if (s != TB_OK) return s;
         if (q.dH) {
             if (!make_map(&g_rows, g, q.n, cols, c.ldg, box_rows(q.n), bf)) return TB_ERR_CUDA;

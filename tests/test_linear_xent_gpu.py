@@ -139,7 +139,7 @@ def test_gradients(tb, n, d, v, dtype):
 # several pieces of the vocabulary (of 256 MiB of G), launches of the loss, and with 7,000 columns
 # pieces whose dH is split as well; row lengths whose fp32 sums TMA can and cannot write
 @pytest.mark.parametrize("dtype", [BF, HF])
-@pytest.mark.parametrize("n, d, v", [(40000, 24, 5000), (20000, 32, 7000), (20000, 33, 7000)])
+@pytest.mark.parametrize("n, d, v", [(40000, 24, 5000), (20000, 32, 7000), (20000, 33, 7000), (36000, 400, 4001)])
 def test_pieces_of_the_vocabulary(tb, n, d, v, dtype):
     H, W, t, dloss = problem(n, d, v, dtype, 2)
     loss, lse = forward(tb, H, W, t)
