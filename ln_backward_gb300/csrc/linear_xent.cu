@@ -23,8 +23,8 @@
 // the clock.  bf16 8,192 x 32,000 x 4,096: loss 1,130 us (1,900 TFLOP/s), gradient 3,590 to
 // 3,690 us (1,750 to 1,790 TFLOP/s; a cuBLAS product reaches 1,871 in a burst and 1,707 for
 // seconds).  Short contractions are bound by the epilogue and by the loads' latency: fp16
-// 1,021 x 50,257 x 768, gradient, 157 us (126 us at 1,871 TFLOP/s); bf16 37 rows against the
-// same weights, loss, 22 us, of which about 13 read W at 6 TB/s.
+// 1,021 x 50,257 x 768, gradient, 157 to 170 us by board (126 us at 1,871 TFLOP/s); bf16 37 rows
+// against the same weights, loss, 22 us, of which about 13 read W at 6 TB/s.
 //
 // The accumulators are fp32, but tensor cores cut off what an addition shifts below the sum's
 // last place, where fp32 arithmetic rounds: at D = 4,096 a logit comes out smaller by 4e-6 of
