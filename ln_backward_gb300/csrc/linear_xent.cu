@@ -276,6 +276,13 @@ __device__ __forceinline__ unsigned long long add_pair(unsigned long long a, uns
 }
 
 constexpr float kLog2e = 1.44269504088896341f;
+// exp(l - b) is exp2(l log2(e) - b log2(e)) in one FMA, off by a factor of two to the rounding of
+// b log2(e): 2^-10 of a power at |b| = 2^14, 16 powers at 2^28, and beyond 2^31 (columns masked by
+// -1e10, say) as many as make it inf or 0. The loss takes that rounding out of a group's sum again, where
+// the sum is scaled anyway, and above kAlone, where fp32 numbers lie 32 apart, counts the largest logit
+// alone. The gradient forms l - lse first where |lse| is above kFar. (So did the loss: a branch in
+// every 32 columns, 79 -> 82 us for 4,096 x 50,257 x 256.)
+constexpr float kAlone = 268435456.f, kFar = 16384.f;
 
 // ---------------------------------------------------------------- arguments
 struct Weigh {
@@ -552,14 +559,15 @@ __device__ __forceinline__ void put_sums(unsigned char* box, const CUtensorMap* 
     }
 }
 
-// Folds 32 logits into a row's maximum m and sum s of exp(l - base(m)); base is 0 where the
-// maximum is infinite, so that a logit of +inf gives lse = +inf and rows of -inf give -inf.
+// Folds a group of logits into a row's maximum m and sum s of exp(l - base(m)); base is 0 where the
+// maximum is infinite, so that a logit of +inf gives lse = +inf and rows of -inf give -inf.  `off`:
+// the powers of two by which the group's sum is too large.
 __device__ __forceinline__ float base_of(float m) { return isinf(m) ? 0.f : m; }
 
-__device__ __forceinline__ void fold(float& m, float& s, float m2, float s2) {
+__device__ __forceinline__ void fold(float& m, float& s, float m2, float s2, float off = 0.f) {
     const float top = fmaxf(m, m2), b = base_of(top);
     const float x = s == 0.f ? 0.f : s * exp2_fast((base_of(m) - b) * kLog2e);
-    const float y = s2 == 0.f ? 0.f : s2 * exp2_fast((base_of(m2) - b) * kLog2e);
+    const float y = s2 == 0.f ? 0.f : s2 * exp2_fast(__fmaf_rn(base_of(m2) - b, kLog2e, -off));
     m = top;
     s = x + y;
 }
@@ -735,13 +743,14 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             int hit = -1;                             // the target's column in this tile
             const float weight = tile.weight;
             float lse2 = 0.f;
-            bool counts = false;
+            bool counts = false, far = false;
             if constexpr (K == kLse || K == kGrad) {
                 counts = live && tile.target != p.ignore && tile.target >= 0 && tile.target < p.vocab;
                 const int64_t c = tile.target - (K == kGrad ? p.b_base : 0) - n0;
                 if (counts && c >= c0 && c < width) hit = (int)c;
                 if constexpr (K == kGrad) {
-                    lse2 = tile.lse * kLog2e - kGBits<Fmt>;
+                    far = fabsf(tile.lse) > kFar && !isinf(tile.lse);
+                    lse2 = (far ? 0.f : tile.lse * kLog2e) - kGBits<Fmt>;
                     // a row that is weighted with 0 counts for nothing, not for 0 * NaN (dW)
                     counts = counts && weight != 0.f;
                 }
@@ -770,8 +779,10 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 #pragma unroll
                     for (int i = 4; i < 32; ++i) top4[i & 3] = fmaxf(top4[i & 3], v[i]);
                     const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-                    const unsigned long long b2 = pair_of(-base_of(top) * kLog2e, -base_of(top) * kLog2e),
-                                             scale = pair_of(kLog2e, kLog2e);
+                    // (finite: a column behind the vocabulary's end is -inf)
+                    const float base = base_of(top), at = fmaxf(base * kLog2e, -3.4028235e38f),
+                                off = __fmaf_rn(base, kLog2e, -at);
+                    const unsigned long long b2 = pair_of(-at, -at), scale = pair_of(kLog2e, kLog2e);
                     unsigned long long sum[4] = {0, 0, 0, 0};
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -781,8 +792,15 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     }
                     float part, part2;
                     split_pair(add_pair(add_pair(sum[0], sum[1]), add_pair(sum[2], sum[3])), part, part2);
-                    fold(m, s, top, part + part2);
+                    part += part2;
+                    const bool alone = fabsf(base) > kAlone;
+                    if (alone && part == part) part = 1.f;
+                    fold(m, s, top, part, alone ? 0.f : off);
                 } else if constexpr (K == kGrad) {
+                    if (far) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] -= tile.lse;
+                    }
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         split_pair(fma_pair(pair_of(v[i], v[i + 1]), pair_of(kLog2e, kLog2e), pair_of(-lse2, -lse2)),

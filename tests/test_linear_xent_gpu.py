@@ -355,3 +355,68 @@ def test_graph_replay_streams_and_two_calls_at_once(tb):
         for x, y in zip(o, eager):
             assert torch.equal(x, y)
     assert tb.tb_device_error() == 0
+
+
+def masked_problem(dtype, value, columns, n=70, d=72, v=700, seed=14):
+    """Columns of the vocabulary masked by an additive term: the hidden states' first element is a
+    constant, and `value` over it the masked columns' first weight."""
+    H, W, t, dloss = problem(n, d, v, dtype, seed, ignored=0.0)
+    H[:, 0] = 1.0 if dtype == BF else 16384.0
+    W[:, 0] = 0.0
+    W[columns, 0] = value / H[0, 0].item()
+    t = torch.arange(n, device="cuda") % 64 + 640                       # 640 .. 699: never masked below
+    t[t >= v] = v - 1
+    return H, W, t, dloss
+
+
+@pytest.mark.parametrize("dtype, values", [(BF, (-1e10, 2.0 ** 33 * -1.7, -1e30, -3.3e38)),
+                                           (HF, (-2.0 ** 29, -1.7 * 2.0 ** 28, -1e9))])
+@pytest.mark.parametrize("columns", [slice(0, 640), slice(32, 64), slice(3, 500)])
+def test_masks_of_low_values(tb, dtype, values, columns):
+    """A masked column counts exp(-large) = 0 whatever the large value is: the same bits as with a
+    mask of -10,000, in 32-column groups that hold nothing else as well."""
+    H, W, t, dloss = masked_problem(dtype, -1e4, columns)
+    loss, lse = forward(tb, H, W, t)
+    keep = torch.ones(W.shape[0], dtype=torch.bool, device="cuda")
+    keep[columns] = False
+    check_forward(loss, lse, H, W[keep].contiguous(), t - int((~keep).sum()))
+    dH, dW = backward(tb, dloss, H, W, t, lse)
+    assert not dW[columns].any()
+    for value in values:
+        H, W, t, dloss = masked_problem(dtype, value, columns)
+        got = forward(tb, H, W, t)
+        assert torch.equal(got[0], loss) and torch.equal(got[1], lse), value
+        dH2, dW2 = backward(tb, dloss, H, W, t, lse)
+        assert torch.equal(dH2, dH) and torch.equal(dW2, dW), value
+
+
+@pytest.mark.parametrize("dtype, values", [(BF, (-1e10, 2.0 ** 33 * 1.7, 1e30, -3.3e38, 3.3e38)),
+                                           (HF, (-2.0 ** 29, 1.7 * 2.0 ** 28, 1e9))])
+def test_rows_whose_logits_are_all_far_from_zero(tb, dtype, values):
+    """lse is its largest logit to fp32's last places, and G = exp(l - lse) is what it says for
+    that lse: at most 1, and 0 in columns that lie far below."""
+    n, v = 70, 700
+    for value in values:
+        H, W, t, dloss = masked_problem(dtype, value, slice(0, v))
+        l = (H[0, 0].double() * W[0, 0].double()).item()
+        loss, lse = forward(tb, H, W, t)
+        # the other terms of a logit and log(700) are below one of fp32's places, of which
+        # truncated additions lose one each
+        assert ((lse.double() - l).abs() <= abs(l) * 2.0 ** -20).all(), value
+        assert (loss.abs() <= abs(l) * 2.0 ** -20).all(), value
+        # one column above all others: p = 1 there, and where it is the target nothing is left
+        H, W, t, dloss = masked_problem(dtype, abs(value), slice(0, 1))
+        t[:35] = 0
+        loss, lse = forward(tb, H, W, t)
+        top = (H.double() @ W[0].double())
+        assert ((lse.double() - top).abs() <= top.abs() * 2.0 ** -20).all(), value
+        # what the logits of a second call are, the first's were: l - lse = 0 where l is the maximum
+        dH, dW = backward(tb, dloss, H, W, t, lse)
+        assert not dH[:35].any()
+        G = torch.zeros(n, v, device="cuda", dtype=torch.float64)
+        G[35:, 0] = 1.0
+        G[torch.arange(35, n), t[35:]] -= 1.0
+        want, size = (G @ W.double()) * dloss.double()[:, None], (G.abs() @ W.double().abs()) * dloss.double()[:, None]
+        half = torch.finfo(dtype).eps / 2
+        assert ((dH.double() - want).abs() <= size * (half + 2.0 ** -17) + 2.0 ** -25)[:, 1:].all(), value
+        assert dW.isfinite().all()
