@@ -105,6 +105,28 @@ tb_status tb_device_error(int* code, int reset);
  */
 tb_status tb_layernorm_bwd_selftest_timeout(int64_t wait_limit_ns, void* stream);
 
+/*
+ * tb_linear_xent_selftest_timeout -- the same for the output layer's products,
+ * whose waits stand between two CTAs: their bulk copies, their tensor-core
+ * instructions and the accumulators that they hand over.  It runs the loss's
+ * product on one pair of CTAs over three small internal problems (zeroed
+ * buffers the call allocates and frees), TB_LINEAR_XENT_SELFTEST_LAUNCHES
+ * launches in all, each with one thing withheld: the copies of one of the two
+ * CTAs, the word that an accumulator is complete, or the word that it is free
+ * again.  Every launch sets the device error word to TB_ERR_TIMEOUT, waits
+ * (bounded as well) for all copies and tensor-core instructions that either CTA
+ * had started, and returns.  The call synchronises
+ * `stream` and resets the device error word before each launch; afterwards the
+ * word is the last launch's, TB_ERR_TIMEOUT.
+ *   wait_limit_ns  1,000 .. 1,000,000,000
+ *   launches       out: launches whose waits gave up
+ * Returns TB_OK once the kernels have finished, TB_ERR_INVALID_VALUE (limit out
+ * of range, launches == NULL), TB_ERR_OOM or TB_ERR_CUDA.
+ */
+#define TB_LINEAR_XENT_SELFTEST_LAUNCHES 11
+
+tb_status tb_linear_xent_selftest_timeout(int64_t wait_limit_ns, int* launches, void* stream);
+
 /* ======================================================================== */
 /* Fused mixed-precision AdamW (multi-tensor)                               */
 /* ======================================================================== */

@@ -17,7 +17,7 @@ from ._binding import (  # noqa: F401
     tb_layernorm_bwd, tb_layernorm_bwd_noalloc, tb_layernorm_bwd_selftest_timeout,
     tb_layernorm_bwd_workspace_size,
     tb_linear_xent, tb_linear_xent_bwd, tb_linear_xent_bwd_workspace_size,
-    tb_linear_xent_workspace_size,
+    tb_linear_xent_selftest_timeout, tb_linear_xent_workspace_size,
     tb_qk_norm_rope, tb_qk_norm_rope_bwd, tb_qk_norm_rope_bwd_workspace_size,
     tb_rmsnorm_bwd, tb_rmsnorm_bwd_workspace_size,
     tb_rope, tb_rope_bwd, tb_rope_freqs, tb_softmax_bwd, tb_softmax_bwd_causal,

@@ -35,7 +35,8 @@ EXPORTS = ("tb_status_string", "tb_version", "tb_device_error", "tb_adamw_plan_c
            "tb_adamw_step_device", "tb_adamw_selftest_stale_counter", "tb_rope_freqs", "tb_rope",
            "tb_rope_bwd", "tb_qk_norm_rope", "tb_qk_norm_rope_bwd_workspace_size",
            "tb_qk_norm_rope_bwd", "tb_linear_xent_workspace_size", "tb_linear_xent",
-           "tb_linear_xent_bwd_workspace_size", "tb_linear_xent_bwd")
+           "tb_linear_xent_bwd_workspace_size", "tb_linear_xent_bwd",
+           "tb_linear_xent_selftest_timeout")
 
 
 class TbError(RuntimeError):
@@ -121,6 +122,8 @@ def _load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.tb_adamw_step_device.restype = i32
     lib.tb_layernorm_bwd_selftest_timeout.argtypes = [i64, vp]
     lib.tb_layernorm_bwd_selftest_timeout.restype = i32
+    lib.tb_linear_xent_selftest_timeout.argtypes = [i64, ctypes.POINTER(i32), vp]
+    lib.tb_linear_xent_selftest_timeout.restype = i32
     lib.tb_adamw_selftest_stale_counter.argtypes = [vp, ctypes.c_uint64, vp]
     lib.tb_adamw_selftest_stale_counter.restype = i32
     # tb_heads* and tb_rope_angles*: the binding passes addresses into one packed array
@@ -228,6 +231,19 @@ def tb_layernorm_bwd_selftest_timeout(wait_limit_ns: int = 2_000_000, stream=Non
     waits run out; synchronises. tb_device_error() then reports TB_ERR_TIMEOUT."""
     _check("tb_layernorm_bwd_selftest_timeout",
            lib.tb_layernorm_bwd_selftest_timeout(int(wait_limit_ns), _stream(stream)))
+
+
+TB_LINEAR_XENT_SELFTEST_LAUNCHES = 11
+
+
+def tb_linear_xent_selftest_timeout(wait_limit_ns: int = 2_000_000, stream=None) -> int:
+    """Runs the output layer's product on one pair of CTAs, TB_LINEAR_XENT_SELFTEST_LAUNCHES times with
+    something withheld, so that its bounded waits run out; synchronises. Returns the number of launches
+    that gave up; tb_device_error() then reports TB_ERR_TIMEOUT."""
+    launches = ctypes.c_int(0)
+    _check("tb_linear_xent_selftest_timeout",
+           lib.tb_linear_xent_selftest_timeout(int(wait_limit_ns), ctypes.byref(launches), _stream(stream)))
+    return launches.value
 
 
 # ----------------------------------------------------------------------------- AdamW

@@ -40,8 +40,11 @@
 // dloss / max |dloss|, which is exactly 1 for a mean.  That copy also holds zeros for the rows
 // that take no part, whatever their H is.
 //
-// Every mbarrier wait is bounded (about one second of %globaltimer); on expiry the device
-// error word is set and the CTAs drain what they issued and return.
+// Every mbarrier wait is bounded (about one second of %globaltimer).  On expiry the device error
+// word is set and the warp goes to its end, where the pair's first CTA waits for all boxes and MMAs that
+// either CTA started, however far each had come: at the end of every launch, where it costs nothing, so
+// that nothing has to tell the warps of each other's failures.  tb_linear_xent_selftest_timeout runs
+// that path.
 #include <cuda.h>
 
 #include <algorithm>
@@ -53,6 +56,10 @@ namespace tb {
 namespace {
 
 enum Kind { kLse = 0, kGrad = 1, kDH = 2, kDW = 3 };
+// What the self-test leaves out, so that waits run out: the boxes of the pair's first or second CTA,
+// the word that an accumulator is full, the last word that it is empty again (its barrier counts one
+// arrival more).
+enum Withheld { kNothing = 0, kBoxes0 = 1, kBoxes1 = 2, kFull = 3, kEmpty = 4 };
 
 constexpr int kTile = 256;                   // rows and columns of a CTA pair's tile
 constexpr int kHalf = 128;                   // of which one CTA stages and drains
@@ -154,19 +161,24 @@ __device__ __forceinline__ unsigned long long now_ns() {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
-template <bool Acquire>
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, int* err) {
-    const unsigned long long t0 = now_ns();
+// kEnd: waits at a warp's end, for what the warps that may still be waiting themselves finish.
+enum Waits { kRelaxed, kAcquire, kEnd };
+struct Product;
+__device__ unsigned long long wait_ns(const Product* p);
+__device__ int* error_word(const Product* p);
+template <int How>
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const Product* p) {
+    const unsigned long long t0 = now_ns(), limit = How == kEnd ? 4 * kWaitLimitNs : wait_ns(p);
     for (uint32_t it = 1; it < (1u << 30); ++it) {
-        if (mbar_try<Acquire>(bar, parity)) return true;
-        if ((it & 63u) == 0 && now_ns() - t0 > kWaitLimitNs) break;
+        if (mbar_try<How != kRelaxed>(bar, parity)) return true;
+        if ((it & 63u) == 0 && now_ns() - t0 > limit) break;
     }
-    atomicExch(err, (int)TB_ERR_TIMEOUT);
+    atomicExch(error_word(p), (int)TB_ERR_TIMEOUT);
     return false;
 }
-template <bool Acquire = true>
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* err) {
-    return mbar_try<Acquire>(bar, parity) || mbar_wait_slow<Acquire>(bar, parity, err);
+template <int How = kAcquire>
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Product* p) {
+    return mbar_try<How != kRelaxed>(bar, parity) || mbar_wait_slow<How>(bar, parity, p);
 }
 // A box of `map` at column x (a multiple of 64), row y into this CTA's shared memory,
 // counted on the mbarrier of the pair's first CTA.
@@ -301,6 +313,8 @@ struct Product {
     int out_map;              // results go out by TMA (16-byte aligned rows), else element by element
     int b_base;               // kGrad, kDH: first vocabulary row of the piece
     int* err;
+    unsigned long long wait_ns;   // bound of every wait
+    int withhold;             // self-test: a Withheld
     // kLse, kGrad
     const int64_t* target;    // of this launch's rows
     int64_t ignore;
@@ -317,6 +331,9 @@ struct Product {
     void* out;                // [rows][cols] 16-bit
     Weigh weigh;              // kGrad
 };
+
+__device__ __forceinline__ unsigned long long wait_ns(const Product* p) { return p->wait_ns; }
+__device__ __forceinline__ int* error_word(const Product* p) { return p->err; }
 
 // fp16's G is held times 2^14, so that probabilities down to 2^-38 stay above its last step;
 // the products undo it in fp32.  bf16 has fp32's range.
@@ -588,7 +605,8 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     uint64_t* bars = reinterpret_cast<uint64_t*>(outbox + kOutboxes * kOutBytes);
     const uint32_t stage0 = smem_addr(smem), bar0 = smem_addr(bars);
     const uint32_t full = bar0, empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
-                   acc_empty = acc_full + 16, drain = acc_empty + 16, slot = drain + 8;
+                   acc_empty = acc_full + 16, drain = acc_empty + 16, done = drain + 8, issued = done + 8,
+                   slot = issued + 4;
     // (the shuffle tells the compiler that a warp agrees on its number)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
@@ -599,10 +617,11 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(acc_full + 8 * i, 1);
-            mbar_init(acc_empty + 8 * i, 2 * Epi);    // of both CTAs
+            mbar_init(acc_full + 8 * i, p.withhold == kFull ? 2 : 1);
+            mbar_init(acc_empty + 8 * i, 2 * Epi + (p.withhold == kEmpty));    // of both CTAs
         }
         mbar_init(drain, 1);
+        mbar_init(done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) {
@@ -627,14 +646,13 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const uint32_t leader_full = map_to(full, 0);
         const uint32_t a_bytes = (kAMn || p.a_rows == kHalf ? 2 * kHalf : p.a_rows) * kStageK * 2;
         const uint32_t stage_bytes = a_bytes + p.width * kStageK * 2;      // of both CTAs
-        int it = 0, failed = 0;
+        int it = 0;
         Feed<K> feed(p, &map_a, &map_b, (int)rank, pair, pairs, tiles);
+        if (p.withhold == kBoxes0 + (int)rank) feed.t = tiles;
         for (; feed.more(); feed.next(), ++it) {
             const int s = it % kStages;
-            if (it >= kStages && !__all_sync(0xffffffffu, mbar_wait(empty + 8 * s, (it / kStages - 1) & 1, p.err))) {
-                failed = 1;
+            if (it >= kStages && !__all_sync(0xffffffffu, mbar_wait(empty + 8 * s, (it / kStages - 1) & 1, &p)))
                 break;
-            }
             const uint32_t at = stage0 + s * kStageBytes, bar = leader_full + 8 * s;
             if (elect_one()) {
                 if (rank == 0) mbar_expect(full + 8 * s, stage_bytes);
@@ -644,9 +662,34 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             }
             if (feed.k + 1 == feed.k_hi) feed.look(feed.t + pairs);
         }
-        if (failed && rank == 0)      // what both CTAs issued ends on these barriers
-            for (int q = max(0, it - kStages); q < it; ++q)
-                mbar_wait(full + 8 * (q % kStages), (q / kStages) & 1, p.err);
+        // The way out: first the MMAs, which the first CTA issues, and the word of them, which goes to both.
+        // Then the boxes, which end on the first CTA's barriers.  Stages that both CTAs issued complete by
+        // themselves.  After a wait that gave up one may have issued stages, at most a ring of them, that the
+        // other has not: such a phase counts the second CTA's boxes, which never come, or lacks the first
+        // CTA's arrival.  Both are made good (no MMA waits for them any more), so that every phase ends with
+        // its last box.
+        if (rank == 1 && elect_one())
+            asm volatile("st.shared::cluster.u32 [%0], %1;\n\t"
+                         "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%2];" ::"r"(map_to(issued, 0)),
+                         "r"(it), "r"(map_to(done, 0))
+                         : "memory");
+        __syncwarp();
+        const bool ended = __all_sync(0xffffffffu, mbar_wait<kEnd>(drain, 0, &p));
+        if (rank == 0 && ended && __all_sync(0xffffffffu, mbar_wait<kEnd>(done, 0, &p))) {
+            const int peer = *reinterpret_cast<volatile int*>(smem + (issued - stage0));
+            const uint32_t bytes1 = ((kAMn || p.a_rows == kHalf ? kHalf : 0) + p.width / 2) * kStageK * 2;
+            if (it != peer && elect_one())
+                for (int q = min(it, peer); q < max(it, peer); ++q) {
+                    const uint32_t bar = full + 8 * (q % kStages);
+                    if (q < it)
+                        asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes1)
+                                     : "memory");
+                    else mbar_expect(bar, bytes1);
+                }
+            __syncwarp();
+            for (int q = max(0, max(it, peer) - kStages); q < max(it, peer); ++q)
+                mbar_wait<kEnd>(full + 8 * (q % kStages), (q / kStages) & 1, &p);
+        }
     } else if (warp == 1) {
         if (rank == 0) {
             // The whole warp walks the stages and one lane issues: the operands of an MMA are uniform
@@ -667,7 +710,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 int k_lo, k_hi;
                 stages_of(p, p.splits > 1 ? t / (p.m_tiles * p.n_tiles) : 0, &k_lo, &k_hi);
                 const int buf = n & 1;
-                if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait<false>(acc_empty + 8 * buf, (n / 2 - 1) & 1, p.err))) {
+                if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait<kRelaxed>(acc_empty + 8 * buf, (n / 2 - 1) & 1, &p))) {
                     ok = false;
                     break;
                 }
@@ -675,7 +718,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 const uint32_t d = tmem + buf * kTile;
                 uint32_t accumulate = 0;
                 for (int k = k_lo; k < k_hi; ++k) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * s, parity, p.err))) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * s, parity, &p))) {
                         ok = false;
                         break;
                     }
@@ -692,10 +735,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 }
                 if (ok && elect_one()) mma_commit(acc_full + 8 * buf);
             }
-            if (!ok) {
-                if (elect_one()) mma_commit(drain);
-                mbar_wait(drain, 0, p.err);
-            }
+            if (elect_one()) mma_commit(drain);
         }
     } else if (K == kGrad && (warp == 2 || warp == 3)) {
         if (p.weigh.weight) weigh_rows<Fmt, Epi>(p, lane, blockIdx.x * 2 + (warp & 1), gridDim.x * 2, tops);
@@ -737,7 +777,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             const int share = (all + 32 * kParts - 1) / (32 * kParts) * 32;
             const int c0 = part_no * share, width = min(all, c0 + share);
             const uint32_t acc = tmem + buf * kTile + ((uint32_t)(quad * 32) << 16);
-            if (!__all_sync(0xffffffffu, mbar_wait<false>(acc_full + 8 * buf, (n / 2) & 1, p.err))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait<kRelaxed>(acc_full + 8 * buf, (n / 2) & 1, &p))) break;
             tmem_fence_after();
             ahead = look(t + pairs);
             int hit = -1;                             // the target's column in this tile
@@ -1083,10 +1123,11 @@ bool make_sums_map(CUtensorMap* map, float* p, int64_t splits, int64_t rows, int
 }
 
 template <class Fmt, int K, int Epi = kFewWarps>
-tb_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, const Product& p,
-                         cudaStream_t st) {
+tb_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, Product p, cudaStream_t st,
+                         int most_pairs = 1 << 20) {
+    if (!p.wait_ns) p.wait_ns = kWaitLimitNs;
     const void* kernel = reinterpret_cast<const void*>(&product_kernel<Fmt, K, Epi>);
-    const int pairs = resident_clusters(kernel, kThreadsOf(Epi), kSmem, 2);
+    const int pairs = std::min(most_pairs, resident_clusters(kernel, kThreadsOf(Epi), kSmem, 2));
     if (pairs < 1) return TB_ERR_CUDA;
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles * p.splits;
     // (pairs without a tile still take their share of weigh_rows)
@@ -1399,8 +1440,70 @@ tb_status run_grad(const Problem& q, const Cut& c) {
     return launch_status();
 }
 
+// One pair of CTAs over rows x vocab logits of d elements with something withheld; sets *gave_up to
+// whether a wait ran out.
+tb_status run_withheld(int64_t rows, int64_t d, int64_t vocab, int withheld, int64_t wait_limit_ns, unsigned char* mem,
+                       int* err, cudaStream_t st, bool* gave_up) {
+    Product p{};
+    p.m_tiles = (int)ceil_div(rows, kTile), p.n_tiles = (int)ceil_div(vocab, kTile), p.splits = 1;
+    p.k_stages = (int)ceil_div(d, kStageK);
+    p.rows = (int)rows, p.cols = p.vocab = (int)vocab;
+    p.width = kTile, p.a_rows = box_rows(rows);
+    p.err = err, p.wait_ns = (unsigned long long)wait_limit_ns, p.withhold = withheld;
+    auto take = [&](int64_t bytes) {
+        unsigned char* at = mem;
+        mem += round_up(bytes, 256);
+        return at;
+    };
+    const void* H = take(rows * d * 2);
+    const void* W = take(vocab * d * 2);
+    p.target = reinterpret_cast<const int64_t*>(take(rows * 8));
+    p.target_logit = reinterpret_cast<float*>(take(rows * 4));
+    p.part = reinterpret_cast<float2*>(take(rows * (kFewWarps / 4) * p.n_tiles * (int64_t)sizeof(float2)));
+    CUtensorMap a, b;
+    if (!make_map(&a, H, rows, d, d, p.a_rows, true) || !make_map(&b, W, vocab, d, d, p.width / 2, true)) return TB_ERR_CUDA;
+    int word = 0;
+    if (cudaMemcpyAsync(err, &word, sizeof(int), cudaMemcpyHostToDevice, st) != cudaSuccess) return TB_ERR_CUDA;
+    const tb_status s = launch_product<BF16, kLse>(a, b, a, p, st, 1);
+    if (s != TB_OK) return s;
+    if (cudaMemcpyAsync(&word, err, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return TB_ERR_CUDA;
+    *gave_up = word == (int)TB_ERR_TIMEOUT;
+    return TB_OK;
+}
+
 }  // namespace
 }  // namespace tb
+
+extern "C" tb_status tb_linear_xent_selftest_timeout(int64_t wait_limit_ns, int* launches, void* stream) {
+    using namespace tb;
+    if (!launches || wait_limit_ns < 1000 || wait_limit_ns > (int64_t)kWaitLimitNs) return TB_ERR_INVALID_VALUE;
+    *launches = 0;
+    int* err = device_error_word();
+    if (!err) return TB_ERR_CUDA;
+    // more stages than the ring has, over four tiles; all stages in the ring; a result in the pair's first
+    // CTA alone
+    constexpr int64_t kSizes[3][3] = {{256, 512, 1024}, {256, 128, 256}, {40, 320, 1024}};
+    constexpr size_t kBytes = 2 << 20;       // the first needs 1.4 MB
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    void* mem = nullptr;
+    if (cudaMalloc(&mem, kBytes) != cudaSuccess) {
+        cudaGetLastError();
+        return TB_ERR_OOM;
+    }
+    tb_status s = cudaMemsetAsync(mem, 0, kBytes, st) == cudaSuccess ? TB_OK : TB_ERR_CUDA;
+    for (const auto& n : kSizes)
+        for (int what = kBoxes0; what <= kEmpty && s == TB_OK; ++what) {
+            if (what == kEmpty && n[2] <= 2 * kTile) continue;     // nothing waits for a third accumulator
+            bool gave_up = false;
+            s = run_withheld(n[0], n[1], n[2], what, wait_limit_ns, static_cast<unsigned char*>(mem), err, st, &gave_up);
+            if (s == TB_OK && gave_up) ++*launches;
+        }
+    if (cudaStreamSynchronize(st) != cudaSuccess) s = TB_ERR_CUDA;
+    if (cudaFree(mem) != cudaSuccess) s = TB_ERR_CUDA;
+    return s;
+}
 
 extern "C" tb_status tb_linear_xent_workspace_size(int64_t rows, int64_t D, int64_t vocab, tb_dtype dtype,
                                                    size_t* bytes) {
