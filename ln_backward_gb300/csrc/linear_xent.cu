@@ -28,7 +28,8 @@
 //
 // The accumulators are fp32, but tensor cores cut off what an addition shifts below the sum's
 // last place, where fp32 arithmetic rounds: at D = 4,096 a logit comes out smaller by 4e-6 of
-// itself (fp32: 7e-7 either way), and the losses, of 7.7 in the mean square, are off by 1.4e-5.
+// itself (fp32: 7e-7 either way), and the losses, of 7.7 in the mean square, are off by 1.4e-5.  An
+// accumulator of dH or dW takes at most kChain elements.
 //
 // The operands need no transposed copies: dH contracts over the vocabulary, along which W
 // is not contiguous, and dW over the tokens, along which neither G nor H is; those operands
@@ -371,7 +372,7 @@ __device__ __forceinline__ void tile_at(const Product& p, unsigned t, int* split
 __device__ __forceinline__ void stages_of(const Product& p, int split, int* lo, int* hi) {
     *lo = 0;
     *hi = p.k_stages;
-    if (p.splits > 1) {           // (a split a pair of at most 2^24 / 64 stages: no overflow)
+    if (p.splits > 1) {           // (at most 256 splits of 2^24 / 64 stages: no overflow)
         *lo = (int)((unsigned)split * p.k_stages / (unsigned)p.splits);
         *hi = (int)((unsigned)(split + 1) * p.k_stages / (unsigned)p.splits);
     }
@@ -1156,11 +1157,17 @@ struct Cut {
 // machine when its tiles do not.  The result has n x d elements.  The cost counts in stages (64 contracted elements of a tile, about 0.3 us): waves of
 // tiles, about eight more for each one's epilogue, and for the sums that the splits leave a launch and
 // their bytes.  (fp16 1,021 x 768 against 50,257: six splits, 160 us; none, 314 us.)
+// And as many as keep what one accumulator takes below kChain contracted elements: what its truncated
+// additions cut off a sum of one sign grows with them, 1e-9 of the sum an element, 6e-5 at kChain, an
+// eighth of fp16's half step (1,048,576 rows in one accumulator: two half steps). The splits are added
+// in fp32.
+constexpr int64_t kChain = 65536;
 int pick_splits(int64_t n, int64_t d, int64_t k_stages, int64_t pairs) {
     const int64_t tiles = ceil_div(n, kTile) * ceil_div(d, kTile);
-    int best = 1;
+    const int64_t fewest = ceil_div(k_stages, kChain / kStageK);
+    int best = (int)fewest;
     double least = 1e30;
-    for (int64_t s = 1; s <= std::min<int64_t>(pairs, k_stages); ++s) {
+    for (int64_t s = fewest; s <= std::max(fewest, std::min<int64_t>(pairs, k_stages)); ++s) {
         const double cost = (double)ceil_div(tiles * s, pairs) * ((double)ceil_div(k_stages, s) + 8.0) +
                             (s > 1 ? 12.0 + (double)s * (0.05 + (double)(n * d) / 450000.0) : 0.0);
         if (cost < least * 0.97) least = cost, best = (int)s;

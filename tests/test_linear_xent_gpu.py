@@ -13,6 +13,8 @@ Bounds, with u = 2^-24 and the products of 16-bit values exact in fp32:
 
 and one rounding of every 16-bit result.
 """
+import math
+
 import pytest
 import torch
 
@@ -420,3 +422,22 @@ def test_rows_whose_logits_are_all_far_from_zero(tb, dtype, values):
         half = torch.finfo(dtype).eps / 2
         assert ((dH.double() - want).abs() <= size * (half + 2.0 ** -17) + 2.0 ** -25)[:, 1:].all(), value
         assert dW.isfinite().all()
+
+
+def test_a_million_rows_of_one_sign(tb):
+    """dW's sums over the rows: equal terms whose sum fp16 holds exactly. A tensor core's accumulator
+    that takes all of them cuts off 1e-9 of the sum for every element, 1e-3 here, two half steps of
+    fp16; the tiles are as many as the pairs of CTAs, so that nothing else splits the rows."""
+    n, d, v = 1 << 20, 19 * 256, 1000
+    H = torch.ones(n, d, dtype=HF, device="cuda")
+    W = torch.zeros(v, d, dtype=HF, device="cuda")
+    t = torch.zeros(n, dtype=torch.int64, device="cuda")
+    lse = torch.full((n,), math.log(v), device="cuda")
+    dloss = torch.full((n,), 1.0 / n, device="cuda")
+    _, dW = backward(tb, dloss, H, W, t, lse, "W")
+    # G = 2^14 / 1000 = 16.384 is held as 1049 / 64, a tenth of a step away and far from a tie
+    want = torch.full((v,), 1049 / 64 / 2 ** 14, dtype=HF, device="cuda")
+    assert want[1].item() == 1049 / 64 / 2 ** 14
+    assert torch.equal(dW[1:], want[1:, None].expand(v - 1, d))
+    # the target's: (1049 / 64 - 16384) / 2^14 rounded, in G to a step of 8 and in dW likewise
+    assert ((dW[0].double() + 1 - 1 / v).abs() <= 2.0 ** -10).all()
