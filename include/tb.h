@@ -641,7 +641,8 @@ tb_status tb_qk_norm_rope_bwd(const tb_heads* dq_out, const tb_heads* dk_out,
  * dloss of 0 takes no part in the gradient either.  A logit of +inf gives lse = +inf.
  *
  * tb_linear_xent
- *   H, W             device [rows, D] and [vocab, D], TB_BF16 or TB_F16, 16-byte aligned
+ *   H, W             device [rows, D] and [vocab, D], TB_BF16 or TB_F16, 16-byte aligned; 2-byte
+ *                    where D is not a multiple of 8 (rows of such a matrix start on any element)
  *   targets          device int64 [rows]
  *   loss, lse        out: fp32 [rows]
  *   ignore_index     any value; -100 is usual

@@ -1024,7 +1024,8 @@ join_splits_kernel(const float* sums, int splits, int64_t n, int cols, const flo
 }
 
 // Rows padded with zeros.  A thread writes one 16-byte vector; what it reads starts on any element,
-// so it loads the words around it (inside the matrix) and shifts.
+// so it loads the words around it and shifts.  The matrix itself may start on any element: of the words
+// at its two ends, only the half that is inside is read.
 struct Pad {
     const void* in[2];        // H, W
     void* out[2];
@@ -1043,18 +1044,21 @@ __global__ void __launch_bounds__(256) pad_kernel(const __grid_constant__ Pad p)
     const int64_t rows = p.rows[which];
     const int cols = p.cols;
     const unsigned per_row = (unsigned)p.ld / 8;
-    const int64_t total = rows * cols;
+    const bool odd = reinterpret_cast<uintptr_t>(in) & 2;    // the matrix starts in the middle of a word
+    const uint16_t* elements = static_cast<const uint16_t*>(in);
+    const unsigned* w = reinterpret_cast<const unsigned*>(elements - odd);
+    const int64_t end = rows * cols + odd, words = end >> 1;  // whole words up to the matrix's end
     const int64_t row0 = (int64_t)(blockIdx.x - (which ? p.ctas : 0)) * pad_rows_a_cta(p.ld);
     const int64_t rows_here = min(rows - row0, pad_rows_a_cta(p.ld));
     for (unsigned i = threadIdx.x; i < (unsigned)rows_here * per_row; i += 256) {
         const unsigned r = i / per_row, c = (i - r * per_row) * 8;
-        const int64_t at = (row0 + r) * cols + c, word = at >> 1;
-        const int64_t words = total >> 1;        // whole words of the matrix
-        const unsigned* w = reinterpret_cast<const unsigned*>(in);
+        const int64_t at = (row0 + r) * cols + c + odd, word = at >> 1;
         unsigned x[5];
 #pragma unroll
-        for (int k = 0; k < 5; ++k)
-            x[k] = word + k < words ? w[word + k] : word + k == words && (total & 1) ? static_cast<const uint16_t*>(in)[total - 1] : 0u;
+        for (int k = 0; k < 5; ++k) {
+            if (odd && word + k == 0) x[k] = (unsigned)elements[0] << 16;
+            else x[k] = word + k < words ? w[word + k] : word + k == words && (end & 1) ? elements[end - 1 - odd] : 0u;
+        }
         if (at & 1) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[k] = __funnelshift_r(x[k], x[k + 1], 16);
@@ -1239,6 +1243,9 @@ Cut cut_call(int64_t n, int64_t d, int64_t v, bool bwd, int sms) {
 // boxes hold those rows and the second CTA loads none.  What the MMAs read in their place is what the
 // memory held; it reaches only rows that nothing stores.
 int box_rows(int64_t rows) { return rows < kHalf ? (int)round_up(rows, 8) : kHalf; }
+
+// What TMA reads starts on 16 bytes; where it reads a padded copy, the copy does.
+uintptr_t operand_alignment(int64_t d) { return d % 8 ? 2 : 16; }
 
 // A tile's MMAs take 0.3 to 0.7 us for 64 contracted elements, and the epilogue waits for a whole
 // tile: 2^24 of them stay well inside the wait limit.
@@ -1531,7 +1538,7 @@ extern "C" tb_status tb_linear_xent(const void* H, const void* W, const int64_t*
     if (s != TB_OK) return s;
     if (rows == 0) return TB_OK;
     if (!H || !W || !targets || !loss || !lse) return TB_ERR_INVALID_VALUE;
-    if (!aligned_to(H, 16) || !aligned_to(W, 16) || !aligned_to(targets, 8) || !aligned_to(loss, 4) ||
+    if (!aligned_to(H, operand_alignment(D)) || !aligned_to(W, operand_alignment(D)) || !aligned_to(targets, 8) || !aligned_to(loss, 4) ||
         !aligned_to(lse, 4))
         return TB_ERR_MISALIGNED;
     const Range in[3] = {range_of(H, rows * D, 2), range_of(W, vocab * D, 2), range_of(targets, rows, 8)};
@@ -1577,7 +1584,7 @@ extern "C" tb_status tb_linear_xent_bwd(const float* dloss, const void* H, const
         return TB_OK;
     }
     if (!dloss || !H || !W || !targets || !lse) return TB_ERR_INVALID_VALUE;
-    if (!aligned_to(H, 16) || !aligned_to(W, 16) || !aligned_to(targets, 8) || !aligned_to(dloss, 4) ||
+    if (!aligned_to(H, operand_alignment(D)) || !aligned_to(W, operand_alignment(D)) || !aligned_to(targets, 8) || !aligned_to(dloss, 4) ||
         !aligned_to(lse, 4) || !aligned_to(dH, 2) || !aligned_to(dW, 2))
         return TB_ERR_MISALIGNED;
     const Range in[5] = {range_of(H, rows * D, 2), range_of(W, vocab * D, 2), range_of(targets, rows, 8),

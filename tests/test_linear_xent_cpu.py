@@ -93,3 +93,12 @@ def test_binding_refusals(tb):
         tb.tb_linear_xent_bwd(f, H, W, t, f, None, W.float(), None)
     with pytest.raises(ValueError, match="CUDA"):
         tb.tb_linear_xent(H, W, t, f, f.clone(), None)
+
+
+@pytest.mark.parametrize("how, refused", [(dict(H=0x1000002, d=63), False), (dict(W=0x2000006, d=65), False),
+                                          (dict(H=0x1000001, d=63), True), (dict(W=0x2000003, d=63), True),
+                                          (dict(H=0x1000002, d=72), True), (dict(W=0x2000008, d=8), True)])
+def test_alignment_of_the_operands(tb, how, refused):
+    """16 bytes where the matrices are read as they are, an element where a padded copy is."""
+    for call in (fwd, bwd):
+        assert (call(tb, **how) == MISALIGNED) == refused

@@ -441,3 +441,22 @@ def test_a_million_rows_of_one_sign(tb):
     assert torch.equal(dW[1:], want[1:, None].expand(v - 1, d))
     # the target's: (1049 / 64 - 16384) / 2^14 rounded, in G to a step of 8 and in dW likewise
     assert ((dW[0].double() + 1 - 1 / v).abs() <= 2.0 ** -10).all()
+
+
+# rows of a matrix whose D is not a multiple of 8 start on any element, and so does a slice of them
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("n, d, v", [(1, 1, 1), (3, 1, 2), (37, 7, 300), (130, 33, 515), (41, 770, 1003), (5, 12, 9)])
+@pytest.mark.parametrize("off_h, off_w", [(1, 0), (0, 1), (3, 6), (2, 5)])
+def test_operands_that_start_on_any_element(tb, n, d, v, off_h, off_w, dtype):
+    H, W, t, dloss = problem(n, d, v, dtype, 15)
+    loss, lse = forward(tb, H, W, t)
+    dH, dW = backward(tb, dloss, H, W, t, lse)
+    moved = []
+    for x, off in ((H, off_h), (W, off_w)):         # between NaNs, so that nothing else can be read unseen
+        buf = torch.full((x.numel() + off + 9,), float("nan"), dtype=dtype, device="cuda")
+        buf[off:off + x.numel()] = x.flatten()
+        moved.append(buf[off:off + x.numel()].view_as(x))
+    got = forward(tb, *moved, t)
+    assert torch.equal(got[0], loss) and torch.equal(got[1], lse)
+    dH2, dW2 = backward(tb, dloss, *moved, t, lse)
+    assert torch.equal(dH2, dH) and torch.equal(dW2, dW)
