@@ -272,3 +272,27 @@ def test_binding_refusals(tb):
         tb.tb_rope(q, k, q, k, fr)
     with pytest.raises(ValueError, match="CUDA"):
         tb.tb_qk_norm_rope(q, k, torch.ones(64), torch.ones(64), q, k)
+
+
+# pi to 60 places (public constant), for angles formed apart from the library's binary fractions
+PI = "3.14159265358979323846264338327950288419716939937510582097494"
+
+
+@pytest.mark.parametrize("rot, base", [(64, 10000), (128, 500000), (6, 100)])
+def test_far_positions_against_long_decimals(tb, rot, base):
+    """The angle of a far position, as the kernels form it from the table, against one formed in 60
+    decimal places from base^(-2i/rot) itself."""
+    from decimal import Decimal, localcontext
+    with localcontext() as ctx:
+        ctx.prec = 60
+        table, _ = tb.tb_rope_freqs(rot, float(base), device="cpu")
+        for pos in (1, 131071, 2 ** 31 + 3, -131071, 2 ** 40 + 1):
+            for i, entry in enumerate(table.tolist()):
+                phase = (pos * entry) & ((1 << 64) - 1)              # what 64-bit arithmetic leaves
+                got = Decimal(phase) / Decimal(1 << 64)              # of a turn
+                w = Decimal(base) ** (Decimal(-2 * i) / rot) / (2 * Decimal(PI))
+                want = w * pos % 1
+                off = abs(got - want) % 1
+                off = min(off, 1 - off)
+                # the table: pow and a product or two in double, then half of 2^-64 a position
+                assert off <= abs(pos) * (w * 4 * Decimal(2) ** -53 + Decimal(2) ** -65)
