@@ -460,3 +460,24 @@ def test_operands_that_start_on_any_element(tb, n, d, v, off_h, off_w, dtype):
     assert torch.equal(got[0], loss) and torch.equal(got[1], lse)
     dH2, dW2 = backward(tb, dloss, *moved, t, lse)
     assert torch.equal(dH2, dH) and torch.equal(dW2, dW)
+
+
+@pytest.mark.parametrize("n, d, v", [(300, 136, 900), (5000, 40, 600)])
+@pytest.mark.parametrize("dtype, powers", [(BF, 16), (BF, 90), (HF, 10), (HF, 24)])
+def test_row_weights_of_many_sizes(tb, n, d, v, dtype, powers):
+    """Signed weights spread over powers of two, some rows far below the largest: dH keeps its accuracy
+    for every row; dW is off by a rounding of H times the weight over the largest, which fp16 holds to
+    half a step of 2^-24 where that is small."""
+    H, W, t, dloss = problem(n, d, v, dtype, 16)
+    g = torch.Generator(device="cuda").manual_seed(17)
+    dloss = torch.exp2(-powers * torch.rand(n, generator=g, device="cuda")) * (torch.randint(0, 2, (n,), generator=g, device="cuda") * 2 - 1)
+    dloss[7] = 64.0
+    _, lse = forward(tb, H, W, t)
+    dH, dW = backward(tb, dloss, H, W, t, lse)
+    check_backward(dH, dW, dloss, H, W, t, lse)
+    # every weight times a power of two moves nothing but the exponent, where the type has room
+    if dtype == BF:
+        dH2, dW2 = backward(tb, dloss * 2.0 ** -20, H, W, t, lse)
+        big = dH.abs() > 2.0 ** -80
+        assert torch.equal(dH2[big], (dH.float() * 2.0 ** -20).to(BF)[big])
+        assert torch.equal(dW2, (dW.float() * 2.0 ** -20).to(BF))
