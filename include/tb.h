@@ -656,8 +656,9 @@ tb_status tb_qk_norm_rope_bwd(const tb_heads* dq_out, const tb_heads* dk_out,
  *   dH, dW           out: [rows, D] and [vocab, D] in dtype, overwritten; either may be
  *                    NULL when it is not wanted
  * Sums are fp32, in the tensor cores' accumulators, which truncate: a sum of n terms of one sign
- * comes out smaller by about 1e-9 n of itself, where n is D in a logit and at most 65,536 in dH and
- * dW (longer sums are added from such parts).  Results are bitwise reproducible on one device
+ * comes out smaller by about 1e-9 n of itself, where n is at most 1,280 in the loss's logits and
+ * 65,536 in dH and dW (longer sums are added from such parts), and D in the logits that the
+ * gradient forms again for G, whose own rounding is far above that.  Results are bitwise reproducible on one device
  * model.  Two values are
  * rounded to dtype on the way: G, and for dW the rows of H times dloss / max |dloss| (exact
  * where every dloss is the same, as for a mean).  TB_F16 holds G times 2^14, so that

@@ -27,9 +27,9 @@
 // against the same weights, loss, 22 us, of which about 13 read W at 6 TB/s.
 //
 // The accumulators are fp32, but tensor cores cut off what an addition shifts below the sum's
-// last place, where fp32 arithmetic rounds: at D = 4,096 a logit comes out smaller by 4e-6 of
-// itself (fp32: 7e-7 either way), and the losses, of 7.7 in the mean square, are off by 1.4e-5.  An
-// accumulator of dH or dW takes at most kChain elements.
+// last place, where fp32 arithmetic rounds: a sum comes out smaller by 1e-9 of itself for every contracted
+// element.  So an accumulator of the loss's logits takes at most 1,280 elements (kChunkStages), one of dH
+// or dW at most kChain, and longer sums are added from those in fp32.
 //
 // The operands need no transposed copies: dH contracts over the vocabulary, along which W
 // is not contiguous, and dW over the tokens, along which neither G nor H is; those operands
@@ -78,6 +78,14 @@ constexpr int kEpiWarp = 4;                  // first of the epilogue warps
 constexpr int kFewWarps = 8, kManyWarps = 16;
 constexpr int kShortStages = 384 / kStageK;
 constexpr int kThreadsOf(int epi) { return (kEpiWarp + epi) * 32; }
+// Contracted elements that one accumulator of the loss's logits takes, at most: what truncation cuts off
+// grows with them.  More come in equal chunks, one accumulator after the other, which sixteen epilogue
+// warps add up in fp32 registers (64 columns of a row each).  Losses of 1,024 x 32,000 against 64 bits
+// at 1,024 / 1,536 / 2,048 / 4,096 / 8,192 contracted elements: in one accumulator 0.63 / 0.91 / 1.13 /
+// 1.85 / 2.86e-6 off, in chunks of 1,024 or fewer 0.63 / 0.44 / 0.55 / 0.43 / 0.32e-6 (fp32: 0.22 to
+// 0.56e-6).  It costs what the larger epilogue waits for: 64 x 32,000 x 4,096 52.7 -> 54.0 us, 8,192 x
+// 32,000 x 4,096 1% and below; with 1,024 as the limit 37 x 50,257 x 1,088 27.9 -> 30.7.
+constexpr int kChunkStages = 1280 / kStageK;
 constexpr int kOutCols = 32;
 constexpr int kOutBytes = 32 * kOutCols * 2; // what an epilogue warp stores at once: 32 rows
 constexpr int kOutboxes = 16;                // one or two for each epilogue warp
@@ -248,6 +256,16 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
         :
         : "memory");
 }
+// 16 columns, there when it returns.
+__device__ __forceinline__ void tmem_read16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
 // A box of 32 rows by 32 columns from shared memory to `map` at column x, row y; what lies outside
 // the matrix is dropped.
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, uint32_t src) {
@@ -309,6 +327,7 @@ struct Weigh {
 struct Product {
     int m_tiles, n_tiles, splits, k_stages;
     int rows, cols;           // of the result
+    int chunk;                // kLse: stages of an accumulator, where a tile has more
     int width;                // columns of a tile: at most kTile, fewer where that fills the last wave
     int a_rows;               // K-major A: rows of a box, fewer than kHalf where the result has no more
     int out_map;              // results go out by TMA (16-byte aligned rows), else element by element
@@ -590,8 +609,49 @@ __device__ __forceinline__ void fold(float& m, float& s, float m2, float s2, flo
     s = x + y;
 }
 
+// Folds columns c .. c + 31 of a tile into a row's maximum and sum; `hit`, the target's column or -1,
+// leaves its logit.
+__device__ __forceinline__ void fold_logits(float (&v)[32], int c, int width, int hit, float* target_logit, float& m,
+                                            float& s) {
+                        if ((hit & ~31) == c) {           // (hit = -1: no chunk)
+                            float x = v[0];
+    #pragma unroll
+                            for (int i = 1; i < 32; ++i) x = c + i == hit ? v[i] : x;
+                            *target_logit = x;
+                        }
+                        if (c + 32 > width) {
+    #pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c + i >= width) v[i] = __int_as_float(0xff800000);
+                        }
+                        // four chains each: one of 31 maxima and one of 32 sums take longer than the
+                        // exponentials
+                        float top4[4] = {v[0], v[1], v[2], v[3]};
+    #pragma unroll
+                        for (int i = 4; i < 32; ++i) top4[i & 3] = fmaxf(top4[i & 3], v[i]);
+                        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+                        // (finite: a column behind the vocabulary's end is -inf)
+                        const float base = base_of(top), at = fmaxf(base * kLog2e, -3.4028235e38f),
+                                    off = __fmaf_rn(base, kLog2e, -at);
+                        const unsigned long long b2 = pair_of(-at, -at), scale = pair_of(kLog2e, kLog2e);
+                        unsigned long long sum[4] = {0, 0, 0, 0};
+    #pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float lo, hi;
+                            split_pair(fma_pair(pair_of(v[2 * i], v[2 * i + 1]), scale, b2), lo, hi);
+                            sum[i & 3] = add_pair(sum[i & 3], pair_of(exp2_fast(lo), exp2_fast(hi)));
+                        }
+                        float part, part2;
+                        split_pair(add_pair(add_pair(sum[0], sum[1]), add_pair(sum[2], sum[3])), part, part2);
+                        part += part2;
+                        const bool alone = fabsf(base) > kAlone;
+                        if (alone && part == part) part = 1.f;
+                        fold(m, s, top, part, alone ? 0.f : off);
+}
+
 // ---------------------------------------------------------------- the product
-template <class Fmt, int K, int Epi>
+// Long: kLse of tiles that have more stages than an accumulator takes.
+template <class Fmt, int K, int Epi, bool Long>
 __global__ void __launch_bounds__(kThreadsOf(Epi), 1)
 product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                const __grid_constant__ CUtensorMap map_out, const __grid_constant__ Product p) {
@@ -707,39 +767,94 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             uint32_t s = 0, parity = 0;
             int n = 0;
             bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs, ++n) {
-                int k_lo, k_hi;
-                stages_of(p, p.splits > 1 ? t / (p.m_tiles * p.n_tiles) : 0, &k_lo, &k_hi);
-                const int buf = n & 1;
-                if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait<kRelaxed>(acc_empty + 8 * buf, (n / 2 - 1) & 1, &p))) {
-                    ok = false;
-                    break;
-                }
-                tmem_fence_after();
-                const uint32_t d = tmem + buf * kTile;
-                uint32_t accumulate = 0;
-                for (int k = k_lo; k < k_hi; ++k) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * s, parity, &p))) {
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                int k, k_hi;
+                stages_of(p, p.splits > 1 ? t / (p.m_tiles * p.n_tiles) : 0, &k, &k_hi);
+                do {                  // (one accumulator, unless Long)
+                    const int buf = n & 1, end = Long ? min(k_hi, k + p.chunk) : k_hi;
+                    if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait<kRelaxed>(acc_empty + 8 * buf, (n / 2 - 1) & 1, &p))) {
                         ok = false;
                         break;
                     }
-                    const uint32_t a = a0 + s * (kStageBytes >> 4), b = b0 + s * (kStageBytes >> 4);
-                    if (elect_one()) {
-                        mma_pair<false>(d, a, b, idesc, accumulate);
+                    tmem_fence_after();
+                    const uint32_t d = tmem + buf * kTile;
+                    uint32_t accumulate = 0;
+                    for (; k < end; ++k) {
+                        if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * s, parity, &p))) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t a = a0 + s * (kStageBytes >> 4), b = b0 + s * (kStageBytes >> 4);
+                        if (elect_one()) {
+                            mma_pair<false>(d, a, b, idesc, accumulate);
 #pragma unroll
-                        for (int j = 1; j < kStageK / 16; ++j)
-                            mma_pair<true>(d, a + j * step_a, b + j * step_b, idesc, 1);
-                        mma_commit(empty + 8 * s);
+                            for (int j = 1; j < kStageK / 16; ++j)
+                                mma_pair<true>(d, a + j * step_a, b + j * step_b, idesc, 1);
+                            mma_commit(empty + 8 * s);
+                        }
+                        accumulate = 1;
+                        if (++s == kStages) s = 0, parity ^= 1;
                     }
-                    accumulate = 1;
-                    if (++s == kStages) s = 0, parity ^= 1;
-                }
-                if (ok && elect_one()) mma_commit(acc_full + 8 * buf);
+                    if (ok && elect_one()) mma_commit(acc_full + 8 * buf);
+                    ++n;
+                } while (Long && ok && k < k_hi);
             }
             if (elect_one()) mma_commit(drain);
         }
     } else if (K == kGrad && (warp == 2 || warp == 3)) {
         if (p.weigh.weight) weigh_rows<Fmt, Epi>(p, lane, blockIdx.x * 2 + (warp & 1), gridDim.x * 2, tops);
+    } else if (Long && warp >= kEpiWarp) {
+        // as below; a tile is long, so its target is there before its logits are
+        const int quad = warp & 3, part_no = (warp - kEpiWarp) >> 2;
+        const uint32_t leader_empty = map_to(acc_empty, 0);
+        int n = 0;
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            int split, mt, nt;
+            tile_at(p, (unsigned)t, &split, &mt, &nt);
+            const int row = mt * kTile + (int)rank * kHalf + quad * 32 + lane;
+            const bool live = row < p.rows;
+            const int64_t target = live ? p.target[row] : p.ignore;
+            const int n0 = nt * p.width, all = min(p.width, p.cols - n0);
+            const int share = (all + 32 * kParts - 1) / (32 * kParts) * 32;      // 32 or 64
+            const int c0 = part_no * share, width = min(all, c0 + share);
+            unsigned long long sum[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[i] = 0;
+            for (int k = 0; k < p.k_stages; k += p.chunk, ++n) {
+                const int buf = n & 1;
+                if (!__all_sync(0xffffffffu, mbar_wait<kRelaxed>(acc_full + 8 * buf, (n / 2) & 1, &p))) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+                const uint32_t acc = tmem + buf * kTile + ((uint32_t)(quad * 32) << 16) + c0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t r[16];
+                    tmem_read16(acc + 16 * j, r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        sum[8 * j + i] = add_pair(sum[8 * j + i], pair_of(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
+                }
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(leader_empty + 8 * buf);
+            }
+            if (!ok) break;
+            const int64_t c = target - n0;
+            const int hit = target != p.ignore && target >= 0 && target < p.vocab && c >= c0 && c < width ? (int)c : -1;
+            float m = __int_as_float(0xff800000), s = 0.f;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (c0 + 32 * g >= width) break;
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) split_pair(sum[16 * g + i], v[2 * i], v[2 * i + 1]);
+                fold_logits(v, c0 + 32 * g, width, hit, p.target_logit + row, m, s);
+            }
+            if (live) p.part[((int64_t)nt * kParts + part_no) * p.rows + row] = make_float2(m, s);
+        }
     } else if (warp >= kEpiWarp) {
         // TMEM lanes 32 quad .. 32 quad + 31 (a warp reaches those of its number modulo 4), and
         // one of the parts of the tile's columns
@@ -803,40 +918,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
                 if constexpr (K == kLse) {
-                    if ((hit & ~31) == c) {           // (hit = -1: no chunk)
-                        float x = v[0];
-#pragma unroll
-                        for (int i = 1; i < 32; ++i) x = c + i == hit ? v[i] : x;
-                        p.target_logit[row] = x;
-                    }
-                    if (c + 32 > width) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i >= width) v[i] = __int_as_float(0xff800000);
-                    }
-                    // four chains each: one of 31 maxima and one of 32 sums take longer than the
-                    // exponentials
-                    float top4[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-                    for (int i = 4; i < 32; ++i) top4[i & 3] = fmaxf(top4[i & 3], v[i]);
-                    const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-                    // (finite: a column behind the vocabulary's end is -inf)
-                    const float base = base_of(top), at = fmaxf(base * kLog2e, -3.4028235e38f),
-                                off = __fmaf_rn(base, kLog2e, -at);
-                    const unsigned long long b2 = pair_of(-at, -at), scale = pair_of(kLog2e, kLog2e);
-                    unsigned long long sum[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float lo, hi;
-                        split_pair(fma_pair(pair_of(v[2 * i], v[2 * i + 1]), scale, b2), lo, hi);
-                        sum[i & 3] = add_pair(sum[i & 3], pair_of(exp2_fast(lo), exp2_fast(hi)));
-                    }
-                    float part, part2;
-                    split_pair(add_pair(add_pair(sum[0], sum[1]), add_pair(sum[2], sum[3])), part, part2);
-                    part += part2;
-                    const bool alone = fabsf(base) > kAlone;
-                    if (alone && part == part) part = 1.f;
-                    fold(m, s, top, part, alone ? 0.f : off);
+                    fold_logits(v, c, width, hit, p.target_logit + row, m, s);
                 } else if constexpr (K == kGrad) {
                     if (far) {
 #pragma unroll
@@ -1127,18 +1209,18 @@ bool make_sums_map(CUtensorMap* map, float* p, int64_t splits, int64_t rows, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class Fmt, int K, int Epi = kFewWarps>
+template <class Fmt, int K, int Epi = kFewWarps, bool Long = false>
 tb_status launch_product(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, Product p, cudaStream_t st,
                          int most_pairs = 1 << 20) {
     if (!p.wait_ns) p.wait_ns = kWaitLimitNs;
-    const void* kernel = reinterpret_cast<const void*>(&product_kernel<Fmt, K, Epi>);
+    const void* kernel = reinterpret_cast<const void*>(&product_kernel<Fmt, K, Epi, Long>);
     const int pairs = std::min(most_pairs, resident_clusters(kernel, kThreadsOf(Epi), kSmem, 2));
     if (pairs < 1) return TB_ERR_CUDA;
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles * p.splits;
     // (pairs without a tile still take their share of weigh_rows)
     const int64_t grid = 2 * (p.weigh.weight ? pairs : std::min<int64_t>(tiles, pairs));
-    if (launch_clusters<true>(product_kernel<Fmt, K, Epi>, dim3((unsigned)grid), dim3(kThreadsOf(Epi)), kSmem, st, 2, a, b,
-                              out, p) != cudaSuccess)
+    if (launch_clusters<true>(product_kernel<Fmt, K, Epi, Long>, dim3((unsigned)grid), dim3(kThreadsOf(Epi)), kSmem, st, 2, a,
+                              b, out, p) != cudaSuccess)
         return TB_ERR_CUDA;
     return launch_status();
 }
@@ -1148,6 +1230,7 @@ struct Cut {
     int lse_width, grad_width;   // columns of a tile of logits
     int64_t lse_tiles;
     int lse_warps, grad_warps;   // of the epilogue of logits
+    bool lse_long;            // logits in several accumulators
     int64_t ld;               // padded row length of H and W (D where no copy is needed)
     bool pad;
     int64_t piece, pieces;    // gradient: columns of a piece of the vocabulary
@@ -1214,7 +1297,8 @@ Cut cut_call(int64_t n, int64_t d, int64_t v, bool bwd, int sms) {
         c.lse_width = pick_width(ceil_div(rows, kTile), v, sms / 2);
         c.lse_tiles = ceil_div(v, c.lse_width);
         const bool many = ceil_div(d, kStageK) <= kShortStages && ceil_div(rows, kTile) * c.lse_tiles > 8 * (sms / 2);
-        c.lse_warps = many ? kManyWarps : kFewWarps;
+        c.lse_long = ceil_div(d, kStageK) > kChunkStages;
+        c.lse_warps = many || c.lse_long ? kManyWarps : kFewWarps;
         c.off_part = take((size_t)rows * (c.lse_warps / 4) * c.lse_tiles * sizeof(float2));
         c.off_logit = take((size_t)rows * sizeof(float));
     } else {
@@ -1326,8 +1410,10 @@ tb_status run_loss(const Problem& q, const Cut& c) {
         p.vocab = (int)q.v;
         p.part = reinterpret_cast<float2*>(q.ws + c.off_part);
         p.target_logit = reinterpret_cast<float*>(q.ws + c.off_logit);
-        const tb_status s = c.lse_warps == kManyWarps ? launch_product<Fmt, kLse, kManyWarps>(a, b, a, p, q.st)
-                                                      : launch_product<Fmt, kLse>(a, b, a, p, q.st);
+        p.chunk = (int)ceil_div(p.k_stages, ceil_div(p.k_stages, kChunkStages));
+        const tb_status s = c.lse_long                  ? launch_product<Fmt, kLse, kManyWarps, true>(a, b, a, p, q.st)
+                            : c.lse_warps == kManyWarps ? launch_product<Fmt, kLse, kManyWarps>(a, b, a, p, q.st)
+                                                        : launch_product<Fmt, kLse>(a, b, a, p, q.st);
         if (s != TB_OK) return s;
         const bool few = rows <= 32 * q.sms;
         const dim3 grid((unsigned)ceil_div(rows, few ? 8 : 32));

@@ -481,3 +481,38 @@ def test_row_weights_of_many_sizes(tb, n, d, v, dtype, powers):
         big = dH.abs() > 2.0 ** -80
         assert torch.equal(dH2[big], (dH.float() * 2.0 ** -20).to(BF)[big])
         assert torch.equal(dW2, (dW.float() * 2.0 ** -20).to(BF))
+
+
+# logits of more contracted elements than one accumulator takes: chunks of equal and of unequal length,
+# one element over, several launches of the loss, tiles narrower than a pair's
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("n, d, v", [(1, 1281, 1), (37, 1288, 700), (300, 2048, 1000), (129, 4100, 515), (513, 1500, 777),
+                                     (17000, 1344, 300), (41, 4096, 20011), (5, 16384, 33), (70, 1280, 300)])
+def test_long_contractions(tb, n, d, v, dtype):
+    H, W, t, dloss = problem(n, d, v, dtype, 18)
+    loss, lse = forward(tb, H, W, t)
+    check_forward(loss, lse, H, W, t)
+    again = forward(tb, H, W, t)
+    assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+    if dtype == HF:
+        dloss = dloss * 1024
+    dH, dW = backward(tb, dloss, H, W, t, lse)
+    check_backward(dH, dW, dloss, H, W, t, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("d", [1024, 1280, 4096, 16384, 65536, 65544])
+def test_logits_whose_terms_have_one_sign(tb, d, dtype):
+    """A chunk of 1,280 elements is 80 additions of 16, each cut off by less than 2^-23 of what the sum
+    has reached, half of the chunk in the mean: 80 * 2^-24 of the logit. At most 52 chunks are added in
+    fp32, off by half of 2^-23 of the sum so far each. In one accumulator, 65,536 elements are off by 6e-5."""
+    n, v = 3, 300
+    H = torch.ones(n, d, dtype=dtype, device="cuda")
+    W = torch.zeros(v, d, dtype=dtype, device="cuda")
+    W[5] = 851.7 / d
+    logit = W[5, 0].double().item() * d
+    t = torch.tensor([5, 0, 299], device="cuda")
+    loss, lse = forward(tb, H, W, t)
+    room = logit * (80 + 52 + 2) * 2.0 ** -24
+    assert ((lse.double() - logit).abs() <= room).all(), (lse.double() - logit).abs().max().item() / logit
+    assert loss[0].abs() <= logit * 2.0 ** -23 and ((loss[1:].double() - logit).abs() <= room).all()
