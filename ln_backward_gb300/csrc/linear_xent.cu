@@ -20,10 +20,11 @@
 //
 // What bounds it: the tensor cores.  A stage's MMAs take 237 ns with operands at hand, 277 ns
 // with them coming from L2 (2.1 GHz, one launch); under continuous load the power limit sets
-// the clock.  bf16 8,192 x 32,000 x 4,096: loss 1,130 us (1,900 TFLOP/s), gradient 3,590 to
-// 3,690 us (1,750 to 1,790 TFLOP/s; a cuBLAS product reaches 1,871 in a burst and 1,707 for
-// seconds).  Short contractions are bound by the epilogue and by the loads' latency: fp16
-// 1,021 x 50,257 x 768, gradient, 157 to 170 us by board (126 us at 1,871 TFLOP/s); bf16 37 rows
+// the clock.  bf16 8,192 x 32,000 x 4,096 over several boards: loss 1,149 to 1,168 us (1,840 to 1,870
+// TFLOP/s), gradient 3,690 to 3,760 us (1,715 to 1,745 TFLOP/s; 3,950 us, 1,631, after a second of nothing
+// else; a cuBLAS product reaches 1,871 in a burst and 1,707 for seconds).  Short contractions are bound by the epilogue, the loads' latency and, below
+// about 450 contracted elements, by G, which is written once and read twice: fp16 1,021 x 50,257 x 768,
+// gradient, 158 to 184 us by run, as the buffers happen to lie (126 us at 1,871 TFLOP/s); bf16 37 rows
 // against the same weights, loss, 22 us, of which about 13 read W at 6 TB/s.
 //
 // The accumulators are fp32, but tensor cores cut off what an addition shifts below the sum's
@@ -39,7 +40,8 @@
 // every entry of G would share (bf16 1/7168 is 0.19% off, and dH and dW were).  dH takes it in
 // fp32 in the epilogue; dW contracts over the rows, so there H is scaled beforehand, by
 // dloss / max |dloss|, which is exactly 1 for a mean.  That copy also holds zeros for the rows
-// that take no part, whatever their H is.
+// that take no part, whatever their H is.  fp16 lets a power of two of small weights travel in G
+// instead (shift_of), where it costs no bits.
 //
 // Every mbarrier wait is bounded (about one second of %globaltimer).  On expiry the device error
 // word is set and the warp goes to its end, where the pair's first CTA waits for all boxes and MMAs that
@@ -362,6 +364,19 @@ constexpr float kGBits = std::is_same<Fmt, F16>::value ? 14.f : 0.f;
 template <class Fmt>
 constexpr float kGScale = std::is_same<Fmt, F16>::value ? 16384.f : 1.f;
 
+// The power of two by which fp16 holds a row's G smaller and its scaled H larger: dW contracts over the
+// rows, so the weights have to be in one of the two, and H times a small weight falls below fp16's
+// normal numbers (2^-14) while G has room there.  Three powers stay in H, which is seldom that small,
+// and more than eight would take G of ordinary probabilities (2^-20 and above) out of the normal
+// numbers.  dH takes it out again with the row's weight.
+template <class Fmt>
+__device__ __forceinline__ int shift_of(float weight, float top) {
+    if constexpr (std::is_same<Fmt, BF16>::value) return 0;
+    const int apart = (int)(__float_as_uint(top) >> 23) - (int)(__float_as_uint(weight) << 1 >> 24);
+    return min(max(apart - 3, 0), 8);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }
+
 // An element of dH; a row of weight 0 takes no part, whatever its sums are.
 template <class Fmt>
 __device__ __forceinline__ float weigh(float sum, float weight) {
@@ -428,7 +443,15 @@ __device__ __forceinline__ void weigh_top(const Product& p, int thread, float* t
     }
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (thread % 32 == 0) tops[thread / 32] = m;
-    asm volatile("bar.arrive 1, %0;" ::"n"(kWeighThreads<Epi>) : "memory");
+    // fp16's G needs the largest weight itself
+    if constexpr (std::is_same<Fmt, F16>::value) asm volatile("bar.sync 1, %0;" ::"n"(kWeighThreads<Epi>) : "memory");
+    else asm volatile("bar.arrive 1, %0;" ::"n"(kWeighThreads<Epi>) : "memory");
+}
+template <int Epi>
+__device__ __forceinline__ float largest(const float* tops) {
+    float m = tops[0];
+    for (int i = 1; i < Epi; ++i) m = fmaxf(m, tops[i]);
+    return m == 0.f ? 1.f : m;
 }
 
 // By the other two; part 0 .. parts - 1 of all CTAs' warps.
@@ -437,9 +460,7 @@ __device__ __forceinline__ void weigh_rows(const Product& p, int lane, unsigned 
                                            const float* tops) {
     using T = typename Fmt::T;
     asm volatile("bar.sync 1, %0;" ::"n"(kWeighThreads<Epi>) : "memory");
-    float m = tops[0];
-    for (int i = 1; i < Epi; ++i) m = fmaxf(m, tops[i]);
-    if (m == 0.f) m = 1.f;
+    const float m = largest<Epi>(tops);
     if (part == 0 && lane == 0) *p.weigh.top = m;
     if (!p.weigh.scaled) return;
     const uint4* H = static_cast<const uint4*>(p.weigh.H);
@@ -467,7 +488,7 @@ __device__ __forceinline__ void weigh_rows(const Product& p, int lane, unsigned 
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (at[k] < 0) break;
-            const float f = w[k] / m;
+            const float f = w[k] / m * power_of_two(shift_of<Fmt>(w[k], m));
             float y[8];
             unpack8<Fmt>(x[k], y);
 #pragma unroll
@@ -861,7 +882,10 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const int quad = warp & 3, part_no = (warp - kEpiWarp) >> 2;
         const uint32_t leader_empty = map_to(acc_empty, 0);
         if (K == kGrad && p.weigh.weight) weigh_top<Fmt, Epi>(p, threadIdx.x - kEpiWarp * 32, tops);
-        const float top_weight = K == kDW ? *p.top : 1.f;
+        constexpr bool kShifts = std::is_same<Fmt, F16>::value && (K == kGrad || K == kDH);
+        float top_weight = 1.f;
+        if constexpr (K == kGrad && kShifts) top_weight = p.weigh.weight ? largest<Epi>(tops) : *p.top;
+        else if constexpr (K == kDW || kShifts) top_weight = *p.top;
         Outbox<Fmt, kOutboxes / Epi> box{outbox + (warp - kEpiWarp) * (kOutboxes / Epi) * kOutBytes, &map_out, lane, 0};
         // What a tile's row needs from memory is asked for while the tile before it is worked on: a
         // load's latency at the start of every tile is as long as the work on one of few stages.
@@ -897,7 +921,8 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             tmem_fence_after();
             ahead = look(t + pairs);
             int hit = -1;                             // the target's column in this tile
-            const float weight = tile.weight;
+            float weight = tile.weight, one_hot = kGScale<Fmt>;
+            if constexpr (K == kDH && kShifts) weight *= power_of_two(shift_of<Fmt>(weight, top_weight));
             float lse2 = 0.f;
             bool counts = false, far = false;
             if constexpr (K == kLse || K == kGrad) {
@@ -907,6 +932,11 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 if constexpr (K == kGrad) {
                     far = fabsf(tile.lse) > kFar && !isinf(tile.lse);
                     lse2 = (far ? 0.f : tile.lse * kLog2e) - kGBits<Fmt>;
+                    if constexpr (kShifts) {
+                        const int e = shift_of<Fmt>(weight, top_weight);
+                        lse2 += (float)e;
+                        one_hot *= power_of_two(-e);
+                    }
                     // a row that is weighted with 0 counts for nothing, not for 0 * NaN (dW)
                     counts = counts && weight != 0.f;
                 }
@@ -933,7 +963,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     }
                     if ((hit & ~31) == c) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = c + i == hit ? v[i] - kGScale<Fmt> : v[i];
+                        for (int i = 0; i < 32; ++i) v[i] = c + i == hit ? v[i] - one_hot : v[i];
                     }
                     if (!counts) {                    // a row that takes no part
 #pragma unroll
@@ -1080,12 +1110,13 @@ join_kernel(const float2* part, const float* target_logit, const int64_t* target
 template <class Fmt, int V>
 __global__ void __launch_bounds__(256)
 join_splits_kernel(const float* sums, int splits, int64_t n, int cols, const float* weight, bool by_row,
-                   typename Fmt::T* out) {
+                   const float* top, typename Fmt::T* out) {
     pdl_wait();
     pdl_trigger();
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
     if (i >= n) return;
-    const float w = by_row ? weight[i / cols] : *weight;
+    float w = by_row ? weight[i / cols] : *weight;
+    if (std::is_same<Fmt, F16>::value && by_row) w *= power_of_two(shift_of<Fmt>(w, *top));
     float v[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] = 0.f;
@@ -1426,13 +1457,13 @@ tb_status run_loss(const Problem& q, const Cut& c) {
 }
 
 template <class Fmt>
-bool join_splits(const float* sums, int splits, int64_t n, int64_t cols, const float* weight, bool by_row, void* out,
-                 cudaStream_t st) {
+bool join_splits(const float* sums, int splits, int64_t n, int64_t cols, const float* weight, bool by_row,
+                 const float* top, void* out, cudaStream_t st) {
     using T = typename Fmt::T;
     const bool vec = cols % 4 == 0 && aligned_to(out, 8);
     const dim3 grid((unsigned)ceil_div(n, vec ? 1024 : 256));
     return launch_pdl(vec ? join_splits_kernel<Fmt, 4> : join_splits_kernel<Fmt, 1>, grid, dim3(256), 0, st, sums, splits,
-                      n, (int)cols, weight, by_row, static_cast<T*>(out)) == cudaSuccess;
+                      n, (int)cols, weight, by_row, top, static_cast<T*>(out)) == cudaSuccess;
 }
 
 template <class Fmt>
@@ -1527,14 +1558,14 @@ tb_status run_grad(const Problem& q, const Cut& c) {
             }
             s = launch_product<Fmt, kDW>(g_cols, h_cols, out, r, q.st);
             if (s != TB_OK) return s;
-            if (r.sums && !join_splits<Fmt>(r.sums, r.splits, cols * q.d, q.d, top, false, r.out, q.st))
+            if (r.sums && !join_splits<Fmt>(r.sums, r.splits, cols * q.d, q.d, top, false, top, r.out, q.st))
                 return TB_ERR_CUDA;
         }
     }
     if (q.dH && c.splits > 1) {
         const int used = (int)std::min<int64_t>(c.splits, ceil_div(std::min(c.piece, q.v), kStageK));
         if (!join_splits<Fmt>(reinterpret_cast<const float*>(q.ws + c.off_sums), used, q.n * q.d, q.d, weight, true,
-                              q.dH, q.st))
+                              top, q.dH, q.st))
             return TB_ERR_CUDA;
     }
     return launch_status();

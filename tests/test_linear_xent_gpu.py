@@ -516,3 +516,42 @@ def test_logits_whose_terms_have_one_sign(tb, d, dtype):
     room = logit * (80 + 52 + 2) * 2.0 ** -24
     assert ((lse.double() - logit).abs() <= room).all(), (lse.double() - logit).abs().max().item() / logit
     assert loss[0].abs() <= logit * 2.0 ** -23 and ((loss[1:].double() - logit).abs() <= room).all()
+
+
+@pytest.mark.parametrize("n, d, v", [(300, 136, 900), (700, 40, 5003), (2000, 64, 40)])
+def test_light_rows_keep_their_bits_in_fp16(tb, n, d, v):
+    """Vocabulary rows that only tokens of small weight touch: one token of weight 2^12 knows its target,
+    all others weigh 2^-6 to 2^-2, a part in 2^14 to 2^18 of it, and their gradients are numbers that
+    fp16 holds well. Each is a product of two roundings, of G and of the scaled H, as for equal weights."""
+    H, W, t, _ = problem(n, d, v, HF, 19, ignored=0.0)
+    g = torch.Generator(device="cuda").manual_seed(20)
+    dloss = torch.exp2(-6 + 4 * torch.rand(n, generator=g, device="cuda"))
+    dloss[0] = 4096.0
+    H[:, 0], W[:, 0] = 0.0, 0.0                     # the heavy token's logits: 200 at its target, else 0
+    H[0] = 0.0
+    H[0, 0], W[v - 1, 0] = 200.0, 1.0
+    t[0] = v - 1
+    t[1:] = t[1:] % (v - 1)
+    _, lse = forward(tb, H, W, t)
+    dH, dW = backward(tb, dloss, H, W, t, lse)
+    l, err_l = logits64(H[1:], W)
+    p = (l - lse[1:].double()[:, None]).exp()
+    G = p.clone()
+    G[torch.arange(n - 1, device="cuda"), t[1:]] -= 1.0
+    G *= dloss[1:].double()[:, None]
+    half = torch.finfo(HF).eps / 2
+    h = H[1:].double()
+    want, size = (G.T @ h)[:v - 1], (G.abs().T @ h.abs())[:v - 1]
+    # G's and H's rounding, the exponent's, the additions; G below fp16's normal numbers: half a step of
+    # 2^-24 under at least 2^6; elements of H below 2^-6 of the largest, half a step of what carries them
+    p_err = (p * (err_l + 8 * U * 20) + 2.0 ** -31) * dloss[1:].double()[:, None]
+    room = size * (2 * half + half * half + 2 * U * (n + 16)) + (p_err.T @ h.abs())[:v - 1]
+    room += (G.abs().T.sum(1, keepdim=True))[:v - 1] * 2.0 ** -13 * half
+    room = room + (want.abs() + room) * half + 2.0 ** -25
+    off = (dW[:v - 1].double() - want).abs()
+    assert (off <= room).all(), (off / room).max().item()
+    # and the light rows' dH
+    want, size = G @ W.double(), G.abs() @ W.double().abs()
+    room = size * (half + 2 * U * (v + 16)) + p_err @ W.double().abs()
+    room = room + (want.abs() + room) * half + 2.0 ** -25
+    assert ((dH[1:].double() - want).abs() <= room).all()
