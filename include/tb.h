@@ -32,9 +32,11 @@
  *     RMSNorm) prefetch their first rows into L2, but they load and store no
  *     global memory before every earlier kernel on the stream has completed and
  *     its writes are visible.  Stream order is kept exactly.
- *   - fp32 pointers must be 4-byte aligned and 16-bit pointers 2-byte aligned
- *     (TB_ERR_MISALIGNED otherwise).  Any larger alignment is optional: 16-byte
- *     aligned buffers take the vectorised path, others a scalar one.
+ *   - fp32 pointers must be 4-byte aligned, 16-bit pointers 2-byte aligned and
+ *     64-bit ones 8-byte aligned (TB_ERR_MISALIGNED otherwise).  Any larger
+ *     alignment is optional: 16-byte aligned buffers take the vectorised path,
+ *     others a scalar one.  Two exceptions: workspaces are 16-byte aligned, and
+ *     so are the output layer's H and W where D is a multiple of 8.
  *   - The calls are not thread-safe against tb_adamw_plan_destroy of the plan
  *     they use; otherwise they may be called from several host threads.
  */
@@ -76,11 +78,13 @@ int tb_version(void);
 /*
  * tb_device_error -- read (and optionally clear) the device-side error word of
  * the current device.  Kernels that wait on an mbarrier for their own bulk
- * copies give up after about one second; they then set this word to
+ * copies (and, in the output layer's loss, tensor-core instructions) give up
+ * after about one second; they then set this word to
  * TB_ERR_TIMEOUT, drain what they issued and return early (their outputs are
  * then undefined).  tb_adamw_step_device sets it to TB_ERR_INVALID_VALUE when
- * the step counter it reads is below 1.  This call synchronises the current
- * device.
+ * the step counter it reads is below 1, and tb_linear_xent when a target is
+ * neither in the vocabulary nor ignore_index.  This call synchronises the
+ * current device.
  *   code   out: 0 when no kernel gave up since the last reset
  *   reset  nonzero: clear the word after reading it
  * Returns TB_OK, TB_ERR_INVALID_VALUE (code == NULL) or TB_ERR_CUDA.
@@ -559,9 +563,11 @@ tb_status tb_rope_freqs(int rotary_dim, double base, const tb_rope_scaling* scal
  *                   Elements of a buffer outside the views are not touched.
  *   head_dim        1 .. 1024
  *   dtype           TB_F32, TB_BF16 or TB_F16, of all four
- * Sizes, strides and pointers that are multiples of 16 bytes (8, or two elements) take
- * vectorised kernels, others a general one.  The sines of 16-bit calls are good to
- * 2^-21, those of fp32 calls to fp32 accuracy.
+ * Heads are read by vectors of 16 bytes, 8 bytes or two elements, the widest for which
+ * head_dim and rotary_dim are multiples of two vectors and pointers and strides of one:
+ * 16-bit heads of up to 512, 256 and 256 elements, fp32 heads of up to 256 (16 bytes) and
+ * 256 (two elements).  Others take a general kernel, one element at a time.  The sines of
+ * 16-bit calls are good to 2^-20, those of fp32 calls to fp32 accuracy.
  * Errors: TB_ERR_INVALID_VALUE, TB_ERR_UNSUPPORTED_DTYPE, TB_ERR_MISALIGNED,
  * TB_ERR_ALIAS, TB_ERR_CUDA.
  */
@@ -631,8 +637,12 @@ tb_status tb_qk_norm_rope_bwd(const tb_heads* dq_out, const tb_heads* dk_out,
  *     dH = dloss * (G W),   dW = G^T (dloss * H)
  * The loss keeps the logits in accumulators only; the gradient forms them again, one
  * piece of the vocabulary at a time, and holds one piece of G (rounded to dtype) in the
- * workspace, at most about 256 MiB unless rows exceeds 65,536.  (The pages take the
- * softmax backward on stored probabilities: tb_softmax_bwd.)
+ * workspace, at most about 256 MiB unless rows exceeds 65,536 (then 4,096 bytes a row).  Beside
+ * G the gradient's workspace holds a copy of H, fp32 sums of dH (rows * D * 4 bytes, times the
+ * parts that the vocabulary is split into) where it takes several pieces or parts, and fp32 sums
+ * of dW (a piece's columns * D * 4 bytes, times the parts of the rows) where the rows are split.
+ * Both calls' workspaces hold padded copies of H and W where D is not a multiple of 8.  (The
+ * pages take the softmax backward on stored probabilities: tb_softmax_bwd.)
  *
  * A row whose target is ignore_index takes no part, whatever its H is: its loss is +0, its
  * dH is 0 and it adds nothing to dW.  Its lse is written.  A target outside [0, vocab) that
@@ -662,8 +672,11 @@ tb_status tb_qk_norm_rope_bwd(const tb_heads* dq_out, const tb_heads* dk_out,
  * model.  Two values are
  * rounded to dtype on the way: G, and for dW the rows of H times dloss / max |dloss| (exact
  * where every dloss is the same, as for a mean).  TB_F16 holds G times 2^14, so that
- * probabilities down to 2^-38 count.
- * D not a multiple of 8 costs a padded copy of H and W in the workspace per call.
+ * probabilities down to 2^-38 count; of a dloss that is an 8th of the largest or less up to eight
+ * powers of two go into G instead of H (probabilities down to 2^-30), so that elements of H around 1
+ * keep their bits with weights 2^22 below the largest.
+ * Logits of any size are taken, -1e10 or the type's lowest value as a mask among them; an lse so
+ * large that fp32 has no place for the logarithm beside it is the row's largest logit.
  * Results must not overlap inputs, each other or the workspace.  rows == 0 writes zeros to
  * dW and nothing else.
  * Errors: TB_ERR_INVALID_VALUE (null or negative; D or vocab below 1; rows, D or vocab above

@@ -27,10 +27,12 @@
 // at a time).
 //
 // Measured at bf16 2 x 8,192 tokens of 32 + 8 heads of 128, norm and rotation (50 us at the
-// copy bandwidth): 58.8 us.  What did not pay there: loads a group ahead in a persistent
+// copy bandwidth): 58.8 to 59.1 us.  What did not pay there: loads a group ahead in a persistent
 // grid (71 us), a ring of cp.async copies (69 us) or of bulk copies (76 us) per warp; all
 // spend on addresses and bookkeeping what they save in waiting, and the kernel is bound by
-// issue slots first.
+// issue slots first.  At its 80 registers the forward with the norm spills: 40 bytes a thread of
+// 16-bit heads of 128, 64 to 84 of 80, 96 and 192, 104 where the lanes are not known when compiling;
+// the fp32 gradient 96 bytes at 10 and 12 lanes.
 #include <math.h>
 
 #include <algorithm>
@@ -152,8 +154,8 @@ struct Chunk {                    // a vector of E elements as loaded
 // cos and sin of turn * pos * freq, times the magnitude.  The 32-bit fraction of a turn
 // is signed, so it converts to a float in [-1, 1] of half turns with a relative error of
 // 2^-24.  16-bit outputs take the hardware's sine and cosine (absolute error below
-// 2^-21 on [-pi, pi], against a rounding of 2^-9 or 2^-12 of the output); fp32 outputs
-// take the library's.
+// 2^-21 on [-pi, pi], 2^-20 with the roundings of the angle, against a rounding of 2^-9 or 2^-12 of
+// the output); fp32 outputs take the library's.
 template <class Fmt>
 __device__ __forceinline__ void cos_sin(const Args& a, long long pos, unsigned long long freq,
                                         float* c, float* s) {
