@@ -154,7 +154,7 @@ struct Chunk {                    // a vector of E elements as loaded
 // cos and sin of turn * pos * freq, times the magnitude.  The 32-bit fraction of a turn
 // is signed, so it converts to a float in [-1, 1] of half turns with a relative error of
 // 2^-24.  16-bit outputs take the hardware's sine and cosine (absolute error below
-// 2^-21 on [-pi, pi], 2^-20 with the roundings of the angle, against a rounding of 2^-9 or 2^-12 of
+// 2^-21 on [-pi, pi], 2^-20 with the roundings of the angle, against a rounding of 2^-8 or 2^-11 of
 // the output); fp32 outputs take the library's.
 template <class Fmt>
 __device__ __forceinline__ void cos_sin(const Args& a, long long pos, unsigned long long freq,

@@ -374,10 +374,11 @@ def masked_problem(dtype, value, columns, n=70, d=72, v=700, seed=14):
 @pytest.mark.parametrize("dtype, values", [(BF, (-1e10, 2.0 ** 33 * -1.7, -1e30, -3.3e38)),
                                            (HF, (-2.0 ** 29, -1.7 * 2.0 ** 28, -1e9))])
 @pytest.mark.parametrize("columns", [slice(0, 640), slice(32, 64), slice(3, 500)])
-def test_masks_of_low_values(tb, dtype, values, columns):
+@pytest.mark.parametrize("d", [72, 600, 1304])                     # 16 and 8 epilogue warps, several chunks
+def test_masks_of_low_values(tb, d, dtype, values, columns):
     """A masked column counts exp(-large) = 0 whatever the large value is: the same bits as with a
     mask of -10,000, in 32-column groups that hold nothing else as well."""
-    H, W, t, dloss = masked_problem(dtype, -1e4, columns)
+    H, W, t, dloss = masked_problem(dtype, -1e4, columns, d=d)
     loss, lse = forward(tb, H, W, t)
     keep = torch.ones(W.shape[0], dtype=torch.bool, device="cuda")
     keep[columns] = False
@@ -385,7 +386,7 @@ def test_masks_of_low_values(tb, dtype, values, columns):
     dH, dW = backward(tb, dloss, H, W, t, lse)
     assert not dW[columns].any()
     for value in values:
-        H, W, t, dloss = masked_problem(dtype, value, columns)
+        H, W, t, dloss = masked_problem(dtype, value, columns, d=d)
         got = forward(tb, H, W, t)
         assert torch.equal(got[0], loss) and torch.equal(got[1], lse), value
         dH2, dW2 = backward(tb, dloss, H, W, t, lse)
