@@ -21,11 +21,12 @@
 // What bounds it: the tensor cores.  A stage's MMAs take 237 ns with operands at hand, 277 ns
 // with them coming from L2 (2.1 GHz, one launch); under continuous load the power limit sets
 // the clock.  bf16 8,192 x 32,000 x 4,096 over several boards: loss 1,149 to 1,177 us (1,825 to 1,870
-// TFLOP/s), gradient 3,690 to 3,760 us (1,715 to 1,745 TFLOP/s; 3,950 us, 1,631, after a second of nothing
-// else; a cuBLAS product reaches 1,871 in a burst and 1,707 for seconds).  Short contractions are bound by the epilogue, the loads' latency and, below
-// about 450 contracted elements, by G, which is written once and read twice: fp16 1,021 x 50,257 x 768,
-// gradient, 158 to 184 us by run, as the buffers happen to lie (126 us at 1,871 TFLOP/s); bf16 37 rows
-// against the same weights, loss, 22 us, of which about 13 read W at 6 TB/s.
+// TFLOP/s), gradient 3,690 to 3,760 us (1,715 to 1,745 TFLOP/s; 3,950 us, 1,631, after a second of
+// nothing else; a cuBLAS product reaches 1,871 in a burst and 1,707 for seconds).  Short contractions
+// are bound by the epilogue, the loads' latency and, below about 450 contracted elements, by G, which is
+// written once and read twice: fp16 1,021 x 50,257 x 768, gradient, 158 to 184 us by run, as the buffers
+// happen to lie (126 us at 1,871 TFLOP/s); bf16 37 rows against the same weights, loss, 22 us, of which
+// about 13 read W at 6 TB/s.
 //
 // The accumulators are fp32, but tensor cores cut off what an addition shifts below the sum's
 // last place, where fp32 arithmetic rounds: a sum comes out smaller by 1e-9 of itself for every contracted
