@@ -701,6 +701,73 @@ tb_status tb_linear_xent_bwd(const float* dloss, const void* H, const void* W,
                              tb_dtype dtype, void* workspace, size_t workspace_bytes,
                              void* stream);
 
+/* ======================================================================== */
+/* Gated feed-forward projections                                            */
+/* ======================================================================== */
+/*
+ * The first half of a gated feed-forward block, both projections with the activation and
+ * the product in one pass, and its gradient.  (The pages have no counterpart.)  With inputs
+ * X [rows, D] and weights Wg, Wu [F, D]:
+ *     G = X Wg^T,  U = X Wu^T,  H = act(G) * U
+ * and, for the gradient dH,
+ *     dG = dH * U * act'(G),  dU = dH * act(G)
+ *     dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X
+ * The block's last projection is a plain matrix product.
+ */
+typedef enum tb_activation {
+    TB_ACT_SILU = 0,          /* x / (1 + exp(-x))                                        */
+    TB_ACT_GELU = 1,          /* x (1 + erf(x / sqrt(2))) / 2                             */
+    TB_ACT_GELU_TANH = 2      /* x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2        */
+} tb_activation;
+
+/*
+ * tb_gated_linear
+ *   X, Wg, Wu        device [rows, D], [F, D] and [F, D], TB_BF16 or TB_F16; halves of one
+ *                    weight [2 F, D] are taken as they are
+ *   H                out: [rows, F]
+ *   G, U             out: [rows, F], rounded to dtype, what the gradient needs; both NULL
+ *                    when it is not wanted (H is formed from the unrounded sums either way)
+ *   workspace        device scratch of tb_gated_linear_workspace_size() bytes, 16-byte
+ *                    aligned, contents ignored; may be NULL when that is 0.  It holds fp32
+ *                    sums of G and U where few tiles make the call split the contraction.
+ *                    Calls that may run at the same time need workspaces of their own, and
+ *                    so do graphs that may.
+ * tb_gated_linear_bwd
+ *   dH               [rows, F]: gradient of H
+ *   G, U             what the forward call kept
+ *   dX, dWg, dWu     out: [rows, D], [F, D] and [F, D], overwritten; dX, or dWg and dWu
+ *                    together, may be NULL when they are not wanted
+ *   workspace        as above, of tb_gated_linear_bwd_workspace_size() bytes.  It holds dG
+ *                    and dU (4 bytes an element of H) and fp32 sums of results whose
+ *                    contraction is split.
+ * D and F are multiples of 8 and every buffer is 16-byte aligned.  Sums are fp32, in the tensor
+ * cores' accumulators, which truncate: a sum of n terms of one sign comes out smaller by about
+ * 1e-9 n of itself, n at most 65,536 (longer sums are added from such parts).  dG and dU are
+ * rounded to dtype on their way into the products; TB_F16 holds them times a power of two that
+ * brings the largest of them to 2^14 .. 2^15, so that small gradients keep their bits.  Results
+ * are bitwise reproducible on one device model.  Results must not overlap inputs, each other or
+ * the workspace.  rows == 0 writes zeros to dWg and dWu and nothing else.
+ * Errors: TB_ERR_INVALID_VALUE (null or negative; D or F no multiple of 8 or below 8; rows, D or
+ * F above 2^24, a product of two of them above 2^38; only one of G and U, or of dWg and dWu;
+ * no result wanted; unknown activation), TB_ERR_UNSUPPORTED_DTYPE (TB_F32 has no such tensor-core
+ * product), TB_ERR_MISALIGNED, TB_ERR_ALIAS, TB_ERR_WORKSPACE, TB_ERR_CUDA.
+ */
+tb_status tb_gated_linear_workspace_size(int64_t rows, int64_t D, int64_t F, tb_dtype dtype,
+                                         size_t* bytes);
+
+tb_status tb_gated_linear(const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
+                          int64_t rows, int64_t D, int64_t F, tb_activation act, tb_dtype dtype,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+tb_status tb_gated_linear_bwd_workspace_size(int64_t rows, int64_t D, int64_t F, tb_dtype dtype,
+                                             size_t* bytes);
+
+tb_status tb_gated_linear_bwd(const void* dH, const void* X, const void* Wg, const void* Wu,
+                              const void* G, const void* U, void* dX, void* dWg, void* dWu,
+                              int64_t rows, int64_t D, int64_t F, tb_activation act,
+                              tb_dtype dtype, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

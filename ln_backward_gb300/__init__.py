@@ -14,6 +14,8 @@ from ._binding import (  # noqa: F401
     tb_adamw_step_device,
     tb_cast_from_f32, tb_cast_to_f32,
     tb_device_error,
+    tb_gated_linear, tb_gated_linear_bwd, tb_gated_linear_bwd_workspace_size,
+    tb_gated_linear_workspace_size,
     tb_layernorm_bwd, tb_layernorm_bwd_noalloc, tb_layernorm_bwd_selftest_timeout,
     tb_layernorm_bwd_workspace_size,
     tb_linear_xent, tb_linear_xent_bwd, tb_linear_xent_bwd_workspace_size,

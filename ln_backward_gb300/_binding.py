@@ -36,7 +36,8 @@ EXPORTS = ("tb_status_string", "tb_version", "tb_device_error", "tb_adamw_plan_c
            "tb_rope_bwd", "tb_qk_norm_rope", "tb_qk_norm_rope_bwd_workspace_size",
            "tb_qk_norm_rope_bwd", "tb_linear_xent_workspace_size", "tb_linear_xent",
            "tb_linear_xent_bwd_workspace_size", "tb_linear_xent_bwd",
-           "tb_linear_xent_selftest_timeout")
+           "tb_linear_xent_selftest_timeout", "tb_gated_linear_workspace_size", "tb_gated_linear",
+           "tb_gated_linear_bwd_workspace_size", "tb_gated_linear_bwd")
 
 
 class TbError(RuntimeError):
@@ -151,6 +152,13 @@ def _load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.tb_linear_xent_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, vp,
                                        ctypes.c_size_t, vp]
     lib.tb_linear_xent_bwd.restype = i32
+    for fn in (lib.tb_gated_linear_workspace_size, lib.tb_gated_linear_bwd_workspace_size):
+        fn.argtypes = [i64, i64, i64, i32, ctypes.POINTER(ctypes.c_size_t)]
+        fn.restype = i32
+    lib.tb_gated_linear.argtypes = [vp] * 6 + [i64, i64, i64, i32, i32, vp, ctypes.c_size_t, vp]
+    lib.tb_gated_linear.restype = i32
+    lib.tb_gated_linear_bwd.argtypes = [vp] * 9 + [i64, i64, i64, i32, i32, vp, ctypes.c_size_t, vp]
+    lib.tb_gated_linear_bwd.restype = i32
     return lib
 
 
@@ -745,3 +753,65 @@ def tb_linear_xent_bwd(dloss: torch.Tensor, H: torch.Tensor, W: torch.Tensor, ta
            lib.tb_linear_xent_bwd(_ptr(dloss), _ptr(H), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dH),
                                   _ptr(dW), rows, D, vocab, int(ignore_index), _dtype(H),
                                   _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- gated projections
+ACTIVATION = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _gated_sizes(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, activation: str):
+    if X.dim() != 2 or Wg.dim() != 2 or Wg.shape != Wu.shape or X.shape[1] != Wg.shape[1]:
+        raise ValueError("X must be [rows, D], Wg and Wu [F, D], got "
+                         f"{tuple(X.shape)}, {tuple(Wg.shape)} and {tuple(Wu.shape)}")
+    if not X.dtype == Wg.dtype == Wu.dtype:
+        raise ValueError("X, Wg and Wu must share a dtype")
+    if activation not in ACTIVATION:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATION)}")
+    rows, D = X.shape
+    return rows, D, Wg.shape[0], ACTIVATION[activation]
+
+
+def tb_gated_linear_workspace_size(rows: int, D: int, F: int, dtype: torch.dtype) -> int:
+    return _workspace_size(lib.tb_gated_linear_workspace_size, "tb_gated_linear_workspace_size",
+                           int(rows), int(D), int(F), _DTYPE[dtype])
+
+
+def tb_gated_linear_bwd_workspace_size(rows: int, D: int, F: int, dtype: torch.dtype) -> int:
+    return _workspace_size(lib.tb_gated_linear_bwd_workspace_size,
+                           "tb_gated_linear_bwd_workspace_size", int(rows), int(D), int(F),
+                           _DTYPE[dtype])
+
+
+def tb_gated_linear(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, H: torch.Tensor,
+                    G: Optional[torch.Tensor] = None, U: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, activation: str = "silu",
+                    stream=None) -> None:
+    """H = act(X Wg^T) * (X Wu^T) in one pass. G and U receive the two products for
+    tb_gated_linear_bwd; leave them out when serving."""
+    rows, D, F, act = _gated_sizes(X, Wg, Wu, activation)
+    for t, name in ((H, "H"), (G, "G"), (U, "U")):
+        if t is not None:
+            _want(t, rows * F, X.dtype, name)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("tb_gated_linear",
+           lib.tb_gated_linear(_ptr(X), _ptr(Wg), _ptr(Wu), _ptr(H), _ptr(G), _ptr(U), rows, D, F,
+                               act, _dtype(X), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def tb_gated_linear_bwd(dH: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor,
+                        G: torch.Tensor, U: torch.Tensor, dX: Optional[torch.Tensor],
+                        dWg: Optional[torch.Tensor], dWu: Optional[torch.Tensor],
+                        workspace: Optional[torch.Tensor], activation: str = "silu",
+                        stream=None) -> None:
+    """Gradients of tb_gated_linear: dX, dWg and dWu (overwritten; None: not wanted) from dH and
+    what the forward kept."""
+    rows, D, F, act = _gated_sizes(X, Wg, Wu, activation)
+    for t, n, name in ((dH, rows * F, "dH"), (G, rows * F, "G"), (U, rows * F, "U"),
+                       (dX, rows * D, "dX"), (dWg, F * D, "dWg"), (dWu, F * D, "dWu")):
+        if t is not None:
+            _want(t, n, X.dtype, name)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("tb_gated_linear_bwd",
+           lib.tb_gated_linear_bwd(_ptr(dH), _ptr(X), _ptr(Wg), _ptr(Wu), _ptr(G), _ptr(U), _ptr(dX),
+                                   _ptr(dWg), _ptr(dWu), rows, D, F, act, _dtype(X), _ptr(workspace),
+                                   ws_bytes, _stream(stream)))
