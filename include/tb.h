@@ -702,6 +702,49 @@ tb_status tb_linear_xent_bwd(const float* dloss, const void* H, const void* W,
                              void* stream);
 
 /* ======================================================================== */
+/* Causal attention over whole prompts                                       */
+/* ======================================================================== */
+/*
+ * The attention product between the rotated queries and keys and the output projection, without
+ * the scores in memory.  (The pages take attention's softmax backward on stored probabilities:
+ * tb_softmax_bwd_causal.)  For token i of a sequence and the tokens j <= i of the same one:
+ *     s_ij  = scale * q_i . k_j,   lse_i = log sum_j exp(s_ij)
+ *     out_i = sum_j exp(s_ij - lse_i) v_j
+ * for every query head; heads_q / heads_k query heads in a row share a head of k and v.
+ *
+ * A sequence is one batch entry, or, with offsets, a run of tokens of the one row: sequence i is
+ * tokens offsets[i] .. offsets[i + 1] - 1, any number of them, 0 and 1 included.  Tokens before the
+ * first or behind the last sequence are not written, and whatever they hold (NaN included) reaches
+ * no other token; nor does a token reach another sequence's.  Within a sequence k and v are finite:
+ * an infinity or NaN may reach the rows of up to 127 tokens before it.  Offsets that do not count
+ * up within 0 .. seq set the device error word to TB_ERR_INVALID_VALUE (tb_device_error); their
+ * sequences are cut to the row.
+ *
+ * tb_attention
+ *   q, k, v          [batch, seq, heads, head_dim] by tb_heads; k and v have the same number of
+ *                    heads, a divisor of q's
+ *   out              as many heads as q; shares no element with q, k or v
+ *   lse              out: fp32 [batch, heads_q, seq], contiguous, what the gradient needs; NULL
+ *                    when it is not wanted (serving)
+ *   batch, seq       >= 0, batch <= 2^20, seq <= 2^30
+ *   head_dim         a multiple of 8, 8 .. 128
+ *   offsets          device int64 [sequences + 1], 8-byte aligned; NULL: every batch entry is a
+ *                    sequence (sequences is 0 then).  With offsets batch is 1.
+ *   scale            > 0; 1 / sqrt(head_dim) is usual
+ *   dtype            TB_BF16 or TB_F16
+ * Data starts on 16 bytes and strides are multiples of 8 elements, not 0 (except of a size of 1)
+ * and below 2^39.
+ * Sums are fp32.  P = exp(s - m), m within 8 ln 2 of the row's running maximum, is rounded to dtype on
+ * its way into the second product; the sum below it is not.  Results are bitwise reproducible.
+ * Errors: TB_ERR_INVALID_VALUE, TB_ERR_UNSUPPORTED_DTYPE (TB_F32 has no such tensor-core product),
+ * TB_ERR_MISALIGNED, TB_ERR_ALIAS, TB_ERR_CUDA.
+ */
+tb_status tb_attention(const tb_heads* q, const tb_heads* k, const tb_heads* v, const tb_heads* out,
+                       float* lse, int64_t batch, int64_t seq, int64_t head_dim,
+                       const int64_t* offsets, int64_t sequences, float scale, tb_dtype dtype,
+                       void* stream);
+
+/* ======================================================================== */
 /* Gated feed-forward projections                                            */
 /* ======================================================================== */
 /*

@@ -37,7 +37,7 @@ EXPORTS = ("tb_status_string", "tb_version", "tb_device_error", "tb_adamw_plan_c
            "tb_qk_norm_rope_bwd", "tb_linear_xent_workspace_size", "tb_linear_xent",
            "tb_linear_xent_bwd_workspace_size", "tb_linear_xent_bwd",
            "tb_linear_xent_selftest_timeout", "tb_gated_linear_workspace_size", "tb_gated_linear",
-           "tb_gated_linear_bwd_workspace_size", "tb_gated_linear_bwd")
+           "tb_gated_linear_bwd_workspace_size", "tb_gated_linear_bwd", "tb_attention")
 
 
 class TbError(RuntimeError):
@@ -152,6 +152,8 @@ def _load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.tb_linear_xent_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, vp,
                                        ctypes.c_size_t, vp]
     lib.tb_linear_xent_bwd.restype = i32
+    lib.tb_attention.argtypes = [heads, heads, heads, heads, vp, i64, i64, i64, vp, i64, f32, i32, vp]
+    lib.tb_attention.restype = i32
     for fn in (lib.tb_gated_linear_workspace_size, lib.tb_gated_linear_bwd_workspace_size):
         fn.argtypes = [i64, i64, i64, i32, ctypes.POINTER(ctypes.c_size_t)]
         fn.restype = i32
@@ -753,6 +755,88 @@ def tb_linear_xent_bwd(dloss: torch.Tensor, H: torch.Tensor, W: torch.Tensor, ta
            lib.tb_linear_xent_bwd(_ptr(dloss), _ptr(H), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dH),
                                   _ptr(dW), rows, D, vocab, int(ignore_index), _dtype(H),
                                   _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- attention
+class _AttentionCall:
+    """The tb_heads of a call's tensors, packed as in _HeadsCall: the first has the query heads, and so
+    have those numbered in ``like_q``; the others have the key heads."""
+
+    __slots__ = ("words", "p", "batch", "seq", "dim", "code", "device", "heads_q", "heads_k", "offsets",
+                 "sequences", "scale")
+
+    def __init__(self, names, tensors, like_q, offsets: Optional[torch.Tensor], scale: Optional[float]):
+        q = tensors[0]
+        shape = q.shape
+        if len(shape) != 4:
+            raise ValueError(f"{names[0]} must be [batch, seq, heads, head_dim], got {tuple(shape)}")
+        batch, seq, self.heads_q, dim = shape
+        dtype, device = q.dtype, q.get_device()
+        heads_k, words = None, []
+        for i, t in enumerate(tensors):
+            shape = t.shape
+            b, s, h, d = shape if len(shape) == 4 else (-1, -1, -1, -1)
+            if b != batch or s != seq or d != dim:
+                raise ValueError(f"{names[i]} must be [batch, seq, heads, head_dim] with the batch, "
+                                 f"seq and head_dim of {names[0]}, got {tuple(shape)}")
+            if i in like_q:
+                if h != self.heads_q:
+                    raise ValueError(f"{names[i]} must have {self.heads_q} heads, got {h}")
+            elif heads_k is None:
+                heads_k = h
+            elif h != heads_k:
+                raise ValueError(f"{names[i]} must have {heads_k} heads, got {h}")
+            if t.dtype != dtype:
+                raise ValueError(f"{names[i]} must be {dtype} like {names[0]}, got {t.dtype}")
+            sb, ss, sh, sd = t.stride()
+            if sd != 1 and dim > 1:
+                raise ValueError(f"the last dimension of {names[i]} must be contiguous")
+            if t.get_device() != device:
+                raise ValueError(f"{names[i]} is on {t.device}, {names[0]} on {q.device}")
+            words += (t.data_ptr(), sb, ss, sh, h)
+        if device < 0:
+            raise ValueError("tensors passed to libtb must be CUDA tensors")
+        if device != _current_device():
+            raise ValueError(f"tensor on cuda:{device}, but the current device is "
+                             f"cuda:{_current_device()}")
+        self.offsets, self.sequences = None, 0
+        if offsets is not None:
+            if offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.numel() < 1:
+                raise ValueError("offsets must hold an int64 for the start of each sequence and one for the last's end")
+            if offsets.get_device() != device:
+                raise ValueError(f"offsets are on {offsets.device}, {names[0]} on cuda:{device}")
+            self.offsets, self.sequences = _ptr(offsets), offsets.numel() - 1
+        self.words = array("q", words)
+        at = self.words.buffer_info()[0]
+        self.p = [at + i * _HEADS_BYTES for i in range(len(tensors))]
+        self.batch, self.seq, self.dim, self.device, self.heads_k = batch, seq, dim, device, heads_k
+        self.scale = dim ** -0.5 if scale is None else float(scale)
+        self.code = _DTYPE.get(dtype)
+        if self.code is None:
+            raise TbError("dtype", 2)
+
+    def sums(self, t: torch.Tensor, name: str) -> Optional[int]:
+        """Address of a contiguous fp32 [batch, heads_q, seq]."""
+        _want(t, self.batch * self.heads_q * self.seq, _F32, name)
+        return _ptr(t)
+
+    def stream(self, stream) -> Optional[int]:
+        return _raw_stream(self.device) if stream is None and _raw_stream else _stream(stream)
+
+
+def tb_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                 lse: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
+                 scale: Optional[float] = None, stream=None) -> None:
+    """Causal attention of [batch, seq, heads, head_dim] tensors (any strides but the last); k and v
+    may have fewer heads than q. ``offsets``: int64, the first token of each of the sequences packed
+    into the one row, and the last's end; None: every batch entry is a sequence. lse (fp32
+    [batch, heads_q, seq]) receives what tb_attention_bwd needs; leave it out when serving.
+    ``scale``: head_dim ** -0.5 by default."""
+    c = _AttentionCall(("q", "k", "v", "out"), (q, k, v, out), (0, 3), offsets, scale)
+    sums = None if lse is None else c.sums(lse, "lse")
+    _check("tb_attention",
+           lib.tb_attention(*c.p, sums, c.batch, c.seq, c.dim, c.offsets, c.sequences, c.scale, c.code,
+                            c.stream(stream)))
 
 
 # ----------------------------------------------------------------------------- gated projections
