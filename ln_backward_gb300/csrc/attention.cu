@@ -36,7 +36,8 @@ struct Args {
 struct Item {
     Span span;
     int head;
-    int blocks[2];            // of keys that the two tiles of 128 read; 0: no such tile
+    int blocks0, blocks1;     // of keys that the two tiles of 128 read; 0: no such tile
+    __device__ __forceinline__ int blocks(int t) const { return t ? blocks1 : blocks0; }
 };
 __device__ __forceinline__ bool find_item(const Args& p, unsigned index, Item* it) {
     const unsigned heads = (unsigned)p.heads;
@@ -49,8 +50,8 @@ __device__ __forceinline__ bool find_item(const Args& p, unsigned index, Item* i
         it->span = Span{(int)(slot % batch), 0, p.tokens.seq, p.tiles - 1 - (int)(slot / batch)};
     }
     const int left = it->span.len - it->span.tile * kPair;
-    it->blocks[0] = 2 * it->span.tile + 1;
-    it->blocks[1] = left > kRows ? 2 * it->span.tile + 2 : 0;
+    it->blocks0 = 2 * it->span.tile + 1;
+    it->blocks1 = left > kRows ? 2 * it->span.tile + 2 : 0;
     return true;
 }
 
@@ -106,10 +107,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         int n = 0, items = 0, tails = 0;     // tiles staged, items, tails mended
         bool ok = true;
         for (; more && ok; more = false, ++items) {
-            const int blocks = max(it.blocks[0], it.blocks[1]), kv_head = it.head / p.group;
+            const int blocks = max(it.blocks0, it.blocks1), kv_head = it.head / p.group;
             const int q_row = it.span.first + it.span.tile * kPair;
             for (int t = 0; t < 2; ++t) {
-                if (!it.blocks[t]) continue;
+                if (!it.blocks(t)) continue;
                 // (one item: the queries' place is free)
                 if (elect_one()) {
                     mbar_expect(q_full + 8 * t, L::kTileBytes);
@@ -155,7 +156,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         mbar_wait<kEnd>(drain, 0, &p);
         if (items)
             for (int t = 0; t < 2; ++t)
-                if (it.blocks[t]) mbar_wait<kEnd>(q_full + 8 * t, (items - 1) & 1, &p);
+                if (it.blocks(t)) mbar_wait<kEnd>(q_full + 8 * t, (items - 1) & 1, &p);
         for (int i = max(0, n - L::kRing); i < n; ++i) mbar_wait<kEnd>(full + 8 * (i % L::kRing), (i / L::kRing) & 1, &p);
     } else if (warp == 1) {
         const uint32_t by_rows = instruction(kBf, kRows, false), by_cols = instruction(kBf, cols, true);
@@ -164,9 +165,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         int have[2] = {0, 0};                // P taken
         bool ok = true;
         for (; more && ok; more = false, ++items) {
-            const int blocks = max(it.blocks[0], it.blocks[1]);
+            const int blocks = max(it.blocks0, it.blocks1);
             // block i from the end is read by a tile when it is not behind the tile's last
-            auto reads = [&](int t, int i) { return it.blocks[t] && i < blocks && blocks - 1 - i < it.blocks[t]; };
+            auto reads = [&](int t, int i) { return it.blocks(t) && i < blocks && blocks - 1 - i < it.blocks(t); };
             auto scores = [&](int t, int place) {
                 if (elect_one()) {
                     uint32_t a = tile_desc(q0 + t * L::kTileBytes, false), b = tile_desc(ring0 + place * L::kTileBytes, false);
@@ -180,7 +181,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             };
             auto wait_ring = [&](int i) { return __all_sync(0xffffffffu, mbar_wait(full + 8 * (i % L::kRing), (i / L::kRing) & 1, &p)); };
             for (int t = 0; t < 2 && ok; ++t)
-                if (it.blocks[t]) ok = __all_sync(0xffffffffu, mbar_wait(q_full + 8 * t, items & 1, &p));
+                if (it.blocks(t)) ok = __all_sync(0xffffffffu, mbar_wait(q_full + 8 * t, items & 1, &p));
             if (!ok || !wait_ring(n)) break;
             for (int t = 0; t < 2; ++t)
                 if (reads(t, 0)) scores(t, n % L::kRing);
@@ -228,34 +229,43 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const unsigned long long c2 = pair_of(p.scale_log2, p.scale_log2);
         int have = 0, items = 0;
         bool ok = true;
-        for (; more && ok && it.blocks[t]; more = false, ++items) {
+        for (; more && ok && it.blocks(t); more = false, ++items) {
             float top = 0.f, base = 0.f;     // the maximum that P is taken against, and it times scale_log2
             unsigned long long total[2] = {0, 0};
-            for (int i = 0; i < it.blocks[t]; ++i, ++have) {
+            for (int i = 0; i < it.blocks(t); ++i, ++have) {
                 if (!__all_sync(0xffffffffu, mbar_wait(s_full + 8 * t, have & 1, &p))) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after();
-                uint32_t r[4][32];
+                // The row's scores in two halves: the maximum over the second, then the first, which stays in
+                // registers while the second comes again behind it.  (Whole rows in registers leave none for the rest.)
+                uint32_t a[32], b[32];
+                tmem_load32(mine + 64, a);
+                tmem_load32(mine + 96, b);
+                tmem_wait(a);
+                tmem_wait(b);
+                auto hide = [&](uint32_t (&x)[32], int from) {       // tokens behind the row's own
 #pragma unroll
-                for (int g = 0; g < 4; ++g) tmem_load32(mine + 32 * g, r[g]);
+                    for (int e = 0; e < 32; ++e) x[e] = from + e > row ? 0xff800000u : x[e];
+                };
+                float m4[4] = {__int_as_float(0xff800000), __int_as_float(0xff800000), __int_as_float(0xff800000), __int_as_float(0xff800000)};
+                auto highest = [&](const uint32_t (&x)[32]) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) tmem_wait(r[g]);
-                if (i == 0) {                // the block of the tile's own tokens
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * g + e > row) r[g][e] = 0xff800000u;
-                }
-                float m4[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) m4[e] = __uint_as_float(r[0][e]);
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-#pragma unroll
-                    for (int e = g ? 0 : 4; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(r[g][e]));
+                    for (int e = 0; e < 32; e += 2)
+                        m4[e / 2 & 3] = fmaxf(m4[e / 2 & 3], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+                };
+                const bool own = i == 0;     // the block of the tile's own tokens
+                if (own) hide(a, 64), hide(b, 96);
+                highest(a);
+                highest(b);
+                tmem_load32(mine, a);
+                tmem_load32(mine + 32, b);
+                tmem_wait(a);
+                tmem_wait(b);
+                if (own) hide(a, 0), hide(b, 32);
+                highest(a);
+                highest(b);
                 const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 if (i == 0) {
                     top = m == __int_as_float(0xff800000) ? 0.f : m;
@@ -277,20 +287,31 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     }
                 }
                 const unsigned long long b2 = pair_of(-base, -base);
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
+                auto powers = [&](const uint32_t (&x)[32], uint32_t to) {
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float lo, hi;
-                        split_pair(fma_pair(pair_of(__uint_as_float(r[g][2 * e]), __uint_as_float(r[g][2 * e + 1])), c2, b2), lo, hi);
+                        split_pair(fma_pair(pair_of(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, b2), lo, hi);
                         lo = exp2_fast(lo);
                         hi = exp2_fast(hi);
                         total[e & 1] = add_pair(total[e & 1], pair_of(lo, hi));
                         w[e] = pack2<Fmt>(lo, hi);
                     }
-                    tmem_store16(mine + 16 * g, w);
-                }
+                    tmem_store16(to, w);
+                };
+                // (P's columns lie over the first half's scores, which are in registers by now)
+                uint32_t c[32];
+                tmem_load32(mine + 64, c);
+                powers(a, mine);
+                tmem_wait(c);
+                tmem_load32(mine + 96, a);
+                powers(b, mine + 16);
+                if (own) hide(c, 64);
+                powers(c, mine + 32);
+                tmem_wait(a);
+                if (own) hide(a, 96);
+                powers(a, mine + 48);
                 tmem_stored();
                 tmem_fence_before();
                 __syncwarp();
