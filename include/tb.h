@@ -744,6 +744,35 @@ tb_status tb_attention(const tb_heads* q, const tb_heads* k, const tb_heads* v, 
                        const int64_t* offsets, int64_t sequences, float scale, tb_dtype dtype,
                        void* stream);
 
+/*
+ * tb_attention_bwd -- its gradient.  With p_ij = exp(s_ij - lse_i):
+ *     dp_ij = dout_i . v_j,   ds_ij = p_ij (dp_ij - dout_i . out_i)
+ *     dv_j = sum_i p_ij dout_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j
+ * dk and dv are summed over the query heads that share a key head.
+ *   dout             gradient of out
+ *   q, k, v          the forward's inputs; out, lse: what it wrote
+ *   dq, dk, dv       out: as q, k and v, overwritten; they share no element with an input or with
+ *                    each other (views of one joint buffer are told apart)
+ *   workspace        device scratch of tb_attention_bwd_workspace_size() bytes, 16-byte aligned,
+ *                    contents ignored.  Calls that may run at the same time need workspaces of
+ *                    their own, and so do graphs that may.
+ * Other arguments, sequences, alignment and errors as tb_attention, plus TB_ERR_WORKSPACE; q and dout
+ * are finite within a sequence as k and v are.  Sums are fp32; P and dS are rounded to dtype on their way
+ * into the last three products.  TB_F16 holds P times 2^14, and dS times a power of two by the largest
+ * norms of a row of dout and of v, so that small gradients keep their bits.  Every sum is taken in a
+ * fixed order: results are bitwise reproducible.
+ */
+tb_status tb_attention_bwd_workspace_size(int64_t batch, int64_t seq, int64_t heads_q,
+                                          int64_t heads_k, int64_t head_dim, tb_dtype dtype,
+                                          size_t* bytes);
+
+tb_status tb_attention_bwd(const tb_heads* dout, const tb_heads* q, const tb_heads* k,
+                           const tb_heads* v, const tb_heads* out, const float* lse,
+                           const tb_heads* dq, const tb_heads* dk, const tb_heads* dv,
+                           int64_t batch, int64_t seq, int64_t head_dim, const int64_t* offsets,
+                           int64_t sequences, float scale, tb_dtype dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 /* ======================================================================== */
 /* Gated feed-forward projections                                            */
 /* ======================================================================== */

@@ -12,7 +12,8 @@ from ._binding import (  # noqa: F401
     tb_adamw_grad_norm, tb_adamw_grad_norm_workspace_size, tb_adamw_plan_create,
     tb_adamw_plan_destroy, tb_adamw_selftest_stale_counter, tb_adamw_step, tb_adamw_step_clipped,
     tb_adamw_step_device,
-    tb_attention, tb_cast_from_f32, tb_cast_to_f32,
+    tb_attention, tb_attention_bwd, tb_attention_bwd_workspace_size,
+    tb_cast_from_f32, tb_cast_to_f32,
     tb_device_error,
     tb_gated_linear, tb_gated_linear_bwd, tb_gated_linear_bwd_workspace_size,
     tb_gated_linear_workspace_size,

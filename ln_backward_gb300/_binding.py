@@ -37,7 +37,8 @@ EXPORTS = ("tb_status_string", "tb_version", "tb_device_error", "tb_adamw_plan_c
            "tb_qk_norm_rope_bwd", "tb_linear_xent_workspace_size", "tb_linear_xent",
            "tb_linear_xent_bwd_workspace_size", "tb_linear_xent_bwd",
            "tb_linear_xent_selftest_timeout", "tb_gated_linear_workspace_size", "tb_gated_linear",
-           "tb_gated_linear_bwd_workspace_size", "tb_gated_linear_bwd", "tb_attention")
+           "tb_gated_linear_bwd_workspace_size", "tb_gated_linear_bwd", "tb_attention",
+           "tb_attention_bwd_workspace_size", "tb_attention_bwd")
 
 
 class TbError(RuntimeError):
@@ -154,6 +155,12 @@ def _load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.tb_linear_xent_bwd.restype = i32
     lib.tb_attention.argtypes = [heads, heads, heads, heads, vp, i64, i64, i64, vp, i64, f32, i32, vp]
     lib.tb_attention.restype = i32
+    lib.tb_attention_bwd_workspace_size.argtypes = [i64, i64, i64, i64, i64, i32,
+                                                    ctypes.POINTER(ctypes.c_size_t)]
+    lib.tb_attention_bwd_workspace_size.restype = i32
+    lib.tb_attention_bwd.argtypes = ([heads] * 5 + [vp] + [heads] * 3 +
+                                     [i64, i64, i64, vp, i64, f32, i32, vp, ctypes.c_size_t, vp])
+    lib.tb_attention_bwd.restype = i32
     for fn in (lib.tb_gated_linear_workspace_size, lib.tb_gated_linear_bwd_workspace_size):
         fn.argtypes = [i64, i64, i64, i32, ctypes.POINTER(ctypes.c_size_t)]
         fn.restype = i32
@@ -837,6 +844,30 @@ def tb_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.T
     _check("tb_attention",
            lib.tb_attention(*c.p, sums, c.batch, c.seq, c.dim, c.offsets, c.sequences, c.scale, c.code,
                             c.stream(stream)))
+
+
+def tb_attention_bwd_workspace_size(batch: int, seq: int, heads_q: int, heads_k: int, head_dim: int,
+                                    dtype: torch.dtype) -> int:
+    return _workspace_size(lib.tb_attention_bwd_workspace_size, "tb_attention_bwd_workspace_size",
+                           int(batch), int(seq), int(heads_q), int(heads_k), int(head_dim),
+                           _DTYPE[dtype])
+
+
+def tb_attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     out: torch.Tensor, lse: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor,
+                     dv: torch.Tensor, workspace: Optional[torch.Tensor],
+                     offsets: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     stream=None) -> None:
+    """Gradient of tb_attention: dq, dk and dv (overwritten) from dout, the forward's inputs and
+    what it wrote."""
+    c = _AttentionCall(("q", "k", "v", "dout", "out", "dq", "dk", "dv"), (q, k, v, dout, out, dq, dk, dv),
+                       (0, 3, 4, 5), offsets, scale)
+    pq, pk, pv, py, po, gq, gk, gv = c.p
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("tb_attention_bwd",
+           lib.tb_attention_bwd(py, pq, pk, pv, po, c.sums(lse, "lse"), gq, gk, gv, c.batch, c.seq, c.dim,
+                                c.offsets, c.sequences, c.scale, c.code, _ptr(workspace), ws_bytes,
+                                c.stream(stream)))
 
 
 # ----------------------------------------------------------------------------- gated projections

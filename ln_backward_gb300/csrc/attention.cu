@@ -9,7 +9,6 @@ namespace {
 constexpr int kPair = 2 * kRows;             // queries of a CTA: two tiles that share its keys
 constexpr int kSoftmaxWarp = 4;              // first of eight: four for each tile
 constexpr int kThreads = (kSoftmaxWarp + 8) * 32;
-constexpr int kOutStage = 32 * 128;          // what a warp stages of its results: 32 rows of 64 columns
 
 template <int Blocks>                        // of 64 columns of a head
 struct Layout {
@@ -142,11 +141,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 if (mend) {
                     if (!__all_sync(0xffffffffu, mbar_wait<kEnd>(tail, tails & 1, &p))) ok = false;
                     ++tails;
-                    for (int b = 0; b < Blocks; ++b)
-                        for (int x = rows * 8 + lane; x < kRows * 8; x += 32)
-                            *reinterpret_cast<uint4*>(smem + (at - q0) + b * kBox + x * 16) = make_uint4(0, 0, 0, 0);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
+                    clear_behind<Blocks>(smem + (at - q0), rows, lane);
                     if (lane == 0) mbar_arrive(full + 8 * s);
                 }
             }
@@ -330,31 +325,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     0.693147180559945309f * (base + log2f(l));
             T* out = static_cast<T*>(p.out) + it.span.batch * p.out_batch + token * p.out_seq + it.head * p.out_head;
             unsigned char* box = smem + L::kOut + (warp - kSoftmaxWarp) * kOutStage;
-            for (int x = 0; x < cols; x += 64) {
-                uint32_t o[2][32];
-                tmem_load32(sum + x, o[0]);
-                tmem_load32(sum + x + 32, o[1]);
-                tmem_wait(o[0]);
-                tmem_wait(o[1]);
-                __syncwarp();
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    uint4 v;
-                    uint32_t* h = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        h[e] = pack2<Fmt>(__uint_as_float(o[g / 4][g % 4 * 8 + 2 * e]) * inv, __uint_as_float(o[g / 4][g % 4 * 8 + 2 * e + 1]) * inv);
-                    *reinterpret_cast<uint4*>(box + lane * 128 + ((g ^ (lane & 7)) * 16)) = v;
-                }
-                __syncwarp();
-                const int c = lane & 7;      // 16 bytes of a row, eight lanes a row
-                if (x + 8 * c < p.dim)
-#pragma unroll
-                    for (int y = lane >> 3; y < 32; y += 4)
-                        if (y < rows)
-                            *reinterpret_cast<uint4*>(out + y * p.out_seq + x + 8 * c) =
-                                *reinterpret_cast<const uint4*>(box + y * 128 + ((c ^ (y & 7)) * 16));
-            }
+            store_rows<Fmt>(box, sum, inv, out, p.out_seq, rows, p.dim, lane);
         }
     }
     __syncwarp();

@@ -83,6 +83,50 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return r;
 }
 
+// 32 rows of a result from tensor memory, a row a lane, times the lane's factor and rounded, to `rows` rows
+// `stride` apart: through shared memory, from which eight lanes write a row's 64 columns.  `box`: the warp's own,
+// 1,024-byte aligned.
+constexpr int kOutStage = 32 * 128;
+template <class Fmt>
+__device__ __forceinline__ void store_rows(unsigned char* box, uint32_t tmem, float factor, typename Fmt::T* out, int64_t stride,
+                                           int rows, int dim, int lane) {
+    for (int x = 0; x < dim; x += 64) {
+        uint32_t o[2][32];
+        tmem_load32(tmem + x, o[0]);
+        tmem_load32(tmem + x + 32, o[1]);
+        tmem_wait(o[0]);
+        tmem_wait(o[1]);
+        __syncwarp();
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                h[e] = pack2<Fmt>(__uint_as_float(o[g / 4][g % 4 * 8 + 2 * e]) * factor,
+                                  __uint_as_float(o[g / 4][g % 4 * 8 + 2 * e + 1]) * factor);
+            *reinterpret_cast<uint4*>(box + lane * 128 + ((g ^ (lane & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        __syncwarp();
+        const int c = lane & 7;              // 16 bytes of a row
+        if (x + 8 * c < dim)
+#pragma unroll
+            for (int y = lane >> 3; y < 32; y += 4)
+                if (y < rows)
+                    *reinterpret_cast<uint4*>(out + y * stride + x + 8 * c) =
+                        *reinterpret_cast<const uint4*>(box + y * 128 + ((c ^ (y & 7)) * 16));
+    }
+}
+
+// A tile of `Blocks` boxes whose rows from `rows` on are to be zeros, which whatever lies there need not be
+// times 0.  By a whole warp, before the tile is handed to the MMAs.
+template <int Blocks>
+__device__ __forceinline__ void clear_behind(unsigned char* tile, int rows, int lane) {
+    for (int b = 0; b < Blocks; ++b)
+        for (int x = rows * 8 + lane; x < kRows * 8; x += 32) *reinterpret_cast<uint4*>(tile + b * kBox + x * 16) = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+
 // ---------------------------------------------------------------- sequences
 // The tokens of a call: `batch` rows of `seq` tokens.  With offsets, sequences packed into the one row:
 // number i is tokens offsets[i] .. offsets[i + 1] - 1.

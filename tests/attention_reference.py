@@ -58,6 +58,48 @@ def forward(q, k, v, scale, offsets=None):
     return out, lse, out_off, lse_off
 
 
+def backward(dout, q, k, v, out, lse, scale, offsets=None):
+    """dq, dk, dv of the formula, with out and lse as they are given, and the bounds of what each may be off before
+    its rounding; NaN where no sequence has the token."""
+    half = torch.finfo(q.dtype).eps / 2
+    b, seq, hq, d = q.shape
+    group = hq // k.shape[2]
+    inside = [(row, lo, hi) for row, lo, hi in spans(b, seq, offsets) if hi > lo]
+    res = [torch.full(x.shape, math.nan, dtype=torch.float64, device=q.device) for x in (q, k, v)]
+    off = [torch.zeros_like(x) for x in res]
+    floor_p = floor_s = 0.0
+    if q.dtype == torch.float16 and inside:   # below the normal numbers of what P and dS are held times
+        most = max(dout[r, a:z].double().norm(dim=-1).max().item() for r, a, z in inside) * \
+            max(v[r, a:z].double().norm(dim=-1).max().item() for r, a, z in inside)
+        floor_p, floor_s = 2.0 ** -14 * 2.0 ** -25, 2 * most * 2.0 ** -12 * 2.0 ** -25
+    for row, lo, hi in inside:
+        n = hi - lo
+        for h in range(k.shape[2]):
+            mine = slice(h * group, (h + 1) * group)
+            qq, kk, vv = q[row, lo:hi, mine].double(), k[row, lo:hi, h].double(), v[row, lo:hi, h].double()
+            up, oo = dout[row, lo:hi, mine].double(), out[row, lo:hi, mine].double()
+            s, e = _scores(qq, kk, scale)
+            sums = lse[row, mine, lo:hi].double()[..., None]
+            p = torch.exp(s - sums)
+            e = e + 4 * F32 * sums.abs() + 8 * F32 * (1 + (s - sums).abs().nan_to_num(0.0, 0.0, 0.0))
+            dp = torch.einsum("ihd,jd->hij", up, vv)
+            delta = torch.einsum("ihd,ihd->hi", up, oo)[..., None]
+            ds = p * (dp - delta)
+            dp_off = (d / 16 + 16) * F32 * torch.einsum("ihd,jd->hij", up.abs(), vv.abs()) \
+                + (d / 8 + 8) * F32 * torch.einsum("ihd,ihd->hi", up.abs(), oo.abs())[..., None]
+            open_ = torch.ones(n, n, dtype=torch.bool, device=q.device).tril()
+            p_off = p * (e + half) + floor_p * open_
+            ds_off = ds.abs() * (e + half + 4 * F32) + p * dp_off + floor_s * open_
+            add = (n * group / 16 + 32) * F32
+            for i, (x, x_off, rows, eq) in enumerate(((ds * scale, ds_off * scale, kk, "hij,jd->ihd"),
+                                                      (ds * scale, ds_off * scale, qq, "hij,ihd->jd"),
+                                                      (p, p_off, up, "hij,ihd->jd"))):
+                at = (row, slice(lo, hi), mine if i == 0 else h)
+                res[i][at] = torch.einsum(eq, x, rows)
+                off[i][at] = torch.einsum(eq, x_off + add * x.abs(), rows.abs())
+    return res, off
+
+
 def near(got, want, slack, what):
     """got is want's rounding to its type, give or take `slack` before the rounding; NaN in want: not looked at."""
     live = ~want.isnan()
