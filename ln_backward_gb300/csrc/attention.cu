@@ -10,6 +10,9 @@ constexpr int kPair = 2 * kRows;             // queries of a CTA: two tiles that
 constexpr int kSoftmaxWarp = 4;              // first of eight: four for each tile
 constexpr int kThreads = (kSoftmaxWarp + 8) * 32;
 
+// A block's sum of P, above which a row's maximum is looked for again: far from fp16's end.
+constexpr float kMost = 8192.f;
+
 template <int Blocks>                        // of 64 columns of a head
 struct Layout {
     static constexpr int kTileBytes = Blocks * kBox;
@@ -165,11 +168,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             auto reads = [&](int t, int i) { return it.blocks(t) && i < blocks && blocks - 1 - i < it.blocks(t); };
             auto scores = [&](int t, int place) {
                 if (elect_one()) {
-                    uint32_t a = tile_desc(q0 + t * L::kTileBytes, false), b = tile_desc(ring0 + place * L::kTileBytes, false);
-                    for (int k = 0; k < steps; ++k) {
-                        const uint32_t at = k < 4 ? k * 2 : (kBox >> 4) + (k - 4) * 2;
-                        mma_smem(score + t * kRows, a + at, b + at, by_rows, k > 0);
-                    }
+                    product_by_rows<Blocks>(score + t * kRows, tile_desc(q0 + t * L::kTileBytes, false),
+                                            tile_desc(ring0 + place * L::kTileBytes, false), steps, by_rows);
                     mma_done(s_full + 8 * t);
                 }
                 __syncwarp();
@@ -198,9 +198,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         tmem_fence_after();
                         const bool first = i == 0 || !reads(t, i - 1);
                         if (elect_one()) {
-                            const uint32_t b = tile_desc(ring0 + value % L::kRing * L::kTileBytes, true);
-                            for (int k = 0; k < kRows / 16; ++k)
-                                mma_tmem(result + t * kRows, score + t * kRows + 8 * k, b + k * (2048 >> 4), by_cols, !first || k > 0);
+                            product_over_tokens(result + t * kRows, score + t * kRows, kRows / 4,
+                                                tile_desc(ring0 + value % L::kRing * L::kTileBytes, true), by_cols, !first);
                             if (i + 1 == blocks) mma_done(o_full + 8 * t);
                         }
                         __syncwarp();
@@ -225,88 +224,93 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         int have = 0, items = 0;
         bool ok = true;
         for (; more && ok && it.blocks(t); more = false, ++items) {
-            float top = 0.f, base = 0.f;     // the maximum that P is taken against, and it times scale_log2
-            unsigned long long total[2] = {0, 0};
+            float base = 0.f;                // P is 2^(score * scale_log2 - base)
+            unsigned long long total = 0;
             for (int i = 0; i < it.blocks(t); ++i, ++have) {
                 if (!__all_sync(0xffffffffu, mbar_wait(s_full + 8 * t, have & 1, &p))) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after();
-                // The row's scores in two halves: the maximum over the second, then the first, which stays in
-                // registers while the second comes again behind it.  (Whole rows in registers leave none for the rest.)
-                uint32_t a[32], b[32];
-                tmem_load32(mine + 64, a);
-                tmem_load32(mine + 96, b);
-                tmem_wait(a);
-                tmem_wait(b);
-                auto hide = [&](uint32_t (&x)[32], int from) {       // tokens behind the row's own
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = from + e > row ? 0xff800000u : x[e];
-                };
-                float m4[4] = {__int_as_float(0xff800000), __int_as_float(0xff800000), __int_as_float(0xff800000), __int_as_float(0xff800000)};
-                auto highest = [&](const uint32_t (&x)[32]) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        m4[e / 2 & 3] = fmaxf(m4[e / 2 & 3], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-                };
-                const bool own = i == 0;     // the block of the tile's own tokens
-                if (own) hide(a, 64), hide(b, 96);
-                highest(a);
-                highest(b);
-                tmem_load32(mine, a);
-                tmem_load32(mine + 32, b);
-                tmem_wait(a);
-                tmem_wait(b);
-                if (own) hide(a, 0), hide(b, 32);
-                highest(a);
-                highest(b);
-                const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                if (i == 0) {
-                    top = m == __int_as_float(0xff800000) ? 0.f : m;
-                    base = top * p.scale_log2;
-                } else if (__any_sync(0xffffffffu, m * p.scale_log2 > base + 8.f)) {
-                    // P may reach 2^8 before everything is taken against a new maximum
-                    const float next = fmaxf(top, m), f = exp2_fast(base - next * p.scale_log2);
-                    top = next;
-                    base = next * p.scale_log2;
-                    const unsigned long long f2 = pair_of(f, f);
-                    total[0] = mul_pair(total[0], f2);
-                    total[1] = mul_pair(total[1], f2);
-                    for (int x = 0; x < cols; x += 16) {
-                        uint32_t o[16];
-                        tmem_read16(sum + x, o);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_store16(sum + x, o);
-                    }
-                }
-                const unsigned long long b2 = pair_of(-base, -base);
-                auto powers = [&](const uint32_t (&x)[32], uint32_t to) {
-                    uint32_t w[16];
+                uint32_t a[32], b[32], w[4][16];
+                unsigned long long sums[2];
+                // 32 columns from g * 32 on: P, and its sum
+                auto powers = [&](const uint32_t (&x)[32], int g) {
+                    const unsigned long long b2 = pair_of(-base, -base);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float lo, hi;
                         split_pair(fma_pair(pair_of(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, b2), lo, hi);
                         lo = exp2_fast(lo);
                         hi = exp2_fast(hi);
-                        total[e & 1] = add_pair(total[e & 1], pair_of(lo, hi));
-                        w[e] = pack2<Fmt>(lo, hi);
+                        sums[e & 1] = add_pair(sums[e & 1], pair_of(lo, hi));
+                        w[g][e] = pack2<Fmt>(lo, hi);
                     }
-                    tmem_store16(to, w);
                 };
-                // (P's columns lie over the first half's scores, which are in registers by now)
-                uint32_t c[32];
-                tmem_load32(mine + 64, c);
-                powers(a, mine);
-                tmem_wait(c);
-                tmem_load32(mine + 96, a);
-                powers(b, mine + 16);
-                if (own) hide(c, 64);
-                powers(c, mine + 32);
-                tmem_wait(a);
-                if (own) hide(a, 96);
-                powers(a, mine + 48);
+                auto hide = [&](uint32_t (&x)[32], int from) {       // tokens behind the row's own
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = from + e > row ? 0xff800000u : x[e];
+                };
+                auto all_powers = [&](bool own) {                    // the next columns come meanwhile
+                    sums[0] = sums[1] = 0;
+                    tmem_load32(mine, a);
+                    tmem_load32(mine + 32, b);
+                    tmem_wait(a);
+                    if (own) hide(a, 0);
+                    powers(a, 0);
+                    tmem_wait(b);
+                    tmem_load32(mine + 64, a);
+                    if (own) hide(b, 32);
+                    powers(b, 1);
+                    tmem_wait(a);
+                    tmem_load32(mine + 96, b);
+                    if (own) hide(a, 64);
+                    powers(a, 2);
+                    tmem_wait(b);
+                    if (own) hide(b, 96);
+                    powers(b, 3);
+                };
+                auto highest = [&](bool own) {
+                    float m4[4] = {__int_as_float(0xff800000), __int_as_float(0xff800000), __int_as_float(0xff800000), __int_as_float(0xff800000)};
+                    for (int x = 0; x < kRows; x += 32) {
+                        tmem_load32(mine + x, a);
+                        tmem_wait(a);
+                        if (own) hide(a, x);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            m4[e / 2 & 3] = fmaxf(m4[e / 2 & 3], fmaxf(__uint_as_float(a[e]), __uint_as_float(a[e + 1])));
+                    }
+                    return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                };
+                if (i == 0) {                // the block of the tile's own tokens
+                    const float m = highest(true);
+                    base = m == __int_as_float(0xff800000) ? 0.f : m * p.scale_log2;
+                    all_powers(true);
+                } else {
+                    // P against what it was taken against before; where a row's sum shows that it grew beyond
+                    // kMost, everything is taken against the new maximum.
+                    all_powers(false);
+                    float lo, hi;
+                    split_pair(add_pair(sums[0], sums[1]), lo, hi);
+                    const bool grew = !(lo + hi <= kMost);       // (one row's growth leaves the others as they are)
+                    if (__any_sync(0xffffffffu, grew)) {
+                        const float most = highest(false) * p.scale_log2, next = grew ? fmaxf(base, most) : base,
+                                    f = exp2_fast(base - next);
+                        base = next;
+                        total = mul_pair(total, pair_of(f, f));
+                        for (int x = 0; x < cols; x += 16) {
+                            uint32_t o[16];
+                            tmem_read16(sum + x, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_store16(sum + x, o);
+                        }
+                        all_powers(false);
+                    }
+                }
+                total = add_pair(total, add_pair(sums[0], sums[1]));
+#pragma unroll
+                for (int g = 0; g < 4; ++g) tmem_store16(mine + 16 * g, w[g]);       // over scores that are done with
                 tmem_stored();
                 tmem_fence_before();
                 __syncwarp();
@@ -314,7 +318,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             }
             if (!ok) break;
             float l0, l1;
-            split_pair(add_pair(total[0], total[1]), l0, l1);
+            split_pair(total, l0, l1);
             const float l = l0 + l1, inv = 1.f / l;
             if (!__all_sync(0xffffffffu, mbar_wait(o_full + 8 * t, items & 1, &p))) break;
             tmem_fence_after();

@@ -33,22 +33,66 @@ __host__ __device__ constexpr uint32_t instruction(bool bf16, int cols, bool b_m
     return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)b_mn << 16) | ((uint32_t)(cols / 8) << 17) |
            ((uint32_t)(kRows / 16) << 24);
 }
-// d += A B^T, 16 contracted elements.  A in shared memory, or 16-bit pairs in tensor memory.
-__device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-        "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh), "r"(accumulate)
-        : "memory");
+// 16 contracted elements.  A in shared memory, or 16-bit pairs in tensor memory.  Add: onto what d holds; otherwise
+// `add` says whether.
+template <bool Add>
+__device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    if constexpr (Add)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.eq.u32 p, 0, 0;\n\t"
+            "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, 0, 0;\n\t"
+            "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh)
+            : "memory");
 }
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-        "mov.b64 y, {%2, %4};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh), "r"(accumulate)
-        : "memory");
+template <bool Add>
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add = 1) {
+    if constexpr (Add)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.eq.u32 p, 0, 0;\n\t"
+            "mov.b64 y, {%2, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+            "mov.b64 y, {%2, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh), "r"(add)
+            : "memory");
+}
+// Two tiles' rows against each other over `steps` times 16 of a head's elements, by descriptors of their first boxes.
+// An MMA of 128 x 128 x 16 takes 64 clocks, and one thread issues them all: no loop where the head is whole.
+template <int Blocks>
+__device__ __forceinline__ void product_by_rows(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc) {
+    mma_smem<false>(d, a, b, idesc);
+    if (steps == 4 * Blocks) {
+#pragma unroll
+        for (int k = 1; k < 4 * Blocks; ++k) {
+            const uint32_t at = (k < 4 ? 0 : kBox >> 4) + k % 4 * 2;
+            mma_smem<true>(d, a + at, b + at, idesc);
+        }
+    } else {
+        for (int k = 1; k < steps; ++k) {
+            const uint32_t at = (k < 4 ? 0 : kBox >> 4) + k % 4 * 2;
+            mma_smem<true>(d, a + at, b + at, idesc);
+        }
+    }
+}
+// d (+)= A B over the 128 tokens of B's rows.  A lies in tensor memory, 64 tokens (32 columns) and the others
+// `apart` columns behind.
+__device__ __forceinline__ void product_over_tokens(uint32_t d, uint32_t a, uint32_t apart, uint32_t b, uint32_t idesc, bool add) {
+    mma_tmem<false>(d, a, b, idesc, add);
+#pragma unroll
+    for (int k = 1; k < kRows / 16; ++k) mma_tmem<true>(d, a + (k < 4 ? 8 * k : apart + 8 * (k - 4)), b + k * (2048 >> 4), idesc);
 }
 // Arrives on an mbarrier of this CTA when the MMAs issued so far are done.
 __device__ __forceinline__ void mma_done(uint32_t bar) {

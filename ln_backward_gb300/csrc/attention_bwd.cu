@@ -14,10 +14,13 @@ constexpr int kHalfCols = kRows / 2;         // columns of a tile that one of th
 template <int Blocks>
 struct Layout {
     static constexpr int kTileBytes = Blocks * kBox;
-    static constexpr int kRing = Blocks == 1 ? 4 : 2;            // tiles of each of the two streams
+    static constexpr int kRing0 = Blocks == 1 ? 5 : 3;           // tiles of the stream that is read last
+    static constexpr int kRing1 = Blocks == 1 ? 4 : 2;           // and of the other
     static constexpr int kStream = 2 * kTileBytes;               // behind the two tiles that stay
-    static constexpr int kAux = kStream + 2 * kRing * kTileBytes;
-    static constexpr int kBars = kAux + 2 * 2 * kRows * 4;       // log sums and deltas of two query tiles
+    static constexpr int kAux = kStream + (kRing0 + kRing1) * kTileBytes;
+    static constexpr int kBars = kAux + 2 * kRows * 4;           // log sums and deltas of a query tile
+    static __device__ __forceinline__ int ring(int i) { return i ? kRing1 : kRing0; }
+    static __device__ __forceinline__ int at(int i, int n) { return kStream + (i * kRing0 + n % ring(i)) * kTileBytes; }
     static constexpr int kBytes = kBars + 1024 + 256;            // alignment, barriers
 };
 
@@ -51,7 +54,7 @@ __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((12
 struct Bars {
     uint32_t keep, ring[2], ring_free[2], first, second, first_taken, second_taken, aux, aux_free, all, tail, drain, slot;
 };
-template <int Ring>
+template <class L>
 __device__ __forceinline__ Bars bars_at(uint32_t at) {
     Bars b;
     auto take = [&](int n) {
@@ -60,16 +63,16 @@ __device__ __forceinline__ Bars bars_at(uint32_t at) {
         return x;
     };
     b.keep = take(2);
-    for (int i = 0; i < 2; ++i) b.ring[i] = take(Ring), b.ring_free[i] = take(Ring);
+    b.ring[0] = take(L::kRing0), b.ring[1] = take(L::kRing1), b.ring_free[0] = take(L::kRing0), b.ring_free[1] = take(L::kRing1);
     b.first = take(2), b.second = take(1), b.first_taken = take(1), b.second_taken = take(1);
     b.aux = take(2), b.aux_free = take(2), b.all = take(1), b.tail = take(1), b.drain = take(1), b.slot = at;
     return b;
 }
-template <int Ring>
+template <class L>
 __device__ __forceinline__ void init_bars(const Bars& b) {
     for (int i = 0; i < 2; ++i) {
         mbar_init(b.keep + 8 * i, 1);
-        for (int s = 0; s < Ring; ++s) {
+        for (int s = 0; s < L::ring(i); ++s) {
             mbar_init(b.ring[i] + 8 * s, 1);
             mbar_init(b.ring_free[i] + 8 * s, 1);
         }
@@ -105,22 +108,6 @@ __device__ __forceinline__ void load_tile(unsigned char* smem, uint32_t smem0, u
     __syncwarp();
 }
 
-// A product of 128 x 128 over a head's elements, both operands by rows.
-__device__ __forceinline__ void product_by_rows(uint32_t d, uint32_t a_tile, uint32_t b_tile, int steps, uint32_t idesc) {
-    const uint32_t a = tile_desc(a_tile, false), b = tile_desc(b_tile, false);
-    for (int k = 0; k < steps; ++k) {
-        const uint32_t at = k < 4 ? k * 2 : (kBox >> 4) + (k - 4) * 2;
-        mma_smem(d, a + at, b + at, idesc, k > 0);
-    }
-}
-// d += A B over 128 tokens, A in the two halves of a tile's tensor memory (see half_of), B's rows the tokens.
-__device__ __forceinline__ void product_over_tokens(uint32_t d, uint32_t a, uint32_t b_tile, uint32_t idesc, bool add) {
-    const uint32_t b = tile_desc(b_tile, true);
-#pragma unroll
-    for (int k = 0; k < kRows / 16; ++k)
-        mma_tmem(d, a + (k < 4 ? 8 * k : kHalfCols + 8 * (k - 4)), b + k * (2048 >> 4), idesc, add || k > 0);
-}
-
 // ---------------------------------------------------------------- dK and dV
 // A CTA has 128 keys of one key head, and walks the query tiles of the sequence from its own on, of every
 // query head of the group.  Transposed: keys are rows, so that P^T and dS^T are left operands as they come.
@@ -134,9 +121,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
     extern __shared__ unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t smem0 = smem_addr(smem);
-    const Bars bar = bars_at<L::kRing>(smem0 + L::kBars);
+    const Bars bar = bars_at<L>(smem0 + L::kBars);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) init_bars<L::kRing>(bar);
+    if (threadIdx.x == 0) init_bars<L>(bar);
     if (warp == 3) tmem_alloc_all(bar.slot);
     tmem_fence_before();
     __syncthreads();
@@ -165,13 +152,14 @@ dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
             const int token = span.first + span.tile * kRows;
             load_tile<Blocks>(smem, smem0, smem0, &map_k, token, kv_head, span.batch, kRows, bar.keep, 0, nullptr, lane, &p);
             for (; n < steps && ok; ++n) {
-                const int s = n % L::kRing, row = tile_of(n) * kRows;
+                const int row = tile_of(n) * kRows;
                 for (int i = 0; i < 2; ++i) {      // queries, gradients
-                    if (n >= L::kRing && !__all_sync(0xffffffffu, mbar_wait(bar.ring_free[i] + 8 * s, (n / L::kRing - 1) & 1, &p))) {
+                    const int ring = L::ring(i), s = n % ring;
+                    if (n >= ring && !__all_sync(0xffffffffu, mbar_wait(bar.ring_free[i] + 8 * s, (n / ring - 1) & 1, &p))) {
                         ok = false;
                         break;
                     }
-                    load_tile<Blocks>(smem, smem0, smem0 + L::kStream + (i * L::kRing + s) * L::kTileBytes, i ? &map_do : &map_q,
+                    load_tile<Blocks>(smem, smem0, smem0 + L::at(i, n), i ? &map_do : &map_q,
                                       span.first + row, head_of(n), span.batch, span.len - row, bar.ring[i] + 8 * s, bar.tail, &tails,
                                       lane, &p);
                     if (n == 0 && i == 0)
@@ -185,20 +173,21 @@ dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
         if (live)
             for (int i = 0; i < 2; ++i) {
                 mbar_wait<kEnd>(bar.keep + 8 * i, 0, &p);
-                for (int q = max(0, n - L::kRing); q < n; ++q) mbar_wait<kEnd>(bar.ring[i] + 8 * (q % L::kRing), (q / L::kRing) & 1, &p);
+                for (int q = max(0, n - L::ring(i)); q < n; ++q)
+                    mbar_wait<kEnd>(bar.ring[i] + 8 * (q % L::ring(i)), (q / L::ring(i)) & 1, &p);
             }
     } else if (warp == 1) {
         const int cols = (p.dim + 15) / 16 * 16;
         const uint32_t by_rows = instruction(kBf, kRows, false), by_cols = instruction(kBf, cols, true);
-        const uint32_t k_tile = smem0, v_tile = smem0 + L::kTileBytes;
-        auto tile = [&](int i, int n) { return smem0 + L::kStream + (i * L::kRing + n % L::kRing) * L::kTileBytes; };
+        const uint32_t k_tile = tile_desc(smem0, false), v_tile = tile_desc(smem0 + L::kTileBytes, false);
+        auto tile = [&](int i, int n) { return smem0 + L::at(i, n); };
         auto wait_ring = [&](int i, int n) {
-            return __all_sync(0xffffffffu, mbar_wait(bar.ring[i] + 8 * (n % L::kRing), (n / L::kRing) & 1, &p));
+            return __all_sync(0xffffffffu, mbar_wait(bar.ring[i] + 8 * (n % L::ring(i)), (n / L::ring(i)) & 1, &p));
         };
         auto scores = [&](int n) {
             if (!wait_ring(0, n)) return false;
             if (elect_one()) {
-                product_by_rows(score, k_tile, tile(0, n), cols / 16, by_rows);
+                product_by_rows<Blocks>(score, k_tile, tile_desc(tile(0, n), false), cols / 16, by_rows);
                 mma_done(bar.first);
             }
             __syncwarp();
@@ -207,7 +196,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
         auto dprobs = [&](int n) {
             if (!wait_ring(1, n)) return false;
             if (elect_one()) {
-                product_by_rows(dprob, v_tile, tile(1, n), cols / 16, by_rows);
+                product_by_rows<Blocks>(dprob, v_tile, tile_desc(tile(1, n), false), cols / 16, by_rows);
                 mma_done(bar.second);
             }
             __syncwarp();
@@ -219,15 +208,15 @@ dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
             // P^T lies over the scores: the next ones follow its product, in order
             if (!__all_sync(0xffffffffu, mbar_wait(bar.first_taken, n & 1, &p))) break;
             tmem_fence_after();
-            if (elect_one()) product_over_tokens(dv, score, tile(1, n), by_cols, n > 0);
+            if (elect_one()) product_over_tokens(dv, score, kHalfCols, tile_desc(tile(1, n), true), by_cols, n > 0);
             __syncwarp();
             if (n + 1 < steps && !scores(n + 1)) break;
             if (!__all_sync(0xffffffffu, mbar_wait(bar.second_taken, n & 1, &p))) break;
             tmem_fence_after();
             if (elect_one()) {
-                product_over_tokens(dk, dprob, tile(0, n), by_cols, n > 0);
-                mma_done(bar.ring_free[0] + 8 * (n % L::kRing));
-                mma_done(bar.ring_free[1] + 8 * (n % L::kRing));
+                product_over_tokens(dk, dprob, kHalfCols, tile_desc(tile(0, n), true), by_cols, n > 0);
+                mma_done(bar.ring_free[0] + 8 * (n % L::kRing0));
+                mma_done(bar.ring_free[1] + 8 * (n % L::kRing1));
                 if (n + 1 == steps) mma_done(bar.all);
             }
             __syncwarp();
@@ -247,14 +236,17 @@ dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
                 const int row = row0 + 32 * i + lane;
                 x[i] = row < span.len ? aux[row] : make_float2(__int_as_float(0x7f800000), 0.f);
             }
-            if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(bar.aux_free + 8 * (n & 1), (n / 2 - 1) & 1, &p))) break;
+            // the log sums are read with the scores, the deltas with dP: each is free for the next tile behind that
+            if (n && !__all_sync(0xffffffffu, mbar_wait(bar.aux_free, (n - 1) & 1, &p))) break;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                table[(n & 1) * 2 * kRows + 32 * i + lane] = x[i].x - kPShift<Fmt>;
-                table[(n & 1) * 2 * kRows + kRows + 32 * i + lane] = x[i].y * f;
-            }
+            for (int i = 0; i < 4; ++i) table[32 * i + lane] = x[i].x - kPShift<Fmt>;
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar.aux + 8 * (n & 1));
+            if (lane == 0) mbar_arrive(bar.aux);
+            if (n && !__all_sync(0xffffffffu, mbar_wait(bar.aux_free + 8, (n - 1) & 1, &p))) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) table[kRows + 32 * i + lane] = x[i].y * f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar.aux + 8);
         }
     } else if (warp >= kWorkWarp && live) {
         const int half = (warp - kWorkWarp) >> 2, quad = warp & 3, row = quad * 32 + lane;
@@ -263,11 +255,10 @@ dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
         const int shift = ds_shift<Fmt>(p.norms);
         const float f = power_of_two(shift - kPShift<Fmt>);
         const unsigned long long c2 = pair_of(p.scale_log2, p.scale_log2), f2 = pair_of(f, f), minus = pair_of(-1.f, -1.f);
+        const float4 *sums = reinterpret_cast<const float4*>(smem + L::kAux) + half * kHalfCols / 4, *deltas = sums + kRows / 4;
         bool ok = true;
         for (int n = 0; n < steps; ++n) {
-            const float4* sums = reinterpret_cast<const float4*>(smem + L::kAux + (n & 1) * 2 * kRows * 4) + half * kHalfCols / 4;
-            const float4* deltas = sums + kRows / 4;
-            if (!__all_sync(0xffffffffu, mbar_wait(bar.aux + 8 * (n & 1), (n / 2) & 1, &p)) ||
+            if (!__all_sync(0xffffffffu, mbar_wait(bar.aux, n & 1, &p)) ||
                 !__all_sync(0xffffffffu, mbar_wait(bar.first, n & 1, &p))) {
                 ok = false;
                 break;
@@ -308,8 +299,12 @@ dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
             tmem_stored();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar.first_taken);
-            if (!__all_sync(0xffffffffu, mbar_wait(bar.second, n & 1, &p))) {
+            if (lane == 0) {
+                mbar_arrive(bar.first_taken);
+                mbar_arrive(bar.aux_free);
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(bar.aux + 8, n & 1, &p)) ||
+                !__all_sync(0xffffffffu, mbar_wait(bar.second, n & 1, &p))) {
                 ok = false;
                 break;
             }
@@ -341,7 +336,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(bar.second_taken);
-                mbar_arrive(bar.aux_free + 8 * (n & 1));
+                mbar_arrive(bar.aux_free + 8);
             }
         }
         if (ok && __all_sync(0xffffffffu, mbar_wait(bar.all, 0, &p))) {
@@ -372,9 +367,9 @@ dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUt
     extern __shared__ unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t smem0 = smem_addr(smem);
-    const Bars bar = bars_at<L::kRing>(smem0 + L::kBars);
+    const Bars bar = bars_at<L>(smem0 + L::kBars);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) init_bars<L::kRing>(bar);
+    if (threadIdx.x == 0) init_bars<L>(bar);
     if (warp == 3) tmem_alloc_all(bar.slot);
     tmem_fence_before();
     __syncthreads();
@@ -401,13 +396,14 @@ dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUt
             const int token = span.first + span.tile * kRows;
             load_tile<Blocks>(smem, smem0, smem0, &map_q, token, head, span.batch, kRows, bar.keep, 0, nullptr, lane, &p);
             for (; n < steps && ok; ++n) {
-                const int s = n % L::kRing, row = (steps - 1 - n) * kRows;
+                const int row = (steps - 1 - n) * kRows;
                 for (int i = 0; i < 2; ++i) {      // keys, values
-                    if (n >= L::kRing && !__all_sync(0xffffffffu, mbar_wait(bar.ring_free[i] + 8 * s, (n / L::kRing - 1) & 1, &p))) {
+                    const int ring = L::ring(i), s = n % ring;
+                    if (n >= ring && !__all_sync(0xffffffffu, mbar_wait(bar.ring_free[i] + 8 * s, (n / ring - 1) & 1, &p))) {
                         ok = false;
                         break;
                     }
-                    load_tile<Blocks>(smem, smem0, smem0 + L::kStream + (i * L::kRing + s) * L::kTileBytes, i ? &map_v : &map_k,
+                    load_tile<Blocks>(smem, smem0, smem0 + L::at(i, n), i ? &map_v : &map_k,
                                       span.first + row, kv_head, span.batch, span.len - row, bar.ring[i] + 8 * s, bar.tail, &tails,
                                       lane, &p);
                     if (n == 0 && i == 0)
@@ -420,20 +416,21 @@ dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUt
         if (live)
             for (int i = 0; i < 2; ++i) {
                 mbar_wait<kEnd>(bar.keep + 8 * i, 0, &p);
-                for (int q = max(0, n - L::kRing); q < n; ++q) mbar_wait<kEnd>(bar.ring[i] + 8 * (q % L::kRing), (q / L::kRing) & 1, &p);
+                for (int q = max(0, n - L::ring(i)); q < n; ++q)
+                    mbar_wait<kEnd>(bar.ring[i] + 8 * (q % L::ring(i)), (q / L::ring(i)) & 1, &p);
             }
     } else if (warp == 1) {
         const int cols = (p.dim + 15) / 16 * 16;
         const uint32_t by_rows = instruction(kBf, kRows, false), by_cols = instruction(kBf, cols, true);
-        const uint32_t q_tile = smem0, do_tile = smem0 + L::kTileBytes;
-        auto tile = [&](int i, int n) { return smem0 + L::kStream + (i * L::kRing + n % L::kRing) * L::kTileBytes; };
+        const uint32_t q_tile = tile_desc(smem0, false), do_tile = tile_desc(smem0 + L::kTileBytes, false);
+        auto tile = [&](int i, int n) { return smem0 + L::at(i, n); };
         auto wait_ring = [&](int i, int n) {
-            return __all_sync(0xffffffffu, mbar_wait(bar.ring[i] + 8 * (n % L::kRing), (n / L::kRing) & 1, &p));
+            return __all_sync(0xffffffffu, mbar_wait(bar.ring[i] + 8 * (n % L::ring(i)), (n / L::ring(i)) & 1, &p));
         };
         auto scores = [&](int n) {
             if (!wait_ring(0, n)) return false;
             if (elect_one()) {
-                product_by_rows(score + (n & 1) * kRows, q_tile, tile(0, n), cols / 16, by_rows);
+                product_by_rows<Blocks>(score + (n & 1) * kRows, q_tile, tile_desc(tile(0, n), false), cols / 16, by_rows);
                 mma_done(bar.first + 8 * (n & 1));
             }
             __syncwarp();
@@ -442,9 +439,9 @@ dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUt
         auto dprobs = [&](int n) {
             if (!wait_ring(1, n)) return false;
             if (elect_one()) {
-                product_by_rows(dprob, do_tile, tile(1, n), cols / 16, by_rows);
+                product_by_rows<Blocks>(dprob, do_tile, tile_desc(tile(1, n), false), cols / 16, by_rows);
                 mma_done(bar.second);
-                mma_done(bar.ring_free[1] + 8 * (n % L::kRing));
+                mma_done(bar.ring_free[1] + 8 * (n % L::kRing1));
             }
             __syncwarp();
             return true;
@@ -458,8 +455,8 @@ dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUt
             tmem_fence_after();
             if (n + 1 < steps && !dprobs(n + 1)) break;
             if (elect_one()) {
-                product_over_tokens(dq, score + (n & 1) * kRows, tile(0, n), by_cols, n > 0);
-                mma_done(bar.ring_free[0] + 8 * (n % L::kRing));
+                product_over_tokens(dq, score + (n & 1) * kRows, kHalfCols, tile_desc(tile(0, n), true), by_cols, n > 0);
+                mma_done(bar.ring_free[0] + 8 * (n % L::kRing0));
                 if (n + 1 == steps) mma_done(bar.all);
             }
             __syncwarp();
