@@ -6,26 +6,28 @@
 namespace tb {
 namespace {
 
-constexpr int kPair = 2 * kRows;             // queries of a CTA: two tiles that share its keys
+constexpr int kItem = 2 * kSpan;             // queries of a pair: two tiles of each CTA share the pair's keys
 constexpr int kSoftmaxWarp = 4;              // first of eight: four for each tile
 constexpr int kThreads = (kSoftmaxWarp + 8) * 32;
-
 // A block's sum of P, above which a row's maximum is looked for again: far from fp16's end.
 constexpr float kMost = 8192.f;
 
 template <int Blocks>                        // of 64 columns of a head
 struct Layout {
-    static constexpr int kTileBytes = Blocks * kBox;
-    static constexpr int kRing = Blocks == 1 ? 8 : 4;            // tiles of keys and values
-    static constexpr int kOut = (2 + kRing) * kTileBytes;        // behind the queries and the ring
+    static constexpr int kTileBytes = Blocks * kBox;             // of queries
+    static constexpr int kKeyBytes = Blocks * kHalfBox;          // half a block's keys
+    static constexpr int kValueBytes = kBox;                     // a block's values, half their columns
+    static constexpr int kStageBytes = kBox, kRing = 8;
+    static constexpr int kStage0 = 2 * kTileBytes;
+    static constexpr int kOut = kStage0 + kRing * kStageBytes;
     static constexpr int kBars = kOut + 8 * kOutStage;
-    static constexpr int kBytes = kBars + 1024 + 256;            // alignment, barriers
+    static constexpr int kBytes = kBars + 1024 + 512;            // alignment, barriers
 };
 
 struct Args {
     Tokens tokens;
     int heads, group, dim;    // query heads, of which `group` share a key head
-    int tiles;                // pairs of query tiles of a batch entry, without offsets
+    int tiles;                // of kItem queries of a batch entry, without offsets
     float scale_log2;         // scale * log2(e)
     void* out;
     int64_t out_batch, out_seq, out_head;    // strides in elements
@@ -34,11 +36,11 @@ struct Args {
     unsigned long long wait_ns;
 };
 
-// What a CTA works on: the queries of tile `tile` (256 of them) and of the tile behind, of one head.
+// What a pair works on: kItem queries of one head.  Tile t of CTA r begins 256 t + 128 r behind the first of them.
 struct Item {
     Span span;
     int head;
-    int blocks0, blocks1;     // of keys that the two tiles of 128 read; 0: no such tile
+    int blocks0, blocks1;     // of 128 keys that the pair's two tiles read; 0: no such tile
     __device__ __forceinline__ int blocks(int t) const { return t ? blocks1 : blocks0; }
 };
 __device__ __forceinline__ bool find_item(const Args& p, unsigned index, Item* it) {
@@ -46,14 +48,14 @@ __device__ __forceinline__ bool find_item(const Args& p, unsigned index, Item* i
     it->head = (int)(index % heads);
     const unsigned slot = index / heads;
     if (p.tokens.offsets) {
-        if (!find_tile(p.tokens, kPair, (int)slot, true, &it->span)) return false;
+        if (!find_tile(p.tokens, kItem, (int)slot, true, &it->span)) return false;
     } else {                  // the longest first, over all heads and batch entries
         const unsigned batch = (unsigned)p.tokens.batch;
         it->span = Span{(int)(slot % batch), 0, p.tokens.seq, p.tiles - 1 - (int)(slot / batch)};
     }
-    const int left = it->span.len - it->span.tile * kPair;
-    it->blocks0 = 2 * it->span.tile + 1;
-    it->blocks1 = left > kRows ? 2 * it->span.tile + 2 : 0;
+    const int all = (it->span.len + kRows - 1) / kRows, left = it->span.len - it->span.tile * kItem;
+    it->blocks0 = min(4 * it->span.tile + 2, all);
+    it->blocks1 = left > kSpan ? min(4 * it->span.tile + 4, all) : 0;
     return true;
 }
 
@@ -61,38 +63,44 @@ __device__ __forceinline__ bool find_item(const Args& p, unsigned index, Item* i
 template <class Fmt, int Blocks>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Args p) {
+                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_out, const __grid_constant__ Args p) {
     using L = Layout<Blocks>;
     using T = typename Fmt::T;
     constexpr bool kBf = std::is_same<Fmt, BF16>::value;
     extern __shared__ unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    const uint32_t q0 = smem_addr(smem), ring0 = q0 + 2 * L::kTileBytes, bar0 = q0 + L::kBars;
-    const uint32_t full = bar0, empty = full + 8 * L::kRing, q_full = empty + 8 * L::kRing, q_empty = q_full + 16,
-                   s_full = q_empty + 16, p_full = s_full + 16, o_full = p_full + 16, o_empty = o_full + 16,
-                   tail = o_empty + 16, drain = tail + 8, slot = drain + 8;
+    const uint32_t q0 = smem_addr(smem), ring0 = q0 + L::kStage0, bar0 = q0 + L::kBars;
+    const uint32_t answer = bar0, full = answer + 16, empty = full + 8 * L::kRing, q_full = empty + 8 * L::kRing, q_empty = q_full + 16,
+                   s_full = q_empty + 16, p_full = s_full + 16, o_full = p_full + 16, o_empty = o_full + 16, tail = o_empty + 16,
+                   drain = tail + 8, done = drain + 8, work_full = done + 8, work_empty = work_full + 8, issued = work_empty + 8,
+                   slot = issued + 12;
+    static_assert(L::kRing * 16 + 6 * 16 + 5 * 8 + 16 + 16 <= 512);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cta_rank();
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::kRing; ++i) {
-            mbar_init(full + 8 * i, 1);
+            mbar_init(full + 8 * i, 2);      // an arrival of either CTA, and their bytes
             mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full + 8 * i, 1);
+            mbar_init(q_full + 8 * i, 2);
             mbar_init(q_empty + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, 4);
+            mbar_init(p_full + 8 * i, 8);    // the warps of a tile, of both CTAs
             mbar_init(o_full + 8 * i, 1);
-            mbar_init(o_empty + 8 * i, 4);
+            mbar_init(o_empty + 8 * i, 8);
         }
         mbar_init(tail, 1);
         mbar_init(drain, 1);
+        mbar_init(done, 1);
+        init_work(work_full, work_empty, 2 * (1 + 8) + 1);     // the warps that load, those of the softmax, and the MMAs'
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) tmem_alloc_all(slot);
     tmem_fence_before();
     __syncthreads();
+    cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + (slot - q0));
     pdl_wait();
@@ -102,128 +110,169 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     // The tensor memory: scores of both tiles (their first half becomes P), then results.
     const uint32_t score = tmem, result = tmem + 2 * kRows;
     const int cols = (p.dim + 15) / 16 * 16;
-    Item it;
-    bool more = find_item(p, blockIdx.x, &it);
+    // What each warp works on, and behind it: asked for while the present work is begun.
+    Work work{answer, work_full, work_empty, 0};
+    Item it, next;
+    bool live = find_item(p, blockIdx.x >> 1, &it), next_live = false, more = true;
+    auto ask = [&] {
+        unsigned cluster;
+        more = next_work(work, lane, &cluster, &p);
+        next_live = more && find_item(p, cluster, &next);
+    };
+    auto move_on = [&] { it = next, live = next_live; };
 
     if (warp == 0) {
-        int n = 0, items = 0, tails = 0;     // tiles staged, items, tails mended
+        int n = 0, queries[2] = {0, 0}, tails = 0;       // keys and values staged, tiles of queries, ends mended
         bool ok = true;
-        for (; more && ok; more = false, ++items) {
+        for (; more; move_on()) {
+            if (!ok || !live) {
+                ask();
+                continue;
+            }
             const int blocks = max(it.blocks0, it.blocks1), kv_head = it.head / p.group;
-            const int q_row = it.span.first + it.span.tile * kPair;
             for (int t = 0; t < 2; ++t) {
                 if (!it.blocks(t)) continue;
-                // (one item: the queries' place is free)
+                if (queries[t] && !__all_sync(0xffffffffu, mbar_wait(q_empty + 8 * t, (queries[t] - 1) & 1, &p))) {
+                    ok = false;
+                    break;
+                }
                 if (elect_one()) {
-                    mbar_expect(q_full + 8 * t, L::kTileBytes);
+                    const uint32_t bar = map_to(q_full + 8 * t, 0);
+                    mbar_expect_at(bar, L::kTileBytes);
                     for (int b = 0; b < Blocks; ++b)
-                        tma_tile(q0 + t * L::kTileBytes + b * kBox, &map_q, 64 * b, q_row + t * kRows, it.head, it.span.batch,
-                                 q_full + 8 * t);
+                        tma_tile(q0 + t * L::kTileBytes + b * kBox, &map_q, 64 * b,
+                                 it.span.first + it.span.tile * kItem + t * kSpan + (int)rank * kRows, it.head, it.span.batch, bar);
                 }
                 __syncwarp();
+                ++queries[t];
             }
-            for (int i = 0; i < 2 * blocks && ok; ++i, ++n) {      // keys, values of the last block, then the one before
-                const int s = n % L::kRing, block = blocks - 1 - i / 2;
-                const bool values = i & 1;
+            ask();
+            // keys, values of the last block, then of the one before
+            for (int i = 0; i < 2 * blocks && ok; ++i) {
+                const int s = n % L::kRing, block = blocks - 1 - i / 2, row = it.span.first + block * kRows;
                 if (n >= L::kRing && !__all_sync(0xffffffffu, mbar_wait(empty + 8 * s, (n / L::kRing - 1) & 1, &p))) {
                     ok = false;
                     break;
                 }
                 const int rows = it.span.len - block * kRows;
-                // Behind the sequence's end lie other tokens or nothing: P is 0 there, but 0 times what they
-                // hold need not be.
-                const bool mend = values && rows < kRows;
-                const uint32_t at = ring0 + s * L::kTileBytes, bar = mend ? tail : full + 8 * s;
-                if (elect_one()) {
-                    mbar_expect(bar, L::kTileBytes);
-                    for (int b = 0; b < Blocks; ++b)
-                        tma_tile(at + b * kBox, values ? &map_v : &map_k, 64 * b, it.span.first + block * kRows, kv_head,
-                                 it.span.batch, bar);
-                }
-                __syncwarp();
-                if (mend) {
-                    if (!__all_sync(0xffffffffu, mbar_wait<kEnd>(tail, tails & 1, &p))) ok = false;
-                    ++tails;
-                    clear_behind<Blocks>(smem + (at - q0), rows, lane);
-                    if (lane == 0) mbar_arrive(full + 8 * s);
-                }
-            }
-        }
-        // The way out: the MMAs, then the loads that no MMA waited for.
-        __syncwarp();
-        mbar_wait<kEnd>(drain, 0, &p);
-        if (items)
-            for (int t = 0; t < 2; ++t)
-                if (it.blocks(t)) mbar_wait<kEnd>(q_full + 8 * t, (items - 1) & 1, &p);
-        for (int i = max(0, n - L::kRing); i < n; ++i) mbar_wait<kEnd>(full + 8 * (i % L::kRing), (i / L::kRing) & 1, &p);
-    } else if (warp == 1) {
-        const uint32_t by_rows = instruction(kBf, kRows, false), by_cols = instruction(kBf, cols, true);
-        const int steps = cols / 16;
-        int n = 0, items = 0;                // tiles of the ring taken
-        int have[2] = {0, 0};                // P taken
-        bool ok = true;
-        for (; more && ok; more = false, ++items) {
-            const int blocks = max(it.blocks0, it.blocks1);
-            // block i from the end is read by a tile when it is not behind the tile's last
-            auto reads = [&](int t, int i) { return it.blocks(t) && i < blocks && blocks - 1 - i < it.blocks(t); };
-            auto scores = [&](int t, int place) {
-                if (elect_one()) {
-                    product_by_rows<Blocks>(score + t * kRows, tile_desc(q0 + t * L::kTileBytes, false),
-                                            tile_desc(ring0 + place * L::kTileBytes, false), steps, by_rows);
-                    mma_done(s_full + 8 * t);
-                }
-                __syncwarp();
-            };
-            auto wait_ring = [&](int i) { return __all_sync(0xffffffffu, mbar_wait(full + 8 * (i % L::kRing), (i / L::kRing) & 1, &p)); };
-            for (int t = 0; t < 2 && ok; ++t)
-                if (it.blocks(t)) ok = __all_sync(0xffffffffu, mbar_wait(q_full + 8 * t, items & 1, &p));
-            if (!ok || !wait_ring(n)) break;
-            for (int t = 0; t < 2; ++t)
-                if (reads(t, 0)) scores(t, n % L::kRing);
-            if (elect_one()) mma_done(empty + 8 * (n % L::kRing));
-            __syncwarp();
-            for (int i = 0; i < blocks && ok; ++i) {
-                const int value = n + 1 + 2 * i, key = value + 1;
-                if (!wait_ring(value) || (i + 1 < blocks && !wait_ring(key))) {
-                    ok = false;
-                    break;
-                }
-                for (int t = 0; t < 2; ++t) {
-                    if (reads(t, i)) {
-                        if (!__all_sync(0xffffffffu, mbar_wait(p_full + 8 * t, have[t] & 1, &p))) {
-                            ok = false;
-                            break;
-                        }
-                        ++have[t];
-                        tmem_fence_after();
-                        const bool first = i == 0 || !reads(t, i - 1);
-                        if (elect_one()) {
-                            product_over_tokens(result + t * kRows, score + t * kRows, kRows / 4,
-                                                tile_desc(ring0 + value % L::kRing * L::kTileBytes, true), by_cols, !first);
-                            if (i + 1 == blocks) mma_done(o_full + 8 * t);
-                        }
-                        __syncwarp();
+                const uint32_t at = ring0 + s * L::kStageBytes, leader = map_to(full + 8 * s, 0);
+                if (i & 1) {
+                    // Behind the sequence's end lie other tokens or nothing: P is 0 there, but 0 times what they
+                    // hold need not be.
+                    const bool mend = rows < kRows;
+                    const uint32_t bar = mend ? map_to(tail, rank) : leader;
+                    if (elect_one()) {
+                        mbar_expect_at(bar, L::kValueBytes);
+                        tma_tile(at, &map_v, (int)rank * cols / 2, row, kv_head, it.span.batch, bar);
                     }
-                    if (reads(t, i + 1)) scores(t, key % L::kRing);
-                }
-                if (!ok) break;
-                if (elect_one()) {
-                    mma_done(empty + 8 * (value % L::kRing));
-                    if (i + 1 < blocks) mma_done(empty + 8 * (key % L::kRing));
+                    __syncwarp();
+                    if (mend) {
+                        mbar_wait<kEnd>(tail, tails++ & 1, &p);
+                        clear_behind(smem + (at - q0), 1, kRows, rows, lane);
+                        if (lane == 0) mbar_arrive_release(leader);
+                    }
+                } else if (elect_one()) {
+                    mbar_expect_at(leader, L::kKeyBytes);
+                    for (int b = 0; b < Blocks; ++b)
+                        tma_tile(at + b * kHalfBox, &map_k, 64 * b, row + (int)rank * (kRows / 2), kv_head, it.span.batch, leader);
                 }
                 __syncwarp();
+                ++n;
             }
-            n += 2 * blocks;
         }
-        if (elect_one()) mma_done(drain);
+        const int mine[3] = {n, queries[0], queries[1]}, rings[3] = {L::kRing, 1, 1};
+        way_out<3>(rank, mine, rings, drain, done, issued, smem + (issued - q0), &p, [&](int s, int i, uint32_t* parity) {
+            if (s) {
+                *parity = i & 1;
+                return q_full + 8 * (s - 1);
+            }
+            *parity = (i / L::kRing) & 1;
+            return full + 8 * (i % L::kRing);
+        });
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const uint32_t by_rows = instruction(kBf, kRows, false), by_cols = instruction(kBf, cols, true);
+            int n = 0, have[2] = {0, 0}, uses[2] = {0, 0};       // tiles of the ring taken, P taken, items of a tile
+            bool ok = true;
+            auto wait_ring = [&](int i) { return __all_sync(0xffffffffu, mbar_wait(full + 8 * (i % L::kRing), (i / L::kRing) & 1, &p)); };
+            for (; more; move_on()) {
+                if (!ok || !live) {
+                    ask();
+                    continue;
+                }
+                const int blocks = max(it.blocks0, it.blocks1);
+                // block i from the end is read by a tile when it is not behind the tile's last
+                auto reads = [&](int t, int i) { return i < blocks && blocks - 1 - i < it.blocks(t); };
+                auto scores = [&](int t, int place, bool last) {
+                    if (elect_one()) {
+                        product_by_rows<Blocks>(score + t * kRows, q0 + t * L::kTileBytes, ring0 + place * L::kStageBytes, cols / 16, by_rows);
+                        mma_commit(s_full + 8 * t);
+                        if (last) mma_commit(q_empty + 8 * t);
+                    }
+                    __syncwarp();
+                };
+                ok = wait_ring(n);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (!ok || !it.blocks(t)) continue;
+                    ok = __all_sync(0xffffffffu, mbar_wait(q_full + 8 * t, uses[t] & 1, &p));
+                    if (ok && reads(t, 0)) scores(t, n % L::kRing, blocks == 1);
+                }
+                if (ok && elect_one()) mma_commit(empty + 8 * (n % L::kRing));
+                __syncwarp();
+                ask();
+                for (int i = 0; i < blocks && ok; ++i) {
+                    const int value = n + 1 + 2 * i, key = value + 1;
+                    if (!wait_ring(value) || (i + 1 < blocks && !wait_ring(key))) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (ok && reads(t, i)) {
+                            const bool first = i == 0 || !reads(t, i - 1);
+                            ok = __all_sync(0xffffffffu, mbar_wait(p_full + 8 * t, have[t] & 1, &p)) &&
+                                 (!first || !uses[t] || __all_sync(0xffffffffu, mbar_wait<kRelaxed>(o_empty + 8 * t, (uses[t] - 1) & 1, &p)));
+                            if (!ok) break;
+                            ++have[t];
+                            tmem_fence_after();
+                            if (elect_one()) {
+                                product_over_tokens(result + t * kRows, score + t * kRows, kRows / 4,
+                                                    ring0 + value % L::kRing * L::kStageBytes, by_cols, !first);
+                                if (i + 1 == blocks) mma_commit(o_full + 8 * t);
+                            }
+                            __syncwarp();
+                        }
+                        if (ok && reads(t, i + 1)) scores(t, key % L::kRing, i + 2 == blocks);
+                    }
+                    if (!ok) break;
+                    if (elect_one()) {
+                        mma_commit(empty + 8 * (value % L::kRing));
+                        if (i + 1 < blocks) mma_commit(empty + 8 * (key % L::kRing));
+                    }
+                    __syncwarp();
+                }
+                n += 2 * blocks;
+                for (int t = 0; t < 2; ++t) uses[t] += it.blocks(t) != 0;
+            }
+            if (elect_one()) mma_commit(drain);
+        }
+    } else if (warp == 3) {
+        hand_out(work, rank, &p);
     } else if (warp >= kSoftmaxWarp) {
         const int t = (warp - kSoftmaxWarp) >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t mine = score + t * kRows + lanes, sum = result + t * kRows + lanes;
+        const uint32_t taken = map_to(p_full + 8 * t, 0), free = map_to(o_empty + 8 * t, 0);
         const unsigned long long c2 = pair_of(p.scale_log2, p.scale_log2);
-        int have = 0, items = 0;
+        const float lowest = __int_as_float(0xff800000);
+        int have = 0, uses = 0;              // scores taken, results
         bool ok = true;
-        for (; more && ok && it.blocks(t); more = false, ++items) {
+        for (; more; move_on()) {
+            ask();
+            if (!ok || !live || !it.blocks(t)) continue;
+            const int in_seq = it.span.tile * kItem + t * kSpan + (int)rank * kRows;     // the tile's first query
+            const int rows = min(32, it.span.len - in_seq - quad * 32);                  // of this warp, none: 0 or less
             float base = 0.f;                // P is 2^(score * scale_log2 - base)
             unsigned long long total = 0;
             for (int i = 0; i < it.blocks(t); ++i, ++have) {
@@ -232,118 +281,142 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     break;
                 }
                 tmem_fence_after();
-                uint32_t a[32], b[32], w[4][16];
-                unsigned long long sums[2];
-                // 32 columns from g * 32 on: P, and its sum
-                auto powers = [&](const uint32_t (&x)[32], int g) {
-                    const unsigned long long b2 = pair_of(-base, -base);
+                const int ahead = in_seq - (it.blocks(t) - 1 - i) * kRows;       // of the tile's first query before the block
+                uint32_t w[2][32];
+                if (rows <= 0 || ahead < 0) {        // nobody's queries (whatever P holds stays in their rows), or a block
+                                                     // that begins behind the tile's last
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float lo, hi;
-                        split_pair(fma_pair(pair_of(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, b2), lo, hi);
-                        lo = exp2_fast(lo);
-                        hi = exp2_fast(hi);
-                        sums[e & 1] = add_pair(sums[e & 1], pair_of(lo, hi));
-                        w[g][e] = pack2<Fmt>(lo, hi);
-                    }
-                };
-                auto hide = [&](uint32_t (&x)[32], int from) {       // tokens behind the row's own
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = from + e > row ? 0xff800000u : x[e];
-                };
-                auto all_powers = [&](bool own) {                    // the next columns come meanwhile
-                    sums[0] = sums[1] = 0;
-                    tmem_load32(mine, a);
-                    tmem_load32(mine + 32, b);
-                    tmem_wait(a);
-                    if (own) hide(a, 0);
-                    powers(a, 0);
-                    tmem_wait(b);
-                    tmem_load32(mine + 64, a);
-                    if (own) hide(b, 32);
-                    powers(b, 1);
-                    tmem_wait(a);
-                    tmem_load32(mine + 96, b);
-                    if (own) hide(a, 64);
-                    powers(a, 2);
-                    tmem_wait(b);
-                    if (own) hide(b, 96);
-                    powers(b, 3);
-                };
-                auto highest = [&](bool own) {
-                    float m4[4] = {__int_as_float(0xff800000), __int_as_float(0xff800000), __int_as_float(0xff800000), __int_as_float(0xff800000)};
-                    for (int x = 0; x < kRows; x += 32) {
-                        tmem_load32(mine + x, a);
-                        tmem_wait(a);
-                        if (own) hide(a, x);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            m4[e / 2 & 3] = fmaxf(m4[e / 2 & 3], fmaxf(__uint_as_float(a[e]), __uint_as_float(a[e + 1])));
-                    }
-                    return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                };
-                if (i == 0) {                // the block of the tile's own tokens
-                    const float m = highest(true);
-                    base = m == __int_as_float(0xff800000) ? 0.f : m * p.scale_log2;
-                    all_powers(true);
+                    for (int e = 0; e < 32; ++e) w[0][e] = w[1][e] = 0;
                 } else {
-                    // P against what it was taken against before; where a row's sum shows that it grew beyond
-                    // kMost, everything is taken against the new maximum.
-                    all_powers(false);
-                    float lo, hi;
-                    split_pair(add_pair(sums[0], sums[1]), lo, hi);
-                    const bool grew = !(lo + hi <= kMost);       // (one row's growth leaves the others as they are)
-                    if (__any_sync(0xffffffffu, grew)) {
-                        const float most = highest(false) * p.scale_log2, next = grew ? fmaxf(base, most) : base,
-                                    f = exp2_fast(base - next);
-                        base = next;
-                        total = mul_pair(total, pair_of(f, f));
-                        for (int x = 0; x < cols; x += 16) {
-                            uint32_t o[16];
-                            tmem_read16(sum + x, o);
+                    unsigned long long sums[2];
+                    auto hide = [&](uint32_t (&x)[32], int at) {     // tokens behind the row's own
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_store16(sum + x, o);
+                        for (int e = 0; e < 32; ++e) x[e] = at + e > row ? 0xff800000u : x[e];
+                    };
+                    auto all_powers = [&](bool hides) {              // P of the block, and its sum
+                        sums[0] = sums[1] = 0;
+                        const unsigned long long b2 = pair_of(-base, -base);
+                        auto powers = [&](const uint32_t (&x)[32], int g) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float lo, hi;
+                                split_pair(fma_pair(pair_of(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, b2), lo, hi);
+                                lo = exp2_fast(lo);
+                                hi = exp2_fast(hi);
+                                sums[e & 1] = add_pair(sums[e & 1], pair_of(lo, hi));
+                                w[g / 2][16 * (g & 1) + e] = pack2<Fmt>(lo, hi);
+                            }
+                        };
+                        uint32_t x[32], y[32];       // the next columns come meanwhile
+                        tmem_load32(mine, x);
+                        tmem_wait(x);
+                        tmem_load32(mine + 32, y);
+                        if (hides) hide(x, 0);
+                        powers(x, 0);
+                        tmem_wait(y);
+                        tmem_load32(mine + 64, x);
+                        if (hides) hide(y, 32);
+                        powers(y, 1);
+                        tmem_wait(x);
+                        tmem_load32(mine + 96, y);
+                        if (hides) hide(x, 64);
+                        powers(x, 2);
+                        tmem_wait(y);
+                        if (hides) hide(y, 96);
+                        powers(y, 3);
+                    };
+                    auto highest = [&](bool hides) {                 // (by the whole warp)
+                        float m4[4] = {lowest, lowest, lowest, lowest};
+#pragma unroll 1         // (four blocks of scores at once would take all registers)
+                        for (int g = 0; g < 4; ++g) {
+                            uint32_t x[32];
+                            tmem_load32(mine + 32 * g, x);
+                            tmem_wait(x);
+                            if (hides) hide(x, 32 * g);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2)
+                                m4[e / 2 & 3] = fmaxf(m4[e / 2 & 3], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
                         }
+                        return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    };
+                    if (ahead == 0) {        // the block of the tile's own tokens: up to here there is nothing to rescale
+                        const float m = highest(true);
+                        base = m == lowest ? 0.f : m * p.scale_log2;
+                        all_powers(true);
+                    } else {
+                        // P against what it was taken against before; where a row's sum shows that it grew beyond
+                        // kMost, everything is taken against the new maximum.  (One row's growth leaves the others
+                        // as they are.)
                         all_powers(false);
-                    }
-                }
-                total = add_pair(total, add_pair(sums[0], sums[1]));
+                        float lo, hi;
+                        split_pair(add_pair(sums[0], sums[1]), lo, hi);
+                        const bool grew = !(lo + hi <= kMost);
+                        if (__any_sync(0xffffffffu, grew)) {
+                            const float most = highest(false) * p.scale_log2, next = grew ? fmaxf(base, most) : base,
+                                        f = exp2_fast(base - next);
+                            base = next;
+                            total = mul_pair(total, pair_of(f, f));
+                            for (int x = 0; x < cols; x += 16) {
+                                uint32_t o[16];
+                                tmem_read16(sum + x, o);
 #pragma unroll
-                for (int g = 0; g < 4; ++g) tmem_store16(mine + 16 * g, w[g]);       // over scores that are done with
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_store16(sum + x, o);
+                            }
+                            all_powers(false);
+                        }
+                    }
+                    total = add_pair(total, add_pair(sums[0], sums[1]));
+                }
+                tmem_store32(mine, w[0]);    // over scores that are done with
+                tmem_store32(mine + 32, w[1]);
                 tmem_stored();
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + 8 * t);
+                if (lane == 0) mbar_arrive_cluster(taken);
             }
-            if (!ok) break;
+            if (!ok) continue;
+            if (!__all_sync(0xffffffffu, mbar_wait(o_full + 8 * t, uses++ & 1, &p))) {
+                ok = false;
+                continue;
+            }
+            tmem_fence_after();
             float l0, l1;
             split_pair(total, l0, l1);
-            const float l = l0 + l1, inv = 1.f / l;
-            if (!__all_sync(0xffffffffu, mbar_wait(o_full + 8 * t, items & 1, &p))) break;
-            tmem_fence_after();
-            const int in_seq = it.span.tile * kPair + t * kRows + quad * 32, rows = min(32, it.span.len - in_seq);
-            const int64_t token = it.span.first + in_seq;
+            const float l = l0 + l1;
+            const int token = it.span.first + in_seq + quad * 32;
             if (p.lse && lane < rows)
                 p.lse[((int64_t)it.span.batch * p.heads + it.head) * p.tokens.seq + token + lane] =
                     0.693147180559945309f * (base + log2f(l));
-            T* out = static_cast<T*>(p.out) + it.span.batch * p.out_batch + token * p.out_seq + it.head * p.out_head;
-            unsigned char* box = smem + L::kOut + (warp - kSoftmaxWarp) * kOutStage;
-            store_rows<Fmt>(box, sum, inv, out, p.out_seq, rows, p.dim, lane);
+            auto give_back = [&] {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(free);
+            };
+            if (rows > 0) {
+                const Place to{&map_out, static_cast<T*>(p.out) + it.span.batch * p.out_batch + token * p.out_seq + it.head * p.out_head,
+                               p.out_seq, token, it.head, it.span.batch};
+                store_rows<Fmt>(smem + L::kOut + (warp - kSoftmaxWarp) * kOutStage, sum, 1.f / l, to, rows, 0, p.dim, lane, give_back);
+            } else {
+                give_back();
+            }
         }
+        stored_all(lane);
     }
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
+    cluster_sync();             // no CTA leaves while the other may signal or read it
     if (warp == 2) tmem_free_all(tmem);
 }
 
 // ---------------------------------------------------------------- host
 template <class Fmt, int Blocks>
-tb_status launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const Args& p, int64_t items, cudaStream_t st) {
+tb_status launch(const CUtensorMap (&m)[4], const Args& p, int64_t items, cudaStream_t st) {
     using L = Layout<Blocks>;
-    if (resident_ctas_per_sm(reinterpret_cast<const void*>(&attention_kernel<Fmt, Blocks>), kThreads, L::kBytes) < 1) return TB_ERR_CUDA;
-    return launch_pdl(attention_kernel<Fmt, Blocks>, dim3((unsigned)items), dim3(kThreads), L::kBytes, st, q, k, v, p) == cudaSuccess
+    if (resident_clusters(reinterpret_cast<const void*>(&attention_kernel<Fmt, Blocks>), kThreads, L::kBytes, 2) < 1) return TB_ERR_CUDA;
+    return launch_clusters<true>(attention_kernel<Fmt, Blocks>, dim3((unsigned)(2 * items)), dim3(kThreads), L::kBytes, st, 2, m[0], m[1], m[2],
+                                 m[3], p) == cudaSuccess
                ? launch_status()
                : TB_ERR_CUDA;
 }
@@ -373,12 +446,12 @@ extern "C" tb_status tb_attention(const tb_heads* q, const tb_heads* k, const tb
     }
     if (overlap(sums, starts) || overlap(starts, range_of_view(view[3], head_dim))) return TB_ERR_ALIAS;
     if (offsets && sequences == 0) return TB_OK;
-    const int64_t tiles = ceil_div(seq, kPair), slots = offsets ? slots_of(seq, sequences, kPair) : tiles * batch;
-    if (slots > ((1ll << 31) - 1) / q->heads) return TB_ERR_INVALID_VALUE;
+    const int64_t tiles = ceil_div(seq, kItem), slots = offsets ? slots_of(seq, sequences, kItem) : tiles * batch;
+    if (slots > (1ll << 30) / q->heads) return TB_ERR_INVALID_VALUE;
     const bool bf = dtype == TB_BF16;
-    CUtensorMap maps[3];
-    for (int i = 0; i < 3; ++i)
-        if (!make_heads_map(&maps[i], *given[i], batch, seq, head_dim, bf)) return TB_ERR_CUDA;
+    CUtensorMap m[4];
+    for (int i = 0; i < 4; ++i)
+        if (!make_heads_map(&m[i], *given[i], batch, seq, head_dim, i == 1 ? kRows / 2 : kRows, bf, i == 3)) return TB_ERR_CUDA;
     Args p{};
     if (!(p.err = device_error_word())) return TB_ERR_CUDA;
     p.tokens = Tokens{offsets, (int)sequences, (int)batch, (int)seq, p.err};
@@ -391,6 +464,6 @@ extern "C" tb_status tb_attention(const tb_heads* q, const tb_heads* k, const tb
     p.wait_ns = kWaitLimitNs;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t items = slots * q->heads;
-    if (head_dim <= 64) return bf ? launch<BF16, 1>(maps[0], maps[1], maps[2], p, items, st) : launch<F16, 1>(maps[0], maps[1], maps[2], p, items, st);
-    return bf ? launch<BF16, 2>(maps[0], maps[1], maps[2], p, items, st) : launch<F16, 2>(maps[0], maps[1], maps[2], p, items, st);
+    if (head_dim <= 64) return bf ? launch<BF16, 1>(m, p, items, st) : launch<F16, 1>(m, p, items, st);
+    return bf ? launch<BF16, 2>(m, p, items, st) : launch<F16, 2>(m, p, items, st);
 }

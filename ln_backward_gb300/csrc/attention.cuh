@@ -1,5 +1,5 @@
-// attention.cuh -- what the kernels of causal attention share: the sequences of a call, one-CTA
-// tcgen05 products with the left operand in shared or tensor memory, and loads by TMA.
+// attention.cuh -- what the kernels of causal attention share: the sequences of a call, tcgen05
+// products of a pair of CTAs with the first operand in shared or tensor memory, and loads by TMA.
 #pragma once
 
 #include "heads_view.cuh"
@@ -8,95 +8,83 @@
 namespace tb {
 namespace {
 
-constexpr int kRows = 128;                   // queries or keys of a tile: TMEM's lanes
+constexpr int kRows = 128;                   // queries or keys of a CTA's tile: TMEM's lanes
+constexpr int kSpan = 2 * kRows;             // of a pair of CTAs
 constexpr int kBox = kRows * 64 * 2;         // 64 columns of a tile, swizzled over 128 bytes
+constexpr int kHalfBox = kBox / 2;           // and of half its rows
+
+// A pair of CTAs (a cluster of two SMs) works on 256 rows, 128 each, against tiles of 128 tokens that both need.
+// tcgen05.mma.cta_group::2 takes each CTA's rows from its own shared or tensor memory and half of the other
+// operand from either: the operands' way through shared memory, 128 bytes a clock, would bound products of one
+// CTA (128 x 128 x 16: 64 clocks of MMA, 64 of reading both operands, and the next tiles come in beside).
 
 // ---------------------------------------------------------------- PTX
+// Hands shared memory that this CTA's threads wrote to the pair's first CTA.  (What lies in tensor memory is handed
+// over between tcgen05 fences by mbar_arrive_cluster: a release waits about 900 clocks.)
+__device__ __forceinline__ void mbar_arrive_release(uint32_t remote_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// 64 columns from x on of 128 rows from y on of one head of one batch entry; zeros outside the tensor.
+__device__ __forceinline__ void mbar_expect_at(uint32_t remote_bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(remote_bar), "r"(bytes) : "memory");
+}
+// A box of 64 columns from x on of the map's number of rows from y on of one head of one batch entry; zeros
+// outside the tensor.  Counted on an mbarrier of either CTA.
 __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int x, int y, int head, int batch, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
         " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(head), "r"(batch), "r"(bar)
         : "memory");
 }
-// Operand descriptors (see desc_low): rows of 64 columns contracted along the columns, or, kMn, along
-// the rows, with the next 64 columns a box further on.
-constexpr uint32_t kMn = 1;
-__device__ __forceinline__ uint32_t tile_desc(uint32_t addr, bool mn) {
-    return ((addr & 0x3FFFF) >> 4) | ((mn ? (uint32_t)kBox >> 4 : 1u) << 16);
-}
+// Instruction descriptor of 256 rows by `cols`; b_mn: the second operand's rows are contracted.
 __host__ __device__ constexpr uint32_t instruction(bool bf16, int cols, bool b_mn) {
     return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)b_mn << 16) | ((uint32_t)(cols / 8) << 17) |
-           ((uint32_t)(kRows / 16) << 24);
+           ((uint32_t)(kSpan / 16) << 24);
 }
-// 16 contracted elements.  A in shared memory, or 16-bit pairs in tensor memory.  Add: onto what d holds; otherwise
-// `add` says whether.
+// 16 contracted elements, the first operand 16-bit pairs in tensor memory.  Add: onto what d holds; otherwise `add`
+// says whether.
 template <bool Add>
-__device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
-    if constexpr (Add)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.eq.u32 p, 0, 0;\n\t"
-            "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-            "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, 0, 0;\n\t"
-            "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-            "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh)
-            : "memory");
-}
-template <bool Add>
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add = 1) {
+__device__ __forceinline__ void mma_pair_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add = 1) {
     if constexpr (Add)
         asm volatile(
             "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.eq.u32 p, 0, 0;\n\t"
             "mov.b64 y, {%2, %4};\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
             "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh)
             : "memory");
     else
         asm volatile(
             "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\t"
             "mov.b64 y, {%2, %4};\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
             "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh), "r"(add)
             : "memory");
 }
-// Two tiles' rows against each other over `steps` times 16 of a head's elements, by descriptors of their first boxes.
-// An MMA of 128 x 128 x 16 takes 64 clocks, and one thread issues them all: no loop where the head is whole.
+// 256 rows against 128 over `steps` times 16 of a head's elements.  a: 128 rows of each CTA, b: 64, by the addresses
+// of their first boxes.  One thread issues all MMAs, each of 64 clocks: no loop where the head is whole.
 template <int Blocks>
-__device__ __forceinline__ void product_by_rows(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc) {
-    mma_smem<false>(d, a, b, idesc);
+__device__ __forceinline__ void product_by_rows(uint32_t d, uint32_t a_tile, uint32_t b_tile, int steps, uint32_t idesc) {
+    const uint32_t a = desc_low<false>(a_tile), b = desc_low<false>(b_tile);
+    mma_pair<false>(d, a, b, idesc, 0);
     if (steps == 4 * Blocks) {
 #pragma unroll
-        for (int k = 1; k < 4 * Blocks; ++k) {
-            const uint32_t at = (k < 4 ? 0 : kBox >> 4) + k % 4 * 2;
-            mma_smem<true>(d, a + at, b + at, idesc);
-        }
+        for (int k = 1; k < 4 * Blocks; ++k)
+            mma_pair<true>(d, a + (k < 4 ? 0 : kBox >> 4) + k % 4 * 2, b + (k < 4 ? 0 : kHalfBox >> 4) + k % 4 * 2, idesc, 1);
     } else {
-        for (int k = 1; k < steps; ++k) {
-            const uint32_t at = (k < 4 ? 0 : kBox >> 4) + k % 4 * 2;
-            mma_smem<true>(d, a + at, b + at, idesc);
-        }
+        for (int k = 1; k < steps; ++k)
+            mma_pair<true>(d, a + (k < 4 ? 0 : kBox >> 4) + k % 4 * 2, b + (k < 4 ? 0 : kHalfBox >> 4) + k % 4 * 2, idesc, 1);
     }
 }
-// d (+)= A B over the 128 tokens of B's rows.  A lies in tensor memory, 64 tokens (32 columns) and the others
-// `apart` columns behind.
-__device__ __forceinline__ void product_over_tokens(uint32_t d, uint32_t a, uint32_t apart, uint32_t b, uint32_t idesc, bool add) {
-    mma_tmem<false>(d, a, b, idesc, add);
+// d (+)= A B over the 128 tokens of B's rows, of which each CTA has half the columns.  A lies in tensor memory,
+// 64 tokens (32 columns) and the others `apart` columns behind.
+__device__ __forceinline__ void product_over_tokens(uint32_t d, uint32_t a, uint32_t apart, uint32_t b_tile, uint32_t idesc, bool add) {
+    const uint32_t b = desc_low<true>(b_tile);
+    mma_pair_tmem<false>(d, a, b, idesc, add);
 #pragma unroll
-    for (int k = 1; k < kRows / 16; ++k) mma_tmem<true>(d, a + (k < 4 ? 8 * k : apart + 8 * (k - 4)), b + k * (2048 >> 4), idesc);
-}
-// Arrives on an mbarrier of this CTA when the MMAs issued so far are done.
-__device__ __forceinline__ void mma_done(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    for (int k = 1; k < kRows / 16; ++k) mma_pair_tmem<true>(d, a + (k < 4 ? 8 * k : apart + 8 * (k - 4)), b + k * (2048 >> 4), idesc);
 }
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -105,70 +93,226 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+        "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+        "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+        : "memory");
+}
+// A quarter of the lanes' 16 (those of `addr`) by 64 columns, as a matrix instruction's accumulator lies in a warp:
+// r[4 k + 2 h + b] is row lane / 4 + 8 h, column 8 k + lane % 4 * 2 + b.  There after tmem_wait.
+__device__ __forceinline__ void tmem_load_16x64(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+        "%30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+// The same 16 rows by 64 columns as 16-bit pairs, 32 columns: r[2 k + h] is row lane / 4 + 8 h, columns 8 k +
+// lane % 4 * 2 and the one behind.
+__device__ __forceinline__ void tmem_store_16x64(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_alloc_all(uint32_t slot) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(kTmemCols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_free_all(uint32_t tmem) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 __device__ __forceinline__ unsigned long long mul_pair(unsigned long long a, unsigned long long b) {
     unsigned long long r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// Two values as 16-bit pairs lie in TMEM and in registers: the first in the low half.
+// Two values as 16-bit pairs lie in TMEM and in registers: the first in the low half.  (Volatile: it stays where it is
+// written.  Sunk behind a branch to where the pairs are stored, it keeps twice the registers alive.)
 template <class Fmt>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
-    if constexpr (std::is_same<Fmt, BF16>::value) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    if constexpr (std::is_same<Fmt, BF16>::value) asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
-// 32 rows of a result from tensor memory, a row a lane, times the lane's factor and rounded, to `rows` rows
-// `stride` apart: through shared memory, from which eight lanes write a row's 64 columns.  `box`: the warp's own,
-// 1,024-byte aligned.
-constexpr int kOutStage = 32 * 128;
-template <class Fmt>
-__device__ __forceinline__ void store_rows(unsigned char* box, uint32_t tmem, float factor, typename Fmt::T* out, int64_t stride,
-                                           int rows, int dim, int lane) {
-    for (int x = 0; x < dim; x += 64) {
-        uint32_t o[2][32];
-        tmem_load32(tmem + x, o[0]);
-        tmem_load32(tmem + x + 32, o[1]);
-        tmem_wait(o[0]);
-        tmem_wait(o[1]);
+// Where a result's rows go: by TMA in boxes of 32 columns by 32 rows, or, where fewer rows are a sequence's, one by one.
+struct Place {
+    const CUtensorMap* map;
+    void* data;               // of the warp's first row
+    int64_t stride;           // from one row to the next, in elements
+    int token, head, batch;   // of that row
+};
+// Columns from .. dim - 1 of 32 rows of a result from tensor memory, a row a lane, times the lane's factor and rounded,
+// to the first `rows` rows of `to`, through the warp's two boxes of shared memory.  A lane's 16-byte pieces lie at piece ^ (row / 2 & 3), the
+// pattern of a 64-byte swizzle: no two lanes of a quarter warp share banks.  `read` is called when the last columns
+// are in registers.  (Stores from registers held the warps up for the time that the memory took: 4,000 clocks for
+// 64 KB of every CTA at once.)
+constexpr int kOutBox = 32 * 64, kOutStage = 2 * kOutBox;
+template <class Fmt, class F>
+__device__ __forceinline__ void store_rows(unsigned char* boxes, uint32_t tmem, float factor, const Place& to, int rows, int from,
+                                           int dim, int lane, F read) {
+    for (int x = from; x < dim; x += 32) {
+        unsigned char* box = boxes + (x & 32 ? kOutBox : 0);
+        uint32_t o[32];
+        tmem_load32(tmem + x, o);
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");       // the box is free
+        tmem_wait(o);
         __syncwarp();
+        if (x + 32 >= dim) read();
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
+        for (int g = 0; g < 4; ++g) {
             uint32_t h[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                h[e] = pack2<Fmt>(__uint_as_float(o[g / 4][g % 4 * 8 + 2 * e]) * factor,
-                                  __uint_as_float(o[g / 4][g % 4 * 8 + 2 * e + 1]) * factor);
-            *reinterpret_cast<uint4*>(box + lane * 128 + ((g ^ (lane & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+                h[e] = pack2<Fmt>(__uint_as_float(o[8 * g + 2 * e]) * factor, __uint_as_float(o[8 * g + 2 * e + 1]) * factor);
+            *reinterpret_cast<uint4*>(box + lane * 64 + ((g ^ (lane / 2 & 3)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
         }
-        __syncwarp();
-        const int c = lane & 7;              // 16 bytes of a row
-        if (x + 8 * c < dim)
+        if (rows >= 32) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(to.map),
+                             "r"(x), "r"(to.token), "r"(to.head), "r"(to.batch), "r"(smem_addr(box))
+                             : "memory");
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+        } else {
+            __syncwarp();
+            const int c = lane & 3;
 #pragma unroll
-            for (int y = lane >> 3; y < 32; y += 4)
-                if (y < rows)
-                    *reinterpret_cast<uint4*>(out + y * stride + x + 8 * c) =
-                        *reinterpret_cast<const uint4*>(box + y * 128 + ((c ^ (y & 7)) * 16));
+            for (int i = 0; i < 4; ++i) {
+                const int y = lane / 4 + 8 * i;
+                if (y < rows && x + 8 * c < dim)
+                    *reinterpret_cast<uint4*>(static_cast<typename Fmt::T*>(to.data) + y * to.stride + x + 8 * c) =
+                        *reinterpret_cast<const uint4*>(box + y * 64 + ((c ^ (y / 2 & 3)) * 16));
+            }
+            __syncwarp();
+        }
     }
 }
+__device__ __forceinline__ void stored_all(int lane) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
 
-// A tile of `Blocks` boxes whose rows from `rows` on are to be zeros, which whatever lies there need not be
-// times 0.  By a whole warp, before the tile is handed to the MMAs.
-template <int Blocks>
-__device__ __forceinline__ void clear_behind(unsigned char* tile, int rows, int lane) {
-    for (int b = 0; b < Blocks; ++b)
-        for (int x = rows * 8 + lane; x < kRows * 8; x += 32) *reinterpret_cast<uint4*>(tile + b * kBox + x * 16) = make_uint4(0, 0, 0, 0);
+// Rows from `rows` on of `boxes` boxes as zeros: whatever lies behind a sequence's end need not be 0 times 0.  By
+// a whole warp, before the tile is handed to the MMAs.
+__device__ __forceinline__ void clear_behind(unsigned char* tile, int boxes, int box_rows, int rows, int lane) {
+    for (int b = 0; b < boxes; ++b)
+        for (int x = max(rows, 0) * 8 + lane; x < box_rows * 8; x += 32)
+            *reinterpret_cast<uint4*>(tile + (b * box_rows * 8 + x) * 16) = make_uint4(0, 0, 0, 0);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
+}
+
+// ---------------------------------------------------------------- work
+// A pair stays on its SMs: its first CTA asks for the next cluster of the grid that has not started, whose work
+// the pair then does.  (A cluster's launch, set-up and first loads take longer than short tiles.)  Both CTAs get the
+// answer, one at a time: each warp that needs it reads it and says so, then the first CTA asks again.  The answers
+// come to the clusters as they get done, so uneven sequences even out.  A warp whose wait gave up reads on without
+// working, so that the others come to their end.
+struct Work {
+    uint32_t answer, full, empty;    // 16 bytes, 16-byte aligned; barriers
+    uint32_t parity;
+};
+__device__ __forceinline__ void init_work(uint32_t full, uint32_t empty, int readers) {   // warps of both CTAs that work
+    mbar_init(full, 1);
+    mbar_init(empty, readers + 1);                   // and the second CTA's that hands out
+}
+// By one warp of each CTA: asks until there is nothing left.
+template <class P>
+__device__ __forceinline__ void hand_out(const Work& w, uint32_t rank, const P* p) {
+    for (uint32_t n = 0;; ++n) {
+        if (elect_one()) {
+            mbar_expect(w.full, 16);
+        }
+        __syncwarp();
+        if (rank == 0) {
+            if (n && !__all_sync(0xffffffffu, mbar_wait<kWork>(w.empty, (n - 1) & 1, p))) return;
+            if (elect_one())
+                asm volatile(
+                    "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128"
+                    " [%0], [%1];" ::"r"(w.answer),
+                    "r"(w.full)
+                    : "memory");
+            __syncwarp();
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait<kWork>(w.full, n & 1, p))) return;
+        uint32_t more;
+        asm volatile(
+            "{\n\t.reg .b128 r;\n\t.reg .pred q;\n\tld.shared.b128 r, [%1];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 q, r;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+            : "=r"(more)
+            : "r"(w.answer)
+            : "memory");
+        __syncwarp();
+        if (rank == 1 && elect_one()) mbar_arrive_release(map_to(w.empty, 0));
+        if (!more) return;
+    }
+}
+// By every warp that works: the next cluster's number; false when there is none, or a wait gave up.
+template <class P>
+__device__ __forceinline__ bool next_work(Work& w, int lane, unsigned* cluster, const P* p) {
+    if (!__all_sync(0xffffffffu, mbar_wait<kWork>(w.full, w.parity, p))) return false;
+    w.parity ^= 1;
+    uint32_t more, x = 0;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred q;\n\tld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 q, r;\n\tselp.u32 %0, 1, 0, q;\n\t"
+        "mov.u32 %1, 0;\n\t@q clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(more), "=r"(x)
+        : "r"(w.answer)
+        : "memory");
+    // (the arrival names what was read, and so comes behind it)
+    __syncwarp();
+    if (lane == 0)
+        asm volatile("{\n\t.reg .b32 t;\n\tand.b32 t, %1, 0;\n\tadd.u32 t, t, %0;\n\t"
+                     "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [t];\n\t}" ::"r"(map_to(w.empty, 0)), "r"(x + more)
+                     : "memory");
+    *cluster = x >> 1;
+    return more != 0;
+}
+
+// The way out of the warp that loads: the MMAs, which the first CTA issues, then the boxes, which end on the first
+// CTA's barriers.  Each phase of those counts an arrival of either CTA.  After a wait that gave up one may have
+// loaded what the other has not: the first CTA arrives in its place, so that every phase ends with its last box.
+// `mine`: loads of this CTA by stream, bar_of(stream, i, &parity): the barrier of load i, rings: how many a stream
+// has open at most.  `words`: the streams' counts of the second CTA, in the first one's shared memory.
+template <int Streams, class P, class F>
+__device__ __forceinline__ void way_out(uint32_t rank, const int (&mine)[Streams], const int (&rings)[Streams], uint32_t drain,
+                                        uint32_t done, uint32_t words, const unsigned char* words_at, const P* p, F bar_of) {
+    if (rank == 1 && elect_one()) {
+#pragma unroll
+        for (int s = 0; s < Streams; ++s)
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to(words + 4 * s, 0)), "r"(mine[s]) : "memory");
+        mbar_arrive_release(map_to(done, 0));
+    }
+    __syncwarp();
+    const bool ended = __all_sync(0xffffffffu, mbar_wait<kWork>(drain, 0, p));
+    if (rank != 0 || !ended || !__all_sync(0xffffffffu, mbar_wait<kEnd>(done, 0, p))) return;
+#pragma unroll
+    for (int s = 0; s < Streams; ++s) {
+        const int peer = reinterpret_cast<const volatile int*>(words_at)[s], all = max(mine[s], peer);
+        uint32_t parity;
+        if (elect_one())
+            for (int i = min(mine[s], peer); i < all; ++i) mbar_arrive(bar_of(s, i, &parity));
+        __syncwarp();
+        for (int i = max(0, all - rings[s]); i < all; ++i) {
+            const uint32_t bar = bar_of(s, i, &parity);
+            mbar_wait<kEnd>(bar, parity, p);
+        }
+    }
 }
 
 // ---------------------------------------------------------------- sequences
@@ -213,23 +357,25 @@ __device__ __forceinline__ bool find_tile(const Tokens& t, int size, int slot, b
 }
 
 // ---------------------------------------------------------------- host
-// A tensor of heads as a caller describes it, [batch, seq, heads, head_dim], as boxes of 64 columns by 128 tokens.
-inline bool make_heads_map(CUtensorMap* map, const tb_heads& h, int64_t batch, int64_t seq, int64_t dim, bool bf16) {
+// A tensor of heads as a caller describes it, [batch, seq, heads, head_dim], as boxes of 64 columns by some tokens,
+// swizzled over 128 bytes; `out`: of 32 columns by 32 tokens, swizzled over 64.
+inline bool make_heads_map(CUtensorMap* map, const tb_heads& h, int64_t batch, int64_t seq, int64_t dim, int tokens, bool bf16,
+                           bool out = false) {
     const EncodeFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)seq, (cuuint64_t)h.heads, (cuuint64_t)batch};
     const cuuint64_t row = (cuuint64_t)dim * 2;      // of a dimension of size 1, whose stride is anything
     const cuuint64_t strides[3] = {seq > 1 ? (cuuint64_t)h.stride_seq * 2 : row, h.heads > 1 ? (cuuint64_t)h.stride_head * 2 : row,
                                    batch > 1 ? (cuuint64_t)h.stride_batch * 2 : row};
-    const cuuint32_t box[4] = {64, kRows, 1, 1};
+    const cuuint32_t box[4] = {out ? 32u : 64u, out ? 32u : (cuuint32_t)tokens, 1, 1};
     const cuuint32_t ones[4] = {1, 1, 1, 1};
     return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, h.data, dims, strides, box, ones,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, out ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // What every entry point checks of a call's sizes.
-constexpr int64_t kMaxTokens = 1ll << 30;    // of a batch entry: token numbers are 32-bit
+constexpr int64_t kMaxTokens = 1ll << 25;    // of a batch entry: a tile's work stays well inside the limit of its waits
 constexpr int64_t kMaxHeadDim = 128;
 inline tb_status check_call(int64_t batch, int64_t seq, int64_t dim, const int64_t* offsets, int64_t sequences, float scale,
                             tb_dtype dtype) {

@@ -9,25 +9,43 @@ namespace {
 
 constexpr int kWorkWarp = 4;                 // first of the eight that turn scores into P and dS
 constexpr int kThreads = (kWorkWarp + 8) * 32;
-constexpr int kHalfCols = kRows / 2;         // columns of a tile that one of the two warps of a row quarter takes
+constexpr int kHalfCols = kRows / 2;         // columns of a tile that one of the two warps of some rows takes
 
-template <int Blocks>
+// Shared memory: two tiles that stay while a CTA works on its rows, and the tiles that stream by.  Those are staged in
+// both of the forms that products take them in, each CTA half: 64 tokens with all columns, to be multiplied by rows,
+// and 128 tokens with half the columns, to be summed over the tokens.
+template <int Blocks, int... Rings>          // of 64 columns of a head; places of each stream
 struct Layout {
+    static constexpr int kStreams = sizeof...(Rings);
     static constexpr int kTileBytes = Blocks * kBox;
-    static constexpr int kRing0 = Blocks == 1 ? 5 : 3;           // tiles of the stream that is read last
-    static constexpr int kRing1 = Blocks == 1 ? 4 : 2;           // and of the other
-    static constexpr int kStream = 2 * kTileBytes;               // behind the two tiles that stay
-    static constexpr int kAux = kStream + (kRing0 + kRing1) * kTileBytes;
+    static constexpr int kStageBytes = kBox;
+    static constexpr int kStages = (Rings + ...);
+    static constexpr int kStage0 = 2 * kTileBytes;
+    static constexpr int kOut = kStage0 + kStages * kStageBytes;
+    static constexpr int kAux = kOut + 8 * kOutStage;
     static constexpr int kBars = kAux + 2 * kRows * 4;           // log sums and deltas of a query tile
-    static __device__ __forceinline__ int ring(int i) { return i ? kRing1 : kRing0; }
-    static __device__ __forceinline__ int at(int i, int n) { return kStream + (i * kRing0 + n % ring(i)) * kTileBytes; }
-    static constexpr int kBytes = kBars + 1024 + 256;            // alignment, barriers
+    static constexpr int kBytes = kBars + 1024 + 512;            // alignment, barriers
+    static __host__ __device__ constexpr int ring(int s) {
+        constexpr int r[kStreams] = {Rings...};
+        return r[s];
+    }
+    static __host__ __device__ constexpr int first(int s) {      // stage of a stream
+        int n = 0;
+        for (int i = 0; i < s; ++i) n += ring(i);
+        return n;
+    }
 };
+// Queries and gradients of the output by rows, then both summed over.
+template <int Blocks>
+using LayoutKv = Layout<Blocks, 2, 2, 2, 2>;
+// Keys and values by rows, keys summed over.
+template <int Blocks>
+using LayoutQ = Layout<Blocks, 2, 2, 3>;
 
 struct Args {
     Tokens tokens;
     int heads, kv_heads, group, dim;
-    int tiles;                // of a batch entry, without offsets
+    int tiles;                // of 256 tokens of a batch entry, without offsets
     float scale, scale_log2;
     const float2* aux;        // [batch][heads][seq]: lse * log2(e), dout . out
     const unsigned* norms;    // fp16: the largest norms of a dout and of a v, as bits
@@ -50,9 +68,10 @@ __device__ __forceinline__ int ds_shift(const unsigned* norms) {
 }
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }
 
-// What both kernels set up and take down.
+// Barriers of either kernel.
 struct Bars {
-    uint32_t keep, ring[2], ring_free[2], first, second, first_taken, second_taken, aux, aux_free, all, tail, drain, slot;
+    uint32_t answer, keep, keep_free, full, free, first, second, first_taken, second_taken, aux, aux_free, acc, acc_free, tail, drain,
+        done, work_full, work_empty, words, slot;
 };
 template <class L>
 __device__ __forceinline__ Bars bars_at(uint32_t at) {
@@ -62,71 +81,173 @@ __device__ __forceinline__ Bars bars_at(uint32_t at) {
         at += 8 * n;
         return x;
     };
-    b.keep = take(2);
-    b.ring[0] = take(L::kRing0), b.ring[1] = take(L::kRing1), b.ring_free[0] = take(L::kRing0), b.ring_free[1] = take(L::kRing1);
+    b.answer = take(2);                      // (16-byte aligned)
+    b.keep = take(2), b.keep_free = take(2);
+    b.full = take(L::kStages), b.free = take(L::kStages);
     b.first = take(2), b.second = take(1), b.first_taken = take(1), b.second_taken = take(1);
-    b.aux = take(2), b.aux_free = take(2), b.all = take(1), b.tail = take(1), b.drain = take(1), b.slot = at;
+    b.aux = take(2), b.aux_free = take(2), b.acc = take(1), b.acc_free = take(1);
+    b.tail = take(1), b.drain = take(1), b.done = take(1), b.work_full = take(1), b.work_empty = take(1);
+    b.words = take(3), b.slot = at;
+    static_assert((2 + 4 + 2 * L::kStages + 5 + 6 + 5 + 3) * 8 + 4 <= 512 && L::kStreams + 2 <= 6);
     return b;
 }
 template <class L>
-__device__ __forceinline__ void init_bars(const Bars& b) {
+__device__ __forceinline__ void init_bars(const Bars& b, int readers) {
+    for (int i = 0; i < L::kStages; ++i) {
+        mbar_init(b.full + 8 * i, 2);        // an arrival of either CTA, and their bytes
+        mbar_init(b.free + 8 * i, 1);
+    }
     for (int i = 0; i < 2; ++i) {
-        mbar_init(b.keep + 8 * i, 1);
-        for (int s = 0; s < L::ring(i); ++s) {
-            mbar_init(b.ring[i] + 8 * s, 1);
-            mbar_init(b.ring_free[i] + 8 * s, 1);
-        }
+        mbar_init(b.keep + 8 * i, 2);
+        mbar_init(b.keep_free + 8 * i, 1);
         mbar_init(b.first + 8 * i, 1);
         mbar_init(b.aux + 8 * i, 1);
         mbar_init(b.aux_free + 8 * i, 8);
     }
     mbar_init(b.second, 1);
-    mbar_init(b.first_taken, 8);
-    mbar_init(b.second_taken, 8);
-    mbar_init(b.all, 1);
+    mbar_init(b.first_taken, 16);            // the warps of both CTAs
+    mbar_init(b.second_taken, 16);
+    mbar_init(b.acc, 1);
+    mbar_init(b.acc_free, 16);
     mbar_init(b.tail, 1);
     mbar_init(b.drain, 1);
+    mbar_init(b.done, 1);
+    init_work(b.work_full, b.work_empty, readers);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
-// Loads a tile of 128 tokens, those behind the sequence's end as zeros, by a whole warp.
-template <int Blocks, class P>
-__device__ __forceinline__ void load_tile(unsigned char* smem, uint32_t smem0, uint32_t at, const CUtensorMap* map, int token,
-                                          int head, int batch, int rows, uint32_t bar, uint32_t tail, int* tails, int lane,
-                                          const P* p) {
-    const bool mend = rows < kRows;
-    if (elect_one()) {
-        mbar_expect(mend ? tail : bar, Blocks * kBox);
-        for (int b = 0; b < Blocks; ++b) tma_tile(at + b * kBox, map, 64 * b, token, head, batch, mend ? tail : bar);
+// What the loading warp of a CTA has staged, by stream, and the tiles that stay.
+template <class L, int Blocks>
+struct Loader {
+    const Args& p;
+    const Bars& bar;
+    unsigned char* smem;
+    uint32_t smem0, rank;
+    int lane, loaded[L::kStreams], kept[2], tails;
+    __device__ __forceinline__ Loader(const Args& p_, const Bars& b_, unsigned char* s_, uint32_t s0_, uint32_t r_, int l_)
+        : p(p_), bar(b_), smem(s_), smem0(s0_), rank(r_), lane(l_), loaded{}, kept{}, tails(0) {}
+    // One of the tiles that stay: this CTA's 128 tokens from `token` on.
+    __device__ __forceinline__ bool keep(int i, const CUtensorMap* map, int token, int head, int batch) {
+        if (kept[i] && !__all_sync(0xffffffffu, mbar_wait(bar.keep_free + 8 * i, (kept[i] - 1) & 1, &p))) return false;
+        if (elect_one()) {
+            const uint32_t to = map_to(bar.keep + 8 * i, 0);
+            mbar_expect_at(to, L::kTileBytes);
+            for (int b = 0; b < Blocks; ++b) tma_tile(smem0 + i * L::kTileBytes + b * kBox, map, 64 * b, token, head, batch, to);
+        }
+        __syncwarp();
+        ++kept[i];
+        return true;
     }
-    __syncwarp();
-    if (!mend) return;
-    mbar_wait<kEnd>(tail, *tails & 1, p);
-    ++*tails;
-    clear_behind<Blocks>(smem + (at - smem0), rows, lane);
-    if (lane == 0) mbar_arrive(bar);
-    __syncwarp();
-}
+    __device__ __forceinline__ uint32_t place(int s) const { return L::first(s) + loaded[s] % L::ring(s); }
+    __device__ __forceinline__ bool room(int s) const {
+        const int ring = L::ring(s);
+        return loaded[s] < ring || __all_sync(0xffffffffu, mbar_wait(bar.free + 8 * place(s), (loaded[s] / ring - 1) & 1, &p));
+    }
+    // The next tile of stream s (the map's box is half the tokens, by rows, or all of them and half the `cols`
+    // columns): counted on the first CTA's barrier, or on this CTA's own while its end is to be mended.
+    __device__ __forceinline__ void load(int s, bool by_rows, const CUtensorMap* map, int token, int head, int batch, int cols, bool mend) {
+        if (elect_one()) {
+            const uint32_t to = mend ? map_to(bar.tail, rank) : map_to(bar.full + 8 * place(s), 0);
+            const uint32_t at = smem0 + L::kStage0 + place(s) * L::kStageBytes;
+            // (of a tile to be mended, the bytes of all streams are counted before)
+            if (!mend) mbar_expect_at(to, bytes(by_rows));
+            if (by_rows)
+                for (int b = 0; b < Blocks; ++b) tma_tile(at + b * kHalfBox, map, 64 * b, token + (int)rank * (kRows / 2), head, batch, to);
+            else tma_tile(at, map, (int)rank * cols / 2, token, head, batch, to);
+        }
+        __syncwarp();
+    }
+    static __device__ __forceinline__ int bytes(bool by_rows) { return by_rows ? Blocks * kHalfBox : kBox; }
+    __device__ __forceinline__ void expect_mended(int n) {
+        if (elect_one()) mbar_expect_at(map_to(bar.tail, rank), n);
+        __syncwarp();
+    }
+    __device__ __forceinline__ void wait_mended() { mbar_wait<kEnd>(bar.tail, tails++ & 1, &p); }
+    // `rows`: tokens of the tile that are the sequence's.
+    __device__ __forceinline__ void mend(int s, bool by_rows, int rows) {
+        clear_behind(smem + L::kStage0 + place(s) * L::kStageBytes, by_rows ? Blocks : 1, by_rows ? kRows / 2 : kRows,
+                     by_rows ? rows - (int)rank * (kRows / 2) : rows, lane);
+        if (lane == 0) mbar_arrive_release(map_to(bar.full + 8 * place(s), 0));
+        __syncwarp();
+    }
+    __device__ __forceinline__ void leave() const {
+        constexpr int n = L::kStreams + 2;
+        int mine[n], rings[n];
+        for (int s = 0; s < L::kStreams; ++s) mine[s] = loaded[s], rings[s] = L::ring(s);
+        for (int i = 0; i < 2; ++i) mine[L::kStreams + i] = kept[i], rings[L::kStreams + i] = 1;
+        way_out<n>(rank, mine, rings, bar.drain, bar.done, bar.words, smem + (bar.words - smem0), &p, [&](int s, int i, uint32_t* parity) {
+            if (s >= L::kStreams) {
+                *parity = i & 1;
+                return bar.keep + 8 * (s - L::kStreams);
+            }
+            *parity = (i / L::ring(s)) & 1;
+            return bar.full + 8 * (L::first(s) + i % L::ring(s));
+        });
+    }
+};
+
+// What the warp that issues the MMAs takes from a stream: place n.
+template <class L>
+struct Stages {
+    const Args& p;
+    const Bars& bar;
+    uint32_t smem0;
+    __device__ __forceinline__ uint32_t tile(int s, int n) const {
+        return smem0 + L::kStage0 + (L::first(s) + n % L::ring(s)) * L::kStageBytes;
+    }
+    __device__ __forceinline__ bool wait(int s, int n) const {
+        return __all_sync(0xffffffffu, mbar_wait(bar.full + 8 * (L::first(s) + n % L::ring(s)), (n / L::ring(s)) & 1, &p));
+    }
+    __device__ __forceinline__ void free(int s, int n) const { mma_commit(bar.free + 8 * (L::first(s) + n % L::ring(s))); }
+};
+
+struct Maps {
+    CUtensorMap q, q_rows, k, k_rows, v, v_rows, dout, dout_rows;    // 128 tokens a box; _rows: 64
+    CUtensorMap out0, out1;
+};
 
 // ---------------------------------------------------------------- dK and dV
-// A CTA has 128 keys of one key head, and walks the query tiles of the sequence from its own on, of every
-// query head of the group.  Transposed: keys are rows, so that P^T and dS^T are left operands as they come.
+// A pair has 256 keys of one key head, and walks the query tiles of the sequence from its own on, of every
+// query head of the group.  Transposed: keys are rows, so that P^T and dS^T are first operands as they come.
+struct Keys {
+    Span span;
+    int head;
+    int first, each, steps;   // query tiles: the first, of a head, of all heads
+    __device__ __forceinline__ int tile(int i) const { return first + i % each; }
+    __device__ __forceinline__ int query_head(int i, int group) const { return head * group + i / each; }
+};
+__device__ __forceinline__ bool find_keys(const Args& p, unsigned index, Keys* k) {
+    k->head = (int)(index % (unsigned)p.kv_heads);
+    const unsigned slot = index / (unsigned)p.kv_heads;
+    if (p.tokens.offsets) {
+        if (!find_tile(p.tokens, kSpan, (int)slot, false, &k->span)) return false;
+    } else {                  // the longest first
+        const unsigned batch = (unsigned)p.tokens.batch;
+        k->span = Span{(int)(slot % batch), 0, p.tokens.seq, (int)(slot / batch)};
+    }
+    k->first = 2 * k->span.tile;
+    k->each = (k->span.len + kRows - 1) / kRows - k->first;
+    k->steps = k->each * p.group;
+    return true;
+}
+
 template <class Fmt, int Blocks>
-__global__ void __launch_bounds__(kThreads, 1)
-dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-           const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do, const __grid_constant__ Args p) {
-    using L = Layout<Blocks>;
+__global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant__ Maps m, const __grid_constant__ Args p) {
+    using L = LayoutKv<Blocks>;
     using T = typename Fmt::T;
     constexpr bool kBf = std::is_same<Fmt, BF16>::value;
+    enum { kQRows, kDoRows, kDoSum, kQSum };
     extern __shared__ unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t smem0 = smem_addr(smem);
     const Bars bar = bars_at<L>(smem0 + L::kBars);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) init_bars<L>(bar);
+    const uint32_t rank = cta_rank();
+    if (threadIdx.x == 0) init_bars<L>(bar, 2 * 10 + 1);         // loads, log sums, work; the MMAs
     if (warp == 3) tmem_alloc_all(bar.slot);
     tmem_fence_before();
     __syncthreads();
+    cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + (bar.slot - smem0));
     pdl_wait();
@@ -134,245 +255,331 @@ dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CU
     pdl_trigger();
 
     const uint32_t score = tmem, dprob = tmem + kRows, dv = tmem + 2 * kRows, dk = tmem + 3 * kRows;
-    Span span;
-    const int kv_head = (int)(blockIdx.x % (unsigned)p.kv_heads);
-    const unsigned place = blockIdx.x / (unsigned)p.kv_heads;
-    bool live = true;
-    if (p.tokens.offsets) live = find_tile(p.tokens, kRows, (int)place, false, &span);
-    else span = Span{(int)(place % (unsigned)p.tokens.batch), 0, p.tokens.seq, (int)(place / (unsigned)p.tokens.batch)};
-    const int each = live ? (span.len + kRows - 1) / kRows - span.tile : 0;   // query tiles of a head
-    const int steps = each * p.group;
-    auto tile_of = [&](int n) { return span.tile + n % each; };
-    auto head_of = [&](int n) { return kv_head * p.group + n / each; };
+    const int cols = (p.dim + 15) / 16 * 16;
+    Work work{bar.answer, bar.work_full, bar.work_empty, 0};
+    Keys it, next;
+    bool live = find_keys(p, blockIdx.x >> 1, &it), next_live = false, more = true;
+    auto ask = [&] {
+        unsigned cluster;
+        more = next_work(work, lane, &cluster, &p);
+        next_live = more && find_keys(p, cluster, &next);
+    };
+    auto move_on = [&] { it = next, live = next_live; };
 
     if (warp == 0) {
-        int tails = 0, n = 0;
+        Loader<L, Blocks> load(p, bar, smem, smem0, rank, lane);
         bool ok = true;
-        if (live) {
-            const int token = span.first + span.tile * kRows;
-            load_tile<Blocks>(smem, smem0, smem0, &map_k, token, kv_head, span.batch, kRows, bar.keep, 0, nullptr, lane, &p);
-            for (; n < steps && ok; ++n) {
-                const int row = tile_of(n) * kRows;
-                for (int i = 0; i < 2; ++i) {      // queries, gradients
-                    const int ring = L::ring(i), s = n % ring;
-                    if (n >= ring && !__all_sync(0xffffffffu, mbar_wait(bar.ring_free[i] + 8 * s, (n / ring - 1) & 1, &p))) {
-                        ok = false;
-                        break;
+        for (; more; move_on()) {
+            if (!ok || !live) {
+                ask();
+                continue;
+            }
+            const int token = it.span.first + it.span.tile * kSpan + (int)rank * kRows, batch = it.span.batch;
+            ok = load.keep(0, &m.k, token, it.head, batch) && load.keep(1, &m.v, token, it.head, batch);
+            ask();
+            for (int i = 0; i < it.steps && ok; ++i) {
+                const int row = it.tile(i) * kRows, head = it.query_head(i, p.group), rows = it.span.len - row;
+                const bool mend = rows < kRows;
+                if (mend) load.expect_mended(2 * load.bytes(true) + 2 * load.bytes(false));
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    ok = ok && load.room(s);
+                    if (!ok) break;
+                    const bool by_rows = s < 2;
+                    load.load(s, by_rows, s == kQRows ? &m.q_rows : s == kDoRows ? &m.dout_rows : s == kDoSum ? &m.dout : &m.q,
+                              it.span.first + row, head, batch, cols, mend);
+                    if (!mend) ++load.loaded[s];
+                }
+                if (mend && ok) {
+                    load.wait_mended();
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        load.mend(s, s < 2, rows);
+                        ++load.loaded[s];
                     }
-                    load_tile<Blocks>(smem, smem0, smem0 + L::at(i, n), i ? &map_do : &map_q,
-                                      span.first + row, head_of(n), span.batch, span.len - row, bar.ring[i] + 8 * s, bar.tail, &tails,
-                                      lane, &p);
-                    if (n == 0 && i == 0)
-                        load_tile<Blocks>(smem, smem0, smem0 + L::kTileBytes, &map_v, token, kv_head, span.batch, kRows, bar.keep + 8,
-                                          0, nullptr, lane, &p);
                 }
             }
         }
-        // The way out: the MMAs, then the loads that no MMA waited for.
-        mbar_wait<kEnd>(bar.drain, 0, &p);
-        if (live)
-            for (int i = 0; i < 2; ++i) {
-                mbar_wait<kEnd>(bar.keep + 8 * i, 0, &p);
-                for (int q = max(0, n - L::ring(i)); q < n; ++q)
-                    mbar_wait<kEnd>(bar.ring[i] + 8 * (q % L::ring(i)), (q / L::ring(i)) & 1, &p);
-            }
+        load.leave();
     } else if (warp == 1) {
-        const int cols = (p.dim + 15) / 16 * 16;
-        const uint32_t by_rows = instruction(kBf, kRows, false), by_cols = instruction(kBf, cols, true);
-        const uint32_t k_tile = tile_desc(smem0, false), v_tile = tile_desc(smem0 + L::kTileBytes, false);
-        auto tile = [&](int i, int n) { return smem0 + L::at(i, n); };
-        auto wait_ring = [&](int i, int n) {
-            return __all_sync(0xffffffffu, mbar_wait(bar.ring[i] + 8 * (n % L::ring(i)), (n / L::ring(i)) & 1, &p));
-        };
-        auto scores = [&](int n) {
-            if (!wait_ring(0, n)) return false;
-            if (elect_one()) {
-                product_by_rows<Blocks>(score, k_tile, tile_desc(tile(0, n), false), cols / 16, by_rows);
-                mma_done(bar.first);
+        if (rank == 0) {
+            const uint32_t by_rows = instruction(kBf, kRows, false), by_cols = instruction(kBf, cols, true);
+            const Stages<L> st{p, bar, smem0};
+            int n = 0, items = 0;            // query tiles taken, in all
+            bool ok = true;
+            auto scores = [&](int at, bool last) {
+                if (!st.wait(kQRows, at)) return false;
+                if (elect_one()) {
+                    product_by_rows<Blocks>(score, smem0, st.tile(kQRows, at), cols / 16, by_rows);
+                    mma_commit(bar.first);
+                    st.free(kQRows, at);
+                    if (last) mma_commit(bar.keep_free);
+                }
+                __syncwarp();
+                return true;
+            };
+            auto dprobs = [&](int at, bool last) {
+                if (!st.wait(kDoRows, at)) return false;
+                if (elect_one()) {
+                    product_by_rows<Blocks>(dprob, smem0 + L::kTileBytes, st.tile(kDoRows, at), cols / 16, by_rows);
+                    mma_commit(bar.second);
+                    st.free(kDoRows, at);
+                    if (last) mma_commit(bar.keep_free + 8);
+                }
+                __syncwarp();
+                return true;
+            };
+            for (; more; move_on()) {
+                if (!ok || !live) {
+                    ask();
+                    continue;
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait(bar.keep, items & 1, &p)) && scores(n, it.steps == 1) &&
+                     __all_sync(0xffffffffu, mbar_wait(bar.keep + 8, items & 1, &p)) && dprobs(n, it.steps == 1);
+                ask();
+                for (int i = 0; i < it.steps && ok; ++i, ++n) {
+                    // P^T lies over the scores: the next ones follow its product, in order
+                    const bool more_tiles = i + 1 < it.steps, last = i + 2 == it.steps;
+                    ok = st.wait(kDoSum, n) && __all_sync(0xffffffffu, mbar_wait<kRelaxed>(bar.first_taken, n & 1, &p)) &&
+                         (i || !items || __all_sync(0xffffffffu, mbar_wait<kRelaxed>(bar.acc_free, (items - 1) & 1, &p)));
+                    if (!ok) break;
+                    tmem_fence_after();
+                    if (elect_one()) {
+                        product_over_tokens(dv, score, kHalfCols, st.tile(kDoSum, n), by_cols, i > 0);
+                        st.free(kDoSum, n);
+                    }
+                    __syncwarp();
+                    if (more_tiles && !scores(n + 1, last)) ok = false;
+                    ok = ok && st.wait(kQSum, n) && __all_sync(0xffffffffu, mbar_wait<kRelaxed>(bar.second_taken, n & 1, &p));
+                    if (!ok) break;
+                    tmem_fence_after();
+                    if (elect_one()) {
+                        product_over_tokens(dk, dprob, kHalfCols, st.tile(kQSum, n), by_cols, i > 0);
+                        st.free(kQSum, n);
+                        if (!more_tiles) mma_commit(bar.acc);
+                    }
+                    __syncwarp();
+                    if (more_tiles && !dprobs(n + 1, last)) ok = false;
+                }
+                ++items;
             }
-            __syncwarp();
-            return true;
-        };
-        auto dprobs = [&](int n) {
-            if (!wait_ring(1, n)) return false;
-            if (elect_one()) {
-                product_by_rows<Blocks>(dprob, v_tile, tile_desc(tile(1, n), false), cols / 16, by_rows);
-                mma_done(bar.second);
-            }
-            __syncwarp();
-            return true;
-        };
-        bool ok = live && __all_sync(0xffffffffu, mbar_wait(bar.keep, 0, &p)) && scores(0) &&
-                  __all_sync(0xffffffffu, mbar_wait(bar.keep + 8, 0, &p)) && dprobs(0);
-        for (int n = 0; n < steps && ok; ++n) {
-            // P^T lies over the scores: the next ones follow its product, in order
-            if (!__all_sync(0xffffffffu, mbar_wait(bar.first_taken, n & 1, &p))) break;
-            tmem_fence_after();
-            if (elect_one()) product_over_tokens(dv, score, kHalfCols, tile_desc(tile(1, n), true), by_cols, n > 0);
-            __syncwarp();
-            if (n + 1 < steps && !scores(n + 1)) break;
-            if (!__all_sync(0xffffffffu, mbar_wait(bar.second_taken, n & 1, &p))) break;
-            tmem_fence_after();
-            if (elect_one()) {
-                product_over_tokens(dk, dprob, kHalfCols, tile_desc(tile(0, n), true), by_cols, n > 0);
-                mma_done(bar.ring_free[0] + 8 * (n % L::kRing0));
-                mma_done(bar.ring_free[1] + 8 * (n % L::kRing1));
-                if (n + 1 == steps) mma_done(bar.all);
-            }
-            __syncwarp();
-            if (n + 1 < steps && !dprobs(n + 1)) break;
+            if (elect_one()) mma_commit(bar.drain);
         }
-        if (elect_one()) mma_done(bar.drain);
     } else if (warp == 2) {
-        // log sums and deltas of the next query tile; a query behind the end has P = 0
+        // log sums and deltas of the next query tile, negated; a query behind the end has P = 0
         const float f = power_of_two(ds_shift<Fmt>(p.norms) - kPShift<Fmt>);
         float* table = reinterpret_cast<float*>(smem + L::kAux);
-        for (int n = 0; n < steps; ++n) {
-            float2 x[4];
-            const int row0 = tile_of(n) * kRows;
-            const float2* aux = p.aux + ((int64_t)span.batch * p.heads + head_of(n)) * p.tokens.seq + span.first;
+        int n = 0;
+        bool ok = true;
+        for (; more; move_on()) {
+            ask();
+            if (!ok || !live) continue;
+            for (int i = 0; i < it.steps; ++i, ++n) {
+                float2 x[4];
+                const int row0 = it.tile(i) * kRows;
+                const float2* aux = p.aux + ((int64_t)it.span.batch * p.heads + it.query_head(i, p.group)) * p.tokens.seq + it.span.first;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = row0 + 32 * i + lane;
-                x[i] = row < span.len ? aux[row] : make_float2(__int_as_float(0x7f800000), 0.f);
+                for (int k = 0; k < 4; ++k) {
+                    const int row = row0 + 32 * k + lane;
+                    x[k] = row < it.span.len ? aux[row] : make_float2(__int_as_float(0x7f800000), 0.f);
+                }
+                // the log sums are read with the scores, the deltas with dP: each is free for the next tile behind that
+                if (n && !__all_sync(0xffffffffu, mbar_wait(bar.aux_free, (n - 1) & 1, &p))) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) table[32 * k + lane] = kPShift<Fmt> - x[k].x;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar.aux);
+                if (n && !__all_sync(0xffffffffu, mbar_wait(bar.aux_free + 8, (n - 1) & 1, &p))) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) table[kRows + 32 * k + lane] = -x[k].y * f;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar.aux + 8);
             }
-            // the log sums are read with the scores, the deltas with dP: each is free for the next tile behind that
-            if (n && !__all_sync(0xffffffffu, mbar_wait(bar.aux_free, (n - 1) & 1, &p))) break;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) table[32 * i + lane] = x[i].x - kPShift<Fmt>;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar.aux);
-            if (n && !__all_sync(0xffffffffu, mbar_wait(bar.aux_free + 8, (n - 1) & 1, &p))) break;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) table[kRows + 32 * i + lane] = x[i].y * f;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar.aux + 8);
         }
-    } else if (warp >= kWorkWarp && live) {
-        const int half = (warp - kWorkWarp) >> 2, quad = warp & 3, row = quad * 32 + lane;
+    } else if (warp == 3) {
+        hand_out(work, rank, &p);
+    } else {
+        const int half = (warp - kWorkWarp) >> 2, quad = warp & 3;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t s_at = score + lanes + half * kHalfCols, d_at = dprob + lanes + half * kHalfCols;
+        const uint32_t s_taken = map_to(bar.first_taken, 0), d_taken = map_to(bar.second_taken, 0), acc_free = map_to(bar.acc_free, 0);
         const int shift = ds_shift<Fmt>(p.norms);
         const float f = power_of_two(shift - kPShift<Fmt>);
-        const unsigned long long c2 = pair_of(p.scale_log2, p.scale_log2), f2 = pair_of(f, f), minus = pair_of(-1.f, -1.f);
-        const float4 *sums = reinterpret_cast<const float4*>(smem + L::kAux) + half * kHalfCols / 4, *deltas = sums + kRows / 4;
+        const unsigned long long c2 = pair_of(p.scale_log2, p.scale_log2), f2 = pair_of(f, f);
+        // (a lane's columns are 8 k + lane % 4 * 2 and the next, of four rows: a quarter of the table's values that a lane
+        // with a row of its own needs, which took 1,500 of a tile's 3,100 clocks of shared memory)
+        const float2 *sums = reinterpret_cast<const float2*>(smem + L::kAux) + half * kHalfCols / 2 + lane % 4, *deltas = sums + kRows / 2;
+        int n = 0, items = 0;
         bool ok = true;
-        for (int n = 0; n < steps; ++n) {
-            if (!__all_sync(0xffffffffu, mbar_wait(bar.aux, n & 1, &p)) ||
-                !__all_sync(0xffffffffu, mbar_wait(bar.first, n & 1, &p))) {
-                ok = false;
-                break;
-            }
-            tmem_fence_after();
-            unsigned long long prob[32];
-            uint32_t a[32], b[32];
-            tmem_load32(s_at, a);
-            tmem_load32(s_at + 32, b);
-            const bool own = tile_of(n) == span.tile;
-            auto powers = [&](uint32_t (&x)[32], int from) {
-                if (own) {       // queries before the row's own token
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = half * kHalfCols + from + e < row ? 0xff800000u : x[e];
+        for (; more; move_on()) {
+            ask();
+            if (!ok || !live) continue;
+            const int mine = it.first + (int)rank;           // this CTA's keys as a query tile
+            for (int i = 0; i < it.steps; ++i, ++n) {
+                if (!__all_sync(0xffffffffu, mbar_wait(bar.aux, n & 1, &p)) || !__all_sync(0xffffffffu, mbar_wait<kRelaxed>(bar.first, n & 1, &p))) {
+                    ok = false;
+                    break;
                 }
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float4 l = sums[(from + 2 * e) / 4];
+                tmem_fence_after();
+                const int tile = it.tile(i);
+                unsigned long long prob[2][16];
+                if (tile >= mine) {
+                    const int row = quad * 32 + lane / 4, col = half * kHalfCols + lane % 4 * 2;
+                    uint32_t x[2][32];
+                    tmem_load_16x64(s_at, x[0]);
+                    tmem_load_16x64(s_at + (16u << 16), x[1]);
+                    tmem_wait(x[0]);
+                    tmem_wait(x[1]);
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
-                        float lo, hi;
-                        split_pair(fma_pair(pair_of(__uint_as_float(x[2 * (e + g)]), __uint_as_float(x[2 * (e + g) + 1])), c2,
-                                            mul_pair(g ? pair_of(l.z, l.w) : pair_of(l.x, l.y), minus)), lo, hi);
-                        lo = exp2_fast(lo);
-                        hi = exp2_fast(hi);
-                        prob[from / 2 + e + g] = pair_of(lo, hi);
-                        w[e + g] = pack2<Fmt>(lo, hi);
-                    }
-                }
-                tmem_store16(s_at + from / 2, w);
-            };
-            // (the first half's P lies over scores that both halves of this warp have in registers)
-            tmem_wait(a);
-            tmem_wait(b);
-            powers(a, 0);
-            powers(b, 32);
-            tmem_stored();
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar.first_taken);
-                mbar_arrive(bar.aux_free);
-            }
-            if (!__all_sync(0xffffffffu, mbar_wait(bar.aux + 8, n & 1, &p)) ||
-                !__all_sync(0xffffffffu, mbar_wait(bar.second, n & 1, &p))) {
-                ok = false;
-                break;
-            }
-            tmem_fence_after();
-            tmem_load32(d_at, a);
-            tmem_load32(d_at + 32, b);
-            auto slopes = [&](const uint32_t (&x)[32], int from) {
-                uint32_t w[16];
+                        if (tile == mine) {      // queries before the row's own token
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const float4 d = deltas[(from + 2 * e) / 4];
+                            for (int e = 0; e < 32; ++e)
+                                if (col + e / 4 * 8 + (e & 1) < row + 16 * g + (e & 2 ? 8 : 0)) x[g][e] = 0xff800000u;
+                        }
+                        uint32_t w[16];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float2 l = sums[4 * k];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float lo, hi;
+                                split_pair(fma_pair(pair_of(__uint_as_float(x[g][4 * k + 2 * h]), __uint_as_float(x[g][4 * k + 2 * h + 1])), c2,
+                                                    pair_of(l.x, l.y)), lo, hi);
+                                lo = exp2_fast(lo);
+                                hi = exp2_fast(hi);
+                                prob[g][2 * k + h] = pair_of(lo, hi);
+                                w[2 * k + h] = pack2<Fmt>(lo, hi);
+                            }
+                        }
+                        tmem_store_16x64(s_at + ((uint32_t)(16 * g) << 16), w);
+                    }
+                } else {                         // all before the keys
+                    const uint32_t none[16] = {};
+                    tmem_store_16x64(s_at, none);
+                    tmem_store_16x64(s_at + (16u << 16), none);
+                }
+                tmem_stored();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_cluster(s_taken);
+                    mbar_arrive(bar.aux_free);
+                }
+                if (!__all_sync(0xffffffffu, mbar_wait(bar.aux + 8, n & 1, &p)) || !__all_sync(0xffffffffu, mbar_wait<kRelaxed>(bar.second, n & 1, &p))) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+                if (tile >= mine) {
+                    uint32_t x[2][32];
+                    tmem_load_16x64(d_at, x[0]);
+                    tmem_load_16x64(d_at + (16u << 16), x[1]);
+                    tmem_wait(x[0]);
+                    tmem_wait(x[1]);
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
-                        const unsigned long long dp = pair_of(__uint_as_float(x[2 * (e + g)]), __uint_as_float(x[2 * (e + g) + 1]));
-                        const unsigned long long delta = mul_pair(g ? pair_of(d.z, d.w) : pair_of(d.x, d.y), minus);
-                        float lo, hi;
-                        split_pair(mul_pair(prob[from / 2 + e + g], kBf ? add_pair(dp, delta) : fma_pair(dp, f2, delta)), lo, hi);
-                        w[e + g] = pack2<Fmt>(lo, hi);
+                        uint32_t w[16];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float2 d = deltas[4 * k];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const unsigned long long dp = pair_of(__uint_as_float(x[g][4 * k + 2 * h]), __uint_as_float(x[g][4 * k + 2 * h + 1]));
+                                float lo, hi;
+                                split_pair(mul_pair(prob[g][2 * k + h], kBf ? add_pair(dp, pair_of(d.x, d.y)) : fma_pair(dp, f2, pair_of(d.x, d.y))), lo, hi);
+                                w[2 * k + h] = pack2<Fmt>(lo, hi);
+                            }
+                        }
+                        tmem_store_16x64(d_at + ((uint32_t)(16 * g) << 16), w);
                     }
+                } else {
+                    const uint32_t none[16] = {};
+                    tmem_store_16x64(d_at, none);
+                    tmem_store_16x64(d_at + (16u << 16), none);
                 }
-                tmem_store16(d_at + from / 2, w);
+                tmem_stored();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_cluster(d_taken);
+                    mbar_arrive(bar.aux_free + 8);
+                }
+            }
+            if (!ok) continue;
+            if (!__all_sync(0xffffffffu, mbar_wait<kRelaxed>(bar.acc, items++ & 1, &p))) {
+                ok = false;
+                continue;
+            }
+            tmem_fence_after();
+            auto give_back = [&] {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(acc_free);
             };
-            tmem_wait(a);
-            tmem_wait(b);
-            slopes(a, 0);
-            slopes(b, 32);
-            tmem_stored();
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar.second_taken);
-                mbar_arrive(bar.aux_free + 8);
+            const int in_seq = it.span.tile * kSpan + (int)rank * kRows + quad * 32, rows = min(32, it.span.len - in_seq);
+            if (rows > 0) {
+                const int token = it.span.first + in_seq, g = !half;     // dV, dK
+                const Place to{half ? &m.out0 : &m.out1,
+                               static_cast<T*>(half ? p.grad0 : p.grad1) + it.span.batch * p.stride[g][0] + token * p.stride[g][1] + it.head * p.stride[g][2],
+                               p.stride[g][1], token, it.head, it.span.batch};
+                store_rows<Fmt>(smem + L::kOut + (warp - kWorkWarp) * kOutStage, (half ? dk : dv) + lanes,
+                                half ? p.scale * power_of_two(-shift) : power_of_two(-kPShift<Fmt>), to, rows, 0, p.dim, lane, give_back);
+            } else {
+                give_back();
             }
         }
-        if (ok && __all_sync(0xffffffffu, mbar_wait(bar.all, 0, &p))) {
-            tmem_fence_after();
-            const int in_seq = span.tile * kRows + quad * 32, rows = min(32, span.len - in_seq);
-            T* out = static_cast<T*>(half ? p.grad0 : p.grad1) + span.batch * p.stride[!half][0] +
-                     (int64_t)(span.first + in_seq) * p.stride[!half][1] + kv_head * p.stride[!half][2];
-            const float factor = half ? p.scale * power_of_two(-shift) : power_of_two(-kPShift<Fmt>);
-            store_rows<Fmt>(smem + (warp - kWorkWarp) * kOutStage, (half ? dk : dv) + lanes, factor, out, p.stride[!half][1], rows,
-                            p.dim, lane);
-        }
+        stored_all(lane);
     }
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
+    cluster_sync();             // no CTA leaves while the other may signal or read it
     if (warp == 3) tmem_free_all(tmem);
 }
 
 // ---------------------------------------------------------------- dQ
-// A CTA has 128 queries of one head, and walks the key tiles up to its own.
+// A pair has 256 queries of one head, and walks the key tiles up to its own, the last first.
+struct Queries {
+    Span span;
+    int head, steps;          // key tiles
+};
+__device__ __forceinline__ bool find_queries(const Args& p, unsigned index, Queries* q) {
+    q->head = (int)(index % (unsigned)p.heads);
+    const unsigned slot = index / (unsigned)p.heads;
+    if (p.tokens.offsets) {
+        if (!find_tile(p.tokens, kSpan, (int)slot, true, &q->span)) return false;
+    } else {
+        const unsigned batch = (unsigned)p.tokens.batch;
+        q->span = Span{(int)(slot % batch), 0, p.tokens.seq, p.tiles - 1 - (int)(slot / batch)};
+    }
+    q->steps = min(2 * q->span.tile + 2, (q->span.len + kRows - 1) / kRows);
+    return true;
+}
+
 template <class Fmt, int Blocks>
-__global__ void __launch_bounds__(kThreads, 1)
-dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-          const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do, const __grid_constant__ Args p) {
-    using L = Layout<Blocks>;
+__global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__ Maps m, const __grid_constant__ Args p) {
+    using L = LayoutQ<Blocks>;
     using T = typename Fmt::T;
     constexpr bool kBf = std::is_same<Fmt, BF16>::value;
+    enum { kKRows, kVRows, kKSum };
     extern __shared__ unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t smem0 = smem_addr(smem);
     const Bars bar = bars_at<L>(smem0 + L::kBars);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) init_bars<L>(bar);
+    const uint32_t rank = cta_rank();
+    if (threadIdx.x == 0) init_bars<L>(bar, 2 * 9 + 1);
     if (warp == 3) tmem_alloc_all(bar.slot);
     tmem_fence_before();
     __syncthreads();
+    cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + (bar.slot - smem0));
     pdl_wait();
@@ -381,164 +588,220 @@ dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUt
 
     // scores in two places, the second for the next key tile; dS lies over them
     const uint32_t score = tmem, dprob = tmem + 2 * kRows, dq = tmem + 3 * kRows;
-    Span span;
-    const int head = (int)(blockIdx.x % (unsigned)p.heads), kv_head = head / p.group;
-    const unsigned place = blockIdx.x / (unsigned)p.heads;
-    bool live = true;
-    if (p.tokens.offsets) live = find_tile(p.tokens, kRows, (int)place, true, &span);
-    else span = Span{(int)(place % (unsigned)p.tokens.batch), 0, p.tokens.seq, p.tiles - 1 - (int)(place / (unsigned)p.tokens.batch)};
-    const int steps = live ? span.tile + 1 : 0;       // key tiles, the last first
+    const int cols = (p.dim + 15) / 16 * 16;
+    Work work{bar.answer, bar.work_full, bar.work_empty, 0};
+    Queries it, next;
+    bool live = find_queries(p, blockIdx.x >> 1, &it), next_live = false, more = true;
+    auto ask = [&] {
+        unsigned cluster;
+        more = next_work(work, lane, &cluster, &p);
+        next_live = more && find_queries(p, cluster, &next);
+    };
+    auto move_on = [&] { it = next, live = next_live; };
 
     if (warp == 0) {
-        int tails = 0, n = 0;
+        Loader<L, Blocks> load(p, bar, smem, smem0, rank, lane);
         bool ok = true;
-        if (live) {
-            const int token = span.first + span.tile * kRows;
-            load_tile<Blocks>(smem, smem0, smem0, &map_q, token, head, span.batch, kRows, bar.keep, 0, nullptr, lane, &p);
-            for (; n < steps && ok; ++n) {
-                const int row = (steps - 1 - n) * kRows;
-                for (int i = 0; i < 2; ++i) {      // keys, values
-                    const int ring = L::ring(i), s = n % ring;
-                    if (n >= ring && !__all_sync(0xffffffffu, mbar_wait(bar.ring_free[i] + 8 * s, (n / ring - 1) & 1, &p))) {
-                        ok = false;
-                        break;
-                    }
-                    load_tile<Blocks>(smem, smem0, smem0 + L::at(i, n), i ? &map_v : &map_k,
-                                      span.first + row, kv_head, span.batch, span.len - row, bar.ring[i] + 8 * s, bar.tail, &tails,
-                                      lane, &p);
-                    if (n == 0 && i == 0)
-                        load_tile<Blocks>(smem, smem0, smem0 + L::kTileBytes, &map_do, token, head, span.batch, kRows, bar.keep + 8, 0,
-                                          nullptr, lane, &p);
+        for (; more; move_on()) {
+            if (!ok || !live) {
+                ask();
+                continue;
+            }
+            const int token = it.span.first + it.span.tile * kSpan + (int)rank * kRows, batch = it.span.batch, kv_head = it.head / p.group;
+            ok = load.keep(0, &m.q, token, it.head, batch) && load.keep(1, &m.dout, token, it.head, batch);
+            ask();
+            for (int i = 0; i < it.steps && ok; ++i) {
+                const int row = (it.steps - 1 - i) * kRows, rows = it.span.len - row;
+                // (scores of keys behind the end are hidden)
+                const bool mend = rows < kRows;
+                if (mend) load.expect_mended(load.bytes(true) + load.bytes(false));
+#pragma unroll
+                for (int s = 0; s < 3; ++s) {
+                    ok = ok && load.room(s);
+                    if (!ok) break;
+                    load.load(s, s < 2, s == kKRows ? &m.k_rows : s == kVRows ? &m.v_rows : &m.k, it.span.first + row, kv_head, batch, cols,
+                              mend && s != kKRows);
+                    if (!mend || s == kKRows) ++load.loaded[s];
+                }
+                if (mend && ok) {
+                    load.wait_mended();
+                    load.mend(kVRows, true, rows);
+                    load.mend(kKSum, false, rows);
+                    ++load.loaded[kVRows], ++load.loaded[kKSum];
                 }
             }
         }
-        mbar_wait<kEnd>(bar.drain, 0, &p);
-        if (live)
-            for (int i = 0; i < 2; ++i) {
-                mbar_wait<kEnd>(bar.keep + 8 * i, 0, &p);
-                for (int q = max(0, n - L::ring(i)); q < n; ++q)
-                    mbar_wait<kEnd>(bar.ring[i] + 8 * (q % L::ring(i)), (q / L::ring(i)) & 1, &p);
-            }
+        load.leave();
     } else if (warp == 1) {
-        const int cols = (p.dim + 15) / 16 * 16;
-        const uint32_t by_rows = instruction(kBf, kRows, false), by_cols = instruction(kBf, cols, true);
-        const uint32_t q_tile = tile_desc(smem0, false), do_tile = tile_desc(smem0 + L::kTileBytes, false);
-        auto tile = [&](int i, int n) { return smem0 + L::at(i, n); };
-        auto wait_ring = [&](int i, int n) {
-            return __all_sync(0xffffffffu, mbar_wait(bar.ring[i] + 8 * (n % L::ring(i)), (n / L::ring(i)) & 1, &p));
-        };
-        auto scores = [&](int n) {
-            if (!wait_ring(0, n)) return false;
-            if (elect_one()) {
-                product_by_rows<Blocks>(score + (n & 1) * kRows, q_tile, tile_desc(tile(0, n), false), cols / 16, by_rows);
-                mma_done(bar.first + 8 * (n & 1));
+        if (rank == 0) {
+            const uint32_t by_rows = instruction(kBf, kRows, false), by_cols = instruction(kBf, cols, true);
+            const Stages<L> st{p, bar, smem0};
+            int n = 0, items = 0;            // key tiles taken, in all
+            bool ok = true;
+            auto scores = [&](int at, bool last) {
+                if (!st.wait(kKRows, at)) return false;
+                if (elect_one()) {
+                    product_by_rows<Blocks>(score + (at & 1) * kRows, smem0, st.tile(kKRows, at), cols / 16, by_rows);
+                    mma_commit(bar.first + 8 * (at & 1));
+                    st.free(kKRows, at);
+                    if (last) mma_commit(bar.keep_free);
+                }
+                __syncwarp();
+                return true;
+            };
+            auto dprobs = [&](int at, bool last) {
+                if (!st.wait(kVRows, at)) return false;
+                if (elect_one()) {
+                    product_by_rows<Blocks>(dprob, smem0 + L::kTileBytes, st.tile(kVRows, at), cols / 16, by_rows);
+                    mma_commit(bar.second);
+                    st.free(kVRows, at);
+                    if (last) mma_commit(bar.keep_free + 8);
+                }
+                __syncwarp();
+                return true;
+            };
+            for (; more; move_on()) {
+                if (!ok || !live) {
+                    ask();
+                    continue;
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait(bar.keep, items & 1, &p)) && scores(n, it.steps == 1) &&
+                     __all_sync(0xffffffffu, mbar_wait(bar.keep + 8, items & 1, &p)) && dprobs(n, it.steps == 1);
+                ask();
+                for (int i = 0; i < it.steps && ok; ++i, ++n) {
+                    // The place of the scores of n + 1 held dS of n - 1, whose product came before.
+                    const bool more_tiles = i + 1 < it.steps, last = i + 2 == it.steps;
+                    if (more_tiles && !scores(n + 1, last)) ok = false;
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait<kRelaxed>(bar.second_taken, n & 1, &p));
+                    if (!ok) break;
+                    tmem_fence_after();
+                    if (more_tiles && !dprobs(n + 1, last)) ok = false;
+                    ok = ok && st.wait(kKSum, n) &&
+                         (i || !items || __all_sync(0xffffffffu, mbar_wait<kRelaxed>(bar.acc_free, (items - 1) & 1, &p)));
+                    if (!ok) break;
+                    tmem_fence_after();
+                    if (elect_one()) {
+                        product_over_tokens(dq, score + (n & 1) * kRows, kHalfCols, st.tile(kKSum, n), by_cols, i > 0);
+                        st.free(kKSum, n);
+                        if (!more_tiles) mma_commit(bar.acc);
+                    }
+                    __syncwarp();
+                }
+                ++items;
             }
-            __syncwarp();
-            return true;
-        };
-        auto dprobs = [&](int n) {
-            if (!wait_ring(1, n)) return false;
-            if (elect_one()) {
-                product_by_rows<Blocks>(dprob, do_tile, tile_desc(tile(1, n), false), cols / 16, by_rows);
-                mma_done(bar.second);
-                mma_done(bar.ring_free[1] + 8 * (n % L::kRing1));
-            }
-            __syncwarp();
-            return true;
-        };
-        bool ok = live && __all_sync(0xffffffffu, mbar_wait(bar.keep, 0, &p)) && scores(0) &&
-                  __all_sync(0xffffffffu, mbar_wait(bar.keep + 8, 0, &p)) && dprobs(0);
-        for (int n = 0; n < steps && ok; ++n) {
-            // The place of the scores of n + 1 held dS of n - 1, whose product came before.
-            if (n + 1 < steps && !scores(n + 1)) break;
-            if (!__all_sync(0xffffffffu, mbar_wait(bar.second_taken, n & 1, &p))) break;
-            tmem_fence_after();
-            if (n + 1 < steps && !dprobs(n + 1)) break;
-            if (elect_one()) {
-                product_over_tokens(dq, score + (n & 1) * kRows, kHalfCols, tile_desc(tile(0, n), true), by_cols, n > 0);
-                mma_done(bar.ring_free[0] + 8 * (n % L::kRing0));
-                if (n + 1 == steps) mma_done(bar.all);
-            }
-            __syncwarp();
+            if (elect_one()) mma_commit(bar.drain);
         }
-        if (elect_one()) mma_done(bar.drain);
-    } else if (warp >= kWorkWarp && live) {
+    } else if (warp == 3) {
+        hand_out(work, rank, &p);
+    } else if (warp >= kWorkWarp) {
         const int half = (warp - kWorkWarp) >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t d_at = dprob + lanes + half * kHalfCols;
+        const uint32_t taken = map_to(bar.second_taken, 0), acc_free = map_to(bar.acc_free, 0);
         const int shift = ds_shift<Fmt>(p.norms);
-        const int in_seq = span.tile * kRows + quad * 32, rows = min(32, span.len - in_seq);
-        float2 aux = make_float2(0.f, 0.f);
-        if (lane < rows) aux = p.aux[((int64_t)span.batch * p.heads + head) * p.tokens.seq + span.first + in_seq + lane];
-        const float base = (float)shift - aux.x;
-        const unsigned long long c2 = pair_of(p.scale_log2, p.scale_log2), b2 = pair_of(base, base), delta = pair_of(-aux.y, -aux.y);
+        const unsigned long long c2 = pair_of(p.scale_log2, p.scale_log2);
+        const int share = (cols / 2 + 31) / 32 * 32, from = half * share, to_col = min(p.dim, from + share);  // of dQ's columns
+        int n = 0, items = 0;
         bool ok = true;
-        for (int n = 0; n < steps; ++n) {
-            const uint32_t s_at = score + (n & 1) * kRows + lanes + half * kHalfCols;
-            if (!__all_sync(0xffffffffu, mbar_wait(bar.first + 8 * (n & 1), (n / 2) & 1, &p))) {
+        for (; more; move_on()) {
+            ask();
+            if (!ok || !live) continue;
+            const int in_seq = it.span.tile * kSpan + (int)rank * kRows + quad * 32, rows = min(32, it.span.len - in_seq);
+            const int mine = 2 * it.span.tile + (int)rank;       // this CTA's queries as a key tile
+            float2 aux = make_float2(0.f, 0.f);
+            if (lane < rows) aux = p.aux[((int64_t)it.span.batch * p.heads + it.head) * p.tokens.seq + it.span.first + in_seq + lane];
+            const float base = (float)shift - aux.x;
+            const unsigned long long b2 = pair_of(base, base), delta = pair_of(-aux.y, -aux.y);
+            for (int i = 0; i < it.steps; ++i, ++n) {
+                const uint32_t s_at = score + (n & 1) * kRows + lanes + half * kHalfCols;
+                const int tile = it.steps - 1 - i;
+                if (!__all_sync(0xffffffffu, mbar_wait<kRelaxed>(bar.first + 8 * (n & 1), (n / 2) & 1, &p))) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+                unsigned long long prob[32];
+                uint32_t a[32], b[32];
+                if (tile <= mine) {
+                    tmem_load32(s_at, a);
+                    tmem_load32(s_at + 32, b);
+                    auto powers = [&](uint32_t (&x)[32], int at) {
+                        if (tile == mine) {      // tokens behind the row's own
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = half * kHalfCols + at + e > row ? 0xff800000u : x[e];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float lo, hi;
+                            split_pair(fma_pair(pair_of(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, b2), lo, hi);
+                            prob[at / 2 + e] = pair_of(exp2_fast(lo), exp2_fast(hi));
+                        }
+                    };
+                    tmem_wait(a);
+                    tmem_wait(b);
+                    powers(a, 0);
+                    powers(b, 32);
+                }
+                if (!__all_sync(0xffffffffu, mbar_wait<kRelaxed>(bar.second, n & 1, &p))) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+                if (tile <= mine) {
+                    tmem_load32(d_at, a);
+                    tmem_load32(d_at + 32, b);
+                    auto slopes = [&](const uint32_t (&x)[32], int at) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const unsigned long long dp = pair_of(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                            float lo, hi;
+                            split_pair(mul_pair(prob[at / 2 + e], add_pair(dp, delta)), lo, hi);
+                            w[e] = pack2<Fmt>(lo, hi);
+                        }
+                        tmem_store16(s_at + at / 2, w);
+                    };
+                    tmem_wait(a);
+                    tmem_wait(b);
+                    slopes(a, 0);
+                    slopes(b, 32);
+                } else {                         // all keys behind the queries
+                    const uint32_t none[32] = {};
+                    tmem_store32(s_at, none);
+                }
+                tmem_stored();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(taken);
+            }
+            if (!ok) continue;
+            if (!__all_sync(0xffffffffu, mbar_wait<kRelaxed>(bar.acc, items++ & 1, &p))) {
                 ok = false;
-                break;
+                continue;
             }
             tmem_fence_after();
-            unsigned long long prob[32];
-            uint32_t a[32], b[32];
-            tmem_load32(s_at, a);
-            tmem_load32(s_at + 32, b);
-            auto powers = [&](uint32_t (&x)[32], int from) {
-                if (n == 0) {    // tokens behind the row's own
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = half * kHalfCols + from + e > row ? 0xff800000u : x[e];
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float lo, hi;
-                    split_pair(fma_pair(pair_of(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, b2), lo, hi);
-                    prob[from / 2 + e] = pair_of(exp2_fast(lo), exp2_fast(hi));
-                }
+            auto give_back = [&] {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(acc_free);
             };
-            tmem_wait(a);
-            tmem_wait(b);
-            powers(a, 0);
-            powers(b, 32);
-            if (!__all_sync(0xffffffffu, mbar_wait(bar.second, n & 1, &p))) {
-                ok = false;
-                break;
+            if (rows > 0 && from < to_col) {
+                const int token = it.span.first + in_seq;
+                const Place to{&m.out0,
+                               static_cast<T*>(p.grad0) + it.span.batch * p.stride[0][0] + token * p.stride[0][1] + it.head * p.stride[0][2],
+                               p.stride[0][1], token, it.head, it.span.batch};
+                store_rows<Fmt>(smem + L::kOut + (warp - kWorkWarp) * kOutStage, dq + lanes, p.scale * power_of_two(-shift), to, rows, from,
+                                to_col, lane, give_back);
+            } else {
+                give_back();
             }
-            tmem_fence_after();
-            tmem_load32(d_at, a);
-            tmem_load32(d_at + 32, b);
-            auto slopes = [&](const uint32_t (&x)[32], int from) {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const unsigned long long dp = pair_of(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-                    float lo, hi;
-                    split_pair(mul_pair(prob[from / 2 + e], add_pair(dp, delta)), lo, hi);
-                    w[e] = pack2<Fmt>(lo, hi);
-                }
-                tmem_store16(s_at + from / 2, w);
-            };
-            tmem_wait(a);
-            tmem_wait(b);
-            slopes(a, 0);
-            slopes(b, 32);
-            tmem_stored();
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar.second_taken);
         }
-        // (the keys' and values' places are free once all products are done)
-        if (ok && __all_sync(0xffffffffu, mbar_wait(bar.all, 0, &p)) && half == 0) {
-            tmem_fence_after();
-            T* out = static_cast<T*>(p.grad0) + span.batch * p.stride[0][0] + (int64_t)(span.first + in_seq) * p.stride[0][1] +
-                     head * p.stride[0][2];
-            store_rows<Fmt>(smem + L::kStream + quad * kOutStage, dq + lanes, p.scale * power_of_two(-shift), out, p.stride[0][1], rows,
-                            p.dim, lane);
-        }
+        stored_all(lane);
     }
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
+    cluster_sync();             // no CTA leaves while the other may signal or read it
     if (warp == 3) tmem_free_all(tmem);
 }
 
@@ -610,28 +873,31 @@ size_t workspace_bytes_for(int64_t batch, int64_t seq, int64_t heads) {
 }
 
 template <class Fmt, int Blocks>
-tb_status launch(const CUtensorMap (&m)[4], Args p, const Rows& r, const View (&grad)[3], int64_t batch, int64_t seq, cudaStream_t st) {
-    using L = Layout<Blocks>;
-    const void *a = reinterpret_cast<const void*>(&dkv_kernel<Fmt, Blocks>), *b = reinterpret_cast<const void*>(&dq_kernel<Fmt, Blocks>);
-    if (resident_ctas_per_sm(a, kThreads, L::kBytes) < 1 || resident_ctas_per_sm(b, kThreads, L::kBytes) < 1) return TB_ERR_CUDA;
+tb_status launch(Maps& m, Args p, const Rows& r, const tb_heads* const (&grads)[3], const View (&grad)[3], int64_t batch, int64_t seq,
+                 cudaStream_t st) {
+    constexpr bool bf = std::is_same<Fmt, BF16>::value;
+    constexpr int kv_bytes = LayoutKv<Blocks>::kBytes, q_bytes = LayoutQ<Blocks>::kBytes;
+    if (resident_clusters(reinterpret_cast<const void*>(&dkv_kernel<Fmt, Blocks>), kThreads, kv_bytes, 2) < 1 ||
+        resident_clusters(reinterpret_cast<const void*>(&dq_kernel<Fmt, Blocks>), kThreads, q_bytes, 2) < 1)
+        return TB_ERR_CUDA;
     int64_t ctas = r.ctas;
-    if (std::is_same<Fmt, F16>::value) {
+    if (!bf) {
         if (cudaMemsetAsync(r.norms, 0, 2 * sizeof(unsigned), st) != cudaSuccess) return TB_ERR_CUDA;
         ctas += ceil_div(batch * seq * r.kv_heads, kRowThreads / 8);
     }
     if (launch_pdl(rows_kernel<Fmt>, dim3((unsigned)ctas), dim3(kRowThreads), 0, st, r) != cudaSuccess) return TB_ERR_CUDA;
-    const int64_t slots = r.offsets ? slots_of(seq, r.sequences, kRows) : p.tiles * batch;
-    auto gradient = [&](int i, const View& v, void** to) {
-        *to = const_cast<char*>(v.p);
-        for (int k = 0; k < 3; ++k) p.stride[i][k] = v.s[k];
+    const int64_t slots = r.offsets ? slots_of(seq, r.sequences, kSpan) : p.tiles * batch;
+    auto gradient = [&](int i, int of, void** data, CUtensorMap* map) {
+        *data = const_cast<char*>(grad[of].p);
+        for (int k = 0; k < 3; ++k) p.stride[i][k] = grad[of].s[k];
+        return make_heads_map(map, *grads[of], batch, seq, p.dim, 32, bf, true);
     };
-    gradient(0, grad[1], &p.grad0);
-    gradient(1, grad[2], &p.grad1);
-    if (launch_pdl(dkv_kernel<Fmt, Blocks>, dim3((unsigned)(slots * p.kv_heads)), dim3(kThreads), L::kBytes, st, m[0], m[1], m[2], m[3],
-                   p) != cudaSuccess)
+    if (!gradient(0, 1, &p.grad0, &m.out0) || !gradient(1, 2, &p.grad1, &m.out1)) return TB_ERR_CUDA;
+    if (launch_clusters<true>(dkv_kernel<Fmt, Blocks>, dim3((unsigned)(2 * slots * p.kv_heads)), dim3(kThreads), kv_bytes, st, 2, m, p) !=
+        cudaSuccess)
         return TB_ERR_CUDA;
-    gradient(0, grad[0], &p.grad0);
-    if (launch_pdl(dq_kernel<Fmt, Blocks>, dim3((unsigned)(slots * p.heads)), dim3(kThreads), L::kBytes, st, m[0], m[1], m[2], m[3], p) !=
+    if (!gradient(0, 0, &p.grad0, &m.out0)) return TB_ERR_CUDA;
+    if (launch_clusters<true>(dq_kernel<Fmt, Blocks>, dim3((unsigned)(2 * slots * p.heads)), dim3(kThreads), q_bytes, st, 2, m, p) !=
         cudaSuccess)
         return TB_ERR_CUDA;
     return launch_status();
@@ -694,12 +960,16 @@ extern "C" tb_status tb_attention_bwd(const tb_heads* dout, const tb_heads* q, c
         if (overlap(ws, range_of_view(grad[i], head_dim))) return TB_ERR_ALIAS;
     if (overlap(ws, sums) || overlap(ws, starts)) return TB_ERR_ALIAS;
     if (offsets && sequences == 0) return TB_OK;
-    const int64_t tiles = ceil_div(seq, kRows), slots = offsets ? slots_of(seq, sequences, kRows) : tiles * batch;
-    if (slots > ((1ll << 31) - 1) / q->heads || rows > (1ll << 35)) return TB_ERR_INVALID_VALUE;
+    const int64_t tiles = ceil_div(seq, kSpan), slots = offsets ? slots_of(seq, sequences, kSpan) : tiles * batch;
+    if (slots > (1ll << 30) / q->heads || rows > (1ll << 35)) return TB_ERR_INVALID_VALUE;
     const bool bf = dtype == TB_BF16;
-    CUtensorMap m[4];
+    Maps m{};
+    CUtensorMap* const whole[4] = {&m.q, &m.k, &m.v, &m.dout};
+    CUtensorMap* const by_rows[4] = {&m.q_rows, &m.k_rows, &m.v_rows, &m.dout_rows};
     for (int i = 0; i < 4; ++i)
-        if (!make_heads_map(&m[i], *in[i], batch, seq, head_dim, bf)) return TB_ERR_CUDA;
+        if (!make_heads_map(whole[i], *in[i], batch, seq, head_dim, kRows, bf) ||
+            !make_heads_map(by_rows[i], *in[i], batch, seq, head_dim, kRows / 2, bf))
+            return TB_ERR_CUDA;
     Args p{};
     if (!(p.err = device_error_word())) return TB_ERR_CUDA;
     unsigned char* mem = static_cast<unsigned char*>(workspace);
@@ -722,6 +992,6 @@ extern "C" tb_status tb_attention_bwd(const tb_heads* dout, const tb_heads* q, c
     r.batch = (int)batch, r.seq = (int)seq, r.heads = p.heads, r.kv_heads = p.kv_heads, r.dim = p.dim;
     r.ctas = ceil_div(rows, kRowThreads / 8);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (head_dim <= 64) return bf ? launch<BF16, 1>(m, p, r, grad, batch, seq, st) : launch<F16, 1>(m, p, r, grad, batch, seq, st);
-    return bf ? launch<BF16, 2>(m, p, r, grad, batch, seq, st) : launch<F16, 2>(m, p, r, grad, batch, seq, st);
+    if (head_dim <= 64) return bf ? launch<BF16, 1>(m, p, r, grads, grad, batch, seq, st) : launch<F16, 1>(m, p, r, grads, grad, batch, seq, st);
+    return bf ? launch<BF16, 2>(m, p, r, grads, grad, batch, seq, st) : launch<F16, 2>(m, p, r, grads, grad, batch, seq, st);
 }

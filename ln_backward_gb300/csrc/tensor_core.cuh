@@ -94,12 +94,13 @@ __device__ __forceinline__ unsigned long long now_ns() {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
-// kEnd: waits at a warp's end, for what the warps that may still be waiting themselves finish.
-enum Waits { kRelaxed, kAcquire, kEnd };
+// kEnd: waits at a warp's end, for what the warps that may still be waiting themselves finish.  kWork: for other
+// warps to finish a whole piece of work, of many waits of theirs.
+enum Waits { kRelaxed, kAcquire, kEnd, kWork };
 // P: a kernel's arguments, with the bound of its waits (wait_ns) and the device error word (err).
 template <int How, class P>
 __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const P* p) {
-    const unsigned long long t0 = now_ns(), limit = How == kEnd ? 4 * kWaitLimitNs : p->wait_ns;
+    const unsigned long long t0 = now_ns(), limit = How == kWork ? 64 * kWaitLimitNs : How == kEnd ? 4 * kWaitLimitNs : p->wait_ns;
     for (uint32_t it = 1; it < (1u << 30); ++it) {
         if (mbar_try<How != kRelaxed>(bar, parity)) return true;
         if ((it & 63u) == 0 && now_ns() - t0 > limit) break;
