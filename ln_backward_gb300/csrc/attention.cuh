@@ -156,13 +156,13 @@ struct Place {
 };
 // Columns from .. dim - 1 of 32 rows of a result from tensor memory, a row a lane, times the lane's factor and rounded,
 // to the first `rows` rows of `to`, through the warp's two boxes of shared memory.  A lane's 16-byte pieces lie at piece ^ (row / 2 & 3), the
-// pattern of a 64-byte swizzle: no two lanes of a quarter warp share banks.  `read` is called when the last columns
+// pattern of a 64-byte swizzle: no two lanes of a quarter warp share banks.  Arrives on `free` when the last columns
 // are in registers.  (Stores from registers held the warps up for the time that the memory took: 4,000 clocks for
 // 64 KB of every CTA at once.)
 constexpr int kOutBox = 32 * 64, kOutStage = 2 * kOutBox;
-template <class Fmt, class F>
+template <class Fmt>
 __device__ __forceinline__ void store_rows(unsigned char* boxes, uint32_t tmem, float factor, const Place& to, int rows, int from,
-                                           int dim, int lane, F read) {
+                                           int dim, int lane, uint32_t free) {
     for (int x = from; x < dim; x += 32) {
         unsigned char* box = boxes + (x & 32 ? kOutBox : 0);
         uint32_t o[32];
@@ -170,7 +170,11 @@ __device__ __forceinline__ void store_rows(unsigned char* boxes, uint32_t tmem, 
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");       // the box is free
         tmem_wait(o);
         __syncwarp();
-        if (x + 32 >= dim) read();
+        if (x + 32 >= dim) {
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(free);
+        }
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             uint32_t h[4];
@@ -207,7 +211,8 @@ __device__ __forceinline__ void stored_all(int lane) {
 }
 
 // Rows from `rows` on of `boxes` boxes as zeros: whatever lies behind a sequence's end need not be 0 times 0.  By
-// a whole warp, before the tile is handed to the MMAs.
+// a whole warp, which waits for the tile's loads and hands it to the MMAs; another than the one that loads, which
+// goes on meanwhile.
 __device__ __forceinline__ void clear_behind(unsigned char* tile, int boxes, int box_rows, int rows, int lane) {
     for (int b = 0; b < boxes; ++b)
         for (int x = max(rows, 0) * 8 + lane; x < box_rows * 8; x += 32)
@@ -328,31 +333,71 @@ struct Span {
     int batch, first, len, tile;
 };
 
-// Tiles of `size` tokens are numbered so that a sequence is found without adding up the lengths before it:
-// sequence i's are slots floor(offsets[i] / size) + i and on, as floor((o + n) / size) - floor(o / size) + 1
-// is at least ceil(n / size).  Some slots have no tile.
+// A call's tiles of `size` tokens are dealt out by slots, at least as many as there are tiles.
 __host__ __device__ inline int64_t slots_of(int64_t tokens, int64_t sequences, int size) { return tokens / size + sequences; }
 
-// The tile in a slot, by a whole warp; false: none.  `last_first`: a sequence's last tile in its first slot.
+// The tile in a slot, by a whole warp; false: none.  Tiles are the longer to work on the further they lie from one end
+// of their sequence, the first one (from_last false: a query's keys begin there) or the last.  Sorted, and of up to
+// kSorted sequences: those that take longest are in the first slots, over all sequences, so that the pairs' work ends
+// together.  Otherwise sequence after sequence, the longest of each first, numbered so that a sequence is found without adding up the lengths before it: sequence i's slots are
+// floor(offsets[i] / size) + i and on, as floor((o + n) / size) - floor(o / size) + 1 is at least ceil(n / size).
 // Offsets that do not count up within the row are cut to it, and reported in the device error word.
-__device__ __forceinline__ bool find_tile(const Tokens& t, int size, int slot, bool last_first, Span* s) {
+constexpr int kSorted = 128;
+template <bool Sorted>
+__device__ __forceinline__ bool find_tile(const Tokens& t, int size, int slot, bool from_last, Span* s) {
     const int lane = threadIdx.x & 31;
     auto offset = [&](int i) { return (int)min(max(t.offsets[i], (int64_t)0), (int64_t)t.seq); };
-    int lo = 0, hi = t.sequences;        // the sequence is the last whose first slot is not behind `slot`
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-        const bool before = at < hi && offset(at) / size + at <= slot;
-        const int n = __popc(__ballot_sync(0xffffffffu, before));
-        if (n == 0) return false;
-        lo += (n - 1) * step;
-        hi = min(lo + step, hi);
+    auto tiles_of = [&](int i) { return (max(offset(i + 1) - offset(i), 0) + size - 1) / size; };
+    int seq, far;                        // the sequence, and how far from the end the tile lies
+    if (Sorted && t.sequences <= kSorted) {
+        int n[kSorted / 32];
+#pragma unroll
+        for (int i = 0; i < kSorted / 32; ++i) n[i] = 32 * i + lane < t.sequences ? tiles_of(32 * i + lane) : 0;
+        auto as_far = [&](int d) {       // tiles at least that far away
+            int c = 0;
+#pragma unroll
+            for (int i = 0; i < kSorted / 32; ++i) c += max(n[i] - d, 0);
+            return (int)__reduce_add_sync(0xffffffffu, (unsigned)c);
+        };
+        if (slot >= as_far(0)) return false;
+        int most = 0;
+#pragma unroll
+        for (int i = 0; i < kSorted / 32; ++i) most = max(most, n[i]);
+        int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);    // as_far(lo) > slot >= as_far(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (as_far(mid) > slot) lo = mid;
+            else hi = mid;
+        }
+        int k = slot - as_far(lo + 1);   // of the sequences that have one there
+        far = lo;
+        seq = 0;
+#pragma unroll
+        for (int i = 0; i < kSorted / 32; ++i) {
+            const unsigned has = __ballot_sync(0xffffffffu, n[i] > far);
+            const int c = __popc(has);
+            if (k >= 0 && k < c) seq = 32 * i + (int)__fns(has, 0, k + 1);
+            k -= c;
+        }
+    } else {
+        int lo = 0, hi = t.sequences;    // the sequence is the last whose first slot is not behind `slot`
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+            const bool before = at < hi && offset(at) / size + at <= slot;
+            const int c = __popc(__ballot_sync(0xffffffffu, before));
+            if (c == 0) return false;
+            lo += (c - 1) * step;
+            hi = min(lo + step, hi);
+        }
+        seq = lo;
+        const int k = slot - (offset(seq) / size + seq), tiles = tiles_of(seq);
+        if (k < 0 || k >= tiles) return false;
+        far = tiles - 1 - k;
     }
-    const int64_t a = t.offsets[lo], b = t.offsets[lo + 1];
+    const int64_t a = t.offsets[seq], b = t.offsets[seq + 1];
     if ((a < 0 || b < a || b > t.seq) && lane == 0) atomicExch(t.err, (int)TB_ERR_INVALID_VALUE);
-    const int first = offset(lo), len = max(offset(lo + 1) - first, 0), tiles = (len + size - 1) / size;
-    const int k = slot - (first / size + lo);
-    if (k < 0 || k >= tiles) return false;
-    *s = Span{0, first, len, last_first ? tiles - 1 - k : k};
+    const int first = offset(seq), len = max(offset(seq + 1) - first, 0);
+    *s = Span{0, first, len, from_last ? (len + size - 1) / size - 1 - far : far};
     return true;
 }
 

@@ -70,7 +70,7 @@ __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((12
 
 // Barriers of either kernel.
 struct Bars {
-    uint32_t answer, keep, keep_free, full, free, first, second, first_taken, second_taken, aux, aux_free, acc, acc_free, tail, drain,
+    uint32_t answer, keep, keep_free, full, free, first, second, first_taken, second_taken, aux, aux_free, acc, acc_free, tail, mended, drain,
         done, work_full, work_empty, words, slot;
 };
 template <class L>
@@ -86,9 +86,9 @@ __device__ __forceinline__ Bars bars_at(uint32_t at) {
     b.full = take(L::kStages), b.free = take(L::kStages);
     b.first = take(2), b.second = take(1), b.first_taken = take(1), b.second_taken = take(1);
     b.aux = take(2), b.aux_free = take(2), b.acc = take(1), b.acc_free = take(1);
-    b.tail = take(1), b.drain = take(1), b.done = take(1), b.work_full = take(1), b.work_empty = take(1);
+    b.tail = take(1), b.mended = take(1), b.drain = take(1), b.done = take(1), b.work_full = take(1), b.work_empty = take(1);
     b.words = take(3), b.slot = at;
-    static_assert((2 + 4 + 2 * L::kStages + 5 + 6 + 5 + 3) * 8 + 4 <= 512 && L::kStreams + 2 <= 6);
+    static_assert((2 + 4 + 2 * L::kStages + 5 + 6 + 6 + 3) * 8 + 4 <= 512 && L::kStreams + 2 <= 6);
     return b;
 }
 template <class L>
@@ -110,6 +110,7 @@ __device__ __forceinline__ void init_bars(const Bars& b, int readers) {
     mbar_init(b.acc, 1);
     mbar_init(b.acc_free, 16);
     mbar_init(b.tail, 1);
+    mbar_init(b.mended, 1);
     mbar_init(b.drain, 1);
     mbar_init(b.done, 1);
     init_work(b.work_full, b.work_empty, readers);
@@ -158,17 +159,12 @@ struct Loader {
         __syncwarp();
     }
     static __device__ __forceinline__ int bytes(bool by_rows) { return by_rows ? Blocks * kHalfBox : kBox; }
-    __device__ __forceinline__ void expect_mended(int n) {
+    // Before a tile to be mended: `n` bytes in all streams.  (One at a time.)
+    __device__ __forceinline__ bool expect_mended(int n) {
+        if (tails++ && !__all_sync(0xffffffffu, mbar_wait(bar.mended, tails & 1, &p))) return false;
         if (elect_one()) mbar_expect_at(map_to(bar.tail, rank), n);
         __syncwarp();
-    }
-    __device__ __forceinline__ void wait_mended() { mbar_wait<kEnd>(bar.tail, tails++ & 1, &p); }
-    // `rows`: tokens of the tile that are the sequence's.
-    __device__ __forceinline__ void mend(int s, bool by_rows, int rows) {
-        clear_behind(smem + L::kStage0 + place(s) * L::kStageBytes, by_rows ? Blocks : 1, by_rows ? kRows / 2 : kRows,
-                     by_rows ? rows - (int)rank * (kRows / 2) : rows, lane);
-        if (lane == 0) mbar_arrive_release(map_to(bar.full + 8 * place(s), 0));
-        __syncwarp();
+        return true;
     }
     __device__ __forceinline__ void leave() const {
         constexpr int n = L::kStreams + 2;
@@ -183,6 +179,28 @@ struct Loader {
             *parity = (i / L::ring(s)) & 1;
             return bar.full + 8 * (L::first(s) + i % L::ring(s));
         });
+    }
+};
+
+// The warp that mends tiles at a sequence's end.  `rows`: tokens of the tile that are the sequence's.
+template <class L, int Blocks>
+struct Mender {
+    const Args& p;
+    const Bars& bar;
+    unsigned char* smem;
+    uint32_t rank;
+    int lane, tails;
+    __device__ __forceinline__ bool wait() { return __all_sync(0xffffffffu, mbar_wait(bar.tail, tails++ & 1, &p)); }
+    // Tile n of stream s.
+    __device__ __forceinline__ void mend(int s, int n, bool by_rows, int rows) const {
+        const int place = L::first(s) + n % L::ring(s);
+        clear_behind(smem + L::kStage0 + place * L::kStageBytes, by_rows ? Blocks : 1, by_rows ? kRows / 2 : kRows,
+                     by_rows ? rows - (int)rank * (kRows / 2) : rows, lane);
+        if (lane == 0) mbar_arrive_release(map_to(bar.full + 8 * place, 0));
+    }
+    __device__ __forceinline__ void done() const {
+        if (lane == 0) mbar_arrive(bar.mended);
+        __syncwarp();
     }
 };
 
@@ -220,7 +238,7 @@ __device__ __forceinline__ bool find_keys(const Args& p, unsigned index, Keys* k
     k->head = (int)(index % (unsigned)p.kv_heads);
     const unsigned slot = index / (unsigned)p.kv_heads;
     if (p.tokens.offsets) {
-        if (!find_tile(p.tokens, kSpan, (int)slot, false, &k->span)) return false;
+        if (!find_tile<true>(p.tokens, kSpan, (int)slot, true, &k->span)) return false;
     } else {                  // the longest first
         const unsigned batch = (unsigned)p.tokens.batch;
         k->span = Span{(int)(slot % batch), 0, p.tokens.seq, (int)(slot / batch)};
@@ -280,7 +298,10 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
             for (int i = 0; i < it.steps && ok; ++i) {
                 const int row = it.tile(i) * kRows, head = it.query_head(i, p.group), rows = it.span.len - row;
                 const bool mend = rows < kRows;
-                if (mend) load.expect_mended(2 * load.bytes(true) + 2 * load.bytes(false));
+                if (mend && !load.expect_mended(2 * load.bytes(true) + 2 * load.bytes(false))) {
+                    ok = false;
+                    break;
+                }
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     ok = ok && load.room(s);
@@ -288,15 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
                     const bool by_rows = s < 2;
                     load.load(s, by_rows, s == kQRows ? &m.q_rows : s == kDoRows ? &m.dout_rows : s == kDoSum ? &m.dout : &m.q,
                               it.span.first + row, head, batch, cols, mend);
-                    if (!mend) ++load.loaded[s];
-                }
-                if (mend && ok) {
-                    load.wait_mended();
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        load.mend(s, s < 2, rows);
-                        ++load.loaded[s];
-                    }
+                    ++load.loaded[s];
                 }
             }
         }
@@ -366,7 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
             if (elect_one()) mma_commit(bar.drain);
         }
     } else if (warp == 2) {
-        // log sums and deltas of the next query tile, negated; a query behind the end has P = 0
+        // The ends of sequences; log sums and deltas of the next query tile, negated.  A query behind the end has P = 0.
+        Mender<L, Blocks> ends{p, bar, smem, rank, lane, 0};
         const float f = power_of_two(ds_shift<Fmt>(p.norms) - kPShift<Fmt>);
         float* table = reinterpret_cast<float*>(smem + L::kAux);
         int n = 0;
@@ -382,6 +396,15 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
                 for (int k = 0; k < 4; ++k) {
                     const int row = row0 + 32 * k + lane;
                     x[k] = row < it.span.len ? aux[row] : make_float2(__int_as_float(0x7f800000), 0.f);
+                }
+                if (it.span.len - row0 < kRows) {
+                    if (!ends.wait()) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) ends.mend(s, n, s < 2, it.span.len - row0);
+                    ends.done();
                 }
                 // the log sums are read with the scores, the deltas with dP: each is free for the next tile behind that
                 if (n && !__all_sync(0xffffffffu, mbar_wait(bar.aux_free, (n - 1) & 1, &p))) {
@@ -418,8 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
         int n = 0, items = 0;
         bool ok = true;
         for (; more; move_on()) {
-            ask();
-            if (!ok || !live) continue;
+            if (!ok || !live) {
+                ask();
+                continue;
+            }
             const int mine = it.first + (int)rank;           // this CTA's keys as a query tile
             for (int i = 0; i < it.steps; ++i, ++n) {
                 if (!__all_sync(0xffffffffu, mbar_wait(bar.aux, n & 1, &p)) || !__all_sync(0xffffffffu, mbar_wait<kRelaxed>(bar.first, n & 1, &p))) {
@@ -512,17 +537,13 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
                     mbar_arrive(bar.aux_free + 8);
                 }
             }
+            ask();
             if (!ok) continue;
             if (!__all_sync(0xffffffffu, mbar_wait<kRelaxed>(bar.acc, items++ & 1, &p))) {
                 ok = false;
                 continue;
             }
             tmem_fence_after();
-            auto give_back = [&] {
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(acc_free);
-            };
             const int in_seq = it.span.tile * kSpan + (int)rank * kRows + quad * 32, rows = min(32, it.span.len - in_seq);
             if (rows > 0) {
                 const int token = it.span.first + in_seq, g = !half;     // dV, dK
@@ -530,9 +551,11 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
                                static_cast<T*>(half ? p.grad0 : p.grad1) + it.span.batch * p.stride[g][0] + token * p.stride[g][1] + it.head * p.stride[g][2],
                                p.stride[g][1], token, it.head, it.span.batch};
                 store_rows<Fmt>(smem + L::kOut + (warp - kWorkWarp) * kOutStage, (half ? dk : dv) + lanes,
-                                half ? p.scale * power_of_two(-shift) : power_of_two(-kPShift<Fmt>), to, rows, 0, p.dim, lane, give_back);
+                                half ? p.scale * power_of_two(-shift) : power_of_two(-kPShift<Fmt>), to, rows, 0, p.dim, lane, acc_free);
             } else {
-                give_back();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(acc_free);
             }
         }
         stored_all(lane);
@@ -554,7 +577,7 @@ __device__ __forceinline__ bool find_queries(const Args& p, unsigned index, Quer
     q->head = (int)(index % (unsigned)p.heads);
     const unsigned slot = index / (unsigned)p.heads;
     if (p.tokens.offsets) {
-        if (!find_tile(p.tokens, kSpan, (int)slot, true, &q->span)) return false;
+        if (!find_tile<true>(p.tokens, kSpan, (int)slot, false, &q->span)) return false;
     } else {
         const unsigned batch = (unsigned)p.tokens.batch;
         q->span = Span{(int)(slot % batch), 0, p.tokens.seq, p.tiles - 1 - (int)(slot / batch)};
@@ -575,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
     const Bars bar = bars_at<L>(smem0 + L::kBars);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
-    if (threadIdx.x == 0) init_bars<L>(bar, 2 * 9 + 1);
+    if (threadIdx.x == 0) init_bars<L>(bar, 2 * 10 + 1);
     if (warp == 3) tmem_alloc_all(bar.slot);
     tmem_fence_before();
     __syncthreads();
@@ -614,20 +637,17 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
                 const int row = (it.steps - 1 - i) * kRows, rows = it.span.len - row;
                 // (scores of keys behind the end are hidden)
                 const bool mend = rows < kRows;
-                if (mend) load.expect_mended(load.bytes(true) + load.bytes(false));
+                if (mend && !load.expect_mended(load.bytes(true) + load.bytes(false))) {
+                    ok = false;
+                    break;
+                }
 #pragma unroll
                 for (int s = 0; s < 3; ++s) {
                     ok = ok && load.room(s);
                     if (!ok) break;
                     load.load(s, s < 2, s == kKRows ? &m.k_rows : s == kVRows ? &m.v_rows : &m.k, it.span.first + row, kv_head, batch, cols,
                               mend && s != kKRows);
-                    if (!mend || s == kKRows) ++load.loaded[s];
-                }
-                if (mend && ok) {
-                    load.wait_mended();
-                    load.mend(kVRows, true, rows);
-                    load.mend(kKSum, false, rows);
-                    ++load.loaded[kVRows], ++load.loaded[kKSum];
+                    ++load.loaded[s];
                 }
             }
         }
@@ -691,6 +711,25 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
             }
             if (elect_one()) mma_commit(bar.drain);
         }
+    } else if (warp == 2) {
+        Mender<L, Blocks> ends{p, bar, smem, rank, lane, 0};
+        int n = 0;
+        bool ok = true;
+        for (; more; move_on()) {
+            ask();
+            if (!ok || !live) continue;
+            const int rows = it.span.len - (it.steps - 1) * kRows;
+            if (rows < kRows) {              // the first keys and values end with the sequence
+                if (!ends.wait()) {
+                    ok = false;
+                    continue;
+                }
+                ends.mend(kVRows, n, true, rows);
+                ends.mend(kKSum, n, false, rows);
+                ends.done();
+            }
+            n += it.steps;
+        }
     } else if (warp == 3) {
         hand_out(work, rank, &p);
     } else if (warp >= kWorkWarp) {
@@ -704,8 +743,10 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
         int n = 0, items = 0;
         bool ok = true;
         for (; more; move_on()) {
-            ask();
-            if (!ok || !live) continue;
+            if (!ok || !live) {
+                ask();
+                continue;
+            }
             const int in_seq = it.span.tile * kSpan + (int)rank * kRows + quad * 32, rows = min(32, it.span.len - in_seq);
             const int mine = 2 * it.span.tile + (int)rank;       // this CTA's queries as a key tile
             float2 aux = make_float2(0.f, 0.f);
@@ -774,26 +815,24 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(taken);
             }
+            ask();
             if (!ok) continue;
             if (!__all_sync(0xffffffffu, mbar_wait<kRelaxed>(bar.acc, items++ & 1, &p))) {
                 ok = false;
                 continue;
             }
             tmem_fence_after();
-            auto give_back = [&] {
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(acc_free);
-            };
             if (rows > 0 && from < to_col) {
                 const int token = it.span.first + in_seq;
                 const Place to{&m.out0,
                                static_cast<T*>(p.grad0) + it.span.batch * p.stride[0][0] + token * p.stride[0][1] + it.head * p.stride[0][2],
                                p.stride[0][1], token, it.head, it.span.batch};
                 store_rows<Fmt>(smem + L::kOut + (warp - kWorkWarp) * kOutStage, dq + lanes, p.scale * power_of_two(-shift), to, rows, from,
-                                to_col, lane, give_back);
+                                to_col, lane, acc_free);
             } else {
-                give_back();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(acc_free);
             }
         }
         stored_all(lane);
@@ -807,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
 
 // ---------------------------------------------------------------- before the products
 // A row's log sum in powers of two and dout . out; fp16: the largest norms of the rows of dout and of v in any
-// sequence too.  Eight lanes a row, 16 bytes at a time.
+// sequence too.  Eight lanes a row, 16 bytes at a time, kRowsAtOnce rows in flight.
 struct Rows {
     const void *dout, *out, *v;
     int64_t stride[3][3];     // of batch, seq, head
@@ -816,9 +855,9 @@ struct Rows {
     unsigned* norms;
     const int64_t* offsets;
     int sequences, batch, seq, heads, kv_heads, dim;
-    int64_t ctas;             // of rows of dout; the others have rows of v
+    unsigned chunks, ctas;    // of a head's tokens; of rows of dout, the others have rows of v
 };
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 256, kRowsAtOnce = 2, kRowsCta = kRowThreads / 8 * kRowsAtOnce;
 
 template <class Fmt>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ Rows p) {
@@ -826,42 +865,60 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     pdl_wait();
     pdl_trigger();
     const bool of_v = blockIdx.x >= p.ctas;
-    const int heads = of_v ? p.kv_heads : p.heads, part = threadIdx.x & 7;
-    const int64_t row = ((int64_t)blockIdx.x - (of_v ? p.ctas : 0)) * (kRowThreads / 8) + threadIdx.x / 8;
-    const int64_t token = row / heads;
-    const int head = (int)(row - token * heads);
-    const int batch = (int)(token / p.seq), at = (int)(token - (int64_t)batch * p.seq);
-    const bool live = batch < p.batch;
-    float dot = 0.f, square = 0.f;
-    if (live) {
-        auto row_of = [&](const void* x, int i) {
-            return static_cast<const char*>(x) + (batch * p.stride[i][0] + at * p.stride[i][1] + head * p.stride[i][2]) * 2;
-        };
-        const char *a = row_of(of_v ? p.v : p.dout, of_v ? 2 : 0), *b = of_v ? nullptr : row_of(p.out, 1);
-        for (int c = part * 8; c < p.dim; c += 64) {
-            float x[8], y[8];
-            unpack8<Fmt>(*reinterpret_cast<const uint4*>(a + 2 * c), x);
-            if (!of_v) unpack8<Fmt>(*reinterpret_cast<const uint4*>(b + 2 * c), y);
+    const unsigned heads = of_v ? p.kv_heads : p.heads, part = threadIdx.x & 7;
+    const unsigned cta = blockIdx.x - (of_v ? p.ctas : 0), row = cta / p.chunks, chunk = cta - row * p.chunks;   // of a head's tokens
+    const unsigned batch = row / heads, head = row - batch * heads;
+    auto start = [&](const void* x, int i) {
+        return static_cast<const char*>(x) + (batch * p.stride[i][0] + head * p.stride[i][2] + part * 8) * 2;
+    };
+    const char *a = start(of_v ? p.v : p.dout, of_v ? 2 : 0), *b = start(p.out, 1);
+    const int64_t step_a = p.stride[of_v ? 2 : 0][1] * 2, step_b = p.stride[1][1] * 2;
+    const int at = (int)chunk * kRowsCta + threadIdx.x / 8;
+    uint4 x[kRowsAtOnce][2], y[kRowsAtOnce][2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (!of_v) dot = __fmaf_rn(x[e], y[e], dot);
-                if constexpr (kNorms) square = __fmaf_rn(x[e], x[e], square);
+    for (int i = 0; i < kRowsAtOnce; ++i) {
+        const int s = at + i * (kRowThreads / 8);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {    // 64 columns each
+            x[i][c] = y[i][c] = make_uint4(0, 0, 0, 0);
+            if (s < p.seq && (int)part * 8 + 64 * c < p.dim) {
+                x[i][c] = ld_stream_u4(a + s * step_a + 128 * c);
+                if (!of_v) y[i][c] = ld_stream_u4(b + s * step_b + 128 * c);
             }
         }
     }
+    unsigned most = 0;
 #pragma unroll
-    for (int o = 4; o; o >>= 1) {
-        dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if constexpr (kNorms) square += __shfl_xor_sync(0xffffffffu, square, o);
-    }
-    if (live && !of_v && part == 0) {
-        const int64_t i = ((int64_t)batch * heads + head) * p.seq + at;
-        p.aux[i] = make_float2(p.lse[i] * kLog2e, dot);
+    for (int i = 0; i < kRowsAtOnce; ++i) {
+        const int s = at + i * (kRowThreads / 8);
+        float dot = 0.f, square = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float u[8], v[8];
+            unpack8<Fmt>(x[i][c], u);
+            unpack8<Fmt>(y[i][c], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                dot = __fmaf_rn(u[e], v[e], dot);
+                if constexpr (kNorms) square = __fmaf_rn(u[e], u[e], square);
+            }
+        }
+#pragma unroll
+        for (int o = 4; o; o >>= 1) {
+            dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            if constexpr (kNorms) square += __shfl_xor_sync(0xffffffffu, square, o);
+        }
+        if (s < p.seq && !of_v && part == 0) {
+            const int64_t k = (int64_t)row * p.seq + s;
+            p.aux[k] = make_float2(p.lse[k] * kLog2e, dot);
+        }
+        if constexpr (kNorms) {
+            const bool counts = s < p.seq && square <= 3.4028235e38f && (!p.offsets || (s >= p.offsets[0] && s < p.offsets[p.sequences]));
+            if (counts) most = max(most, __float_as_uint(sqrtf(square) * 1.0001f));
+        }
     }
     if constexpr (kNorms) {
-        const bool counts = live && square <= 3.4028235e38f &&
-                            (!p.offsets || (at >= p.offsets[0] && at < p.offsets[p.sequences]));
-        const unsigned most = __reduce_max_sync(0xffffffffu, counts ? __float_as_uint(sqrtf(square) * 1.0001f) : 0u);
+        most = __reduce_max_sync(0xffffffffu, most);
         if ((threadIdx.x & 31) == 0 && most) atomicMax(p.norms + of_v, most);
     }
 }
@@ -880,10 +937,10 @@ tb_status launch(Maps& m, Args p, const Rows& r, const tb_heads* const (&grads)[
     if (resident_clusters(reinterpret_cast<const void*>(&dkv_kernel<Fmt, Blocks>), kThreads, kv_bytes, 2) < 1 ||
         resident_clusters(reinterpret_cast<const void*>(&dq_kernel<Fmt, Blocks>), kThreads, q_bytes, 2) < 1)
         return TB_ERR_CUDA;
-    int64_t ctas = r.ctas;
+    int64_t ctas = (int64_t)r.chunks * batch * r.heads;
     if (!bf) {
         if (cudaMemsetAsync(r.norms, 0, 2 * sizeof(unsigned), st) != cudaSuccess) return TB_ERR_CUDA;
-        ctas += ceil_div(batch * seq * r.kv_heads, kRowThreads / 8);
+        ctas += (int64_t)r.chunks * batch * r.kv_heads;
     }
     if (launch_pdl(rows_kernel<Fmt>, dim3((unsigned)ctas), dim3(kRowThreads), 0, st, r) != cudaSuccess) return TB_ERR_CUDA;
     const int64_t slots = r.offsets ? slots_of(seq, r.sequences, kSpan) : p.tiles * batch;
@@ -961,7 +1018,7 @@ extern "C" tb_status tb_attention_bwd(const tb_heads* dout, const tb_heads* q, c
     if (overlap(ws, sums) || overlap(ws, starts)) return TB_ERR_ALIAS;
     if (offsets && sequences == 0) return TB_OK;
     const int64_t tiles = ceil_div(seq, kSpan), slots = offsets ? slots_of(seq, sequences, kSpan) : tiles * batch;
-    if (slots > (1ll << 30) / q->heads || rows > (1ll << 35)) return TB_ERR_INVALID_VALUE;
+    if (slots > (1ll << 30) / q->heads || ceil_div(seq, kRowsCta) * batch > (1ll << 30) / q->heads) return TB_ERR_INVALID_VALUE;
     const bool bf = dtype == TB_BF16;
     Maps m{};
     CUtensorMap* const whole[4] = {&m.q, &m.k, &m.v, &m.dout};
@@ -990,7 +1047,7 @@ extern "C" tb_status tb_attention_bwd(const tb_heads* dout, const tb_heads* q, c
     r.lse = lse, r.aux = const_cast<float2*>(p.aux), r.norms = const_cast<unsigned*>(p.norms);
     r.offsets = offsets, r.sequences = (int)sequences;
     r.batch = (int)batch, r.seq = (int)seq, r.heads = p.heads, r.kv_heads = p.kv_heads, r.dim = p.dim;
-    r.ctas = ceil_div(rows, kRowThreads / 8);
+    r.chunks = (unsigned)ceil_div(seq, kRowsCta), r.ctas = r.chunks * (unsigned)(batch * q->heads);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (head_dim <= 64) return bf ? launch<BF16, 1>(m, p, r, grads, grad, batch, seq, st) : launch<F16, 1>(m, p, r, grads, grad, batch, seq, st);
     return bf ? launch<BF16, 2>(m, p, r, grads, grad, batch, seq, st) : launch<F16, 2>(m, p, r, grads, grad, batch, seq, st);
