@@ -113,7 +113,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     // The tensor memory: scores of both tiles (their first half becomes P), then results.
     const uint32_t score = tmem, result = tmem + 2 * kRows;
     const int cols = (p.dim + 15) / 16 * 16;
-    // What each warp works on, and behind it: asked for while the present work is begun.
+    // What each warp works on, and behind it: asked for when the present work is all under way.  (The answer waits for
+    // the slowest warp to have read the one before.)
     Work work{answer, work_full, work_empty, 0};
     Item it, next;
     bool live = find_item(p, blockIdx.x >> 1, &it), next_live = false, more = true;
@@ -149,7 +150,6 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 __syncwarp();
                 ++queries[t];
             }
-            ask();
             // keys, values of the last block, then of the one before
             for (int i = 0; i < 2 * blocks && ok; ++i) {
                 const int s = n % L::kRing, block = blocks - 1 - i / 2, row = it.span.first + block * kRows;
@@ -181,6 +181,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 __syncwarp();
                 ++n;
             }
+            ask();
         }
         const int mine[3] = {n, queries[0], queries[1]}, rings[3] = {L::kRing, 1, 1};
         way_out<3>(rank, mine, rings, drain, done, issued, smem + (issued - q0), &p, [&](int s, int i, uint32_t* parity) {
@@ -222,7 +223,6 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 }
                 if (ok && elect_one()) mma_commit(empty + 8 * (n % L::kRing));
                 __syncwarp();
-                ask();
                 for (int i = 0; i < blocks && ok; ++i) {
                     const int value = n + 1 + 2 * i, key = value + 1;
                     if (!wait_ring(value) || (i + 1 < blocks && !wait_ring(key))) {
@@ -256,6 +256,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 }
                 n += 2 * blocks;
                 for (int t = 0; t < 2; ++t) uses[t] += it.blocks(t) != 0;
+                ask();
             }
             if (elect_one()) mma_commit(drain);
         }
@@ -263,12 +264,15 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         int n = 0, tails = 0;                // tiles of the ring, mended ones
         bool ok = true;
         for (; more; move_on()) {
-            ask();
-            if (!ok || !live) continue;
+            if (!ok || !live) {
+                ask();
+                continue;
+            }
             const int blocks = max(it.blocks0, it.blocks1), rows = it.span.len - (blocks - 1) * kRows, s = (n + 1) % L::kRing;
             if (rows < kRows) {              // the first values end with the sequence
                 if (!__all_sync(0xffffffffu, mbar_wait(tail, tails++ & 1, &p))) {
                     ok = false;
+                    ask();
                     continue;
                 }
                 clear_behind(smem + L::kStage0 + s * L::kStageBytes, 1, kRows, rows, lane);
@@ -278,6 +282,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 }
             }
             n += 2 * blocks;
+            ask();
         }
     } else if (warp == 3) {
         hand_out(work, rank, &p);

@@ -294,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
             }
             const int token = it.span.first + it.span.tile * kSpan + (int)rank * kRows, batch = it.span.batch;
             ok = load.keep(0, &m.k, token, it.head, batch) && load.keep(1, &m.v, token, it.head, batch);
-            ask();
             for (int i = 0; i < it.steps && ok; ++i) {
                 const int row = it.tile(i) * kRows, head = it.query_head(i, p.group), rows = it.span.len - row;
                 const bool mend = rows < kRows;
@@ -312,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
                     ++load.loaded[s];
                 }
             }
+            ask();
         }
         load.leave();
     } else if (warp == 1) {
@@ -349,7 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
                 }
                 ok = __all_sync(0xffffffffu, mbar_wait(bar.keep, items & 1, &p)) && scores(n, it.steps == 1) &&
                      __all_sync(0xffffffffu, mbar_wait(bar.keep + 8, items & 1, &p)) && dprobs(n, it.steps == 1);
-                ask();
                 for (int i = 0; i < it.steps && ok; ++i, ++n) {
                     // P^T lies over the scores: the next ones follow its product, in order
                     const bool more_tiles = i + 1 < it.steps, last = i + 2 == it.steps;
@@ -375,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
                     if (more_tiles && !dprobs(n + 1, last)) ok = false;
                 }
                 ++items;
+                ask();
             }
             if (elect_one()) mma_commit(bar.drain);
         }
@@ -386,8 +386,10 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
         int n = 0;
         bool ok = true;
         for (; more; move_on()) {
-            ask();
-            if (!ok || !live) continue;
+            if (!ok || !live) {
+                ask();
+                continue;
+            }
             for (int i = 0; i < it.steps; ++i, ++n) {
                 float2 x[4];
                 const int row0 = it.tile(i) * kRows;
@@ -424,6 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar.aux + 8);
             }
+            ask();
         }
     } else if (warp == 3) {
         hand_out(work, rank, &p);
@@ -632,7 +635,6 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
             }
             const int token = it.span.first + it.span.tile * kSpan + (int)rank * kRows, batch = it.span.batch, kv_head = it.head / p.group;
             ok = load.keep(0, &m.q, token, it.head, batch) && load.keep(1, &m.dout, token, it.head, batch);
-            ask();
             for (int i = 0; i < it.steps && ok; ++i) {
                 const int row = (it.steps - 1 - i) * kRows, rows = it.span.len - row;
                 // (scores of keys behind the end are hidden)
@@ -650,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
                     ++load.loaded[s];
                 }
             }
+            ask();
         }
         load.leave();
     } else if (warp == 1) {
@@ -687,7 +690,6 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
                 }
                 ok = __all_sync(0xffffffffu, mbar_wait(bar.keep, items & 1, &p)) && scores(n, it.steps == 1) &&
                      __all_sync(0xffffffffu, mbar_wait(bar.keep + 8, items & 1, &p)) && dprobs(n, it.steps == 1);
-                ask();
                 for (int i = 0; i < it.steps && ok; ++i, ++n) {
                     // The place of the scores of n + 1 held dS of n - 1, whose product came before.
                     const bool more_tiles = i + 1 < it.steps, last = i + 2 == it.steps;
@@ -708,6 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
                     __syncwarp();
                 }
                 ++items;
+                ask();
             }
             if (elect_one()) mma_commit(bar.drain);
         }
@@ -716,12 +719,15 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
         int n = 0;
         bool ok = true;
         for (; more; move_on()) {
-            ask();
-            if (!ok || !live) continue;
+            if (!ok || !live) {
+                ask();
+                continue;
+            }
             const int rows = it.span.len - (it.steps - 1) * kRows;
             if (rows < kRows) {              // the first keys and values end with the sequence
                 if (!ends.wait()) {
                     ok = false;
+                    ask();
                     continue;
                 }
                 ends.mend(kVRows, n, true, rows);
@@ -729,6 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
                 ends.done();
             }
             n += it.steps;
+            ask();
         }
     } else if (warp == 3) {
         hand_out(work, rank, &p);
