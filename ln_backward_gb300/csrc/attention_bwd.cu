@@ -62,7 +62,7 @@ constexpr int kPShift = std::is_same<Fmt, F16>::value ? 14 : 0;
 template <class Fmt>
 __device__ __forceinline__ int ds_shift(const unsigned* norms) {
     if constexpr (std::is_same<Fmt, BF16>::value) return 0;
-    const float bound = 2.f * __uint_as_float(norms[0]) * __uint_as_float(norms[1]);
+    const float bound = 2.f * __uint_as_float(__ldcg(norms)) * __uint_as_float(__ldcg(norms + 1));
     const int e = (int)(__float_as_uint(bound) >> 23);
     return e == 0 || e == 255 ? 0 : min(max(13 + 127 - e, -100), 100);
 }
@@ -608,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
     cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + (bar.slot - smem0));
-    pdl_wait();
+    // This kernel follows dkv_kernel, whose results it does not touch, and starts as that one's CTAs end: every CTA of it
+    // had seen all earlier kernels complete before it let this one start.  It ends after it (see the end).
     asm volatile("fence.proxy.async;" ::: "memory");
     pdl_trigger();
 
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
             const int in_seq = it.span.tile * kSpan + (int)rank * kRows + quad * 32, rows = min(32, it.span.len - in_seq);
             const int mine = 2 * it.span.tile + (int)rank;       // this CTA's queries as a key tile
             float2 aux = make_float2(0.f, 0.f);
-            if (lane < rows) aux = p.aux[((int64_t)it.span.batch * p.heads + it.head) * p.tokens.seq + it.span.first + in_seq + lane];
+            if (lane < rows) aux = __ldcg(&p.aux[((int64_t)it.span.batch * p.heads + it.head) * p.tokens.seq + it.span.first + in_seq + lane]);
             const float base = (float)shift - aux.x;
             const unsigned long long b2 = pair_of(base, base), delta = pair_of(-aux.y, -aux.y);
             for (int i = 0; i < it.steps; ++i, ++n) {
@@ -849,6 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
     __syncthreads();
     cluster_sync();             // no CTA leaves while the other may signal or read it
     if (warp == 3) tmem_free_all(tmem);
+    pdl_wait();                 // what waits for this kernel waits for both
 }
 
 // ---------------------------------------------------------------- before the products

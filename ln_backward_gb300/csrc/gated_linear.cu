@@ -26,7 +26,7 @@ struct Args {
     // kUp: up.  kBack: two products in one launch, the one with the longer tiles first.
     Tiles part[2];
     int first;                // kBack: which product part[0] is, 0: dX, 1: dW
-    int light, extra;         // kBack: pairs from `light` on have a tile of part[0] less, and `extra` of part[1] more
+    int light, extra;         // kBack: pairs from `light` on have a tile of part[0] less, and first `extra` of part[1]
     int rows, inner, hidden;  // N, F, D
     int half;                 // kUp: columns of a tile of G and of U; kBack: inner rounded up, columns of dG in the workspace
     int a_rows;               // rows of a box of X or dG by rows: fewer than kHalf where there are no more
@@ -111,13 +111,12 @@ __device__ __forceinline__ bool pair_tile(const Args& p, int pair, int pairs, in
         return true;
     }
     j -= mine;
-    int64_t t = 0;
-    if (p.extra && pair >= p.light && j < p.extra) {
-        t = (int64_t)(pair - p.light) * p.extra + j;
-    } else {
-        if (p.extra && pair >= p.light) j -= p.extra;
-        t = (int64_t)(p.extra ? (pairs - p.light) * p.extra : 0) + pair + (int64_t)j * pairs;
-    }
+    // the shorter ones begin with the pairs that have a long one less
+    const bool light = pair >= p.light;
+    const int place = light ? pair - p.light : pair + pairs - p.light;
+    int64_t t;
+    if (light && j < p.extra) t = (int64_t)place * p.extra + j;
+    else t = (int64_t)(pairs - p.light) * p.extra + place + (int64_t)(j - (light ? p.extra : 0)) * pairs;
     if (t >= p.part[1].count) return false;
     *w = tile_at(p.part[1], 1, (unsigned)t);
     return true;
@@ -495,7 +494,8 @@ struct Gate {
     const void *dH, *G, *U;
     void* out;                // [rows][2][half], zeros behind a row's `inner`
     float* unscale;           // fp16: written by the second pass
-    unsigned* top;            // fp16: magnitude as bits, zeroed before the first pass
+    unsigned* tops;           // fp16: magnitude as bits, of each CTA of the first pass
+    int n_tops;
     int64_t rows;
     int inner, half;
 };
@@ -514,7 +514,15 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(const __grid_constant__ 
     const int64_t vectors = p.rows * per_row, step = (int64_t)gridDim.x * kThreads;
     float scale = 1.f;
     if constexpr (!Top && std::is_same<Fmt, F16>::value) {
-        const int e = shift_for(*p.top);
+        __shared__ unsigned most_of[kThreads / 32];
+        unsigned m = 0;
+        for (int i = threadIdx.x; i < p.n_tops; i += kThreads) m = max(m, p.tops[i]);
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (threadIdx.x % 32 == 0) most_of[threadIdx.x / 32] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) m = max(m, most_of[i]);
+        const int e = shift_for(m);
         scale = power_of_two(e);
         if (blockIdx.x == 0 && threadIdx.x == 0) *p.unscale = power_of_two(-e);
     }
@@ -558,8 +566,15 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(const __grid_constant__ 
         }
     }
     if constexpr (Top) {
+        __shared__ unsigned most_of[kThreads / 32];
         most = __reduce_max_sync(0xffffffffu, most);
-        if (threadIdx.x % 32 == 0 && most) atomicMax(p.top, most);
+        if (threadIdx.x % 32 == 0) most_of[threadIdx.x / 32] = most;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+#pragma unroll
+            for (int i = 1; i < kThreads / 32; ++i) most = max(most, most_of[i]);
+            p.tops[blockIdx.x] = most;
+        }
     }
 }
 
@@ -627,7 +642,7 @@ constexpr int64_t kChain = 65536;
 struct Cut {
     int half, splits;         // kUp: columns of a tile of G, parts of the contraction
     int64_t inner;            // kBack: F rounded up to whole stages
-    int splits_x, splits_w;
+    int splits_x, splits_w, gate_ctas;
     size_t off_sums, off_dg, off_sums_x, off_sums_w, off_scale, total;
 };
 
@@ -654,23 +669,20 @@ void pick_up(int64_t n, int64_t d, int64_t f, int64_t pairs, Cut* c) {
 }
 
 // Two products' tiles dealt to the pairs: the longer ones round robin, then the shorter, of which the pairs
-// with one long tile less first get as many as fill the gap.
+// with one long tile less first get as many as fill the gap, and then the first of the others.
 struct Deal {
     int light, extra;
     double cost;
 };
 Deal deal(int64_t long_tiles, double long_cost, int64_t short_tiles, double short_cost, int64_t pairs) {
     Deal r{0, 0, 0.0};
-    const int64_t more = long_tiles % pairs, base = long_tiles / pairs;
+    const int64_t heavy = long_tiles % pairs, light = pairs - heavy, base = long_tiles / pairs;
     int64_t extra = 0;
-    if (more && short_tiles) {
-        extra = (int64_t)(long_cost / short_cost + 0.5);
-        extra = std::min(extra, short_tiles / (pairs - more));
-    }
-    const int64_t rest = ceil_div(short_tiles - extra * (pairs - more), pairs);
-    r.light = (int)more, r.extra = (int)extra;
-    const double heavy = (double)(base + (more > 0)) * long_cost, light = (double)base * long_cost + (double)extra * short_cost;
-    r.cost = std::max(heavy, light) + (double)rest * short_cost;
+    if (heavy && short_tiles) extra = std::min((int64_t)(long_cost / short_cost + 0.5), short_tiles / light);
+    const int64_t rest = short_tiles - extra * light, each = rest / pairs, over = rest % pairs;
+    r.light = (int)heavy, r.extra = (int)extra;
+    r.cost = std::max((double)base * long_cost + (double)(extra + each + (over > 0)) * short_cost,
+                      heavy ? (double)(base + 1) * long_cost + (double)(each + (over > light)) * short_cost : 0.0);
     return r;
 }
 
@@ -717,7 +729,8 @@ Cut cut_call(int64_t n, int64_t d, int64_t f, bool back, int sms) {
         c.off_dg = take((size_t)n * 2 * c.inner * 2);
         if (c.splits_x > 1) c.off_sums_x = take((size_t)c.splits_x * n * d * sizeof(float));
         if (c.splits_w > 1) c.off_sums_w = take((size_t)c.splits_w * 2 * f * d * sizeof(float));
-        c.off_scale = take(2 * sizeof(float));
+        c.gate_ctas = (int)std::min<int64_t>(ceil_div(n * c.inner / 8, kThreads), 8ll * sms);
+        c.off_scale = take((1 + (size_t)c.gate_ctas) * sizeof(float));
     }
     c.total = at;
     return c;
@@ -829,14 +842,11 @@ tb_status run_back(const Problem& q, const Cut& c) {
     float* scale = reinterpret_cast<float*>(q.ws + c.off_scale);
     Gate e{};
     e.dH = q.dH, e.G = q.G, e.U = q.U, e.out = dg;
-    e.unscale = scale, e.top = reinterpret_cast<unsigned*>(scale + 1);
+    e.unscale = scale, e.tops = reinterpret_cast<unsigned*>(scale + 1), e.n_tops = c.gate_ctas;
     e.rows = q.n, e.inner = (int)q.f, e.half = (int)c.inner;
-    const int64_t ctas = std::min<int64_t>(ceil_div(q.n * c.inner / 8, kThreads), 8ll * q.sms);
-    if (!bf) {
-        if (cudaMemsetAsync(e.top, 0, sizeof(unsigned), q.st) != cudaSuccess) return TB_ERR_CUDA;
-        if (launch_pdl(gate_kernel<Fmt, Act, true>, dim3((unsigned)ctas), dim3(kThreads), 0, q.st, e) != cudaSuccess)
-            return TB_ERR_CUDA;
-    }
+    const int ctas = c.gate_ctas;
+    if (!bf && launch_pdl(gate_kernel<Fmt, Act, true>, dim3((unsigned)ctas), dim3(kThreads), 0, q.st, e) != cudaSuccess)
+        return TB_ERR_CUDA;
     if (launch_pdl(gate_kernel<Fmt, Act, false>, dim3((unsigned)ctas), dim3(kThreads), 0, q.st, e) != cudaSuccess)
         return TB_ERR_CUDA;
 
