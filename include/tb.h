@@ -8,6 +8,8 @@
  *   - the LayerNorm backward (dX, dgamma, dbeta);
  *   - rotary positions and the per-head RMS norm of queries and keys, with their
  *     gradients;
+ *   - causal attention over whole prompts, with its gradient;
+ *   - the gated projections of a feed-forward block, with their gradients;
  *   - the softmax cross entropy of a linear output layer, with its gradients.
  *
  * Sources (web pages on the subject; cited by page title and section):
@@ -17,7 +19,7 @@
  *
  * Conventions for every entry point
  *   - Buffers are device-accessible memory owned by the caller, row-major and
- *     contiguous (queries and keys are strided: see tb_heads).  The library
+ *     contiguous (queries, keys and values are strided: see tb_heads).  The library
  *     keeps no pointer after a call returns, except the AdamW plan's copy of
  *     the tensor table (see tb_adamw_plan_create).
  *   - `stream` is a cudaStream_t passed as void*; NULL is the legacy default
@@ -25,8 +27,8 @@
  *     fault inside a kernel surfaces at the caller's next synchronisation.
  *   - Argument errors are reported synchronously, before anything is enqueued,
  *     as a tb_status.  A failed launch reports TB_ERR_CUDA.
- *   - The softmax, LayerNorm, RMSNorm, rotary and output-layer kernels are
- *     launched as programmatic
+ *   - The softmax, LayerNorm, RMSNorm, rotary, attention, gated and output-layer
+ *     kernels are launched as programmatic
  *     dependents of the work before them on `stream`: their blocks may start
  *     while the previous kernel drains, set up shared memory and (LayerNorm,
  *     RMSNorm) prefetch their first rows into L2, but they load and store no
@@ -35,8 +37,9 @@
  *   - fp32 pointers must be 4-byte aligned, 16-bit pointers 2-byte aligned and
  *     64-bit ones 8-byte aligned (TB_ERR_MISALIGNED otherwise).  Any larger
  *     alignment is optional: 16-byte aligned buffers take the vectorised path,
- *     others a scalar one.  Two exceptions: workspaces are 16-byte aligned, and
- *     so are the output layer's H and W where D is a multiple of 8.
+ *     others a scalar one.  Exceptions: workspaces are 16-byte aligned, and
+ *     so are attention's heads, the gated projections' matrices, and the output
+ *     layer's H and W where D is a multiple of 8.
  *   - The calls are not thread-safe against tb_adamw_plan_destroy of the plan
  *     they use; otherwise they may be called from several host threads.
  */
@@ -78,12 +81,14 @@ int tb_version(void);
 /*
  * tb_device_error -- read (and optionally clear) the device-side error word of
  * the current device.  Kernels that wait on an mbarrier for their own bulk
- * copies (and, in the output layer's loss, tensor-core instructions) give up
+ * copies (and, in attention, the gated projections and the output layer's loss,
+ * tensor-core instructions) give up
  * after about one second; they then set this word to
  * TB_ERR_TIMEOUT, drain what they issued and return early (their outputs are
  * then undefined).  tb_adamw_step_device sets it to TB_ERR_INVALID_VALUE when
- * the step counter it reads is below 1, and tb_linear_xent when a target is
- * neither in the vocabulary nor ignore_index.  This call synchronises the
+ * the step counter it reads is below 1, tb_linear_xent when a target is
+ * neither in the vocabulary nor ignore_index, and the attention calls when offsets
+ * do not count up within the row.  This call synchronises the
  * current device.
  *   code   out: 0 when no kernel gave up since the last reset
  *   reset  nonzero: clear the word after reading it
@@ -130,6 +135,21 @@ tb_status tb_layernorm_bwd_selftest_timeout(int64_t wait_limit_ns, void* stream)
 #define TB_LINEAR_XENT_SELFTEST_LAUNCHES 11
 
 tb_status tb_linear_xent_selftest_timeout(int64_t wait_limit_ns, int* launches, void* stream);
+
+/*
+ * tb_attention_selftest_timeout, tb_gated_linear_selftest_timeout -- the same for
+ * the kernels of attention (forward, the gradient of keys and values, that of
+ * queries; heads of 64 and 128) and for the two products of the gated projections:
+ * TB_ATTENTION_SELFTEST_LAUNCHES and TB_GATED_LINEAR_SELFTEST_LAUNCHES launches on
+ * small internal problems, each with the loads of one of the two CTAs withheld, or
+ * a word by which the warps hand over what lies in tensor memory.
+ */
+#define TB_ATTENTION_SELFTEST_LAUNCHES 30
+#define TB_GATED_LINEAR_SELFTEST_LAUNCHES 8
+
+tb_status tb_attention_selftest_timeout(int64_t wait_limit_ns, int* launches, void* stream);
+
+tb_status tb_gated_linear_selftest_timeout(int64_t wait_limit_ns, int* launches, void* stream);
 
 /* ======================================================================== */
 /* Fused mixed-precision AdamW (multi-tensor)                               */
@@ -716,7 +736,7 @@ tb_status tb_linear_xent_bwd(const float* dloss, const void* H, const void* W,
  * tokens offsets[i] .. offsets[i + 1] - 1, any number of them, 0 and 1 included.  Tokens before the
  * first or behind the last sequence are not written, and whatever they hold (NaN included) reaches
  * no other token; nor does a token reach another sequence's.  Within a sequence k and v are finite:
- * an infinity or NaN may reach the rows of up to 127 tokens before it.  Offsets that do not count
+ * an infinity or NaN may reach the results of up to 255 tokens before it.  Offsets that do not count
  * up within 0 .. seq set the device error word to TB_ERR_INVALID_VALUE (tb_device_error); their
  * sequences are cut to the row.
  *
@@ -726,7 +746,7 @@ tb_status tb_linear_xent_bwd(const float* dloss, const void* H, const void* W,
  *   out              as many heads as q; shares no element with q, k or v
  *   lse              out: fp32 [batch, heads_q, seq], contiguous, what the gradient needs; NULL
  *                    when it is not wanted (serving)
- *   batch, seq       >= 0, batch <= 2^20, seq <= 2^30
+ *   batch, seq       >= 0, batch <= 2^20, seq <= 2^25
  *   head_dim         a multiple of 8, 8 .. 128
  *   offsets          device int64 [sequences + 1], 8-byte aligned; NULL: every batch entry is a
  *                    sequence (sequences is 0 then).  With offsets batch is 1.
@@ -734,8 +754,8 @@ tb_status tb_linear_xent_bwd(const float* dloss, const void* H, const void* W,
  *   dtype            TB_BF16 or TB_F16
  * Data starts on 16 bytes and strides are multiples of 8 elements, not 0 (except of a size of 1)
  * and below 2^39.
- * Sums are fp32.  P = exp(s - m), m within 8 ln 2 of the row's running maximum, is rounded to dtype on
- * its way into the second product; the sum below it is not.  Results are bitwise reproducible.
+ * Sums are fp32.  P = exp(s - m), m the maximum of keys before or one that is at most ln 8192 below it, is
+ * rounded to dtype on its way into the second product; the sum below it is not.  Results are bitwise reproducible.
  * Errors: TB_ERR_INVALID_VALUE, TB_ERR_UNSUPPORTED_DTYPE (TB_F32 has no such tensor-core product),
  * TB_ERR_MISALIGNED, TB_ERR_ALIAS, TB_ERR_CUDA.
  */

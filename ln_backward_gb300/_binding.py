@@ -38,7 +38,8 @@ EXPORTS = ("tb_status_string", "tb_version", "tb_device_error", "tb_adamw_plan_c
            "tb_linear_xent_bwd_workspace_size", "tb_linear_xent_bwd",
            "tb_linear_xent_selftest_timeout", "tb_gated_linear_workspace_size", "tb_gated_linear",
            "tb_gated_linear_bwd_workspace_size", "tb_gated_linear_bwd", "tb_attention",
-           "tb_attention_bwd_workspace_size", "tb_attention_bwd")
+           "tb_attention_bwd_workspace_size", "tb_attention_bwd", "tb_attention_selftest_timeout",
+           "tb_gated_linear_selftest_timeout")
 
 
 class TbError(RuntimeError):
@@ -126,6 +127,9 @@ def _load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.tb_layernorm_bwd_selftest_timeout.restype = i32
     lib.tb_linear_xent_selftest_timeout.argtypes = [i64, ctypes.POINTER(i32), vp]
     lib.tb_linear_xent_selftest_timeout.restype = i32
+    for fn in (lib.tb_attention_selftest_timeout, lib.tb_gated_linear_selftest_timeout):
+        fn.argtypes = [i64, ctypes.POINTER(i32), vp]
+        fn.restype = i32
     lib.tb_adamw_selftest_stale_counter.argtypes = [vp, ctypes.c_uint64, vp]
     lib.tb_adamw_selftest_stale_counter.restype = i32
     # tb_heads* and tb_rope_angles*: the binding passes addresses into one packed array
@@ -260,6 +264,25 @@ def tb_linear_xent_selftest_timeout(wait_limit_ns: int = 2_000_000, stream=None)
     launches = ctypes.c_int(0)
     _check("tb_linear_xent_selftest_timeout",
            lib.tb_linear_xent_selftest_timeout(int(wait_limit_ns), ctypes.byref(launches), _stream(stream)))
+    return launches.value
+
+
+TB_ATTENTION_SELFTEST_LAUNCHES, TB_GATED_LINEAR_SELFTEST_LAUNCHES = 30, 8
+
+
+def tb_attention_selftest_timeout(wait_limit_ns: int = 2_000_000, stream=None) -> int:
+    """The same for attention's kernels: TB_ATTENTION_SELFTEST_LAUNCHES launches."""
+    launches = ctypes.c_int(0)
+    _check("tb_attention_selftest_timeout",
+           lib.tb_attention_selftest_timeout(int(wait_limit_ns), ctypes.byref(launches), _stream(stream)))
+    return launches.value
+
+
+def tb_gated_linear_selftest_timeout(wait_limit_ns: int = 2_000_000, stream=None) -> int:
+    """The same for the gated projections' products: TB_GATED_LINEAR_SELFTEST_LAUNCHES launches."""
+    launches = ctypes.c_int(0)
+    _check("tb_gated_linear_selftest_timeout",
+           lib.tb_gated_linear_selftest_timeout(int(wait_limit_ns), ctypes.byref(launches), _stream(stream)))
     return launches.value
 
 

@@ -1,6 +1,26 @@
 // attention.cu -- causal attention over whole prompts.
 //
 //     s_ij = scale q_i . k_j for j <= i,  lse_i = log sum_j exp(s_ij),  out_i = sum_j exp(s_ij - lse_i) v_j
+//
+// One pass over the keys: P = exp(s - m) is taken against a row's maximum of earlier blocks, sums and results are
+// fp32, and where a row's sums show that the maximum has grown by much, results and sums are scaled to the new one.
+// So P needs no maximum of its own block before it, and is at most kMost, far from fp16's end.
+//
+// A pair of CTAs (see attention.cuh) takes 512 queries of one head, two tiles of 128 in each CTA, and walks the blocks
+// of 128 keys from the last one down.  Each CTA stages half of a block's keys (by rows) and half of its values' columns,
+// 16 KB each, in a ring of eight.  Scores lie in tensor memory, P as 16-bit pairs over them, the results beside them:
+// 512 columns at heads of 128.  Warp 0 loads, warp 1 of the first CTA issues the MMAs, warp 2 mends sequences' ends,
+// warp 3 hands out work, four warps for each tile turn scores into P, a row a lane, and write the results.  While one tile's
+// warps work the other's products run: P V of a block and the next scores, 1,024 clocks at heads of 128.
+//
+// What bounds it: the chain of one tile's block.  At heads of 128 its scores and P V take 1,024 clocks, handing over about
+// 400, P 1,100 (512 of them powers, at 32 a clock and SM), so a pair's two tiles need 2,700 where their MMAs need 2,048;
+// a piece of work adds the start of its first two blocks and its results, about 10,000.  bf16 4 x 4,096 tokens, 32 heads of
+// 128: 381 us in a stream of calls, 1,440 TFLOP/s, 77 % of cuBLAS's burst (419 us, 1,310, behind a cold start).
+// One CTA with tiles of its own took 466 us there: operands crossed shared memory at its 128 bytes a clock.  Heads of 64
+// are bound by P: fp16 16,384 tokens, 8 heads, 274 us, 1,000 TFLOP/s.  Two warps for the same rows instead of one: 449
+// against 440 us; a row's maximum before P: the same; registers shared out by setmaxnreg (208 and 88): 641 us, as the
+// compiler spills in both shares.
 #include "attention.cuh"
 
 namespace tb {
@@ -34,6 +54,7 @@ struct Args {
     float* lse;               // [batch][heads][seq]; NULL: not wanted
     int* err;
     unsigned long long wait_ns;
+    int withhold;             // self-test: a Withheld
 };
 
 // What a pair works on: kItem queries of one head.  Tile t of CTA r begins 256 t + 128 r behind the first of them.
@@ -88,9 +109,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + 8 * i, 2);
             mbar_init(q_empty + 8 * i, 1);
-            mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, 8);    // the warps of a tile, of both CTAs
-            mbar_init(o_full + 8 * i, 1);
+            mbar_init(s_full + 8 * i, 1 + (p.withhold == kScores));
+            mbar_init(p_full + 8 * i, 8 + (p.withhold == kTaken));   // the warps of a tile, of both CTAs
+            mbar_init(o_full + 8 * i, 1 + (p.withhold == kResults));
             mbar_init(o_empty + 8 * i, 8);
         }
         mbar_init(tail, 1);
@@ -127,7 +148,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 
     if (warp == 0) {
         int n = 0, queries[2] = {0, 0}, tails = 0;       // keys and values staged, tiles of queries, ends mended
-        bool ok = true;
+        bool ok = p.withhold != kLoads0 + (int)rank;
         for (; more; move_on()) {
             if (!ok || !live) {
                 ask();
@@ -448,7 +469,35 @@ tb_status launch(const CUtensorMap (&m)[4], const Args& p, int64_t items, cudaSt
                : TB_ERR_CUDA;
 }
 
+// The self-test's share of this kernel.
+template <int Blocks>
+tb_status withheld(int64_t wait_limit_ns, int* err, unsigned char* mem, cudaStream_t st, int* launches) {
+    const int64_t dim = 64 * Blocks;
+    tb_heads h[4];
+    for (int i = 0; i < 4; ++i) h[i] = self_heads(&mem, i == 1 || i == 2 ? 1 : kSelfHeads, dim);
+    CUtensorMap m[4];
+    for (int i = 0; i < 4; ++i)
+        if (!make_heads_map(&m[i], h[i], 1, kSelfTokens, dim, i == 1 ? kRows / 2 : kRows, true, i == 3)) return TB_ERR_CUDA;
+    Args p{};
+    p.tokens = Tokens{nullptr, 0, 1, (int)kSelfTokens, err};
+    p.heads = p.group = (int)kSelfHeads, p.dim = (int)dim;
+    p.tiles = (int)ceil_div(kSelfTokens, kItem);
+    p.scale_log2 = 1.f;
+    p.out = h[3].data, p.out_batch = h[3].stride_batch, p.out_seq = h[3].stride_seq, p.out_head = h[3].stride_head;
+    p.err = err, p.wait_ns = (unsigned long long)wait_limit_ns;
+    return run_withheld(err, st, launches, [&](int what) {
+        p.withhold = what;
+        return launch<BF16, Blocks>(m, p, p.tiles * kSelfHeads, st);
+    });
+}
+
 }  // namespace
+
+tb_status attention_withheld(int64_t wait_limit_ns, int* err, unsigned char* mem, cudaStream_t st, int* launches) {
+    const tb_status s = withheld<1>(wait_limit_ns, err, mem, st, launches);
+    return s == TB_OK ? withheld<2>(wait_limit_ns, err, mem, st, launches) : s;
+}
+
 }  // namespace tb
 
 extern "C" tb_status tb_attention(const tb_heads* q, const tb_heads* k, const tb_heads* v, const tb_heads* out, float* lse,

@@ -2,6 +2,26 @@
 //
 //     p_ij = exp(s_ij - lse_i),  dp_ij = dout_i . v_j,  ds_ij = p_ij (dp_ij - dout_i . out_i)
 //     dv_j = sum_i p_ij dout_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j
+//
+// Three kernels: rows_kernel forms dout . out of every row; dkv_kernel walks the queries of a tile of keys (four
+// products: scores, dP, dV, dK), dq_kernel the keys of a tile of queries (three: scores and dP again, dQ).  Five products
+// would do if one walk gave all three gradients, but then dQ of a tile is a sum over CTAs: of atomics, whose order
+// changes its bits, or of fp32 partial sums in memory.  All sums here stay in tensor memory, in one order.
+//
+// Pairs of CTAs work on 256 keys or queries (see attention.cuh).  Tiles that stream by are staged in both forms, by rows for
+// scores and dP, by columns for the sums over tokens.  P and dS are first operands of the products over tokens and go from
+// the warps back to tensor memory, over the scores and dP (dkv), or over the scores of which there are two (dq).  Eight
+// warps work, two for the same rows, 64 columns each.  The key heads' gradients are summed over their group's query heads in
+// the same accumulators.
+//
+// What bounds them at heads of 128 (bf16 4 x 4,096 tokens, 32 heads): dkv 2,750 clocks a tile of 128 queries where the MMAs
+// need 2,048: P takes 990 and dS 900, mostly powers, and reads of tensor memory whose port the MMAs share; 745 us, 1,475
+// TFLOP/s of its four products.  dq 1,800 clocks where 1,536 are needed; 533 us, 1,550 TFLOP/s of its three.  Together with the
+// rows 1,360 us in a stream of calls, 1,010 TFLOP/s of the formula's five products, 54 % of cuBLAS's burst.  A piece of work
+// adds 4,000 to 6,000 clocks, which tells on short sequences: 8,192 packed tokens of 1 to 2,047 395 us, 607 TFLOP/s.
+// One CTA with tiles of its own: 965 and 998 us.  Log sums and deltas taken off by the tensor cores, as products over three
+// parts of 8 or 11 bits: P 840 and dS 400 clocks, but the parts' way to the other CTA and the added products took
+// that back (1,360 us at best).
 #include "attention.cuh"
 
 namespace tb {
@@ -53,6 +73,7 @@ struct Args {
     int64_t stride[2][3];     // of batch, seq, head in elements
     int* err;
     unsigned long long wait_ns;
+    int withhold;             // self-test: a Withheld
 };
 
 // fp16 holds P times 2^14 and dS times the power of two that keeps it below 2^15 whatever the scores are:
@@ -92,7 +113,7 @@ __device__ __forceinline__ Bars bars_at(uint32_t at) {
     return b;
 }
 template <class L>
-__device__ __forceinline__ void init_bars(const Bars& b, int readers) {
+__device__ __forceinline__ void init_bars(const Bars& b, int readers, int withhold) {
     for (int i = 0; i < L::kStages; ++i) {
         mbar_init(b.full + 8 * i, 2);        // an arrival of either CTA, and their bytes
         mbar_init(b.free + 8 * i, 1);
@@ -100,14 +121,14 @@ __device__ __forceinline__ void init_bars(const Bars& b, int readers) {
     for (int i = 0; i < 2; ++i) {
         mbar_init(b.keep + 8 * i, 2);
         mbar_init(b.keep_free + 8 * i, 1);
-        mbar_init(b.first + 8 * i, 1);
+        mbar_init(b.first + 8 * i, 1 + (withhold == kScores));
         mbar_init(b.aux + 8 * i, 1);
         mbar_init(b.aux_free + 8 * i, 8);
     }
     mbar_init(b.second, 1);
-    mbar_init(b.first_taken, 16);            // the warps of both CTAs
-    mbar_init(b.second_taken, 16);
-    mbar_init(b.acc, 1);
+    mbar_init(b.first_taken, 16 + (withhold == kTaken));         // the warps of both CTAs
+    mbar_init(b.second_taken, 16 + (withhold == kTaken));
+    mbar_init(b.acc, 1 + (withhold == kResults));
     mbar_init(b.acc_free, 16);
     mbar_init(b.tail, 1);
     mbar_init(b.mended, 1);
@@ -261,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
     const Bars bar = bars_at<L>(smem0 + L::kBars);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
-    if (threadIdx.x == 0) init_bars<L>(bar, 2 * 10 + 1);         // loads, log sums, work; the MMAs
+    if (threadIdx.x == 0) init_bars<L>(bar, 2 * 10 + 1, p.withhold);     // loads, log sums, work; the MMAs
     if (warp == 3) tmem_alloc_all(bar.slot);
     tmem_fence_before();
     __syncthreads();
@@ -286,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
 
     if (warp == 0) {
         Loader<L, Blocks> load(p, bar, smem, smem0, rank, lane);
-        bool ok = true;
+        bool ok = p.withhold != kLoads0 + (int)rank;
         for (; more; move_on()) {
             if (!ok || !live) {
                 ask();
@@ -297,9 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
             for (int i = 0; i < it.steps && ok; ++i) {
                 const int row = it.tile(i) * kRows, head = it.query_head(i, p.group), rows = it.span.len - row;
                 const bool mend = rows < kRows;
-                if (mend && !load.expect_mended(2 * load.bytes(true) + 2 * load.bytes(false))) {
-                    ok = false;
-                    break;
+                if (mend) {                      // all of it, or nothing
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) ok = ok && load.room(s);
+                    ok = ok && load.expect_mended(2 * load.bytes(true) + 2 * load.bytes(false));
+                    if (!ok) break;
                 }
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
@@ -601,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
     const Bars bar = bars_at<L>(smem0 + L::kBars);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
-    if (threadIdx.x == 0) init_bars<L>(bar, 2 * 10 + 1);
+    if (threadIdx.x == 0) init_bars<L>(bar, 2 * 10 + 1, p.withhold);
     if (warp == 3) tmem_alloc_all(bar.slot);
     tmem_fence_before();
     __syncthreads();
@@ -628,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
 
     if (warp == 0) {
         Loader<L, Blocks> load(p, bar, smem, smem0, rank, lane);
-        bool ok = true;
+        bool ok = p.withhold != kLoads0 + (int)rank;
         for (; more; move_on()) {
             if (!ok || !live) {
                 ask();
@@ -640,9 +663,11 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
                 const int row = (it.steps - 1 - i) * kRows, rows = it.span.len - row;
                 // (scores of keys behind the end are hidden)
                 const bool mend = rows < kRows;
-                if (mend && !load.expect_mended(load.bytes(true) + load.bytes(false))) {
-                    ok = false;
-                    break;
+                if (mend) {                      // all of it, or nothing
+#pragma unroll
+                    for (int s = 0; s < 3; ++s) ok = ok && load.room(s);
+                    ok = ok && load.expect_mended(load.bytes(true) + load.bytes(false));
+                    if (!ok) break;
                 }
 #pragma unroll
                 for (int s = 0; s < 3; ++s) {
@@ -938,14 +963,35 @@ size_t workspace_bytes_for(int64_t batch, int64_t seq, int64_t heads) {
     return 256 + padded((size_t)(batch * heads * seq) * sizeof(float2));      // norms, aux
 }
 
-template <class Fmt, int Blocks>
-tb_status launch(Maps& m, Args p, const Rows& r, const tb_heads* const (&grads)[3], const View (&grad)[3], int64_t batch, int64_t seq,
-                 cudaStream_t st) {
+// The products of dK and dV, and of dQ.
+template <class Fmt, int Blocks, bool Kv, bool Dq>
+tb_status launch_products(Maps& m, Args p, const tb_heads* const (&grads)[3], const View (&grad)[3], int64_t batch, int64_t seq,
+                          int64_t slots, cudaStream_t st) {
     constexpr bool bf = std::is_same<Fmt, BF16>::value;
     constexpr int kv_bytes = LayoutKv<Blocks>::kBytes, q_bytes = LayoutQ<Blocks>::kBytes;
     if (resident_clusters(reinterpret_cast<const void*>(&dkv_kernel<Fmt, Blocks>), kThreads, kv_bytes, 2) < 1 ||
         resident_clusters(reinterpret_cast<const void*>(&dq_kernel<Fmt, Blocks>), kThreads, q_bytes, 2) < 1)
         return TB_ERR_CUDA;
+    auto gradient = [&](int i, int of, void** data, CUtensorMap* map) {
+        *data = const_cast<char*>(grad[of].p);
+        for (int k = 0; k < 3; ++k) p.stride[i][k] = grad[of].s[k];
+        return make_heads_map(map, *grads[of], batch, seq, p.dim, 32, bf, true);
+    };
+    if (!gradient(0, 1, &p.grad0, &m.out0) || !gradient(1, 2, &p.grad1, &m.out1)) return TB_ERR_CUDA;
+    if (Kv && launch_clusters<true>(dkv_kernel<Fmt, Blocks>, dim3((unsigned)(2 * slots * p.kv_heads)), dim3(kThreads), kv_bytes, st, 2, m, p) !=
+        cudaSuccess)
+        return TB_ERR_CUDA;
+    if (!gradient(0, 0, &p.grad0, &m.out0)) return TB_ERR_CUDA;
+    if (Dq && launch_clusters<true>(dq_kernel<Fmt, Blocks>, dim3((unsigned)(2 * slots * p.heads)), dim3(kThreads), q_bytes, st, 2, m, p) !=
+        cudaSuccess)
+        return TB_ERR_CUDA;
+    return launch_status();
+}
+
+template <class Fmt, int Blocks>
+tb_status launch(Maps& m, Args p, const Rows& r, const tb_heads* const (&grads)[3], const View (&grad)[3], int64_t batch, int64_t seq,
+                 cudaStream_t st) {
+    constexpr bool bf = std::is_same<Fmt, BF16>::value;
     int64_t ctas = (int64_t)r.chunks * batch * r.heads;
     if (!bf) {
         if (cudaMemsetAsync(r.norms, 0, 2 * sizeof(unsigned), st) != cudaSuccess) return TB_ERR_CUDA;
@@ -953,24 +999,70 @@ tb_status launch(Maps& m, Args p, const Rows& r, const tb_heads* const (&grads)[
     }
     if (launch_pdl(rows_kernel<Fmt>, dim3((unsigned)ctas), dim3(kRowThreads), 0, st, r) != cudaSuccess) return TB_ERR_CUDA;
     const int64_t slots = r.offsets ? slots_of(seq, r.sequences, kSpan) : p.tiles * batch;
-    auto gradient = [&](int i, int of, void** data, CUtensorMap* map) {
-        *data = const_cast<char*>(grad[of].p);
-        for (int k = 0; k < 3; ++k) p.stride[i][k] = grad[of].s[k];
-        return make_heads_map(map, *grads[of], batch, seq, p.dim, 32, bf, true);
-    };
-    if (!gradient(0, 1, &p.grad0, &m.out0) || !gradient(1, 2, &p.grad1, &m.out1)) return TB_ERR_CUDA;
-    if (launch_clusters<true>(dkv_kernel<Fmt, Blocks>, dim3((unsigned)(2 * slots * p.kv_heads)), dim3(kThreads), kv_bytes, st, 2, m, p) !=
-        cudaSuccess)
-        return TB_ERR_CUDA;
-    if (!gradient(0, 0, &p.grad0, &m.out0)) return TB_ERR_CUDA;
-    if (launch_clusters<true>(dq_kernel<Fmt, Blocks>, dim3((unsigned)(2 * slots * p.heads)), dim3(kThreads), q_bytes, st, 2, m, p) !=
-        cudaSuccess)
-        return TB_ERR_CUDA;
-    return launch_status();
+    return launch_products<Fmt, Blocks, true, true>(m, p, grads, grad, batch, seq, slots, st);
+}
+
+// The self-test's share of these kernels.
+template <int Blocks>
+tb_status withheld(int64_t wait_limit_ns, int* err, unsigned char* mem, cudaStream_t st, int* launches) {
+    const int64_t dim = 64 * Blocks;
+    tb_heads h[7];                       // q, k, v, dout; dq, dk, dv
+    for (int i = 0; i < 7; ++i) h[i] = self_heads(&mem, i == 0 || i == 3 || i == 4 ? kSelfHeads : 1, dim);
+    Maps m{};
+    CUtensorMap* const whole[4] = {&m.q, &m.k, &m.v, &m.dout};
+    CUtensorMap* const by_rows[4] = {&m.q_rows, &m.k_rows, &m.v_rows, &m.dout_rows};
+    for (int i = 0; i < 4; ++i)
+        if (!make_heads_map(whole[i], h[i], 1, kSelfTokens, dim, kRows, true) || !make_heads_map(by_rows[i], h[i], 1, kSelfTokens, dim, kRows / 2, true))
+            return TB_ERR_CUDA;
+    const tb_heads* const grads[3] = {&h[4], &h[5], &h[6]};
+    View grad[3];
+    for (int i = 0; i < 3; ++i) grad[i] = view_of(grads[i], 1, kSelfTokens);
+    Args p{};
+    p.tokens = Tokens{nullptr, 0, 1, (int)kSelfTokens, err};
+    p.heads = p.group = (int)kSelfHeads, p.kv_heads = 1, p.dim = (int)dim;
+    p.tiles = (int)ceil_div(kSelfTokens, kSpan);
+    p.scale = p.scale_log2 = 1.f;
+    p.aux = reinterpret_cast<const float2*>(mem);
+    p.err = err, p.wait_ns = (unsigned long long)wait_limit_ns;
+    tb_status s = run_withheld(err, st, launches, [&](int what) {
+        p.withhold = what;
+        return launch_products<BF16, Blocks, true, false>(m, p, grads, grad, 1, kSelfTokens, p.tiles, st);
+    });
+    if (s == TB_OK)
+        s = run_withheld(err, st, launches, [&](int what) {
+            p.withhold = what;
+            return launch_products<BF16, Blocks, false, true>(m, p, grads, grad, 1, kSelfTokens, p.tiles, st);
+        });
+    return s;
 }
 
 }  // namespace
+
+tb_status attention_withheld(int64_t wait_limit_ns, int* err, unsigned char* mem, cudaStream_t st, int* launches);   // attention.cu
+
 }  // namespace tb
+
+extern "C" tb_status tb_attention_selftest_timeout(int64_t wait_limit_ns, int* launches, void* stream) {
+    using namespace tb;
+    if (!launches || wait_limit_ns < 1000 || wait_limit_ns > (int64_t)kWaitLimitNs) return TB_ERR_INVALID_VALUE;
+    *launches = 0;
+    int* err = device_error_word();
+    if (!err) return TB_ERR_CUDA;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    void* data = nullptr;
+    if (cudaMalloc(&data, kSelfBytes) != cudaSuccess) {
+        cudaGetLastError();
+        return TB_ERR_OOM;
+    }
+    unsigned char* mem = static_cast<unsigned char*>(data);
+    tb_status s = cudaMemsetAsync(data, 0, kSelfBytes, st) == cudaSuccess ? TB_OK : TB_ERR_CUDA;
+    if (s == TB_OK) s = attention_withheld(wait_limit_ns, err, mem, st, launches);
+    if (s == TB_OK) s = withheld<1>(wait_limit_ns, err, mem, st, launches);
+    if (s == TB_OK) s = withheld<2>(wait_limit_ns, err, mem, st, launches);
+    if (cudaStreamSynchronize(st) != cudaSuccess) s = TB_ERR_CUDA;
+    if (cudaFree(data) != cudaSuccess) s = TB_ERR_CUDA;
+    return s;
+}
 
 extern "C" tb_status tb_attention_bwd_workspace_size(int64_t batch, int64_t seq, int64_t heads_q, int64_t heads_k, int64_t head_dim,
                                                      tb_dtype dtype, size_t* bytes) {

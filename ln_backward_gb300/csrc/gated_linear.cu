@@ -3,7 +3,22 @@
 //     G = X Wg^T,  U = X Wu^T,  H = act(G) * U
 //     dG = dH * U * act'(G),  dU = dH * act(G),  dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X
 //
-// X [N, D] hidden states, Wg and Wu [F, D] weights, 16-bit.
+// X [N, D] hidden states, Wg and Wu [F, D] weights, 16-bit.  Products are 256 x 256 tiles on pairs of CTAs, a ring of six
+// 32 KB stages in each and two accumulators in tensor memory, as the output layer's (linear_xent.cu).
+//
+// Forward: a tile is 256 rows by 128 columns of G and the same 128 of U; one CTA stages Wg's rows, the other Wu's, so that
+// both products of an element meet in one accumulator and H needs no pass of its own.  Few rows read both weights once:
+// the columns of a tile are chosen so that the tiles fill the pairs, and where even narrow tiles are fewer, the contraction
+// is split into fp32 sums that a second kernel joins (pick_up).
+// Gradient: gate_kernel forms dG and dU, 16-bit, side by side in the workspace; one launch has the tiles of dX, which
+// contracts over both weights, and of dWg and dWu, which contract over the rows, and deals them out so that the pairs end
+// together (deal).  fp16's dG and dU are held times a power of two that a pass before finds.
+//
+// What bounds it: the tensor cores under the power limit.  bf16 8,192 x 4,096 x 11,008: forward with G and U kept 750 to
+// 870 us by board and load (1,700 to 1,970 TFLOP/s, 91 to 105 % of cuBLAS's burst), gradient 1,750 to 1,970 us, of which
+// 135 are gate_kernel's 901 MB at 6.7 TB/s and the products run at 1,960 TFLOP/s in a single launch.  16 rows against the same
+// weights: 35 us, 5.1 TB/s; 138 tiles of 80 columns on 76 pairs leave 10 % of them idle, and filling the rings about 4 us.
+// fp16 1,021 x 768 x 2,048: forward 12 us, gradient 30 us (four launches).
 #include "tensor_core.cuh"
 
 namespace tb {
@@ -11,6 +26,9 @@ namespace {
 
 // kUp: both projections and the activation.  kBack: the products of the gradient.
 enum Kind { kUp = 0, kBack = 1 };
+// What the self-test leaves out, so that waits run out: the boxes of the pair's first or second CTA, the word that an
+// accumulator is full, the last word that it is empty again.
+enum Withheld { kNothing = 0, kBoxes0 = 1, kBoxes1 = 2, kFull = 3, kEmpty = 4 };
 
 constexpr int kThreadsOf(int epi) { return (kEpiWarp + epi) * 32; }
 constexpr int kSmem = kStages * kStageBytes + kOutboxes * kOutBytes + 1024 + 256;   // alignment, barriers
@@ -37,6 +55,7 @@ struct Args {
     void *H, *G, *U;          // kUp; G and U may be NULL
     int* err;
     unsigned long long wait_ns;
+    int withhold;             // self-test: a Withheld
 };
 // kUp: X, Wg, Wu; H, G, U or the sums.  kBack: dG by rows, Wg, Wu, dG and X by columns; dX, dWg, dWu or sums.
 struct Maps {
@@ -232,8 +251,8 @@ gated_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) 
             mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(acc_full + 8 * i, 1);
-            mbar_init(acc_empty + 8 * i, 2 * Epi);    // of both CTAs
+            mbar_init(acc_full + 8 * i, 1 + (p.withhold == kFull));
+            mbar_init(acc_empty + 8 * i, 2 * Epi + (p.withhold == kEmpty));    // of both CTAs
         }
         mbar_init(drain, 1);
         mbar_init(done, 1);
@@ -260,6 +279,7 @@ gated_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) 
         const uint32_t leader_full = map_to(full, 0);
         int it = 0;
         Feed<K> feed(p, maps, (int)rank, pair, pairs);
+        if (p.withhold == kBoxes0 + (int)rank) feed.live = false;
         for (; feed.live; feed.next(), ++it) {
             const int s = it % kStages;
             if (it >= kStages && !__all_sync(0xffffffffu, mbar_wait(empty + 8 * s, (it / kStages - 1) & 1, &p)))
@@ -775,10 +795,10 @@ struct Problem {
 };
 
 template <class Fmt, int K, int Act, int Epi = 8>
-tb_status launch_product(const Maps& m, Args p, int64_t tiles, cudaStream_t st) {
-    p.wait_ns = kWaitLimitNs;
+tb_status launch_product(const Maps& m, Args p, int64_t tiles, cudaStream_t st, int most_pairs = 1 << 20) {
+    if (!p.wait_ns) p.wait_ns = kWaitLimitNs;
     const void* kernel = reinterpret_cast<const void*>(&gated_kernel<Fmt, K, Epi, Act>);
-    const int pairs = resident_clusters(kernel, kThreadsOf(Epi), kSmem, 2);
+    const int pairs = std::min(most_pairs, resident_clusters(kernel, kThreadsOf(Epi), kSmem, 2));
     if (pairs < 1) return TB_ERR_CUDA;
     const int64_t grid = std::min<int64_t>(tiles, pairs);
     if (K == kBack) {
@@ -941,8 +961,75 @@ tb_status check_workspace(const Buffers& b, const void* workspace, size_t have, 
     return TB_OK;
 }
 
+// One pair over 256 x 256 of X and 768 x 256 of both weights: more stages than the ring has, over six tiles.
+tb_status run_withheld(int64_t wait_limit_ns, int* err, unsigned char* mem, cudaStream_t st, int* launches) {
+    constexpr int64_t n = 256, d = 256, f = 768;
+    auto take = [&](int64_t bytes) {
+        unsigned char* at = mem;
+        mem += bytes;
+        return at;
+    };
+    const void *X = take(n * d * 2), *Wg = take(f * d * 2), *Wu = take(f * d * 2), *H = take(n * f * 2), *dg = take(n * 2 * f * 2),
+               *dX = take(n * d * 2), *dWg = take(f * d * 2), *dWu = take(f * d * 2);
+    for (int k = kUp; k <= kBack; ++k)
+        for (int what = kBoxes0; what <= kEmpty; ++what) {
+            Maps m{};
+            Args p{};
+            p.rows = (int)n, p.hidden = (int)d, p.inner = (int)f, p.a_rows = kHalf, p.out_map = 1;
+            p.err = err, p.wait_ns = (unsigned long long)wait_limit_ns, p.withhold = what;
+            int word = 0;
+            if (cudaMemcpyAsync(err, &word, sizeof(int), cudaMemcpyHostToDevice, st) != cudaSuccess) return TB_ERR_CUDA;
+            tb_status s;
+            if (k == kUp) {
+                p.half = kHalf;
+                p.H = const_cast<void*>(H);
+                p.part[0] = Tiles{1, (int)(f / kHalf), 1, (int)(d / kStageK), (int)(f / kHalf)};
+                if (!make_map(&m.in[0], X, n, d, d, kHalf, true) || !make_map(&m.in[1], Wg, f, d, d, kHalf, true) ||
+                    !make_map(&m.in[2], Wu, f, d, d, kHalf, true) || !make_map(&m.out[0], H, n, f, f, 32, true, true))
+                    return TB_ERR_CUDA;
+                s = launch_product<BF16, kUp, TB_ACT_SILU>(m, p, p.part[0].count, st, 1);
+            } else {
+                p.half = (int)f;
+                p.part[0] = Tiles{1, 1, 1, (int)(2 * f / kStageK), 1};
+                p.part[1] = Tiles{(int)(2 * f / kTile), 1, 1, (int)(n / kStageK), (int)(2 * f / kTile)};
+                if (!make_map(&m.in[0], dg, n, 2 * f, 2 * f, kHalf, true) || !make_map(&m.in[1], Wg, f, d, d, kStageK, true) ||
+                    !make_map(&m.in[2], Wu, f, d, d, kStageK, true) || !make_map(&m.in[3], dg, n, 2 * f, 2 * f, kStageK, true) ||
+                    !make_map(&m.in[4], X, n, d, d, kStageK, true) || !make_map(&m.out[0], dX, n, d, d, 32, true, true) ||
+                    !make_map(&m.out[1], dWg, f, d, d, 32, true, true) || !make_map(&m.out[2], dWu, f, d, d, 32, true, true))
+                    return TB_ERR_CUDA;
+                s = launch_product<BF16, kBack, 0>(m, p, p.part[0].count + p.part[1].count, st, 1);
+            }
+            if (s != TB_OK) return s;
+            if (cudaMemcpyAsync(&word, err, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+                cudaStreamSynchronize(st) != cudaSuccess)
+                return TB_ERR_CUDA;
+            *launches += word == (int)TB_ERR_TIMEOUT;
+        }
+    return TB_OK;
+}
+
 }  // namespace
 }  // namespace tb
+
+extern "C" tb_status tb_gated_linear_selftest_timeout(int64_t wait_limit_ns, int* launches, void* stream) {
+    using namespace tb;
+    if (!launches || wait_limit_ns < 1000 || wait_limit_ns > (int64_t)kWaitLimitNs) return TB_ERR_INVALID_VALUE;
+    *launches = 0;
+    int* err = device_error_word();
+    if (!err) return TB_ERR_CUDA;
+    constexpr size_t kBytes = 4 << 20;       // 2.9 MB are needed
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    void* mem = nullptr;
+    if (cudaMalloc(&mem, kBytes) != cudaSuccess) {
+        cudaGetLastError();
+        return TB_ERR_OOM;
+    }
+    tb_status s = cudaMemsetAsync(mem, 0, kBytes, st) == cudaSuccess ? TB_OK : TB_ERR_CUDA;
+    if (s == TB_OK) s = run_withheld(wait_limit_ns, err, static_cast<unsigned char*>(mem), st, launches);
+    if (cudaStreamSynchronize(st) != cudaSuccess) s = TB_ERR_CUDA;
+    if (cudaFree(mem) != cudaSuccess) s = TB_ERR_CUDA;
+    return s;
+}
 
 extern "C" tb_status tb_gated_linear_workspace_size(int64_t rows, int64_t D, int64_t F, tb_dtype dtype, size_t* bytes) {
     return tb::workspace(rows, D, F, dtype, false, bytes);
