@@ -523,7 +523,7 @@ extern "C" tb_status tb_attention(const tb_heads* q, const tb_heads* k, const tb
     if (overlap(sums, starts) || overlap(starts, range_of_view(view[3], head_dim))) return TB_ERR_ALIAS;
     if (offsets && sequences == 0) return TB_OK;
     const int64_t tiles = ceil_div(seq, kItem), slots = offsets ? slots_of(seq, sequences, kItem) : tiles * batch;
-    if (slots > (1ll << 30) / q->heads) return TB_ERR_INVALID_VALUE;
+    if (slots > ((1ll << 30) - 1) / q->heads) return TB_ERR_INVALID_VALUE;
     const bool bf = dtype == TB_BF16;
     CUtensorMap m[4];
     for (int i = 0; i < 4; ++i)

@@ -352,7 +352,8 @@ constexpr int kSorted = 128;
 template <bool Sorted>
 __device__ __forceinline__ bool find_tile(const Tokens& t, int size, int slot, bool from_last, Span* s) {
     const int lane = threadIdx.x & 31;
-    auto offset = [&](int i) { return (int)min(max(t.offsets[i], (int64_t)0), (int64_t)t.seq); };
+    // (from L2: dq_kernel starts before the kernel in front of it has ended)
+    auto offset = [&](int i) { return (int)min(max((int64_t)__ldcg((const long long*)t.offsets + i), (int64_t)0), (int64_t)t.seq); };
     auto tiles_of = [&](int i) { return (max(offset(i + 1) - offset(i), 0) + size - 1) / size; };
     int seq, far;                        // the sequence, and how far from the end the tile lies
     if (Sorted && t.sequences <= kSorted) {
@@ -400,7 +401,7 @@ __device__ __forceinline__ bool find_tile(const Tokens& t, int size, int slot, b
         if (k < 0 || k >= tiles) return false;
         far = tiles - 1 - k;
     }
-    const int64_t a = t.offsets[seq], b = t.offsets[seq + 1];
+    const int64_t a = __ldcg((const long long*)t.offsets + seq), b = __ldcg((const long long*)t.offsets + seq + 1);
     if ((a < 0 || b < a || b > t.seq) && lane == 0) atomicExch(t.err, (int)TB_ERR_INVALID_VALUE);
     const int first = offset(seq), len = max(offset(seq + 1) - first, 0);
     *s = Span{0, first, len, from_last ? (len + size - 1) / size - 1 - far : far};

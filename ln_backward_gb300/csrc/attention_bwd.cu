@@ -1119,7 +1119,7 @@ extern "C" tb_status tb_attention_bwd(const tb_heads* dout, const tb_heads* q, c
     if (overlap(ws, sums) || overlap(ws, starts)) return TB_ERR_ALIAS;
     if (offsets && sequences == 0) return TB_OK;
     const int64_t tiles = ceil_div(seq, kSpan), slots = offsets ? slots_of(seq, sequences, kSpan) : tiles * batch;
-    if (slots > (1ll << 30) / q->heads || ceil_div(seq, kRowsCta) * batch > (1ll << 30) / q->heads) return TB_ERR_INVALID_VALUE;
+    if (slots > ((1ll << 30) - 1) / q->heads || ceil_div(seq, kRowsCta) * batch > (1ll << 30) / q->heads) return TB_ERR_INVALID_VALUE;
     const bool bf = dtype == TB_BF16;
     Maps m{};
     CUtensorMap* const whole[4] = {&m.q, &m.k, &m.v, &m.dout};

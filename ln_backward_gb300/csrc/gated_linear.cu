@@ -679,7 +679,7 @@ void pick_up(int64_t n, int64_t d, int64_t f, int64_t pairs, Cut* c) {
         if (!whole && n >= kHalf) continue;
         const int64_t tiles = m_tiles * ceil_div(f, half);
         const double stage = std::max(0.4, half / 128.0);
-        for (int64_t s = fewest; s <= std::min<int64_t>(std::max(fewest, stages), 64); ++s) {
+        for (int64_t s = fewest; s <= std::max(fewest, std::min<int64_t>(stages, 64)); ++s) {
             if (s > 1 && (!whole || (s > fewest && tiles * s > 2 * pairs))) break;
             const double cost = (double)ceil_div(tiles * s, pairs) * ((double)ceil_div(stages, s) * stage + 8.0) +
                                 (s > 1 ? 12.0 + (double)s * (0.05 + (double)(n * f) / 100000.0) : 0.0);

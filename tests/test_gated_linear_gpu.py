@@ -122,6 +122,15 @@ def test_forward(tb, n, d, f, dtype):
     assert tb.tb_device_error() == 0
 
 
+def test_a_very_long_contraction(tb):
+    """More elements than 64 accumulators take: as many parts as it needs."""
+    n, d, f = 2, 65 * 65536, 8
+    X, Wg, Wu, _ = inputs(n, d, f, torch.bfloat16, seed=3)
+    H, G, U = forward(tb, X, Wg, Wu, "silu")
+    check_forward(X, Wg, Wu, "silu", H, G, U)
+    assert tb.tb_device_error() == 0
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("n, d, f", SIZES + [(5000, 64, 136), (40000, 16, 24)])
 def test_backward(tb, n, d, f, dtype):
