@@ -297,8 +297,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     continue;
                 }
                 clear_behind(smem + L::kStage0 + s * L::kStageBytes, 1, kRows, rows, lane);
+                cleared(lane);
                 if (lane == 0) {
-                    mbar_arrive_release(map_to(full + 8 * s, 0));
+                    mbar_arrive_cluster(map_to(full + 8 * s, 0));
                     mbar_arrive(mended);
                 }
             }

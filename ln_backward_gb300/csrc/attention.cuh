@@ -221,8 +221,13 @@ __device__ __forceinline__ void clear_behind(unsigned char* tile, int boxes, int
     for (int b = 0; b < boxes; ++b)
         for (int x = max(rows, 0) * 8 + lane; x < box_rows * 8; x += 32)
             *reinterpret_cast<uint4*>(tile + (b * box_rows * 8 + x) * 16) = make_uint4(0, 0, 0, 0);
+}
+// Behind it, before the arrivals: what the warp wrote is there for the MMAs of either CTA.  (One release for all
+// arrivals, each of which would wait about 900 clocks for its own.)
+__device__ __forceinline__ void cleared(int lane) {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
+    if (lane == 0) asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- work

@@ -212,15 +212,20 @@ struct Mender {
     uint32_t rank;
     int lane, tails;
     __device__ __forceinline__ bool wait() { return __all_sync(0xffffffffu, mbar_wait(bar.tail, tails++ & 1, &p)); }
-    // Tile n of stream s.
-    __device__ __forceinline__ void mend(int s, int n, bool by_rows, int rows) const {
-        const int place = L::first(s) + n % L::ring(s);
-        clear_behind(smem + L::kStage0 + place * L::kStageBytes, by_rows ? Blocks : 1, by_rows ? kRows / 2 : kRows,
-                     by_rows ? rows - (int)rank * (kRows / 2) : rows, lane);
-        if (lane == 0) mbar_arrive_release(map_to(bar.full + 8 * place, 0));
-    }
-    __device__ __forceinline__ void done() const {
-        if (lane == 0) mbar_arrive(bar.mended);
+    // Tile n of the streams from `first` on, those below 2 by rows.
+    __device__ __forceinline__ void mend(int first, int n, int rows) const {
+#pragma unroll
+        for (int s = 0; s < L::kStreams; ++s)
+            if (s >= first)
+                clear_behind(smem + L::kStage0 + (L::first(s) + n % L::ring(s)) * L::kStageBytes, s < 2 ? Blocks : 1, s < 2 ? kRows / 2 : kRows,
+                             s < 2 ? rows - (int)rank * (kRows / 2) : rows, lane);
+        cleared(lane);
+        if (lane == 0) {
+#pragma unroll
+            for (int s = 0; s < L::kStreams; ++s)
+                if (s >= first) mbar_arrive_cluster(map_to(bar.full + 8 * (L::first(s) + n % L::ring(s)), 0));
+            mbar_arrive(bar.mended);
+        }
         __syncwarp();
     }
 };
@@ -416,20 +421,18 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
             for (int i = 0; i < it.steps; ++i, ++n) {
                 float2 x[4];
                 const int row0 = it.tile(i) * kRows;
+                if (it.span.len - row0 < kRows) {        // (before the loads, which its release would wait for)
+                    if (!ends.wait()) {
+                        ok = false;
+                        break;
+                    }
+                    ends.mend(0, n, it.span.len - row0);
+                }
                 const float2* aux = p.aux + ((int64_t)it.span.batch * p.heads + it.query_head(i, p.group)) * p.tokens.seq + it.span.first;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int row = row0 + 32 * k + lane;
                     x[k] = row < it.span.len ? aux[row] : make_float2(__int_as_float(0x7f800000), 0.f);
-                }
-                if (it.span.len - row0 < kRows) {
-                    if (!ends.wait()) {
-                        ok = false;
-                        break;
-                    }
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) ends.mend(s, n, s < 2, it.span.len - row0);
-                    ends.done();
                 }
                 // the log sums are read with the scores, the deltas with dP: each is free for the next tile behind that
                 if (n && !__all_sync(0xffffffffu, mbar_wait(bar.aux_free, (n - 1) & 1, &p))) {
@@ -756,9 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
                     ask();
                     continue;
                 }
-                ends.mend(kVRows, n, true, rows);
-                ends.mend(kKSum, n, false, rows);
-                ends.done();
+                ends.mend(kVRows, n, rows);
             }
             n += it.steps;
             ask();
