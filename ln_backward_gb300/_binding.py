@@ -788,67 +788,94 @@ def tb_linear_xent_bwd(dloss: torch.Tensor, H: torch.Tensor, W: torch.Tensor, ta
 
 
 # ----------------------------------------------------------------------------- attention
+_I64 = torch.int64
+
+
 class _AttentionCall:
     """The tb_heads of a call's tensors, packed as in _HeadsCall: the first has the query heads, and so
-    have those numbered in ``like_q``; the others have the key heads."""
+    have those numbered in ``like_q``; the others have the key heads. What is right takes one test a tensor
+    here; _complain says what is wrong."""
 
-    __slots__ = ("words", "p", "batch", "seq", "dim", "code", "device", "heads_q", "heads_k", "offsets",
-                 "sequences", "scale")
+    __slots__ = ("words", "p", "batch", "seq", "dim", "code", "device", "heads_q", "offsets", "sequences",
+                 "scale")
 
     def __init__(self, names, tensors, like_q, offsets: Optional[torch.Tensor], scale: Optional[float]):
         q = tensors[0]
-        shape = q.shape
-        if len(shape) != 4:
-            raise ValueError(f"{names[0]} must be [batch, seq, heads, head_dim], got {tuple(shape)}")
-        batch, seq, self.heads_q, dim = shape
-        dtype, device = q.dtype, q.get_device()
-        heads_k, words = None, []
-        for i, t in enumerate(tensors):
-            shape = t.shape
-            b, s, h, d = shape if len(shape) == 4 else (-1, -1, -1, -1)
-            if b != batch or s != seq or d != dim:
-                raise ValueError(f"{names[i]} must be [batch, seq, heads, head_dim] with the batch, "
-                                 f"seq and head_dim of {names[0]}, got {tuple(shape)}")
-            if i in like_q:
-                if h != self.heads_q:
-                    raise ValueError(f"{names[i]} must have {self.heads_q} heads, got {h}")
-            elif heads_k is None:
-                heads_k = h
-            elif h != heads_k:
-                raise ValueError(f"{names[i]} must have {heads_k} heads, got {h}")
-            if t.dtype != dtype:
-                raise ValueError(f"{names[i]} must be {dtype} like {names[0]}, got {t.dtype}")
-            sb, ss, sh, sd = t.stride()
-            if sd != 1 and dim > 1:
-                raise ValueError(f"the last dimension of {names[i]} must be contiguous")
-            if t.get_device() != device:
-                raise ValueError(f"{names[i]} is on {t.device}, {names[0]} on {q.device}")
-            words += (t.data_ptr(), sb, ss, sh, h)
+        device, dtype = q.get_device(), q.dtype
+        try:
+            batch, seq, heads_q, dim = q.shape
+            heads_k, words = -1, []
+            for i, t in enumerate(tensors):
+                b, s, h, d = t.shape
+                sb, ss, sh, sd = t.stride()
+                if i in like_q:
+                    right = h == heads_q
+                else:
+                    if heads_k < 0:
+                        heads_k = h
+                    right = h == heads_k
+                if not right or b != batch or s != seq or d != dim or sd != 1 and dim > 1 \
+                        or t.dtype != dtype or t.get_device() != device:
+                    self._complain(names, tensors, like_q)
+                words += (t.data_ptr(), sb, ss, sh, h)
+        except ValueError:                    # not four dimensions
+            self._complain(names, tensors, like_q)
+            raise
         if device < 0:
             raise ValueError("tensors passed to libtb must be CUDA tensors")
         if device != _current_device():
             raise ValueError(f"tensor on cuda:{device}, but the current device is "
                              f"cuda:{_current_device()}")
-        self.offsets, self.sequences = None, 0
-        if offsets is not None:
-            if offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.numel() < 1:
+        if offsets is None:
+            self.offsets, self.sequences = None, 0
+        else:
+            self.sequences = offsets.numel() - 1
+            if offsets.dtype != _I64 or offsets.dim() != 1 or self.sequences < 0:
                 raise ValueError("offsets must hold an int64 for the start of each sequence and one for the last's end")
             if offsets.get_device() != device:
                 raise ValueError(f"offsets are on {offsets.device}, {names[0]} on cuda:{device}")
-            self.offsets, self.sequences = _ptr(offsets), offsets.numel() - 1
-        self.words = array("q", words)
-        at = self.words.buffer_info()[0]
-        self.p = [at + i * _HEADS_BYTES for i in range(len(tensors))]
-        self.batch, self.seq, self.dim, self.device, self.heads_k = batch, seq, dim, device, heads_k
-        self.scale = dim ** -0.5 if scale is None else float(scale)
+            if not offsets.is_contiguous():
+                raise ValueError("tensors passed to libtb must be contiguous")
+            self.offsets = offsets.data_ptr()
+        self.words = words = array("q", words)
+        at = words.buffer_info()[0]
+        self.p = range(at, at + len(tensors) * _HEADS_BYTES, _HEADS_BYTES)
+        self.batch, self.seq, self.dim, self.device, self.heads_q = batch, seq, dim, device, heads_q
+        self.scale = dim ** -0.5 if scale is None else scale
         self.code = _DTYPE.get(dtype)
         if self.code is None:
             raise TbError("dtype", 2)
 
+    @staticmethod
+    def _complain(names, tensors, like_q):
+        q = tensors[0]
+        if q.dim() != 4:
+            raise ValueError(f"{names[0]} must be [batch, seq, heads, head_dim], got {tuple(q.shape)}")
+        batch, seq, heads_q, dim = q.shape
+        heads_k = None
+        for i, t in enumerate(tensors):
+            if t.dim() != 4 or t.shape[:2] != q.shape[:2] or t.shape[3] != dim:
+                raise ValueError(f"{names[i]} must be [batch, seq, heads, head_dim] with the batch, "
+                                 f"seq and head_dim of {names[0]}, got {tuple(t.shape)}")
+            if i not in like_q and heads_k is None:
+                heads_k = t.shape[2]
+            want = heads_q if i in like_q else heads_k
+            if t.shape[2] != want:
+                raise ValueError(f"{names[i]} must have {want} heads, got {t.shape[2]}")
+            if t.dtype != q.dtype:
+                raise ValueError(f"{names[i]} must be {q.dtype} like {names[0]}, got {t.dtype}")
+            if t.stride(3) != 1 and dim > 1:
+                raise ValueError(f"the last dimension of {names[i]} must be contiguous")
+            if t.get_device() != q.get_device():
+                raise ValueError(f"{names[i]} is on {t.device}, {names[0]} on {q.device}")
+
     def sums(self, t: torch.Tensor, name: str) -> Optional[int]:
         """Address of a contiguous fp32 [batch, heads_q, seq]."""
-        _want(t, self.batch * self.heads_q * self.seq, _F32, name)
-        return _ptr(t)
+        if t.numel() != self.batch * self.heads_q * self.seq or t.dtype != _F32:
+            _want(t, self.batch * self.heads_q * self.seq, _F32, name)
+        if t.get_device() != self.device or not t.is_contiguous():
+            return _ptr(t)
+        return t.data_ptr() or None
 
     def stream(self, stream) -> Optional[int]:
         return _raw_stream(self.device) if stream is None and _raw_stream else _stream(stream)
@@ -897,16 +924,35 @@ def tb_attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
 ACTIVATION = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 
-def _gated_sizes(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, activation: str):
+def _gated_call(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, activation: str, others):
+    """(rows, D, F, activation's and dtype's numbers, device, addresses of X, Wg, Wu and of ``others``). Others are
+    (tensor or None, its size, its name); sizes are products of rows N, D and F."""
     if X.dim() != 2 or Wg.dim() != 2 or Wg.shape != Wu.shape or X.shape[1] != Wg.shape[1]:
         raise ValueError("X must be [rows, D], Wg and Wu [F, D], got "
                          f"{tuple(X.shape)}, {tuple(Wg.shape)} and {tuple(Wu.shape)}")
-    if not X.dtype == Wg.dtype == Wu.dtype:
+    dtype = X.dtype
+    if not dtype == Wg.dtype == Wu.dtype:
         raise ValueError("X, Wg and Wu must share a dtype")
-    if activation not in ACTIVATION:
+    act = ACTIVATION.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATION)}")
     rows, D = X.shape
-    return rows, D, Wg.shape[0], ACTIVATION[activation]
+    F = Wg.shape[0]
+    sizes = {"NF": rows * F, "ND": rows * D, "FD": F * D}
+    tensors = [X, Wg, Wu]
+    for t, size, name in others:
+        if t is not None and (t.numel() != sizes[size] or t.dtype != dtype):
+            _want(t, sizes[size], dtype, name)
+        tensors.append(t)
+    device = X.get_device()
+    here = device >= 0 and device == _current_device()
+    p = [None if t is None else t.data_ptr() or None if here and t.get_device() == device and t.is_contiguous() else _ptr(t)
+         for t in tensors]
+    return rows, D, F, act, _dtype(X), device, p
+
+
+def _scratch(workspace: Optional[torch.Tensor]):
+    return (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
 
 
 def tb_gated_linear_workspace_size(rows: int, D: int, F: int, dtype: torch.dtype) -> int:
@@ -926,14 +972,11 @@ def tb_gated_linear(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, H: torc
                     stream=None) -> None:
     """H = act(X Wg^T) * (X Wu^T) in one pass. G and U receive the two products for
     tb_gated_linear_bwd; leave them out when serving."""
-    rows, D, F, act = _gated_sizes(X, Wg, Wu, activation)
-    for t, name in ((H, "H"), (G, "G"), (U, "U")):
-        if t is not None:
-            _want(t, rows * F, X.dtype, name)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    rows, D, F, act, code, device, p = _gated_call(X, Wg, Wu, activation,
+                                                   ((H, "NF", "H"), (G, "NF", "G"), (U, "NF", "U")))
     _check("tb_gated_linear",
-           lib.tb_gated_linear(_ptr(X), _ptr(Wg), _ptr(Wu), _ptr(H), _ptr(G), _ptr(U), rows, D, F,
-                               act, _dtype(X), _ptr(workspace), ws_bytes, _stream(stream)))
+           lib.tb_gated_linear(*p, rows, D, F, act, code, *_scratch(workspace),
+                               _raw_stream(device) if stream is None and _raw_stream else _stream(stream)))
 
 
 def tb_gated_linear_bwd(dH: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor,
@@ -943,13 +986,9 @@ def tb_gated_linear_bwd(dH: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu:
                         stream=None) -> None:
     """Gradients of tb_gated_linear: dX, dWg and dWu (overwritten; None: not wanted) from dH and
     what the forward kept."""
-    rows, D, F, act = _gated_sizes(X, Wg, Wu, activation)
-    for t, n, name in ((dH, rows * F, "dH"), (G, rows * F, "G"), (U, rows * F, "U"),
-                       (dX, rows * D, "dX"), (dWg, F * D, "dWg"), (dWu, F * D, "dWu")):
-        if t is not None:
-            _want(t, n, X.dtype, name)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    rows, D, F, act, code, device, p = _gated_call(
+        X, Wg, Wu, activation, ((dH, "NF", "dH"), (G, "NF", "G"), (U, "NF", "U"), (dX, "ND", "dX"), (dWg, "FD", "dWg"),
+                                (dWu, "FD", "dWu")))
     _check("tb_gated_linear_bwd",
-           lib.tb_gated_linear_bwd(_ptr(dH), _ptr(X), _ptr(Wg), _ptr(Wu), _ptr(G), _ptr(U), _ptr(dX),
-                                   _ptr(dWg), _ptr(dWu), rows, D, F, act, _dtype(X), _ptr(workspace),
-                                   ws_bytes, _stream(stream)))
+           lib.tb_gated_linear_bwd(p[3], *p[:3], *p[4:], rows, D, F, act, code, *_scratch(workspace),
+                                   _raw_stream(device) if stream is None and _raw_stream else _stream(stream)))
