@@ -70,6 +70,8 @@ struct Args {
     const float2* aux;        // [batch][heads][seq]: lse * log2(e), dout . out
     const unsigned* norms;    // fp16: the largest norms of a dout and of a v, as bits
     void *grad0, *grad1;      // dQ; or dK and dV
+    int parts;                // dkv: pieces of work that share a key head's query heads
+    float* sums;              // [parts][batch][seq][kv_heads][2][dim]: dK's and dV's where there are several
     int64_t stride[2][3];     // of batch, seq, head in elements
     int* err;
     unsigned long long wait_ns;
@@ -255,14 +257,17 @@ struct Maps {
 // query head of the group.  Transposed: keys are rows, so that P^T and dS^T are first operands as they come.
 struct Keys {
     Span span;
-    int head;
+    int head, part;
     int first, each, steps;   // query tiles: the first, of a head, of all heads
+    int query0;               // the first query head
     __device__ __forceinline__ int tile(int i) const { return first + i % each; }
-    __device__ __forceinline__ int query_head(int i, int group) const { return head * group + i / each; }
+    __device__ __forceinline__ int query_head(int i) const { return query0 + i / each; }
 };
 __device__ __forceinline__ bool find_keys(const Args& p, unsigned index, Keys* k) {
-    k->head = (int)(index % (unsigned)p.kv_heads);
-    const unsigned slot = index / (unsigned)p.kv_heads;
+    const unsigned heads = (unsigned)(p.kv_heads * p.parts), slot = index / heads, which = index - slot * heads;
+    k->head = (int)(which / (unsigned)p.parts);
+    k->part = (int)(which - (unsigned)(k->head * p.parts));
+    k->query0 = k->head * p.group + k->part * (p.group / p.parts);
     if (p.tokens.offsets) {
         if (!find_tile<true>(p.tokens, kSpan, (int)slot, true, &k->span)) return false;
     } else {                  // the longest first
@@ -271,8 +276,28 @@ __device__ __forceinline__ bool find_keys(const Args& p, unsigned index, Keys* k
     }
     k->first = 2 * k->span.tile;
     k->each = (k->span.len + kRows - 1) / kRows - k->first;
-    k->steps = k->each * p.group;
+    k->steps = k->each * (p.group / p.parts);
     return true;
+}
+
+// 32 rows of sums, a row a lane, to memory.
+__device__ __forceinline__ void store_sums(float* out, uint32_t tmem, bool live, int dim, int lane, uint32_t free) {
+#pragma unroll 1
+    for (int x = 0; x < dim; x += 32) {
+        uint32_t o[32];
+        tmem_load32(tmem + x, o);
+        tmem_wait(o);
+        if (x + 32 >= dim) {
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(free);
+        }
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (x + 4 * i < dim) *reinterpret_cast<uint4*>(out + x + 4 * i) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+    }
 }
 
 template <class Fmt, int Blocks>
@@ -321,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
             const int token = it.span.first + it.span.tile * kSpan + (int)rank * kRows, batch = it.span.batch;
             ok = load.keep(0, &m.k, token, it.head, batch) && load.keep(1, &m.v, token, it.head, batch);
             for (int i = 0; i < it.steps && ok; ++i) {
-                const int row = it.tile(i) * kRows, head = it.query_head(i, p.group), rows = it.span.len - row;
+                const int row = it.tile(i) * kRows, head = it.query_head(i), rows = it.span.len - row;
                 const bool mend = rows < kRows;
                 if (mend) {                      // all of it, or nothing
 #pragma unroll
@@ -428,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
                     }
                     ends.mend(0, n, it.span.len - row0);
                 }
-                const float2* aux = p.aux + ((int64_t)it.span.batch * p.heads + it.query_head(i, p.group)) * p.tokens.seq + it.span.first;
+                const float2* aux = p.aux + ((int64_t)it.span.batch * p.heads + it.query_head(i)) * p.tokens.seq + it.span.first;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int row = row0 + 32 * k + lane;
@@ -574,7 +599,11 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
             }
             tmem_fence_after();
             const int in_seq = it.span.tile * kSpan + (int)rank * kRows + quad * 32, rows = min(32, it.span.len - in_seq);
-            if (rows > 0) {
+            if (rows > 0 && p.sums) {
+                const int64_t token = ((int64_t)it.part * p.tokens.batch + it.span.batch) * p.tokens.seq + it.span.first + in_seq + lane;
+                store_sums(p.sums + ((token * p.kv_heads + it.head) * 2 + !half) * p.dim, (half ? dk : dv) + lanes, lane < rows, p.dim, lane,
+                           acc_free);
+            } else if (rows > 0) {
                 const int token = it.span.first + in_seq, g = !half;     // dV, dK
                 const Place to{half ? &m.out0 : &m.out1,
                                static_cast<T*>(half ? p.grad0 : p.grad1) + it.span.batch * p.stride[g][0] + token * p.stride[g][1] + it.head * p.stride[g][2],
@@ -958,10 +987,56 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     }
 }
 
+// dK and dV from the sums of several pieces, in their order; eight elements a thread.
+struct Join {
+    const float* sums;
+    void* out[2];             // dK, dV
+    int64_t stride[2][3];
+    const unsigned* norms;
+    const int64_t* offsets;
+    int sequences, parts, batch, seq, heads, dim;
+    float scale;
+};
+template <class Fmt>
+__global__ void __launch_bounds__(kRowThreads) join_kernel(const __grid_constant__ Join p) {
+    pdl_wait();
+    pdl_trigger();
+    const unsigned each = (unsigned)p.dim / 8;
+    const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x, row = i / (2 * each);       // of [batch][seq][heads]
+    const unsigned at = (unsigned)(i - row * (2 * each)), which = at >= each, c = (at - which * each) * 8;
+    const int64_t token = row / p.heads, rows = (int64_t)p.batch * p.seq * p.heads;
+    const int head = (int)(row - token * p.heads), batch = (int)(token / p.seq), s = (int)(token - (int64_t)batch * p.seq);
+    if (row >= rows || (p.offsets && (s < p.offsets[0] || s >= p.offsets[p.sequences]))) return;
+    float v[8] = {};
+    for (int k = 0; k < p.parts; ++k) {
+        const float4* x = reinterpret_cast<const float4*>(p.sums + ((k * rows + row) * 2 + which) * p.dim + c);
+        const float4 a = __ldcs(x), b = __ldcs(x + 1);
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+    }
+    const float f = which ? power_of_two(-kPShift<Fmt>) : p.scale * power_of_two(-ds_shift<Fmt>(p.norms));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= f;
+    typename Fmt::T* out = static_cast<typename Fmt::T*>(p.out[which]) + batch * p.stride[which][0] + s * p.stride[which][1] + head * p.stride[which][2] + c;
+    *reinterpret_cast<uint4*>(out) = pack8<Fmt>(v);
+}
+
 // ---------------------------------------------------------------- host
+// Pieces that the query heads of a key head are dealt to, where the tiles of keys are too few for the machine and have
+// enough to do that the sums pay.  bf16, heads of 128, in one piece and as this says: 2,048 tokens of 8 heads over one
+// 204 and 54 us, 8,192 767 and 341, 4,096 of 32 over four 404 and 358; 600 tokens of 8 heads of 64 over one 77 and 28.
+constexpr int kSms = 152;                    // of a GB300: the cut, and the workspace, do not ask the device
+int parts_for(int64_t batch, int64_t seq, int64_t heads, int64_t kv_heads) {
+    const int64_t pieces = ceil_div(seq, kSpan) * batch * kv_heads, group = heads / kv_heads;
+    if (ceil_div(seq, kRows) * group < 16) return 1;
+    int64_t parts = 1;
+    while (parts < group && (pieces * parts < kSms || group % parts)) ++parts;   // two for each pair of SMs
+    return (int)parts;
+}
 size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
-size_t workspace_bytes_for(int64_t batch, int64_t seq, int64_t heads) {
-    return 256 + padded((size_t)(batch * heads * seq) * sizeof(float2));      // norms, aux
+size_t aux_bytes(int64_t batch, int64_t seq, int64_t heads) { return padded((size_t)(batch * heads * seq) * sizeof(float2)); }
+size_t workspace_bytes_for(int64_t batch, int64_t seq, int64_t heads, int64_t kv_heads, int64_t dim, int parts) {
+    return 256 + aux_bytes(batch, seq, heads) +      // norms, aux, sums
+           (parts > 1 ? (size_t)parts * batch * seq * kv_heads * 2 * dim * sizeof(float) : 0);
 }
 
 // The products of dK and dV, and of dQ.
@@ -979,7 +1054,7 @@ tb_status launch_products(Maps& m, Args p, const tb_heads* const (&grads)[3], co
         return make_heads_map(map, *grads[of], batch, seq, p.dim, 32, bf, true);
     };
     if (!gradient(0, 1, &p.grad0, &m.out0) || !gradient(1, 2, &p.grad1, &m.out1)) return TB_ERR_CUDA;
-    if (Kv && launch_clusters<true>(dkv_kernel<Fmt, Blocks>, dim3((unsigned)(2 * slots * p.kv_heads)), dim3(kThreads), kv_bytes, st, 2, m, p) !=
+    if (Kv && launch_clusters<true>(dkv_kernel<Fmt, Blocks>, dim3((unsigned)(2 * slots * p.kv_heads * p.parts)), dim3(kThreads), kv_bytes, st, 2, m, p) !=
         cudaSuccess)
         return TB_ERR_CUDA;
     if (!gradient(0, 0, &p.grad0, &m.out0)) return TB_ERR_CUDA;
@@ -1000,7 +1075,20 @@ tb_status launch(Maps& m, Args p, const Rows& r, const tb_heads* const (&grads)[
     }
     if (launch_pdl(rows_kernel<Fmt>, dim3((unsigned)ctas), dim3(kRowThreads), 0, st, r) != cudaSuccess) return TB_ERR_CUDA;
     const int64_t slots = r.offsets ? slots_of(seq, r.sequences, kSpan) : p.tiles * batch;
-    return launch_products<Fmt, Blocks, true, true>(m, p, grads, grad, batch, seq, slots, st);
+    const tb_status s = launch_products<Fmt, Blocks, true, true>(m, p, grads, grad, batch, seq, slots, st);
+    if (s != TB_OK || p.parts == 1) return s;
+    Join j{};
+    j.sums = p.sums, j.norms = p.norms, j.offsets = r.offsets, j.sequences = r.sequences;
+    j.parts = p.parts, j.batch = (int)batch, j.seq = (int)seq, j.heads = p.kv_heads, j.dim = p.dim, j.scale = p.scale;
+    for (int i = 0; i < 2; ++i) {
+        j.out[i] = const_cast<char*>(grad[1 + i].p);
+        for (int k = 0; k < 3; ++k) j.stride[i][k] = grad[1 + i].s[k];
+    }
+    // (behind dq_kernel, which ends behind dkv_kernel)
+    return launch_pdl(join_kernel<Fmt>, dim3((unsigned)ceil_div(batch * seq * p.kv_heads * 2 * (p.dim / 8), kRowThreads)), dim3(kRowThreads), 0, st,
+                      j) == cudaSuccess
+               ? launch_status()
+               : TB_ERR_CUDA;
 }
 
 // The self-test's share of these kernels.
@@ -1020,7 +1108,7 @@ tb_status withheld(int64_t wait_limit_ns, int* err, unsigned char* mem, cudaStre
     for (int i = 0; i < 3; ++i) grad[i] = view_of(grads[i], 1, kSelfTokens);
     Args p{};
     p.tokens = Tokens{nullptr, 0, 1, (int)kSelfTokens, err};
-    p.heads = p.group = (int)kSelfHeads, p.kv_heads = 1, p.dim = (int)dim;
+    p.heads = p.group = (int)kSelfHeads, p.kv_heads = p.parts = 1, p.dim = (int)dim;
     p.tiles = (int)ceil_div(kSelfTokens, kSpan);
     p.scale = p.scale_log2 = 1.f;
     p.aux = reinterpret_cast<const float2*>(mem);
@@ -1074,7 +1162,7 @@ extern "C" tb_status tb_attention_bwd_workspace_size(int64_t batch, int64_t seq,
     *bytes = 0;
     if (batch == 0 || seq == 0 || heads_q == 0) return TB_OK;
     if (heads_k == 0 || heads_q % heads_k) return TB_ERR_INVALID_VALUE;
-    *bytes = workspace_bytes_for(batch, seq, heads_q);
+    *bytes = workspace_bytes_for(batch, seq, heads_q, heads_k, head_dim, parts_for(batch, seq, heads_q, heads_k));
     return TB_OK;
 }
 
@@ -1100,7 +1188,6 @@ extern "C" tb_status tb_attention_bwd(const tb_heads* dout, const tb_heads* q, c
     if (k->heads == 0 || q->heads % k->heads || !lse) return TB_ERR_INVALID_VALUE;
     if (!aligned_to(lse, 4)) return TB_ERR_MISALIGNED;
     const int64_t rows = batch * seq * q->heads;
-    const size_t need = workspace_bytes_for(batch, seq, q->heads);
     const Range sums = range_of(lse, rows, 4), starts = range_of(offsets, offsets ? sequences + 1 : 0, 8);
     for (int i = 0; i < 3; ++i) {
         for (int j = 0; j < 5; ++j)
@@ -1110,6 +1197,8 @@ extern "C" tb_status tb_attention_bwd(const tb_heads* dout, const tb_heads* q, c
         const Range g = range_of_view(grad[i], head_dim);
         if (overlap(g, sums) || overlap(g, starts)) return TB_ERR_ALIAS;
     }
+    const int parts = parts_for(batch, seq, q->heads, k->heads);
+    const size_t need = workspace_bytes_for(batch, seq, q->heads, k->heads, head_dim, parts);
     if (!workspace || workspace_bytes < need) return TB_ERR_WORKSPACE;
     if (!aligned_to(workspace, 16)) return TB_ERR_MISALIGNED;
     const Range ws = range_of(workspace, (int64_t)need, 1);
@@ -1138,6 +1227,8 @@ extern "C" tb_status tb_attention_bwd(const tb_heads* dout, const tb_heads* q, c
     p.scale = scale, p.scale_log2 = scale * kLog2e;
     p.norms = reinterpret_cast<unsigned*>(mem);
     p.aux = reinterpret_cast<float2*>(mem + 256);
+    p.parts = parts;
+    if (parts > 1) p.sums = reinterpret_cast<float*>(mem + 256 + aux_bytes(batch, seq, q->heads));
     p.wait_ns = kWaitLimitNs;
     Rows r{};
     const int of[3] = {3, 4, 2};

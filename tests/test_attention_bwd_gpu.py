@@ -67,6 +67,19 @@ def test_groups(tb, hq, hk):
     check(tb, problem(tb, 1, 400, hq, hk, 64, BF, seed=hq))
 
 
+@pytest.mark.parametrize("layout", ["joint", "bhsd"])
+@pytest.mark.parametrize("b, s, hq, hk, d, dtype", [(1, 600, 8, 1, 128, BF), (2, 300, 12, 1, 64, HALF), (1, 2100, 8, 2, 72, BF),
+                                                    (1, 1030, 30, 3, 64, HALF), (3, 257, 16, 2, 128, HALF), (1, 129, 64, 1, 24, BF)])
+def test_query_heads_in_several_pieces(tb, b, s, hq, hk, d, dtype, layout):
+    """Few tiles of keys, many query heads: several pairs of CTAs share a key head, and their sums are joined."""
+    check(tb, problem(tb, b, s, hq, hk, d, dtype, layout, seed=s), layout=layout)
+
+
+@pytest.mark.parametrize("offsets", [[0, 130, 300], [7, 8, 8, 640], [0, 1000]])
+def test_packed_in_several_pieces(tb, offsets):
+    check(tb, problem(tb, 1, 1000, 8, 1, 64, BF, seed=5, offsets=offsets), offsets)
+
+
 @pytest.mark.parametrize("dtype", [BF, HALF])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("name", PACKED)
