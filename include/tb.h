@@ -749,8 +749,8 @@ tb_status tb_linear_xent_bwd(const float* dloss, const void* H, const void* W,
  *   batch, seq       >= 0, batch <= 2^20, seq <= 2^25
  *   head_dim         a multiple of 8, 8 .. 128
  *   offsets          device int64 [sequences + 1], 8-byte aligned; NULL: every batch entry is a
- *                    sequence (sequences is 0 then).  With offsets batch is 1.
- *   scale            > 0; 1 / sqrt(head_dim) is usual
+ *                    sequence (sequences is 0 then).  With offsets batch is 1 and sequences <= 2^24.
+ *   scale            > 0, <= 2^127; 1 / sqrt(head_dim) is usual
  *   dtype            TB_BF16 or TB_F16
  * Data starts on 16 bytes and strides are multiples of 8 elements, not 0 (except of a size of 1)
  * and below 2^39.
@@ -774,7 +774,9 @@ tb_status tb_attention(const tb_heads* q, const tb_heads* k, const tb_heads* v, 
  *   dq, dk, dv       out: as q, k and v, overwritten; they share no element with an input or with
  *                    each other (views of one joint buffer are told apart)
  *   workspace        device scratch of tb_attention_bwd_workspace_size() bytes, 16-byte aligned,
- *                    contents ignored.  Calls that may run at the same time need workspaces of
+ *                    contents ignored: 8 bytes a row of out, and, where tiles of keys are too few
+ *                    for the machine, fp32 sums of dk and dv from several pieces of the query
+ *                    heads that share a key head.  Calls that may run at the same time need workspaces of
  *                    their own, and so do graphs that may.
  * Other arguments, sequences, alignment and errors as tb_attention, plus TB_ERR_WORKSPACE; q and dout
  * are finite within a sequence as k and v are.  Sums are fp32; P and dS are rounded to dtype on their way

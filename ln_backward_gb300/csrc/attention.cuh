@@ -461,7 +461,7 @@ inline tb_status check_call(int64_t batch, int64_t seq, int64_t dim, const int64
                             tb_dtype dtype) {
     if (batch < 0 || seq < 0 || batch > (1 << 20) || seq > kMaxTokens) return TB_ERR_INVALID_VALUE;
     if (dim < 8 || dim % 8 || dim > kMaxHeadDim) return TB_ERR_INVALID_VALUE;
-    if (!(scale > 0.f && scale <= 3.4028235e38f)) return TB_ERR_INVALID_VALUE;
+    if (!(scale > 0.f && scale <= 0x1p127f)) return TB_ERR_INVALID_VALUE;   // times log2(e) is finite too
     if (offsets ? batch != 1 || sequences < 0 || sequences > (1 << 24) : sequences != 0) return TB_ERR_INVALID_VALUE;
     if (!aligned_to(offsets, 8)) return TB_ERR_MISALIGNED;
     if (dtype != TB_BF16 && dtype != TB_F16) return TB_ERR_UNSUPPORTED_DTYPE;

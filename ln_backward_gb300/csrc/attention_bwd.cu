@@ -1025,6 +1025,8 @@ __global__ void __launch_bounds__(kRowThreads) join_kernel(const __grid_constant
 // enough to do that the sums pay.  bf16, heads of 128, in one piece and as this says: 2,048 tokens of 8 heads over one
 // 204 and 54 us, 8,192 767 and 341, 4,096 of 32 over four 404 and 358; 600 tokens of 8 heads of 64 over one 77 and 28.
 constexpr int kSms = 152;                    // of a GB300: the cut, and the workspace, do not ask the device
+// Grids, and with them the bytes of a workspace, stay within their types.
+bool fits(int64_t batch, int64_t seq, int64_t heads) { return ceil_div(seq, kRowsCta) * batch <= (1ll << 30) / heads; }
 int parts_for(int64_t batch, int64_t seq, int64_t heads, int64_t kv_heads) {
     const int64_t pieces = ceil_div(seq, kSpan) * batch * kv_heads, group = heads / kv_heads;
     if (ceil_div(seq, kRows) * group < 16) return 1;
@@ -1161,7 +1163,7 @@ extern "C" tb_status tb_attention_bwd_workspace_size(int64_t batch, int64_t seq,
     if (s != TB_OK) return s;
     *bytes = 0;
     if (batch == 0 || seq == 0 || heads_q == 0) return TB_OK;
-    if (heads_k == 0 || heads_q % heads_k) return TB_ERR_INVALID_VALUE;
+    if (heads_k == 0 || heads_q % heads_k || !fits(batch, seq, heads_q)) return TB_ERR_INVALID_VALUE;
     *bytes = workspace_bytes_for(batch, seq, heads_q, heads_k, head_dim, parts_for(batch, seq, heads_q, heads_k));
     return TB_OK;
 }
@@ -1184,8 +1186,8 @@ extern "C" tb_status tb_attention_bwd(const tb_heads* dout, const tb_heads* q, c
         if (t->heads != q->heads) return TB_ERR_INVALID_VALUE;
     for (const tb_heads* t : {v, dk, dv})
         if (t->heads != k->heads) return TB_ERR_INVALID_VALUE;
-    if (batch == 0 || seq == 0 || q->heads == 0) return TB_OK;
-    if (k->heads == 0 || q->heads % k->heads || !lse) return TB_ERR_INVALID_VALUE;
+    if (batch == 0 || seq == 0 || (q->heads == 0 && k->heads == 0)) return TB_OK;
+    if (q->heads == 0 || k->heads == 0 || q->heads % k->heads || !lse) return TB_ERR_INVALID_VALUE;
     if (!aligned_to(lse, 4)) return TB_ERR_MISALIGNED;
     const int64_t rows = batch * seq * q->heads;
     const Range sums = range_of(lse, rows, 4), starts = range_of(offsets, offsets ? sequences + 1 : 0, 8);
@@ -1209,7 +1211,7 @@ extern "C" tb_status tb_attention_bwd(const tb_heads* dout, const tb_heads* q, c
     if (overlap(ws, sums) || overlap(ws, starts)) return TB_ERR_ALIAS;
     if (offsets && sequences == 0) return TB_OK;
     const int64_t tiles = ceil_div(seq, kSpan), slots = offsets ? slots_of(seq, sequences, kSpan) : tiles * batch;
-    if (slots > ((1ll << 30) - 1) / q->heads || ceil_div(seq, kRowsCta) * batch > (1ll << 30) / q->heads) return TB_ERR_INVALID_VALUE;
+    if (slots > ((1ll << 30) - 1) / q->heads || !fits(batch, seq, q->heads)) return TB_ERR_INVALID_VALUE;
     const bool bf = dtype == TB_BF16;
     Maps m{};
     CUtensorMap* const whole[4] = {&m.q, &m.k, &m.v, &m.dout};

@@ -127,3 +127,23 @@ def test_binding_refuses(tb):
                       ((q.transpose(2, 3).contiguous().transpose(2, 3), k, k, o), "contiguous")):
         with pytest.raises(ValueError, match=what):
             tb.tb_attention(*bad)
+
+
+def test_no_query_head_leaves_no_gradient_of_keys(tb):
+    """dk and dv would be sums over nothing: heads of keys without one that asks them are refused, no head at all is not."""
+    none = dict(heads=0)
+    query = dict(q=none, dout=none, out=none, dq=none)
+    assert bwd(tb, **query) == INVALID
+    assert bwd(tb, **query, k=none, v=none, dk=none, dv=none, ws=None) == OK
+
+
+def test_scale_that_leaves_the_range_in_powers_of_two(tb):
+    assert fwd(tb, scale=3e38) == INVALID and bwd(tb, scale=3e38) == INVALID
+    assert fwd(tb, scale=2.0 ** 127, batch=0) == OK
+
+
+def test_workspace_of_a_call_beyond_every_grid(tb):
+    size = ctypes.c_size_t(7)
+    call = tb._binding.lib.tb_attention_bwd_workspace_size
+    assert call(2 ** 20, 2 ** 25, 2 ** 20, 2 ** 20, 128, BF16, ctypes.byref(size)) == INVALID
+    assert call(1, 2 ** 25, 64, 8, 128, BF16, ctypes.byref(size)) == OK and size.value >= 8 * 64 * 2 ** 25
