@@ -755,7 +755,10 @@ tb_status tb_linear_xent_bwd(const float* dloss, const void* H, const void* W,
  * Data starts on 16 bytes and strides are multiples of 8 elements, not 0 (except of a size of 1)
  * and below 2^39.
  * Sums are fp32.  P = exp(s - m), m the maximum of keys before or one that is at most ln 8192 below it, is
- * rounded to dtype on its way into the second product; the sum below it is not.  Results are bitwise reproducible.
+ * rounded to dtype on its way into the second product; the sum below it is not.  (TB_F16: below 2^-14 P has fewer
+ * bits, each key's is off by 2^-25 at most.)  Scores may be of any size: fp32 holds them, m is taken off before the
+ * power, and keys whose scores lie far below the others' or overflow to -inf take no part.  lse is m rounded to fp32, and
+ * with the logarithm of the sum rounded once more.  Results are bitwise reproducible.
  * Errors: TB_ERR_INVALID_VALUE, TB_ERR_UNSUPPORTED_DTYPE (TB_F32 has no such tensor-core product),
  * TB_ERR_MISALIGNED, TB_ERR_ALIAS, TB_ERR_CUDA.
  */

@@ -31,6 +31,12 @@ constexpr int kSoftmaxWarp = 4;              // first of eight: four for each ti
 constexpr int kThreads = (kSoftmaxWarp + 8) * 32;
 // A block's sum of P, above which a row's maximum is looked for again: far from fp16's end.
 constexpr float kMost = 8192.f;
+// P is taken in one FMA from a score, 2^(s c - b), b = m c rounded to fp32 for a row's maximum m.  That rounding is a factor
+// of all of the row's P, which its sum takes out again: at most 2^(2^-5) below kFar, but from |b| = 2^28 on (keys masked
+// by -1e10, say) it leaves P's range.  Beyond kFar m is taken off the scores first, exact for scores next to it, in a pass of
+// its own that only warps with such a row make, behind the one for all: a branch within that one took 299 instead of 273 us
+// for fp16 16,384 tokens, 8 heads of 64 (269 without either).
+constexpr float kFar = 0x1p20f;
 
 template <int Blocks>                        // of 64 columns of a head
 struct Layout {
@@ -48,7 +54,7 @@ struct Args {
     Tokens tokens;
     int heads, group, dim;    // query heads, of which `group` share a key head
     int tiles;                // of kItem queries of a batch entry, without offsets
-    float scale_log2;         // scale * log2(e)
+    float scale, scale_log2;  // and times log2(e)
     void* out;
     int64_t out_batch, out_seq, out_head;    // strides in elements
     float* lse;               // [batch][heads][seq]; NULL: not wanted
@@ -324,8 +330,17 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             }
             const int in_seq = it.span.tile * kItem + t * kSpan + (int)rank * kRows;     // the tile's first query
             const int rows = min(32, it.span.len - in_seq - quad * 32);                  // of this warp, none: 0 or less
-            float base = 0.f;                // P is 2^(score * scale_log2 - base)
+            // P is 2^((score - m) * scale_log2), m = `top`, a maximum of the row's scores.  (lowest: none yet, or all were;
+            // m is 0 and P too.)
+            float top = lowest;
             unsigned long long total = 0;
+            auto anchor = [&] { return top == lowest ? 0.f : top; };
+            auto beyond = [&] { return !(fabsf(anchor() * p.scale_log2) < kFar); };
+            // the power of two that P has too much by the rounding of m * scale_log2
+            auto rest = [&] {
+                const float m = anchor(), b = __fmul_rn(m, p.scale_log2);
+                return beyond() ? 0.f : __fmaf_rn(m, p.scale_log2, -b);
+            };
             for (int i = 0; i < it.blocks(t); ++i, ++have) {
                 if (!__all_sync(0xffffffffu, mbar_wait(s_full + 8 * t, have & 1, &p))) {
                     ok = false;
@@ -344,10 +359,18 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 #pragma unroll
                         for (int e = 0; e < 32; ++e) x[e] = at + e > row ? 0xff800000u : x[e];
                     };
-                    auto all_powers = [&](bool hides) {              // P of the block, and its sum
+                    // P of the block, and its sum; Any: of rows that may lie far from zero
+                    auto all_powers = [&](auto any, bool hides) {
+                        constexpr bool kAny = decltype(any)::value;
                         sums[0] = sums[1] = 0;
-                        const unsigned long long b2 = pair_of(-base, -base);
-                        auto powers = [&](const uint32_t (&x)[32], int g) {
+                        const float m = anchor(), less = kAny && beyond() ? m : 0.f, b = kAny && beyond() ? 0.f : __fmul_rn(m, -p.scale_log2);
+                        const unsigned long long b2 = pair_of(b, b);
+                        auto powers = [&](uint32_t (&x)[32], int g) {
+                            if (hides) hide(x, 32 * g);
+                            if constexpr (kAny) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - less);
+                            }
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 float lo, hi;
@@ -362,18 +385,14 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         tmem_load32(mine, x);
                         tmem_wait(x);
                         tmem_load32(mine + 32, y);
-                        if (hides) hide(x, 0);
                         powers(x, 0);
                         tmem_wait(y);
                         tmem_load32(mine + 64, x);
-                        if (hides) hide(y, 32);
                         powers(y, 1);
                         tmem_wait(x);
                         tmem_load32(mine + 96, y);
-                        if (hides) hide(x, 64);
                         powers(x, 2);
                         tmem_wait(y);
-                        if (hides) hide(y, 96);
                         powers(y, 3);
                     };
                     auto highest = [&](bool hides) {                 // (by the whole warp)
@@ -390,22 +409,28 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         }
                         return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     };
-                    if (ahead == 0) {        // the block of the tile's own tokens: up to here there is nothing to rescale
-                        const float m = highest(true);
-                        base = m == lowest ? 0.f : m * p.scale_log2;
-                        all_powers(true);
+                    // The block of the tile's own tokens first: up to there nothing is to be rescaled.  Then P against what it
+                    // was taken against before; where a row's sum shows that it grew beyond kMost, everything is taken
+                    // against the new maximum.  (One row's growth leaves the others as they are.)  So it is where a row has no
+                    // maximum yet, and in every block of rows far from zero: a log sum is a multiple of large steps
+                    // there, and less than a score would make the gradient's P more than 1.
+                    bool again;
+                    if (ahead == 0) {
+                        top = highest(true);
+                        all_powers(std::false_type{}, true);
+                        again = beyond();
                     } else {
-                        // P against what it was taken against before; where a row's sum shows that it grew beyond
-                        // kMost, everything is taken against the new maximum.  (One row's growth leaves the others
-                        // as they are.)
-                        all_powers(false);
+                        all_powers(std::false_type{}, false);
                         float lo, hi;
                         split_pair(add_pair(sums[0], sums[1]), lo, hi);
-                        const bool grew = !(lo + hi <= kMost);
-                        if (__any_sync(0xffffffffu, grew)) {
-                            const float most = highest(false) * p.scale_log2, next = grew ? fmaxf(base, most) : base,
-                                        f = exp2_fast(base - next);
-                            base = next;
+                        again = !(lo + hi <= kMost) || top == lowest || beyond();
+                    }
+                    if (__any_sync(0xffffffffu, again)) {
+                        if (ahead) {
+                            const float before = anchor(), before_rest = rest(), most = highest(false);
+                            const bool first = top == lowest;
+                            if (again) top = fmaxf(top, most);
+                            const float f = first ? 0.f : exp2_fast(__fmaf_rn(before - anchor(), p.scale_log2, rest() - before_rest));
                             total = mul_pair(total, pair_of(f, f));
                             for (int x = 0; x < cols; x += 16) {
                                 uint32_t o[16];
@@ -414,8 +439,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                                 for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                                 tmem_store16(sum + x, o);
                             }
-                            all_powers(false);
                         }
+                        all_powers(std::true_type{}, ahead == 0);
                     }
                     total = add_pair(total, add_pair(sums[0], sums[1]));
                 }
@@ -437,9 +462,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             split_pair(total, l0, l1);
             const float l = l0 + l1;
             const int token = it.span.first + in_seq + quad * 32;
+            // (the gradient rounds a score to fp32 and takes its row's log sum off: rounded alike here, a row of one large
+            // key has the very score, whatever its size)
             if (p.lse && lane < rows)
                 p.lse[((int64_t)it.span.batch * p.heads + it.head) * p.tokens.seq + token + lane] =
-                    0.693147180559945309f * (base + log2f(l));
+                    __fmaf_rn(0.693147180559945309f, log2f(l) - rest(), __fmul_rn(anchor(), p.scale));
             if (rows > 0) {
                 const Place to{&map_out, static_cast<T*>(p.out) + it.span.batch * p.out_batch + token * p.out_seq + it.head * p.out_head,
                                p.out_seq, token, it.head, it.span.batch};
@@ -483,7 +510,7 @@ tb_status withheld(int64_t wait_limit_ns, int* err, unsigned char* mem, cudaStre
     p.tokens = Tokens{nullptr, 0, 1, (int)kSelfTokens, err};
     p.heads = p.group = (int)kSelfHeads, p.dim = (int)dim;
     p.tiles = (int)ceil_div(kSelfTokens, kItem);
-    p.scale_log2 = 1.f;
+    p.scale = p.scale_log2 = 1.f;
     p.out = h[3].data, p.out_batch = h[3].stride_batch, p.out_seq = h[3].stride_seq, p.out_head = h[3].stride_head;
     p.err = err, p.wait_ns = (unsigned long long)wait_limit_ns;
     return run_withheld(err, st, launches, [&](int what) {
@@ -534,7 +561,7 @@ extern "C" tb_status tb_attention(const tb_heads* q, const tb_heads* k, const tb
     p.tokens = Tokens{offsets, (int)sequences, (int)batch, (int)seq, p.err};
     p.heads = (int)q->heads, p.group = (int)(q->heads / k->heads), p.dim = (int)head_dim;
     p.tiles = (int)tiles;
-    p.scale_log2 = scale * kLog2e;
+    p.scale = scale, p.scale_log2 = scale * kLog2e;
     p.out = out->data;
     p.out_batch = view[3].s[0], p.out_seq = view[3].s[1], p.out_head = view[3].s[2];
     p.lse = lse;
