@@ -784,7 +784,8 @@ tb_status tb_attention(const tb_heads* q, const tb_heads* k, const tb_heads* v, 
  * Other arguments, sequences, alignment and errors as tb_attention, plus TB_ERR_WORKSPACE; q and dout
  * are finite within a sequence as k and v are.  Sums are fp32; P and dS are rounded to dtype on their way
  * into the last three products.  TB_F16 holds P times 2^14, and dS times a power of two by the largest
- * norms of a row of dout and of v, so that small gradients keep their bits.  Every sum is taken in a
+ * norms of a row of dout and of v, so that small gradients keep their bits.  Where |lse| is above 1,024
+ * a score is rounded to fp32 and lse taken off before the power.  Every sum is taken in a
  * fixed order: results are bitwise reproducible.
  */
 tb_status tb_attention_bwd_workspace_size(int64_t batch, int64_t seq, int64_t heads_q,

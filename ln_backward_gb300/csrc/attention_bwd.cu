@@ -69,7 +69,7 @@ struct Args {
     int heads, kv_heads, group, dim;
     int tiles;                // of 256 tokens of a batch entry, without offsets
     float scale, scale_log2;
-    const float2* aux;        // [batch][heads][seq]: lse * log2(e), dout . out
+    const float2* aux;        // [batch][heads][seq]: lse, dout . out
     const unsigned* norms;    // fp16: the largest norms of a dout and of a v, as bits
     void *grad0, *grad1;      // dQ; or dK and dV
     int parts;                // dkv: pieces of work that share a key head's query heads
@@ -93,10 +93,36 @@ __device__ __forceinline__ int ds_shift(const unsigned* norms) {
 }
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }
 
+// P is one FMA and a power of a score, 2^(s c - lse log2(e)): off by the rounding of either product, 2^-24 of |s| and of |lse|,
+// which is 2^-13 of P at kFarSum, a fourth of fp16's own rounding.  Beyond it the score is rounded to fp32 first, as the
+// forward's log sums have it, and the log sum taken off: exact next to each other, so that a row's one large key has P = 1
+// whatever its size.  (Without that P was off by 14 % at 1e6 and by a factor of 8 at 1e7.)
+constexpr float kFarSum = 1024.f;
+__device__ __forceinline__ bool far_sum(float lse) { return !(fabsf(lse) <= kFarSum); }
+// That is done to 64 columns of scores where they lie, before P is taken; column c's log sum is that of aux[step * c], and
+// from column `left` on 0.  (Done to the registers on P's way, the branch alone cost 2.6 % of the gradient of 8,192 packed
+// tokens.)
+__device__ __noinline__ void take_off_sums(uint32_t tmem, float scale, const float2* aux, int step, int left) {
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        uint32_t x[32];
+        tmem_load32(tmem + 32 * half, x);
+        tmem_wait(x);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const int c = 32 * half + e;
+            const float sum = c < left ? __ldcg(&aux[step * c]).x : 0.f;
+            x[e] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(x[e]), scale), -sum));
+        }
+        tmem_store32(tmem + 32 * half, x);
+    }
+    tmem_stored();
+}
+
 // Barriers of either kernel.
 struct Bars {
     uint32_t answer, keep, keep_free, full, free, first, second, first_taken, second_taken, aux, aux_free, acc, acc_free, tail, mended, drain,
-        done, work_full, work_empty, words, slot;
+        done, work_full, work_empty, words, slot, far;
 };
 template <class L>
 __device__ __forceinline__ Bars bars_at(uint32_t at) {
@@ -112,8 +138,8 @@ __device__ __forceinline__ Bars bars_at(uint32_t at) {
     b.first = take(2), b.second = take(1), b.first_taken = take(1), b.second_taken = take(1);
     b.aux = take(2), b.aux_free = take(2), b.acc = take(1), b.acc_free = take(1);
     b.tail = take(1), b.mended = take(1), b.drain = take(1), b.done = take(1), b.work_full = take(1), b.work_empty = take(1);
-    b.words = take(3), b.slot = at;
-    static_assert((2 + 4 + 2 * L::kStages + 5 + 6 + 6 + 3) * 8 + 4 <= 512 && L::kStreams + 2 <= 6);
+    b.words = take(3), b.slot = at, b.far = at + 4;
+    static_assert((2 + 4 + 2 * L::kStages + 5 + 6 + 6 + 3) * 8 + 8 <= 512 && L::kStreams + 2 <= 6);
     return b;
 }
 template <class L>
@@ -459,15 +485,20 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int row = row0 + 32 * k + lane;
-                    x[k] = row < it.span.len ? aux[row] : make_float2(__int_as_float(0x7f800000), 0.f);
+                    x[k] = row < it.span.len ? aux[row] : make_float2(0.f, 0.f);
                 }
+                const bool far = __any_sync(0xffffffffu, far_sum(x[0].x) || far_sum(x[1].x) || far_sum(x[2].x) || far_sum(x[3].x));
                 // the log sums are read with the scores, the deltas with dP: each is free for the next tile behind that
                 if (n && !__all_sync(0xffffffffu, mbar_wait(bar.aux_free, (n - 1) & 1, &p))) {
                     ok = false;
                     break;
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) table[32 * k + lane] = kPShift<Fmt> - x[k].x;
+                for (int k = 0; k < 4; ++k) {
+                    const float sum = far ? 0.f : x[k].x;        // (a far tile's are taken off the scores)
+                    table[32 * k + lane] = row0 + 32 * k + lane < it.span.len ? __fmaf_rn(-sum, kLog2e, (float)kPShift<Fmt>) : __int_as_float(0xff800000);
+                }
+                if (lane == 0) *reinterpret_cast<volatile int*>(smem + (bar.far - smem0)) = far;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar.aux);
                 if (n && !__all_sync(0xffffffffu, mbar_wait(bar.aux_free + 8, (n - 1) & 1, &p))) {
@@ -490,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
         const uint32_t s_taken = map_to(bar.first_taken, 0), d_taken = map_to(bar.second_taken, 0), acc_free = map_to(bar.acc_free, 0);
         const int shift = ds_shift<Fmt>(p.norms);
         const float f = power_of_two(shift - kPShift<Fmt>);
-        const unsigned long long c2 = pair_of(p.scale_log2, p.scale_log2), f2 = pair_of(f, f);
+        const unsigned long long f2 = pair_of(f, f);
         // (a lane's columns are 8 k + lane % 4 * 2 and the next, of four rows: a quarter of the table's values that a lane
         // with a row of its own needs, which took 1,500 of a tile's 3,100 clocks of shared memory)
         const float2 *sums = reinterpret_cast<const float2*>(smem + L::kAux) + half * kHalfCols / 2 + lane % 4, *deltas = sums + kRows / 2;
@@ -512,11 +543,19 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
                 unsigned long long prob[2][16];
                 if (tile >= mine) {
                     const int row = quad * 32 + lane / 4, col = half * kHalfCols + lane % 4 * 2;
+                    const bool far = *reinterpret_cast<volatile int*>(smem + (bar.far - smem0));
+                    if (far) {
+                        const int query = tile * kRows + half * kHalfCols;
+                        take_off_sums(s_at, p.scale, p.aux + ((int64_t)it.span.batch * p.heads + it.query_head(i)) * p.tokens.seq + it.span.first + query,
+                                      1, it.span.len - query);
+                    }
                     uint32_t x[2][32];
                     tmem_load_16x64(s_at, x[0]);
                     tmem_load_16x64(s_at + (16u << 16), x[1]);
                     tmem_wait(x[0]);
                     tmem_wait(x[1]);
+                    const float c = far ? kLog2e : p.scale_log2;
+                    const unsigned long long c2 = pair_of(c, c);
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         if (tile == mine) {      // queries before the row's own token
@@ -803,7 +842,6 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
         const uint32_t d_at = dprob + lanes + half * kHalfCols;
         const uint32_t taken = map_to(bar.second_taken, 0), acc_free = map_to(bar.acc_free, 0);
         const int shift = ds_shift<Fmt>(p.norms);
-        const unsigned long long c2 = pair_of(p.scale_log2, p.scale_log2);
         const int share = (cols / 2 + 31) / 32 * 32, from = half * share, to_col = min(p.dim, from + share);  // of dQ's columns
         int n = 0, items = 0;
         bool ok = true;
@@ -815,9 +853,11 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
             const int in_seq = it.span.tile * kSpan + (int)rank * kRows + quad * 32, rows = min(32, it.span.len - in_seq);
             const int mine = 2 * it.span.tile + (int)rank;       // this CTA's queries as a key tile
             float2 aux = make_float2(0.f, 0.f);
-            if (lane < rows) aux = __ldcg(&p.aux[((int64_t)it.span.batch * p.heads + it.head) * p.tokens.seq + it.span.first + in_seq + lane]);
-            const float base = (float)shift - aux.x;
-            const unsigned long long b2 = pair_of(base, base), delta = pair_of(-aux.y, -aux.y);
+            const float2* own = &p.aux[((int64_t)it.span.batch * p.heads + it.head) * p.tokens.seq + it.span.first + in_seq + lane];
+            if (lane < rows) aux = __ldcg(own);
+            const bool far = __any_sync(0xffffffffu, far_sum(aux.x));
+            const float base = far ? (float)shift : __fmaf_rn(-aux.x, kLog2e, (float)shift), c = far ? kLog2e : p.scale_log2;
+            const unsigned long long b2 = pair_of(base, base), c2 = pair_of(c, c), delta = pair_of(-aux.y, -aux.y);
             for (int i = 0; i < it.steps; ++i, ++n) {
                 const uint32_t s_at = score + (n & 1) * kRows + lanes + half * kHalfCols;
                 const int tile = it.steps - 1 - i;
@@ -829,6 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
                 unsigned long long prob[32];
                 uint32_t a[32], b[32];
                 if (tile <= mine) {
+                    if (far) take_off_sums(s_at, p.scale, own, 0, lane < rows ? 2 * kHalfCols : 0);
                     tmem_load32(s_at, a);
                     tmem_load32(s_at + 32, b);
                     auto powers = [&](uint32_t (&x)[32], int at) {
@@ -911,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- before the products
-// A row's log sum in powers of two and dout . out; fp16: the largest norms of the rows of dout and of v in any
+// A row's log sum and dout . out; fp16: the largest norms of the rows of dout and of v in any
 // sequence too.  Eight lanes a row, 16 bytes at a time, kRowsAtOnce rows in flight.
 struct Rows {
     const void *dout, *out, *v;
@@ -976,7 +1017,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         }
         if (s < p.seq && !of_v && part == 0) {
             const int64_t k = (int64_t)row * p.seq + s;
-            p.aux[k] = make_float2(p.lse[k] * kLog2e, dot);
+            p.aux[k] = make_float2(p.lse[k], dot);
         }
         if constexpr (kNorms) {
             const bool counts = s < p.seq && square <= 3.4028235e38f && (!p.offsets || (s >= p.offsets[0] && s < p.offsets[p.sequences]));

@@ -1,15 +1,19 @@
 """Attention whose scores lie far from zero: keys masked by low values, rows of large scores only, and scores beyond
-fp32's range, against the formula in 64 bits.
+fp32's range, and their gradients, against the formula in 64 bits.
 
 Every score here is a sum of products that fp32 holds exactly, whatever their order: multiples of the last place of
 the largest.  So P differs from the formula's by what is done behind the scores: a row's maximum is taken off (exact
 between neighbours), the difference times scale * log2(e) has three roundings of itself, the power 2 ulp.  A log
-sum is a score, rounded to fp32, and the logarithm of a sum, added with one rounding.
+sum is a score, rounded to fp32, and the logarithm of a sum, added with one rounding.  The gradient's P comes from
+a score and a log sum as it is given: each is off by half a step of fp32, the score by nothing where scale is a power of
+two and the log sum is so large that it is taken off the score itself.
 """
 import math
 
 import pytest
 import torch
+
+import attention_reference as ref
 
 pytestmark = pytest.mark.gpu
 F32 = 2.0 ** -23
@@ -139,3 +143,94 @@ def test_scores_below_all_numbers(tb, dead):
     q, k, v = masked(400, 2, 1, 64, BF, 2.0 ** 200, dead)
     k[:, :100, :, 9], q[..., 9] = -256.0, 16.0
     check_forward(tb, q, k, v, 0.25)
+
+
+def check_backward(tb, dout, q, k, v, scale):
+    scale = torch.tensor(scale, dtype=torch.float32).item()
+    out, lse = forward(tb, q, k, v, scale)
+    n, hq, hk, d = q.shape[1], q.shape[2], k.shape[2], q.shape[3]
+    grads = [torch.full_like(x, -7.0) for x in (q, k, v)]
+    ws = torch.full((tb.tb_attention_bwd_workspace_size(1, n, hq, hk, d, q.dtype),), 0xFF, dtype=torch.uint8, device="cuda")
+    tb.tb_attention_bwd(dout, q, k, v, out, lse, *grads, ws, scale=scale)
+    assert tb.tb_device_error() == 0
+    half, group = torch.finfo(q.dtype).eps / 2, hq // hk
+    s, sums = scores(q, k, scale), lse[0].double()[..., None]
+    p = torch.exp(s - sums)
+    e = F32 / 2 * (s.abs() + sums.abs())
+    if math.frexp(scale)[0] == 0.5:
+        e = torch.where(sums.abs() > 1024, 0.0, e)
+    e = torch.expm1(e.nan_to_num(0.0, 0.0, 0.0) + 4 * F32 * (1 + (s - sums).abs().nan_to_num(0.0, 0.0, 0.0)).clamp(max=400))
+    qq, kk, vv, up, oo = (x[0].double() for x in (q, k, v, dout, out))
+    kk, vv = kk.repeat_interleave(group, 1), vv.repeat_interleave(group, 1)
+    dp, delta = torch.einsum("ihd,jhd->hij", up, vv), torch.einsum("ihd,ihd->hi", up, oo)[..., None]
+    ds = p * (dp - delta)
+    dp_off = (d / 16 + 16) * F32 * torch.einsum("ihd,jhd->hij", up.abs(), vv.abs()) \
+        + (d / 8 + 8) * F32 * torch.einsum("ihd,ihd->hi", up.abs(), oo.abs())[..., None]
+    # a power below 2^-126 is 0; fp16: below the normal numbers of what P and dS are held times
+    floor_p, floor_s = 2.0 ** -126, 2.0 ** -126 * (dp - delta).abs()
+    if q.dtype == HALF:
+        most = up.norm(dim=-1).max().item() * vv.norm(dim=-1).max().item()
+        floor_p, floor_s = 2.0 ** -39, 2 * most * 2.0 ** -37
+    open_ = torch.ones(n, n, dtype=torch.bool, device="cuda").tril()
+    p_off = torch.where(p > 0, p * (e + half), 0.0) + floor_p * open_
+    ds_off = torch.where(p > 0, ds.abs() * (e + half + 4 * F32) + p * dp_off, 0.0) + floor_s * open_
+    add = (n * group / 16 + 32) * F32
+    over = lambda x: x.unflatten(1, (hk, group)).sum(2)
+    for got, x, off, rows, eq, what in ((grads[0], ds * scale, ds_off * scale, kk, "hij,jhd->ihd", "dq"),
+                                        (grads[1], ds * scale, ds_off * scale, qq, "hij,ihd->jhd", "dk"), (grads[2], p, p_off, up, "hij,ihd->jhd", "dv")):
+        want, slack = torch.einsum(eq, x, rows), torch.einsum(eq, off + add * x.abs(), rows.abs())
+        if what != "dq":
+            want, slack = over(want), over(slack)
+        ref.near(got[0], want, slack, what)
+
+
+def slopes(q, seed=9):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(q.shape, generator=g, device="cuda") * 0.01).to(q.dtype)
+
+
+@pytest.mark.parametrize("dtype, low", [(BF, 1e4), (BF, 3e8), (BF, 1e10), (BF, 1e30), (HALF, 1e4), (HALF, 3e8), (HALF, 2.0 ** 29)])
+@pytest.mark.parametrize("name", DEAD)
+def test_gradient_of_keys_masked_by_low_values(tb, name, dtype, low):
+    q, k, v = masked(600, 2, 1, 64, dtype, low, DEAD[name])
+    check_backward(tb, slopes(q), q, k, v, 0.25)
+
+
+# (with other scales than powers of two the scores' own rounding leaves nothing of P beyond 2^24)
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dtype, power, scale", [(BF, 8, 0.3), (BF, 12, 0.25), (BF, 13, 0.3), (BF, 16, 0.088388346), (BF, 20, 0.25), (BF, 22, 0.3),
+                                                 (BF, 24, 0.25), (BF, 27, 0.25), (BF, 33, 0.25), (BF, 60, 0.25), (HALF, 12, 0.3), (HALF, 16, 0.25),
+                                                 (HALF, 20, 0.25), (HALF, 22, 0.3), (HALF, 26, 0.25), (HALF, 29, 0.25)])
+def test_gradient_of_rows_of_scores_far_from_zero(tb, dtype, power, scale, sign):
+    q, k, v = large(300, 2, 1, 64, dtype, sign * 2.0 ** power, seed=power)
+    check_backward(tb, slopes(q), q, k, v, scale)
+
+
+@pytest.mark.parametrize("offsets", [None, [0, 1, 130, 400]])
+@pytest.mark.parametrize("dtype", [BF, HALF])
+@pytest.mark.parametrize("score", [2e3, 1e4, 5e4, 2e5, 1e6, 1e7, 1e8])
+def test_one_large_key(tb, score, dtype, offsets):
+    """Every row's one large key is its sequence's first: P is 1 and 0, out the key's v and dv the sum of dout, at
+    any scale and whatever fp32 makes of the score."""
+    n, d = 400, 64
+    starts = offsets or [0, n]
+    q, k, v = zeros(n, 2, d, dtype), zeros(n, 1, d, dtype), values(n, 1, d, dtype, 1)
+    root = 2.0 ** (math.frexp(score)[1] // 2)
+    q[..., 0] = root
+    k[:, starts[:-1], :, 0] = score / root / 0.3
+    dout, at = slopes(q), None if offsets is None else torch.tensor(offsets, device="cuda")
+    out, lse = torch.zeros_like(q), torch.zeros(1, 2, n, device="cuda")
+    tb.tb_attention(q, k, v, out, lse, offsets=at, scale=0.3)
+    grads = [torch.zeros_like(x) for x in (q, k, v)]
+    ws = torch.empty(tb.tb_attention_bwd_workspace_size(1, n, 2, 1, d, dtype), dtype=torch.uint8, device="cuda")
+    tb.tb_attention_bwd(dout, q, k, v, out, lse, *grads, ws, offsets=at, scale=0.3)
+    assert tb.tb_device_error() == 0
+    for a, b in zip(starts, starts[1:]):
+        assert torch.equal(out[0, a:b], v[0, a].expand(b - a, 2, d))
+        want, size = dout[0, a:b].double().sum((0, 1)), dout[0, a:b].double().abs().sum((0, 1))
+        ref.near(grads[2][0, a, 0], want, size * (2 * (b - a) / 16 + 32) * F32, "dv")
+        assert (grads[2][0, a + 1:b] == 0).all()
+        # dS of a key's own v is dout . v, formed twice in fp32
+        dp = torch.einsum("ihd,d->ih", dout[0, a:b].double().abs(), v[0, a, 0].double().abs()) * (d / 8 + 24) * F32
+        dp = dp + (2.0 ** -24 * dp.max() if dtype == HALF else 0.0)
+        ref.near(grads[0][0, a:b, :, 0], torch.zeros(b - a, 2, dtype=torch.float64, device="cuda"), 0.3 * dp * k[0, a, 0, 0].double().abs(), "dq")
