@@ -159,7 +159,8 @@ struct Place {
     int token, head, batch;   // of that row
 };
 // Columns from .. dim - 1 of 32 rows of a result from tensor memory, a row a lane, times the lane's factor and rounded,
-// to the first `rows` rows of `to`, through the warp's two boxes of shared memory.  A lane's 16-byte pieces lie at piece ^ (row / 2 & 3), the
+// to the first `rows` rows of `to`, through the warp's two boxes of shared memory, in turn.  Of stores before the call any
+// may still read either box: they are waited for, which costs nothing, as a piece of work lies between.  A lane's 16-byte pieces lie at piece ^ (row / 2 & 3), the
 // pattern of a 64-byte swizzle: no two lanes of a quarter warp share banks.  Arrives on `free` when the last columns
 // are in registers.  (Stores from registers held the warps up for the time that the memory took: 4,000 clocks for
 // 64 KB of every CTA at once.)
@@ -171,7 +172,10 @@ __device__ __forceinline__ void store_rows(unsigned char* boxes, uint32_t tmem, 
         unsigned char* box = boxes + (x & 32 ? kOutBox : 0);
         uint32_t o[32];
         tmem_load32(tmem + x, o);
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");       // the box is free
+        if (lane == 0) {         // the box is free
+            if (x == from) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        }
         tmem_wait(o);
         __syncwarp();
         if (x + 32 >= dim) {
