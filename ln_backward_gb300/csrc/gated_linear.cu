@@ -387,6 +387,7 @@ gated_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) 
         float unscale = 1.f;
         if constexpr (K == kBack && std::is_same<Fmt, F16>::value) unscale = *p.unscale;
         int n = 0;
+        bool sums_before = false;
         Where w;
         for (; pair_tile<K>(p, pair, pairs, n, &w); ++n) {
             const int buf = n & 1;
@@ -461,6 +462,9 @@ gated_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) 
                 }
             } else {
                 box.map = &maps.out[which];
+                // Sums fill both boxes and leave in one store; 16-bit results allow for one that still reads the other box.
+                if (sums_before && !sums && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                sums_before = sums;
                 auto work = [&](const uint32_t (&r)[32], int c) {
                     float v[32];
 #pragma unroll

@@ -279,7 +279,8 @@ struct Outbox {
 };
 
 // The same for 32 fp32 columns: one box of both halves' size, swizzled over 128 bytes, of split z.
-// `add`: onto what is there.  (Every element of dH's sums gets one addition a launch: the order of
+// Stores before it are waited for.  An Outbox::put of two boxes behind it lets one store go on reading: the caller waits for
+// this one, which reads both boxes.  `add`: onto what is there.  (Every element of dH's sums gets one addition a launch: the order of
 // the pieces decides the result, nothing else.)
 __device__ __forceinline__ void put_sums(unsigned char* box, const CUtensorMap* map, int lane, const float (&v)[32],
                                          int x, int y, int z, bool add) {
