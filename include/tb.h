@@ -737,8 +737,9 @@ tb_status tb_linear_xent_bwd(const float* dloss, const void* H, const void* W,
  * first or behind the last sequence are not written, and whatever they hold (NaN included) reaches
  * no other token; nor does a token reach another sequence's.  Within a sequence k and v are finite:
  * an infinity or NaN may reach the results of up to 255 tokens before it.  Offsets that do not count
- * up within 0 .. seq set the device error word to TB_ERR_INVALID_VALUE (tb_device_error); their
- * sequences are cut to the row.
+ * up within 0 .. seq set the device error word to TB_ERR_INVALID_VALUE (tb_device_error): of a sequence
+ * with tokens or without, each pair of them is looked at.  Their sequences are cut to the row, and
+ * what that call leaves in out and lse, or in the gradients, is undefined; nothing else is written.
  *
  * tb_attention
  *   q, k, v          [batch, seq, heads, head_dim] by tb_heads; k and v have the same number of

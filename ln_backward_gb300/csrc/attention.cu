@@ -75,6 +75,9 @@ __device__ __forceinline__ bool find_item(const Args& p, unsigned index, Item* i
     it->head = (int)(index % heads);
     const unsigned slot = index / heads;
     if (p.tokens.offsets) {
+        // (there are at least as many slots as sequences)
+        if (it->head == 0 && threadIdx.x == 2 * 32 && slot < (unsigned)p.tokens.sequences)
+            check_offsets(p.tokens.offsets, slot, p.tokens.seq, p.err);
         // (sorted, short items of few blocks would follow each other, whose latency nothing hides: 147 us, 136 so, of 8,192
         // tokens in 11 sequences, 32 heads of 128)
         if (!find_tile<false>(p.tokens, kItem, (int)slot, false, &it->span)) return false;

@@ -356,7 +356,12 @@ __host__ __device__ inline int64_t slots_of(int64_t tokens, int64_t sequences, i
 // Otherwise sequence after sequence, the longest tiles of each first, numbered so that a sequence is found without
 // adding up the lengths before it: sequence i's slots are floor(offsets[i] / size) + i and on, as floor((o + n) / size) -
 // floor(o / size) + 1 is at least ceil(n / size).
-// Offsets that do not count up within the row are cut to it, and reported in the device error word.
+// Offsets that do not count up within the row are cut to it: tiles stay inside, whatever they share or miss.  check_offsets
+// reports them in the device error word, of sequence i, tiles or none.
+__device__ __forceinline__ void check_offsets(const int64_t* offsets, int64_t i, int seq, int* err) {
+    const int64_t a = __ldcg((const long long*)offsets + i), b = __ldcg((const long long*)offsets + i + 1);
+    if (a < 0 || b < a || b > seq) atomicExch(err, (int)TB_ERR_INVALID_VALUE);
+}
 constexpr int kSorted = 128;
 template <bool Sorted>
 __device__ __forceinline__ bool find_tile(const Tokens& t, int size, int slot, bool from_last, Span* s) {
@@ -410,8 +415,6 @@ __device__ __forceinline__ bool find_tile(const Tokens& t, int size, int slot, b
         if (k < 0 || k >= tiles) return false;
         far = tiles - 1 - k;
     }
-    const int64_t a = __ldcg((const long long*)t.offsets + seq), b = __ldcg((const long long*)t.offsets + seq + 1);
-    if ((a < 0 || b < a || b > t.seq) && lane == 0) atomicExch(t.err, (int)TB_ERR_INVALID_VALUE);
     const int first = offset(seq), len = max(offset(seq + 1) - first, 0);
     *s = Span{0, first, len, from_last ? (len + size - 1) / size - 1 - far : far};
     return true;

@@ -953,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
 
 // ---------------------------------------------------------------- before the products
 // A row's log sum and dout . out; fp16: the largest norms of the rows of dout and of v in any
-// sequence too.  Eight lanes a row, 16 bytes at a time, kRowsAtOnce rows in flight.
+// sequence too.  The call's offsets are checked here.  Eight lanes a row, 16 bytes at a time, kRowsAtOnce rows in flight.
 struct Rows {
     const void *dout, *out, *v;
     int64_t stride[3][3];     // of batch, seq, head
@@ -961,6 +961,7 @@ struct Rows {
     float2* aux;
     unsigned* norms;
     const int64_t* offsets;
+    int* err;
     int sequences, batch, seq, heads, kv_heads, dim;
     unsigned chunks, ctas;    // of a head's tokens; of rows of dout, the others have rows of v
 };
@@ -971,6 +972,9 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     constexpr bool kNorms = std::is_same<Fmt, F16>::value;
     pdl_wait();
     pdl_trigger();
+    if (p.offsets)
+        for (int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; i < p.sequences; i += (int64_t)gridDim.x * kRowThreads)
+            check_offsets(p.offsets, i, p.seq, p.err);
     const bool of_v = blockIdx.x >= p.ctas;
     const unsigned heads = of_v ? p.kv_heads : p.heads, part = threadIdx.x & 7;
     const unsigned cta = blockIdx.x - (of_v ? p.ctas : 0), row = cta / p.chunks, chunk = cta - row * p.chunks;   // of a head's tokens
@@ -1283,7 +1287,7 @@ extern "C" tb_status tb_attention_bwd(const tb_heads* dout, const tb_heads* q, c
         for (int j = 0; j < 3; ++j) r.stride[i][j] = read[of[i]].s[j];
     }
     r.lse = lse, r.aux = const_cast<float2*>(p.aux), r.norms = const_cast<unsigned*>(p.norms);
-    r.offsets = offsets, r.sequences = (int)sequences;
+    r.err = p.err, r.offsets = offsets, r.sequences = (int)sequences;
     r.batch = (int)batch, r.seq = (int)seq, r.heads = p.heads, r.kv_heads = p.kv_heads, r.dim = p.dim;
     r.chunks = (unsigned)ceil_div(seq, kRowsCta), r.ctas = r.chunks * (unsigned)(batch * q->heads);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
