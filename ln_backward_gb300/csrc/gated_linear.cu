@@ -86,10 +86,11 @@ __device__ __forceinline__ void act_and_slope(float x, float& a, float& slope) {
         a = x * c;
         slope = __fmaf_rn(x, 0.3989422804014327f * exp2_fast(-0.5f * kLog2e * x * x), c);
     } else {
-        const float x2 = x * x;
-        const float s = sigmoid(1.5957691216057308f * x * __fmaf_rn(0.044715f, x2, 1.f));
+        // from 16 on either side the sigmoid is 0 or 1 and the slope with it; x's cube would leave fp32 long before bf16 ends
+        const float y = fabsf(x) > 16.f ? copysignf(16.f, x) : x, y2 = y * y;
+        const float s = sigmoid(1.5957691216057308f * y * __fmaf_rn(0.044715f, y2, 1.f));
         a = x * s;
-        slope = s * __fmaf_rn(1.5957691216057308f * x * (1.f - s), __fmaf_rn(3 * 0.044715f, x2, 1.f), 1.f);
+        slope = s * __fmaf_rn(1.5957691216057308f * y * (1.f - s), __fmaf_rn(3 * 0.044715f, y2, 1.f), 1.f);
     }
 }
 
