@@ -105,8 +105,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     const uint32_t answer = bar0, full = answer + 16, empty = full + 8 * L::kRing, q_full = empty + 8 * L::kRing, q_empty = q_full + 16,
                    s_full = q_empty + 16, p_full = s_full + 16, o_full = p_full + 16, o_empty = o_full + 16, tail = o_empty + 16, mended = tail + 8,
                    drain = mended + 8, done = drain + 8, work_full = done + 8, work_empty = work_full + 8, issued = work_empty + 8,
-                   slot = issued + 12;
-    static_assert(L::kRing * 16 + 6 * 16 + 6 * 8 + 16 + 16 <= 512);
+                   slot = issued + 12, stopped = slot + 4;
+    static_assert(L::kRing * 16 + 6 * 16 + 6 * 8 + 16 + 20 <= 512);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
 
@@ -127,6 +127,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         mbar_init(mended, 1);
         mbar_init(drain, 1);
         mbar_init(done, 1);
+        *reinterpret_cast<volatile int*>(smem + (stopped - q0)) = 0;
         init_work(work_full, work_empty, 2 * (2 + 8) + 1);     // the warps that load and mend, those of the softmax, and the MMAs'
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -154,9 +155,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         next_live = more && find_item(p, cluster, &next);
     };
     auto move_on = [&] { it = next, live = next_live; };
+    const Tails ends{tail, mended, stopped};
 
     if (warp == 0) {
-        int n = 0, queries[2] = {0, 0}, tails = 0;       // keys and values staged, tiles of queries, ends mended
+        int n = 0, queries[2] = {0, 0}, tails = 0;       // keys and values staged, tiles of queries, ends
+        uint32_t last = 0;                               // barrier of the last end
         bool ok = p.withhold != kLoads0 + (int)rank;
         for (; more; move_on()) {
             if (!ok || !live) {
@@ -194,9 +197,13 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     // hold need not be.
                     const bool mend = rows < kRows;
                     const uint32_t bar = mend ? map_to(tail, rank) : leader;
-                    if (mend && tails++ && !__all_sync(0xffffffffu, mbar_wait(mended, tails & 1, &p))) {
-                        ok = false;
-                        break;
+                    if (mend) {
+                        if (!ends.next(tails, &p)) {
+                            ok = false;
+                            break;
+                        }
+                        ++tails;
+                        last = leader;
                     }
                     if (elect_one()) {
                         mbar_expect_at(bar, L::kValueBytes);
@@ -213,6 +220,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             }
             ask();
         }
+        if (ends.left_over(tails, &p) && lane == 0) mbar_arrive_cluster(last);
+        __syncwarp();
         const int mine[3] = {n, queries[0], queries[1]}, rings[3] = {L::kRing, 1, 1};
         way_out<3>(rank, mine, rings, drain, done, issued, smem + (issued - q0), &p, [&](int s, int i, uint32_t* parity) {
             if (s) {
@@ -301,6 +310,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const int blocks = max(it.blocks0, it.blocks1), rows = it.span.len - (blocks - 1) * kRows, s = (n + 1) % L::kRing;
             if (rows < kRows) {              // the first values end with the sequence
                 if (!__all_sync(0xffffffffu, mbar_wait(tail, tails++ & 1, &p))) {
+                    ends.stop(tails, lane);
                     ok = false;
                     ask();
                     continue;

@@ -234,6 +234,50 @@ __device__ __forceinline__ void cleared(int lane) {
     if (lane == 0) asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 
+__device__ __forceinline__ int load_shared(uint32_t at) {
+    int x;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    return x;
+}
+// Waits until tail number `loaded` is mended or the mending warp has stopped: then `mended` may be two phases further,
+// and a wait for that one's parity would not see it.
+template <class P>
+__device__ __noinline__ bool tail_settled(uint32_t mended, uint32_t stopped, int loaded, unsigned long long limit, const P* p) {
+    const unsigned long long t0 = now_ns();
+    for (uint32_t it = 1; it < (1u << 30); ++it) {
+        if (load_shared(stopped) || mbar_try<true>(mended, (loaded - 1) & 1)) return true;
+        if ((it & 63u) == 0 && now_ns() - t0 > limit) break;
+    }
+    atomicExch(p->err, (int)TB_ERR_TIMEOUT);
+    return false;
+}
+// A tile that ends with its sequence is counted on its CTA's own barrier (`tail`) while the mending warp clears what
+// lies behind, one at a time; that warp then arrives in the loading warp's place, and on `mended`.  Where its wait gave up it
+// leaves the number of the tile, counted from 1, that it mends no more, and ends that one's phase of `mended`: the loading
+// warp loads no other, and on its way out arrives itself for the one that it may have loaded meanwhile, behind its bytes.
+struct Tails {
+    uint32_t tail, mended;
+    uint32_t stopped;         // a word, 0 at first
+    __device__ __forceinline__ void stop(int number, int lane) const {     // by the mending warp, once
+        if (lane == 0) {
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(stopped), "r"(number) : "memory");
+            mbar_arrive(mended);
+        }
+        __syncwarp();
+    }
+    // Before the loading warp's tail number `loaded` + 1.
+    template <class P>
+    __device__ __forceinline__ bool next(int loaded, const P* p) const {
+        return (!loaded || __all_sync(0xffffffffu, mbar_wait(mended, (loaded - 1) & 1, p))) && __all_sync(0xffffffffu, load_shared(stopped) == 0);
+    }
+    // On its way out: whether it has to arrive for the last one.
+    template <class P>
+    __device__ __forceinline__ bool left_over(int loaded, const P* p) const {
+        return loaded && __all_sync(0xffffffffu, mbar_wait<kEnd>(tail, (loaded - 1) & 1, p)) &&
+               __all_sync(0xffffffffu, tail_settled(mended, stopped, loaded, 4 * kWaitLimitNs, p)) && __all_sync(0xffffffffu, load_shared(stopped) == loaded);
+    }
+};
+
 // ---------------------------------------------------------------- work
 // A pair stays on its SMs: its first CTA asks for the next cluster of the grid that has not started, whose work
 // the pair then does.  (A cluster's launch, set-up and first loads take longer than short tiles.)  Both CTAs get the
@@ -452,8 +496,9 @@ inline tb_status run_withheld(int* err, cudaStream_t st, int* launches, F launch
     }
     return TB_OK;
 }
-// The problem of the self-tests: 512 tokens, two query heads of one key head, zeros in `mem` (kSelfBytes of them).
-constexpr int64_t kSelfTokens = 512, kSelfHeads = 2;
+// The problem of the self-tests: three whole tiles and one that ends with the sequence, two query heads of one key head,
+// zeros in `mem` (kSelfBytes of them).
+constexpr int64_t kSelfTokens = 500, kSelfHeads = 2;
 constexpr size_t kSelfBytes = 4 << 20;
 inline tb_heads self_heads(unsigned char** mem, int64_t heads, int64_t dim) {
     const tb_heads h{*mem, kSelfTokens * heads * dim, heads * dim, dim, heads};

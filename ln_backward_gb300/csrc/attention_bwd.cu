@@ -122,7 +122,7 @@ __device__ __noinline__ void take_off_sums(uint32_t tmem, float scale, const flo
 // Barriers of either kernel.
 struct Bars {
     uint32_t answer, keep, keep_free, full, free, first, second, first_taken, second_taken, aux, aux_free, acc, acc_free, tail, mended, drain,
-        done, work_full, work_empty, words, slot, far;
+        done, work_full, work_empty, words, slot, far, stopped;
 };
 template <class L>
 __device__ __forceinline__ Bars bars_at(uint32_t at) {
@@ -138,12 +138,13 @@ __device__ __forceinline__ Bars bars_at(uint32_t at) {
     b.first = take(2), b.second = take(1), b.first_taken = take(1), b.second_taken = take(1);
     b.aux = take(2), b.aux_free = take(2), b.acc = take(1), b.acc_free = take(1);
     b.tail = take(1), b.mended = take(1), b.drain = take(1), b.done = take(1), b.work_full = take(1), b.work_empty = take(1);
-    b.words = take(3), b.slot = at, b.far = at + 4;
-    static_assert((2 + 4 + 2 * L::kStages + 5 + 6 + 6 + 3) * 8 + 8 <= 512 && L::kStreams + 2 <= 6);
+    b.words = take(3), b.slot = at, b.far = at + 4, b.stopped = at + 8;
+    static_assert((2 + 4 + 2 * L::kStages + 5 + 6 + 6 + 3) * 8 + 12 <= 512 && L::kStreams + 2 <= 6);
     return b;
 }
 template <class L>
-__device__ __forceinline__ void init_bars(const Bars& b, int readers, int withhold) {
+__device__ __forceinline__ void init_bars(const Bars& b, volatile int* stopped, int readers, int withhold) {
+    *stopped = 0;
     for (int i = 0; i < L::kStages; ++i) {
         mbar_init(b.full + 8 * i, 2);        // an arrival of either CTA, and their bytes
         mbar_init(b.free + 8 * i, 1);
@@ -175,9 +176,11 @@ struct Loader {
     const Bars& bar;
     unsigned char* smem;
     uint32_t smem0, rank;
-    int lane, loaded[L::kStreams], kept[2], tails;
+    Tails ends;
+    int lane, loaded[L::kStreams], kept[2], tails, last;      // ends, and the tile number of the last one
     __device__ __forceinline__ Loader(const Args& p_, const Bars& b_, unsigned char* s_, uint32_t s0_, uint32_t r_, int l_)
-        : p(p_), bar(b_), smem(s_), smem0(s0_), rank(r_), lane(l_), loaded{}, kept{}, tails(0) {}
+        : p(p_), bar(b_), smem(s_), smem0(s0_), rank(r_),
+          ends{b_.tail, b_.mended, b_.stopped}, lane(l_), loaded{}, kept{}, tails(0), last(0) {}
     // One of the tiles that stay: this CTA's 128 tokens from `token` on.
     __device__ __forceinline__ bool keep(int i, const CUtensorMap* map, int token, int head, int batch) {
         if (kept[i] && !__all_sync(0xffffffffu, mbar_wait(bar.keep_free + 8 * i, (kept[i] - 1) & 1, &p))) return false;
@@ -212,12 +215,21 @@ struct Loader {
     static __device__ __forceinline__ int bytes(bool by_rows) { return by_rows ? Blocks * kHalfBox : kBox; }
     // Before a tile to be mended: `n` bytes in all streams.  (One at a time.)
     __device__ __forceinline__ bool expect_mended(int n) {
-        if (tails++ && !__all_sync(0xffffffffu, mbar_wait(bar.mended, tails & 1, &p))) return false;
+        if (!ends.next(tails, &p)) return false;
+        ++tails;
+        last = loaded[0];
         if (elect_one()) mbar_expect_at(map_to(bar.tail, rank), n);
         __syncwarp();
         return true;
     }
-    __device__ __forceinline__ void leave() const {
+    // `first`: the streams from it on are mended.
+    __device__ __forceinline__ void leave(int first) const {
+        if (ends.left_over(tails, &p) && lane == 0) {
+#pragma unroll
+            for (int s = 0; s < L::kStreams; ++s)
+                if (s >= first) mbar_arrive_cluster(map_to(bar.full + 8 * (L::first(s) + last % L::ring(s)), 0));
+        }
+        __syncwarp();
         constexpr int n = L::kStreams + 2;
         int mine[n], rings[n];
         for (int s = 0; s < L::kStreams; ++s) mine[s] = loaded[s], rings[s] = L::ring(s);
@@ -240,8 +252,17 @@ struct Mender {
     const Bars& bar;
     unsigned char* smem;
     uint32_t rank;
+    Tails ends;
     int lane, tails;
-    __device__ __forceinline__ bool wait() { return __all_sync(0xffffffffu, mbar_wait(bar.tail, tails++ & 1, &p)); }
+    __device__ __forceinline__ bool wait() {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar.tail, tails & 1, &p))) {
+            stop();
+            return false;
+        }
+        ++tails;
+        return true;
+    }
+    __device__ __forceinline__ void stop() const { ends.stop(tails + 1, lane); }
     // Tile n of the streams from `first` on, those below 2 by rows.
     __device__ __forceinline__ void mend(int first, int n, int rows) const {
 #pragma unroll
@@ -340,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
     const Bars bar = bars_at<L>(smem0 + L::kBars);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
-    if (threadIdx.x == 0) init_bars<L>(bar, 2 * 10 + 1, p.withhold);     // loads, log sums, work; the MMAs
+    if (threadIdx.x == 0) init_bars<L>(bar, reinterpret_cast<volatile int*>(smem + (bar.stopped - smem0)), 2 * 10 + 1, p.withhold);     // loads, log sums, work; the MMAs
     if (warp == 3) tmem_alloc_all(bar.slot);
     tmem_fence_before();
     __syncthreads();
@@ -394,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
             }
             ask();
         }
-        load.leave();
+        load.leave(0);
     } else if (warp == 1) {
         if (rank == 0) {
             const uint32_t by_rows = instruction(kBf, kRows, false), by_cols = instruction(kBf, cols, true);
@@ -461,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
         }
     } else if (warp == 2) {
         // The ends of sequences; log sums and deltas of the next query tile, negated.  A query behind the end has P = 0.
-        Mender<L, Blocks> ends{p, bar, smem, rank, lane, 0};
+        Mender<L, Blocks> ends{p, bar, smem, rank, {bar.tail, bar.mended, bar.stopped}, lane, 0};
         const float f = power_of_two(ds_shift<Fmt>(p.norms) - kPShift<Fmt>);
         float* table = reinterpret_cast<float*>(smem + L::kAux);
         int n = 0;
@@ -490,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
                 const bool far = __any_sync(0xffffffffu, far_sum(x[0].x) || far_sum(x[1].x) || far_sum(x[2].x) || far_sum(x[3].x));
                 // the log sums are read with the scores, the deltas with dP: each is free for the next tile behind that
                 if (n && !__all_sync(0xffffffffu, mbar_wait(bar.aux_free, (n - 1) & 1, &p))) {
+                    ends.stop();
                     ok = false;
                     break;
                 }
@@ -502,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar.aux);
                 if (n && !__all_sync(0xffffffffu, mbar_wait(bar.aux_free + 8, (n - 1) & 1, &p))) {
+                    ends.stop();
                     ok = false;
                     break;
                 }
@@ -697,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
     const Bars bar = bars_at<L>(smem0 + L::kBars);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
-    if (threadIdx.x == 0) init_bars<L>(bar, 2 * 10 + 1, p.withhold);
+    if (threadIdx.x == 0) init_bars<L>(bar, reinterpret_cast<volatile int*>(smem + (bar.stopped - smem0)), 2 * 10 + 1, p.withhold);
     if (warp == 3) tmem_alloc_all(bar.slot);
     tmem_fence_before();
     __syncthreads();
@@ -753,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
             }
             ask();
         }
-        load.leave();
+        load.leave(kVRows);
     } else if (warp == 1) {
         if (rank == 0) {
             const uint32_t by_rows = instruction(kBf, kRows, false), by_cols = instruction(kBf, cols, true);
@@ -814,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) dq_kernel(const __grid_constant__
             if (elect_one()) mma_commit(bar.drain);
         }
     } else if (warp == 2) {
-        Mender<L, Blocks> ends{p, bar, smem, rank, lane, 0};
+        Mender<L, Blocks> ends{p, bar, smem, rank, {bar.tail, bar.mended, bar.stopped}, lane, 0};
         int n = 0;
         bool ok = true;
         for (; more; move_on()) {
