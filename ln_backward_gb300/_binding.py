@@ -841,7 +841,7 @@ class _AttentionCall:
         at = words.buffer_info()[0]
         self.p = range(at, at + len(tensors) * _HEADS_BYTES, _HEADS_BYTES)
         self.batch, self.seq, self.dim, self.device, self.heads_q = batch, seq, dim, device, heads_q
-        self.scale = dim ** -0.5 if scale is None else scale
+        self.scale = (dim or 1) ** -0.5 if scale is None else scale     # (the library refuses heads of 0)
         self.code = _DTYPE.get(dtype)
         if self.code is None:
             raise TbError("dtype", 2)
