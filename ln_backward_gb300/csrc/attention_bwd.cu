@@ -995,9 +995,6 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     constexpr bool kNorms = std::is_same<Fmt, F16>::value;
     pdl_wait();
     pdl_trigger();
-    if (p.offsets)
-        for (int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; i < p.sequences; i += (int64_t)gridDim.x * kRowThreads)
-            check_offsets(p.offsets, i, p.seq, p.err);
     const bool of_v = blockIdx.x >= p.ctas;
     const unsigned heads = of_v ? p.kv_heads : p.heads, part = threadIdx.x & 7;
     const unsigned cta = blockIdx.x - (of_v ? p.ctas : 0), row = cta / p.chunks, chunk = cta - row * p.chunks;   // of a head's tokens
@@ -1055,6 +1052,9 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         most = __reduce_max_sync(0xffffffffu, most);
         if ((threadIdx.x & 31) == 0 && most) atomicMax(p.norms + of_v, most);
     }
+    if (p.offsets)
+        for (int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; i < p.sequences; i += (int64_t)gridDim.x * kRowThreads)
+            check_offsets(p.offsets, i, p.seq, p.err);
 }
 
 // dK and dV from the sums of several pieces, in their order; eight elements a thread.
