@@ -18,9 +18,9 @@
 // What bounds them at heads of 128 (bf16 4 x 4,096 tokens, 32 heads): dkv 2,750 clocks a tile of 128 queries where the MMAs
 // need 2,048: P takes 990 and dS 900, mostly powers, and reads of tensor memory whose port the MMAs share; 745 us, 1,475
 // TFLOP/s of its four products.  dq 1,800 clocks where 1,536 are needed; 533 us, 1,550 TFLOP/s of its three.  Together with the
-// rows 1,360 us while the clocks last, 1,010 TFLOP/s of the formula's five products, 54 % of cuBLAS's burst; 1,505 to 1,535 us, 900
-// TFLOP/s, call after call under the power limit.  A piece of work
-// adds 4,000 to 6,000 clocks, which tells on short sequences: 8,192 packed tokens of 1 to 2,047 395 us, 607 TFLOP/s.
+// rows 1,360 us while the clocks last, 1,010 TFLOP/s of the formula's five products, 54 % of cuBLAS's burst; 1,500 to 1,535 us, 900
+// to 920 TFLOP/s, call after call under the power limit.  A piece of work
+// adds 4,000 to 6,000 clocks, which tells on short sequences: 8,192 packed tokens of 1 to 2,047 396 us, 605 TFLOP/s.
 // One CTA with tiles of its own: 965 and 998 us.  Log sums and deltas taken off by the tensor cores, as products over three
 // parts of 8 or 11 bits: P 840 and dS 400 clocks, but the parts' way to the other CTA and the added products took
 // that back (1,360 us at best).

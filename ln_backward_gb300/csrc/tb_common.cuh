@@ -89,6 +89,11 @@ inline tb_status launch_status() {
 // at once.  pdl_trigger() lets the next programmatic dependent be scheduled
 // early; that kernel still waits for this one to complete before it touches
 // memory, so the trigger may be placed anywhere.
+// One kernel does otherwise: attention's dq_kernel follows dkv_kernel, shares only
+// inputs with it, loads and stores from its start and waits at its end.  It needs
+// that every thread of dkv_kernel waits before it triggers, so that whatever came
+// before dkv_kernel is complete when dq_kernel starts, and that nothing but
+// dkv_kernel is ever launched right before it.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
