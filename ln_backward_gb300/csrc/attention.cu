@@ -35,7 +35,7 @@ constexpr float kMost = 8192.f;
 // of all of the row's P, which its sum takes out again: at most 2^(2^-13) below kFar, where the largest P is still 1 in
 // fp16, but from |b| = 2^28 on (keys masked by -1e10, say) it leaves P's range.  Beyond kFar m is taken off the scores first,
 // exact for scores next to it, in a pass of its own that only warps with such a row make, behind the one for all: a branch
-// within that one took 299 instead of 273 us for fp16 16,384 tokens, 8 heads of 64 (269 without either).
+// within that one took 299 us for fp16 16,384 tokens, 8 heads of 64, this 266.
 constexpr float kFar = 0x1p12f;
 
 template <int Blocks>                        // of 64 columns of a head
