@@ -16,7 +16,8 @@
 // What bounds it: the chain of one tile's block.  At heads of 128 its scores and P V take 1,024 clocks, handing over about
 // 400, P 1,100 (512 of them powers, at 32 a clock and SM), so a pair's two tiles need 2,700 where their MMAs need 2,048;
 // a piece of work adds the start of its first two blocks and its results, about 10,000.  bf16 4 x 4,096 tokens, 32 heads of
-// 128: 407 us among others in a stream, under the power limit, 1,350 TFLOP/s, 72 % of cuBLAS's burst; 372 us, 1,480, in tens.
+// 128: 407 to 414 us among others in a stream, under the power limit, 1,330 to 1,350 TFLOP/s, 72 % of cuBLAS's burst;
+// 372 us, 1,480 TFLOP/s, in tens.
 // One CTA with tiles of its own took 466 us there: operands crossed shared memory at its 128 bytes a clock.  Heads of 64
 // are bound by P: fp16 16,384 tokens, 8 heads, 266 us, 1,030 TFLOP/s.  Two warps for the same rows instead of one: 449
 // against 440 us; a row's maximum before P: the same; registers shared out by setmaxnreg (208 and 88): 641 us, as the

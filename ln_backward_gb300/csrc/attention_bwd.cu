@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1) dkv_kernel(const __grid_constant_
     const Bars bar = bars_at<L>(smem0 + L::kBars);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
-    if (threadIdx.x == 0) init_bars<L>(bar, reinterpret_cast<volatile int*>(smem + (bar.stopped - smem0)), 2 * 10 + 1, p.withhold);     // loads, log sums, work; the MMAs
+    if (threadIdx.x == 0)                    // loads, log sums, work; the MMAs
+        init_bars<L>(bar, reinterpret_cast<volatile int*>(smem + (bar.stopped - smem0)), 2 * 10 + 1, p.withhold);
     if (warp == 3) tmem_alloc_all(bar.slot);
     tmem_fence_before();
     __syncthreads();
