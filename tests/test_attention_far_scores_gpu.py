@@ -234,3 +234,55 @@ def test_one_large_key(tb, score, dtype, offsets):
         dp = torch.einsum("ihd,d->ih", dout[0, a:b].double().abs(), v[0, a, 0].double().abs()) * (d / 8 + 24) * F32
         dp = dp + (2.0 ** -24 * dp.max() if dtype == HALF else 0.0)
         ref.near(grads[0][0, a:b, :, 0], torch.zeros(b - a, 2, dtype=torch.float64, device="cuda"), 0.3 * dp * k[0, a, 0, 0].double().abs(), "dq")
+
+
+@pytest.mark.parametrize("hq, hk, d", [(16, 1, 64), (12, 2, 128), (8, 8, 72)])
+@pytest.mark.parametrize("dtype", [BF, HALF])
+def test_gradient_of_grouped_heads(tb, dtype, hq, hk, d):
+    """The same where several pieces of work share a key head, each head's scores at a distance of its own from zero."""
+    n = 700
+    q, k, v = large(n, hq, hk, d, torch.float32, 2.0 ** 20, seed=d)
+    q *= 2.0 ** (torch.arange(hq, device="cuda") % 7 - 6)[:, None]
+    q, k, v = q.to(dtype), k.to(dtype), v.to(dtype)
+    check_backward(tb, slopes(q), q, k, v, 0.25)
+
+
+@pytest.mark.parametrize("dtype", [BF, HALF])
+def test_batch_entries_and_sequences_do_not_mix(tb, dtype):
+    """Sequences of near and far scores beside each other: each has the bits that it has alone.  (Of the packed row two pieces
+    of work share a key head, whose sums are joined: dk and dv are the same terms in another order, both sums off by at
+    most (m / 16 + 32) 2^-23 of their m terms' magnitudes, and rounded; |dS| is at most 2 |dout| max |v|.)"""
+    n, d = 300, 64
+    parts = [large(n, 4, 2, d, dtype, s, seed=i) for i, s in enumerate((1.0, 2.0 ** 22, 64.0, -2.0 ** 14))]
+    alone = []
+
+    def grads(q, k, v, dout, offsets=None):
+        out, lse = torch.empty_like(q), torch.empty(q.shape[0], 4, q.shape[1], device="cuda")
+        tb.tb_attention(q, k, v, out, lse, offsets=offsets)
+        got = [torch.empty_like(x) for x in (q, k, v)]
+        ws = torch.empty(tb.tb_attention_bwd_workspace_size(q.shape[0], q.shape[1], 4, 2, d, dtype), dtype=torch.uint8, device="cuda")
+        tb.tb_attention_bwd(dout, q, k, v, out, lse, *got, ws, offsets=offsets)
+        return [out, *got]
+
+    # (one row of dout and of v in each that is as large: fp16's power of two goes by all sequences)
+    for i, (q, k, v) in enumerate(parts):
+        dout = slopes(q, seed=i)
+        dout[:, 0], v[:, 0] = 1.0, 4.0
+        parts[i] = (q, k, v, dout)
+        alone.append(grads(q, k, v, dout))
+    batch = grads(*(torch.cat([p[j] for p in parts]) for j in range(4)))
+    packed = grads(*(torch.cat([p[j] for p in parts], 1) for j in range(4)), offsets=torch.arange(0, 4 * n + 1, n, device="cuda"))
+    assert tb.tb_device_error() == 0
+    for j in range(4):
+        for i in range(4):
+            assert torch.equal(batch[j][i:i + 1], alone[i][j]), (i, j)
+            mine = packed[j][:, i * n:(i + 1) * n]
+            if j < 2:
+                assert torch.equal(mine, alone[i][j]), (i, j)
+                continue
+            q, _, v, dout = (x[0].double() for x in parts[i])
+            terms = dout.abs().unflatten(1, (2, 2)).sum((0, 2)) if j == 3 else \
+                2 * v.norm(dim=-1).max() * d ** -0.5 * (dout.norm(dim=-1, keepdim=True) * q.abs()).unflatten(1, (2, 2)).sum((0, 2))
+            slack, size = (2 * n / 16 + 32) * F32 * terms, torch.maximum(mine.double().abs(), alone[i][j].double().abs())
+            bound = 2 * slack + torch.finfo(dtype).eps * (size + slack) + torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+            assert ((mine.double() - alone[i][j].double()).abs() <= bound).all(), (i, j)
